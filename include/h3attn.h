@@ -115,6 +115,68 @@ H3_API h3_status h3_rope_apply(const void* q_in, void* q_out, const void* k_in, 
                         const int32_t* cu_requests, int32_t num_requests,
                         const float* start_frames, const h3_rope_cfg* cfg, h3_stream_t stream);
 
+/* ---- Norm of queries and keys per head, with the rotation -------------------------------------
+ * The step before attention in models that norm their queries and keys: every row x (one token,
+ * one head; D values) becomes
+ *   z = x * w / sqrt(mean(x^2) + eps)          w: [D], one weight for Q's heads, one for K's
+ *   y = the rotation of h3_rope_apply applied to z (tags, bands, start frames as there), or z
+ *       itself when pos and tag are NULL (queries and keys of cross attention)
+ * in one pass.  Sums and rotation are fp32 and the result is rounded to bf16 once.  The angle is
+ * good to about 1e-7 turns at any position (fp32 radians are not used). */
+enum { H3_WEIGHT_F32 = 0, H3_WEIGHT_BF16 = 1 };
+
+typedef struct {
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_k_heads; /* 0 when k is NULL; may differ from num_q_heads */
+  int32_t head_dim;    /* 64 or 128 */
+  int32_t weight_type; /* H3_WEIGHT_F32 or H3_WEIGHT_BF16: both weights */
+  float eps;           /* <= 0 selects 1e-6 */
+  /* Elements between the tokens of a tensor (its heads and dims contiguous), a multiple of 8 and
+   * at least heads * head_dim, so q and k may be parts of a fused projection; 0 = contiguous. */
+  int64_t q_stride, k_stride;         /* q, k */
+  int64_t q_out_stride, k_out_stride; /* q_out, k_out (backward: dq_out, dk_out) */
+  int64_t dq_stride, dk_stride;       /* backward: dq, dk */
+} h3_qk_norm_desc;
+
+/* q, k           : device bf16 [num_tokens, heads, head_dim]; k and k_out NULL for Q alone.
+ * q_out, k_out   : the same shapes; may be q and k themselves with their strides (in place), must
+ *                  not otherwise overlap any input.  Only rows [0, num_tokens) are read or written.
+ * q_weight, k_weight : device [head_dim] of desc->weight_type, 16-byte aligned.
+ * pos, tag, cu_requests, num_requests, start_frames, cfg: as for h3_rope_apply; pos and tag both
+ *                  NULL for the norm alone (the others are then not used).
+ * Errors: H3_ERR_NULL, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED, H3_ERR_MISALIGNED, H3_ERR_CUDA. */
+H3_API h3_status h3_qk_norm_rope(const h3_qk_norm_desc* desc, const void* q, void* q_out,
+                                 const void* k, void* k_out, const void* q_weight,
+                                 const void* k_weight, const float* pos, const uint8_t* tag,
+                                 const int32_t* cu_requests, int32_t num_requests,
+                                 const float* start_frames, const h3_rope_cfg* cfg,
+                                 h3_stream_t stream);
+
+/* Workspace bytes of h3_qk_norm_rope_bwd (the CTAs' shares of the weights' gradients); 0 for an
+ * unsupported head_dim. */
+H3_API size_t h3_qk_norm_rope_bwd_workspace_size(int32_t head_dim);
+
+/* Gradient of h3_qk_norm_rope: with dy the gradient of y, dz = the inverse rotation of dy and
+ * r = 1 / sqrt(mean(x^2) + eps),
+ *   dw = sum over tokens and heads of dz x r;   dx = r (dz w - x r^2 mean(dz w x)).
+ * dq_out, dk_out : device bf16, the gradients of q_out and k_out.
+ * q, k, weights, pos ... cfg: the forward's inputs (not its outputs).
+ * dq, dk         : device bf16, written; may be dq_out and dk_out, or q and k, with their strides.
+ * dq_weight, dk_weight : device fp32 [head_dim], written (0 when num_tokens is 0).
+ * workspace      : device, >= h3_qk_norm_rope_bwd_workspace_size() bytes, 16-byte aligned; need not
+ *                  be initialised.  Calls that may run at the same time need separate workspaces.
+ * The result does not depend on timing: shares are summed in a fixed order.
+ * Errors: as above, and H3_ERR_WORKSPACE. */
+H3_API h3_status h3_qk_norm_rope_bwd(const h3_qk_norm_desc* desc, const void* dq_out,
+                                     const void* dk_out, const void* q, const void* k,
+                                     const void* q_weight, const void* k_weight, const float* pos,
+                                     const uint8_t* tag, const int32_t* cu_requests,
+                                     int32_t num_requests, const float* start_frames,
+                                     const h3_rope_cfg* cfg, void* dq, void* dk, float* dq_weight,
+                                     float* dk_weight, void* workspace, size_t workspace_bytes,
+                                     h3_stream_t stream);
+
 /* Bytes of device workspace h3_varlen_attn_fwd wants for these sizes: the work plan written by
  * the call itself (segment order and item prefix, 8 bytes per segment, plus a 16-byte header,
  * rounded up to 256) and, when max_seqlen >= 1024, a split area after it (about 42 MB at

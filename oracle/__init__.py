@@ -34,6 +34,8 @@ from .continuation import (ContinuationPlan, continuation_plan, continuation_pac
                            continuation_append, masked_update)
 from .vsa import (vsa_block_counts, vsa_block_count, vsa_block_ids, vsa_block_means,
                   vsa_block_scores, vsa_select, vsa_attention)
+from .norm import norm_rope, norm_rope_grad
+from .cross import cross_attention, cross_attention_grad
 
 __all__ = [
     "varlen_attention", "attention_weights", "dense_masked_attention_bruteforce",
@@ -42,5 +44,6 @@ __all__ = [
     "axis_window_count", "window_count", "window_ids", "window_partition", "window_pack",
     "window_unpack", "vsa_block_counts", "vsa_block_count", "vsa_block_ids", "vsa_block_means",
     "vsa_block_scores", "vsa_select", "vsa_attention", "ContinuationPlan", "continuation_plan",
-    "continuation_pack", "continuation_append", "masked_update",
+    "continuation_pack", "continuation_append", "masked_update", "norm_rope", "norm_rope_grad", "cross_attention",
+    "cross_attention_grad",
 ]

@@ -7,6 +7,8 @@ kernels.  There is no CPU or PyTorch fallback: if the library is missing, every 
 
 Calls:
   rope_apply        modality-tagged RoPE of Q and K with the continuation time shift
+  qk_norm_rope / qk_norm_rope_bwd   RMS norm of Q and K per head with the rotation (or without)
+                    in the same pass, and its gradient
   varlen_attn_fwd   block-diagonal softmax attention over cu_seqlens segments
   window_count / window_pack / window_unpack   shifted 3D window partition and row gather/scatter
   window_attn_fwd   shifted 3D window attention read and written in place on the grid
@@ -29,7 +31,8 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-__all__ = ["H3Error", "RopeConfig", "lib_path", "load_library", "rope_apply", "varlen_attn_fwd",
+__all__ = ["H3Error", "RopeConfig", "lib_path", "load_library", "rope_apply", "qk_norm_rope",
+           "qk_norm_rope_bwd_workspace_size", "qk_norm_rope_bwd", "varlen_attn_fwd",
            "varlen_attn_fwd_noalloc", "window_attn_fwd", "vsa_block_count",
            "vsa_select_workspace_size", "vsa_select", "vsa_attn_workspace_size", "vsa_attn_fwd",
            "ContinuationConfig",
@@ -69,6 +72,16 @@ class RopeConfig(ctypes.Structure):
 _I = ctypes.c_int32
 
 
+_L = ctypes.c_int64
+
+
+class _QkNormDesc(ctypes.Structure):
+    """Mirror of h3_qk_norm_desc."""
+    _fields_ = [("num_tokens", _I), ("num_q_heads", _I), ("num_k_heads", _I), ("head_dim", _I),
+                ("weight_type", _I), ("eps", ctypes.c_float), ("q_stride", _L), ("k_stride", _L),
+                ("q_out_stride", _L), ("k_out_stride", _L), ("dq_stride", _L), ("dk_stride", _L)]
+
+
 class ContinuationConfig(ctypes.Structure):
     """Mirror of h3_continuation_cfg."""
     _fields_ = [("text_rows", _I), ("clip_video_frames", _I), ("clip_audio_rows", _I),
@@ -102,6 +115,11 @@ def load_library():
     sigs = {
         "h3_rope_apply": (I32, [P, P, P, P, I32, I32, I32, P, P, P, I32, P,
                                 ctypes.POINTER(RopeConfig), P]),
+        "h3_qk_norm_rope": (I32, [ctypes.POINTER(_QkNormDesc), P, P, P, P, P, P, P, P, P, I32, P,
+                                  ctypes.POINTER(RopeConfig), P]),
+        "h3_qk_norm_rope_bwd_workspace_size": (U64, [I32]),
+        "h3_qk_norm_rope_bwd": (I32, [ctypes.POINTER(_QkNormDesc), P, P, P, P, P, P, P, P, P, I32, P,
+                                      ctypes.POINTER(RopeConfig), P, P, P, P, P, U64, P]),
         "h3_varlen_attn_workspace_size": (U64, [I32, I32, I32, I32]),
         "h3_varlen_attn_fwd": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P, U64, P]),
         "h3_varlen_attn_fwd_noalloc": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P]),
@@ -215,6 +233,156 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, ta
                                ctypes.byref(cfg) if cfg is not None else None, _stream(dev))
     _check(st, "h3_rope_apply")
     return q_out, k_out
+
+
+def _rows(t: torch.Tensor, name: str, device: torch.device, shape=None) -> int:
+    """Check bf16 [C, H, D] rows with heads and dims contiguous (a part of a fused projection is
+    fine); returns the token stride in elements, 0 for contiguous rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [C, H, D]")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    C, H, D = t.shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D) or (C > 1 and t.stride(0) < H * D):
+        raise ValueError(f"{name} must have contiguous heads and dims within a token")
+    return t.stride(0) if C > 1 else 0
+
+
+def _norm_inputs(q, k, q_weight, k_weight, pos, tag, cu_requests, start_frames, num_tokens, eps):
+    """Checks shared by qk_norm_rope and its backward; returns (descriptor, num_requests)."""
+    dev = q.device
+    q_stride, k_stride, hk = _rows(q, "q", dev), 0, 0
+    C, H, D = q.shape
+    n = C if num_tokens is None else int(num_tokens)
+    if not 0 <= n <= C:
+        raise ValueError("num_tokens must lie within the capacity of q")
+    if k is not None:
+        k_stride, hk = _rows(k, "k", dev), k.shape[1]
+        if k.shape[0] != C or k.shape[2] != D:
+            raise ValueError("k must have q's tokens and head_dim")
+    for name, w in (("q_weight", q_weight),) + ((("k_weight", k_weight),) if k is not None else ()):
+        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+        _require(w, name, q_weight.dtype, dev)
+        if tuple(w.shape) != (D,):
+            raise ValueError(f"{name} must be [head_dim]")
+    nreq = 0
+    if (pos is None) != (tag is None):
+        raise ValueError("pos and tag are given together")
+    if pos is None:
+        if cu_requests is not None or start_frames is not None:
+            raise ValueError("cu_requests and start_frames need pos and tag")
+    else:
+        _require(pos, "pos", torch.float32, dev)
+        _require(tag, "tag", torch.uint8, dev)
+        if pos.dim() != 2 or pos.shape[1] != 3 or pos.shape[0] < n or tag.numel() < n:
+            raise ValueError("pos must be [>= num_tokens, 3] and tag [>= num_tokens]")
+        if cu_requests is not None:
+            _require(cu_requests, "cu_requests", torch.int32, dev)
+            nreq = cu_requests.numel() - 1
+        if start_frames is not None:
+            _require(start_frames, "start_frames", torch.float32, dev)
+            if start_frames.numel() < max(nreq, 1):
+                raise ValueError("start_frames must have one entry per request")
+    desc = _QkNormDesc(n, H, hk, D, int(q_weight.dtype == torch.bfloat16), float(eps), q_stride, k_stride)
+    return desc, nreq
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: torch.Tensor,
+                 k_weight: Optional[torch.Tensor], pos: Optional[torch.Tensor] = None,
+                 tag: Optional[torch.Tensor] = None, cu_requests: Optional[torch.Tensor] = None,
+                 start_frames: Optional[torch.Tensor] = None, num_tokens: Optional[int] = None,
+                 eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, cfg: Optional[RopeConfig] = None):
+    """RMS norm of every head's row of q [C, Hq, D] and k [C, Hk, D] (bf16) times q_weight / k_weight
+    [D] (float32 or bfloat16), then the tagged RoPE of rope_apply; without pos and tag the norm alone.
+
+    q and k may be parts of a fused projection (heads and dims contiguous, any token stride that is
+    a multiple of 8); eps <= 0 selects 1e-6.  Writes new contiguous tensors unless q_out / k_out are
+    given (q and k themselves are allowed); rows past num_tokens are left as they were.  Returns
+    (q_out, k_out).
+    """
+    desc, nreq = _norm_inputs(q, k, q_weight, k_weight, pos, tag, cu_requests, start_frames, num_tokens, eps)
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    desc.q_out_stride = _rows(q_out, "q_out", dev, q.shape)
+    if k is None:
+        k_out = None
+    else:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        desc.k_out_stride = _rows(k_out, "k_out", dev, k.shape)
+    if desc.num_tokens == 0:
+        return q_out, k_out
+    lib = load_library()
+    with torch.cuda.device(dev):
+        st = lib.h3_qk_norm_rope(ctypes.byref(desc), _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out),
+                                 _ptr(q_weight), _ptr(k_weight) if k is not None else None, _ptr(pos),
+                                 _ptr(tag), _ptr(cu_requests), nreq, _ptr(start_frames),
+                                 ctypes.byref(cfg) if cfg is not None else None, _stream(dev))
+    _check(st, "h3_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace_size(head_dim: int) -> int:
+    return int(load_library().h3_qk_norm_rope_bwd_workspace_size(head_dim))
+
+
+def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: torch.Tensor,
+                     k: Optional[torch.Tensor], q_weight: torch.Tensor, k_weight: Optional[torch.Tensor],
+                     pos: Optional[torch.Tensor] = None, tag: Optional[torch.Tensor] = None,
+                     cu_requests: Optional[torch.Tensor] = None,
+                     start_frames: Optional[torch.Tensor] = None, num_tokens: Optional[int] = None,
+                     eps: float = 1e-6, dq: Optional[torch.Tensor] = None,
+                     dk: Optional[torch.Tensor] = None, cfg: Optional[RopeConfig] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """Gradient of qk_norm_rope: from dq_out, dk_out (bf16, the gradients of its outputs) and its
+    inputs to (dq, dk bf16, dq_weight, dk_weight float32 [D]).  dq and dk may be parts of a fused
+    gradient, or dq_out and dk_out, or q and k; the weights' gradients sum over tokens and heads in
+    a fixed order.
+    """
+    desc, nreq = _norm_inputs(q, k, q_weight, k_weight, pos, tag, cu_requests, start_frames, num_tokens, eps)
+    dev, D = q.device, q.shape[2]
+    lib = load_library()
+    if desc.num_tokens == 0 and q.numel() == 0:  # no rows at all: no buffer to point at
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
+        dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if dk is None and k is not None else dk
+        dw = torch.zeros((2, D), dtype=torch.float32, device=dev)
+        return dq, dk, dw[0], dw[1] if k is not None else None
+    desc.q_out_stride = _rows(dq_out, "dq_out", dev, q.shape)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    desc.dq_stride = _rows(dq, "dq", dev, q.shape)
+    if k is None:
+        dk = dk_out = None
+    else:
+        desc.k_out_stride = _rows(dk_out, "dk_out", dev, k.shape)
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        desc.dk_stride = _rows(dk, "dk", dev, k.shape)
+    dw = torch.empty((2, D), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(1, int(lib.h3_qk_norm_rope_bwd_workspace_size(D))), dtype=torch.uint8,
+                                device=dev)
+    _require(workspace, "workspace", torch.uint8, dev)
+    with torch.cuda.device(dev):
+        st = lib.h3_qk_norm_rope_bwd(ctypes.byref(desc), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k),
+                                     _ptr(q_weight), _ptr(k_weight) if k is not None else None, _ptr(pos),
+                                     _ptr(tag), _ptr(cu_requests), nreq, _ptr(start_frames),
+                                     ctypes.byref(cfg) if cfg is not None else None, _ptr(dq), _ptr(dk),
+                                     _ptr(dw[0]), _ptr(dw[1]) if k is not None else None,
+                                     _ptr(workspace), workspace.numel(), _stream(dev))
+    _check(st, "h3_qk_norm_rope_bwd")
+    return dq, dk, dw[0], dw[1] if k is not None else None
 
 
 def varlen_attn_workspace_size(num_segments: int, num_heads: int, max_seqlen: int, head_dim: int) -> int:

@@ -64,6 +64,7 @@
 #include <utility>
 
 #include "h3_internal.h"
+#include "launch.h"
 #include "sm103_ptx.cuh"
 
 namespace h3 {
@@ -1470,37 +1471,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-}
-
-// Launch with programmatic stream serialization: the kernel may be scheduled while the previous
-// kernel in the stream finishes (it calls grid_dependency_wait() before reading that kernel's
-// results), which hides the launch latency between the plan, attention and merge kernels.
-template <typename... Params, typename... Args>
-cudaError_t launch_programmatic(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
-                                cudaStream_t stream, Args&&... args) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
-int num_sms_of_current_device() {
-  static std::atomic<int> cached[64];  // 0 until looked up; racing lookups store the same value
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int n = cached[dev].load(std::memory_order_relaxed);
-  if (n == 0) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    cached[dev].store(n, std::memory_order_relaxed);
-  }
-  return n;
 }
 
 template <int D, int kMode>

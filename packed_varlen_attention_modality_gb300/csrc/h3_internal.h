@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -26,6 +27,47 @@ cudaError_t launch_rope(const void* q_in, void* q_out, const void* k_in, void* k
                         int num_tokens, int num_heads, int head_dim, const float* pos,
                         const uint8_t* tag, const int32_t* cu_requests, int num_requests,
                         const float* start_frames, const RopeTables& tables, cudaStream_t stream);
+
+// ---- norm of Q and K rows with the rotation ------------------------------------------------
+// Frequencies in turns per position unit (inverse frequency / 2 pi) as hi + lo float pairs, from
+// fp64 on the host; video_axis as in RopeTables.
+struct NormRopeTables {
+  float2 text[kMaxPairs];
+  float2 audio[kMaxPairs];
+  float2 video[kMaxPairs];
+  uint8_t video_axis[kMaxPairs];
+  float audio_hz;
+  float video_fps;
+};
+// One of Q and K; strides in elements between tokens, heads and dims contiguous.  Forward: out =
+// the normed and rotated rows; backward: out = dx.
+struct NormRopeTensor {
+  int heads;  // 0: absent
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* dy;
+  __nv_bfloat16* out;
+  int64_t x_stride, dy_stride, out_stride;
+  const void* weight;  // [D], bf16 or fp32
+  float* dw;           // backward: [D]
+};
+struct NormRopeArgs {
+  NormRopeTensor t[2];
+  int num_tokens;
+  int weight_bf16;
+  float eps;
+  const float* pos;  // null: no rotation
+  const uint8_t* tag;
+  const int32_t* cu_requests;
+  int num_requests;
+  const float* start_frames;
+  float* partials;  // backward: norm_bwd_workspace_bytes()
+  NormRopeTables tab;
+};
+constexpr int kNormBwdMaxCtas = 608;  // 4 x 152 SMs
+constexpr size_t norm_bwd_workspace_bytes(int head_dim) {
+  return static_cast<size_t>(kNormBwdMaxCtas) * 2 * head_dim * sizeof(float);
+}
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int head_dim, bool backward, cudaStream_t stream);
 
 // ---- window partition ---------------------------------------------------------------------
 struct WindowGeom {

@@ -247,6 +247,162 @@ h3_status h3_rope_apply(const void* q_in, void* q_out, const void* k_in, void* k
                                    reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ---- norm of Q and K rows with the rotation -------------------------------------------------------
+
+namespace {
+
+bool make_norm_tables(const h3_rope_cfg* cfg, int head_dim, h3::NormRopeTables* tab) {
+  h3_rope_cfg c{};
+  if (cfg != nullptr) c = *cfg;
+  int dims[3] = {c.video_dims_t, c.video_dims_h, c.video_dims_w};
+  if (dims[0] == 0 && dims[1] == 0 && dims[2] == 0) {
+    dims[0] = head_dim / 2;
+    dims[1] = dims[2] = head_dim / 4;
+  }
+  int sum = 0;
+  for (int d : dims) {
+    if (d < 0 || d > head_dim || d % 2 != 0) return false;
+    sum += d;
+  }
+  if (sum != head_dim) return false;
+  // base^(-2j/d) / (2 pi), split into two floats
+  auto turns = [](float base, int j, int d) {
+    const double f = std::pow(base > 0 ? static_cast<double>(base) : 10000.0, -2.0 * j / d) /
+                     6.283185307179586476925286766559;
+    const float hi = static_cast<float>(f);
+    return make_float2(hi, static_cast<float>(f - hi));
+  };
+  for (int j = 0; j < head_dim / 2; ++j) {
+    tab->text[j] = turns(c.base_text, j, head_dim);
+    tab->audio[j] = turns(c.base_audio, j, head_dim);
+    int axis = 0, jl = j;
+    while (jl >= dims[axis] / 2) jl -= dims[axis++] / 2;
+    tab->video_axis[j] = static_cast<uint8_t>(axis);
+    tab->video[j] = turns(c.base_video, jl, dims[axis]);
+  }
+  tab->audio_hz = c.audio_hz > 0 ? c.audio_hz : 40.f;
+  tab->video_fps = c.video_fps > 0 ? c.video_fps : 24.f;
+  return true;
+}
+
+// Checks shared by the forward and the backward, and the arguments common to both.
+h3_status norm_rope_args(const h3_qk_norm_desc* d, const void* q, const void* k, const void* q_weight,
+                         const void* k_weight, const float* pos, const uint8_t* tag,
+                         const int32_t* cu_requests, int32_t num_requests, const float* start_frames,
+                         const h3_rope_cfg* cfg, h3::NormRopeArgs* a) {
+  if (d == nullptr || q == nullptr || q_weight == nullptr) return H3_ERR_NULL;
+  if ((pos == nullptr) != (tag == nullptr)) return H3_ERR_NULL;
+  if (k != nullptr && k_weight == nullptr) return H3_ERR_NULL;
+  if (d->num_tokens < 0 || d->num_q_heads <= 0 || d->num_q_heads > 65535 || d->num_k_heads < 0 ||
+      d->num_k_heads > 65535 || (k != nullptr) != (d->num_k_heads > 0))
+    return H3_ERR_INVALID_ARG;
+  if (d->weight_type != H3_WEIGHT_F32 && d->weight_type != H3_WEIGHT_BF16) return H3_ERR_INVALID_ARG;
+  if (!(d->eps <= 0.f || std::isfinite(d->eps))) return H3_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return H3_ERR_UNSUPPORTED;
+  if (cu_requests != nullptr && num_requests <= 0) return H3_ERR_INVALID_ARG;
+  if (!aligned16(q) || (k != nullptr && !aligned16(k)) || !aligned16(q_weight) ||
+      (k != nullptr && !aligned16(k_weight)))
+    return H3_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(cu_requests) |
+       reinterpret_cast<uintptr_t>(start_frames)) & 3u)
+    return H3_ERR_MISALIGNED;
+  if (!make_norm_tables(cfg, d->head_dim, &a->tab)) return H3_ERR_INVALID_ARG;
+  a->num_tokens = d->num_tokens;
+  a->weight_bf16 = d->weight_type == H3_WEIGHT_BF16;
+  a->eps = d->eps > 0.f ? d->eps : 1e-6f;
+  a->pos = pos;
+  a->tag = tag;
+  a->cu_requests = cu_requests;
+  a->num_requests = cu_requests != nullptr ? num_requests : 1;
+  a->start_frames = start_frames;
+  a->t[0].heads = d->num_q_heads;
+  a->t[0].x = static_cast<const __nv_bfloat16*>(q);
+  a->t[0].weight = q_weight;
+  a->t[1].heads = d->num_k_heads;
+  a->t[1].x = static_cast<const __nv_bfloat16*>(k);
+  a->t[1].weight = k_weight;
+  return H3_OK;
+}
+
+// A token stride in elements: 0 selects contiguous rows; else at least a row, whole 16-byte units.
+h3_status token_stride(int64_t stride, int heads, int head_dim, int64_t* out) {
+  const int64_t row = static_cast<int64_t>(heads) * head_dim;
+  if (stride == 0) stride = row;
+  if (stride < row || stride > INT32_MAX) return H3_ERR_INVALID_ARG;
+  if (stride % 8 != 0) return H3_ERR_MISALIGNED;
+  *out = stride;
+  return H3_OK;
+}
+
+}  // namespace
+
+h3_status h3_qk_norm_rope(const h3_qk_norm_desc* desc, const void* q, void* q_out, const void* k,
+                          void* k_out, const void* q_weight, const void* k_weight, const float* pos,
+                          const uint8_t* tag, const int32_t* cu_requests, int32_t num_requests,
+                          const float* start_frames, const h3_rope_cfg* cfg, h3_stream_t stream) {
+  h3::NormRopeArgs a{};
+  h3_status st = norm_rope_args(desc, q, k, q_weight, k_weight, pos, tag, cu_requests, num_requests,
+                                start_frames, cfg, &a);
+  if (st != H3_OK) return st;
+  if (q_out == nullptr || (k != nullptr) != (k_out != nullptr)) return H3_ERR_NULL;
+  if (!aligned16(q_out) || !aligned16(k_out)) return H3_ERR_MISALIGNED;
+  const int D = desc->head_dim;
+  if ((st = token_stride(desc->q_stride, a.t[0].heads, D, &a.t[0].x_stride)) != H3_OK ||
+      (st = token_stride(desc->k_stride, a.t[1].heads, D, &a.t[1].x_stride)) != H3_OK ||
+      (st = token_stride(desc->q_out_stride, a.t[0].heads, D, &a.t[0].out_stride)) != H3_OK ||
+      (st = token_stride(desc->k_out_stride, a.t[1].heads, D, &a.t[1].out_stride)) != H3_OK)
+    return st;
+  a.t[0].out = static_cast<__nv_bfloat16*>(q_out);
+  a.t[1].out = static_cast<__nv_bfloat16*>(k_out);
+  if (desc->num_tokens == 0) return H3_OK;
+  if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
+  return from_cuda(h3::launch_norm_rope(a, D, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t h3_qk_norm_rope_bwd_workspace_size(int32_t head_dim) {
+  return head_dim == 64 || head_dim == 128 ? h3::norm_bwd_workspace_bytes(head_dim) : 0;
+}
+
+h3_status h3_qk_norm_rope_bwd(const h3_qk_norm_desc* desc, const void* dq_out, const void* dk_out,
+                              const void* q, const void* k, const void* q_weight,
+                              const void* k_weight, const float* pos, const uint8_t* tag,
+                              const int32_t* cu_requests, int32_t num_requests,
+                              const float* start_frames, const h3_rope_cfg* cfg, void* dq, void* dk,
+                              float* dq_weight, float* dk_weight, void* workspace,
+                              size_t workspace_bytes, h3_stream_t stream) {
+  h3::NormRopeArgs a{};
+  h3_status st = norm_rope_args(desc, q, k, q_weight, k_weight, pos, tag, cu_requests, num_requests,
+                                start_frames, cfg, &a);
+  if (st != H3_OK) return st;
+  const bool has_k = k != nullptr;
+  if (dq_out == nullptr || dq == nullptr || dq_weight == nullptr || has_k != (dk_out != nullptr) ||
+      has_k != (dk != nullptr) || has_k != (dk_weight != nullptr))
+    return H3_ERR_NULL;
+  if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) ||
+      ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u))
+    return H3_ERR_MISALIGNED;
+  const int D = desc->head_dim;
+  if ((st = token_stride(desc->q_stride, a.t[0].heads, D, &a.t[0].x_stride)) != H3_OK ||
+      (st = token_stride(desc->k_stride, a.t[1].heads, D, &a.t[1].x_stride)) != H3_OK ||
+      (st = token_stride(desc->q_out_stride, a.t[0].heads, D, &a.t[0].dy_stride)) != H3_OK ||
+      (st = token_stride(desc->k_out_stride, a.t[1].heads, D, &a.t[1].dy_stride)) != H3_OK ||
+      (st = token_stride(desc->dq_stride, a.t[0].heads, D, &a.t[0].out_stride)) != H3_OK ||
+      (st = token_stride(desc->dk_stride, a.t[1].heads, D, &a.t[1].out_stride)) != H3_OK)
+    return st;
+  if (workspace == nullptr || workspace_bytes < h3::norm_bwd_workspace_bytes(D))
+    return H3_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return H3_ERR_MISALIGNED;
+  a.t[0].dy = static_cast<const __nv_bfloat16*>(dq_out);
+  a.t[1].dy = static_cast<const __nv_bfloat16*>(dk_out);
+  a.t[0].out = static_cast<__nv_bfloat16*>(dq);
+  a.t[1].out = static_cast<__nv_bfloat16*>(dk);
+  a.t[0].dw = dq_weight;
+  a.t[1].dw = dk_weight;
+  a.partials = static_cast<float*>(workspace);
+  if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
+  return from_cuda(h3::launch_norm_rope(a, D, true, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 size_t h3_varlen_attn_workspace_size(int32_t num_segments, int32_t num_heads, int32_t max_seqlen,
                                      int32_t head_dim) {
   (void)num_heads;
