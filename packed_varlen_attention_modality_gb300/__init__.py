@@ -25,6 +25,7 @@ Calls:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence, Tuple
@@ -162,11 +163,19 @@ def _check(status: int, where: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """Make `device` current for a call (nothing to do, and nothing spent, when it already is)."""
+    return _SAME_DEVICE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _require(t: torch.Tensor, name: str, dtype, device: torch.device):
@@ -324,7 +333,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: torch.Ten
     if desc.num_tokens == 0:
         return q_out, k_out
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib.h3_qk_norm_rope(ctypes.byref(desc), _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out),
                                  _ptr(q_weight), _ptr(k_weight) if k is not None else None, _ptr(pos),
                                  _ptr(tag), _ptr(cu_requests), nreq, _ptr(start_frames),
@@ -369,20 +378,20 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: to
         if dk is None:
             dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
         desc.dk_stride = _rows(dk, "dk", dev, k.shape)
-    dw = torch.empty((2, D), dtype=torch.float32, device=dev)
+    dqw, dkw = torch.empty((2, D), dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = torch.empty(max(1, int(lib.h3_qk_norm_rope_bwd_workspace_size(D))), dtype=torch.uint8,
                                 device=dev)
     _require(workspace, "workspace", torch.uint8, dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         st = lib.h3_qk_norm_rope_bwd(ctypes.byref(desc), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k),
                                      _ptr(q_weight), _ptr(k_weight) if k is not None else None, _ptr(pos),
                                      _ptr(tag), _ptr(cu_requests), nreq, _ptr(start_frames),
                                      ctypes.byref(cfg) if cfg is not None else None, _ptr(dq), _ptr(dk),
-                                     _ptr(dw[0]), _ptr(dw[1]) if k is not None else None,
+                                     _ptr(dqw), _ptr(dkw) if k is not None else None,
                                      _ptr(workspace), workspace.numel(), _stream(dev))
     _check(st, "h3_qk_norm_rope_bwd")
-    return dq, dk, dw[0], dw[1] if k is not None else None
+    return dq, dk, dqw, dkw if k is not None else None
 
 
 def varlen_attn_workspace_size(num_segments: int, num_heads: int, max_seqlen: int, head_dim: int) -> int:

@@ -265,20 +265,22 @@ bool make_norm_tables(const h3_rope_cfg* cfg, int head_dim, h3::NormRopeTables* 
     sum += d;
   }
   if (sum != head_dim) return false;
-  // base^(-2j/d) / (2 pi), split into two floats
-  auto turns = [](float base, int j, int d) {
-    const double f = std::pow(base > 0 ? static_cast<double>(base) : 10000.0, -2.0 * j / d) /
-                     6.283185307179586476925286766559;
-    const float hi = static_cast<float>(f);
-    return make_float2(hi, static_cast<float>(f - hi));
+  // base^(-2j/d) / (2 pi) for j in [0, d/2), each split into two floats; the ladder is a running
+  // product in fp64 (relative error under 1e-14 after 64 steps)
+  auto ladder = [](float base, int d, float2* out) {
+    if (d == 0) return;
+    const double step = std::pow(base > 0 ? static_cast<double>(base) : 10000.0, -2.0 / d);
+    double f = 1.0 / 6.283185307179586476925286766559;
+    for (int j = 0; j < d / 2; ++j, f *= step) {
+      const float hi = static_cast<float>(f);
+      out[j] = make_float2(hi, static_cast<float>(f - hi));
+    }
   };
-  for (int j = 0; j < head_dim / 2; ++j) {
-    tab->text[j] = turns(c.base_text, j, head_dim);
-    tab->audio[j] = turns(c.base_audio, j, head_dim);
-    int axis = 0, jl = j;
-    while (jl >= dims[axis] / 2) jl -= dims[axis++] / 2;
-    tab->video_axis[j] = static_cast<uint8_t>(axis);
-    tab->video[j] = turns(c.base_video, jl, dims[axis]);
+  ladder(c.base_text, head_dim, tab->text);
+  ladder(c.base_audio, head_dim, tab->audio);
+  for (int axis = 0, j = 0; axis < 3; ++axis) {
+    ladder(c.base_video, dims[axis], tab->video + j);
+    for (int i = 0; i < dims[axis] / 2; ++i, ++j) tab->video_axis[j] = static_cast<uint8_t>(axis);
   }
   tab->audio_hz = c.audio_hz > 0 ? c.audio_hz : 40.f;
   tab->video_fps = c.video_fps > 0 ? c.video_fps : 24.f;
@@ -306,7 +308,7 @@ h3_status norm_rope_args(const h3_qk_norm_desc* d, const void* q, const void* k,
   if ((reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(cu_requests) |
        reinterpret_cast<uintptr_t>(start_frames)) & 3u)
     return H3_ERR_MISALIGNED;
-  if (!make_norm_tables(cfg, d->head_dim, &a->tab)) return H3_ERR_INVALID_ARG;
+  if (pos != nullptr && !make_norm_tables(cfg, d->head_dim, &a->tab)) return H3_ERR_INVALID_ARG;
   a->num_tokens = d->num_tokens;
   a->weight_bf16 = d->weight_type == H3_WEIGHT_BF16;
   a->eps = d->eps > 0.f ? d->eps : 1e-6f;

@@ -7,10 +7,13 @@
 //             dx = r (g - x r^2 mean(g x))
 //
 // Memory-bound: the forward reads x and writes y once, the backward reads x and dy and writes dx
-// once; positions and tags are 13 bytes a token.  A row is D / 8 lanes of 16 bytes, so its sums
-// are 3 or 4 shuffle steps and x never leaves registers between the norm and the rotation.  The
-// (cos, sin) of a token's pairs are computed once by the CTA into shared memory and serve all
-// heads of Q and K.  All arithmetic is fp32; the results are rounded to bf16 once.
+// once; positions and tags are 13 bytes a token.  A row is D / 8 lanes of 16 bytes (a warp holds
+// two rows at D = 128, four at 64), so its sums are 4 or 3 shuffle steps and x stays in registers
+// between the norm and the rotation.  A warp takes a token, computes the token's (cos, sin) once
+// -- each lane a share, traded by shuffles -- keeps them in registers and runs over the heads of Q
+// and K; when tokens are few, a token's heads are dealt to several warps.  Warps share nothing but
+// the frequency tables, so no barrier separates the loads of one token from those of the next.
+// All arithmetic is fp32; the results are rounded to bf16 once.
 //
 // Angles are kept in turns as a pair of floats (coordinate and frequency both hi + lo), so the
 // phase is good to about 1e-7 turns whatever the position; fp32 radians would lose 1e-3 already at
@@ -25,13 +28,24 @@ namespace h3 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;  // tokens of a CTA's group
+constexpr int kWarps = kThreads / 32;
+// Rows a lane has in flight and CTAs an SM holds with the registers that takes.  The forward of
+// 58,758 tokens x 80 heads x 128 takes 369 us so (6.5 TB/s, 96 % of a plain copy's rate); 4 rows
+// and 4 CTAs 377 us, 4 and 5 403 us (spills).  The backward of 29,001 tokens takes 295 us (6.0 TB/s,
+// 89 %: two reads to a write); 3 rows 324 us, 2 rows 349 us.
+constexpr int kFwdUnroll = 8, kFwdCtas = 3;
+constexpr int kBwdUnroll = 4, kBwdCtas = 2;
+constexpr int kFewUnroll = 1;
 
-// (cos, sin) of pair j of token n.
-__device__ __forceinline__ float2 token_cos_sin(const NormRopeArgs& a, int n, int j) {
+struct Tables {  // shared-memory copy of the frequencies: lanes index them apart
+  float2 f[3][kMaxPairs];  // text, video, audio (the tags' order)
+};
+
+// (cos, sin) of pair j of token n; axis_j: the coordinate that drives the pair in video rows.
+__device__ __forceinline__ float2 token_cos_sin(const NormRopeArgs& a, const Tables& tab, int n, int j, int axis_j) {
   const int tg = a.tag[n];
   const float* p = a.pos + 3 * static_cast<size_t>(n);
-  const int axis = tg == 1 ? a.tab.video_axis[j] : 0;
+  const int axis = tg == 1 ? axis_j : 0;
   float ch = p[axis], cl = 0.f;
   if (axis == 0 && a.start_frames != nullptr) {
     int lo = 0, hi = a.num_requests - 1;  // largest r with cu_requests[r] <= n
@@ -51,7 +65,7 @@ __device__ __forceinline__ float2 token_cos_sin(const NormRopeArgs& a, int n, in
     cl = __fadd_rn(__fsub_rn(ch, __fsub_rn(sum, b)), __fsub_rn(qh, b)) + ql;
     ch = sum;
   }
-  const float2 inv = tg == 1 ? a.tab.video[j] : (tg == 2 ? a.tab.audio[j] : a.tab.text[j]);
+  const float2 inv = tab.f[tg <= 2 ? tg : 0][j];
   const float turns = __fmul_rn(ch, inv.x);
   const float rest = fmaf(cl, inv.x, fmaf(ch, inv.y, fmaf(ch, inv.x, -turns)));
   float s, c;
@@ -66,170 +80,216 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+// Eight values of a row as packed pairs of floats, evens and odds apart: e[0] = (x0, x2),
+// e[1] = (x4, x6), o[0] = (x1, x3), o[1] = (x5, x7), so that two rotation pairs share each
+// two-lane multiply-add.
+struct Row8 {
+  float2 e[2], o[2];
+};
+__device__ __forceinline__ Row8 unpack8(const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  Row8 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  for (int i = 0; i < 2; ++i) {
+    r.e[i] = make_float2(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i + 1] << 16));
+    r.o[i] = make_float2(__uint_as_float(w[2 * i] & 0xffff0000u),
+                         __uint_as_float(w[2 * i + 1] & 0xffff0000u));
   }
+  return r;
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const Row8& r) {
+  return make_uint4(pack_bf16x2(r.e[0].x, r.o[0].x), pack_bf16x2(r.e[0].y, r.o[0].y),
+                    pack_bf16x2(r.e[1].x, r.o[1].x), pack_bf16x2(r.e[1].y, r.o[1].y));
 }
-__device__ __forceinline__ void load_weight(const void* w, int bf16, int col, float (&out)[8]) {
-  if (bf16) {
-    unpack8(*(static_cast<const uint4*>(w) + col / 8), out);
-  } else {
-    const float4* p = static_cast<const float4*>(w) + col / 4;
-    const float4 a = p[0], b = p[1];
-    out[0] = a.x; out[1] = a.y; out[2] = a.z; out[3] = a.w;
-    out[4] = b.x; out[5] = b.y; out[6] = b.z; out[7] = b.w;
+__device__ __forceinline__ Row8 load_weight(const void* w, int bf16, int col) {
+  if (bf16) return unpack8(*(static_cast<const uint4*>(w) + col / 8));
+  const float4* p = static_cast<const float4*>(w) + col / 4;
+  const float4 a = p[0], b = p[1];
+  Row8 r;
+  r.e[0] = make_float2(a.x, a.z);
+  r.o[0] = make_float2(a.y, a.w);
+  r.e[1] = make_float2(b.x, b.z);
+  r.o[1] = make_float2(b.y, b.w);
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
+
+// The cosines and sines of this lane's four pairs of a token.
+struct CosSin {
+  float2 c[2], s[2];  // pairs (0, 1) and (2, 3)
+};
+
+// A lane's place: row group g of the warp (kGroups rows at a time), columns [col, col + 8) of it.
+template <int D>
+struct Lane {
+  static constexpr int kLanes = D / 8, kGroups = 32 / kLanes, kOwn = 4 / kGroups;
+  int lane, group, col;
+  uint32_t axes;  // two bits each: axis of the kOwn pairs whose angle this lane computes
+  __device__ __forceinline__ Lane(const NormRopeArgs& a)
+      : lane(threadIdx.x & 31), group(lane / kLanes), col(lane % kLanes * 8), axes(0u) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      axes |= static_cast<uint32_t>(a.tab.video_axis[col / 2 + group * kOwn + i]) << (2 * i);
   }
+  __device__ __forceinline__ CosSin cos_sin(const NormRopeArgs& a, const Tables& tab, int n) const {
+    float2 own[kOwn], all[4];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      own[i] = token_cos_sin(a, tab, n, col / 2 + group * kOwn + i, (axes >> (2 * i)) & 3u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int from = lane % kLanes + kLanes * (i / kOwn);
+      all[i].x = __shfl_sync(0xffffffffu, own[i % kOwn].x, from);
+      all[i].y = __shfl_sync(0xffffffffu, own[i % kOwn].y, from);
+    }
+    CosSin r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r.c[i] = make_float2(all[2 * i].x, all[2 * i + 1].x);
+      r.s[i] = make_float2(all[2 * i].y, all[2 * i + 1].y);
+    }
+    return r;
+  }
+};
+
+__device__ __forceinline__ void fill_tables(const NormRopeArgs& a, Tables& tab) {
+  if (threadIdx.x < kMaxPairs) {
+    tab.f[0][threadIdx.x] = a.tab.text[threadIdx.x];
+    tab.f[1][threadIdx.x] = a.tab.video[threadIdx.x];
+    tab.f[2][threadIdx.x] = a.tab.audio[threadIdx.x];
+  }
+  __syncthreads();
 }
 
-// Rows of one tensor for a group of tokens [tok0, tok0 + ntok): row slot s takes rows s, s + R, ...
-// of the group's ntok * heads rows; f(x, dy, cs pointer) -> result, kUnroll rows' loads in flight.
+// Heads of one tensor of token n, kUnroll rows a lane in flight: the warp's part takes batches
+// part, part + parts, ... of kGroups * kUnroll heads.  f(x, dy) -> result; called by whole warps,
+// with zeros past the last head.
 template <int D, int kUnroll, bool kTwo, typename F>
-__device__ __forceinline__ void for_rows(const NormRopeTensor& t, int tok0, int ntok, F&& f) {
-  constexpr int kLanes = D / 8;
-  constexpr int kRows = kThreads / kLanes;
-  const int slot = threadIdx.x / kLanes, col = (threadIdx.x % kLanes) * 8;
-  const int rows = ntok * t.heads;
-  int ti = 0, h = slot;  // token of the group and head of the next row
-  while (h >= t.heads && ti < ntok) { h -= t.heads; ++ti; }
-  // every thread makes the same number of steps: the row sums shuffle across whole warps
-  for (int base = 0; base < rows; base += kRows * kUnroll) {
-    uint4 x[kUnroll], y[kUnroll];
-    int tok[kUnroll], head[kUnroll];
+__device__ __forceinline__ void for_heads(const NormRopeTensor& t, const Lane<D>& ln, int n, int part,
+                                          int parts, F&& f) {
+  constexpr int kBatch = Lane<D>::kGroups * kUnroll;
+  const __nv_bfloat16* x = t.x + n * t.x_stride + ln.group * D + ln.col;
+  const __nv_bfloat16* dy = kTwo ? t.dy + n * t.dy_stride + ln.group * D + ln.col : nullptr;
+  __nv_bfloat16* out = t.out + n * t.out_stride + ln.group * D + ln.col;
+  for (int h = part * kBatch; h < t.heads; h += parts * kBatch) {
+    uint4 xv[kUnroll], yv[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      tok[u] = ti;
-      head[u] = h;
-      x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (ti < ntok) {
-        const size_t n = static_cast<size_t>(tok0 + ti);
-        x[u] = __ldcs(reinterpret_cast<const uint4*>(t.x + n * t.x_stride + h * D + col));
-        if (kTwo) y[u] = __ldcs(reinterpret_cast<const uint4*>(t.dy + n * t.dy_stride + h * D + col));
+      const int head = h + u * Lane<D>::kGroups;  // of the warp's first row
+      xv[u] = yv[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (head + ln.group < t.heads) {
+        xv[u] = __ldcs(reinterpret_cast<const uint4*>(x + head * D));
+        if (kTwo) yv[u] = __ldcs(reinterpret_cast<const uint4*>(dy + head * D));
       }
-      h += kRows;
-      while (h >= t.heads && ti < ntok) { h -= t.heads; ++ti; }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (base + u * kRows >= rows) break;  // uniform: no row of the CTA is left
-      const uint4 r = f(x[u], y[u], min(tok[u], ntok - 1));  // zeros past the last row
-      if (tok[u] < ntok)
-        __stcs(reinterpret_cast<uint4*>(t.out + static_cast<size_t>(tok0 + tok[u]) * t.out_stride +
-                                        head[u] * D + col), r);
+      const int head = h + u * Lane<D>::kGroups;
+      if (head >= t.heads) break;  // the whole warp
+      const uint4 r = f(xv[u], yv[u]);
+      if (head + ln.group < t.heads) __stcs(reinterpret_cast<uint4*>(out + head * D), r);
     }
   }
 }
 
-template <int D, bool kRotate>
-__global__ void __launch_bounds__(kThreads)
-norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int group) {
-  __shared__ __align__(16) float2 cs[kMaxTokens][D / 2];
+template <int D, bool kRotate, int kUnroll>
+__global__ void __launch_bounds__(kThreads, kFwdCtas)
+norm_rope_kernel(const __grid_constant__ NormRopeArgs a, int parts) {
+  __shared__ Tables tab;
+  if (kRotate) fill_tables(a, tab);
   grid_dependency_wait();
   launch_dependents();
-  const int tok0 = blockIdx.x * group;
-  const int ntok = min(group, a.num_tokens - tok0);
-  const int pair0 = (threadIdx.x % (D / 8)) * 4;
-  if (kRotate) {
-    for (int i = threadIdx.x; i < ntok * (D / 2); i += kThreads)
-      cs[i / (D / 2)][i % (D / 2)] = token_cos_sin(a, tok0 + i / (D / 2), i % (D / 2));
-    __syncthreads();
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const NormRopeTensor& t = a.t[k];
-    if (t.heads == 0) break;
-    float w[8];
-    load_weight(t.weight, a.weight_bf16, pair0 * 2, w);
-    for_rows<D, 4, false>(t, tok0, ntok, [&](const uint4& xv, const uint4&, int ti) {
-      float x[8];
-      unpack8(xv, x);
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-      const float r = rsqrtf(row_sum<D / 8>(ss) * (1.f / D) + a.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
-      if (kRotate) {
-        const float4* c = reinterpret_cast<const float4*>(&cs[ti][pair0]);
-        const float4 c01 = c[0], c23 = c[1];
-        const float cc[8] = {c01.x, c01.y, c01.z, c01.w, c23.x, c23.y, c23.z, c23.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = x[2 * i], q = x[2 * i + 1], co = cc[2 * i], si = cc[2 * i + 1];
-          x[2 * i] = fmaf(p, co, -q * si);
-          x[2 * i + 1] = fmaf(p, si, q * co);
-        }
-      }
-      return pack8(x);
-    });
-  }
-}
-
-// Backward.  CTAs loop over token groups and keep their share of dw in registers (8 columns a
-// thread); the shares of a CTA's row slots are summed in slot order and written as one row of
-// partials, which norm_weight_grad_kernel sums in CTA order: the result does not depend on timing.
-template <int D, bool kRotate>
-__global__ void __launch_bounds__(kThreads)
-norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, int group) {
-  constexpr int kLanes = D / 8;
-  constexpr int kRows = kThreads / kLanes;
-  __shared__ __align__(16) float2 cs[kMaxTokens][D / 2];
-  __shared__ float part[kRows][D];
-  grid_dependency_wait();
-  launch_dependents();
-  const int pair0 = (threadIdx.x % kLanes) * 4;
-  float w[2][8], dw[2][8];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (a.t[k].heads > 0) load_weight(a.t[k].weight, a.weight_bf16, pair0 * 2, w[k]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[k][i] = 0.f;
-  }
-  for (int tok0 = blockIdx.x * group; tok0 < a.num_tokens; tok0 += gridDim.x * group) {
-    const int ntok = min(group, a.num_tokens - tok0);
-    if (kRotate) {
-      __syncthreads();  // the previous group's rotations are done
-      for (int i = threadIdx.x; i < ntok * (D / 2); i += kThreads)
-        cs[i / (D / 2)][i % (D / 2)] = token_cos_sin(a, tok0 + i / (D / 2), i % (D / 2));
-      __syncthreads();
-    }
+  const Lane<D> ln(a);
+  const int warps = gridDim.x * kWarps;
+  for (int64_t unit = blockIdx.x * kWarps + threadIdx.x / 32;
+       unit < static_cast<int64_t>(a.num_tokens) * parts; unit += warps) {
+    const int n = static_cast<int>(unit / parts), part = static_cast<int>(unit % parts);
+    CosSin cs;
+    if (kRotate) cs = ln.cos_sin(a, tab, n);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (a.t[k].heads == 0) break;
-      for_rows<D, 2, true>(a.t[k], tok0, ntok, [&](const uint4& xv, const uint4& yv, int ti) {
-        float x[8], g[8];
-        unpack8(xv, x);
-        unpack8(yv, g);
-        if (kRotate) {
-          const float4* c = reinterpret_cast<const float4*>(&cs[ti][pair0]);
-          const float4 c01 = c[0], c23 = c[1];
-          const float cc[8] = {c01.x, c01.y, c01.z, c01.w, c23.x, c23.y, c23.z, c23.w};
+      const NormRopeTensor& t = a.t[k];
+      if (t.heads == 0) break;
+      const Row8 w = load_weight(t.weight, a.weight_bf16, ln.col);
+      for_heads<D, kUnroll, false>(t, ln, n, part, parts, [&](const uint4& xv, const uint4&) {
+        Row8 x = unpack8(xv);
+        float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {  // R(-phi)
-            const float p = g[2 * i], q = g[2 * i + 1], co = cc[2 * i], si = cc[2 * i + 1];
-            g[2 * i] = fmaf(p, co, q * si);
-            g[2 * i + 1] = fmaf(q, co, -p * si);
+        for (int i = 0; i < 2; ++i) ss = ffma2(x.e[i], x.e[i], ffma2(x.o[i], x.o[i], ss));
+        const float2 r = both(rsqrtf(row_sum<D / 8>(ss.x + ss.y) * (1.f / D) + a.eps));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x.e[i] = fmul2(x.e[i], fmul2(r, w.e[i]));
+          x.o[i] = fmul2(x.o[i], fmul2(r, w.o[i]));
+        }
+        if (kRotate) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 e = x.e[i], o = x.o[i];
+            x.e[i] = ffma2(e, cs.c[i], fmul2(minus(o), cs.s[i]));
+            x.o[i] = ffma2(e, cs.s[i], fmul2(o, cs.c[i]));
           }
         }
-        float ss = 0.f, gx = 0.f;
+        return pack8(x);
+      });
+    }
+  }
+}
+
+// Backward.  Warps keep their share of dw in registers (8 columns a lane); the shares of a CTA's
+// rows are summed in a fixed order and written as one row of partials, which
+// norm_weight_grad_kernel sums in a fixed order: the result does not depend on timing.
+template <int D, bool kRotate, int kUnroll>
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
+norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, int parts) {
+  constexpr int kRows = kThreads / (D / 8);
+  __shared__ Tables tab;
+  __shared__ float part_dw[kRows][D];
+  if (kRotate) fill_tables(a, tab);
+  grid_dependency_wait();
+  launch_dependents();
+  const Lane<D> ln(a);
+  const int warps = gridDim.x * kWarps;
+  Row8 dw[2] = {};
+  for (int64_t unit = blockIdx.x * kWarps + threadIdx.x / 32;
+       unit < static_cast<int64_t>(a.num_tokens) * parts; unit += warps) {
+    const int n = static_cast<int>(unit / parts), part = static_cast<int>(unit % parts);
+    CosSin cs;
+    if (kRotate) cs = ln.cos_sin(a, tab, n);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(x[i], x[i], ss);
-          gx = fmaf(g[i] * w[k][i], x[i], gx);
+    for (int k = 0; k < 2; ++k) {
+      const NormRopeTensor& t = a.t[k];
+      if (t.heads == 0) break;
+      const Row8 w = load_weight(t.weight, a.weight_bf16, ln.col);
+      for_heads<D, kUnroll, true>(t, ln, n, part, parts, [&](const uint4& xv, const uint4& yv) {
+        Row8 x = unpack8(xv), g = unpack8(yv);
+        if (kRotate) {  // R(-phi)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 e = g.e[i], o = g.o[i];
+            g.e[i] = ffma2(e, cs.c[i], fmul2(o, cs.s[i]));
+            g.o[i] = ffma2(o, cs.c[i], fmul2(minus(e), cs.s[i]));
+          }
         }
-        const float r = rsqrtf(row_sum<kLanes>(ss) * (1.f / D) + a.eps);
-        const float m = row_sum<kLanes>(gx) * (1.f / D) * r * r;
+        float2 ss = make_float2(0.f, 0.f), gx = ss;
+        Row8 p;  // dz x
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          dw[k][i] = fmaf(g[i] * x[i], r, dw[k][i]);
-          x[i] = r * fmaf(-x[i], m, g[i] * w[k][i]);
+        for (int i = 0; i < 2; ++i) {
+          p.e[i] = fmul2(g.e[i], x.e[i]);
+          p.o[i] = fmul2(g.o[i], x.o[i]);
+          ss = ffma2(x.e[i], x.e[i], ffma2(x.o[i], x.o[i], ss));
+          gx = ffma2(p.e[i], w.e[i], ffma2(p.o[i], w.o[i], gx));
+        }
+        const float rs = rsqrtf(row_sum<D / 8>(ss.x + ss.y) * (1.f / D) + a.eps);
+        const float2 r = both(rs);
+        const float2 m = both(row_sum<D / 8>(gx.x + gx.y) * (-1.f / D) * rs * rs);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          dw[k].e[i] = ffma2(p.e[i], r, dw[k].e[i]);
+          dw[k].o[i] = ffma2(p.o[i], r, dw[k].o[i]);
+          x.e[i] = fmul2(r, ffma2(x.e[i], m, fmul2(g.e[i], w.e[i])));
+          x.o[i] = fmul2(r, ffma2(x.o[i], m, fmul2(g.o[i], w.o[i])));
         }
         return pack8(x);
       });
@@ -239,13 +299,19 @@ norm_rope_bwd_kernel(const __grid_constant__ NormRopeArgs a, int group) {
   for (int k = 0; k < 2; ++k) {
     if (a.t[k].heads == 0) break;
     __syncthreads();
+    float* mine = &part_dw[threadIdx.x / (D / 8)][ln.col];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[threadIdx.x / kLanes][pair0 * 2 + i] = dw[k][i];
+    for (int i = 0; i < 2; ++i) {
+      mine[4 * i] = dw[k].e[i].x;
+      mine[4 * i + 1] = dw[k].o[i].x;
+      mine[4 * i + 2] = dw[k].e[i].y;
+      mine[4 * i + 3] = dw[k].o[i].y;
+    }
     __syncthreads();
     if (threadIdx.x < D) {
       float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) s += part[i][threadIdx.x];
+      for (int i = 0; i < kRows; ++i) s += part_dw[i][threadIdx.x];
       a.partials[(static_cast<size_t>(blockIdx.x) * 2 + k) * D + threadIdx.x] = s;
     }
   }
@@ -274,28 +340,50 @@ norm_weight_grad_kernel(const float* __restrict__ partials, int num_partials, in
   }
 }
 
-// Tokens of a CTA's group: one while that still leaves SMs idle (a token's rows are at most a few
-// steps of the CTA), else four, which computes 256 angles at once.
-int group_tokens(int num_tokens, int sms) { return num_tokens < 4 * kMaxTokens * sms ? 1 : kMaxTokens; }
-
-template <int D>
-cudaError_t launch_d(const NormRopeArgs& a, int sms, bool backward, cudaStream_t stream) {
-  const int group = group_tokens(a.num_tokens, sms);
-  const int groups = (a.num_tokens + group - 1) / group;
-  if (!backward) {
-    auto* kernel = a.pos != nullptr ? norm_rope_kernel<D, true> : norm_rope_kernel<D, false>;
-    return launch_programmatic(kernel, dim3(groups), dim3(kThreads), 0, stream, a, group);
-  }
-  const int grid = groups < kNormBwdMaxCtas ? groups : kNormBwdMaxCtas;
+template <int D, bool kRotate, int kUnroll>
+cudaError_t launch_unroll(const NormRopeArgs& a, int sms, bool backward, cudaStream_t stream) {
+  const int ctas = sms * (backward ? kBwdCtas : kFwdCtas);
+  // a token is dealt to one warp when the tokens alone fill the GPU's warps, else to as many as
+  // fill them, up to one batch of heads a warp
+  constexpr int kBatch = Lane<D>::kGroups * kUnroll;
+  const int64_t n = a.num_tokens, warps = static_cast<int64_t>(ctas) * kWarps;
+  const int heads = a.t[0].heads > a.t[1].heads ? a.t[0].heads : a.t[1].heads;
+  const int64_t most = (heads + kBatch - 1) / kBatch, want = n > 0 ? (warps + n - 1) / n : 1;
+  const int parts = static_cast<int>(want < most ? want : most);
+  const int64_t need = (n * parts + kWarps - 1) / kWarps;
+  int grid = static_cast<int>(need < ctas ? need : ctas);
+  if (!backward)
+    return launch_programmatic(norm_rope_kernel<D, kRotate, kUnroll>, dim3(grid), dim3(kThreads), 0,
+                               stream, a, parts);
+  if (grid > kNormBwdMaxCtas) grid = kNormBwdMaxCtas;
   if (grid > 0) {
-    auto* kernel = a.pos != nullptr ? norm_rope_bwd_kernel<D, true> : norm_rope_bwd_kernel<D, false>;
-    const cudaError_t e = launch_programmatic(kernel, dim3(grid), dim3(kThreads), 0, stream, a, group);
+    const cudaError_t e = launch_programmatic(norm_rope_bwd_kernel<D, kRotate, kUnroll>, dim3(grid),
+                                              dim3(kThreads), 0, stream, a, parts);
     if (e != cudaSuccess) return e;
   }
   // with no rows the weights' gradient is zero: the sum over no partials
   const int columns = a.t[1].heads > 0 ? 2 * D : D;
   return launch_programmatic(norm_weight_grad_kernel, dim3(columns / 8), dim3(8 * kStrands), 0, stream,
                              static_cast<const float*>(a.partials), grid, D, a.t[0].dw, a.t[1].dw);
+}
+
+template <int D>
+cudaError_t launch_d(const NormRopeArgs& a, int sms, bool backward, cudaStream_t stream) {
+  // Few rows: one step of rows for each warp that the GPU holds, or less.  Then a warp takes one
+  // step, so that nothing runs in turn (one token x 48 heads: 3.8 us against 5.1 us at eight rows
+  // a lane); with more rows than that a warp would compute a token's angles again at each step
+  // (the gradient of 320 tokens x 48 heads: 10.4 us so, 7.7 us at four rows a lane).
+  const int heads = a.t[0].heads > a.t[1].heads ? a.t[0].heads : a.t[1].heads;
+  const int64_t steps = (heads + Lane<D>::kGroups - 1) / Lane<D>::kGroups;
+  const bool few = a.num_tokens * steps <= sms * (backward ? kBwdCtas : kFwdCtas) * kWarps;
+  if (a.pos != nullptr) {
+    if (few) return launch_unroll<D, true, kFewUnroll>(a, sms, backward, stream);
+    return backward ? launch_unroll<D, true, kBwdUnroll>(a, sms, true, stream)
+                    : launch_unroll<D, true, kFwdUnroll>(a, sms, false, stream);
+  }
+  if (few) return launch_unroll<D, false, kFewUnroll>(a, sms, backward, stream);
+  return backward ? launch_unroll<D, false, kBwdUnroll>(a, sms, true, stream)
+                  : launch_unroll<D, false, kFwdUnroll>(a, sms, false, stream);
 }
 
 }  // namespace
