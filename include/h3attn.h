@@ -245,6 +245,55 @@ H3_API h3_status h3_varlen_attn_fwd_noalloc(const void* q, const void* k, const 
                                             int32_t capacity, int32_t num_heads, int32_t head_dim,
                                             float softmax_scale, h3_stream_t stream);
 
+/* ---- Packed cross attention --------------------------------------------------------------------
+ * Queries attend to states of another length (an encoder's): segment g's query rows
+ * [cu_seqlens_q[g], cu_seqlens_q[g+1]) attend to the key rows [cu_seqlens_k[g],
+ * cu_seqlens_k[g] + n_g), n_g = seqused_k[g], or the whole key segment when seqused_k is NULL.
+ * Query head h reads key head h / (num_q_heads / num_kv_heads).  Per row, as h3_varlen_attn_fwd:
+ *   S_ij = scale * <q_i, k_j>;  P = softmax_j(S);  o_i = sum_j P_ij v_j;  lse_i = log sum_j exp(S_ij)
+ * Keys that a segment does not use get weight exactly zero (they are never multiplied in, so
+ * NaN/Inf there cannot leak).  A segment without keys gives o = 0 and lse = -inf.  With equal
+ * offsets and head counts this is h3_varlen_attn_fwd. */
+typedef struct {
+  int32_t num_segments;
+  int32_t max_seqlen_q; /* host upper bound on the query rows of a segment, <= capacity_q */
+  int32_t max_seqlen_k; /* host upper bound on the keys n_g a segment uses, <= capacity_k */
+  int32_t capacity_q;   /* rows of q, o (and dq); row stride of lse */
+  int32_t capacity_k;   /* rows of k, v (and dk, dv) */
+  int32_t num_q_heads;
+  int32_t num_kv_heads; /* divides num_q_heads */
+  int32_t head_dim;     /* 64 or 128 */
+  float softmax_scale;  /* <= 0 selects 1/sqrt(head_dim) */
+  /* Elements between the tokens of a tensor (its heads and dims contiguous), a multiple of 8 and
+   * at least heads * head_dim, so k and v may be parts of a fused projection; 0 = contiguous.
+   * o (and its gradient) are contiguous. */
+  int64_t q_stride, k_stride, v_stride;
+} h3_cross_attn_desc;
+
+/* Workspace bytes of h3_varlen_cross_attn_fwd for these sizes; 0 for invalid ones. */
+H3_API size_t h3_varlen_cross_attn_workspace_size(const h3_cross_attn_desc* desc);
+
+/* q          : device bf16 [capacity_q, num_q_heads, head_dim].
+ * k, v       : device bf16 [capacity_k, num_kv_heads, head_dim]; may be NULL when capacity_k is 0.
+ * o          : device bf16 [capacity_q, num_q_heads, head_dim], contiguous; rows of every segment
+ *              written, others untouched.  Must not overlap an input.
+ * lse        : device fp32 [num_q_heads, capacity_q] (natural log) or NULL.
+ * cu_seqlens_q, cu_seqlens_k : device int32 [num_segments + 1] each; must start at 0, not
+ *              decrease, end <= capacity.  Empty segments are allowed on both sides.
+ * seqused_k  : device int32 [num_segments] or NULL: keys used of each key segment (a padded
+ *              batch), 0 <= n_g <= its length.
+ * workspace  : device, h3_varlen_cross_attn_workspace_size() bytes, 16-byte aligned; need not be
+ *              initialised.  Calls that may run at the same time need separate workspaces.
+ * A segment whose offsets or n_g are out of range is skipped (its rows are not written) and one
+ * longer than its bound is computed in full; both are recorded as H3_ERR_BAD_CU_SEQLENS.
+ * Errors: H3_ERR_NULL, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED, H3_ERR_MISALIGNED,
+ *         H3_ERR_WORKSPACE, H3_ERR_CUDA; device-side H3_ERR_BAD_CU_SEQLENS / H3_ERR_TIMEOUT. */
+H3_API h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* desc, const void* q,
+                                          const void* k, const void* v, void* o, float* lse,
+                                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                          const int32_t* seqused_k, void* workspace,
+                                          size_t workspace_bytes, h3_stream_t stream);
+
 /* Number of windows of the partition (host only; no device work).
  * [H3-fast] "window attention across GPUs": along each axis of length L with window w and
  * shift s there are ceil((L + s) / w) windows (edge windows cropped).  Returns -1 on bad input

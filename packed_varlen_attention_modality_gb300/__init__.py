@@ -10,6 +10,8 @@ Calls:
   qk_norm_rope / qk_norm_rope_bwd   RMS norm of Q and K per head with the rotation (or without)
                     in the same pass, and its gradient
   varlen_attn_fwd   block-diagonal softmax attention over cu_seqlens segments
+  varlen_cross_attn_fwd   packed cross attention: keys of another length per segment, query heads
+                    sharing key heads, padded key batches
   window_count / window_pack / window_unpack   shifted 3D window partition and row gather/scatter
   window_attn_fwd   shifted 3D window attention read and written in place on the grid
   vsa_select / vsa_attn_fwd   block-sparse video attention: block gate scores + top-k
@@ -34,7 +36,8 @@ import torch
 
 __all__ = ["H3Error", "RopeConfig", "lib_path", "load_library", "rope_apply", "qk_norm_rope",
            "qk_norm_rope_bwd_workspace_size", "qk_norm_rope_bwd", "varlen_attn_fwd",
-           "varlen_attn_fwd_noalloc", "window_attn_fwd", "vsa_block_count",
+           "varlen_attn_fwd_noalloc", "varlen_cross_attn_workspace_size", "varlen_cross_attn_fwd",
+           "window_attn_fwd", "vsa_block_count",
            "vsa_select_workspace_size", "vsa_select", "vsa_attn_workspace_size", "vsa_attn_fwd",
            "ContinuationConfig",
            "ContinuationPlan", "continuation_config", "continuation_plan", "continuation_pack",
@@ -83,6 +86,13 @@ class _QkNormDesc(ctypes.Structure):
                 ("q_out_stride", _L), ("k_out_stride", _L), ("dq_stride", _L), ("dk_stride", _L)]
 
 
+class _CrossAttnDesc(ctypes.Structure):
+    """Mirror of h3_cross_attn_desc."""
+    _fields_ = [("num_segments", _I), ("max_seqlen_q", _I), ("max_seqlen_k", _I), ("capacity_q", _I),
+                ("capacity_k", _I), ("num_q_heads", _I), ("num_kv_heads", _I), ("head_dim", _I),
+                ("softmax_scale", ctypes.c_float), ("q_stride", _L), ("k_stride", _L), ("v_stride", _L)]
+
+
 class ContinuationConfig(ctypes.Structure):
     """Mirror of h3_continuation_cfg."""
     _fields_ = [("text_rows", _I), ("clip_video_frames", _I), ("clip_audio_rows", _I),
@@ -124,6 +134,8 @@ def load_library():
         "h3_varlen_attn_workspace_size": (U64, [I32, I32, I32, I32]),
         "h3_varlen_attn_fwd": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P, U64, P]),
         "h3_varlen_attn_fwd_noalloc": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P]),
+        "h3_varlen_cross_attn_workspace_size": (U64, [ctypes.POINTER(_CrossAttnDesc)]),
+        "h3_varlen_cross_attn_fwd": (I32, [ctypes.POINTER(_CrossAttnDesc), P, P, P, P, P, P, P, P, P, U64, P]),
         "h3_window_attn_fwd": (I32, [P, P, P, P, P, I32P, I32P, I32P, I32, I32, F32, P]),
         "h3_window_count": (I32, [I32P, I32P, I32P]),
         "h3_window_pack": (I32, [I32P, I32P, I32P, P, P, ctypes.POINTER(P), ctypes.POINTER(P),
@@ -469,6 +481,77 @@ def varlen_attn_fwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                                             int(max_seqlen), C, H, D, scale, _stream(dev))
     _check(st, "h3_varlen_attn_fwd_noalloc")
     return out
+
+
+def _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqused_k, softmax_scale):
+    """Checks shared by the cross attention calls; returns the descriptor."""
+    dev = q.device
+    q_stride, k_stride = _rows(q, "q", dev), _rows(k, "k", dev)
+    v_stride = _rows(v, "v", dev, k.shape)
+    C, H, D = q.shape
+    Ck, Hk, Dk = k.shape
+    if Dk != D:
+        raise ValueError("k and v must have q's head_dim")
+    _require(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
+    _require(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev)
+    S = cu_seqlens_q.numel() - 1
+    if S < 0 or cu_seqlens_k.numel() != S + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must have one entry per segment and one more")
+    if seqused_k is not None:
+        _require(seqused_k, "seqused_k", torch.int32, dev)
+        if seqused_k.numel() != S:
+            raise ValueError("seqused_k must have one entry per segment")
+    return _CrossAttnDesc(S, int(max_seqlen_q), int(max_seqlen_k), C, Ck, H, Hk, D,
+                          0.0 if softmax_scale is None else float(softmax_scale), q_stride, k_stride, v_stride)
+
+
+def varlen_cross_attn_workspace_size(num_segments: int, max_seqlen_q: int, max_seqlen_k: int, capacity_q: int,
+                                     capacity_k: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    desc = _CrossAttnDesc(num_segments, max_seqlen_q, max_seqlen_k, capacity_q, capacity_k, num_q_heads,
+                          num_kv_heads, head_dim)
+    return int(load_library().h3_varlen_cross_attn_workspace_size(ctypes.byref(desc)))
+
+
+def varlen_cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                          cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                          seqused_k: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                          return_lse: bool = False, lse: Optional[torch.Tensor] = None,
+                          softmax_scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None):
+    """Packed cross attention: the query rows of segment g (cu_seqlens_q, int32 [S+1]) attend to the key
+    rows of segment g (cu_seqlens_k, int32 [S+1]; its first seqused_k[g] rows when given).
+
+    q bf16 [Cq, Hq, D]; k, v bf16 [Ck, Hkv, D] with Hkv dividing Hq; each may be a part of a fused
+    projection (heads and dims contiguous, any token stride that is a multiple of 8).  max_seqlen_q
+    and max_seqlen_k bound a segment's rows and used keys.  A segment without keys gives 0 and an LSE
+    of -inf; rows of `out` outside every segment are left untouched.  Returns out [Cq, Hq, D] (and lse
+    fp32 [Hq, Cq] when requested).
+    """
+    desc = _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqused_k, softmax_scale)
+    dev = q.device
+    C, H, _ = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _require(out, "out", torch.bfloat16, dev)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if return_lse and lse is None:
+        lse = torch.empty((H, C), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _require(lse, "lse", torch.float32, dev)
+        if tuple(lse.shape) != (H, C):
+            raise ValueError("lse must be [Hq, Cq]")
+    if C > 0:
+        lib = load_library()
+        if workspace is None:
+            need = int(lib.h3_varlen_cross_attn_workspace_size(ctypes.byref(desc)))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _require(workspace, "workspace", torch.uint8, dev)
+        with _on(dev):
+            st = lib.h3_varlen_cross_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                                              _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(seqused_k),
+                                              _ptr(workspace), workspace.numel(), _stream(dev))
+        _check(st, "h3_varlen_cross_attn_fwd")
+    return (out, lse) if lse is not None else out
 
 
 def window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grid: Sequence[int],

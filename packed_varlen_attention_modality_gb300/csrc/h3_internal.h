@@ -95,6 +95,7 @@ cudaError_t launch_window_unpack(const int32_t* perm, int num_tokens, const void
 constexpr int kAttnModePacked = 0;
 constexpr int kAttnModeWindow = 1;
 constexpr int kAttnModeVsa = 2;
+constexpr int kAttnModeCross = 3;  // packed query segments, key segments of other lengths
 
 // Attention straight on the (T, H, W) grid.
 // Windows: windows of w[] cut with shift s[] (edge windows cropped), nwin[] windows per axis,
@@ -130,6 +131,12 @@ struct AttnArgs {
   int num_heads;
   int head_dim;
   float scale;
+  // cross attention: the key side (cu_seqlens, max_seqlen and capacity are the query side)
+  const int32_t* cu_seqlens_k;
+  const int32_t* seqused_k;
+  int max_seqlen_k;
+  int capacity_k;
+  int num_kv_heads;
   void* workspace;  // attn_plan_bytes(num_segments) bytes: the work plan
   void* split_area;  // packed: attn_split_bytes(head_dim) bytes after the plan, or null (no split)
   unsigned int* err;

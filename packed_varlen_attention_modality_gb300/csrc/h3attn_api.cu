@@ -70,13 +70,16 @@ EncodeTiledFn encode_tiled_fn() {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // 3-D view {D, H, rows} of a bf16 [rows, H, D] tensor; box {64, 1, 128}, 128-byte swizzle.
-bool make_qkv_map(CUtensorMap* m, const void* base, int rows, int heads, int head_dim) {
+// row_stride: elements between rows (0: heads * head_dim).
+bool make_qkv_map(CUtensorMap* m, const void* base, int rows, int heads, int head_dim,
+                  int64_t row_stride = 0) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
-                                 static_cast<cuuint64_t>(heads) * head_dim * 2};
+                                 (row_stride > 0 ? static_cast<cuuint64_t>(row_stride)
+                                                 : static_cast<cuuint64_t>(heads) * head_dim) * 2};
   const cuuint32_t box[3] = {64, 1, 128};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
@@ -108,12 +111,17 @@ bool make_window_map(CUtensorMap* m, const void* base, const int32_t grid[3], co
 }
 
 bool device_is_sm103() {
+  static std::atomic<int> cached[kMaxDevices];  // 0 until looked up; then 1 (no) or 2 (yes)
   int dev = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  const int known = cached[dev].load(std::memory_order_relaxed);
+  if (known != 0) return known == 2;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
     return false;
-  return major == 10 && minor == 3;
+  const bool yes = major == 10 && minor == 3;
+  cached[dev].store(yes ? 2 : 1, std::memory_order_relaxed);
+  return yes;
 }
 
 h3_status from_cuda(cudaError_t e) { return e == cudaSuccess ? H3_OK : H3_ERR_CUDA; }
@@ -503,6 +511,102 @@ h3_status h3_varlen_attn_fwd_noalloc(const void* q, const void* k, const void* v
   a.head_dim = head_dim;
   a.scale = softmax_scale > 0.f ? softmax_scale : static_cast<float>(1.0 / std::sqrt(head_dim));
   a.workspace = scratch;  // the plan kernel rewrites every word the attention kernel reads
+  a.err = device_error_ptr();
+  a.wait_limit_ns = h3::wait_limit_ns();
+  a.stall_after_tiles = h3::stall_after_tiles();
+  if (a.err == nullptr) return H3_ERR_CUDA;
+  return from_cuda(h3::launch_attn_fwd(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---- cross attention -------------------------------------------------------------------------------
+
+namespace {
+
+bool cross_sizes_ok(const h3_cross_attn_desc* d) {
+  return d->num_segments >= 0 && d->num_segments <= 65535 && d->max_seqlen_q >= 0 &&
+         d->max_seqlen_k >= 0 && d->capacity_q >= 0 && d->capacity_k >= 0 &&
+         d->max_seqlen_q <= d->capacity_q && d->max_seqlen_k <= d->capacity_k && d->num_q_heads > 0 &&
+         d->num_q_heads <= 65535 && d->num_kv_heads > 0 && d->num_q_heads % d->num_kv_heads == 0;
+}
+
+// Checks shared by the forward and the backward; strides are returned in elements.
+h3_status check_cross(const h3_cross_attn_desc* d, const void* q, const void* k, const void* v,
+                      const int32_t* cu_q, const int32_t* cu_k, const int32_t* seqused_k,
+                      int64_t strides[3]) {
+  if (d == nullptr || q == nullptr || cu_q == nullptr || cu_k == nullptr) return H3_ERR_NULL;
+  if (!cross_sizes_ok(d)) return H3_ERR_INVALID_ARG;
+  if (d->capacity_k > 0 && (k == nullptr || v == nullptr)) return H3_ERR_NULL;
+  if (d->head_dim != 64 && d->head_dim != 128) return H3_ERR_UNSUPPORTED;
+  if (!(d->softmax_scale <= 0.f || std::isfinite(d->softmax_scale))) return H3_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) ||
+      ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k) |
+        reinterpret_cast<uintptr_t>(seqused_k)) & 3u))
+    return H3_ERR_MISALIGNED;
+  h3_status st;
+  if ((st = token_stride(d->q_stride, d->num_q_heads, d->head_dim, &strides[0])) != H3_OK ||
+      (st = token_stride(d->k_stride, d->num_kv_heads, d->head_dim, &strides[1])) != H3_OK ||
+      (st = token_stride(d->v_stride, d->num_kv_heads, d->head_dim, &strides[2])) != H3_OK)
+    return st;
+  // work items are counted in 32 bits
+  if ((static_cast<int64_t>(d->capacity_q) / 128 + d->num_segments) * d->num_q_heads > INT32_MAX ||
+      (static_cast<int64_t>(d->capacity_k) / 128 + d->num_segments) * d->num_q_heads > INT32_MAX)
+    return H3_ERR_INVALID_ARG;
+  return H3_OK;
+}
+
+float cross_scale(const h3_cross_attn_desc* d) {
+  return d->softmax_scale > 0.f ? d->softmax_scale : static_cast<float>(1.0 / std::sqrt(d->head_dim));
+}
+
+}  // namespace
+
+size_t h3_varlen_cross_attn_workspace_size(const h3_cross_attn_desc* d) {
+  if (d == nullptr || !cross_sizes_ok(d) || d->num_segments == 0) return 0;
+  return h3::attn_workspace_bytes(d->num_segments, d->max_seqlen_k, d->head_dim);
+}
+
+h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* d, const void* q, const void* k,
+                                   const void* v, void* o, float* lse, const int32_t* cu_seqlens_q,
+                                   const int32_t* cu_seqlens_k, const int32_t* seqused_k,
+                                   void* workspace, size_t workspace_bytes, h3_stream_t stream) {
+  int64_t strides[3];
+  const h3_status st = check_cross(d, q, k, v, cu_seqlens_q, cu_seqlens_k, seqused_k, strides);
+  if (st != H3_OK) return st;
+  if (o == nullptr) return H3_ERR_NULL;
+  if (!aligned16(o) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return H3_ERR_MISALIGNED;
+  const size_t need = h3_varlen_cross_attn_workspace_size(d);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return H3_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return H3_ERR_MISALIGNED;
+  if (d->num_segments == 0 || d->max_seqlen_q == 0) return H3_OK;
+  if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
+
+  h3::AttnArgs a{};
+  a.mode = h3::kAttnModeCross;
+  // no keys at all: any valid map will do, its rows are masked
+  const bool none = d->capacity_k == 0;
+  if (!make_qkv_map(&a.tmap_q, q, d->capacity_q, d->num_q_heads, d->head_dim, strides[0]) ||
+      !make_qkv_map(&a.tmap_k, none ? q : k, none ? d->capacity_q : d->capacity_k,
+                    none ? d->num_q_heads : d->num_kv_heads, d->head_dim, strides[none ? 0 : 1]) ||
+      !make_qkv_map(&a.tmap_v, none ? q : v, none ? d->capacity_q : d->capacity_k,
+                    none ? d->num_q_heads : d->num_kv_heads, d->head_dim, strides[none ? 0 : 2]))
+    return H3_ERR_CUDA;
+  a.o = o;
+  a.lse = lse;
+  a.cu_seqlens = cu_seqlens_q;
+  a.num_segments = d->num_segments;
+  a.max_seqlen = d->max_seqlen_q;
+  a.capacity = d->capacity_q;
+  a.num_heads = d->num_q_heads;
+  a.head_dim = d->head_dim;
+  a.scale = cross_scale(d);
+  a.cu_seqlens_k = cu_seqlens_k;
+  a.seqused_k = seqused_k;
+  a.max_seqlen_k = d->max_seqlen_k;
+  a.capacity_k = d->capacity_k;
+  a.num_kv_heads = d->num_kv_heads;
+  a.workspace = workspace;
+  if (d->max_seqlen_k >= h3::kSplitMinSeqlen)
+    a.split_area = static_cast<uint8_t*>(workspace) + h3::attn_plan_bytes(d->num_segments);
   a.err = device_error_ptr();
   a.wait_limit_ns = h3::wait_limit_ns();
   a.stall_after_tiles = h3::stall_after_tiles();
