@@ -1,8 +1,6 @@
-// Softmax attention forward for sm_103a: TMA + tcgen05 + TMEM, in four variants of one kernel
+// Softmax attention forward for sm_103a: TMA + tcgen05 + TMEM, in three variants of one kernel
 // template (the warp roles, rings, barriers and TMEM plan below are shared):
 //   kModePacked  block-diagonal attention over the cu_seqlens segments of a packed sequence;
-//   kModeCross   the same with keys of another length: query segments from cu_seqlens, key segments
-//                from cu_seqlens_k (optionally cut to seqused_k keys), query heads sharing key heads;
 //   kModeWindow  3D (shifted) window attention read and written in place on a (T, H, W) grid:
 //                a 128-row tile is one 5-D TMA box of whole window frames, edge windows masked;
 //   kModeVsa     block-sparse video attention: a tile holds two 64-token query blocks, each
@@ -94,19 +92,14 @@ static_assert(kDefaultWaitLimitNs == kWaitLimitNs, "host and device default wait
 constexpr int kModePacked = kAttnModePacked;  // kernel variants (see h3_internal.h)
 constexpr int kModeWindow = kAttnModeWindow;
 constexpr int kModeVsa = kAttnModeVsa;
-constexpr int kModeCross = kAttnModeCross;
-// packed rows: segments of cu_seqlens with a plan, split and merge
-constexpr bool packed_rows(int mode) { return mode == kModePacked || mode == kModeCross; }
 constexpr int kVsaBlockRows = 64;  // rows of one VSA block = half a 128-row tile
 
 
 // Packed segments: the key/value tiles [kv0, kv0 + nkv) an item covers (all of its segment's,
 // unless the item is a chunk of a split one) and the split: (chunk << 16 | chunks), 0 for a
 // whole item; group = the split item's first entry in the split area.
-// Cross attention: the segment's keys are rows [kv_start, kv_start + kv_len) of key head kv_head.
 struct PackedChunk {
   int kv0, split, group;
-  int kv_start, kv_len, kv_head;
 };
 
 struct WorkDesc {
@@ -127,12 +120,6 @@ struct WorkDesc {
   };
 };
 
-// Key tiles of a segment.  A cross-attention segment without keys takes one tile whose keys are all
-// masked, so that its rows are written (0, with an LSE of -inf) like any others.
-__host__ __device__ constexpr int key_tiles(int keys) {
-  return keys > 0 ? (keys + kBlockN - 1) / kBlockN : 1;
-}
-
 struct ItemShape {
   bool has1;          // second query tile present
   int nkv;            // key/value tiles
@@ -141,12 +128,11 @@ struct ItemShape {
 
 template <int kMode>
 __device__ __forceinline__ ItemShape shape_of(const WorkDesc& d) {
-  if (!packed_rows(kMode)) return ItemShape{d.ntiles == 2, d.nkv, kBlockN};
+  if (kMode != kModePacked) return ItemShape{d.ntiles == 2, d.nkv, kBlockN};
   // a chunk of a split item covers key tiles [kv0, kv0 + nkv); only the segment's last key tile
   // can be partial
-  const int keys = kMode == kModeCross ? d.pk.kv_len : d.seg_len;
-  const int nkv_seg = key_tiles(keys);
-  const int last = d.pk.kv0 + d.nkv == nkv_seg ? keys - (nkv_seg - 1) * kBlockN : kBlockN;
+  const int nkv_seg = (d.seg_len + kBlockN - 1) / kBlockN;
+  const int last = d.pk.kv0 + d.nkv == nkv_seg ? d.seg_len - (nkv_seg - 1) * kBlockN : kBlockN;
   return ItemShape{d.q0 + kBlockM < d.seg_start + d.seg_len, d.nkv, last};
 }
 
@@ -284,29 +270,6 @@ __device__ __forceinline__ int checked_len(const int32_t* __restrict__ cu, int g
   return b - a;
 }
 
-// What the plan of a segmented call reads: query segments and, for cross attention, key segments.
-struct SegmentArgs {
-  const int32_t* cu;
-  int num_segments, capacity, max_seqlen, num_heads;
-  const int32_t* cu_k;    // cross attention
-  const int32_t* seqused_k;  // keys used of each segment, or null: all
-  int capacity_k, max_seqlen_k, group;  // group: query heads per key head
-};
-// Rows and keys of segment g; an invalid segment has neither.
-template <int kMode>
-__device__ __forceinline__ int2 checked_segment(const SegmentArgs& a, int g, unsigned int* err) {
-  const int len = checked_len(a.cu, g, a.capacity, a.max_seqlen, err);
-  if constexpr (kMode != kModeCross) return make_int2(len, len);
-  const int b = a.cu_k[g], e = a.cu_k[g + 1];
-  const int used = a.seqused_k != nullptr ? a.seqused_k[g] : e - b;
-  if (b < 0 || e < b || e > a.capacity_k || (g == 0 && b != 0) || used < 0 || used > e - b) {
-    record_error(err, kErrBadCuSeqlens);
-    return make_int2(0, 0);
-  }
-  if (used > a.max_seqlen_k) record_error(err, kErrBadCuSeqlens);  // computed all the same
-  return make_int2(len, used);
-}
-
 __device__ __forceinline__ uint32_t items_of(int len, int heads) {
   return static_cast<uint32_t>((len + kRowsPerItem - 1) / kRowsPerItem) * heads;
 }
@@ -327,8 +290,6 @@ constexpr int kSplitMaxChunks = 8;
 struct SplitEntry {
   int seg_start, seg_len, head, q0, kv0, kv1, group, split;  // split = chunk << 16 | chunks
 };
-constexpr int kSplitSegShift = 12;  // cross attention: segment index above the group's entry
-static_assert(kSplitMaxEntries < (1 << kSplitSegShift), "entry and segment share a word");
 static_assert(sizeof(SplitEntry) == 8 * sizeof(int32_t), "split entries are 8 words");
 __host__ __device__ constexpr size_t split_groups_offset() {  // first entries of the split items
   return static_cast<size_t>(kSplitMaxEntries) * sizeof(SplitEntry);
@@ -461,39 +422,30 @@ __device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s
   return s_warp[warp] + x - v;
 }
 
-template <int kMode>
 __global__ void __launch_bounds__(kPlanThreads)
-attn_plan_kernel(const __grid_constant__ SegmentArgs seg, uint32_t* __restrict__ ws,
-                 uint8_t* __restrict__ split_area, int wave, unsigned int* err) {
-  constexpr bool kCross = kMode == kModeCross;
+attn_plan_kernel(const int32_t* __restrict__ cu, int num_segments, int capacity, int max_seqlen,
+                 int num_heads, uint32_t* __restrict__ ws, uint8_t* __restrict__ split_area,
+                 int wave, unsigned int* err) {
   __shared__ int s_len[kSortMax];
-  __shared__ int s_keys[kCross ? kSortMax : 1];  // cross attention: keys of each segment
   __shared__ uint32_t s_prefix[kSortMax + 1];   // the item prefix again, for the split's lookups
   __shared__ uint32_t s_warp[kPlanThreads / 32 + 1];
   __shared__ uint32_t s_ngroups;
   grid_dependency_wait();  // cu_seqlens may come from the kernel before this one
   launch_dependents();     // the attention kernel may be scheduled now; it waits for this plan
-  const int32_t* __restrict__ cu = seg.cu;
-  const int S = seg.num_segments, num_heads = seg.num_heads;
+  const int S = num_segments;
   const int tid = threadIdx.x;
   uint32_t* order = ws + kWsHeader;
   uint32_t* prefix = ws + kWsHeader + S;
   const bool sorted = S <= kSortMax;
 
   if (sorted) {
-    // longest first (by keys: what an item costs), ties by position (a stable order): rank =
-    // number of segments before it
-    for (int g = tid; g < S; g += kPlanThreads) {
-      const int2 n = checked_segment<kMode>(seg, g, err);
-      s_len[g] = n.x;
-      if constexpr (kCross) s_keys[g] = n.y;
-    }
+    // longest first, ties by position (a stable order): rank = number of segments before it
+    for (int g = tid; g < S; g += kPlanThreads)
+      s_len[g] = checked_len(cu, g, capacity, max_seqlen, err);
     __syncthreads();
-    const int* s_cost = kCross ? s_keys : s_len;
     for (int g = tid; g < S; g += kPlanThreads) {
       int rank = 0;
-      for (int h = 0; h < S; ++h)
-        rank += (s_cost[h] > s_cost[g]) || (s_cost[h] == s_cost[g] && h < g);
+      for (int h = 0; h < S; ++h) rank += (s_len[h] > s_len[g]) || (s_len[h] == s_len[g] && h < g);
       order[rank] = static_cast<uint32_t>(g);
     }
   } else {
@@ -501,7 +453,7 @@ attn_plan_kernel(const __grid_constant__ SegmentArgs seg, uint32_t* __restrict__
   }
   __syncthreads();
   auto len_of = [&](int g) {
-    return sorted ? s_len[g] : checked_segment<kMode>(seg, g, err).x;
+    return sorted ? s_len[g] : checked_len(cu, g, capacity, max_seqlen, err);
   };
 
   // exclusive prefix of items over the ordered segments: per-thread chunks + block scan
@@ -552,7 +504,7 @@ attn_plan_kernel(const __grid_constant__ SegmentArgs seg, uint32_t* __restrict__
     const int loc = static_cast<int>(item - s_prefix[l]);
     head = loc / pairs;
     q0 = a + (loc % pairs) * kRowsPerItem;
-    nkv = key_tiles(kCross ? s_keys[g] : len);
+    nkv = (len + kBlockN - 1) / kBlockN;
   }
   // How many chunks: the L long items of the wave (at least kSplitMinTiles key tiles) are each cut
   // into c = wave / L chunks (at most kSplitMaxChunks, each of at least 4 key tiles), so that
@@ -586,7 +538,6 @@ attn_plan_kernel(const __grid_constant__ SegmentArgs seg, uint32_t* __restrict__
     e.kv0 = nkv * ch / c;
     e.kv1 = nkv * (ch + 1) / c;
     e.group = static_cast<int>(first);
-    if constexpr (kCross) e.group |= g << kSplitSegShift;  // the keys are found from the segment
     e.split = c > 1 ? (ch << 16 | c) : 0;
     entries[first + ch] = e;
   }
@@ -600,19 +551,11 @@ attn_plan_kernel(const __grid_constant__ SegmentArgs seg, uint32_t* __restrict__
 
 // Item index -> work descriptor: a whole item (binary search of the ordered prefix) or an entry
 // of the split last wave.
-template <int kMode>
 __device__ __forceinline__ WorkDesc decode_item(uint32_t item, const uint32_t* __restrict__ ws,
-                                                const SegmentArgs& seg,
+                                                const int32_t* __restrict__ cu, int S,
                                                 const uint8_t* __restrict__ split_area) {
-  const int32_t* __restrict__ cu = seg.cu;
-  const int S = seg.num_segments;
   WorkDesc d;
   const uint32_t tail = ws[2];
-  auto set_keys = [&](int g) {  // cross attention: the keys of (valid) segment g
-    d.pk.kv_start = seg.cu_k[g];
-    d.pk.kv_len = seg.seqused_k != nullptr ? seg.seqused_k[g] : seg.cu_k[g + 1] - d.pk.kv_start;
-    d.pk.kv_head = d.head / seg.group;
-  };
   if (item >= tail) {
     const SplitEntry e = reinterpret_cast<const SplitEntry*>(split_area)[item - tail];
     d.seg_start = e.seg_start;
@@ -623,10 +566,6 @@ __device__ __forceinline__ WorkDesc decode_item(uint32_t item, const uint32_t* _
     d.nkv = e.kv1 - e.kv0;
     d.pk.split = e.split;
     d.pk.group = e.group;
-    if constexpr (kMode == kModeCross) {
-      d.pk.group = e.group & ((1 << kSplitSegShift) - 1);
-      set_keys(e.group >> kSplitSegShift);
-    }
     return d;
   }
   const uint32_t* order = ws + kWsHeader;
@@ -648,10 +587,6 @@ __device__ __forceinline__ WorkDesc decode_item(uint32_t item, const uint32_t* _
   d.nkv = (len + kBlockN - 1) / kBlockN;
   d.pk.split = 0;
   d.pk.group = 0;
-  if constexpr (kMode == kModeCross) {
-    set_keys(g);
-    d.nkv = key_tiles(d.pk.kv_len);
-  }
   return d;
 }
 
@@ -719,7 +654,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const __grid_constant__ CUtensorMap tmap_q2,  // windows: half-height boxes
                 const __grid_constant__ CUtensorMap tmap_k2,
                 const __grid_constant__ CUtensorMap tmap_v2, __nv_bfloat16* __restrict__ out,
-                float* __restrict__ lse, const __grid_constant__ SegmentArgs seg,
+                float* __restrict__ lse, const int32_t* __restrict__ cu_seqlens, int num_segments,
                 int capacity, int num_heads, float scale, float scale_log2,
                 uint32_t* __restrict__ ws, const __grid_constant__ WindowAttnGeom wg,
                 const uint2* __restrict__ vsa_steps, const int2* __restrict__ vsa_counts,
@@ -727,8 +662,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const uint8_t* __restrict__ split_area) {
   constexpr bool kWin = kMode == kModeWindow;
   constexpr bool kVsa = kMode == kModeVsa;
-  constexpr bool kCross = kMode == kModeCross;
-  constexpr bool kPacked = packed_rows(kMode);
   using C = Cfg<D, kMode>;
   constexpr int SK = C::kStagesK;
   constexpr int SV = C::kStagesV;
@@ -782,7 +715,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
     return;
   // Packed segments: the grid is sized for the most items the capacity allows; a CTA whose first
   // item is past the plan's count has nothing to do, and leaves before any set-up.
-  if constexpr (kPacked) {
+  if constexpr (kMode == kModePacked) {
     if (blockIdx.x >= ws[1]) return;
   }
 
@@ -893,7 +826,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
             else if constexpr (kVsa)
               d = decode_vsa(item, wg, vsa_counts);
             else
-              d = decode_item<kMode>(item, ws, seg, split_area);
+              d = decode_item(item, ws, cu_seqlens, num_segments, split_area);
           } else {
             d.seg_start = 0;
             d.seg_len = -1;
@@ -913,14 +846,14 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const bool hhalf = kWin && d.hbox != wg.w[1];
           // packed segments: every CTA of a (segment, head) streams the same key/value tiles, so
           // they are kept in L2 in preference to the query tiles, which are read once
-          auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, int head, int tile, int row,
+          auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, int tile, int row,
                                uint32_t bar, uint64_t policy) {
             for (int b = 0; b < C::kBoxes; ++b) {
               if constexpr (kWin)
-                tma_load_5d(smem_u32(dst + b * C::kBoxBytes), map, b * 64, head, d.box[2],
+                tma_load_5d(smem_u32(dst + b * C::kBoxBytes), map, b * 64, d.head, d.box[2],
                             d.box[1], d.box[0] + tile * d.fpt, bar);
               else
-                tma_load_3d_hint(smem_u32(dst + b * C::kBoxBytes), map, b * 64, head, row, bar,
+                tma_load_3d_hint(smem_u32(dst + b * C::kBoxBytes), map, b * 64, d.head, row, bar,
                                  policy);
             }
           };
@@ -944,8 +877,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
           } else {
             for (int t = 0; t < (has1 ? 2 : 1); ++t) {
               mbar_arrive_expect_tx(bar_qfull(t), C::kTileBytes);
-              load_tile(sQ + t * C::kTileBytes, hhalf ? &tmap_q2 : &tmap_q, d.head, t,
-                        d.q0 + t * kBlockM, bar_qfull(t), pol_stream);
+              load_tile(sQ + t * C::kTileBytes, hhalf ? &tmap_q2 : &tmap_q, t, d.q0 + t * kBlockM,
+                        bar_qfull(t), pol_stream);
               ++qn[t];
             }
             for (int j = 0; j < nkv && ok; ++j) {
@@ -953,21 +886,20 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 stalled = true;
                 break;
               }
-              const int row = (kCross ? d.pk.kv_start : d.seg_start) + (d.pk.kv0 + j) * kBlockN;
-              const int kv_head = kCross ? d.pk.kv_head : d.head;
+              const int row = d.seg_start + (d.pk.kv0 + j) * kBlockN;
               const int s = static_cast<int>(kt % SK);
               ok = pwait(bar_kempty(s), ((kt / SK) & 1) ^ 1);
               if (!ok) break;
               mbar_arrive_expect_tx(bar_kfull(s), C::kTileBytes);
-              load_tile(sK + s * C::kTileBytes, hhalf ? &tmap_k2 : &tmap_k, kv_head, j, row,
-                        bar_kfull(s), pol_keep);
+              load_tile(sK + s * C::kTileBytes, hhalf ? &tmap_k2 : &tmap_k, j, row, bar_kfull(s),
+                        pol_keep);
               ++kt;
               const int v = static_cast<int>(vt % SV);
               ok = pwait(bar_vempty(v), ((vt / SV) & 1) ^ 1);
               if (!ok) break;
               mbar_arrive_expect_tx(bar_vfull(v), C::kTileBytes);
-              load_tile(sV + v * C::kTileBytes, hhalf ? &tmap_v2 : &tmap_v, kv_head, j, row,
-                        bar_vfull(v), pol_keep);
+              load_tile(sV + v * C::kTileBytes, hhalf ? &tmap_v2 : &tmap_v, j, row, bar_vfull(v),
+                        pol_keep);
               ++vt;
             }
             if (stalled) break;
@@ -1407,8 +1339,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
         for (int u = 0; u < 4; ++u) m4[u] = fmaxf(m4[u], s[124 + u]);
         update_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), j);
-        // a cross-attention row without keys has no max: its weights are exp2(-inf) = 0
-        const float mb = kCross && m_used == -INFINITY ? 0.f : m_used * scale_log2;
+        const float mb = m_used * scale_log2;
         const float2 nm2 = make_float2(-mb, -mb);
         float2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
         uint32_t p[64];
@@ -1475,9 +1406,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
         q_row = d.q0 + t * kBlockM + row;
         valid = q_row < seg_end;
       }
-      const float inv_l = kCross && l == 0.f ? 0.f : 1.f / l;
+      const float inv_l = 1.f / l;
       __nv_bfloat16* orow = out + (static_cast<size_t>(q_row) * num_heads + d.head) * D;
-      if constexpr (kPacked) {
+      if constexpr (kMode == kModePacked) {
         if (d.pk.split != 0) {
           // a chunk of a split item: its partial result (O normalised by its own row sum, and
           // its LSE) goes to the split area; attn_merge_kernel combines the chunks afterwards
@@ -1518,7 +1449,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint4 val = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-            if constexpr (kPacked)
+            if constexpr (kMode == kModePacked)
               st_global_v4_hint(dst + c, val, pol_out);  // written once: not kept over K/V
             else
               dst[c] = val;
@@ -1561,17 +1492,6 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return cudaErrorInvalidDevice;
   uint32_t* ws = static_cast<uint32_t*>(a.workspace);
-  SegmentArgs seg{};
-  seg.cu = a.cu_seqlens;
-  seg.num_segments = a.num_segments;
-  seg.capacity = a.capacity;
-  seg.max_seqlen = a.max_seqlen;
-  seg.num_heads = a.num_heads;
-  seg.cu_k = a.cu_seqlens_k;
-  seg.seqused_k = a.seqused_k;
-  seg.capacity_k = a.capacity_k;
-  seg.max_seqlen_k = a.max_seqlen_k;
-  seg.group = kMode == kModeCross ? a.num_heads / a.num_kv_heads : 1;
   long long max_items, want;
   if (kMode == kModeWindow) {
     // windows hold at most 256 rows: one CTA per SM looping over (window, head) items
@@ -1583,7 +1503,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     max_items = (nblk + 3) / 4 * a.num_heads;
     want = sms;
   } else {
-    e = launch_programmatic(attn_plan_kernel<kMode>, dim3(1), dim3(kPlanThreads), 0, stream, seg, ws,
+    e = launch_programmatic(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.cu_seqlens,
+                            a.num_segments, a.capacity, a.max_seqlen, a.num_heads, ws,
                             static_cast<uint8_t*>(a.split_area), sms, a.err);
     if (e != cudaSuccess) return e;
     e = cudaGetLastError();
@@ -1596,8 +1517,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
     // short chunks overlap one another's set-up and epilogue
     const bool short_job = max_items <= static_cast<long long>(kPersistMaxWaves) * sms;
     if (a.split_area != nullptr) max_items += kSplitMaxEntries;  // chunks of a split last wave
-    const int max_keys = kMode == kModeCross ? a.max_seqlen_k : a.max_seqlen;
-    want = (max_keys <= kPersistMaxSeqlen || short_job) ? sms : max_items;
+    want = (a.max_seqlen <= kPersistMaxSeqlen || short_job) ? sms : max_items;
   }
   if (max_items <= 0) return cudaSuccess;
   const int grid = static_cast<int>(max_items < want ? max_items : want);
@@ -1606,11 +1526,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   e = launch_programmatic(
       attn_fwd_kernel<D, kMode>, dim3(grid), dim3(kThreads), C::kSmemBytes, stream, a.tmap_q,
       a.tmap_k, a.tmap_v, half ? a.tmap_q2 : a.tmap_q, half ? a.tmap_k2 : a.tmap_k,
-      half ? a.tmap_v2 : a.tmap_v, static_cast<__nv_bfloat16*>(a.o), a.lse, seg, a.capacity, a.num_heads, a.scale, scale_log2, static_cast<uint32_t*>(ws),
+      half ? a.tmap_v2 : a.tmap_v, static_cast<__nv_bfloat16*>(a.o), a.lse, a.cu_seqlens,
+      a.num_segments, a.capacity, a.num_heads, a.scale, scale_log2, static_cast<uint32_t*>(ws),
       a.wg, a.vsa_steps, a.vsa_counts, a.err, static_cast<unsigned long long>(a.wait_limit_ns),
       a.stall_after_tiles, static_cast<const uint8_t*>(a.split_area));
   if (e != cudaSuccess) return e;
-  if (packed_rows(kMode) && a.split_area != nullptr)
+  if (kMode == kModePacked && a.split_area != nullptr)
     e = launch_programmatic(attn_merge_kernel<D>, dim3(4 * sms), dim3(kMergeThreads), 0, stream,
                             static_cast<const uint32_t*>(ws),
                             static_cast<const uint8_t*>(a.split_area),
@@ -1632,10 +1553,6 @@ cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t stream) {
     return launch<64, kModeVsa>(a, stream);
   }
   if (a.max_seqlen <= 0 || a.num_segments <= 0) return cudaSuccess;
-  if (a.mode == kModeCross) {
-    if (a.head_dim == 128) return launch<128, kModeCross>(a, stream);
-    return launch<64, kModeCross>(a, stream);
-  }
   if (a.head_dim == 128) return launch<128, kModePacked>(a, stream);
   return launch<64, kModePacked>(a, stream);
 }

@@ -1,0 +1,944 @@
+// Packed cross attention forward for sm_103a (TMA + tcgen05 + TMEM): query segments attend to key
+// segments of other lengths (an encoder's states), query heads share key heads.
+//
+//   S = scale q k^T over the segment's keys,  P = softmax(S),  o = P v,  lse = log sum exp(S)
+//
+// Work item: two 128-row query tiles that share a (segment, key head): consecutive tiles of the
+// key head's query heads, so with shared heads a segment of few rows still fills both tiles.  Both
+// stream the same key/value tiles.  One CTA per SM takes items c, c + G, ... of a list ordered by
+// key count; what a last, partly filled wave leaves idle is used by cutting its items' key ranges
+// into chunks, which a merge kernel joins in chunk order.
+//
+// An encoder's key lists are short (a few 128-key tiles), so an item is over after a few thousand
+// cycles and what happens between items costs as much as the items do.  Hence:
+//   - the MMA warp runs straight on from one item into the next (order PV0_last, S0_first of the
+//     next item, PV1_last, S1_first: the boundary looks like any other step);
+//   - O is read out, normalised and stored by a warpgroup of its own, which hands the accumulator
+//     back before it stores, while the softmax warpgroups are in the next item;
+//   - items are decoded one ahead, and queries and keys have a producer each, so neither waits on
+//     the other's ring;
+//   - a last key tile is multiplied only as far as it holds keys (in steps of 16).
+// With all of it in the softmax warpgroups and one producer (the packed self-attention kernel's
+// structure), 58,758 rows x 558 keys x 40 heads x 128 took 787 us.
+//
+// Warp roles (512 threads; registers moved with setmaxnreg):
+//   warps 0-3 / 4-7   softmax of query tile 0 / 1: thread r owns row r = TMEM lane r
+//   warps 8-11        epilogue of both tiles
+//   warps 12, 13, 15  key/value producer, MMA issuer, scheduler + query producer
+// TMEM (512 columns): O0 [0,128), O1 [128,256), S0/P0 [256,384), S1/P1 [384,512).
+// Shared memory at D = 128: 2 Q + 3 K + 2 V tiles of 32 KB.
+//
+// Keys past the segment's end are masked to -inf by select and the value rows PV reads past it are
+// zeroed in shared memory, so NaN/Inf there cannot leak.  A segment without keys takes one tile
+// whose keys are all masked: its rows come out as 0 with an LSE of -inf.
+// P is rounded to bf16 for the tensor core (half a step, 2^-9 of each weight on average); scores,
+// running max and sum, and O stay fp32, and the result is rounded to bf16 once.
+// Every wait is bounded; a wait that runs out records a timeout and unwinds the CTA.
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "h3_internal.h"
+#include "launch.h"
+#include "sm103_ptx.cuh"
+
+namespace h3 {
+namespace {
+
+constexpr int kBlockM = 128, kBlockN = 128;
+constexpr int kThreads = 512;
+constexpr int kRegsSoftmax = 176, kRegsEpilogue = 64, kRegsOther = 96;
+static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOther == 65536 / 128, "the split of the registers at launch");
+constexpr int kTmemCols = 512, kColO = 0, kColS = 256;
+constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the running max grows by > 2^8
+constexpr int kPlanThreads = 1024;
+constexpr int kSortMax = 256;         // segments ordered by keys up to this count
+constexpr int kHeader = kAttnWsHeaderWords;
+constexpr int kSplitMinTiles = 8;     // cut only items of at least 8 key tiles
+constexpr int kSplitMaxChunks = 64;
+
+__host__ __device__ constexpr int key_tiles(int keys) {
+  return keys > 0 ? (keys + kBlockN - 1) / kBlockN : 1;
+}
+
+// A chunk of the last wave (or a whole item of it): key tiles [kv0, kv1) of a segment's item.
+struct CrossEntry {
+  int segment, kv_head, pair, kv0, kv1;
+  int first;          // the item's first entry
+  int chunk, chunks;  // chunks == 1: whole
+};
+static_assert(sizeof(CrossEntry) == 8 * sizeof(int32_t), "entries are 8 words");
+__host__ __device__ constexpr size_t split_items_offset() {  // first entries of the cut items
+  return static_cast<size_t>(kSplitMaxEntries) * sizeof(CrossEntry);
+}
+__host__ __device__ constexpr size_t split_partials_offset() {
+  return split_items_offset() + static_cast<size_t>(kSplitMaxEntries) * sizeof(uint32_t);
+}
+template <int D>
+constexpr size_t kPartial = static_cast<size_t>(kBlockM) * (D + 1);  // floats of a tile's partial
+
+// Rows and keys of segment g; an invalid segment has neither.
+__device__ __forceinline__ int2 checked_segment(const CrossSegments& s, int g, unsigned int* err) {
+  const int a = s.cu_q[g], b = s.cu_q[g + 1], ka = s.cu_k[g], kb = s.cu_k[g + 1];
+  const int used = s.seqused_k != nullptr ? s.seqused_k[g] : kb - ka;
+  if (a < 0 || b < a || b > s.capacity_q || ka < 0 || kb < ka || kb > s.capacity_k || used < 0 ||
+      used > kb - ka || (g == 0 && (a != 0 || ka != 0))) {
+    record_error(err, kErrBadCuSeqlens);
+    return make_int2(0, 0);
+  }
+  if (b - a > s.max_seqlen_q || used > s.max_seqlen_k) record_error(err, kErrBadCuSeqlens);
+  return make_int2(b - a, used);
+}
+// Items of a segment per key head: pairs of its group * ceil(rows / 128) tiles.
+__device__ __forceinline__ int pairs_of(int rows, int group) {
+  return ((rows + kBlockM - 1) / kBlockM * group + 1) / 2;
+}
+
+__device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s_warp,
+                                                         uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+#pragma unroll 1
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    all += s_warp[w];
+  }
+  total = all;
+  return before + x - v;
+}
+
+// Plan: segment order and item prefix, and the entries of the last wave.  Words of ws: [0] cut
+// items, [1] work items, [2] whole items before the last wave, [3] its entries, then the order
+// [S] and the exclusive prefix [S + 1].
+__global__ void __launch_bounds__(kPlanThreads)
+cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws,
+                  uint8_t* __restrict__ split_area, int wave, unsigned int* err) {
+  __shared__ int s_rows[kSortMax], s_keys[kSortMax], s_order[kSortMax];
+  __shared__ uint32_t s_prefix[kSortMax + 1];
+  __shared__ uint32_t s_warp[kPlanThreads / 32];
+  __shared__ uint32_t s_cut;
+  grid_dependency_wait();
+  launch_dependents();
+  const int S = seg.num_segments, tid = threadIdx.x;
+  uint32_t* order = ws + kHeader;
+  uint32_t* prefix = ws + kHeader + S;
+  const bool sorted = S <= kSortMax;
+  const int group = seg.num_q_heads / seg.num_kv_heads;
+  if (sorted) {
+    if (tid < S) {
+      const int2 n = checked_segment(seg, tid, err);
+      s_rows[tid] = n.x;
+      s_keys[tid] = n.y;
+    }
+    __syncthreads();
+    if (tid < S) {  // most keys first, ties by position
+      int rank = 0;
+      for (int h = 0; h < S; ++h)
+        rank += s_keys[h] > s_keys[tid] || (s_keys[h] == s_keys[tid] && h < tid);
+      s_order[rank] = tid;
+    }
+    __syncthreads();
+  }
+  auto items_at = [&](int i) -> uint32_t {  // of the segment in place i
+    const int rows = sorted ? s_rows[s_order[i]] : checked_segment(seg, i, err).x;
+    return static_cast<uint32_t>(pairs_of(rows, group)) * seg.num_kv_heads;
+  };
+  const int chunk = (S + kPlanThreads - 1) / kPlanThreads;
+  const int lo = min(S, tid * chunk), hi = min(S, lo + chunk);
+  uint32_t local = 0, total;
+  for (int i = lo; i < hi; ++i) local += items_at(i);
+  uint32_t run = block_exclusive_scan(local, s_warp, total);
+  for (int i = lo; i < hi; ++i) {
+    order[i] = static_cast<uint32_t>(sorted ? s_order[i] : i);
+    prefix[i] = run;
+    if (sorted) s_prefix[i] = run;
+    run += items_at(i);
+  }
+  if (tid == 0) {
+    prefix[S] = total;
+    if (sorted) s_prefix[S] = total;
+  }
+  const uint32_t tail = total / wave * wave, R = total - tail;
+  if (split_area == nullptr || !sorted || R == 0 || R > static_cast<uint32_t>(kSplitMaxEntries)) {
+    if (tid == 0) {
+      ws[0] = 0;
+      ws[1] = ws[2] = total;
+      ws[3] = 0;
+    }
+    return;
+  }
+  __syncthreads();  // the prefix is complete
+  CrossEntry e{};
+  int nkv = 0;
+  if (tid < static_cast<int>(R)) {
+    const uint32_t item = tail + tid;
+    int l = 0, h = S - 1;
+    while (l < h) {
+      const int mid = (l + h + 1) >> 1;
+      if (s_prefix[mid] <= item) l = mid; else h = mid - 1;
+    }
+    e.segment = s_order[l];
+    const int pairs = pairs_of(s_rows[e.segment], group);
+    const int loc = static_cast<int>(item - s_prefix[l]);
+    e.kv_head = loc / pairs;
+    e.pair = loc % pairs;
+    nkv = key_tiles(s_keys[e.segment]);
+  }
+  // The wave's long items are cut so that their chunks about fill one round of its CTAs, each of
+  // at least 4 key tiles.
+  const bool longish = nkv >= kSplitMinTiles;
+  uint32_t n_long, entries;
+  block_exclusive_scan(longish ? 1u : 0u, s_warp, n_long);
+  const int want = n_long > 0 ? min(kSplitMaxChunks, wave / static_cast<int>(n_long)) : 1;
+  int c = tid < static_cast<int>(R) ? (longish ? max(1, min(want, nkv / 4)) : 1) : 0;
+  uint32_t first = block_exclusive_scan(static_cast<uint32_t>(c), s_warp, entries);
+  if (entries > static_cast<uint32_t>(kSplitMaxEntries)) {  // more than the area holds: stay whole
+    c = tid < static_cast<int>(R) ? 1 : 0;
+    first = static_cast<uint32_t>(tid);
+    entries = R;
+  }
+  if (tid == 0) s_cut = 0u;
+  __syncthreads();
+  if (c > 1)  // listed for the merge; the list's order is immaterial
+    reinterpret_cast<uint32_t*>(split_area + split_items_offset())[atomicAdd(&s_cut, 1u)] = first;
+  __syncthreads();
+  e.first = static_cast<int>(first);
+  e.chunks = c;
+  for (e.chunk = 0; e.chunk < c; ++e.chunk) {
+    e.kv0 = static_cast<int>(static_cast<int64_t>(nkv) * e.chunk / c);
+    e.kv1 = static_cast<int>(static_cast<int64_t>(nkv) * (e.chunk + 1) / c);
+    reinterpret_cast<CrossEntry*>(split_area)[first + e.chunk] = e;
+  }
+  if (tid == 0) {
+    ws[0] = s_cut;
+    ws[1] = tail + entries;
+    ws[2] = tail;
+    ws[3] = entries;
+  }
+}
+
+struct CrossWork {
+  int ntiles;           // 0: no more work
+  int q0[2], head[2];   // first row and query head of each tile
+  int seg_end;
+  int kv_row, kv_head;  // first key row of the item's first key tile
+  int nkv, last_keys;   // key tiles, and keys in the last of them (0: a segment without keys)
+  int partial;          // entry whose partial results the item writes, -1 for o itself
+};
+
+__device__ __forceinline__ CrossWork decode(uint32_t item, const uint32_t* __restrict__ ws,
+                                            const CrossSegments& seg,
+                                            const uint8_t* __restrict__ split_area) {
+  const int S = seg.num_segments, group = seg.num_q_heads / seg.num_kv_heads;
+  const uint32_t tail = ws[2];
+  CrossWork d;
+  int g, pair, kv0 = 0, kv1 = -1;
+  d.partial = -1;
+  if (item >= tail) {
+    const CrossEntry e = reinterpret_cast<const CrossEntry*>(split_area)[item - tail];
+    g = e.segment;
+    pair = e.pair;
+    d.kv_head = e.kv_head;
+    kv0 = e.kv0;
+    kv1 = e.kv1;
+    if (e.chunks > 1) d.partial = e.first + e.chunk;
+  } else {
+    const uint32_t* prefix = ws + kHeader + S;
+    int lo = 0, hi = S - 1;  // last i with prefix[i] <= item
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= item) lo = mid; else hi = mid - 1;
+    }
+    g = static_cast<int>((ws + kHeader)[lo]);
+    const int pairs = pairs_of(seg.cu_q[g + 1] - seg.cu_q[g], group);
+    const int loc = static_cast<int>(item - prefix[lo]);
+    d.kv_head = loc / pairs;
+    pair = loc % pairs;
+  }
+  const int a = seg.cu_q[g];
+  d.seg_end = seg.cu_q[g + 1];
+  const int per_head = (d.seg_end - a + kBlockM - 1) / kBlockM;
+  d.ntiles = min(2, per_head * group - 2 * pair);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int tile = 2 * pair + t;
+    d.head[t] = d.kv_head * group + tile / per_head;
+    d.q0[t] = a + tile % per_head * kBlockM;
+  }
+  const int ka = seg.cu_k[g];
+  const int keys = seg.seqused_k != nullptr ? seg.seqused_k[g] : seg.cu_k[g + 1] - ka;
+  const int all = key_tiles(keys);
+  if (kv1 < 0) kv1 = all;
+  d.nkv = kv1 - kv0;
+  d.last_keys = kv1 == all ? keys - (all - 1) * kBlockN : kBlockN;
+  d.kv_row = ka + kv0 * kBlockN;
+  return d;
+}
+
+template <int D>
+struct Cfg {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kBlockM * D * 2;
+  static constexpr int kBoxBytes = kBlockM * 128;
+  static constexpr int kStagesK = D == 128 ? 3 : 4, kStagesV = D == 128 ? 2 : 4;
+  // q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_final[2], o_empty[2], l_full[2],
+  // w_full[2], w_empty[2], drain, then k_full, k_empty, v_full, v_empty
+  static constexpr int kNumBars = 21 + 2 * kStagesK + 2 * kStagesV;
+  static constexpr int kSmemBytes = 1024 + kTileBytes * (2 + kStagesK + kStagesV) + kNumBars * 8 + 24 +
+                                    2 * sizeof(CrossWork) + 2 * kBlockM * sizeof(float);
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+  static constexpr uint32_t kIdescQK = idesc_bf16_f32(kBlockM, kBlockN, false);
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(kBlockM, D, true);
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                  const __grid_constant__ CUtensorMap tmap_v, __nv_bfloat16* __restrict__ out,
+                  float* __restrict__ lse, const __grid_constant__ CrossSegments seg, float scale,
+                  float scale_log2, const uint32_t* __restrict__ ws, uint8_t* __restrict__ split_area,
+                  unsigned int* err, unsigned long long wait_ns, unsigned int stall_after) {
+  using C = Cfg<D>;
+  constexpr int SK = C::kStagesK, SV = C::kStagesV;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + 2 * C::kTileBytes;
+  uint8_t* sV = sK + SK * C::kTileBytes;
+  float* s_norm = reinterpret_cast<float*>(sV + SV * C::kTileBytes);  // [2][128]: 1 / row sum
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_norm + 2 * kBlockM);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  CrossWork* work = reinterpret_cast<CrossWork*>(tmem_slot + 2);  // 2-slot ring
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8 * static_cast<uint32_t>(i); };
+  auto bar_qfull = [&](int t) { return bar(t); };
+  auto bar_qempty = [&](int t) { return bar(2 + t); };
+  auto bar_sfull = [&](int t) { return bar(4 + t); };
+  auto bar_phalf = [&](int t) { return bar(6 + t); };
+  auto bar_pfull = [&](int t) { return bar(8 + t); };
+  auto bar_ofinal = [&](int t) { return bar(10 + t); };
+  auto bar_oempty = [&](int t) { return bar(12 + t); };
+  auto bar_lfull = [&](int t) { return bar(14 + t); };
+  auto bar_wfull = [&](int i) { return bar(16 + i); };
+  auto bar_wempty = [&](int i) { return bar(18 + i); };
+  const uint32_t bar_drain = bar(20);
+  auto bar_kfull = [&](int s) { return bar(21 + s); };
+  auto bar_kempty = [&](int s) { return bar(21 + SK + s); };
+  auto bar_vfull = [&](int s) { return bar(21 + 2 * SK + s); };
+  auto bar_vempty = [&](int s) { return bar(21 + 2 * SK + SV + s); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto pwait = [&](uint32_t b, uint32_t parity) { return mbar_wait(b, parity, wait_ns); };
+  // The whole warp polls: a branch for one lane would leave the warp diverged behind it.
+  auto wait_all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, pwait(b, parity)) != 0; };
+  auto wait_long = [&](uint32_t b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_long(b, parity, wait_ns)) != 0;
+  };
+  // One arrival for the warp, after what all its lanes did.
+  auto arrive_warp = [&](uint32_t b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b);
+  };
+
+  grid_dependency_wait();
+  launch_dependents();
+  // a timeout recorded earlier and not read yet: leave at once, all threads together
+  if (__syncthreads_or(err != nullptr && *reinterpret_cast<volatile unsigned int*>(err) == kErrTimeout))
+    return;
+  if (blockIdx.x >= ws[1]) return;
+
+  if (warp == 12 && lane == 0) {
+    tma_prefetch_desc(&tmap_q);
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_qfull(t), 1);
+      mbar_init(bar_qempty(t), 1);
+      mbar_init(bar_sfull(t), 1);
+      mbar_init(bar_phalf(t), 4);  // warps
+      mbar_init(bar_pfull(t), 4);  // warps
+      mbar_init(bar_ofinal(t), 1);
+      mbar_init(bar_oempty(t), 4);  // warps
+      mbar_init(bar_lfull(t), 4);  // warps
+      mbar_init(bar_wfull(t), 1);
+      mbar_init(bar_wempty(t), 14);  // 12 softmax and epilogue warps, key/value producer, MMA warp
+    }
+    for (int s = 0; s < SK; ++s) {
+      mbar_init(bar_kfull(s), 1);
+      mbar_init(bar_kempty(s), 1);
+    }
+    for (int s = 0; s < SV; ++s) {
+      mbar_init(bar_vfull(s), 1);
+      mbar_init(bar_vempty(s), 1);
+    }
+    mbar_init(bar_drain, 1);
+    fence_mbarrier_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Item k from the ring, for one warp (every lane calls).  False when the wait ran out.
+  auto take = [&](int k, CrossWork& d) {
+    if (!wait_long(bar_wfull(k & 1), (k >> 1) & 1)) return false;
+    d = work[k & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_wempty(k & 1));
+    return true;
+  };
+
+  if (warp >= 12) {
+    setmaxnreg_dec<kRegsOther>();
+    if (warp == 12) {
+      // ================= key/value producer =================
+      const uint64_t pol_keep = l2_policy_evict_last();  // shared by the CTAs of a key head
+      uint32_t kt = 0, vt = 0;
+      bool ok = true, stalled = false;
+      CrossWork d;
+      for (int k = 0; ok && !stalled; ++k) {
+        ok = take(k, d);
+        if (!ok || d.ntiles == 0) break;
+        auto load = [&](uint8_t* dst, const CUtensorMap* map, int row, uint32_t b) {
+          if (lane != 0) return;
+          mbar_arrive_expect_tx(b, C::kTileBytes);
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_load_3d_hint(smem_u32(dst + x * C::kBoxBytes), map, x * 64, d.kv_head, row, b, pol_keep);
+        };
+        for (int j = 0; j < d.nkv; ++j) {
+          if (kt >= stall_after) {  // testing hook: as if the loads had stalled
+            stalled = true;
+            break;
+          }
+          const int s = static_cast<int>(kt % SK), v = static_cast<int>(vt % SV);
+          ok = wait_long(bar_kempty(s), ((kt / SK) & 1) ^ 1);
+          if (!ok) break;
+          load(sK + s * C::kTileBytes, &tmap_k, d.kv_row + j * kBlockN, bar_kfull(s));
+          ++kt;
+          ok = wait_long(bar_vempty(v), ((vt / SV) & 1) ^ 1);
+          if (!ok) break;
+          load(sV + v * C::kTileBytes, &tmap_v, d.kv_row + j * kBlockN, bar_vfull(v));
+          ++vt;
+        }
+      }
+      if (!ok && lane == 0) record_error(err, kErrTimeout);
+      // never leave while a copy may still land: the last loads sit on distinct stages
+      for (uint32_t i = 0; i < SK && i < kt; ++i) mbar_wait(bar_kfull((kt - 1 - i) % SK), ((kt - 1 - i) / SK) & 1);
+      for (uint32_t i = 0; i < SV && i < vt; ++i) mbar_wait(bar_vfull((vt - 1 - i) % SV), ((vt - 1 - i) / SV) & 1);
+    } else if (warp == 15) {
+      // ================= scheduler and query producer =================
+      const uint32_t total = ws[1];
+      const uint64_t pol_stream = l2_policy_evict_first();
+      uint32_t qn[2] = {0u, 0u};
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const uint32_t item = blockIdx.x + static_cast<uint32_t>(k) * gridDim.x;
+        CrossWork d{};
+        if (item < total) d = decode(item, ws, seg, split_area);
+        ok = wait_long(bar_wempty(k & 1), ((k >> 1) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          work[k & 1] = d;
+          mbar_arrive(bar_wfull(k & 1));
+        }
+        __syncwarp();
+        if (d.ntiles == 0) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t >= d.ntiles) break;
+          ok = wait_long(bar_qempty(t), (qn[t] & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar_qfull(t), C::kTileBytes);
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_load_3d_hint(smem_u32(sQ + t * C::kTileBytes + x * C::kBoxBytes), &tmap_q, x * 64,
+                               d.head[t], d.q0[t], bar_qfull(t), pol_stream);
+          }
+          ++qn[t];
+        }
+      }
+      if (!ok && lane == 0) record_error(err, kErrTimeout);
+      for (int t = 0; t < 2; ++t)
+        if (qn[t] > 0) mbar_wait(bar_qfull(t), (qn[t] - 1) & 1);
+    } else if (warp == 13) {
+      // ================= MMA issuer =================
+      auto wait_all2 = [&](uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {  // polls overlap
+        bool r0 = mbar_try_wait(b0, p0), r1 = mbar_try_wait(b1, p1);
+        if (!r0) r0 = pwait(b0, p0);
+        if (!r1) r1 = pwait(b1, p1);
+        return __all_sync(0xffffffffu, r0 && r1);
+      };
+      constexpr uint32_t kTile16 = C::kTileBytes >> 4;
+      const SmemDesc dq = sw128_desc_split(smem_u32(sQ), 16, 1024);
+      const SmemDesc dk = sw128_desc_split(smem_u32(sK), 16, 1024);
+      const SmemDesc dv = sw128_desc_split(smem_u32(sV), C::kBoxBytes, 1024);
+      auto issue_qk = [&](int t, int s, uint32_t idesc) {  // S_t = Q_t K_s^T
+        const uint32_t qlo = dq.lo + t * kTile16, klo = dk.lo + s * kTile16;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
+          mma_ss_split(tmem + kColS + 128 * t, qlo + off, dq.hi, klo + off, dk.hi, idesc, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar_sfull(t));
+      };
+      // O_t += P_t V_s over one half of the tile's 16-key steps, as far as `end`
+      auto issue_pv = [&](int t, int s, bool first, int half, int end) {
+        const uint32_t p = tmem + kColS + 128 * t + half * (kBlockN / 32) * 8;
+        const uint32_t vlo = dv.lo + s * kTile16 + half * (kBlockN / 32) * (2048 >> 4);
+        const int n = end - half * (kBlockN / 32);
+        if (n >= kBlockN / 32) {
+#pragma unroll
+          for (int kk = 0; kk < kBlockN / 32; ++kk)
+            mma_ts_split(tmem + kColO + 128 * t, p + kk * 8, vlo + kk * (2048 >> 4), dv.hi, C::kIdescPV,
+                         (!first || kk > 0) ? 1u : 0u);
+        } else {
+#pragma unroll 1
+          for (int kk = 0; kk < n; ++kk)
+            mma_ts_split(tmem + kColO + 128 * t, p + kk * 8, vlo + kk * (2048 >> 4), dv.hi, C::kIdescPV,
+                         (!first || kk > 0) ? 1u : 0u);
+        }
+      };
+      const bool leader = elect_one();
+      struct Item {  // what is needed of an item here
+        int ntiles, nkv, last_keys;
+      } cur{0, 0, 0}, nxt{0, 0, 0};
+      auto take_item = [&](int k, Item& i) {
+        if (!wait_all(bar_wfull(k & 1), (k >> 1) & 1)) return false;
+        i = Item{work[k & 1].ntiles, work[k & 1].nkv, work[k & 1].last_keys};
+        __syncwarp();
+        if (leader) mbar_arrive(bar_wempty(k & 1));
+        return true;
+      };
+      // an item's last key tile is multiplied as far as it holds keys, but at least one step
+      auto steps16 = [](int keys) { return max(1, (keys + 15) / 16); };
+      auto idesc_of = [&](const Item& i, int j) {
+        return j == i.nkv - 1 && i.last_keys < kBlockN
+                   ? idesc_bf16_f32(kBlockM, 16 * steps16(i.last_keys), false) : C::kIdescQK;
+      };
+      uint32_t kc = 0, vc = 0;  // K / V tiles consumed
+      uint32_t qn[2] = {0u, 0u}, pn[2] = {0u, 0u}, un[2] = {0u, 0u};
+      bool ok = take_item(0, cur), issued = false;
+      if (ok && cur.ntiles > 0) {  // the first item's first scores
+        ok = wait_all(bar_kfull(0), 0);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || t >= cur.ntiles) break;
+          ok = wait_all(bar_qfull(t), qn[t]++ & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            issue_qk(t, 0, idesc_of(cur, 0));
+            if (cur.nkv == 1) mma_commit(bar_qempty(t));
+            if (t == cur.ntiles - 1) mma_commit(bar_kempty(0));
+          }
+          issued = true;
+          __syncwarp();
+        }
+        kc = 1;
+      }
+      for (int k = 0; ok && cur.ntiles > 0; ++k) {
+        for (int j = 0; j < cur.nkv && ok; ++j) {
+          const bool last = j + 1 == cur.nkv;
+          const int sv = static_cast<int>(vc % SV), sk = static_cast<int>(kc % SK);
+          if (last) {
+            ok = take_item(k + 1, nxt);
+            if (!ok) break;
+          }
+          // the scores issued in this step: the item's next key tile, or the next item's first
+          const int stiles = last ? nxt.ntiles : cur.ntiles;
+          const uint32_t idesc = last ? idesc_of(nxt, 0) : idesc_of(cur, j + 1);
+          const bool q_done = last ? nxt.nkv == 1 : j + 2 == cur.nkv;  // their item's last scores
+          const int end = last ? steps16(cur.last_keys) : kBlockN / 16;
+          ok = wait_all2(bar_vfull(sv), (vc / SV) & 1, bar_phalf(0), pn[0] & 1);
+          if (!ok) break;
+          if (last && cur.last_keys < 16 * end) {
+            // zero the value rows past the keys as far as PV reads (whole 128-byte rows: the
+            // swizzle permutes 16-byte pieces within a row)
+            uint8_t* vb = sV + sv * C::kTileBytes;
+            const int nrows = 16 * end - cur.last_keys;
+            for (int i = lane; i < nrows * C::kBoxes * 8; i += 32) {
+              const int r = cur.last_keys + i / (C::kBoxes * 8), rem = i % (C::kBoxes * 8);
+              *reinterpret_cast<uint4*>(vb + (rem >> 3) * C::kBoxBytes + r * 128 + (rem & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t < cur.ntiles) {  // PV_t in two halves: P of the first 64 keys comes earlier
+              if (t > 0) ok = wait_all(bar_phalf(t), pn[t] & 1);
+              if (ok && j == 0) ok = wait_all(bar_oempty(t), (un[t] & 1) ^ 1);
+              if (!ok) break;
+              tc_fence_after();
+              if (leader) issue_pv(t, sv, j == 0, 0, end);
+              __syncwarp();
+              ok = t == 0 && stiles > 0 ? wait_all2(bar_pfull(0), pn[0] & 1, bar_kfull(sk), (kc / SK) & 1)
+                                        : wait_all(bar_pfull(t), pn[t] & 1);
+              ++pn[t];
+              if (!ok) break;
+              tc_fence_after();
+              if (leader) {
+                issue_pv(t, sv, false, 1, end);
+                if (last) mma_commit(bar_ofinal(t));
+                if (t == cur.ntiles - 1) mma_commit(bar_vempty(sv));
+              }
+              __syncwarp();
+            }
+            if (t < stiles) {
+              if (last) {
+                ok = wait_all(bar_qfull(t), qn[t]++ & 1);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              if (leader) {
+                issue_qk(t, sk, idesc);
+                if (q_done) mma_commit(bar_qempty(t));
+                if (t == stiles - 1) mma_commit(bar_kempty(sk));
+              }
+              __syncwarp();
+            }
+          }
+          ++vc;
+          if (stiles > 0) ++kc;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (t < cur.ntiles) ++un[t];
+        cur = nxt;
+      }
+      if (!ok && leader) record_error(err, kErrTimeout);
+      if (issued && leader) {  // every MMA issued has completed before TMEM is released
+        mma_commit(bar_drain);
+        mbar_wait(bar_drain, 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 8) {
+    setmaxnreg_dec<kRegsEpilogue>();
+    // ================= epilogue: O / l -> bf16 rows (or fp32 partials) =================
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t fn[2] = {0u, 0u};
+    bool ok = true;
+    CrossWork d;
+    for (int k = 0; ok; ++k) {
+      ok = take(k, d);
+      if (!ok || d.ntiles == 0) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t >= d.ntiles) break;
+        ok = wait_long(bar_lfull(t), fn[t] & 1);
+        if (ok) ok = wait_long(bar_ofinal(t), fn[t] & 1);
+        ++fn[t];
+        if (!ok) break;
+        tc_fence_after();
+        const float inv_l = s_norm[t * kBlockM + row];
+        const uint32_t o_addr = tmem + lane_base + kColO + 128 * t;
+        if (d.partial >= 0) {
+          float* mine = reinterpret_cast<float*>(split_area + split_partials_offset()) +
+                        (static_cast<size_t>(d.partial) * 2 + t) * kPartial<D>;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld32(o_addr + c0, r);
+            tmem_ld_wait();
+            tmem_reg_fence<32>(r);
+            float4* dst = reinterpret_cast<float4*>(mine + static_cast<size_t>(row) * D + c0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              dst[c] = make_float4(__uint_as_float(r[4 * c]) * inv_l, __uint_as_float(r[4 * c + 1]) * inv_l,
+                                   __uint_as_float(r[4 * c + 2]) * inv_l, __uint_as_float(r[4 * c + 3]) * inv_l);
+          }
+          tc_fence_before();
+          arrive_warp(bar_oempty(t));
+          continue;
+        }
+        // Lanes 2i and 2i + 1 trade halves of each 64 bytes, so that an instruction writes whole
+        // 32-byte sectors, two neighbours of a row at a time.
+        const int odd = lane & 1;
+        const int r0 = d.q0[t] + row - odd;  // the even lane's row
+        __nv_bfloat16* p0 = out + (static_cast<size_t>(r0) * seg.num_q_heads + d.head[t]) * D + 16 * odd;
+        __nv_bfloat16* p1 = p0 + static_cast<size_t>(seg.num_q_heads) * D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t r[32], pk[16];
+          tmem_ld32(o_addr + c0, r);
+          tmem_ld_wait();
+          tmem_reg_fence<32>(r);
+          if (c0 == D - 32) {
+            tc_fence_before();
+            arrive_warp(bar_oempty(t));
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            pk[c] = pack_bf16x2(__uint_as_float(r[2 * c]) * inv_l, __uint_as_float(r[2 * c + 1]) * inv_l);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? pk[c] : pk[8 + c], 1);
+            pk[c] = odd ? got : pk[c];
+            pk[8 + c] = odd ? pk[8 + c] : got;
+          }
+          if (r0 < d.seg_end) st_global_v8(p0 + c0, pk);
+          if (r0 + 1 < d.seg_end) st_global_v8(p1 + c0, pk + 8);
+        }
+      }
+    }
+    if (!ok && lane == 0) record_error(err, kErrTimeout);
+  } else {
+    setmaxnreg_inc<kRegsSoftmax>();
+    // ================= softmax (warps 0-3: tile 0, 4-7: tile 1) =================
+    const int t = warp >> 2;
+    const int row = threadIdx.x & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + kColS + 128 * t;
+    const uint32_t o_addr = tmem + lane_base + kColO + 128 * t;
+    const float2 c2 = make_float2(scale_log2, scale_log2);
+    uint32_t sn = 0, un = 0;  // score tiles and items of this query tile seen
+    bool ok = true;
+    CrossWork d;
+    for (int k = 0; ok; ++k) {
+      ok = take(k, d);
+      if (!ok || d.ntiles == 0) break;
+      if (t >= d.ntiles) continue;
+      float m_used = -INFINITY, l = 0.f;
+      // New row max: the reference max moves (and l and O_t are rescaled) only when it grows by more
+      // than 2^kRescaleLog2.  O_t is stable here: PV_t,{j-1} was issued before the scores whose
+      // completion this thread has seen.
+      auto update_max = [&](float mx, int j) {
+        float alpha = 1.f;
+        bool rescale = false;
+        if (mx > m_used && (m_used == -INFINITY || (mx - m_used) * scale_log2 > kRescaleLog2)) {
+          alpha = ex2_approx((m_used - mx) * scale_log2);
+          rescale = j > 0;
+          l *= alpha;
+          m_used = mx;
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld32(o_addr + c0, r);
+            tmem_ld_wait();
+            tmem_reg_fence<32>(r);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
+            tmem_st32(o_addr + c0, r);
+          }
+        }
+        // a row without keys has no max: its weights are exp2(-inf) = 0
+        const float mb = m_used == -INFINITY ? 0.f : m_used * scale_log2;
+        return make_float2(-mb, -mb);
+      };
+      // weights of 64 scores as 32 packed bf16 pairs; acc: four running sums
+      auto weights = [&](const uint32_t* s, float2 nm2, float2 (&acc)[4], uint32_t* p) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float2 x = ffma2(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), c2, nm2);
+          const float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          acc[c & 3] = fadd2(acc[c & 3], e);
+          p[c] = pack_bf16x2(e.x, e.y);
+        }
+      };
+      for (int j = 0; j < d.nkv; ++j) {
+        ok = wait_all(bar_sfull(t), sn++ & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const int keys = j == d.nkv - 1 ? d.last_keys : kBlockN;
+        float2 acc[4] = {{0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // row max of columns: four chains of 3-input steps
+        auto max_of = [&](const uint32_t* s, int n) {
+#pragma unroll
+          for (int c = 0; c < n; c += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              m4[u] = fmax3(m4[u], __uint_as_float(s[c + u]), __uint_as_float(s[c + 4 + u]));
+          return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        };
+        uint32_t s[128], p[32];
+        tmem_ld32(s_addr, s);
+        tmem_ld32(s_addr + 32, s + 32);
+        if (keys <= 64) {  // a short last tile: half the columns
+          tmem_ld_wait();
+          tmem_reg_fence<64>(s);
+#pragma unroll
+          for (int c = 0; c < 64; ++c) s[c] = c < keys ? s[c] : 0xff800000u;
+          weights(s, update_max(max_of(s, 64), j), acc, p);
+          tmem_st32(s_addr, p);
+          tmem_st_wait();
+          tc_fence_before();
+          arrive_warp(bar_phalf(t));
+        } else {
+          tmem_ld32(s_addr + 64, s + 64);
+          tmem_ld32(s_addr + 96, s + 96);
+          tmem_ld_wait();
+          tmem_reg_fence<128>(s);
+          if (keys < kBlockN) {  // keys past the end: by select, so NaN/Inf there is discarded
+#pragma unroll
+            for (int c = 64; c < 128; ++c) s[c] = c < keys ? s[c] : 0xff800000u;
+          }
+          const float2 nm2 = update_max(max_of(s, 128), j);
+          weights(s, nm2, acc, p);
+          tmem_st32(s_addr, p);
+          tmem_st_wait();
+          tc_fence_before();
+          arrive_warp(bar_phalf(t));
+          weights(s + 64, nm2, acc, p);
+          tmem_st32(s_addr + 32, p);
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        arrive_warp(bar_pfull(t));
+        const float2 a01 = fadd2(acc[0], acc[1]), a23 = fadd2(acc[2], acc[3]);
+        l += (a01.x + a01.y) + (a23.x + a23.y);
+      }
+      if (!ok) break;
+      // hand the row's norm to the epilogue, once it has read the previous item's
+      if (un > 0) ok = wait_all(bar_oempty(t), (un - 1) & 1);
+      if (!ok) break;
+      ++un;
+      s_norm[t * kBlockM + row] = l == 0.f ? 0.f : 1.f / l;
+      arrive_warp(bar_lfull(t));
+      const float lse_row = m_used * scale + logf(l);  // -inf without keys
+      const int q_row = d.q0[t] + row;
+      if (d.partial >= 0)
+        (reinterpret_cast<float*>(split_area + split_partials_offset()) +
+         (static_cast<size_t>(d.partial) * 2 + t) * kPartial<D>)[static_cast<size_t>(kBlockM) * D + row] = lse_row;
+      else if (lse != nullptr && q_row < d.seg_end)
+        lse[static_cast<size_t>(d.head[t]) * seg.capacity_q + q_row] = lse_row;
+    }
+    if (!ok && lane == 0) record_error(err, kErrTimeout);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Merge of cut items, in chunk order: lse = log sum_c exp(lse_c), o = sum_c exp(lse_c - lse) o_c.
+// A unit is 16 rows of one tile; memory-bound and short (the partials are in L2).
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = 16;
+constexpr int kMergeUnits = 2 * (kBlockM / kMergeRows);
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads)
+cross_merge_kernel(const uint32_t* __restrict__ ws, const uint8_t* __restrict__ split_area,
+                   __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
+                   const __grid_constant__ CrossSegments seg, const unsigned int* err) {
+  __shared__ float s_w[kMergeRows][kSplitMaxChunks];
+  grid_dependency_wait();
+  launch_dependents();
+  // after a timeout the partials are incomplete: leave the output as it is
+  if (err != nullptr && *reinterpret_cast<const volatile unsigned int*>(err) == kErrTimeout) return;
+  const int n_units = static_cast<int>(ws[0]) * kMergeUnits;
+  const uint32_t* items = reinterpret_cast<const uint32_t*>(split_area + split_items_offset());
+  const float* parts = reinterpret_cast<const float*>(split_area + split_partials_offset());
+  const int group = seg.num_q_heads / seg.num_kv_heads;
+  for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
+    const int e = static_cast<int>(items[unit / kMergeUnits]);
+    const int t = unit % kMergeUnits / (kBlockM / kMergeRows);
+    const int r0 = unit % (kBlockM / kMergeRows) * kMergeRows;
+    const CrossEntry en = reinterpret_cast<const CrossEntry*>(split_area)[e];
+    const int a = seg.cu_q[en.segment], seg_end = seg.cu_q[en.segment + 1];
+    const int per_head = (seg_end - a + kBlockM - 1) / kBlockM, tile = 2 * en.pair + t;
+    const int head = en.kv_head * group + tile / per_head;
+    const int row0 = a + tile % per_head * kBlockM + r0;
+    if (tile >= per_head * group || row0 >= seg_end) continue;  // the whole CTA
+    auto part = [&](int ch) { return parts + (static_cast<size_t>(e + ch) * 2 + t) * kPartial<D>; };
+    __syncthreads();  // the previous unit's weights have been used
+    if (threadIdx.x < kMergeRows) {
+      const int r = threadIdx.x;
+      float mx = -INFINITY, den = 0.f;
+      for (int ch = 0; ch < en.chunks; ++ch) {
+        const float v = part(ch)[static_cast<size_t>(kBlockM) * D + r0 + r];
+        s_w[r][ch] = v;
+        mx = fmaxf(mx, v);
+      }
+      for (int ch = 0; ch < en.chunks; ++ch) den += __expf(s_w[r][ch] - mx);
+      const float all = mx + logf(den);
+      for (int ch = 0; ch < en.chunks; ++ch) s_w[r][ch] = __expf(s_w[r][ch] - all);
+      if (lse != nullptr && row0 + r < seg_end) lse[static_cast<size_t>(head) * seg.capacity_q + row0 + r] = all;
+    }
+    __syncthreads();
+    for (int u = threadIdx.x; u < kMergeRows * (D / 8); u += kMergeThreads) {
+      const int r = u / (D / 8), c = u % (D / 8) * 8;
+      if (row0 + r >= seg_end) continue;
+      float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int ch = 0; ch < en.chunks; ++ch) {
+        const float4* src = reinterpret_cast<const float4*>(part(ch) + static_cast<size_t>(r0 + r) * D + c);
+        const float4 x = src[0], y = src[1];
+        const float w = s_w[r][ch];
+        acc[0] = fmaf(w, x.x, acc[0]);
+        acc[1] = fmaf(w, x.y, acc[1]);
+        acc[2] = fmaf(w, x.z, acc[2]);
+        acc[3] = fmaf(w, x.w, acc[3]);
+        acc[4] = fmaf(w, y.x, acc[4]);
+        acc[5] = fmaf(w, y.y, acc[5]);
+        acc[6] = fmaf(w, y.z, acc[6]);
+        acc[7] = fmaf(w, y.w, acc[7]);
+      }
+      *reinterpret_cast<uint4*>(out + (static_cast<size_t>(row0 + r) * seg.num_q_heads + head) * D + c) =
+          make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                     pack_bf16x2(acc[6], acc[7]));
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch(const CrossArgs& a, cudaStream_t stream) {
+  using C = Cfg<D>;
+  static std::atomic<bool> configured[64];  // the shared-memory opt-in, once per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(cross_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    configured[dev].store(true, std::memory_order_release);
+  }
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  uint32_t* ws = static_cast<uint32_t*>(a.workspace);
+  uint8_t* split = static_cast<uint8_t*>(a.split_area);
+  e = launch_programmatic(cross_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.seg, ws, split, sms, a.err);
+  if (e != cudaSuccess) return e;
+  e = launch_programmatic(cross_attn_kernel<D>, dim3(sms), dim3(kThreads), C::kSmemBytes, stream, a.tmap_q,
+                          a.tmap_k, a.tmap_v, static_cast<__nv_bfloat16*>(a.o), a.lse, a.seg, a.scale,
+                          a.scale * 1.4426950408889634f, static_cast<const uint32_t*>(ws), split, a.err,
+                          static_cast<unsigned long long>(a.wait_limit_ns), a.stall_after_tiles);
+  if (e != cudaSuccess) return e;
+  if (split != nullptr)
+    e = launch_programmatic(cross_merge_kernel<D>, dim3(4 * sms), dim3(kMergeThreads), 0, stream,
+                            static_cast<const uint32_t*>(ws), static_cast<const uint8_t*>(split),
+                            static_cast<__nv_bfloat16*>(a.o), a.lse, a.seg,
+                            static_cast<const unsigned int*>(a.err));
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_cross_attn(const CrossArgs& a, int head_dim, cudaStream_t stream) {
+  return head_dim == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+}
+
+}  // namespace h3

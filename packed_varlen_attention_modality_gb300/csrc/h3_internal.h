@@ -95,7 +95,6 @@ cudaError_t launch_window_unpack(const int32_t* perm, int num_tokens, const void
 constexpr int kAttnModePacked = 0;
 constexpr int kAttnModeWindow = 1;
 constexpr int kAttnModeVsa = 2;
-constexpr int kAttnModeCross = 3;  // packed query segments, key segments of other lengths
 
 // Attention straight on the (T, H, W) grid.
 // Windows: windows of w[] cut with shift s[] (edge windows cropped), nwin[] windows per axis,
@@ -131,12 +130,6 @@ struct AttnArgs {
   int num_heads;
   int head_dim;
   float scale;
-  // cross attention: the key side (cu_seqlens, max_seqlen and capacity are the query side)
-  const int32_t* cu_seqlens_k;
-  const int32_t* seqused_k;
-  int max_seqlen_k;
-  int capacity_k;
-  int num_kv_heads;
   void* workspace;  // attn_plan_bytes(num_segments) bytes: the work plan
   void* split_area;  // packed: attn_split_bytes(head_dim) bytes after the plan, or null (no split)
   unsigned int* err;
@@ -175,6 +168,27 @@ constexpr size_t attn_workspace_bytes(int num_segments, int max_seqlen, int head
   return attn_plan_bytes(num_segments) + (max_seqlen >= kSplitMinSeqlen ? attn_split_bytes(head_dim) : 0);
 }
 cudaError_t launch_attn_fwd(const AttnArgs& a, cudaStream_t stream);
+
+// ---- cross attention ------------------------------------------------------------------------
+struct CrossSegments {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* seqused_k;  // keys used of each segment, or null: all
+  int num_segments, max_seqlen_q, max_seqlen_k, capacity_q, capacity_k, num_q_heads, num_kv_heads;
+};
+struct CrossArgs {
+  CUtensorMap tmap_q, tmap_k, tmap_v;  // 3-D views {D, H, rows}
+  CrossSegments seg;
+  void* o;
+  float* lse;
+  float scale;
+  void* workspace;   // attn_plan_bytes(num_segments): the work plan
+  void* split_area;  // attn_split_bytes(head_dim) after it, or null (no item is cut)
+  unsigned int* err;
+  uint64_t wait_limit_ns;
+  uint32_t stall_after_tiles;
+};
+cudaError_t launch_cross_attn(const CrossArgs& a, int head_dim, cudaStream_t stream);
 
 // ---- VSA block gate + top-k ----------------------------------------------------------------
 struct VsaGeom {

@@ -580,8 +580,7 @@ h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* d, const void* q, c
   if (d->num_segments == 0 || d->max_seqlen_q == 0) return H3_OK;
   if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
 
-  h3::AttnArgs a{};
-  a.mode = h3::kAttnModeCross;
+  h3::CrossArgs a{};
   // no keys at all: any valid map will do, its rows are masked
   const bool none = d->capacity_k == 0;
   if (!make_qkv_map(&a.tmap_q, q, d->capacity_q, d->num_q_heads, d->head_dim, strides[0]) ||
@@ -590,20 +589,12 @@ h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* d, const void* q, c
       !make_qkv_map(&a.tmap_v, none ? q : v, none ? d->capacity_q : d->capacity_k,
                     none ? d->num_q_heads : d->num_kv_heads, d->head_dim, strides[none ? 0 : 2]))
     return H3_ERR_CUDA;
+  a.seg = h3::CrossSegments{cu_seqlens_q, cu_seqlens_k, seqused_k, d->num_segments, d->max_seqlen_q,
+                            d->max_seqlen_k, d->capacity_q, d->capacity_k, d->num_q_heads,
+                            d->num_kv_heads};
   a.o = o;
   a.lse = lse;
-  a.cu_seqlens = cu_seqlens_q;
-  a.num_segments = d->num_segments;
-  a.max_seqlen = d->max_seqlen_q;
-  a.capacity = d->capacity_q;
-  a.num_heads = d->num_q_heads;
-  a.head_dim = d->head_dim;
   a.scale = cross_scale(d);
-  a.cu_seqlens_k = cu_seqlens_k;
-  a.seqused_k = seqused_k;
-  a.max_seqlen_k = d->max_seqlen_k;
-  a.capacity_k = d->capacity_k;
-  a.num_kv_heads = d->num_kv_heads;
   a.workspace = workspace;
   if (d->max_seqlen_k >= h3::kSplitMinSeqlen)
     a.split_area = static_cast<uint8_t*>(workspace) + h3::attn_plan_bytes(d->num_segments);
@@ -611,7 +602,7 @@ h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* d, const void* q, c
   a.wait_limit_ns = h3::wait_limit_ns();
   a.stall_after_tiles = h3::stall_after_tiles();
   if (a.err == nullptr) return H3_ERR_CUDA;
-  return from_cuda(h3::launch_attn_fwd(a, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(h3::launch_cross_attn(a, d->head_dim, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 h3_status h3_window_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse,
