@@ -284,8 +284,9 @@ H3_API size_t h3_varlen_cross_attn_workspace_size(const h3_cross_attn_desc* desc
  *              batch), 0 <= n_g <= its length.
  * workspace  : device, h3_varlen_cross_attn_workspace_size() bytes, 16-byte aligned; need not be
  *              initialised.  Calls that may run at the same time need separate workspaces.
- * A segment whose offsets or n_g are out of range is skipped (its rows are not written) and one
- * longer than its bound is computed in full; both are recorded as H3_ERR_BAD_CU_SEQLENS.
+ * A segment whose offsets or n_g are out of range, or with more rows than max_seqlen_q, is skipped
+ * (its rows are not written); one with more keys than max_seqlen_k is computed in full.  Both are
+ * recorded as H3_ERR_BAD_CU_SEQLENS.
  * Errors: H3_ERR_NULL, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED, H3_ERR_MISALIGNED,
  *         H3_ERR_WORKSPACE, H3_ERR_CUDA; device-side H3_ERR_BAD_CU_SEQLENS / H3_ERR_TIMEOUT. */
 H3_API h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* desc, const void* q,

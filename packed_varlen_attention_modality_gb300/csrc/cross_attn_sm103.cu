@@ -36,8 +36,6 @@
 // Every wait is bounded; a wait that runs out records a timeout and unwinds the CTA.
 #include <cuda_bf16.h>
 
-#include <atomic>
-
 #include "h3_internal.h"
 #include "launch.h"
 #include "sm103_ptx.cuh"
@@ -81,12 +79,12 @@ constexpr size_t kPartial = static_cast<size_t>(kBlockM) * (D + 1);  // floats o
 __device__ __forceinline__ int2 checked_segment(const CrossSegments& s, int g, unsigned int* err) {
   const int a = s.cu_q[g], b = s.cu_q[g + 1], ka = s.cu_k[g], kb = s.cu_k[g + 1];
   const int used = s.seqused_k != nullptr ? s.seqused_k[g] : kb - ka;
-  if (a < 0 || b < a || b > s.capacity_q || ka < 0 || kb < ka || kb > s.capacity_k || used < 0 ||
+  if (a < 0 || b < a || b > s.capacity_q || b - a > s.max_seqlen_q || ka < 0 || kb < ka || kb > s.capacity_k || used < 0 ||
       used > kb - ka || (g == 0 && (a != 0 || ka != 0))) {
     record_error(err, kErrBadCuSeqlens);
     return make_int2(0, 0);
   }
-  if (b - a > s.max_seqlen_q || used > s.max_seqlen_k) record_error(err, kErrBadCuSeqlens);
+  if (used > s.max_seqlen_k) record_error(err, kErrBadCuSeqlens);  // computed all the same
   return make_int2(b - a, used);
 }
 // Items of a segment per key head: pairs of its group * ceil(rows / 128) tiles.
@@ -906,16 +904,8 @@ cross_merge_kernel(const uint32_t* __restrict__ ws, const uint8_t* __restrict__ 
 template <int D>
 cudaError_t launch(const CrossArgs& a, cudaStream_t stream) {
   using C = Cfg<D>;
-  static std::atomic<bool> configured[64];  // the shared-memory opt-in, once per device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = allow_shared_memory<C::kSmemBytes>(cross_attn_kernel<D>);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!configured[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(cross_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-    if (e != cudaSuccess) return e;
-    configured[dev].store(true, std::memory_order_release);
-  }
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return cudaErrorInvalidDevice;
   uint32_t* ws = static_cast<uint32_t*>(a.workspace);

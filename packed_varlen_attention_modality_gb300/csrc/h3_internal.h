@@ -190,6 +190,36 @@ struct CrossArgs {
 };
 cudaError_t launch_cross_attn(const CrossArgs& a, int head_dim, cudaStream_t stream);
 
+// Few rows per segment: at most kCrossTokenRows of (rows x query heads per key head).
+constexpr int kCrossTokenRows = 16;
+constexpr int kCrossTokenCtas = 2432;  // CTAs aimed at: 8 waves of 2 x 152
+struct CrossTokenArgs {
+  CrossSegments seg;
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  __nv_bfloat16* o;
+  float* lse;
+  float scale;
+  int max_rows;            // max_seqlen_q x query heads per key head
+  int chunk_keys, chunks;  // cross_token_split
+  float* partials;         // cross_token_bytes()
+  unsigned int* err;
+};
+void cross_token_split(const CrossSegments& s, int* chunk_keys, int* chunks);
+// floats of a chunk's partial results: rows of head_dim values, then the rows' LSEs (16-byte units)
+constexpr size_t cross_token_partial(int rows, int head_dim) {
+  return static_cast<size_t>(rows) * head_dim + (rows + 3) / 4 * 4;
+}
+inline size_t cross_token_bytes(const CrossSegments& s, int head_dim) {
+  int keys = 0, chunks = 0;
+  cross_token_split(s, &keys, &chunks);
+  const int rows = s.max_seqlen_q * (s.num_q_heads / s.num_kv_heads);
+  const size_t all = static_cast<size_t>(s.num_segments) * s.num_kv_heads * chunks *
+                     cross_token_partial(rows, head_dim) * sizeof(float);
+  return chunks == 1 || all < 256 ? 256 : all;  // never none: the call always takes a workspace
+}
+cudaError_t launch_cross_token(const CrossTokenArgs& a, int head_dim, cudaStream_t stream);
+
 // ---- VSA block gate + top-k ----------------------------------------------------------------
 struct VsaGeom {
   int L[3];   // grid (T, H, W)

@@ -560,8 +560,25 @@ float cross_scale(const h3_cross_attn_desc* d) {
 
 }  // namespace
 
+namespace {
+
+// Few rows per segment take the key-streaming kernel: its 16-row tile holds all of a key head's
+// rows, so K and V are read once.
+bool cross_few_rows(const h3_cross_attn_desc* d) {
+  return static_cast<int64_t>(d->max_seqlen_q) * (d->num_q_heads / d->num_kv_heads) <= h3::kCrossTokenRows;
+}
+
+h3::CrossSegments cross_segments(const h3_cross_attn_desc* d, const int32_t* cu_q, const int32_t* cu_k,
+                                 const int32_t* seqused_k) {
+  return h3::CrossSegments{cu_q, cu_k, seqused_k, d->num_segments, d->max_seqlen_q, d->max_seqlen_k,
+                           d->capacity_q, d->capacity_k, d->num_q_heads, d->num_kv_heads};
+}
+
+}  // namespace
+
 size_t h3_varlen_cross_attn_workspace_size(const h3_cross_attn_desc* d) {
   if (d == nullptr || !cross_sizes_ok(d) || d->num_segments == 0) return 0;
+  if (cross_few_rows(d)) return h3::cross_token_bytes(cross_segments(d, nullptr, nullptr, nullptr), d->head_dim);
   return h3::attn_workspace_bytes(d->num_segments, d->max_seqlen_k, d->head_dim);
 }
 
@@ -580,6 +597,26 @@ h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* d, const void* q, c
   if (d->num_segments == 0 || d->max_seqlen_q == 0) return H3_OK;
   if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
 
+  if (cross_few_rows(d)) {
+    h3::CrossTokenArgs t{};
+    t.seg = cross_segments(d, cu_seqlens_q, cu_seqlens_k, seqused_k);
+    t.q = static_cast<const __nv_bfloat16*>(q);
+    t.k = static_cast<const __nv_bfloat16*>(k);
+    t.v = static_cast<const __nv_bfloat16*>(v);
+    t.q_stride = strides[0];
+    t.k_stride = strides[1];
+    t.v_stride = strides[2];
+    t.o = static_cast<__nv_bfloat16*>(o);
+    t.lse = lse;
+    t.scale = cross_scale(d);
+    t.max_rows = d->max_seqlen_q * (d->num_q_heads / d->num_kv_heads);
+    h3::cross_token_split(t.seg, &t.chunk_keys, &t.chunks);
+    t.partials = static_cast<float*>(workspace);
+    t.err = device_error_ptr();
+    if (t.err == nullptr) return H3_ERR_CUDA;
+    return from_cuda(h3::launch_cross_token(t, d->head_dim, reinterpret_cast<cudaStream_t>(stream)));
+  }
+
   h3::CrossArgs a{};
   // no keys at all: any valid map will do, its rows are masked
   const bool none = d->capacity_k == 0;
@@ -589,9 +626,7 @@ h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* d, const void* q, c
       !make_qkv_map(&a.tmap_v, none ? q : v, none ? d->capacity_q : d->capacity_k,
                     none ? d->num_q_heads : d->num_kv_heads, d->head_dim, strides[none ? 0 : 2]))
     return H3_ERR_CUDA;
-  a.seg = h3::CrossSegments{cu_seqlens_q, cu_seqlens_k, seqused_k, d->num_segments, d->max_seqlen_q,
-                            d->max_seqlen_k, d->capacity_q, d->capacity_k, d->num_q_heads,
-                            d->num_kv_heads};
+  a.seg = cross_segments(d, cu_seqlens_q, cu_seqlens_k, seqused_k);
   a.o = o;
   a.lse = lse;
   a.scale = cross_scale(d);

@@ -39,4 +39,24 @@ inline int num_sms_of_current_device() {
   return n;
 }
 
+// Opt a kernel in to kBytes of dynamic shared memory, once per device (a racing second call is
+// harmless).
+template <int kBytes, typename K>
+inline cudaError_t allow_shared_memory(K* kernel) {
+  static std::atomic<K*> done[64][2];  // kernels of one type (one per head_dim) at most
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  for (auto& d : done[dev])
+    if (d.load(std::memory_order_acquire) == kernel) return cudaSuccess;
+  const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (s != cudaSuccess) return s;
+  for (auto& d : done[dev]) {
+    K* none = nullptr;
+    if (d.compare_exchange_strong(none, kernel, std::memory_order_acq_rel) || none == kernel) break;
+  }
+  return cudaSuccess;
+}
+
 }  // namespace h3
