@@ -268,6 +268,7 @@ typedef struct {
    * at least heads * head_dim, so k and v may be parts of a fused projection; 0 = contiguous.
    * o (and its gradient) are contiguous. */
   int64_t q_stride, k_stride, v_stride;
+  int64_t dq_stride, dk_stride, dv_stride; /* backward: dq, dk, dv */
 } h3_cross_attn_desc;
 
 /* Workspace bytes of h3_varlen_cross_attn_fwd for these sizes; 0 for invalid ones. */
@@ -294,6 +295,34 @@ H3_API h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* desc, const 
                                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
                                           const int32_t* seqused_k, void* workspace,
                                           size_t workspace_bytes, h3_stream_t stream);
+
+/* Workspace bytes of h3_varlen_cross_attn_bwd (the work plan, rowsum(do * o), and the partial sums of
+ * key tiles whose query range is cut: at most about 160 MB at head_dim 128); 0 for invalid sizes. */
+H3_API size_t h3_varlen_cross_attn_bwd_workspace_size(const h3_cross_attn_desc* desc);
+
+/* Gradient of h3_varlen_cross_attn_fwd (with equal offsets, also of h3_varlen_attn_fwd), with
+ * P = exp(S - lse), dP = do v^T, dS = P * (dP - rowsum(do * o)):
+ *   dv = P^T do;   dk = scale dS^T q, both summed over the query heads of a key head;
+ *   dq = scale dS k.
+ * dout, o     : device bf16 [capacity_q, num_q_heads, head_dim], contiguous: the gradient of o, and o.
+ * lse         : device fp32 [num_q_heads, capacity_q], from the forward.
+ * q, k, v, cu_seqlens_q, cu_seqlens_k, seqused_k: the forward's.
+ * dq, dk, dv  : device bf16, shaped as q, k, v (token strides in desc); every row of every segment is
+ *               written (0 for keys a segment does not use, and where a side is empty), others
+ *               untouched.  Must not overlap an input.
+ * workspace   : device, h3_varlen_cross_attn_bwd_workspace_size() bytes, 16-byte aligned; need not be
+ *               initialised.  Calls that may run at the same time need separate workspaces.
+ * Sums over queries and keys are taken in a fixed order: the result does not depend on timing.
+ * A side with capacity 0 may be NULL.  Bad segments as for the forward; a skipped segment's rows are
+ * not written on either side.
+ * Errors: as h3_varlen_cross_attn_fwd. */
+H3_API h3_status h3_varlen_cross_attn_bwd(const h3_cross_attn_desc* desc, const void* dout,
+                                          const void* q, const void* k, const void* v,
+                                          const void* o, const float* lse,
+                                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                          const int32_t* seqused_k, void* dq, void* dk, void* dv,
+                                          void* workspace, size_t workspace_bytes,
+                                          h3_stream_t stream);
 
 /* Number of windows of the partition (host only; no device work).
  * [H3-fast] "window attention across GPUs": along each axis of length L with window w and

@@ -10,8 +10,9 @@ Calls:
   qk_norm_rope / qk_norm_rope_bwd   RMS norm of Q and K per head with the rotation (or without)
                     in the same pass, and its gradient
   varlen_attn_fwd   block-diagonal softmax attention over cu_seqlens segments
-  varlen_cross_attn_fwd   packed cross attention: keys of another length per segment, query heads
-                    sharing key heads, padded key batches
+  varlen_cross_attn_fwd / varlen_cross_attn_bwd   packed cross attention: keys of another length per
+                    segment, query heads sharing key heads, padded key batches; and its gradient
+                    (with equal offsets, that of varlen_attn_fwd)
   window_count / window_pack / window_unpack   shifted 3D window partition and row gather/scatter
   window_attn_fwd   shifted 3D window attention read and written in place on the grid
   vsa_select / vsa_attn_fwd   block-sparse video attention: block gate scores + top-k
@@ -37,6 +38,7 @@ import torch
 __all__ = ["H3Error", "RopeConfig", "lib_path", "load_library", "rope_apply", "qk_norm_rope",
            "qk_norm_rope_bwd_workspace_size", "qk_norm_rope_bwd", "varlen_attn_fwd",
            "varlen_attn_fwd_noalloc", "varlen_cross_attn_workspace_size", "varlen_cross_attn_fwd",
+           "varlen_cross_attn_bwd_workspace_size", "varlen_cross_attn_bwd",
            "window_attn_fwd", "vsa_block_count",
            "vsa_select_workspace_size", "vsa_select", "vsa_attn_workspace_size", "vsa_attn_fwd",
            "ContinuationConfig",
@@ -90,7 +92,8 @@ class _CrossAttnDesc(ctypes.Structure):
     """Mirror of h3_cross_attn_desc."""
     _fields_ = [("num_segments", _I), ("max_seqlen_q", _I), ("max_seqlen_k", _I), ("capacity_q", _I),
                 ("capacity_k", _I), ("num_q_heads", _I), ("num_kv_heads", _I), ("head_dim", _I),
-                ("softmax_scale", ctypes.c_float), ("q_stride", _L), ("k_stride", _L), ("v_stride", _L)]
+                ("softmax_scale", ctypes.c_float), ("q_stride", _L), ("k_stride", _L), ("v_stride", _L),
+                ("dq_stride", _L), ("dk_stride", _L), ("dv_stride", _L)]
 
 
 class ContinuationConfig(ctypes.Structure):
@@ -136,6 +139,9 @@ def load_library():
         "h3_varlen_attn_fwd_noalloc": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P]),
         "h3_varlen_cross_attn_workspace_size": (U64, [ctypes.POINTER(_CrossAttnDesc)]),
         "h3_varlen_cross_attn_fwd": (I32, [ctypes.POINTER(_CrossAttnDesc), P, P, P, P, P, P, P, P, P, U64, P]),
+        "h3_varlen_cross_attn_bwd_workspace_size": (U64, [ctypes.POINTER(_CrossAttnDesc)]),
+        "h3_varlen_cross_attn_bwd": (I32, [ctypes.POINTER(_CrossAttnDesc), P, P, P, P, P, P, P, P, P, P, P, P, P,
+                                           U64, P]),
         "h3_window_attn_fwd": (I32, [P, P, P, P, P, I32P, I32P, I32P, I32, I32, F32, P]),
         "h3_window_count": (I32, [I32P, I32P, I32P]),
         "h3_window_pack": (I32, [I32P, I32P, I32P, P, P, ctypes.POINTER(P), ctypes.POINTER(P),
@@ -552,6 +558,56 @@ def varlen_cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_
                                               _ptr(workspace), workspace.numel(), _stream(dev))
         _check(st, "h3_varlen_cross_attn_fwd")
     return (out, lse) if lse is not None else out
+
+
+def varlen_cross_attn_bwd_workspace_size(num_segments: int, max_seqlen_q: int, max_seqlen_k: int, capacity_q: int,
+                                         capacity_k: int, num_q_heads: int, num_kv_heads: int,
+                                         head_dim: int) -> int:
+    desc = _CrossAttnDesc(num_segments, max_seqlen_q, max_seqlen_k, capacity_q, capacity_k, num_q_heads,
+                          num_kv_heads, head_dim)
+    return int(load_library().h3_varlen_cross_attn_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def varlen_cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                          out: torch.Tensor, lse: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                          cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                          seqused_k: Optional[torch.Tensor] = None, dq: Optional[torch.Tensor] = None,
+                          dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                          softmax_scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradient of varlen_cross_attn_fwd (with equal offsets, of varlen_attn_fwd): from dout (the gradient
+    of its output), its inputs, its output and its LSE to (dq, dk, dv), bf16, shaped as q, k, v.
+
+    dq, dk and dv may be parts of a fused gradient.  Every row of every segment is written (0 for keys
+    that a segment does not use); other rows are left untouched.  The result does not depend on timing.
+    """
+    desc = _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqused_k, softmax_scale)
+    dev = q.device
+    C, H, _ = q.shape
+    for name, t in (("dout", dout), ("out", out)):
+        _require(t, name, torch.bfloat16, dev)
+        if t.shape != q.shape:
+            raise ValueError(f"{name} must have q's shape")
+    _require(lse, "lse", torch.float32, dev)
+    if tuple(lse.shape) != (H, C):
+        raise ValueError("lse must be [Hq, Cq]")
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if dk is None else dk
+    dv = torch.empty(k.shape, dtype=k.dtype, device=dev) if dv is None else dv
+    desc.dq_stride = _rows(dq, "dq", dev, q.shape)
+    desc.dk_stride = _rows(dk, "dk", dev, k.shape)
+    desc.dv_stride = _rows(dv, "dv", dev, k.shape)
+    lib = load_library()
+    if workspace is None:
+        need = int(lib.h3_varlen_cross_attn_bwd_workspace_size(ctypes.byref(desc)))
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _require(workspace, "workspace", torch.uint8, dev)
+    with _on(dev):
+        st = lib.h3_varlen_cross_attn_bwd(ctypes.byref(desc), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                          _ptr(lse), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(seqused_k),
+                                          _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
+                                          _stream(dev))
+    _check(st, "h3_varlen_cross_attn_bwd")
+    return dq, dk, dv
 
 
 def window_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, grid: Sequence[int],

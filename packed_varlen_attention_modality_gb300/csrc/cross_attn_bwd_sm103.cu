@@ -1,0 +1,1171 @@
+// Gradient of packed cross attention (and, with equal offsets, of packed self attention) for
+// sm_103a: TMA + tcgen05 + TMEM.
+//
+//   P = exp(scale q k^T - lse),  dP = do v^T,  delta = rowsum(do * o),  dS = P * (dP - delta)
+//   dv = P^T do,   dk = scale dS^T q,   dq = scale dS k
+//
+// Two kernels, because a sum over queries (dk, dv) and one over keys (dq) cannot both stay in one
+// CTA's accumulators: the dK/dV kernel keeps a 128-key tile and runs over the queries, the dQ kernel
+// keeps a 128-row query tile and runs over the keys.  Each recomputes S and dP (7 products in all
+// instead of 5); in exchange nothing is summed through memory in an order that depends on timing
+// (no atomics), and no fp32 gradient goes through memory.  When there are too few key tiles to fill
+// the GPU, their query range is cut into chunks whose fp32 partial sums a last kernel adds in order.
+//
+// dK/dV works on transposed scores: S^T = K Q^T and dP^T = V dO^T have keys as TMEM lanes, so P^T and
+// dS^T are written back to TMEM as the A operands of dV += P^T dO and dK += dS^T Q, and one copy of Q
+// and dO in shared memory serves both products that read it.  Each thread owns a key row and half the
+// 128 query columns.  Tensor order: dV_i, S_{i+1} while dS_i is computed, dK_i, dP_{i+1} while P_{i+1}
+// is.  TMEM (512 columns): S^T/P^T, dP^T/dS^T, dK, dV.
+// dQ: S = Q K^T (two buffers), dP = dO V^T, dQ += dS K.  Tensor order: S_{j+1}, dP_{j+1}, dQ_j; it runs
+// from one item into the next, since key lists may be a few tiles.
+//
+// P and dS are rounded to bf16 for the tensor core (half a step, 2^-8 relative at most); everything
+// else is fp32 until the gradients are rounded once.  Rows and keys past a segment's end are zeroed
+// in shared memory as far as a product reads them, and masked by select where they would meet an
+// exponential.  Every wait is bounded; a wait that runs out records a timeout and unwinds the CTA.
+#include <cuda_bf16.h>
+
+#include "h3_internal.h"
+#include "launch.h"
+#include "sm103_ptx.cuh"
+
+namespace h3 {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kThreads = 384;
+constexpr int kTmemCols = 512;
+constexpr int kPlanThreads = 1024;
+
+__host__ __device__ constexpr int tiles_of(int n) { return (n + kTile - 1) / kTile; }
+__device__ __forceinline__ int steps16(int n) { return (n + 15) / 16; }
+
+struct Segment {
+  int q0, rows, k0, keys, used;  // key rows of the segment and how many of them it uses
+};
+__device__ __forceinline__ Segment segment_of(const CrossSegments& s, int g) {
+  Segment r;
+  r.q0 = s.cu_q[g];
+  r.rows = s.cu_q[g + 1] - r.q0;
+  r.k0 = s.cu_k[g];
+  r.keys = s.cu_k[g + 1] - r.k0;
+  r.used = s.seqused_k != nullptr ? s.seqused_k[g] : r.keys;
+  return r;
+}
+__device__ __forceinline__ bool valid_segment(const CrossSegments& s, int g, const Segment& r) {
+  return r.q0 >= 0 && r.rows >= 0 && r.q0 <= s.capacity_q - r.rows && r.rows <= s.max_seqlen_q && r.k0 >= 0 &&
+         r.keys >= 0 && r.k0 <= s.capacity_k - r.keys && r.used >= 0 && r.used <= r.keys &&
+         (g > 0 || (r.q0 == 0 && r.k0 == 0));
+}
+
+// ---- plan ------------------------------------------------------------------------------------------
+// Words: [0] dQ items, [1] dK/dV items, [2] chunks of the query range per key tile (at most), [3]
+// spare, then the exclusive prefixes of dQ items [S + 1] and of dK/dV items [S + 1].
+__device__ __forceinline__ int kv_steps(const Segment& r, int group) {  // (head, query tile) pairs
+  return r.used > 0 ? group * tiles_of(r.rows) : 0;
+}
+__device__ __forceinline__ int chunks_of(int steps, int most) { return max(1, min(steps, most)); }
+
+__device__ __forceinline__ uint32_t exclusive_scan(uint32_t v, uint32_t* s_warp, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  uint32_t before = 0;
+  total = 0;
+#pragma unroll 1
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws, int slots, int sms,
+                      unsigned int* err) {
+  __shared__ uint32_t s_warp[kPlanThreads / 32];
+  grid_dependency_wait();
+  launch_dependents();
+  const int S = seg.num_segments, tid = threadIdx.x, group = seg.num_q_heads / seg.num_kv_heads;
+  const int chunk = (S + kPlanThreads - 1) / kPlanThreads;
+  const int lo = min(S, tid * chunk), hi = min(S, lo + chunk);
+  auto checked = [&](int g) {
+    Segment r = segment_of(seg, g);
+    if (!valid_segment(seg, g, r)) {
+      record_error(err, kErrBadCuSeqlens);
+      r.rows = r.keys = r.used = 0;
+    } else if (r.used > seg.max_seqlen_k) {
+      record_error(err, kErrBadCuSeqlens);  // computed all the same
+    }
+    return r;
+  };
+  uint32_t nq = 0, nk = 0, work = 0, total_q, tiles, total_work;  // work: (key tile, step) pairs / 4
+  for (int g = lo; g < hi; ++g) {
+    const Segment r = checked(g);
+    nq += static_cast<uint32_t>(tiles_of(r.rows)) * seg.num_q_heads;
+    const uint32_t t = static_cast<uint32_t>(tiles_of(r.keys)) * seg.num_kv_heads;
+    nk += t;
+    work += static_cast<uint32_t>((static_cast<uint64_t>(t) * kv_steps(r, group) + 3) / 4);
+  }
+  uint32_t at_q = exclusive_scan(nq, s_warp, total_q);
+  exclusive_scan(nk, s_warp, tiles);
+  exclusive_scan(work, s_warp, total_work);
+  // Chunks per key tile: what makes the waves of items (of steps / c steps, and about 3 steps' time
+  // of start and end each) shortest, as far as the slots reach.
+  int most = 1;
+  if (tiles > 0) {
+    const float steps = 4.f * static_cast<float>(total_work) / static_cast<float>(tiles);
+    float best = INFINITY;
+    for (int c = 1; c <= kCrossBwdMaxChunks && static_cast<int64_t>(tiles) * c <= max(slots, static_cast<int>(tiles)); ++c) {
+      const float waves = static_cast<float>((static_cast<int64_t>(tiles) * c + sms - 1) / sms);
+      const float cost = waves * (steps / static_cast<float>(c) + 3.f);
+      if (cost < best) {
+        best = cost;
+        most = c;
+      }
+    }
+  }
+  nk = 0;
+  auto kv_items = [&](const Segment& r) {
+    return static_cast<uint32_t>(tiles_of(r.keys)) * seg.num_kv_heads * chunks_of(kv_steps(r, group), most);
+  };
+  for (int g = lo; g < hi; ++g) nk += kv_items(checked(g));
+  uint32_t total_k, at_k = exclusive_scan(nk, s_warp, total_k);
+  uint32_t* pq = ws + kCrossBwdHeader;
+  uint32_t* pk = pq + S + 1;
+  for (int g = lo; g < hi; ++g) {
+    const Segment r = checked(g);
+    pq[g] = at_q;
+    pk[g] = at_k;
+    at_q += static_cast<uint32_t>(tiles_of(r.rows)) * seg.num_q_heads;
+    at_k += kv_items(r);
+  }
+  if (tid == 0) {
+    pq[S] = total_q;
+    pk[S] = total_k;
+    ws[0] = total_q;
+    ws[1] = total_k;
+    ws[2] = static_cast<uint32_t>(most);
+  }
+}
+
+__device__ __forceinline__ int find_segment(const uint32_t* __restrict__ prefix, int S, uint32_t item) {
+  int lo = 0, hi = S - 1;  // last g with prefix[g] <= item
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= item) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// ---- delta = rowsum(do * o) --------------------------------------------------------------------------
+// D / 8 lanes a row of one head; memory-bound.
+template <int D>
+__global__ void __launch_bounds__(256)
+cross_delta_kernel(const uint4* __restrict__ o, const uint4* __restrict__ dout, int64_t rows, int heads,
+                   int capacity, float* __restrict__ delta) {
+  constexpr int kLanes = D / 8;
+  grid_dependency_wait();
+  launch_dependents();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * (256 / kLanes);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+  constexpr int kUnroll = 4;
+  const int64_t warp_first = first - (threadIdx.x % 32) / kLanes;  // the same for the warp's lanes
+  for (int64_t base = 0; warp_first + base < rows; base += kUnroll * stride) {
+    uint4 x[kUnroll], y[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t r = first + base + u * stride;
+      x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) {
+        x[u] = __ldg(o + r * kLanes + threadIdx.x % kLanes);
+        y[u] = __ldg(dout + r * kLanes + threadIdx.x % kLanes);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int64_t r = first + base + u * stride;
+      const uint32_t a[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, b[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
+        s = fmaf(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u), s);
+      }
+#pragma unroll
+      for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      if (r < rows && threadIdx.x % kLanes == 0) delta[(r % heads) * capacity + r / heads] = s;
+    }
+  }
+}
+
+// ---- shared pieces of the two product kernels ----------------------------------------------------------
+template <int D>
+struct Tiles {
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kBytes = kTile * D * 2;
+  static constexpr int kBoxBytes = kTile * 128;
+};
+
+// One 128-row tile of one head.
+template <int D>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int row, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, Tiles<D>::kBytes);
+#pragma unroll
+  for (int b = 0; b < Tiles<D>::kBoxes; ++b)
+    tma_load_3d(smem_u32(dst + b * Tiles<D>::kBoxBytes), map, b * 64, head, row, bar);
+}
+
+// Zero rows [n, 16 * steps16(n)) of a tile (whole 128-byte rows: the swizzle permutes 16-byte pieces
+// within a row).  One warp; before any product reads the tile.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int n) {
+  const int lane = threadIdx.x & 31, rows = 16 * steps16(n) - n;
+  for (int i = lane; i < rows * Tiles<D>::kBoxes * 8; i += 32) {
+    const int r = n + i / (Tiles<D>::kBoxes * 8), rem = i % (Tiles<D>::kBoxes * 8);
+    *reinterpret_cast<uint4*>(tile + (rem >> 3) * Tiles<D>::kBoxBytes + r * 128 + (rem & 7) * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// D[128 x 16 n16] = A B^T over D, both tiles K-major in shared memory (descriptor low halves).
+template <int D>
+__device__ __forceinline__ void product_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                           uint32_t b_hi, int n16) {
+  const uint32_t idesc = idesc_bf16_f32(kTile, 16 * n16, false);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = ((kk >> 2) * Tiles<D>::kBoxBytes + (kk & 3) * 32) >> 4;
+    mma_ss_split(d_tmem, a_lo + off, a_hi, b_lo + off, b_hi, idesc, kk > 0 ? 1u : 0u);
+  }
+}
+// D[128 x D] (+)= A B over 16 n16 rows of B (row-major tile): A in TMEM as packed bf16, its first 64
+// columns at a, the others at a + 64.
+template <int D>
+__device__ __forceinline__ void product_ts(uint32_t d_tmem, uint32_t a, uint32_t b_lo, uint32_t b_hi, int n16,
+                                           bool first) {
+  constexpr uint32_t idesc = idesc_bf16_f32(kTile, D, true);
+  if (n16 == 8) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      mma_ts_split(d_tmem, a + (kk >> 2) * 64 + (kk & 3) * 8, b_lo + kk * (2048 >> 4), b_hi, idesc,
+                   (!first || kk > 0) ? 1u : 0u);
+  } else {
+#pragma unroll 1
+    for (int kk = 0; kk < n16; ++kk)
+      mma_ts_split(d_tmem, a + (kk >> 2) * 64 + (kk & 3) * 8, b_lo + kk * (2048 >> 4), b_hi, idesc,
+                   (!first || kk > 0) ? 1u : 0u);
+  }
+}
+
+// 32 fp32 columns of this thread's TMEM lane, times f, as bf16 to columns [c0, c0 + 32) of its row:
+// lanes 2i and 2i + 1 trade halves, so that each instruction writes 32-byte sectors.  p0: the even
+// lane's row (+ 16 columns for the odd lane), p1 the odd lane's; wide: both are 32-byte aligned.
+__device__ __forceinline__ void store_columns(const uint32_t* r, float f, __nv_bfloat16* p0, __nv_bfloat16* p1,
+                                              bool ok0, bool ok1, bool wide) {
+  const bool odd = threadIdx.x & 1;
+  uint32_t pk[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    pk[c] = pack_bf16x2(__uint_as_float(r[2 * c]) * f, __uint_as_float(r[2 * c + 1]) * f);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? pk[c] : pk[8 + c], 1);
+    pk[c] = odd ? got : pk[c];
+    pk[8 + c] = odd ? pk[8 + c] : got;
+  }
+  if (ok0) st_global_32(p0, pk, wide);
+  if (ok1) st_global_32(p1, pk + 8, wide);
+}
+
+// ---- dK, dV ---------------------------------------------------------------------------------------------
+struct KvWork {
+  int more;                  // 0: no more work
+  int steps, first;          // (head, query tile) steps of the item: first, first + 1, ...
+  int head0, qtiles;         // step s: head head0 + s / qtiles, query tile s % qtiles
+  int q0, q_end;
+  int kv_head, k_row;        // the key tile
+  int rows, used;            // its rows inside the segment, and how many of them are used
+  int slot;                  // partial sums go to this slot; -1: straight to dk, dv
+};
+
+__device__ __forceinline__ KvWork decode_kv(uint32_t item, const uint32_t* __restrict__ ws, const CrossSegments& seg) {
+  const int S = seg.num_segments, group = seg.num_q_heads / seg.num_kv_heads;
+  const uint32_t* prefix = ws + kCrossBwdHeader + S + 1;
+  const int g = find_segment(prefix, S, item);
+  const Segment r = segment_of(seg, g);
+  const int steps = kv_steps(r, group), chunks = chunks_of(steps, static_cast<int>(ws[2])), tiles = tiles_of(r.keys);
+  int local = static_cast<int>(item - prefix[g]);
+  const int chunk = local % chunks;
+  local /= chunks;
+  KvWork d;
+  d.more = 1;
+  d.kv_head = local / tiles;
+  const int kt = local % tiles;
+  d.k_row = r.k0 + kt * kTile;
+  d.rows = min(kTile, r.keys - kt * kTile);
+  d.used = max(0, min(kTile, r.used - kt * kTile));
+  d.first = static_cast<int>(static_cast<int64_t>(steps) * chunk / chunks);
+  d.steps = static_cast<int>(static_cast<int64_t>(steps) * (chunk + 1) / chunks) - d.first;
+  d.slot = chunks > 1 ? static_cast<int>(item) : -1;
+  d.head0 = d.kv_head * group;
+  d.qtiles = max(1, tiles_of(r.rows));
+  d.q0 = r.q0;
+  d.q_end = r.q0 + r.rows;
+  if (d.used == 0) {  // no key of the tile is used: zeros, written once
+    d.steps = 0;
+    d.slot = -1;
+    if (chunk > 0) d.rows = 0;
+  }
+  return d;
+}
+
+template <int D>
+struct KvCfg {
+  static constexpr int kStages = 2;
+  // kv_full, kv_empty, s_full, dp_full, p_full, ds_full, acc_full, acc_empty, w_full[2], w_empty[2],
+  // drain, then q_full, q_empty, do_full, do_empty, st_full, st_empty
+  static constexpr int kNumBars = 13 + 6 * kStages;
+  static constexpr int kSmemBytes = 1024 + Tiles<D>::kBytes * (2 + 2 * kStages) + kStages * 2 * kTile * 4 +
+                                    kNumBars * 8 + 16 + 2 * sizeof(KvWork);
+  static constexpr int kColS = 0, kColP = 128, kColK = 256, kColV = 384;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
+  using C = KvCfg<D>;
+  using T = Tiles<D>;
+  constexpr int ST = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = sK + T::kBytes;
+  uint8_t* sQ = sV + T::kBytes;
+  uint8_t* sO = sQ + ST * T::kBytes;
+  float* s_lse = reinterpret_cast<float*>(sO + ST * T::kBytes);  // [ST][128], in units of log 2
+  float* s_delta = s_lse + ST * kTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_delta + ST * kTile);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  KvWork* work = reinterpret_cast<KvWork*>(tmem_slot + 4);
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8 * static_cast<uint32_t>(i); };
+  const uint32_t kv_full = bar(0), kv_empty = bar(1), s_full = bar(2), dp_full = bar(3), p_full = bar(4),
+                 ds_full = bar(5), acc_full = bar(6), acc_empty = bar(7), drain = bar(12);
+  auto w_full = [&](int i) { return bar(8 + i); };
+  auto w_empty = [&](int i) { return bar(10 + i); };
+  auto q_full = [&](int s) { return bar(13 + s); };
+  auto q_empty = [&](int s) { return bar(13 + ST + s); };
+  auto do_full = [&](int s) { return bar(13 + 2 * ST + s); };
+  auto do_empty = [&](int s) { return bar(13 + 3 * ST + s); };
+  auto st_full = [&](int s) { return bar(13 + 4 * ST + s); };
+  auto st_empty = [&](int s) { return bar(13 + 5 * ST + s); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(b, parity, a.wait_limit_ns)) != 0;
+  };
+  auto wait_long = [&](uint32_t b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_long(b, parity, a.wait_limit_ns)) != 0;
+  };
+  auto arrive_warp = [&](uint32_t b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b);
+  };
+  auto take = [&](int k, KvWork& d) {
+    if (!wait_long(w_full(k & 1), (k >> 1) & 1)) return false;
+    d = work[k & 1];
+    arrive_warp(w_empty(k & 1));
+    return true;
+  };
+
+  grid_dependency_wait();
+  launch_dependents();
+  if (__syncthreads_or(a.err != nullptr && *reinterpret_cast<volatile unsigned int*>(a.err) == kErrTimeout)) return;
+  const uint32_t total = a.plan[1];
+  if (blockIdx.x >= total) return;
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&a.tmap_q);
+    tma_prefetch_desc(&a.tmap_k);
+    tma_prefetch_desc(&a.tmap_v);
+    tma_prefetch_desc(&a.tmap_do);
+    const uint32_t one[] = {kv_full, kv_empty, s_full, dp_full, acc_full, drain};
+    for (uint32_t b : one) mbar_init(b, 1);
+    const uint32_t warps8[] = {p_full, ds_full, acc_empty};
+    for (uint32_t b : warps8) mbar_init(b, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(w_full(i), 1);
+      mbar_init(w_empty(i), 11);  // compute warps, loads, products, statistics
+    }
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(q_full(s), 1);
+      mbar_init(q_empty(s), 1);
+      mbar_init(do_full(s), 1);
+      mbar_init(do_empty(s), 1);
+      mbar_init(st_full(s), 1);
+      mbar_init(st_empty(s), 8);
+    }
+    fence_mbarrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 8) {
+    // ================= loads =================
+    bool ok = true, stalled = false;
+    uint32_t items = 0, n = 0, nd = 0;  // key tiles, Q tiles, dO tiles loaded so far
+    KvWork d;
+    for (int k = 0; ok && !stalled; ++k) {
+      ok = take(k, d);
+      if (!ok || !d.more) break;
+      if (d.steps == 0) continue;
+      ok = wait(kv_empty, (items & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(kv_full, 2 * T::kBytes);
+        for (int b = 0; b < T::kBoxes; ++b) {
+          tma_load_3d(smem_u32(sK + b * T::kBoxBytes), &a.tmap_k, b * 64, d.kv_head, d.k_row, kv_full);
+          tma_load_3d(smem_u32(sV + b * T::kBoxBytes), &a.tmap_v, b * 64, d.kv_head, d.k_row, kv_full);
+        }
+      }
+      ++items;
+      for (int i = 0; i < d.steps; ++i) {
+        if (n >= a.stall_after_tiles) {  // testing hook: as if the loads had stalled
+          stalled = true;
+          break;
+        }
+        const int s = static_cast<int>(n % ST), step = d.first + i;
+        const int head = d.head0 + step / d.qtiles, row = d.q0 + step % d.qtiles * kTile;
+        ok = wait_long(q_empty(s), ((n / ST) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) load_tile<D>(sQ + s * T::kBytes, &a.tmap_q, head, row, q_full(s));
+        ++n;
+        ok = wait_long(do_empty(s), ((nd / ST) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) load_tile<D>(sO + s * T::kBytes, &a.tmap_do, head, row, do_full(s));
+        ++nd;
+      }
+    }
+    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+    // never leave while a copy may still land
+    if (items > 0) mbar_wait(kv_full, (items - 1) & 1);
+    for (uint32_t i = 0; i < ST && i < n; ++i) mbar_wait(q_full((n - 1 - i) % ST), ((n - 1 - i) / ST) & 1);
+    for (uint32_t i = 0; i < ST && i < nd; ++i) mbar_wait(do_full((nd - 1 - i) % ST), ((nd - 1 - i) / ST) & 1);
+  } else if (warp == 9) {
+    // ================= products =================
+    const bool leader = elect_one();
+    constexpr uint32_t kTile16 = T::kBytes >> 4;
+    const SmemDesc dk = sw128_desc_split(smem_u32(sK), 16, 1024), dv = sw128_desc_split(smem_u32(sV), 16, 1024);
+    const SmemDesc dq = sw128_desc_split(smem_u32(sQ), 16, 1024), dd = sw128_desc_split(smem_u32(sO), 16, 1024);
+    // the same tiles as row-major B operands
+    const SmemDesc rq = sw128_desc_split(smem_u32(sQ), T::kBoxBytes, 1024);
+    const SmemDesc rd = sw128_desc_split(smem_u32(sO), T::kBoxBytes, 1024);
+    bool ok = true, issued = false;
+    uint32_t items = 0, n = 0;  // key tiles; steps whose dK has been issued
+    KvWork d;
+    for (int k = 0; ok; ++k) {
+      ok = take(k, d);
+      if (!ok || !d.more) break;
+      if (d.steps == 0) continue;
+      // rows of a step's query tile, and the two score products (n: the step's number over all items)
+      auto rows_of = [&](int i) { return min(kTile, d.q_end - d.q0 - (d.first + i) % d.qtiles * kTile); };
+      auto scores = [&](int i, uint32_t m) {  // S^T = K Q^T
+        const int s = static_cast<int>(m % ST), rows = rows_of(i);
+        if (!wait(q_full(s), (m / ST) & 1)) return false;
+        if (rows % 16 != 0) zero_rows<D>(sQ + s * T::kBytes, rows);
+        tc_fence_after();
+        if (leader) {
+          product_ss<D>(tmem + C::kColS, dk.lo, dk.hi, dq.lo + s * kTile16, dq.hi, steps16(rows));
+          mma_commit(s_full);
+        }
+        __syncwarp();
+        issued = true;
+        return true;
+      };
+      auto grads = [&](int i, uint32_t m) {  // dP^T = V dO^T
+        const int s = static_cast<int>(m % ST), rows = rows_of(i);
+        if (!wait(do_full(s), (m / ST) & 1)) return false;
+        if (rows % 16 != 0) zero_rows<D>(sO + s * T::kBytes, rows);
+        tc_fence_after();
+        if (leader) {
+          product_ss<D>(tmem + C::kColP, dv.lo, dv.hi, dd.lo + s * kTile16, dd.hi, steps16(rows));
+          mma_commit(dp_full);
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = wait(kv_full, items & 1) && scores(0, n) && grads(0, n);
+      for (int i = 0; i < d.steps && ok; ++i, ++n) {
+        const int s = static_cast<int>(n % ST), n16 = steps16(rows_of(i));
+        ok = wait(p_full, n & 1);
+        if (ok && i == 0) ok = wait(acc_empty, (items & 1) ^ 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {  // dV += P^T dO
+          product_ts<D>(tmem + C::kColV, tmem + C::kColS, rd.lo + s * kTile16, rd.hi, n16, i == 0);
+          mma_commit(do_empty(s));
+        }
+        __syncwarp();
+        if (i + 1 < d.steps) ok = scores(i + 1, n + 1);
+        if (ok) ok = wait(ds_full, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {  // dK += dS^T Q
+          product_ts<D>(tmem + C::kColK, tmem + C::kColP, rq.lo + s * kTile16, rq.hi, n16, i == 0);
+          mma_commit(q_empty(s));
+        }
+        __syncwarp();
+        if (i + 1 < d.steps) ok = grads(i + 1, n + 1);
+      }
+      if (!ok) break;
+      if (leader) {
+        mma_commit(acc_full);
+        mma_commit(kv_empty);
+      }
+      __syncwarp();
+      ++items;
+    }
+    if (!ok && leader) record_error(a.err, kErrTimeout);
+    if (issued && leader) {  // every product issued has completed before TMEM is released
+      mma_commit(drain);
+      mbar_wait(drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ================= scheduler =================
+    for (int k = 0;; ++k) {
+      const uint32_t item = blockIdx.x + static_cast<uint32_t>(k) * gridDim.x;
+      KvWork d{};
+      if (item < total) d = decode_kv(item, a.plan, a.seg);
+      if (!wait_long(w_empty(k & 1), ((k >> 1) & 1) ^ 1)) {
+        if (lane == 0) record_error(a.err, kErrTimeout);
+        break;
+      }
+      if (lane == 0) {
+        work[k & 1] = d;
+        mbar_arrive(w_full(k & 1));
+      }
+      __syncwarp();
+      if (!d.more) break;
+    }
+  } else if (warp == 11) {
+    // ================= row statistics of the query tiles =================
+    bool ok = true;
+    uint32_t n = 0;
+    KvWork d;
+    for (int k = 0; ok; ++k) {
+      ok = take(k, d);
+      if (!ok || !d.more) break;
+      for (int i = 0; i < d.steps; ++i, ++n) {
+        const int s = static_cast<int>(n % ST), step = d.first + i;
+        const size_t at = static_cast<size_t>(d.head0 + step / d.qtiles) * a.seg.capacity_q;
+        const int row = d.q0 + step % d.qtiles * kTile;
+        float l[4], e[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {  // rows past the end: weight exp2(0 - inf) = 0
+          const int r = row + lane + 32 * x;
+          l[x] = r < d.q_end ? a.lse[at + r] * 1.4426950408889634f : INFINITY;
+          e[x] = r < d.q_end ? a.delta[at + r] : 0.f;
+        }
+        ok = wait_long(st_empty(s), ((n / ST) & 1) ^ 1);
+        if (!ok) break;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s_lse[s * kTile + lane + 32 * x] = l[x];
+          s_delta[s * kTile + lane + 32 * x] = e[x];
+        }
+        arrive_warp(st_full(s));
+      }
+    }
+    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+  } else {
+    // ================= P, dS and the epilogue: key row = TMEM lane, query columns by warpgroup =====
+    const int half = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + C::kColS + 64 * half;
+    const uint32_t p_addr = tmem + lane_base + C::kColP + 64 * half;
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    bool ok = true;
+    uint32_t n = 0, items = 0;
+    KvWork d;
+    for (int k = 0; ok; ++k) {
+      ok = take(k, d);
+      if (!ok || !d.more) break;
+      // key rows that take no part (their K and V may be anything): masked by select
+      const bool dead = row >= d.used, any_dead = d.used < kTile;
+      for (int i = 0; i < d.steps; ++i, ++n) {
+        const int s = static_cast<int>(n % ST);
+        const float4* lse4 = reinterpret_cast<const float4*>(s_lse + s * kTile + 64 * half);
+        const float4* del4 = reinterpret_cast<const float4*>(s_delta + s * kTile + 64 * half);
+        ok = wait(st_full(s), (n / ST) & 1) && wait(s_full, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[64];
+        tmem_ld32(s_addr, x);
+        tmem_ld32(s_addr + 32, x + 32);
+        tmem_ld_wait();
+        tmem_reg_fence<64>(x);
+        float p[64];
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float4 v = lse4[c];
+          p[4 * c] = ex2_approx(fmaf(__uint_as_float(x[4 * c]), scale_log2, -v.x));
+          p[4 * c + 1] = ex2_approx(fmaf(__uint_as_float(x[4 * c + 1]), scale_log2, -v.y));
+          p[4 * c + 2] = ex2_approx(fmaf(__uint_as_float(x[4 * c + 2]), scale_log2, -v.z));
+          p[4 * c + 3] = ex2_approx(fmaf(__uint_as_float(x[4 * c + 3]), scale_log2, -v.w));
+        }
+        if (any_dead) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) p[c] = dead ? 0.f : p[c];
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+        tmem_st32(s_addr, w);
+        tmem_st_wait();
+        tc_fence_before();
+        arrive_warp(p_full);
+        ok = wait(dp_full, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld32(p_addr, x);
+        tmem_ld32(p_addr + 32, x + 32);
+        tmem_ld_wait();
+        tmem_reg_fence<64>(x);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float4 v = del4[c];
+          p[4 * c] *= __uint_as_float(x[4 * c]) - v.x;
+          p[4 * c + 1] *= __uint_as_float(x[4 * c + 1]) - v.y;
+          p[4 * c + 2] *= __uint_as_float(x[4 * c + 2]) - v.z;
+          p[4 * c + 3] *= __uint_as_float(x[4 * c + 3]) - v.w;
+        }
+        arrive_warp(st_empty(s));
+        if (any_dead) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) p[c] = dead ? 0.f : p[c];
+        }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+        tmem_st32(p_addr, w);
+        tmem_st_wait();
+        tc_fence_before();
+        arrive_warp(ds_full);
+      }
+      if (!ok) break;
+      // epilogue: warpgroup 0 takes dV, warpgroup 1 dK
+      if (d.steps > 0) {
+        ok = wait(acc_full, items & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      const uint32_t acc = tmem + lane_base + (half == 0 ? C::kColV : C::kColK);
+      const float f = half == 0 ? 1.f : a.scale;
+      const int odd = lane & 1, r0 = row - odd;
+      const int64_t stride = half == 0 ? a.dv_stride : a.dk_stride;
+      __nv_bfloat16* p0 = (half == 0 ? a.dv : a.dk) + (static_cast<int64_t>(d.k_row) + r0) * stride +
+                          d.kv_head * D + 16 * odd;
+      float* part = a.partials + ((static_cast<size_t>(max(d.slot, 0)) * 2 + half) * kTile + row) * D;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        uint32_t x[32];
+        if (d.steps > 0) {
+          tmem_ld32(acc + c0, x);
+          tmem_ld_wait();
+          tmem_reg_fence<32>(x);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] = 0u;
+        }
+        if (d.slot >= 0) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4*>(part + c0 + 4 * c) =
+                make_float4(__uint_as_float(x[4 * c]) * f, __uint_as_float(x[4 * c + 1]) * f,
+                            __uint_as_float(x[4 * c + 2]) * f, __uint_as_float(x[4 * c + 3]) * f);
+        } else {
+          store_columns(x, f, p0 + c0, p0 + stride + c0, r0 < d.rows, r0 + 1 < d.rows, a.wide);
+        }
+      }
+      if (d.steps > 0) {
+        tc_fence_before();
+        arrive_warp(acc_empty);
+        ++items;
+      }
+    }
+    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Sums the chunks of every cut key tile, in chunk order: a CTA per (item of chunk 0, dV or dK) in turn.
+template <int D>
+__global__ void __launch_bounds__(256)
+cross_dkv_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
+  grid_dependency_wait();
+  launch_dependents();
+  if (a.err != nullptr && *reinterpret_cast<const volatile unsigned int*>(a.err) == kErrTimeout) return;
+  if (a.plan[2] <= 1u) return;  // nothing was cut
+  const uint32_t total = a.plan[1];
+  const int S = a.seg.num_segments, group = a.seg.num_q_heads / a.seg.num_kv_heads;
+  const uint32_t* prefix = a.plan + kCrossBwdHeader + S + 1;
+  constexpr int kParts = 8;  // 16 rows each
+  for (uint32_t u = blockIdx.x; u < total * 2 * kParts; u += gridDim.x) {
+    const uint32_t item = u / (2 * kParts);
+    const int which = u / kParts % 2, r0 = u % kParts * (kTile / kParts);
+    const int g = find_segment(prefix, S, item);
+    const Segment r = segment_of(a.seg, g);
+    const int chunks = chunks_of(kv_steps(r, group), static_cast<int>(a.plan[2]));
+    if (chunks == 1 || (item - prefix[g]) % chunks != 0) continue;
+    const KvWork d = decode_kv(item, a.plan, a.seg);
+    if (d.slot < 0) continue;  // zeros, written already
+    const float* part = a.partials + (static_cast<size_t>(d.slot) * 2 + which) * kTile * D;
+    __nv_bfloat16* out = which == 0 ? a.dv : a.dk;
+    const int64_t stride = which == 0 ? a.dv_stride : a.dk_stride;
+    for (int i = threadIdx.x; i < kTile / kParts * (D / 8); i += 256) {
+      const int row = r0 + i / (D / 8), col = i % (D / 8) * 8;
+      if (row >= d.rows) continue;
+      float s[8] = {};
+#pragma unroll 4
+      for (int c = 0; c < chunks; ++c) {
+        const float4* src = reinterpret_cast<const float4*>(part + static_cast<size_t>(c) * 2 * kTile * D + row * D + col);
+        const float4 x = src[0], y = src[1];
+        s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
+        s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+      }
+      *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(d.k_row) + row) * stride + d.kv_head * D + col) =
+          make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+    }
+  }
+}
+
+// ---- dQ -------------------------------------------------------------------------------------------------
+struct QWork {
+  int more;
+  int head, kv_head;
+  int q_row, q_end;
+  int k_row, nkv, last_keys;  // nkv 0: no keys, dq = 0
+};
+
+__device__ __forceinline__ QWork decode_q(uint32_t item, const uint32_t* __restrict__ ws, const CrossSegments& seg) {
+  const int S = seg.num_segments, group = seg.num_q_heads / seg.num_kv_heads;
+  const uint32_t* prefix = ws + kCrossBwdHeader;
+  const int g = find_segment(prefix, S, item);
+  const Segment r = segment_of(seg, g);
+  const int tiles = tiles_of(r.rows), local = static_cast<int>(item - prefix[g]);
+  QWork d;
+  d.more = 1;
+  d.head = local / tiles;
+  d.kv_head = d.head / group;
+  d.q_row = r.q0 + local % tiles * kTile;
+  d.q_end = r.q0 + r.rows;
+  d.k_row = r.k0;
+  d.nkv = tiles_of(r.used);
+  d.last_keys = r.used - (d.nkv - 1) * kTile;
+  return d;
+}
+
+template <int D>
+struct QCfg {
+  static constexpr int kStagesK = 3, kStagesV = 2;
+  // q_full, q_empty, do_full, do_empty, s_full[2], dp_full, dp_read, ds_full[2], acc_full, acc_empty,
+  // w_full[2], w_empty[2], drain, then k_full, k_empty, v_full, v_empty
+  static constexpr int kNumBars = 17 + 2 * kStagesK + 2 * kStagesV;
+  static constexpr int kSmemBytes = 1024 + Tiles<D>::kBytes * (2 + kStagesK + kStagesV) + kNumBars * 8 + 16 +
+                                    2 * sizeof(QWork);
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+  static constexpr int kColS = 0, kColP = 256, kColQ = 384;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
+  using C = QCfg<D>;
+  using T = Tiles<D>;
+  constexpr int SK = C::kStagesK, SV = C::kStagesV;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sO = sQ + T::kBytes;
+  uint8_t* sK = sO + T::kBytes;
+  uint8_t* sV = sK + SK * T::kBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + SV * T::kBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  QWork* work = reinterpret_cast<QWork*>(tmem_slot + 4);
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar = [&](int i) { return bar0 + 8 * static_cast<uint32_t>(i); };
+  const uint32_t q_full = bar(0), q_empty = bar(1), do_full = bar(2), do_empty = bar(3), dp_full = bar(6),
+                 dp_read = bar(7), acc_full = bar(10), acc_empty = bar(11), drain = bar(16);
+  auto s_full = [&](uint32_t i) { return bar(4 + static_cast<int>(i)); };
+  // two of them: dP of the next step is issued before dS of this one is waited for, so a warp may
+  // finish its next dS while another still works on this one
+  auto ds_full = [&](uint32_t i) { return bar(8 + static_cast<int>(i)); };
+  auto w_full = [&](int i) { return bar(12 + i); };
+  auto w_empty = [&](int i) { return bar(14 + i); };
+  auto k_full = [&](int s) { return bar(17 + s); };
+  auto k_empty = [&](int s) { return bar(17 + SK + s); };
+  auto v_full = [&](int s) { return bar(17 + 2 * SK + s); };
+  auto v_empty = [&](int s) { return bar(17 + 2 * SK + SV + s); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(b, parity, a.wait_limit_ns)) != 0;
+  };
+  auto wait_long = [&](uint32_t b, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_long(b, parity, a.wait_limit_ns)) != 0;
+  };
+  auto arrive_warp = [&](uint32_t b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b);
+  };
+  auto take = [&](int k, QWork& d) {
+    if (!wait(w_full(k & 1), (k >> 1) & 1)) return false;
+    d = work[k & 1];
+    arrive_warp(w_empty(k & 1));
+    return true;
+  };
+
+  grid_dependency_wait();
+  launch_dependents();
+  if (__syncthreads_or(a.err != nullptr && *reinterpret_cast<volatile unsigned int*>(a.err) == kErrTimeout)) return;
+  const uint32_t total = a.plan[0];
+  if (blockIdx.x >= total) return;
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&a.tmap_q);
+    tma_prefetch_desc(&a.tmap_k);
+    tma_prefetch_desc(&a.tmap_v);
+    tma_prefetch_desc(&a.tmap_do);
+    const uint32_t one[] = {q_full, q_empty, do_full, do_empty, s_full(0), s_full(1), dp_full, acc_full, drain};
+    for (uint32_t b : one) mbar_init(b, 1);
+    const uint32_t warps8[] = {dp_read, ds_full(0), ds_full(1), acc_empty};
+    for (uint32_t b : warps8) mbar_init(b, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(w_full(i), 1);
+      mbar_init(w_empty(i), 11);  // compute warps, key/value loads, query loads, products
+    }
+    for (int s = 0; s < SK; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+    }
+    for (int s = 0; s < SV; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    fence_mbarrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 8) {
+    // ================= key/value loads =================
+    bool ok = true, stalled = false;
+    uint32_t kt = 0, vt = 0;
+    QWork d;
+    for (int k = 0; ok && !stalled; ++k) {
+      ok = take(k, d);
+      if (!ok || !d.more) break;
+      for (int j = 0; j < d.nkv; ++j) {
+        if (kt >= a.stall_after_tiles) {
+          stalled = true;
+          break;
+        }
+        const int s = static_cast<int>(kt % SK), v = static_cast<int>(vt % SV);
+        ok = wait_long(k_empty(s), ((kt / SK) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) load_tile<D>(sK + s * T::kBytes, &a.tmap_k, d.kv_head, d.k_row + j * kTile, k_full(s));
+        ++kt;
+        ok = wait_long(v_empty(v), ((vt / SV) & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) load_tile<D>(sV + v * T::kBytes, &a.tmap_v, d.kv_head, d.k_row + j * kTile, v_full(v));
+        ++vt;
+      }
+    }
+    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+    for (uint32_t i = 0; i < SK && i < kt; ++i) mbar_wait(k_full((kt - 1 - i) % SK), ((kt - 1 - i) / SK) & 1);
+    for (uint32_t i = 0; i < SV && i < vt; ++i) mbar_wait(v_full((vt - 1 - i) % SV), ((vt - 1 - i) / SV) & 1);
+  } else if (warp == 10) {
+    // ================= query and output-gradient loads =================
+    bool ok = true;
+    uint32_t n = 0, nd = 0;
+    QWork d;
+    for (int k = 0; ok; ++k) {
+      ok = take(k, d);
+      if (!ok || !d.more) break;
+      if (d.nkv == 0) continue;
+      ok = wait_long(q_empty, (n & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) load_tile<D>(sQ, &a.tmap_q, d.head, d.q_row, q_full);
+      ++n;
+      ok = wait_long(do_empty, (nd & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) load_tile<D>(sO, &a.tmap_do, d.head, d.q_row, do_full);
+      ++nd;
+    }
+    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+    if (n > 0) mbar_wait(q_full, (n - 1) & 1);
+    if (nd > 0) mbar_wait(do_full, (nd - 1) & 1);
+  } else if (warp == 11) {
+    // ================= scheduler =================
+    for (int k = 0;; ++k) {
+      const uint32_t item = blockIdx.x + static_cast<uint32_t>(k) * gridDim.x;
+      QWork d{};
+      if (item < total) d = decode_q(item, a.plan, a.seg);
+      if (!wait_long(w_empty(k & 1), ((k >> 1) & 1) ^ 1)) {
+        if (lane == 0) record_error(a.err, kErrTimeout);
+        break;
+      }
+      if (lane == 0) {
+        work[k & 1] = d;
+        mbar_arrive(w_full(k & 1));
+      }
+      __syncwarp();
+      if (!d.more) break;
+    }
+  } else if (warp == 9) {
+    // ================= products =================
+    const bool leader = elect_one();
+    constexpr uint32_t kTile16 = T::kBytes >> 4;
+    const SmemDesc dq = sw128_desc_split(smem_u32(sQ), 16, 1024), dd = sw128_desc_split(smem_u32(sO), 16, 1024);
+    const SmemDesc dk = sw128_desc_split(smem_u32(sK), 16, 1024), dv = sw128_desc_split(smem_u32(sV), 16, 1024);
+    const SmemDesc rk = sw128_desc_split(smem_u32(sK), T::kBoxBytes, 1024);
+    struct Item {
+      int more, nkv, last_keys;
+    } cur{}, nxt{};
+    int at = 0;  // items taken
+    auto next_item = [&](Item& i) {  // the next one with keys
+      QWork d;
+      do {
+        if (!take(at++, d)) return false;
+      } while (d.more && d.nkv == 0);
+      i = Item{d.more, d.nkv, d.last_keys};
+      return true;
+    };
+    auto keys_of = [](const Item& i, int j) { return j == i.nkv - 1 ? i.last_keys : kTile; };
+    uint32_t sc = 0, pc = 0, n = 0, items = 0;  // S and dP tiles issued, dQ steps issued, items begun
+    uint32_t qn = 0;
+    bool ok = next_item(cur), issued = false;
+    auto scores = [&](const Item& i, int j) {  // S = Q K^T of the ring's next K tile
+      const int s = static_cast<int>(sc % SK), keys = keys_of(i, j);
+      bool good = true;
+      if (j == 0) good = wait(q_full, qn & 1);
+      if (good) good = wait(k_full(s), (sc / SK) & 1);
+      if (!good) return false;
+      if (keys % 16 != 0) zero_rows<D>(sK + s * T::kBytes, keys);
+      tc_fence_after();
+      if (leader) {
+        product_ss<D>(tmem + C::kColS + 128 * (sc & 1), dq.lo, dq.hi, dk.lo + s * kTile16, dk.hi, steps16(keys));
+        mma_commit(s_full(sc & 1));
+        if (j == i.nkv - 1) mma_commit(q_empty);
+      }
+      __syncwarp();
+      ++sc;
+      issued = true;
+      return true;
+    };
+    auto grads = [&](const Item& i, int j) {  // dP = dO V^T, once the previous dP has been read
+      const int s = static_cast<int>(pc % SV);
+      bool good = true;
+      if (j == 0) good = wait(do_full, qn++ & 1);
+      if (good) good = wait(v_full(s), (pc / SV) & 1);
+      if (good && pc > 0) good = wait(dp_read, (pc - 1) & 1);
+      if (!good) return false;
+      tc_fence_after();
+      if (leader) {
+        product_ss<D>(tmem + C::kColP, dd.lo, dd.hi, dv.lo + s * kTile16, dv.hi, steps16(keys_of(i, j)));
+        mma_commit(dp_full);
+        mma_commit(v_empty(s));
+        if (j == i.nkv - 1) mma_commit(do_empty);
+      }
+      __syncwarp();
+      ++pc;
+      return true;
+    };
+    if (ok && cur.more) ok = scores(cur, 0) && grads(cur, 0);
+    while (ok && cur.more) {
+      for (int j = 0; j < cur.nkv && ok; ++j, ++n) {
+        const bool last = j == cur.nkv - 1;
+        if (last) ok = next_item(nxt);
+        if (ok && !last) ok = scores(cur, j + 1) && grads(cur, j + 1);
+        if (ok && last && nxt.more) ok = scores(nxt, 0) && grads(nxt, 0);
+        if (ok) ok = wait(ds_full(n & 1), (n >> 1) & 1);
+        if (ok && j == 0) ok = wait(acc_empty, (items & 1) ^ 1);
+        if (!ok) break;
+        tc_fence_after();
+        const int s = static_cast<int>(n % SK);
+        if (leader) {  // dQ += dS K
+          product_ts<D>(tmem + C::kColQ, tmem + C::kColS + 128 * (n & 1), rk.lo + s * kTile16, rk.hi,
+                        steps16(keys_of(cur, j)), j == 0);
+          mma_commit(k_empty(s));
+          if (last) mma_commit(acc_full);
+        }
+        __syncwarp();
+      }
+      ++items;
+      cur = nxt;
+    }
+    if (!ok && leader) record_error(a.err, kErrTimeout);
+    if (issued && leader) {
+      mma_commit(drain);
+      mbar_wait(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ================= dS and the epilogue: query row = TMEM lane, keys by warpgroup ==============
+    const int half = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t p_addr = tmem + lane_base + C::kColP + 64 * half;
+    const float scale_log2 = a.scale * 1.4426950408889634f;
+    bool ok = true;
+    uint32_t n = 0, items = 0;
+    QWork d;
+    for (int k = 0; ok; ++k) {
+      ok = take(k, d);
+      if (!ok || !d.more) break;
+      const int q_row = d.q_row + row;
+      float lse2 = 0.f, delta = 0.f;
+      if (q_row < d.q_end && d.nkv > 0) {
+        const size_t i = static_cast<size_t>(d.head) * a.seg.capacity_q + q_row;
+        lse2 = a.lse[i] * 1.4426950408889634f;
+        delta = a.delta[i];
+      }
+      for (int j = 0; j < d.nkv; ++j, ++n) {
+        const uint32_t s_addr = tmem + lane_base + C::kColS + 128 * (n & 1) + 64 * half;
+        ok = wait(s_full(n & 1), (n >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t x[64];
+        tmem_ld32(s_addr, x);
+        tmem_ld32(s_addr + 32, x + 32);
+        tmem_ld_wait();
+        tmem_reg_fence<64>(x);
+        float p[64];
+#pragma unroll
+        for (int c = 0; c < 64; ++c) p[c] = ex2_approx(fmaf(__uint_as_float(x[c]), scale_log2, -lse2));
+        ok = wait(dp_full, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_ld32(p_addr, x);
+        tmem_ld32(p_addr + 32, x + 32);
+        tmem_ld_wait();
+        tmem_reg_fence<64>(x);
+        tc_fence_before();
+        arrive_warp(dp_read);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(x[c]) - delta;
+        if (j == d.nkv - 1 && d.last_keys < kTile) {  // keys past the end
+#pragma unroll
+          for (int c = 0; c < 64; ++c) p[c] = 64 * half + c < d.last_keys ? p[c] : 0.f;
+        }
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+        tmem_st32(s_addr, w);
+        tmem_st_wait();
+        tc_fence_before();
+        arrive_warp(ds_full(n & 1));
+      }
+      if (!ok) break;
+      if (d.nkv > 0) {
+        ok = wait(acc_full, items & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      // epilogue: each warpgroup stores half the columns
+      const int odd = lane & 1, r0 = d.q_row + row - odd;
+      __nv_bfloat16* p0 = a.dq + static_cast<int64_t>(r0) * a.dq_stride + d.head * D + 16 * odd;
+#pragma unroll 1
+      for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
+        uint32_t x[32];
+        if (d.nkv > 0) {
+          tmem_ld32(tmem + lane_base + C::kColQ + c0, x);
+          tmem_ld_wait();
+          tmem_reg_fence<32>(x);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] = 0u;
+        }
+        store_columns(x, a.scale, p0 + c0, p0 + a.dq_stride + c0, r0 < d.q_end, r0 + 1 < d.q_end, a.wide);
+      }
+      if (d.nkv > 0) {
+        tc_fence_before();
+        arrive_warp(acc_empty);
+        ++items;
+      }
+    }
+    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch(const CrossBwdArgs& a, cudaStream_t stream) {
+  cudaError_t e = allow_shared_memory<KvCfg<D>::kSmemBytes>(cross_dkv_kernel<D>);
+  if (e != cudaSuccess) return e;
+  e = allow_shared_memory<QCfg<D>::kSmemBytes>(cross_dq_kernel<D>);
+  if (e != cudaSuccess) return e;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  e = launch_programmatic(cross_bwd_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.seg, a.plan,
+                          a.slots, sms, a.err);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(a.seg.capacity_q) * a.seg.num_q_heads;
+  if (rows > 0) {
+    constexpr int kPerCta = 256 / (D / 8) * 4;
+    const int64_t want = (rows + kPerCta - 1) / kPerCta, most = static_cast<int64_t>(sms) * 8;
+    e = launch_programmatic(cross_delta_kernel<D>, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(256),
+                            0, stream, static_cast<const uint4*>(a.o), static_cast<const uint4*>(a.dout), rows,
+                            a.seg.num_q_heads, a.seg.capacity_q, a.delta);
+    if (e != cudaSuccess) return e;
+    e = launch_programmatic(cross_dq_kernel<D>, dim3(sms), dim3(kThreads), QCfg<D>::kSmemBytes, stream, a);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.seg.capacity_k > 0) {
+    e = launch_programmatic(cross_dkv_kernel<D>, dim3(sms), dim3(kThreads), KvCfg<D>::kSmemBytes, stream, a);
+    if (e != cudaSuccess) return e;
+    e = launch_programmatic(cross_dkv_sum_kernel<D>, dim3(4 * sms), dim3(256), 0, stream, a);
+  }
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_cross_bwd(const CrossBwdArgs& a, int head_dim, cudaStream_t stream) {
+  return head_dim == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+}
+
+}  // namespace h3

@@ -301,7 +301,7 @@ struct Cfg {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                  const __grid_constant__ CUtensorMap tmap_v, __nv_bfloat16* __restrict__ out,
+                  const __grid_constant__ CUtensorMap tmap_v, __nv_bfloat16* __restrict__ out, int wide,
                   float* __restrict__ lse, const __grid_constant__ CrossSegments seg, float scale,
                   float scale_log2, const uint32_t* __restrict__ ws, uint8_t* __restrict__ split_area,
                   unsigned int* err, unsigned long long wait_ns, unsigned int stall_after) {
@@ -691,8 +691,8 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             pk[c] = odd ? got : pk[c];
             pk[8 + c] = odd ? pk[8 + c] : got;
           }
-          if (r0 < d.seg_end) st_global_v8(p0 + c0, pk);
-          if (r0 + 1 < d.seg_end) st_global_v8(p1 + c0, pk + 8);
+          if (r0 < d.seg_end) st_global_32(p0 + c0, pk, wide);
+          if (r0 + 1 < d.seg_end) st_global_32(p1 + c0, pk + 8, wide);
         }
       }
     }
@@ -913,7 +913,7 @@ cudaError_t launch(const CrossArgs& a, cudaStream_t stream) {
   e = launch_programmatic(cross_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.seg, ws, split, sms, a.err);
   if (e != cudaSuccess) return e;
   e = launch_programmatic(cross_attn_kernel<D>, dim3(sms), dim3(kThreads), C::kSmemBytes, stream, a.tmap_q,
-                          a.tmap_k, a.tmap_v, static_cast<__nv_bfloat16*>(a.o), a.lse, a.seg, a.scale,
+                          a.tmap_k, a.tmap_v, static_cast<__nv_bfloat16*>(a.o), a.wide, a.lse, a.seg, a.scale,
                           a.scale * 1.4426950408889634f, static_cast<const uint32_t*>(ws), split, a.err,
                           static_cast<unsigned long long>(a.wait_limit_ns), a.stall_after_tiles);
   if (e != cudaSuccess) return e;

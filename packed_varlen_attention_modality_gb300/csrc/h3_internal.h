@@ -180,6 +180,7 @@ struct CrossArgs {
   CUtensorMap tmap_q, tmap_k, tmap_v;  // 3-D views {D, H, rows}
   CrossSegments seg;
   void* o;
+  int wide;  // o may be stored in 32-byte pieces
   float* lse;
   float scale;
   void* workspace;   // attn_plan_bytes(num_segments): the work plan
@@ -190,9 +191,52 @@ struct CrossArgs {
 };
 cudaError_t launch_cross_attn(const CrossArgs& a, int head_dim, cudaStream_t stream);
 
+// Gradient.  Work plan: header words, then the item prefixes of the two product kernels.  A key tile's
+// query range may be cut into up to kCrossBwdMaxChunks chunks, whose partial sums take a slot each
+// (two tiles of 128 x head_dim fp32).
+constexpr int kCrossBwdHeader = 4;
+constexpr int kCrossBwdMaxSlots = 1216;  // 8 x 152
+constexpr int kCrossBwdMaxChunks = 16;
+struct CrossBwdArgs {
+  CUtensorMap tmap_q, tmap_k, tmap_v, tmap_do;
+  CrossSegments seg;
+  const void *o, *dout;
+  const float* lse;
+  __nv_bfloat16 *dq, *dk, *dv;
+  int64_t dq_stride, dk_stride, dv_stride;
+  int wide;  // gradients may be stored in 32-byte pieces
+  float scale;
+  uint32_t* plan;
+  float* delta;     // [num_q_heads, capacity_q]
+  float* partials;  // slots x 2 x 128 x head_dim
+  int slots;
+  unsigned int* err;
+  uint64_t wait_limit_ns;
+  uint32_t stall_after_tiles;
+};
+struct CrossBwdWorkspace {
+  size_t delta, partials, bytes;  // offsets (the plan is at 0) and the whole
+  int slots;
+};
+inline CrossBwdWorkspace cross_bwd_workspace(const CrossSegments& s, int head_dim) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  CrossBwdWorkspace w;
+  w.delta = up((kCrossBwdHeader + 2 * (static_cast<size_t>(s.num_segments) + 1)) * sizeof(uint32_t));
+  w.partials = w.delta + up(static_cast<size_t>(s.num_q_heads) * s.capacity_q * sizeof(float));
+  // no more slots than chunks of all key tiles the capacity allows
+  const int64_t tiles = (static_cast<int64_t>(s.capacity_k) / 128 + s.num_segments) * s.num_kv_heads;
+  const int64_t steps = static_cast<int64_t>(s.num_q_heads / s.num_kv_heads) * ((s.max_seqlen_q + 127) / 128);
+  const int64_t chunks = steps < kCrossBwdMaxChunks ? steps : kCrossBwdMaxChunks;
+  const int64_t all = chunks > 1 ? tiles * chunks : 0;  // one chunk goes straight to the gradients
+  w.slots = static_cast<int>(all < kCrossBwdMaxSlots ? all : kCrossBwdMaxSlots);
+  w.bytes = w.partials + static_cast<size_t>(w.slots) * 2 * 128 * head_dim * sizeof(float);
+  return w;
+}
+cudaError_t launch_cross_bwd(const CrossBwdArgs& a, int head_dim, cudaStream_t stream);
+
 // Few rows per segment: at most kCrossTokenRows of (rows x query heads per key head).
 constexpr int kCrossTokenRows = 16;
-constexpr int kCrossTokenCtas = 2432;  // CTAs aimed at: 8 waves of 2 x 152
+constexpr int kCrossTokenCtas = 608;  // CTAs aimed at: two waves of 2 x 152 (8 waves: 64 us, not 58)
 struct CrossTokenArgs {
   CrossSegments seg;
   const __nv_bfloat16 *q, *k, *v;

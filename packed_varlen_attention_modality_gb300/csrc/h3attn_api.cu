@@ -67,6 +67,7 @@ EncodeTiledFn encode_tiled_fn() {
   return fn;
 }
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // 3-D view {D, H, rows} of a bf16 [rows, H, D] tensor; box {64, 1, 128}, 128-byte swizzle.
@@ -628,6 +629,7 @@ h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* d, const void* q, c
     return H3_ERR_CUDA;
   a.seg = cross_segments(d, cu_seqlens_q, cu_seqlens_k, seqused_k);
   a.o = o;
+  a.wide = aligned32(o);
   a.lse = lse;
   a.scale = cross_scale(d);
   a.workspace = workspace;
@@ -638,6 +640,73 @@ h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* d, const void* q, c
   a.stall_after_tiles = h3::stall_after_tiles();
   if (a.err == nullptr) return H3_ERR_CUDA;
   return from_cuda(h3::launch_cross_attn(a, d->head_dim, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t h3_varlen_cross_attn_bwd_workspace_size(const h3_cross_attn_desc* d) {
+  if (d == nullptr || !cross_sizes_ok(d) || d->num_segments == 0) return 0;
+  return h3::cross_bwd_workspace(cross_segments(d, nullptr, nullptr, nullptr), d->head_dim).bytes;
+}
+
+h3_status h3_varlen_cross_attn_bwd(const h3_cross_attn_desc* d, const void* dout, const void* q,
+                                   const void* k, const void* v, const void* o, const float* lse,
+                                   const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                   const int32_t* seqused_k, void* dq, void* dk, void* dv,
+                                   void* workspace, size_t workspace_bytes, h3_stream_t stream) {
+  if (d == nullptr || cu_seqlens_q == nullptr || cu_seqlens_k == nullptr) return H3_ERR_NULL;
+  if (!cross_sizes_ok(d)) return H3_ERR_INVALID_ARG;
+  const bool none_q = d->capacity_q == 0, none_k = d->capacity_k == 0;
+  if (!none_q && (dout == nullptr || q == nullptr || o == nullptr || lse == nullptr || dq == nullptr))
+    return H3_ERR_NULL;
+  if (!none_k && (dk == nullptr || dv == nullptr)) return H3_ERR_NULL;
+  if (none_q && none_k) return d->head_dim == 64 || d->head_dim == 128 ? H3_OK : H3_ERR_UNSUPPORTED;
+  int64_t strides[3];
+  // a side without rows may be NULL: the other side's tensor stands in for the checks
+  h3_status st = check_cross(d, none_q ? k : q, none_k ? q : k, none_k ? q : v, cu_seqlens_q, cu_seqlens_k,
+                             seqused_k, strides);
+  if (st != H3_OK) return st;
+  if (!aligned16(dout) || !aligned16(o) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return H3_ERR_MISALIGNED;
+  h3::CrossBwdArgs a{};
+  if ((st = token_stride(d->dq_stride, d->num_q_heads, d->head_dim, &a.dq_stride)) != H3_OK ||
+      (st = token_stride(d->dk_stride, d->num_kv_heads, d->head_dim, &a.dk_stride)) != H3_OK ||
+      (st = token_stride(d->dv_stride, d->num_kv_heads, d->head_dim, &a.dv_stride)) != H3_OK)
+    return st;
+  const size_t need = h3_varlen_cross_attn_bwd_workspace_size(d);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return H3_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return H3_ERR_MISALIGNED;
+  if (d->num_segments == 0) return H3_OK;
+  if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
+
+  // a side without rows is never read: any valid map will do
+  const int cap_q = none_q ? d->capacity_k : d->capacity_q, cap_k = none_k ? d->capacity_q : d->capacity_k;
+  const int hq = none_q ? d->num_kv_heads : d->num_q_heads, hk = none_k ? d->num_q_heads : d->num_kv_heads;
+  if (!make_qkv_map(&a.tmap_q, none_q ? k : q, cap_q, hq, d->head_dim, strides[none_q ? 1 : 0]) ||
+      !make_qkv_map(&a.tmap_do, none_q ? k : dout, cap_q, hq, d->head_dim, none_q ? strides[1] : 0) ||
+      !make_qkv_map(&a.tmap_k, none_k ? q : k, cap_k, hk, d->head_dim, strides[none_k ? 0 : 1]) ||
+      !make_qkv_map(&a.tmap_v, none_k ? q : v, cap_k, hk, d->head_dim, strides[none_k ? 0 : 2]))
+    return H3_ERR_CUDA;
+  a.seg = cross_segments(d, cu_seqlens_q, cu_seqlens_k, seqused_k);
+  a.o = o;
+  a.dout = dout;
+  a.lse = lse;
+  a.dq = static_cast<__nv_bfloat16*>(dq);
+  a.dk = static_cast<__nv_bfloat16*>(dk);
+  a.dv = static_cast<__nv_bfloat16*>(dv);
+  a.wide = aligned32(dq) && aligned32(dk) && aligned32(dv) &&
+           (a.dq_stride | a.dk_stride | a.dv_stride) % 16 == 0;
+  a.scale = cross_scale(d);
+  const h3::CrossBwdWorkspace w = h3::cross_bwd_workspace(a.seg, d->head_dim);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  a.plan = reinterpret_cast<uint32_t*>(base);
+  a.delta = reinterpret_cast<float*>(base + w.delta);
+  a.partials = reinterpret_cast<float*>(base + w.partials);
+  a.slots = w.slots;
+  a.err = device_error_ptr();
+  a.wait_limit_ns = h3::wait_limit_ns();
+  a.stall_after_tiles = h3::stall_after_tiles();
+  if (a.err == nullptr) return H3_ERR_CUDA;
+  return from_cuda(h3::launch_cross_bwd(a, d->head_dim, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 h3_status h3_window_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse,

@@ -179,6 +179,16 @@ __device__ __forceinline__ void st_global_v8(void* ptr, const uint32_t* r) {
                : "memory");
 }
 
+// The same 32 bytes to a pointer that may be aligned to 16 bytes only (wide: to 32).
+__device__ __forceinline__ void st_global_32(void* ptr, const uint32_t* r, bool wide) {
+  if (wide) {
+    st_global_v8(ptr, r);
+  } else {
+    static_cast<uint4*>(ptr)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    static_cast<uint4*>(ptr)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
+
 // ---------------------------------------------------------------------------------------------
 // tcgen05: tensor memory allocation, MMA, commit, TMEM <-> register moves.
 // ---------------------------------------------------------------------------------------------
