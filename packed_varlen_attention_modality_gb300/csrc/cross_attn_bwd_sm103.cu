@@ -16,8 +16,8 @@
 // and dO in shared memory serves both products that read it.  Each thread owns a key row and half the
 // 128 query columns.  Tensor order: dV_i, S_{i+1} while dS_i is computed, dK_i, dP_{i+1} while P_{i+1}
 // is.  TMEM (512 columns): S^T/P^T, dP^T/dS^T, dK, dV.
-// dQ: S = Q K^T (two buffers), dP = dO V^T, dQ += dS K.  Tensor order: S_{j+1}, dP_{j+1}, dQ_j; it runs
-// from one item into the next, since key lists may be a few tiles.
+// dQ: S = Q K^T (two buffers), dP = dO V^T, dQ += dS K with dS written over dP.  Tensor order: dQ_j,
+// dP_{j+1}, S_{j+2}; it runs from one item into the next, since key lists may be a few tiles.
 //
 // P and dS are rounded to bf16 for the tensor core (half a step, 2^-8 relative at most); everything
 // else is fp32 until the gradients are rounded once.  Rows and keys past a segment's end are zeroed
@@ -331,12 +331,15 @@ __device__ __forceinline__ KvWork decode_kv(uint32_t item, const uint32_t* __res
 
 template <int D>
 struct KvCfg {
-  static constexpr int kStages = 2;
+  // Q is held longest (S to dK), so its ring is a tile deeper than dO's (dP to dV): 7 tiles with K and
+  // V, all that fits at D = 128.
+  static constexpr int kStagesQ = 3, kStagesO = 2;
   // kv_full, kv_empty, s_full, dp_full, p_full, ds_full, acc_full, acc_empty, w_full[2], w_empty[2],
-  // drain, then q_full, q_empty, do_full, do_empty, st_full, st_empty
-  static constexpr int kNumBars = 13 + 6 * kStages;
-  static constexpr int kSmemBytes = 1024 + Tiles<D>::kBytes * (2 + 2 * kStages) + kStages * 2 * kTile * 4 +
+  // drain, then q_full, q_empty, st_full, st_empty, do_full, do_empty
+  static constexpr int kNumBars = 13 + 2 * kStagesQ + 4 * kStagesO;
+  static constexpr int kSmemBytes = Tiles<D>::kBytes * (2 + kStagesQ + kStagesO) + kStagesO * 2 * kTile * 4 +
                                     kNumBars * 8 + 16 + 2 * sizeof(KvWork);
+  static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
   static constexpr int kColS = 0, kColP = 128, kColK = 256, kColV = 384;
 };
 
@@ -345,17 +348,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
   using C = KvCfg<D>;
   using T = Tiles<D>;
-  constexpr int ST = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  constexpr int SQ = C::kStagesQ, SO = C::kStagesO;
+  extern __shared__ __align__(1024) uint8_t smem[];  // no room to align it by hand
   uint8_t* sK = smem;
   uint8_t* sV = sK + T::kBytes;
   uint8_t* sQ = sV + T::kBytes;
-  uint8_t* sO = sQ + ST * T::kBytes;
-  float* s_lse = reinterpret_cast<float*>(sO + ST * T::kBytes);  // [ST][128], in units of log 2
-  float* s_delta = s_lse + ST * kTile;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_delta + ST * kTile);
+  uint8_t* sO = sQ + SQ * T::kBytes;
+  float* s_lse = reinterpret_cast<float*>(sO + SO * T::kBytes);  // [SO][128], in units of log 2
+  float* s_delta = s_lse + SO * kTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_delta + SO * kTile);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   KvWork* work = reinterpret_cast<KvWork*>(tmem_slot + 4);
   const uint32_t bar0 = smem_u32(bars);
@@ -365,15 +366,21 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
   auto w_full = [&](int i) { return bar(8 + i); };
   auto w_empty = [&](int i) { return bar(10 + i); };
   auto q_full = [&](int s) { return bar(13 + s); };
-  auto q_empty = [&](int s) { return bar(13 + ST + s); };
-  auto do_full = [&](int s) { return bar(13 + 2 * ST + s); };
-  auto do_empty = [&](int s) { return bar(13 + 3 * ST + s); };
-  auto st_full = [&](int s) { return bar(13 + 4 * ST + s); };
-  auto st_empty = [&](int s) { return bar(13 + 5 * ST + s); };
+  auto q_empty = [&](int s) { return bar(13 + SQ + s); };
+  auto st_full = [&](int s) { return bar(13 + 2 * SQ + s); };
+  auto st_empty = [&](int s) { return bar(13 + 2 * SQ + SO + s); };
+  auto do_full = [&](int s) { return bar(13 + 2 * SQ + 2 * SO + s); };
+  auto do_empty = [&](int s) { return bar(13 + 2 * SQ + 3 * SO + s); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t b, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(b, parity, a.wait_limit_ns)) != 0;
+  };
+  auto wait2 = [&](uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {  // the polls overlap
+    bool r0 = mbar_try_wait(b0, p0), r1 = mbar_try_wait(b1, p1);
+    if (!r0) r0 = mbar_wait(b0, p0, a.wait_limit_ns);
+    if (!r1) r1 = mbar_wait(b1, p1, a.wait_limit_ns);
+    return __all_sync(0xffffffffu, r0 && r1) != 0;
   };
   auto wait_long = [&](uint32_t b, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_long(b, parity, a.wait_limit_ns)) != 0;
@@ -394,6 +401,10 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
   if (__syncthreads_or(a.err != nullptr && *reinterpret_cast<volatile unsigned int*>(a.err) == kErrTimeout)) return;
   const uint32_t total = a.plan[1];
   if (blockIdx.x >= total) return;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the tiles' swizzle needs it; not met on any known driver
+    if (threadIdx.x == 0) record_error(a.err, kErrTimeout);
+    return;
+  }
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&a.tmap_q);
     tma_prefetch_desc(&a.tmap_k);
@@ -407,13 +418,15 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
       mbar_init(w_full(i), 1);
       mbar_init(w_empty(i), 11);  // compute warps, loads, products, statistics
     }
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < SQ; ++s) {
       mbar_init(q_full(s), 1);
       mbar_init(q_empty(s), 1);
-      mbar_init(do_full(s), 1);
-      mbar_init(do_empty(s), 1);
+    }
+    for (int s = 0; s < SO; ++s) {
       mbar_init(st_full(s), 1);
       mbar_init(st_empty(s), 8);
+      mbar_init(do_full(s), 1);
+      mbar_init(do_empty(s), 1);
     }
     fence_mbarrier_init();
   }
@@ -450,23 +463,23 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
           stalled = true;
           break;
         }
-        const int s = static_cast<int>(n % ST), step = d.first + i;
+        const int s = static_cast<int>(n % SQ), o = static_cast<int>(nd % SO), step = d.first + i;
         const int head = d.head0 + step / d.qtiles, row = d.q0 + step % d.qtiles * kTile;
-        ok = wait_long(q_empty(s), ((n / ST) & 1) ^ 1);
+        ok = wait_long(q_empty(s), ((n / SQ) & 1) ^ 1);
         if (!ok) break;
         if (lane == 0) load_tile<D>(sQ + s * T::kBytes, &a.tmap_q, head, row, q_full(s));
         ++n;
-        ok = wait_long(do_empty(s), ((nd / ST) & 1) ^ 1);
+        ok = wait_long(do_empty(o), ((nd / SO) & 1) ^ 1);
         if (!ok) break;
-        if (lane == 0) load_tile<D>(sO + s * T::kBytes, &a.tmap_do, head, row, do_full(s));
+        if (lane == 0) load_tile<D>(sO + o * T::kBytes, &a.tmap_do, head, row, do_full(o));
         ++nd;
       }
     }
     if (!ok && lane == 0) record_error(a.err, kErrTimeout);
     // never leave while a copy may still land
     if (items > 0) mbar_wait(kv_full, (items - 1) & 1);
-    for (uint32_t i = 0; i < ST && i < n; ++i) mbar_wait(q_full((n - 1 - i) % ST), ((n - 1 - i) / ST) & 1);
-    for (uint32_t i = 0; i < ST && i < nd; ++i) mbar_wait(do_full((nd - 1 - i) % ST), ((nd - 1 - i) / ST) & 1);
+    for (uint32_t i = 0; i < SQ && i < n; ++i) mbar_wait(q_full((n - 1 - i) % SQ), ((n - 1 - i) / SQ) & 1);
+    for (uint32_t i = 0; i < SO && i < nd; ++i) mbar_wait(do_full((nd - 1 - i) % SO), ((nd - 1 - i) / SO) & 1);
   } else if (warp == 9) {
     // ================= products =================
     const bool leader = elect_one();
@@ -483,11 +496,14 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
       ok = take(k, d);
       if (!ok || !d.more) break;
       if (d.steps == 0) continue;
-      // rows of a step's query tile, and the two score products (n: the step's number over all items)
-      auto rows_of = [&](int i) { return min(kTile, d.q_end - d.q0 - (d.first + i) % d.qtiles * kTile); };
-      auto scores = [&](int i, uint32_t m) {  // S^T = K Q^T
-        const int s = static_cast<int>(m % ST), rows = rows_of(i);
-        if (!wait(q_full(s), (m / ST) & 1)) return false;
+      int tile = d.first % d.qtiles;  // query tile of the step whose scores are next
+      auto next_rows = [&] {
+        const int rows = min(kTile, d.q_end - d.q0 - tile * kTile);
+        tile = tile + 1 == d.qtiles ? 0 : tile + 1;
+        return rows;
+      };
+      auto scores = [&](uint32_t m, int rows) {  // S^T = K Q^T of step m (counted over all items)
+        const int s = static_cast<int>(m % SQ);
         if (rows % 16 != 0) zero_rows<D>(sQ + s * T::kBytes, rows);
         tc_fence_after();
         if (leader) {
@@ -495,12 +511,9 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
           mma_commit(s_full);
         }
         __syncwarp();
-        issued = true;
-        return true;
       };
-      auto grads = [&](int i, uint32_t m) {  // dP^T = V dO^T
-        const int s = static_cast<int>(m % ST), rows = rows_of(i);
-        if (!wait(do_full(s), (m / ST) & 1)) return false;
+      auto grads = [&](uint32_t m, int rows) {  // dP^T = V dO^T
+        const int s = static_cast<int>(m % SO);
         if (rows % 16 != 0) zero_rows<D>(sO + s * T::kBytes, rows);
         tc_fence_after();
         if (leader) {
@@ -508,22 +521,34 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
           mma_commit(dp_full);
         }
         __syncwarp();
-        return true;
       };
-      ok = wait(kv_full, items & 1) && scores(0, n) && grads(0, n);
-      for (int i = 0; i < d.steps && ok; ++i, ++n) {
-        const int s = static_cast<int>(n % ST), n16 = steps16(rows_of(i));
+      int rows = next_rows(), rows_next = kTile;
+      ok = wait(kv_full, items & 1) && wait2(q_full(n % SQ), (n / SQ) & 1, do_full(n % SO), (n / SO) & 1);
+      if (!ok) break;
+      scores(n, rows);
+      grads(n, rows);
+      issued = true;
+      for (int i = 0; i < d.steps; ++i, ++n) {
+        const int s = static_cast<int>(n % SQ), o = static_cast<int>(n % SO), n16 = steps16(rows);
+        const uint32_t m = n + 1;
+        const bool more = i + 1 < d.steps;
+        // one wait before each product: it passes while the last ones of the product before it run
         ok = wait(p_full, n & 1);
         if (ok && i == 0) ok = wait(acc_empty, (items & 1) ^ 1);
         if (!ok) break;
         tc_fence_after();
         if (leader) {  // dV += P^T dO
-          product_ts<D>(tmem + C::kColV, tmem + C::kColS, rd.lo + s * kTile16, rd.hi, n16, i == 0);
-          mma_commit(do_empty(s));
+          product_ts<D>(tmem + C::kColV, tmem + C::kColS, rd.lo + o * kTile16, rd.hi, n16, i == 0);
+          mma_commit(do_empty(o));
         }
         __syncwarp();
-        if (i + 1 < d.steps) ok = scores(i + 1, n + 1);
-        if (ok) ok = wait(ds_full, n & 1);
+        if (more) {
+          rows_next = next_rows();
+          ok = wait(q_full(m % SQ), (m / SQ) & 1);
+          if (!ok) break;
+          scores(m, rows_next);
+        }
+        ok = wait(ds_full, n & 1);
         if (!ok) break;
         tc_fence_after();
         if (leader) {  // dK += dS^T Q
@@ -531,7 +556,12 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
           mma_commit(q_empty(s));
         }
         __syncwarp();
-        if (i + 1 < d.steps) ok = grads(i + 1, n + 1);
+        if (more) {
+          ok = wait(do_full(m % SO), (m / SO) & 1);
+          if (!ok) break;
+          grads(m, rows_next);
+        }
+        rows = rows_next;
       }
       if (!ok) break;
       if (leader) {
@@ -573,7 +603,7 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
       ok = take(k, d);
       if (!ok || !d.more) break;
       for (int i = 0; i < d.steps; ++i, ++n) {
-        const int s = static_cast<int>(n % ST), step = d.first + i;
+        const int s = static_cast<int>(n % SO), step = d.first + i;
         const size_t at = static_cast<size_t>(d.head0 + step / d.qtiles) * a.seg.capacity_q;
         const int row = d.q0 + step % d.qtiles * kTile;
         float l[4], e[4];
@@ -583,7 +613,7 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
           l[x] = r < d.q_end ? a.lse[at + r] * 1.4426950408889634f : INFINITY;
           e[x] = r < d.q_end ? a.delta[at + r] : 0.f;
         }
-        ok = wait_long(st_empty(s), ((n / ST) & 1) ^ 1);
+        ok = wait_long(st_empty(s), ((n / SO) & 1) ^ 1);
         if (!ok) break;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -610,10 +640,10 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
       // key rows that take no part (their K and V may be anything): masked by select
       const bool dead = row >= d.used, any_dead = d.used < kTile;
       for (int i = 0; i < d.steps; ++i, ++n) {
-        const int s = static_cast<int>(n % ST);
+        const int s = static_cast<int>(n % SO);
         const float4* lse4 = reinterpret_cast<const float4*>(s_lse + s * kTile + 64 * half);
         const float4* del4 = reinterpret_cast<const float4*>(s_delta + s * kTile + 64 * half);
-        ok = wait(st_full(s), (n / ST) & 1) && wait(s_full, n & 1);
+        ok = wait(st_full(s), (n / SO) & 1) && wait(s_full, n & 1);
         if (!ok) break;
         tc_fence_after();
         uint32_t x[64];
@@ -766,7 +796,7 @@ struct QWork {
   int more;
   int head, kv_head;
   int q_row, q_end;
-  int k_row, nkv, last_keys;  // nkv 0: no keys, dq = 0
+  int k_row, nkv, last_keys;  // nkv 0: no keys, dq = 0 (such items are not handed on)
 };
 
 __device__ __forceinline__ QWork decode_q(uint32_t item, const uint32_t* __restrict__ ws, const CrossSegments& seg) {
@@ -790,11 +820,12 @@ __device__ __forceinline__ QWork decode_q(uint32_t item, const uint32_t* __restr
 template <int D>
 struct QCfg {
   static constexpr int kStagesK = 3, kStagesV = 2;
-  // q_full, q_empty, do_full, do_empty, s_full[2], dp_full, dp_read, ds_full[2], acc_full, acc_empty,
-  // w_full[2], w_empty[2], drain, then k_full, k_empty, v_full, v_empty
-  static constexpr int kNumBars = 17 + 2 * kStagesK + 2 * kStagesV;
+  static constexpr int kWork = 4;  // items decoded ahead: the products look two tiles ahead
+  // q_full, q_empty, do_full, do_empty, s_full[2], dp_full, ds_full, acc_full, acc_empty, drain,
+  // w_full[kWork], w_empty[kWork], then k_full, k_empty, v_full, v_empty
+  static constexpr int kNumBars = 11 + 2 * kWork + 2 * kStagesK + 2 * kStagesV;
   static constexpr int kSmemBytes = 1024 + Tiles<D>::kBytes * (2 + kStagesK + kStagesV) + kNumBars * 8 + 16 +
-                                    2 * sizeof(QWork);
+                                    kWork * sizeof(QWork);
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
   static constexpr int kColS = 0, kColP = 256, kColQ = 384;
 };
@@ -818,21 +849,25 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8 * static_cast<uint32_t>(i); };
   const uint32_t q_full = bar(0), q_empty = bar(1), do_full = bar(2), do_empty = bar(3), dp_full = bar(6),
-                 dp_read = bar(7), acc_full = bar(10), acc_empty = bar(11), drain = bar(16);
+                 ds_full = bar(7), acc_full = bar(8), acc_empty = bar(9), drain = bar(10);
   auto s_full = [&](uint32_t i) { return bar(4 + static_cast<int>(i)); };
-  // two of them: dP of the next step is issued before dS of this one is waited for, so a warp may
-  // finish its next dS while another still works on this one
-  auto ds_full = [&](uint32_t i) { return bar(8 + static_cast<int>(i)); };
-  auto w_full = [&](int i) { return bar(12 + i); };
-  auto w_empty = [&](int i) { return bar(14 + i); };
-  auto k_full = [&](int s) { return bar(17 + s); };
-  auto k_empty = [&](int s) { return bar(17 + SK + s); };
-  auto v_full = [&](int s) { return bar(17 + 2 * SK + s); };
-  auto v_empty = [&](int s) { return bar(17 + 2 * SK + SV + s); };
+  auto w_full = [&](int k) { return bar(11 + k % C::kWork); };
+  auto w_empty = [&](int k) { return bar(11 + C::kWork + k % C::kWork); };
+  constexpr int kRing = 11 + 2 * C::kWork;
+  auto k_full = [&](int s) { return bar(kRing + s); };
+  auto k_empty = [&](int s) { return bar(kRing + SK + s); };
+  auto v_full = [&](int s) { return bar(kRing + 2 * SK + s); };
+  auto v_empty = [&](int s) { return bar(kRing + 2 * SK + SV + s); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t b, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(b, parity, a.wait_limit_ns)) != 0;
+  };
+  auto wait2 = [&](uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {  // the polls overlap
+    bool r0 = mbar_try_wait(b0, p0), r1 = mbar_try_wait(b1, p1);
+    if (!r0) r0 = mbar_wait(b0, p0, a.wait_limit_ns);
+    if (!r1) r1 = mbar_wait(b1, p1, a.wait_limit_ns);
+    return __all_sync(0xffffffffu, r0 && r1) != 0;
   };
   auto wait_long = [&](uint32_t b, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait_long(b, parity, a.wait_limit_ns)) != 0;
@@ -842,9 +877,9 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
     if (lane == 0) mbar_arrive(b);
   };
   auto take = [&](int k, QWork& d) {
-    if (!wait(w_full(k & 1), (k >> 1) & 1)) return false;
-    d = work[k & 1];
-    arrive_warp(w_empty(k & 1));
+    if (!wait(w_full(k), k / C::kWork & 1)) return false;
+    d = work[k % C::kWork];
+    arrive_warp(w_empty(k));
     return true;
   };
 
@@ -860,9 +895,9 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
     tma_prefetch_desc(&a.tmap_do);
     const uint32_t one[] = {q_full, q_empty, do_full, do_empty, s_full(0), s_full(1), dp_full, acc_full, drain};
     for (uint32_t b : one) mbar_init(b, 1);
-    const uint32_t warps8[] = {dp_read, ds_full(0), ds_full(1), acc_empty};
+    const uint32_t warps8[] = {ds_full, acc_empty};
     for (uint32_t b : warps8) mbar_init(b, 8);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kWork; ++i) {
       mbar_init(w_full(i), 1);
       mbar_init(w_empty(i), 11);  // compute warps, key/value loads, query loads, products
     }
@@ -920,7 +955,6 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
     for (int k = 0; ok; ++k) {
       ok = take(k, d);
       if (!ok || !d.more) break;
-      if (d.nkv == 0) continue;
       ok = wait_long(q_empty, (n & 1) ^ 1);
       if (!ok) break;
       if (lane == 0) load_tile<D>(sQ, &a.tmap_q, d.head, d.q_row, q_full);
@@ -935,17 +969,27 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
     if (nd > 0) mbar_wait(do_full, (nd - 1) & 1);
   } else if (warp == 11) {
     // ================= scheduler =================
+    uint32_t item = blockIdx.x;
     for (int k = 0;; ++k) {
-      const uint32_t item = blockIdx.x + static_cast<uint32_t>(k) * gridDim.x;
       QWork d{};
-      if (item < total) d = decode_q(item, a.plan, a.seg);
-      if (!wait_long(w_empty(k & 1), ((k >> 1) & 1) ^ 1)) {
+      for (; item < total; item += gridDim.x) {
+        d = decode_q(item, a.plan, a.seg);
+        if (d.nkv > 0) break;
+        // no keys: zero the tile's rows here
+        const int rows = min(kTile, d.q_end - d.q_row);
+        for (int i = lane; i < rows * (D / 8); i += 32)
+          *reinterpret_cast<uint4*>(a.dq + (static_cast<int64_t>(d.q_row) + i / (D / 8)) * a.dq_stride + d.head * D +
+                                    i % (D / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
+        d.more = 0;
+      }
+      item += gridDim.x;
+      if (!wait_long(w_empty(k), (k / C::kWork & 1) ^ 1)) {
         if (lane == 0) record_error(a.err, kErrTimeout);
         break;
       }
       if (lane == 0) {
-        work[k & 1] = d;
-        mbar_arrive(w_full(k & 1));
+        work[k % C::kWork] = d;
+        mbar_arrive(w_full(k));
       }
       __syncwarp();
       if (!d.more) break;
@@ -959,78 +1003,102 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
     const SmemDesc rk = sw128_desc_split(smem_u32(sK), T::kBoxBytes, 1024);
     struct Item {
       int more, nkv, last_keys;
-    } cur{}, nxt{};
+    };
     int at = 0;  // items taken
-    auto next_item = [&](Item& i) {  // the next one with keys
+    auto next_item = [&](Item& i) {
       QWork d;
-      do {
-        if (!take(at++, d)) return false;
-      } while (d.more && d.nkv == 0);
+      if (!take(at++, d)) return false;
       i = Item{d.more, d.nkv, d.last_keys};
       return true;
     };
     auto keys_of = [](const Item& i, int j) { return j == i.nkv - 1 ? i.last_keys : kTile; };
-    uint32_t sc = 0, pc = 0, n = 0, items = 0;  // S and dP tiles issued, dQ steps issued, items begun
-    uint32_t qn = 0;
-    bool ok = next_item(cur), issued = false;
-    auto scores = [&](const Item& i, int j) {  // S = Q K^T of the ring's next K tile
-      const int s = static_cast<int>(sc % SK), keys = keys_of(i, j);
-      bool good = true;
-      if (j == 0) good = wait(q_full, qn & 1);
-      if (good) good = wait(k_full(s), (sc / SK) & 1);
+    // Three cursors over the items' key tiles: S runs two tiles ahead of dQ, dP one.
+    struct Cursor {
+      Item item;
+      int j;
+      uint32_t n, items;  // tiles and items passed
+    } cs{}, cp{}, cq{};
+    Item queue[2];  // items between the S cursor and the others (at most two tiles: at most two items)
+    uint32_t queued = 0;
+    bool ok = next_item(cs.item), issued = false;
+    if (ok && cs.item.more) {
+      queue[0] = cs.item;
+      queued = 1;
+      cp.item = cq.item = cs.item;
+    }
+    auto scores = [&] {  // S = Q K^T
+      const int s = static_cast<int>(cs.n % SK), keys = keys_of(cs.item, cs.j);
+      bool good = cs.j == 0 ? wait2(q_full, cs.items & 1, k_full(s), (cs.n / SK) & 1)
+                            : wait(k_full(s), (cs.n / SK) & 1);
       if (!good) return false;
       if (keys % 16 != 0) zero_rows<D>(sK + s * T::kBytes, keys);
       tc_fence_after();
+      const bool last = cs.j == cs.item.nkv - 1;
       if (leader) {
-        product_ss<D>(tmem + C::kColS + 128 * (sc & 1), dq.lo, dq.hi, dk.lo + s * kTile16, dk.hi, steps16(keys));
-        mma_commit(s_full(sc & 1));
-        if (j == i.nkv - 1) mma_commit(q_empty);
+        product_ss<D>(tmem + C::kColS + 128 * (cs.n & 1), dq.lo, dq.hi, dk.lo + s * kTile16, dk.hi, steps16(keys));
+        mma_commit(s_full(cs.n & 1));
+        if (last) mma_commit(q_empty);
       }
       __syncwarp();
-      ++sc;
       issued = true;
+      ++cs.n;
+      ++cs.j;
+      if (last) {
+        cs.j = 0;
+        ++cs.items;
+        if (!next_item(cs.item)) return false;
+        queue[queued++ & 1] = cs.item;
+      }
       return true;
     };
-    auto grads = [&](const Item& i, int j) {  // dP = dO V^T, once the previous dP has been read
-      const int s = static_cast<int>(pc % SV);
-      bool good = true;
-      if (j == 0) good = wait(do_full, qn++ & 1);
-      if (good) good = wait(v_full(s), (pc / SV) & 1);
-      if (good && pc > 0) good = wait(dp_read, (pc - 1) & 1);
+    auto grads = [&] {  // dP = dO V^T
+      const int s = static_cast<int>(cp.n % SV);
+      bool good = cp.j == 0 ? wait2(do_full, cp.items & 1, v_full(s), (cp.n / SV) & 1)
+                            : wait(v_full(s), (cp.n / SV) & 1);
       if (!good) return false;
       tc_fence_after();
+      const bool last = cp.j == cp.item.nkv - 1;
       if (leader) {
-        product_ss<D>(tmem + C::kColP, dd.lo, dd.hi, dv.lo + s * kTile16, dv.hi, steps16(keys_of(i, j)));
+        product_ss<D>(tmem + C::kColP, dd.lo, dd.hi, dv.lo + s * kTile16, dv.hi, steps16(keys_of(cp.item, cp.j)));
         mma_commit(dp_full);
         mma_commit(v_empty(s));
-        if (j == i.nkv - 1) mma_commit(do_empty);
+        if (last) mma_commit(do_empty);
       }
       __syncwarp();
-      ++pc;
+      ++cp.n;
+      ++cp.j;
+      if (last) {
+        cp.j = 0;
+        cp.item = queue[++cp.items & 1];
+      }
       return true;
     };
-    if (ok && cur.more) ok = scores(cur, 0) && grads(cur, 0);
-    while (ok && cur.more) {
-      for (int j = 0; j < cur.nkv && ok; ++j, ++n) {
-        const bool last = j == cur.nkv - 1;
-        if (last) ok = next_item(nxt);
-        if (ok && !last) ok = scores(cur, j + 1) && grads(cur, j + 1);
-        if (ok && last && nxt.more) ok = scores(nxt, 0) && grads(nxt, 0);
-        if (ok) ok = wait(ds_full(n & 1), (n >> 1) & 1);
-        if (ok && j == 0) ok = wait(acc_empty, (items & 1) ^ 1);
-        if (!ok) break;
-        tc_fence_after();
-        const int s = static_cast<int>(n % SK);
-        if (leader) {  // dQ += dS K
-          product_ts<D>(tmem + C::kColQ, tmem + C::kColS + 128 * (n & 1), rk.lo + s * kTile16, rk.hi,
-                        steps16(keys_of(cur, j)), j == 0);
-          mma_commit(k_empty(s));
-          if (last) mma_commit(acc_full);
-        }
-        __syncwarp();
+    if (ok && cs.item.more) ok = scores();
+    if (ok && cp.item.more) ok = grads();
+    if (ok && cs.item.more) ok = scores();
+    while (ok && cq.item.more) {
+      const bool last = cq.j == cq.item.nkv - 1;
+      ok = wait(ds_full, cq.n & 1);
+      if (ok && cq.j == 0) ok = wait(acc_empty, (cq.items & 1) ^ 1);
+      if (!ok) break;
+      tc_fence_after();
+      const int s = static_cast<int>(cq.n % SK);
+      if (leader) {  // dQ += dS K
+        product_ts<D>(tmem + C::kColQ, tmem + C::kColP, rk.lo + s * kTile16, rk.hi,
+                      steps16(keys_of(cq.item, cq.j)), cq.j == 0);
+        mma_commit(k_empty(s));
+        if (last) mma_commit(acc_full);
       }
-      ++items;
-      cur = nxt;
+      __syncwarp();
+      ++cq.n;
+      ++cq.j;
+      if (last) {
+        cq.j = 0;
+        cq.item = queue[++cq.items & 1];
+      }
+      // (an item taken but not begun ends the run once it says that there is no more)
+      if (cp.item.more) ok = grads();
+      if (ok && cs.item.more) ok = scores();
     }
     if (!ok && leader) record_error(a.err, kErrTimeout);
     if (issued && leader) {
@@ -1052,7 +1120,7 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
       if (!ok || !d.more) break;
       const int q_row = d.q_row + row;
       float lse2 = 0.f, delta = 0.f;
-      if (q_row < d.q_end && d.nkv > 0) {
+      if (q_row < d.q_end) {
         const size_t i = static_cast<size_t>(d.head) * a.seg.capacity_q + q_row;
         lse2 = a.lse[i] * 1.4426950408889634f;
         delta = a.delta[i];
@@ -1077,8 +1145,6 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
         tmem_ld32(p_addr + 32, x + 32);
         tmem_ld_wait();
         tmem_reg_fence<64>(x);
-        tc_fence_before();
-        arrive_warp(dp_read);
 #pragma unroll
         for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(x[c]) - delta;
         if (j == d.nkv - 1 && d.last_keys < kTile) {  // keys past the end
@@ -1088,38 +1154,28 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-        tmem_st32(s_addr, w);
+        tmem_st32(p_addr, w);
         tmem_st_wait();
         tc_fence_before();
-        arrive_warp(ds_full(n & 1));
+        arrive_warp(ds_full);
       }
+      if (ok) ok = wait(acc_full, items & 1);
       if (!ok) break;
-      if (d.nkv > 0) {
-        ok = wait(acc_full, items & 1);
-        if (!ok) break;
-        tc_fence_after();
-      }
+      tc_fence_after();
       // epilogue: each warpgroup stores half the columns
       const int odd = lane & 1, r0 = d.q_row + row - odd;
       __nv_bfloat16* p0 = a.dq + static_cast<int64_t>(r0) * a.dq_stride + d.head * D + 16 * odd;
 #pragma unroll 1
       for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
         uint32_t x[32];
-        if (d.nkv > 0) {
-          tmem_ld32(tmem + lane_base + C::kColQ + c0, x);
-          tmem_ld_wait();
-          tmem_reg_fence<32>(x);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = 0u;
-        }
+        tmem_ld32(tmem + lane_base + C::kColQ + c0, x);
+        tmem_ld_wait();
+        tmem_reg_fence<32>(x);
         store_columns(x, a.scale, p0 + c0, p0 + a.dq_stride + c0, r0 < d.q_end, r0 + 1 < d.q_end, a.wide);
       }
-      if (d.nkv > 0) {
-        tc_fence_before();
-        arrive_warp(acc_empty);
-        ++items;
-      }
+      tc_fence_before();
+      arrive_warp(acc_empty);
+      ++items;
     }
     if (!ok && lane == 0) record_error(a.err, kErrTimeout);
   }
