@@ -14,10 +14,14 @@
 // dK/dV works on transposed scores: S^T = K Q^T and dP^T = V dO^T have keys as TMEM lanes, so P^T and
 // dS^T are written back to TMEM as the A operands of dV += P^T dO and dK += dS^T Q, and one copy of Q
 // and dO in shared memory serves both products that read it.  Each thread owns a key row and half the
-// 128 query columns.  Tensor order: dV_i, S_{i+1} while dS_i is computed, dK_i, dP_{i+1} while P_{i+1}
-// is.  TMEM (512 columns): S^T/P^T, dP^T/dS^T, dK, dV.
-// dQ: S = Q K^T (two buffers), dP = dO V^T, dQ += dS K with dS written over dP.  Tensor order: dQ_j,
-// dP_{j+1}, S_{j+2}; it runs from one item into the next, since key lists may be a few tiles.
+// 128 query columns.  dV_i and S_{i+1} run while dS_i is computed, dK_i and dP_{i+1} while P_{i+1} is.
+// TMEM (512 columns): S^T/P^T, dP^T/dS^T, dK, dV.
+// dQ: S = Q K^T (two buffers), dP = dO V^T, dQ += dS K with dS written over S.  It runs from one item
+// into the next, since key lists may be a few tiles.
+// In dQ the products come from two warps (S and dP from one, dQ from the other): a warp's polls queue
+// behind its own products, so one warp alone leaves the tensor core idle at each wait (4,096 x 4,096 x
+// 24 x 128: 236 us, 290 with one).  In dK/dV the four products of a step alternate between two chains
+// and one warp keeps them in that order; two warps measured slower there (350 us against 295).
 //
 // P and dS are rounded to bf16 for the tensor core (half a step, 2^-8 relative at most); everything
 // else is fp32 until the gradients are rounded once.  Rows and keys past a segment's end are zeroed
@@ -820,10 +824,10 @@ __device__ __forceinline__ QWork decode_q(uint32_t item, const uint32_t* __restr
 template <int D>
 struct QCfg {
   static constexpr int kStagesK = 3, kStagesV = 2;
-  static constexpr int kWork = 4;  // items decoded ahead: the products look two tiles ahead
-  // q_full, q_empty, do_full, do_empty, s_full[2], dp_full, ds_full, acc_full, acc_empty, drain,
-  // w_full[kWork], w_empty[kWork], then k_full, k_empty, v_full, v_empty
-  static constexpr int kNumBars = 11 + 2 * kWork + 2 * kStagesK + 2 * kStagesV;
+  static constexpr int kWork = 4;  // items decoded ahead
+  // q_full, q_empty, do_full, do_empty, s_full[2], s_empty[2], ds_full[2], dp_full, dp_read, acc_full,
+  // acc_empty, drain[2], w_full[kWork], w_empty[kWork], then k_full, k_empty, v_full, v_empty
+  static constexpr int kNumBars = 16 + 2 * kWork + 2 * kStagesK + 2 * kStagesV;
   static constexpr int kSmemBytes = 1024 + Tiles<D>::kBytes * (2 + kStagesK + kStagesV) + kNumBars * 8 + 16 +
                                     kWork * sizeof(QWork);
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -848,12 +852,16 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
   QWork* work = reinterpret_cast<QWork*>(tmem_slot + 4);
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8 * static_cast<uint32_t>(i); };
-  const uint32_t q_full = bar(0), q_empty = bar(1), do_full = bar(2), do_empty = bar(3), dp_full = bar(6),
-                 ds_full = bar(7), acc_full = bar(8), acc_empty = bar(9), drain = bar(10);
+  const uint32_t q_full = bar(0), q_empty = bar(1), do_full = bar(2), do_empty = bar(3), dp_full = bar(10),
+                 dp_read = bar(11), acc_full = bar(12), acc_empty = bar(13);
   auto s_full = [&](uint32_t i) { return bar(4 + static_cast<int>(i)); };
-  auto w_full = [&](int k) { return bar(11 + k % C::kWork); };
-  auto w_empty = [&](int k) { return bar(11 + C::kWork + k % C::kWork); };
-  constexpr int kRing = 11 + 2 * C::kWork;
+  auto s_empty = [&](uint32_t i) { return bar(6 + static_cast<int>(i)); };
+  // two of them: a warp may finish its next dS while another still works on this one
+  auto ds_full = [&](uint32_t i) { return bar(8 + static_cast<int>(i)); };
+  auto drain = [&](int i) { return bar(14 + i); };
+  auto w_full = [&](int k) { return bar(16 + k % C::kWork); };
+  auto w_empty = [&](int k) { return bar(16 + C::kWork + k % C::kWork); };
+  constexpr int kRing = 16 + 2 * C::kWork;
   auto k_full = [&](int s) { return bar(kRing + s); };
   auto k_empty = [&](int s) { return bar(kRing + SK + s); };
   auto v_full = [&](int s) { return bar(kRing + 2 * SK + s); };
@@ -893,13 +901,14 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
     tma_prefetch_desc(&a.tmap_k);
     tma_prefetch_desc(&a.tmap_v);
     tma_prefetch_desc(&a.tmap_do);
-    const uint32_t one[] = {q_full, q_empty, do_full, do_empty, s_full(0), s_full(1), dp_full, acc_full, drain};
+    const uint32_t one[] = {q_full, q_empty, do_full, do_empty, s_full(0), s_full(1), s_empty(0), s_empty(1),
+                            dp_full, acc_full, drain(0), drain(1)};
     for (uint32_t b : one) mbar_init(b, 1);
-    const uint32_t warps8[] = {ds_full, acc_empty};
+    const uint32_t warps8[] = {ds_full(0), ds_full(1), dp_read, acc_empty};
     for (uint32_t b : warps8) mbar_init(b, 8);
     for (int i = 0; i < C::kWork; ++i) {
       mbar_init(w_full(i), 1);
-      mbar_init(w_empty(i), 11);  // compute warps, key/value loads, query loads, products
+      mbar_init(w_empty(i), 11);  // compute warps, key/value loads, two product warps
     }
     for (int s = 0; s < SK; ++s) {
       mbar_init(k_full(s), 1);
@@ -948,29 +957,10 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
     for (uint32_t i = 0; i < SK && i < kt; ++i) mbar_wait(k_full((kt - 1 - i) % SK), ((kt - 1 - i) / SK) & 1);
     for (uint32_t i = 0; i < SV && i < vt; ++i) mbar_wait(v_full((vt - 1 - i) % SV), ((vt - 1 - i) / SV) & 1);
   } else if (warp == 10) {
-    // ================= query and output-gradient loads =================
+    // ================= scheduler, query and output-gradient loads =================
     bool ok = true;
-    uint32_t n = 0, nd = 0;
-    QWork d;
+    uint32_t item = blockIdx.x, n = 0;
     for (int k = 0; ok; ++k) {
-      ok = take(k, d);
-      if (!ok || !d.more) break;
-      ok = wait_long(q_empty, (n & 1) ^ 1);
-      if (!ok) break;
-      if (lane == 0) load_tile<D>(sQ, &a.tmap_q, d.head, d.q_row, q_full);
-      ++n;
-      ok = wait_long(do_empty, (nd & 1) ^ 1);
-      if (!ok) break;
-      if (lane == 0) load_tile<D>(sO, &a.tmap_do, d.head, d.q_row, do_full);
-      ++nd;
-    }
-    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
-    if (n > 0) mbar_wait(q_full, (n - 1) & 1);
-    if (nd > 0) mbar_wait(do_full, (nd - 1) & 1);
-  } else if (warp == 11) {
-    // ================= scheduler =================
-    uint32_t item = blockIdx.x;
-    for (int k = 0;; ++k) {
       QWork d{};
       for (; item < total; item += gridDim.x) {
         d = decode_q(item, a.plan, a.seg);
@@ -983,127 +973,109 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
         d.more = 0;
       }
       item += gridDim.x;
-      if (!wait_long(w_empty(k), (k / C::kWork & 1) ^ 1)) {
-        if (lane == 0) record_error(a.err, kErrTimeout);
-        break;
-      }
+      ok = wait_long(w_empty(k), (k / C::kWork & 1) ^ 1);
+      if (!ok) break;
       if (lane == 0) {
         work[k % C::kWork] = d;
         mbar_arrive(w_full(k));
       }
       __syncwarp();
       if (!d.more) break;
+      ok = wait_long(q_empty, (n & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) load_tile<D>(sQ, &a.tmap_q, d.head, d.q_row, q_full);
+      ok = wait_long(do_empty, (n & 1) ^ 1);
+      if (!ok) {
+        if (lane == 0) mbar_wait(q_full, n & 1);
+        break;
+      }
+      if (lane == 0) load_tile<D>(sO, &a.tmap_do, d.head, d.q_row, do_full);
+      ++n;
     }
+    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+    if (n > 0) mbar_wait(q_full, (n - 1) & 1);
+    if (n > 0) mbar_wait(do_full, (n - 1) & 1);
   } else if (warp == 9) {
-    // ================= products =================
+    // ================= S and dP =================
     const bool leader = elect_one();
     constexpr uint32_t kTile16 = T::kBytes >> 4;
     const SmemDesc dq = sw128_desc_split(smem_u32(sQ), 16, 1024), dd = sw128_desc_split(smem_u32(sO), 16, 1024);
     const SmemDesc dk = sw128_desc_split(smem_u32(sK), 16, 1024), dv = sw128_desc_split(smem_u32(sV), 16, 1024);
-    const SmemDesc rk = sw128_desc_split(smem_u32(sK), T::kBoxBytes, 1024);
-    struct Item {
-      int more, nkv, last_keys;
-    };
-    int at = 0;  // items taken
-    auto next_item = [&](Item& i) {
-      QWork d;
-      if (!take(at++, d)) return false;
-      i = Item{d.more, d.nkv, d.last_keys};
-      return true;
-    };
-    auto keys_of = [](const Item& i, int j) { return j == i.nkv - 1 ? i.last_keys : kTile; };
-    // Three cursors over the items' key tiles: S runs two tiles ahead of dQ, dP one.
-    struct Cursor {
-      Item item;
-      int j;
-      uint32_t n, items;  // tiles and items passed
-    } cs{}, cp{}, cq{};
-    Item queue[2];  // items between the S cursor and the others (at most two tiles: at most two items)
-    uint32_t queued = 0;
-    bool ok = next_item(cs.item), issued = false;
-    if (ok && cs.item.more) {
-      queue[0] = cs.item;
-      queued = 1;
-      cp.item = cq.item = cs.item;
-    }
-    auto scores = [&] {  // S = Q K^T
-      const int s = static_cast<int>(cs.n % SK), keys = keys_of(cs.item, cs.j);
-      bool good = cs.j == 0 ? wait2(q_full, cs.items & 1, k_full(s), (cs.n / SK) & 1)
-                            : wait(k_full(s), (cs.n / SK) & 1);
-      if (!good) return false;
-      if (keys % 16 != 0) zero_rows<D>(sK + s * T::kBytes, keys);
-      tc_fence_after();
-      const bool last = cs.j == cs.item.nkv - 1;
-      if (leader) {
-        product_ss<D>(tmem + C::kColS + 128 * (cs.n & 1), dq.lo, dq.hi, dk.lo + s * kTile16, dk.hi, steps16(keys));
-        mma_commit(s_full(cs.n & 1));
-        if (last) mma_commit(q_empty);
+    bool ok = true, issued = false;
+    uint32_t n = 0, items = 0;
+    QWork d;
+    for (int k = 0; ok; ++k, ++items) {
+      ok = take(k, d);
+      if (!ok || !d.more) break;
+      for (int j = 0; j < d.nkv; ++j, ++n) {
+        const int s = static_cast<int>(n % SK), v = static_cast<int>(n % SV);
+        const bool last = j == d.nkv - 1;
+        const int keys = last ? d.last_keys : kTile;
+        ok = wait2(s_empty(n & 1), ((n >> 1) & 1) ^ 1, k_full(s), (n / SK) & 1);
+        if (ok && j == 0) ok = wait(q_full, items & 1);
+        if (!ok) break;
+        if (keys % 16 != 0) zero_rows<D>(sK + s * T::kBytes, keys);
+        tc_fence_after();
+        if (leader) {  // S = Q K^T
+          product_ss<D>(tmem + C::kColS + 128 * (n & 1), dq.lo, dq.hi, dk.lo + s * kTile16, dk.hi, steps16(keys));
+          mma_commit(s_full(n & 1));
+          if (last) mma_commit(q_empty);
+        }
+        __syncwarp();
+        issued = true;
+        ok = wait(v_full(v), (n / SV) & 1);
+        if (ok && j == 0) ok = wait(do_full, items & 1);
+        if (ok && n > 0) ok = wait(dp_read, (n - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {  // dP = dO V^T
+          product_ss<D>(tmem + C::kColP, dd.lo, dd.hi, dv.lo + v * kTile16, dv.hi, steps16(keys));
+          mma_commit(dp_full);
+          mma_commit(v_empty(v));
+          if (last) mma_commit(do_empty);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      issued = true;
-      ++cs.n;
-      ++cs.j;
-      if (last) {
-        cs.j = 0;
-        ++cs.items;
-        if (!next_item(cs.item)) return false;
-        queue[queued++ & 1] = cs.item;
-      }
-      return true;
-    };
-    auto grads = [&] {  // dP = dO V^T
-      const int s = static_cast<int>(cp.n % SV);
-      bool good = cp.j == 0 ? wait2(do_full, cp.items & 1, v_full(s), (cp.n / SV) & 1)
-                            : wait(v_full(s), (cp.n / SV) & 1);
-      if (!good) return false;
-      tc_fence_after();
-      const bool last = cp.j == cp.item.nkv - 1;
-      if (leader) {
-        product_ss<D>(tmem + C::kColP, dd.lo, dd.hi, dv.lo + s * kTile16, dv.hi, steps16(keys_of(cp.item, cp.j)));
-        mma_commit(dp_full);
-        mma_commit(v_empty(s));
-        if (last) mma_commit(do_empty);
-      }
-      __syncwarp();
-      ++cp.n;
-      ++cp.j;
-      if (last) {
-        cp.j = 0;
-        cp.item = queue[++cp.items & 1];
-      }
-      return true;
-    };
-    if (ok && cs.item.more) ok = scores();
-    if (ok && cp.item.more) ok = grads();
-    if (ok && cs.item.more) ok = scores();
-    while (ok && cq.item.more) {
-      const bool last = cq.j == cq.item.nkv - 1;
-      ok = wait(ds_full, cq.n & 1);
-      if (ok && cq.j == 0) ok = wait(acc_empty, (cq.items & 1) ^ 1);
-      if (!ok) break;
-      tc_fence_after();
-      const int s = static_cast<int>(cq.n % SK);
-      if (leader) {  // dQ += dS K
-        product_ts<D>(tmem + C::kColQ, tmem + C::kColP, rk.lo + s * kTile16, rk.hi,
-                      steps16(keys_of(cq.item, cq.j)), cq.j == 0);
-        mma_commit(k_empty(s));
-        if (last) mma_commit(acc_full);
-      }
-      __syncwarp();
-      ++cq.n;
-      ++cq.j;
-      if (last) {
-        cq.j = 0;
-        cq.item = queue[++cq.items & 1];
-      }
-      // (an item taken but not begun ends the run once it says that there is no more)
-      if (cp.item.more) ok = grads();
-      if (ok && cs.item.more) ok = scores();
     }
     if (!ok && leader) record_error(a.err, kErrTimeout);
     if (issued && leader) {
-      mma_commit(drain);
-      mbar_wait(drain, 0);
+      mma_commit(drain(0));
+      mbar_wait(drain(0), 0);
+    }
+    __syncwarp();
+  } else if (warp == 11) {
+    // ================= dQ += dS K =================
+    const bool leader = elect_one();
+    constexpr uint32_t kTile16 = T::kBytes >> 4;
+    const SmemDesc rk = sw128_desc_split(smem_u32(sK), T::kBoxBytes, 1024);
+    bool ok = true, issued = false;
+    uint32_t n = 0, items = 0;
+    QWork d;
+    for (int k = 0; ok; ++k, ++items) {
+      ok = take(k, d);
+      if (!ok || !d.more) break;
+      for (int j = 0; j < d.nkv; ++j, ++n) {
+        const int s = static_cast<int>(n % SK);
+        const bool last = j == d.nkv - 1;
+        ok = wait(ds_full(n & 1), (n >> 1) & 1);
+        if (ok && j == 0) ok = wait(acc_empty, (items & 1) ^ 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          product_ts<D>(tmem + C::kColQ, tmem + C::kColS + 128 * (n & 1), rk.lo + s * kTile16, rk.hi,
+                        steps16(last ? d.last_keys : kTile), j == 0);
+          mma_commit(k_empty(s));
+          mma_commit(s_empty(n & 1));
+          if (last) mma_commit(acc_full);
+        }
+        __syncwarp();
+        issued = true;
+      }
+    }
+    if (!ok && leader) record_error(a.err, kErrTimeout);
+    if (issued && leader) {
+      mma_commit(drain(1));
+      mbar_wait(drain(1), 0);
     }
     __syncwarp();
   } else {
@@ -1145,6 +1117,8 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
         tmem_ld32(p_addr + 32, x + 32);
         tmem_ld_wait();
         tmem_reg_fence<64>(x);
+        tc_fence_before();
+        arrive_warp(dp_read);
 #pragma unroll
         for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(x[c]) - delta;
         if (j == d.nkv - 1 && d.last_keys < kTile) {  // keys past the end
@@ -1154,10 +1128,10 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-        tmem_st32(p_addr, w);
+        tmem_st32(s_addr, w);
         tmem_st_wait();
         tc_fence_before();
-        arrive_warp(ds_full);
+        arrive_warp(ds_full(n & 1));
       }
       if (ok) ok = wait(acc_full, items & 1);
       if (!ok) break;
