@@ -28,9 +28,9 @@ Calls:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -86,6 +86,7 @@ class _QkNormDesc(ctypes.Structure):
     _fields_ = [("num_tokens", _I), ("num_q_heads", _I), ("num_k_heads", _I), ("head_dim", _I),
                 ("weight_type", _I), ("eps", ctypes.c_float), ("q_stride", _L), ("k_stride", _L),
                 ("q_out_stride", _L), ("k_out_stride", _L), ("dq_stride", _L), ("dk_stride", _L)]
+    pack = struct.Struct("@5if6q").pack  # the same bytes, several times faster than the class
 
 
 class _CrossAttnDesc(ctypes.Structure):
@@ -94,6 +95,7 @@ class _CrossAttnDesc(ctypes.Structure):
                 ("capacity_k", _I), ("num_q_heads", _I), ("num_kv_heads", _I), ("head_dim", _I),
                 ("softmax_scale", ctypes.c_float), ("q_stride", _L), ("k_stride", _L), ("v_stride", _L),
                 ("dq_stride", _L), ("dk_stride", _L), ("dv_stride", _L)]
+    pack = struct.Struct("@8if4x6q").pack
 
 
 class ContinuationConfig(ctypes.Structure):
@@ -129,18 +131,18 @@ def load_library():
     sigs = {
         "h3_rope_apply": (I32, [P, P, P, P, I32, I32, I32, P, P, P, I32, P,
                                 ctypes.POINTER(RopeConfig), P]),
-        "h3_qk_norm_rope": (I32, [ctypes.POINTER(_QkNormDesc), P, P, P, P, P, P, P, P, P, I32, P,
+        "h3_qk_norm_rope": (I32, [P, P, P, P, P, P, P, P, P, P, I32, P,
                                   ctypes.POINTER(RopeConfig), P]),
         "h3_qk_norm_rope_bwd_workspace_size": (U64, [I32]),
-        "h3_qk_norm_rope_bwd": (I32, [ctypes.POINTER(_QkNormDesc), P, P, P, P, P, P, P, P, P, I32, P,
+        "h3_qk_norm_rope_bwd": (I32, [P, P, P, P, P, P, P, P, P, P, I32, P,
                                       ctypes.POINTER(RopeConfig), P, P, P, P, P, U64, P]),
         "h3_varlen_attn_workspace_size": (U64, [I32, I32, I32, I32]),
         "h3_varlen_attn_fwd": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P, U64, P]),
         "h3_varlen_attn_fwd_noalloc": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P]),
-        "h3_varlen_cross_attn_workspace_size": (U64, [ctypes.POINTER(_CrossAttnDesc)]),
-        "h3_varlen_cross_attn_fwd": (I32, [ctypes.POINTER(_CrossAttnDesc), P, P, P, P, P, P, P, P, P, U64, P]),
-        "h3_varlen_cross_attn_bwd_workspace_size": (U64, [ctypes.POINTER(_CrossAttnDesc)]),
-        "h3_varlen_cross_attn_bwd": (I32, [ctypes.POINTER(_CrossAttnDesc), P, P, P, P, P, P, P, P, P, P, P, P, P,
+        "h3_varlen_cross_attn_workspace_size": (U64, [P]),
+        "h3_varlen_cross_attn_fwd": (I32, [P, P, P, P, P, P, P, P, P, P, U64, P]),
+        "h3_varlen_cross_attn_bwd_workspace_size": (U64, [P]),
+        "h3_varlen_cross_attn_bwd": (I32, [P, P, P, P, P, P, P, P, P, P, P, P, P, P,
                                            U64, P]),
         "h3_window_attn_fwd": (I32, [P, P, P, P, P, I32P, I32P, I32P, I32, I32, F32, P]),
         "h3_window_count": (I32, [I32P, I32P, I32P]),
@@ -188,12 +190,16 @@ def _stream(device: torch.device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-_SAME_DEVICE = contextlib.nullcontext()
-
-
-def _on(device: torch.device):
-    """Make `device` current for a call (nothing to do, and nothing spent, when it already is)."""
-    return _SAME_DEVICE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _launch(fn, where: str, device: torch.device, *args):
+    """Call a launching entry point on `device`'s current stream; raise on a failed status."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        raise H3Error(st, where)
 
 
 def _require(t: torch.Tensor, name: str, dtype, device: torch.device):
@@ -262,6 +268,15 @@ def rope_apply(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, ta
     return q_out, k_out
 
 
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _aux(t: torch.Tensor, name: str, dtype, device: torch.device):
+    """_require, its common case first."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        _require(t, name, dtype, device)
+
+
 def _rows(t: torch.Tensor, name: str, device: torch.device, shape=None) -> int:
     """Check bf16 [C, H, D] rows with heads and dims contiguous (a part of a fused projection is
     fine); returns the token stride in elements, 0 for contiguous rows."""
@@ -269,58 +284,68 @@ def _rows(t: torch.Tensor, name: str, device: torch.device, shape=None) -> int:
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3:
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+    C, H, D = shape3 = t.shape if t.dim() == 3 else (None, None, None)
+    if C is None:
         raise ValueError(f"{name} must be [C, H, D]")
-    if shape is not None and t.shape != shape:
+    if shape is not None and shape3 != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.is_contiguous():
         return 0
-    C, H, D = t.shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D) or (C > 1 and t.stride(0) < H * D):
+    sc, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != D) or (C > 1 and sc < H * D):
         raise ValueError(f"{name} must have contiguous heads and dims within a token")
-    return t.stride(0) if C > 1 else 0
+    return sc if C > 1 else 0
 
 
-def _norm_inputs(q, k, q_weight, k_weight, pos, tag, cu_requests, start_frames, num_tokens, eps):
-    """Checks shared by qk_norm_rope and its backward; returns (descriptor, num_requests)."""
+def _norm_inputs(q, k, q_weight, k_weight, pos, tag, cu_requests, start_frames, num_tokens):
+    """Checks shared by qk_norm_rope and its backward; returns (num_requests, pointers of the rotation's
+    inputs, sizes of the descriptor, q and k strides)."""
     dev = q.device
     q_stride, k_stride, hk = _rows(q, "q", dev), 0, 0
     C, H, D = q.shape
     n = C if num_tokens is None else int(num_tokens)
     if not 0 <= n <= C:
         raise ValueError("num_tokens must lie within the capacity of q")
+    kind = q_weight.dtype if isinstance(q_weight, torch.Tensor) else None
+    if kind is not _F32 and kind is not _BF16:
+        raise TypeError("q_weight must be a float32 or bfloat16 tensor")
+    _aux(q_weight, "q_weight", kind, dev)
+    if q_weight.shape != (D,):
+        raise ValueError("q_weight must be [head_dim]")
     if k is not None:
-        k_stride, hk = _rows(k, "k", dev), k.shape[1]
-        if k.shape[0] != C or k.shape[2] != D:
+        k_stride = _rows(k, "k", dev)
+        Ck, hk, Dk = k.shape
+        if Ck != C or Dk != D:
             raise ValueError("k must have q's tokens and head_dim")
-    for name, w in (("q_weight", q_weight),) + ((("k_weight", k_weight),) if k is not None else ()):
-        if not isinstance(w, torch.Tensor) or w.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
-        _require(w, name, q_weight.dtype, dev)
-        if tuple(w.shape) != (D,):
-            raise ValueError(f"{name} must be [head_dim]")
+        _aux(k_weight, "k_weight", kind, dev)
+        if k_weight.shape != (D,):
+            raise ValueError("k_weight must be [head_dim]")
     nreq = 0
     if (pos is None) != (tag is None):
         raise ValueError("pos and tag are given together")
     if pos is None:
         if cu_requests is not None or start_frames is not None:
             raise ValueError("cu_requests and start_frames need pos and tag")
+        where = (None, None, None, 0, None)
     else:
-        _require(pos, "pos", torch.float32, dev)
-        _require(tag, "tag", torch.uint8, dev)
+        _aux(pos, "pos", _F32, dev)
+        _aux(tag, "tag", _U8, dev)
         if pos.dim() != 2 or pos.shape[1] != 3 or pos.shape[0] < n or tag.numel() < n:
             raise ValueError("pos must be [>= num_tokens, 3] and tag [>= num_tokens]")
+        cu_ptr = frames_ptr = None
         if cu_requests is not None:
-            _require(cu_requests, "cu_requests", torch.int32, dev)
+            _aux(cu_requests, "cu_requests", _I32, dev)
             nreq = cu_requests.numel() - 1
+            cu_ptr = cu_requests.data_ptr()
         if start_frames is not None:
-            _require(start_frames, "start_frames", torch.float32, dev)
+            _aux(start_frames, "start_frames", _F32, dev)
             if start_frames.numel() < max(nreq, 1):
                 raise ValueError("start_frames must have one entry per request")
-    desc = _QkNormDesc(n, H, hk, D, int(q_weight.dtype == torch.bfloat16), float(eps), q_stride, k_stride)
-    return desc, nreq
+            frames_ptr = start_frames.data_ptr()
+        where = (pos.data_ptr(), tag.data_ptr(), cu_ptr, nreq, frames_ptr)
+    return where, (n, H, hk, D, 1 if kind is _BF16 else 0), q_stride, k_stride
 
 
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: torch.Tensor,
@@ -337,26 +362,26 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: torch.Ten
     given (q and k themselves are allowed); rows past num_tokens are left as they were.  Returns
     (q_out, k_out).
     """
-    desc, nreq = _norm_inputs(q, k, q_weight, k_weight, pos, tag, cu_requests, start_frames, num_tokens, eps)
+    where, sizes, q_stride, k_stride = _norm_inputs(q, k, q_weight, k_weight, pos, tag, cu_requests, start_frames,
+                                                    num_tokens)
     dev = q.device
+    q_out_stride = k_out_stride = 0
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    desc.q_out_stride = _rows(q_out, "q_out", dev, q.shape)
+        q_out = torch.empty(q.shape, dtype=_BF16, device=dev)
+    else:
+        q_out_stride = _rows(q_out, "q_out", dev, q.shape)
     if k is None:
         k_out = None
+    elif k_out is None:
+        k_out = torch.empty(k.shape, dtype=_BF16, device=dev)
     else:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        desc.k_out_stride = _rows(k_out, "k_out", dev, k.shape)
-    if desc.num_tokens == 0:
+        k_out_stride = _rows(k_out, "k_out", dev, k.shape)
+    if sizes[0] == 0:
         return q_out, k_out
-    lib = load_library()
-    with _on(dev):
-        st = lib.h3_qk_norm_rope(ctypes.byref(desc), _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out),
-                                 _ptr(q_weight), _ptr(k_weight) if k is not None else None, _ptr(pos),
-                                 _ptr(tag), _ptr(cu_requests), nreq, _ptr(start_frames),
-                                 ctypes.byref(cfg) if cfg is not None else None, _stream(dev))
-    _check(st, "h3_qk_norm_rope")
+    desc = _QkNormDesc.pack(*sizes, eps, q_stride, k_stride, q_out_stride, k_out_stride, 0, 0)
+    _launch(load_library().h3_qk_norm_rope, "h3_qk_norm_rope", dev, desc, q.data_ptr(), q_out.data_ptr(), _ptr(k),
+            _ptr(k_out), q_weight.data_ptr(), k_weight.data_ptr() if k is not None else None, *where,
+            ctypes.byref(cfg) if cfg is not None else None)
     return q_out, k_out
 
 
@@ -377,39 +402,38 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: to
     gradient, or dq_out and dk_out, or q and k; the weights' gradients sum over tokens and heads in
     a fixed order.
     """
-    desc, nreq = _norm_inputs(q, k, q_weight, k_weight, pos, tag, cu_requests, start_frames, num_tokens, eps)
-    dev, D = q.device, q.shape[2]
-    lib = load_library()
-    if desc.num_tokens == 0 and q.numel() == 0:  # no rows at all: no buffer to point at
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if dk is None and k is not None else dk
-        dw = torch.zeros((2, D), dtype=torch.float32, device=dev)
-        return dq, dk, dw[0], dw[1] if k is not None else None
-    desc.q_out_stride = _rows(dq_out, "dq_out", dev, q.shape)
+    where, sizes, q_stride, k_stride = _norm_inputs(q, k, q_weight, k_weight, pos, tag, cu_requests, start_frames,
+                                                    num_tokens)
+    dev, D, has_k = q.device, q.shape[2], k is not None
+    dq_out_stride, dk_out_stride = _rows(dq_out, "dq_out", dev, q.shape), 0
+    dq_stride = dk_stride = 0
     if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    desc.dq_stride = _rows(dq, "dq", dev, q.shape)
-    if k is None:
-        dk = dk_out = None
+        dq = torch.empty(q.shape, dtype=_BF16, device=dev)
     else:
-        desc.k_out_stride = _rows(dk_out, "dk_out", dev, k.shape)
+        dq_stride = _rows(dq, "dq", dev, q.shape)
+    dqw, dkw = torch.empty(D, dtype=_F32, device=dev), None
+    if has_k:
+        dk_out_stride = _rows(dk_out, "dk_out", dev, k.shape)
         if dk is None:
-            dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        desc.dk_stride = _rows(dk, "dk", dev, k.shape)
-    dqw, dkw = torch.empty((2, D), dtype=torch.float32, device=dev)
+            dk = torch.empty(k.shape, dtype=_BF16, device=dev)
+        else:
+            dk_stride = _rows(dk, "dk", dev, k.shape)
+        dkw = torch.empty(D, dtype=_F32, device=dev)
+    else:
+        dk = dk_out = None
+    if sizes[0] == 0 and q.numel() == 0:  # no rows at all: no buffer to point at
+        return dq, dk, dqw.zero_(), dkw.zero_() if has_k else None
+    lib = load_library()
     if workspace is None:
-        workspace = torch.empty(max(1, int(lib.h3_qk_norm_rope_bwd_workspace_size(D))), dtype=torch.uint8,
-                                device=dev)
-    _require(workspace, "workspace", torch.uint8, dev)
-    with _on(dev):
-        st = lib.h3_qk_norm_rope_bwd(ctypes.byref(desc), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k),
-                                     _ptr(q_weight), _ptr(k_weight) if k is not None else None, _ptr(pos),
-                                     _ptr(tag), _ptr(cu_requests), nreq, _ptr(start_frames),
-                                     ctypes.byref(cfg) if cfg is not None else None, _ptr(dq), _ptr(dk),
-                                     _ptr(dqw), _ptr(dkw) if k is not None else None,
-                                     _ptr(workspace), workspace.numel(), _stream(dev))
-    _check(st, "h3_qk_norm_rope_bwd")
-    return dq, dk, dqw, dkw if k is not None else None
+        workspace = torch.empty(max(1, lib.h3_qk_norm_rope_bwd_workspace_size(D)), dtype=_U8, device=dev)
+    else:
+        _require(workspace, "workspace", _U8, dev)
+    desc = _QkNormDesc.pack(*sizes, eps, q_stride, k_stride, dq_out_stride, dk_out_stride, dq_stride, dk_stride)
+    _launch(lib.h3_qk_norm_rope_bwd, "h3_qk_norm_rope_bwd", dev, desc, dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(),
+            _ptr(k), q_weight.data_ptr(), k_weight.data_ptr() if has_k else None, *where,
+            ctypes.byref(cfg) if cfg is not None else None, dq.data_ptr(), _ptr(dk), dqw.data_ptr(), _ptr(dkw),
+            workspace.data_ptr(), workspace.numel())
+    return dq, dk, dqw, dkw
 
 
 def varlen_attn_workspace_size(num_segments: int, num_heads: int, max_seqlen: int, head_dim: int) -> int:
@@ -490,7 +514,8 @@ def varlen_attn_fwd_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 
 
 def _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqused_k, softmax_scale):
-    """Checks shared by the cross attention calls; returns the descriptor."""
+    """Checks shared by the cross attention calls; returns the descriptor's values and the offsets'
+    pointers."""
     dev = q.device
     q_stride, k_stride = _rows(q, "q", dev), _rows(k, "k", dev)
     v_stride = _rows(v, "v", dev, k.shape)
@@ -498,24 +523,27 @@ def _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_
     Ck, Hk, Dk = k.shape
     if Dk != D:
         raise ValueError("k and v must have q's head_dim")
-    _require(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
-    _require(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev)
+    _aux(cu_seqlens_q, "cu_seqlens_q", _I32, dev)
+    _aux(cu_seqlens_k, "cu_seqlens_k", _I32, dev)
     S = cu_seqlens_q.numel() - 1
     if S < 0 or cu_seqlens_k.numel() != S + 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must have one entry per segment and one more")
+    used = None
     if seqused_k is not None:
-        _require(seqused_k, "seqused_k", torch.int32, dev)
+        _aux(seqused_k, "seqused_k", _I32, dev)
         if seqused_k.numel() != S:
             raise ValueError("seqused_k must have one entry per segment")
-    return _CrossAttnDesc(S, int(max_seqlen_q), int(max_seqlen_k), C, Ck, H, Hk, D,
-                          0.0 if softmax_scale is None else float(softmax_scale), q_stride, k_stride, v_stride)
+        used = seqused_k.data_ptr()
+    sizes = (S, int(max_seqlen_q), int(max_seqlen_k), C, Ck, H, Hk, D,
+             0.0 if softmax_scale is None else float(softmax_scale), q_stride, k_stride, v_stride)
+    return sizes, (cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), used)
 
 
 def varlen_cross_attn_workspace_size(num_segments: int, max_seqlen_q: int, max_seqlen_k: int, capacity_q: int,
                                      capacity_k: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
-    desc = _CrossAttnDesc(num_segments, max_seqlen_q, max_seqlen_k, capacity_q, capacity_k, num_q_heads,
-                          num_kv_heads, head_dim)
-    return int(load_library().h3_varlen_cross_attn_workspace_size(ctypes.byref(desc)))
+    desc = _CrossAttnDesc.pack(num_segments, max_seqlen_q, max_seqlen_k, capacity_q, capacity_k, num_q_heads,
+                               num_kv_heads, head_dim, 0.0, 0, 0, 0, 0, 0, 0)
+    return int(load_library().h3_varlen_cross_attn_workspace_size(desc))
 
 
 def varlen_cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -532,40 +560,41 @@ def varlen_cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_
     of -inf; rows of `out` outside every segment are left untouched.  Returns out [Cq, Hq, D] (and lse
     fp32 [Hq, Cq] when requested).
     """
-    desc = _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqused_k, softmax_scale)
+    sizes, offsets = _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqused_k,
+                                   softmax_scale)
     dev = q.device
-    C, H, _ = q.shape
+    C, H = sizes[3], sizes[5]
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _require(out, "out", torch.bfloat16, dev)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if return_lse and lse is None:
-        lse = torch.empty((H, C), dtype=torch.float32, device=dev)
+        out = torch.empty(q.shape, dtype=_BF16, device=dev)
+    else:
+        _require(out, "out", _BF16, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
     if lse is not None:
-        _require(lse, "lse", torch.float32, dev)
-        if tuple(lse.shape) != (H, C):
+        _require(lse, "lse", _F32, dev)
+        if lse.shape != (H, C):
             raise ValueError("lse must be [Hq, Cq]")
+    elif return_lse:
+        lse = torch.empty((H, C), dtype=_F32, device=dev)
     if C > 0:
         lib = load_library()
+        desc = _CrossAttnDesc.pack(*sizes, 0, 0, 0)
         if workspace is None:
-            need = int(lib.h3_varlen_cross_attn_workspace_size(ctypes.byref(desc)))
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-        _require(workspace, "workspace", torch.uint8, dev)
-        with _on(dev):
-            st = lib.h3_varlen_cross_attn_fwd(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                              _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(seqused_k),
-                                              _ptr(workspace), workspace.numel(), _stream(dev))
-        _check(st, "h3_varlen_cross_attn_fwd")
+            need = lib.h3_varlen_cross_attn_workspace_size(desc)
+            workspace = torch.empty(need or 1, dtype=_U8, device=dev)
+        else:
+            _require(workspace, "workspace", _U8, dev)
+        _launch(lib.h3_varlen_cross_attn_fwd, "h3_varlen_cross_attn_fwd", dev, desc, q.data_ptr(), k.data_ptr(),
+                v.data_ptr(), out.data_ptr(), _ptr(lse), *offsets, workspace.data_ptr(), workspace.numel())
     return (out, lse) if lse is not None else out
 
 
 def varlen_cross_attn_bwd_workspace_size(num_segments: int, max_seqlen_q: int, max_seqlen_k: int, capacity_q: int,
                                          capacity_k: int, num_q_heads: int, num_kv_heads: int,
                                          head_dim: int) -> int:
-    desc = _CrossAttnDesc(num_segments, max_seqlen_q, max_seqlen_k, capacity_q, capacity_k, num_q_heads,
-                          num_kv_heads, head_dim)
-    return int(load_library().h3_varlen_cross_attn_bwd_workspace_size(ctypes.byref(desc)))
+    desc = _CrossAttnDesc.pack(num_segments, max_seqlen_q, max_seqlen_k, capacity_q, capacity_k, num_q_heads,
+                               num_kv_heads, head_dim, 0.0, 0, 0, 0, 0, 0, 0)
+    return int(load_library().h3_varlen_cross_attn_bwd_workspace_size(desc))
 
 
 def varlen_cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -580,33 +609,39 @@ def varlen_cross_attn_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, 
     dq, dk and dv may be parts of a fused gradient.  Every row of every segment is written (0 for keys
     that a segment does not use); other rows are left untouched.  The result does not depend on timing.
     """
-    desc = _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqused_k, softmax_scale)
-    dev = q.device
-    C, H, _ = q.shape
+    sizes, offsets = _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqused_k,
+                                   softmax_scale)
+    dev, shape, kshape = q.device, q.shape, k.shape
     for name, t in (("dout", dout), ("out", out)):
-        _require(t, name, torch.bfloat16, dev)
-        if t.shape != q.shape:
+        _aux(t, name, _BF16, dev)
+        if t.shape != shape:
             raise ValueError(f"{name} must have q's shape")
-    _require(lse, "lse", torch.float32, dev)
-    if tuple(lse.shape) != (H, C):
+    _aux(lse, "lse", _F32, dev)
+    if lse.shape != (sizes[5], sizes[3]):
         raise ValueError("lse must be [Hq, Cq]")
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=k.dtype, device=dev) if dk is None else dk
-    dv = torch.empty(k.shape, dtype=k.dtype, device=dev) if dv is None else dv
-    desc.dq_stride = _rows(dq, "dq", dev, q.shape)
-    desc.dk_stride = _rows(dk, "dk", dev, k.shape)
-    desc.dv_stride = _rows(dv, "dv", dev, k.shape)
+    strides = [0, 0, 0]
+    if dq is None:
+        dq = torch.empty(shape, dtype=_BF16, device=dev)
+    else:
+        strides[0] = _rows(dq, "dq", dev, shape)
+    if dk is None:
+        dk = torch.empty(kshape, dtype=_BF16, device=dev)
+    else:
+        strides[1] = _rows(dk, "dk", dev, kshape)
+    if dv is None:
+        dv = torch.empty(kshape, dtype=_BF16, device=dev)
+    else:
+        strides[2] = _rows(dv, "dv", dev, kshape)
     lib = load_library()
+    desc = _CrossAttnDesc.pack(*sizes, *strides)
     if workspace is None:
-        need = int(lib.h3_varlen_cross_attn_bwd_workspace_size(ctypes.byref(desc)))
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _require(workspace, "workspace", torch.uint8, dev)
-    with _on(dev):
-        st = lib.h3_varlen_cross_attn_bwd(ctypes.byref(desc), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                                          _ptr(lse), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(seqused_k),
-                                          _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace.numel(),
-                                          _stream(dev))
-    _check(st, "h3_varlen_cross_attn_bwd")
+        need = lib.h3_varlen_cross_attn_bwd_workspace_size(desc)
+        workspace = torch.empty(need or 1, dtype=_U8, device=dev)
+    else:
+        _require(workspace, "workspace", _U8, dev)
+    _launch(lib.h3_varlen_cross_attn_bwd, "h3_varlen_cross_attn_bwd", dev, desc, dout.data_ptr(), q.data_ptr(),
+            k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), *offsets, dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr(), workspace.data_ptr(), workspace.numel())
     return dq, dk, dv
 
 
