@@ -17,7 +17,8 @@
 // 128 query columns.  dV_i and S_{i+1} run while dS_i is computed, dK_i and dP_{i+1} while P_{i+1} is.
 // TMEM (512 columns): S^T/P^T, dP^T/dS^T, dK, dV.
 // dQ: S = Q K^T (two buffers), dP = dO V^T, dQ += dS K with dS written over S.  It runs from one item
-// into the next, since key lists may be a few tiles.
+// into the next, since key lists may be a few tiles.  A fourth warpgroup computes delta an item ahead (a
+// kernel of its own for it reads do once more: 59 us of a text case's 589).
 // In dQ the products come from two warps (S and dP from one, dQ from the other): a warp's polls queue
 // behind its own products, so one warp alone leaves the tensor core idle at each wait (4,096 x 4,096 x
 // 24 x 128: 236 us, 290 with one).  In dK/dV the four products of a step alternate between two chains
@@ -38,6 +39,9 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kThreads = 384;
+constexpr int kDqThreads = 512;  // registers moved with setmaxnreg
+constexpr int kDqRegsCompute = 168, kDqRegsRows = 80, kDqRegsControl = 96;
+static_assert(2 * kDqRegsCompute + kDqRegsRows + kDqRegsControl == 65536 / 128, "the registers at launch");
 constexpr int kTmemCols = 512;
 constexpr int kPlanThreads = 1024;
 
@@ -63,20 +67,32 @@ __device__ __forceinline__ bool valid_segment(const CrossSegments& s, int g, con
 }
 
 // ---- plan ------------------------------------------------------------------------------------------
-// Words: [0] dQ items, [1] dK/dV items, [2] chunks of the query range per key tile (at most), [3]
-// spare, then the exclusive prefixes of dQ items [S + 1] and of dK/dV items [S + 1].
+// Words: [0] dQ items, [1] dK/dV items, [2] chunks of the query range per key tile (at most), [3] key
+// tiles, then the exclusive prefixes of dQ items, dK/dV items and key tiles, [S + 1] each.
 __device__ __forceinline__ int kv_steps(const Segment& r, int group) {  // (head, query tile) pairs
   return r.used > 0 ? group * tiles_of(r.rows) : 0;
 }
 __device__ __forceinline__ int chunks_of(int steps, int most) { return max(1, min(steps, most)); }
+__device__ __forceinline__ const uint32_t* prefix_q(const uint32_t* plan) { return plan + kCrossBwdHeader; }
+__device__ __forceinline__ const uint32_t* prefix_kv(const uint32_t* plan, int S) {
+  return plan + kCrossBwdHeader + S + 1;
+}
+__device__ __forceinline__ const uint32_t* prefix_tiles(const uint32_t* plan, int S) {
+  return plan + kCrossBwdHeader + 2 * (S + 1);
+}
 
+// Exclusive sum over the block (whole warps) and the total.
 __device__ __forceinline__ uint32_t exclusive_scan(uint32_t v, uint32_t* s_warp, uint32_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   uint32_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
+  }
+  if (warps == 1) {
+    total = __shfl_sync(0xffffffffu, x, 31);
+    return x - v;
   }
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
@@ -84,13 +100,15 @@ __device__ __forceinline__ uint32_t exclusive_scan(uint32_t v, uint32_t* s_warp,
   uint32_t before = 0;
   total = 0;
 #pragma unroll 1
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = 0; w < warps; ++w) {
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
   }
   return before + x - v;
 }
 
+// One block: a warp when the segments fit its lanes (three short scans, no block barrier), else 1,024
+// threads with several segments each.
 __global__ void __launch_bounds__(kPlanThreads)
 cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws, int slots, int sms,
                       unsigned int* err) {
@@ -98,7 +116,7 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
   grid_dependency_wait();
   launch_dependents();
   const int S = seg.num_segments, tid = threadIdx.x, group = seg.num_q_heads / seg.num_kv_heads;
-  const int chunk = (S + kPlanThreads - 1) / kPlanThreads;
+  const int chunk = (S + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
   const int lo = min(S, tid * chunk), hi = min(S, lo + chunk);
   auto checked = [&](int g) {
     Segment r = segment_of(seg, g);
@@ -110,16 +128,19 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
     }
     return r;
   };
-  uint32_t nq = 0, nk = 0, work = 0, total_q, tiles, total_work;  // work: (key tile, step) pairs / 4
+  auto q_items = [&](const Segment& r) { return static_cast<uint32_t>(tiles_of(r.rows)) * seg.num_q_heads; };
+  auto k_tiles = [&](const Segment& r) { return static_cast<uint32_t>(tiles_of(r.keys)) * seg.num_kv_heads; };
+  Segment mine{};  // this thread's only segment, when it has one
+  if (chunk == 1 && lo < hi) mine = checked(lo);
+  auto segment = [&](int g) { return chunk == 1 ? mine : checked(g); };
+  uint32_t nq = 0, nt = 0, work = 0, nk = 0, total_q, tiles, total_work, total_k;
   for (int g = lo; g < hi; ++g) {
-    const Segment r = checked(g);
-    nq += static_cast<uint32_t>(tiles_of(r.rows)) * seg.num_q_heads;
-    const uint32_t t = static_cast<uint32_t>(tiles_of(r.keys)) * seg.num_kv_heads;
-    nk += t;
-    work += static_cast<uint32_t>((static_cast<uint64_t>(t) * kv_steps(r, group) + 3) / 4);
+    const Segment r = segment(g);
+    nq += q_items(r);
+    nt += k_tiles(r);
+    work += static_cast<uint32_t>((static_cast<uint64_t>(k_tiles(r)) * kv_steps(r, group) + 3) / 4);  // in fours
   }
-  uint32_t at_q = exclusive_scan(nq, s_warp, total_q);
-  exclusive_scan(nk, s_warp, tiles);
+  uint32_t at_q = exclusive_scan(nq, s_warp, total_q), at_t = exclusive_scan(nt, s_warp, tiles);
   exclusive_scan(work, s_warp, total_work);
   // Chunks per key tile: what makes the waves of items (of steps / c steps, and about 3 steps' time
   // of start and end each) shortest, as far as the slots reach.
@@ -127,7 +148,7 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
   if (tiles > 0) {
     const float steps = 4.f * static_cast<float>(total_work) / static_cast<float>(tiles);
     float best = INFINITY;
-    for (int c = 1; c <= kCrossBwdMaxChunks && static_cast<int64_t>(tiles) * c <= max(slots, static_cast<int>(tiles)); ++c) {
+    for (int c = 1; c <= kCrossBwdMaxChunks && (c == 1 || static_cast<int64_t>(tiles) * c <= slots); ++c) {
       const float waves = static_cast<float>((static_cast<int64_t>(tiles) * c + sms - 1) / sms);
       const float cost = waves * (steps / static_cast<float>(c) + 3.f);
       if (cost < best) {
@@ -136,27 +157,27 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
       }
     }
   }
-  nk = 0;
-  auto kv_items = [&](const Segment& r) {
-    return static_cast<uint32_t>(tiles_of(r.keys)) * seg.num_kv_heads * chunks_of(kv_steps(r, group), most);
-  };
-  for (int g = lo; g < hi; ++g) nk += kv_items(checked(g));
-  uint32_t total_k, at_k = exclusive_scan(nk, s_warp, total_k);
-  uint32_t* pq = ws + kCrossBwdHeader;
-  uint32_t* pk = pq + S + 1;
+  auto kv_items = [&](const Segment& r) { return k_tiles(r) * chunks_of(kv_steps(r, group), most); };
+  for (int g = lo; g < hi; ++g) nk += kv_items(segment(g));
+  uint32_t at_k = exclusive_scan(nk, s_warp, total_k);
+  uint32_t *pq = ws + kCrossBwdHeader, *pk = pq + S + 1, *pt = pk + S + 1;
   for (int g = lo; g < hi; ++g) {
-    const Segment r = checked(g);
+    const Segment r = segment(g);
     pq[g] = at_q;
     pk[g] = at_k;
-    at_q += static_cast<uint32_t>(tiles_of(r.rows)) * seg.num_q_heads;
+    pt[g] = at_t;
+    at_q += q_items(r);
     at_k += kv_items(r);
+    at_t += k_tiles(r);
   }
   if (tid == 0) {
     pq[S] = total_q;
     pk[S] = total_k;
+    pt[S] = tiles;
     ws[0] = total_q;
     ws[1] = total_k;
     ws[2] = static_cast<uint32_t>(most);
+    ws[3] = tiles;
   }
 }
 
@@ -167,47 +188,6 @@ __device__ __forceinline__ int find_segment(const uint32_t* __restrict__ prefix,
     if (prefix[mid] <= item) lo = mid; else hi = mid - 1;
   }
   return lo;
-}
-
-// ---- delta = rowsum(do * o) --------------------------------------------------------------------------
-// D / 8 lanes a row of one head; memory-bound.
-template <int D>
-__global__ void __launch_bounds__(256)
-cross_delta_kernel(const uint4* __restrict__ o, const uint4* __restrict__ dout, int64_t rows, int heads,
-                   int capacity, float* __restrict__ delta) {
-  constexpr int kLanes = D / 8;
-  grid_dependency_wait();
-  launch_dependents();
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (256 / kLanes);
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
-  constexpr int kUnroll = 4;
-  const int64_t warp_first = first - (threadIdx.x % 32) / kLanes;  // the same for the warp's lanes
-  for (int64_t base = 0; warp_first + base < rows; base += kUnroll * stride) {
-    uint4 x[kUnroll], y[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t r = first + base + u * stride;
-      x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows) {
-        x[u] = __ldg(o + r * kLanes + threadIdx.x % kLanes);
-        y[u] = __ldg(dout + r * kLanes + threadIdx.x % kLanes);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t r = first + base + u * stride;
-      const uint32_t a[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, b[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s = fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
-        s = fmaf(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(b[i] & 0xffff0000u), s);
-      }
-#pragma unroll
-      for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-      if (r < rows && threadIdx.x % kLanes == 0) delta[(r % heads) * capacity + r / heads] = s;
-    }
-  }
 }
 
 // ---- shared pieces of the two product kernels ----------------------------------------------------------
@@ -304,7 +284,7 @@ struct KvWork {
 
 __device__ __forceinline__ KvWork decode_kv(uint32_t item, const uint32_t* __restrict__ ws, const CrossSegments& seg) {
   const int S = seg.num_segments, group = seg.num_q_heads / seg.num_kv_heads;
-  const uint32_t* prefix = ws + kCrossBwdHeader + S + 1;
+  const uint32_t* prefix = prefix_kv(ws, S);
   const int g = find_segment(prefix, S, item);
   const Segment r = segment_of(seg, g);
   const int steps = kv_steps(r, group), chunks = chunks_of(steps, static_cast<int>(ws[2])), tiles = tiles_of(r.keys);
@@ -754,33 +734,35 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
   }
 }
 
-// Sums the chunks of every cut key tile, in chunk order: a CTA per (item of chunk 0, dV or dK) in turn.
+// Sums the chunks of every cut key tile, in chunk order: 16 rows of one tile's dV or dK to a unit.
 template <int D>
 __global__ void __launch_bounds__(256)
 cross_dkv_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
   grid_dependency_wait();
   launch_dependents();
   if (a.err != nullptr && *reinterpret_cast<const volatile unsigned int*>(a.err) == kErrTimeout) return;
-  if (a.plan[2] <= 1u) return;  // nothing was cut
-  const uint32_t total = a.plan[1];
+  const int most = static_cast<int>(a.plan[2]);
+  if (most <= 1) return;  // nothing was cut
   const int S = a.seg.num_segments, group = a.seg.num_q_heads / a.seg.num_kv_heads;
-  const uint32_t* prefix = a.plan + kCrossBwdHeader + S + 1;
-  constexpr int kParts = 8;  // 16 rows each
-  for (uint32_t u = blockIdx.x; u < total * 2 * kParts; u += gridDim.x) {
-    const uint32_t item = u / (2 * kParts);
-    const int which = u / kParts % 2, r0 = u % kParts * (kTile / kParts);
-    const int g = find_segment(prefix, S, item);
+  constexpr int kParts = 8, kRows = kTile / kParts;
+  const uint32_t units = a.plan[3] * 2 * kParts;
+  for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const uint32_t tile = u / (2 * kParts);
+    const int which = u / kParts % 2, r0 = u % kParts * kRows;
+    const int g = find_segment(prefix_tiles(a.plan, S), S, tile);
     const Segment r = segment_of(a.seg, g);
-    const int chunks = chunks_of(kv_steps(r, group), static_cast<int>(a.plan[2]));
-    if (chunks == 1 || (item - prefix[g]) % chunks != 0) continue;
-    const KvWork d = decode_kv(item, a.plan, a.seg);
-    if (d.slot < 0) continue;  // zeros, written already
-    const float* part = a.partials + (static_cast<size_t>(d.slot) * 2 + which) * kTile * D;
-    __nv_bfloat16* out = which == 0 ? a.dv : a.dk;
+    const int chunks = chunks_of(kv_steps(r, group), most), tiles = tiles_of(r.keys);
+    const uint32_t local = tile - prefix_tiles(a.plan, S)[g];
+    const int kt = static_cast<int>(local) % tiles, kv_head = static_cast<int>(local) / tiles;
+    if (chunks == 1 || kt * kTile >= r.used) continue;  // written already
+    const size_t slot = prefix_kv(a.plan, S)[g] + static_cast<size_t>(local) * chunks;
+    const float* part = a.partials + (slot * 2 + which) * kTile * D;
     const int64_t stride = which == 0 ? a.dv_stride : a.dk_stride;
-    for (int i = threadIdx.x; i < kTile / kParts * (D / 8); i += 256) {
+    __nv_bfloat16* out = (which == 0 ? a.dv : a.dk) + (static_cast<int64_t>(r.k0) + kt * kTile) * stride + kv_head * D;
+    const int rows = min(kTile, r.keys - kt * kTile);
+    for (int i = threadIdx.x; i < kRows * (D / 8); i += 256) {
       const int row = r0 + i / (D / 8), col = i % (D / 8) * 8;
-      if (row >= d.rows) continue;
+      if (row >= rows) continue;
       float s[8] = {};
 #pragma unroll 4
       for (int c = 0; c < chunks; ++c) {
@@ -789,7 +771,7 @@ cross_dkv_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
         s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
         s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
       }
-      *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(d.k_row) + row) * stride + d.kv_head * D + col) =
+      *reinterpret_cast<uint4*>(out + row * stride + col) =
           make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
     }
   }
@@ -805,7 +787,7 @@ struct QWork {
 
 __device__ __forceinline__ QWork decode_q(uint32_t item, const uint32_t* __restrict__ ws, const CrossSegments& seg) {
   const int S = seg.num_segments, group = seg.num_q_heads / seg.num_kv_heads;
-  const uint32_t* prefix = ws + kCrossBwdHeader;
+  const uint32_t* prefix = prefix_q(ws);
   const int g = find_segment(prefix, S, item);
   const Segment r = segment_of(seg, g);
   const int tiles = tiles_of(r.rows), local = static_cast<int>(item - prefix[g]);
@@ -826,23 +808,21 @@ struct QCfg {
   static constexpr int kStagesK = 3, kStagesV = 2;
   static constexpr int kWork = 4;  // items decoded ahead
   // q_full, q_empty, do_full, do_empty, s_full[2], s_empty[2], ds_full[2], dp_full, dp_read, acc_full,
-  // acc_empty, drain[2], w_full[kWork], w_empty[kWork], then k_full, k_empty, v_full, v_empty
-  static constexpr int kNumBars = 16 + 2 * kWork + 2 * kStagesK + 2 * kStagesV;
-  static constexpr int kSmemBytes = 1024 + Tiles<D>::kBytes * (2 + kStagesK + kStagesV) + kNumBars * 8 + 16 +
-                                    kWork * sizeof(QWork);
+  // acc_empty, drain[2], d_full[2], d_empty[2], w_full[kWork], w_empty[kWork], then k_full, k_empty, v_full, v_empty
+  static constexpr int kNumBars = 20 + 2 * kWork + 2 * kStagesK + 2 * kStagesV;
+  static constexpr int kSmemBytes = Tiles<D>::kBytes * (2 + kStagesK + kStagesV) + kNumBars * 8 + 16 +
+                                    kWork * sizeof(QWork) + 2 * kTile * sizeof(float2);
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
   static constexpr int kColS = 0, kColP = 256, kColQ = 384;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kDqThreads, 1)
 cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
   using C = QCfg<D>;
   using T = Tiles<D>;
   constexpr int SK = C::kStagesK, SV = C::kStagesV;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // no room to align it by hand
   uint8_t* sQ = smem;
   uint8_t* sO = sQ + T::kBytes;
   uint8_t* sK = sO + T::kBytes;
@@ -850,6 +830,8 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
   uint64_t* bars = reinterpret_cast<uint64_t*>(sV + SV * T::kBytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   QWork* work = reinterpret_cast<QWork*>(tmem_slot + 4);
+  // [2][128]: an item's (lse in units of log 2, delta)
+  float2* s_rows = reinterpret_cast<float2*>(work + C::kWork);
   const uint32_t bar0 = smem_u32(bars);
   auto bar = [&](int i) { return bar0 + 8 * static_cast<uint32_t>(i); };
   const uint32_t q_full = bar(0), q_empty = bar(1), do_full = bar(2), do_empty = bar(3), dp_full = bar(10),
@@ -859,9 +841,11 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
   // two of them: a warp may finish its next dS while another still works on this one
   auto ds_full = [&](uint32_t i) { return bar(8 + static_cast<int>(i)); };
   auto drain = [&](int i) { return bar(14 + i); };
-  auto w_full = [&](int k) { return bar(16 + k % C::kWork); };
-  auto w_empty = [&](int k) { return bar(16 + C::kWork + k % C::kWork); };
-  constexpr int kRing = 16 + 2 * C::kWork;
+  auto d_full = [&](int i) { return bar(16 + (i & 1)); };
+  auto d_empty = [&](int i) { return bar(18 + (i & 1)); };
+  auto w_full = [&](int k) { return bar(20 + k % C::kWork); };
+  auto w_empty = [&](int k) { return bar(20 + C::kWork + k % C::kWork); };
+  constexpr int kRing = 20 + 2 * C::kWork;
   auto k_full = [&](int s) { return bar(kRing + s); };
   auto k_empty = [&](int s) { return bar(kRing + SK + s); };
   auto v_full = [&](int s) { return bar(kRing + 2 * SK + s); };
@@ -896,6 +880,10 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
   if (__syncthreads_or(a.err != nullptr && *reinterpret_cast<volatile unsigned int*>(a.err) == kErrTimeout)) return;
   const uint32_t total = a.plan[0];
   if (blockIdx.x >= total) return;
+  if ((smem_u32(smem) & 1023u) != 0) {  // the tiles' swizzle needs it; not met on any known driver
+    if (threadIdx.x == 0) record_error(a.err, kErrTimeout);
+    return;
+  }
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&a.tmap_q);
     tma_prefetch_desc(&a.tmap_k);
@@ -906,9 +894,13 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
     for (uint32_t b : one) mbar_init(b, 1);
     const uint32_t warps8[] = {ds_full(0), ds_full(1), dp_read, acc_empty};
     for (uint32_t b : warps8) mbar_init(b, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(d_full(i), 4);
+      mbar_init(d_empty(i), 8);
+    }
     for (int i = 0; i < C::kWork; ++i) {
       mbar_init(w_full(i), 1);
-      mbar_init(w_empty(i), 11);  // compute warps, key/value loads, two product warps
+      mbar_init(w_empty(i), 15);  // compute warps, key/value loads, two product warps, row warps
     }
     for (int s = 0; s < SK; ++s) {
       mbar_init(k_full(s), 1);
@@ -929,179 +921,271 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8) {
-    // ================= key/value loads =================
-    bool ok = true, stalled = false;
-    uint32_t kt = 0, vt = 0;
-    QWork d;
-    for (int k = 0; ok && !stalled; ++k) {
-      ok = take(k, d);
-      if (!ok || !d.more) break;
-      for (int j = 0; j < d.nkv; ++j) {
-        if (kt >= a.stall_after_tiles) {
-          stalled = true;
+  if (warp >= 12) {
+    // ================= the rows' lse and delta = rowsum(do * o), an item or two ahead ===========
+    setmaxnreg_dec<kDqRegsRows>();
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kUnroll = 4;
+    const int row = threadIdx.x & 127;
+    // an item's rows of o and do into L2 an item before they are read: their latency is a large part
+    // of a short item's time
+    auto prefetch_rows = [&](const QWork& d) {
+      if (d.q_row + row >= d.q_end) return;
+      const size_t at = (static_cast<size_t>(d.q_row + row) * a.seg.num_q_heads + d.head) * D;
+#pragma unroll
+      for (int c = 0; c < D; c += 64) {
+        prefetch_l2(static_cast<const __nv_bfloat16*>(a.o) + at + c);
+        prefetch_l2(static_cast<const __nv_bfloat16*>(a.dout) + at + c);
+      }
+    };
+    auto delta_rows = [&](int k, const QWork& d) {
+      if (!wait_long(d_empty(k), ((k >> 1) & 1) ^ 1)) return false;
+      const int64_t step = static_cast<int64_t>(a.seg.num_q_heads) * kLanes;  // 16-byte pieces between rows
+      const int64_t at = d.q_row * step + d.head * kLanes + lane % kLanes;
+      const int rows = min(kTile, d.q_end - d.q_row);
+      const size_t stats = static_cast<size_t>(d.head) * a.seg.capacity_q + d.q_row;
+      s_rows[(k & 1) * kTile + row].x = row < rows ? a.lse[stats + row] * 1.4426950408889634f : 0.f;
+#pragma unroll 1
+      for (int r0 = (warp & 3) * 32; r0 < (warp & 3) * 32 + 32; r0 += kRows * kUnroll) {
+        uint4 x[kUnroll], y[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int r = r0 + u * kRows + lane / kLanes;
+          x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < rows) {
+            x[u] = __ldg(static_cast<const uint4*>(a.o) + at + r * step);
+            y[u] = __ldg(static_cast<const uint4*>(a.dout) + at + r * step);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int r = r0 + u * kRows + lane / kLanes;
+          const uint32_t p[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, q[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+          float f = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f = fmaf(__uint_as_float(p[i] << 16), __uint_as_float(q[i] << 16), f);
+            f = fmaf(__uint_as_float(p[i] & 0xffff0000u), __uint_as_float(q[i] & 0xffff0000u), f);
+          }
+#pragma unroll
+          for (int m = kLanes / 2; m > 0; m >>= 1) f += __shfl_xor_sync(0xffffffffu, f, m);
+          if (lane % kLanes == 0) {
+            s_rows[(k & 1) * kTile + r].y = f;
+            if (r < rows) a.delta[stats + r] = f;  // for dK
+          }
+        }
+      }
+      arrive_warp(d_full(k));
+      return true;
+    };
+    QWork d, nxt{};
+    bool ok = take(0, d);
+    for (int k = 0; ok && d.more; ++k) {
+      ok = take(k + 1, nxt);
+      if (ok && nxt.more) prefetch_rows(nxt);
+      if (ok) ok = delta_rows(k, d);
+      d = nxt;
+    }
+    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+  } else if (warp >= 8) {
+    setmaxnreg_dec<kDqRegsControl>();
+    if (warp == 8) {
+      // ================= key/value loads =================
+      bool ok = true, stalled = false;
+      uint32_t kt = 0, vt = 0;
+      QWork d;
+      for (int k = 0; ok && !stalled; ++k) {
+        ok = take(k, d);
+        if (!ok || !d.more) break;
+        for (int j = 0; j < d.nkv; ++j) {
+          if (kt >= a.stall_after_tiles) {
+            stalled = true;
+            break;
+          }
+          const int s = static_cast<int>(kt % SK), v = static_cast<int>(vt % SV);
+          ok = wait_long(k_empty(s), ((kt / SK) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) load_tile<D>(sK + s * T::kBytes, &a.tmap_k, d.kv_head, d.k_row + j * kTile, k_full(s));
+          ++kt;
+          ok = wait_long(v_empty(v), ((vt / SV) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) load_tile<D>(sV + v * T::kBytes, &a.tmap_v, d.kv_head, d.k_row + j * kTile, v_full(v));
+          ++vt;
+        }
+      }
+      if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+      for (uint32_t i = 0; i < SK && i < kt; ++i) mbar_wait(k_full((kt - 1 - i) % SK), ((kt - 1 - i) / SK) & 1);
+      for (uint32_t i = 0; i < SV && i < vt; ++i) mbar_wait(v_full((vt - 1 - i) % SV), ((vt - 1 - i) / SV) & 1);
+    } else if (warp == 10) {
+      // ================= scheduler, query and output-gradient loads =================
+      // Items are handed out kWork - 1 ahead of their queries: the others prepare while the query
+      // tiles' buffers are still taken.
+      bool ok = true, ended = false;
+      uint32_t item = blockIdx.x, n = 0;
+      auto post = [&](int k) {
+        QWork d{};
+        for (; item < total; item += gridDim.x) {
+          d = decode_q(item, a.plan, a.seg);
+          if (d.nkv > 0) break;
+          // no keys: zero the tile's rows here
+          const int rows = min(kTile, d.q_end - d.q_row);
+          for (int i = lane; i < rows * (D / 8); i += 32)
+            *reinterpret_cast<uint4*>(a.dq + (static_cast<int64_t>(d.q_row) + i / (D / 8)) * a.dq_stride + d.head * D +
+                                      i % (D / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
+          d.more = 0;
+        }
+        item += gridDim.x;
+        if (!wait_long(w_empty(k), (k / C::kWork & 1) ^ 1)) return false;
+        if (lane == 0) {
+          work[k % C::kWork] = d;
+          mbar_arrive(w_full(k));
+        }
+        __syncwarp();
+        ended = !d.more;
+        return true;
+      };
+      int posted = 0;
+      for (int k = 0; ok; ++k) {
+        while (ok && !ended && posted < k + C::kWork - 1) ok = post(posted++);
+        if (!ok) break;
+        const QWork d = work[k % C::kWork];  // not overwritten before it is done with here
+        if (!d.more) break;
+        ok = wait_long(q_empty, (n & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) load_tile<D>(sQ, &a.tmap_q, d.head, d.q_row, q_full);
+        ok = wait_long(do_empty, (n & 1) ^ 1);
+        if (!ok) {
+          mbar_wait(q_full, n & 1);
           break;
         }
-        const int s = static_cast<int>(kt % SK), v = static_cast<int>(vt % SV);
-        ok = wait_long(k_empty(s), ((kt / SK) & 1) ^ 1);
-        if (!ok) break;
-        if (lane == 0) load_tile<D>(sK + s * T::kBytes, &a.tmap_k, d.kv_head, d.k_row + j * kTile, k_full(s));
-        ++kt;
-        ok = wait_long(v_empty(v), ((vt / SV) & 1) ^ 1);
-        if (!ok) break;
-        if (lane == 0) load_tile<D>(sV + v * T::kBytes, &a.tmap_v, d.kv_head, d.k_row + j * kTile, v_full(v));
-        ++vt;
+        if (lane == 0) load_tile<D>(sO, &a.tmap_do, d.head, d.q_row, do_full);
+        ++n;
       }
-    }
-    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
-    for (uint32_t i = 0; i < SK && i < kt; ++i) mbar_wait(k_full((kt - 1 - i) % SK), ((kt - 1 - i) / SK) & 1);
-    for (uint32_t i = 0; i < SV && i < vt; ++i) mbar_wait(v_full((vt - 1 - i) % SV), ((vt - 1 - i) / SV) & 1);
-  } else if (warp == 10) {
-    // ================= scheduler, query and output-gradient loads =================
-    bool ok = true;
-    uint32_t item = blockIdx.x, n = 0;
-    for (int k = 0; ok; ++k) {
-      QWork d{};
-      for (; item < total; item += gridDim.x) {
-        d = decode_q(item, a.plan, a.seg);
-        if (d.nkv > 0) break;
-        // no keys: zero the tile's rows here
-        const int rows = min(kTile, d.q_end - d.q_row);
-        for (int i = lane; i < rows * (D / 8); i += 32)
-          *reinterpret_cast<uint4*>(a.dq + (static_cast<int64_t>(d.q_row) + i / (D / 8)) * a.dq_stride + d.head * D +
-                                    i % (D / 8) * 8) = make_uint4(0u, 0u, 0u, 0u);
-        d.more = 0;
+      if (!ok && lane == 0) record_error(a.err, kErrTimeout);
+      if (n > 0) mbar_wait(q_full, (n - 1) & 1);
+      if (n > 0) mbar_wait(do_full, (n - 1) & 1);
+    } else if (warp == 9) {
+      // ================= S and dP =================
+      const bool leader = elect_one();
+      constexpr uint32_t kTile16 = T::kBytes >> 4;
+      const SmemDesc dq = sw128_desc_split(smem_u32(sQ), 16, 1024), dd = sw128_desc_split(smem_u32(sO), 16, 1024);
+      const SmemDesc dk = sw128_desc_split(smem_u32(sK), 16, 1024), dv = sw128_desc_split(smem_u32(sV), 16, 1024);
+      bool ok = true, issued = false;
+      uint32_t n = 0, items = 0;
+      QWork d;
+      for (int k = 0; ok; ++k, ++items) {
+        ok = take(k, d);
+        if (!ok || !d.more) break;
+        for (int j = 0; j < d.nkv; ++j, ++n) {
+          const int s = static_cast<int>(n % SK), v = static_cast<int>(n % SV);
+          const bool last = j == d.nkv - 1;
+          const int keys = last ? d.last_keys : kTile;
+          ok = wait2(s_empty(n & 1), ((n >> 1) & 1) ^ 1, k_full(s), (n / SK) & 1);
+          if (ok && j == 0) ok = wait(q_full, items & 1);
+          if (!ok) break;
+          if (keys % 16 != 0) zero_rows<D>(sK + s * T::kBytes, keys);
+          tc_fence_after();
+          if (leader) {  // S = Q K^T
+            product_ss<D>(tmem + C::kColS + 128 * (n & 1), dq.lo, dq.hi, dk.lo + s * kTile16, dk.hi, steps16(keys));
+            mma_commit(s_full(n & 1));
+            if (last) mma_commit(q_empty);
+          }
+          __syncwarp();
+          issued = true;
+          ok = wait(v_full(v), (n / SV) & 1);
+          if (ok && j == 0) ok = wait(do_full, items & 1);
+          if (ok && n > 0) ok = wait(dp_read, (n - 1) & 1);
+          if (!ok) break;
+          if (keys % 16 != 0) zero_rows<D>(sV + v * T::kBytes, keys);
+          tc_fence_after();
+          if (leader) {  // dP = dO V^T
+            product_ss<D>(tmem + C::kColP, dd.lo, dd.hi, dv.lo + v * kTile16, dv.hi, steps16(keys));
+            mma_commit(dp_full);
+            mma_commit(v_empty(v));
+            if (last) mma_commit(do_empty);
+          }
+          __syncwarp();
+        }
       }
-      item += gridDim.x;
-      ok = wait_long(w_empty(k), (k / C::kWork & 1) ^ 1);
-      if (!ok) break;
-      if (lane == 0) {
-        work[k % C::kWork] = d;
-        mbar_arrive(w_full(k));
+      if (!ok && leader) record_error(a.err, kErrTimeout);
+      if (issued && leader) {
+        mma_commit(drain(0));
+        mbar_wait(drain(0), 0);
       }
       __syncwarp();
-      if (!d.more) break;
-      ok = wait_long(q_empty, (n & 1) ^ 1);
-      if (!ok) break;
-      if (lane == 0) load_tile<D>(sQ, &a.tmap_q, d.head, d.q_row, q_full);
-      ok = wait_long(do_empty, (n & 1) ^ 1);
-      if (!ok) {
-        if (lane == 0) mbar_wait(q_full, n & 1);
-        break;
-      }
-      if (lane == 0) load_tile<D>(sO, &a.tmap_do, d.head, d.q_row, do_full);
-      ++n;
-    }
-    if (!ok && lane == 0) record_error(a.err, kErrTimeout);
-    if (n > 0) mbar_wait(q_full, (n - 1) & 1);
-    if (n > 0) mbar_wait(do_full, (n - 1) & 1);
-  } else if (warp == 9) {
-    // ================= S and dP =================
-    const bool leader = elect_one();
-    constexpr uint32_t kTile16 = T::kBytes >> 4;
-    const SmemDesc dq = sw128_desc_split(smem_u32(sQ), 16, 1024), dd = sw128_desc_split(smem_u32(sO), 16, 1024);
-    const SmemDesc dk = sw128_desc_split(smem_u32(sK), 16, 1024), dv = sw128_desc_split(smem_u32(sV), 16, 1024);
-    bool ok = true, issued = false;
-    uint32_t n = 0, items = 0;
-    QWork d;
-    for (int k = 0; ok; ++k, ++items) {
-      ok = take(k, d);
-      if (!ok || !d.more) break;
-      for (int j = 0; j < d.nkv; ++j, ++n) {
-        const int s = static_cast<int>(n % SK), v = static_cast<int>(n % SV);
-        const bool last = j == d.nkv - 1;
-        const int keys = last ? d.last_keys : kTile;
-        ok = wait2(s_empty(n & 1), ((n >> 1) & 1) ^ 1, k_full(s), (n / SK) & 1);
-        if (ok && j == 0) ok = wait(q_full, items & 1);
-        if (!ok) break;
-        if (keys % 16 != 0) zero_rows<D>(sK + s * T::kBytes, keys);
-        tc_fence_after();
-        if (leader) {  // S = Q K^T
-          product_ss<D>(tmem + C::kColS + 128 * (n & 1), dq.lo, dq.hi, dk.lo + s * kTile16, dk.hi, steps16(keys));
-          mma_commit(s_full(n & 1));
-          if (last) mma_commit(q_empty);
+    } else if (warp == 11) {
+      // ================= dQ += dS K =================
+      const bool leader = elect_one();
+      constexpr uint32_t kTile16 = T::kBytes >> 4;
+      const SmemDesc rk = sw128_desc_split(smem_u32(sK), T::kBoxBytes, 1024);
+      bool ok = true, issued = false;
+      uint32_t n = 0, items = 0;
+      QWork d;
+      for (int k = 0; ok; ++k, ++items) {
+        ok = take(k, d);
+        if (!ok || !d.more) break;
+        for (int j = 0; j < d.nkv; ++j, ++n) {
+          const int s = static_cast<int>(n % SK);
+          const bool last = j == d.nkv - 1;
+          ok = wait(ds_full(n & 1), (n >> 1) & 1);
+          if (ok && j == 0) ok = wait(acc_empty, (items & 1) ^ 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            product_ts<D>(tmem + C::kColQ, tmem + C::kColS + 128 * (n & 1), rk.lo + s * kTile16, rk.hi,
+                          steps16(last ? d.last_keys : kTile), j == 0);
+            mma_commit(k_empty(s));
+            mma_commit(s_empty(n & 1));
+            if (last) mma_commit(acc_full);
+          }
+          __syncwarp();
+          issued = true;
         }
-        __syncwarp();
-        issued = true;
-        ok = wait(v_full(v), (n / SV) & 1);
-        if (ok && j == 0) ok = wait(do_full, items & 1);
-        if (ok && n > 0) ok = wait(dp_read, (n - 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {  // dP = dO V^T
-          product_ss<D>(tmem + C::kColP, dd.lo, dd.hi, dv.lo + v * kTile16, dv.hi, steps16(keys));
-          mma_commit(dp_full);
-          mma_commit(v_empty(v));
-          if (last) mma_commit(do_empty);
-        }
-        __syncwarp();
       }
-    }
-    if (!ok && leader) record_error(a.err, kErrTimeout);
-    if (issued && leader) {
-      mma_commit(drain(0));
-      mbar_wait(drain(0), 0);
-    }
-    __syncwarp();
-  } else if (warp == 11) {
-    // ================= dQ += dS K =================
-    const bool leader = elect_one();
-    constexpr uint32_t kTile16 = T::kBytes >> 4;
-    const SmemDesc rk = sw128_desc_split(smem_u32(sK), T::kBoxBytes, 1024);
-    bool ok = true, issued = false;
-    uint32_t n = 0, items = 0;
-    QWork d;
-    for (int k = 0; ok; ++k, ++items) {
-      ok = take(k, d);
-      if (!ok || !d.more) break;
-      for (int j = 0; j < d.nkv; ++j, ++n) {
-        const int s = static_cast<int>(n % SK);
-        const bool last = j == d.nkv - 1;
-        ok = wait(ds_full(n & 1), (n >> 1) & 1);
-        if (ok && j == 0) ok = wait(acc_empty, (items & 1) ^ 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          product_ts<D>(tmem + C::kColQ, tmem + C::kColS + 128 * (n & 1), rk.lo + s * kTile16, rk.hi,
-                        steps16(last ? d.last_keys : kTile), j == 0);
-          mma_commit(k_empty(s));
-          mma_commit(s_empty(n & 1));
-          if (last) mma_commit(acc_full);
-        }
-        __syncwarp();
-        issued = true;
+      if (!ok && leader) record_error(a.err, kErrTimeout);
+      if (issued && leader) {
+        mma_commit(drain(1));
+        mbar_wait(drain(1), 0);
       }
+      __syncwarp();
     }
-    if (!ok && leader) record_error(a.err, kErrTimeout);
-    if (issued && leader) {
-      mma_commit(drain(1));
-      mbar_wait(drain(1), 0);
-    }
-    __syncwarp();
   } else {
+    setmaxnreg_inc<kDqRegsCompute>();
     // ================= dS and the epilogue: query row = TMEM lane, keys by warpgroup ==============
     const int half = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t p_addr = tmem + lane_base + C::kColP + 64 * half;
     const float scale_log2 = a.scale * 1.4426950408889634f;
     bool ok = true;
-    uint32_t n = 0, items = 0;
-    QWork d;
-    for (int k = 0; ok; ++k) {
-      ok = take(k, d);
-      if (!ok || !d.more) break;
-      const int q_row = d.q_row + row;
-      float lse2 = 0.f, delta = 0.f;
-      if (q_row < d.q_end) {
-        const size_t i = static_cast<size_t>(d.head) * a.seg.capacity_q + q_row;
-        lse2 = a.lse[i] * 1.4426950408889634f;
-        delta = a.delta[i];
-      }
+    uint32_t n = 0;
+    QWork d, nxt;
+    float2 mine = make_float2(0.f, 0.f);  // this row's lse and delta
+    auto begin = [&](int k, QWork& item) {
+      if (!take(k, item)) return false;
+      if (!item.more) return true;
+      if (!wait(d_full(k), (k >> 1) & 1)) return false;
+      return true;
+    };
+    ok = begin(0, d);
+    for (int k = 0; ok && d.more; ++k) {
+      mine = s_rows[(k & 1) * kTile + row];
+      arrive_warp(d_empty(k));
       for (int j = 0; j < d.nkv; ++j, ++n) {
         const uint32_t s_addr = tmem + lane_base + C::kColS + 128 * (n & 1) + 64 * half;
-        ok = wait(s_full(n & 1), (n >> 1) & 1);
+        const bool last = j == d.nkv - 1;
+        // the next item's values, while the products of the last step run
+        if (last) ok = begin(k + 1, nxt);
+        if (ok) ok = wait(s_full(n & 1), (n >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
+        if (last && d.last_keys <= 64 * half) {  // no keys in this warpgroup's columns
+          ok = wait(dp_full, n & 1);
+          if (!ok) break;
+          tc_fence_after();
+          tc_fence_before();
+          arrive_warp(dp_read);
+          arrive_warp(ds_full(n & 1));
+          continue;
+        }
         uint32_t x[64];
         tmem_ld32(s_addr, x);
         tmem_ld32(s_addr + 32, x + 32);
@@ -1109,7 +1193,13 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
         tmem_reg_fence<64>(x);
         float p[64];
 #pragma unroll
-        for (int c = 0; c < 64; ++c) p[c] = ex2_approx(fmaf(__uint_as_float(x[c]), scale_log2, -lse2));
+        for (int c = 0; c < 64; ++c) p[c] = ex2_approx(fmaf(__uint_as_float(x[c]), scale_log2, -mine.x));
+        if (last && d.last_keys < kTile) {
+          // Columns past the keys: their K and V rows are zeros (or not multiplied at all), so any
+          // finite weight adds nothing; a row's own weights are at most 1.
+#pragma unroll
+          for (int c = 0; c < 64; ++c) p[c] = fminf(p[c], 2.f);
+        }
         ok = wait(dp_full, n & 1);
         if (!ok) break;
         tc_fence_after();
@@ -1120,11 +1210,7 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
         tc_fence_before();
         arrive_warp(dp_read);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(x[c]) - delta;
-        if (j == d.nkv - 1 && d.last_keys < kTile) {  // keys past the end
-#pragma unroll
-          for (int c = 0; c < 64; ++c) p[c] = 64 * half + c < d.last_keys ? p[c] : 0.f;
-        }
+        for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(x[c]) - mine.y;
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
@@ -1133,7 +1219,7 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
         tc_fence_before();
         arrive_warp(ds_full(n & 1));
       }
-      if (ok) ok = wait(acc_full, items & 1);
+      if (ok) ok = wait(acc_full, k & 1);
       if (!ok) break;
       tc_fence_after();
       // epilogue: each warpgroup stores half the columns
@@ -1145,11 +1231,13 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
         tmem_ld32(tmem + lane_base + C::kColQ + c0, x);
         tmem_ld_wait();
         tmem_reg_fence<32>(x);
+        if (c0 + 32 == (half + 1) * (D / 2)) {
+          tc_fence_before();
+          arrive_warp(acc_empty);
+        }
         store_columns(x, a.scale, p0 + c0, p0 + a.dq_stride + c0, r0 < d.q_end, r0 + 1 < d.q_end, a.wide);
       }
-      tc_fence_before();
-      arrive_warp(acc_empty);
-      ++items;
+      d = nxt;
     }
     if (!ok && lane == 0) record_error(a.err, kErrTimeout);
   }
@@ -1170,18 +1258,11 @@ cudaError_t launch(const CrossBwdArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  e = launch_programmatic(cross_bwd_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.seg, a.plan,
-                          a.slots, sms, a.err);
+  e = launch_programmatic(cross_bwd_plan_kernel, dim3(1), dim3(a.seg.num_segments <= 32 ? 32 : kPlanThreads), 0, stream,
+                          a.seg, a.plan, a.slots, sms, a.err);
   if (e != cudaSuccess) return e;
-  const int64_t rows = static_cast<int64_t>(a.seg.capacity_q) * a.seg.num_q_heads;
-  if (rows > 0) {
-    constexpr int kPerCta = 256 / (D / 8) * 4;
-    const int64_t want = (rows + kPerCta - 1) / kPerCta, most = static_cast<int64_t>(sms) * 8;
-    e = launch_programmatic(cross_delta_kernel<D>, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(256),
-                            0, stream, static_cast<const uint4*>(a.o), static_cast<const uint4*>(a.dout), rows,
-                            a.seg.num_q_heads, a.seg.capacity_q, a.delta);
-    if (e != cudaSuccess) return e;
-    e = launch_programmatic(cross_dq_kernel<D>, dim3(sms), dim3(kThreads), QCfg<D>::kSmemBytes, stream, a);
+  if (a.seg.capacity_q > 0) {
+    e = launch_programmatic(cross_dq_kernel<D>, dim3(sms), dim3(kDqThreads), QCfg<D>::kSmemBytes, stream, a);
     if (e != cudaSuccess) return e;
   }
   if (a.seg.capacity_k > 0) {

@@ -191,7 +191,8 @@ struct CrossArgs {
 };
 cudaError_t launch_cross_attn(const CrossArgs& a, int head_dim, cudaStream_t stream);
 
-// Gradient.  Work plan: header words, then the item prefixes of the two product kernels.  A key tile's
+// Gradient.  Work plan: header words, then the prefixes of the two product kernels' items and of key
+// tiles.  A key tile's
 // query range may be cut into up to kCrossBwdMaxChunks chunks, whose partial sums take a slot each
 // (two tiles of 128 x head_dim fp32).
 constexpr int kCrossBwdHeader = 4;
@@ -221,7 +222,7 @@ struct CrossBwdWorkspace {
 inline CrossBwdWorkspace cross_bwd_workspace(const CrossSegments& s, int head_dim) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   CrossBwdWorkspace w;
-  w.delta = up((kCrossBwdHeader + 2 * (static_cast<size_t>(s.num_segments) + 1)) * sizeof(uint32_t));
+  w.delta = up((kCrossBwdHeader + 3 * (static_cast<size_t>(s.num_segments) + 1)) * sizeof(uint32_t));
   w.partials = w.delta + up(static_cast<size_t>(s.num_q_heads) * s.capacity_q * sizeof(float));
   // no more slots than chunks of all key tiles the capacity allows
   const int64_t tiles = (static_cast<int64_t>(s.capacity_k) / 128 + s.num_segments) * s.num_kv_heads;
