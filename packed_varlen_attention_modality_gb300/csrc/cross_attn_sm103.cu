@@ -45,7 +45,7 @@ namespace {
 
 constexpr int kBlockM = 128, kBlockN = 128;
 constexpr int kThreads = 512;
-constexpr int kRegsSoftmax = 176, kRegsEpilogue = 64, kRegsOther = 96;
+constexpr int kRegsSoftmax = 176, kRegsEpilogue = 80, kRegsOther = 80;
 static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOther == 65536 / 128, "the split of the registers at launch");
 constexpr int kTmemCols = 512, kColO = 0, kColS = 256;
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the running max grows by > 2^8
@@ -523,100 +523,114 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
       };
       // an item's last key tile is multiplied as far as it holds keys, but at least one step
       auto steps16 = [](int keys) { return max(1, (keys + 15) / 16); };
-      auto idesc_of = [&](const Item& i, int j) {
-        return j == i.nkv - 1 && i.last_keys < kBlockN
-                   ? idesc_bf16_f32(kBlockM, 16 * steps16(i.last_keys), false) : C::kIdescQK;
+      auto idesc_last = [&](const Item& i) {
+        return i.last_keys < kBlockN ? idesc_bf16_f32(kBlockM, 16 * steps16(i.last_keys), false) : C::kIdescQK;
       };
-      uint32_t kc = 0, vc = 0;  // K / V tiles consumed
-      uint32_t qn[2] = {0u, 0u}, pn[2] = {0u, 0u}, un[2] = {0u, 0u};
+      // Ring positions as stage and phase: what the one issuing thread computes between two products
+      // delays them.
+      int sk = 0, sv = 0;
+      uint32_t pk = 0, pv = 0;                                 // phases of the K and V rings
+      uint32_t qp[2] = {0u, 0u}, pp[2] = {0u, 0u}, op[2] = {1u, 1u};  // phases of Q, P and O per tile
+      auto next_k = [&] {
+        if (++sk == SK) {
+          sk = 0;
+          pk ^= 1;
+        }
+      };
       bool ok = take_item(0, cur), issued = false;
       if (ok && cur.ntiles > 0) {  // the first item's first scores
         ok = wait_all(bar_kfull(0), 0);
+        const uint32_t idesc = cur.nkv == 1 ? idesc_last(cur) : C::kIdescQK;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || t >= cur.ntiles) break;
-          ok = wait_all(bar_qfull(t), qn[t]++ & 1);
+          ok = wait_all(bar_qfull(t), qp[t]);
+          qp[t] ^= 1;
           if (!ok) break;
           tc_fence_after();
           if (leader) {
-            issue_qk(t, 0, idesc_of(cur, 0));
+            issue_qk(t, 0, idesc);
             if (cur.nkv == 1) mma_commit(bar_qempty(t));
             if (t == cur.ntiles - 1) mma_commit(bar_kempty(0));
           }
           issued = true;
           __syncwarp();
         }
-        kc = 1;
+        next_k();
       }
-      for (int k = 0; ok && cur.ntiles > 0; ++k) {
-        for (int j = 0; j < cur.nkv && ok; ++j) {
-          const bool last = j + 1 == cur.nkv;
-          const int sv = static_cast<int>(vc % SV), sk = static_cast<int>(kc % SK);
-          if (last) {
-            ok = take_item(k + 1, nxt);
-            if (!ok) break;
-          }
-          // the scores issued in this step: the item's next key tile, or the next item's first
-          const int stiles = last ? nxt.ntiles : cur.ntiles;
-          const uint32_t idesc = last ? idesc_of(nxt, 0) : idesc_of(cur, j + 1);
-          const bool q_done = last ? nxt.nkv == 1 : j + 2 == cur.nkv;  // their item's last scores
-          const int end = last ? steps16(cur.last_keys) : kBlockN / 16;
-          ok = wait_all2(bar_vfull(sv), (vc / SV) & 1, bar_phalf(0), pn[0] & 1);
-          if (!ok) break;
-          if (last && cur.last_keys < 16 * end) {
-            // zero the value rows past the keys as far as PV reads (whole 128-byte rows: the
-            // swizzle permutes 16-byte pieces within a row)
-            uint8_t* vb = sV + sv * C::kTileBytes;
-            const int nrows = 16 * end - cur.last_keys;
-            for (int i = lane; i < nrows * C::kBoxes * 8; i += 32) {
-              const int r = cur.last_keys + i / (C::kBoxes * 8), rem = i % (C::kBoxes * 8);
-              *reinterpret_cast<uint4*>(vb + (rem >> 3) * C::kBoxBytes + r * 128 + (rem & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+      // One step: PV of the item's key tile, and the scores of the next one (its own, or the next item's
+      // first: last).  PV_t runs in two halves, as P of the first 64 keys comes earlier.
+      auto step = [&](bool first, bool last, int stiles, uint32_t idesc, bool q_done, int end) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t < cur.ntiles) {
+            if (t > 0 && !wait_all(bar_phalf(t), pp[t])) return false;
+            if (first) {
+              if (!wait_all(bar_oempty(t), op[t])) return false;
+              op[t] ^= 1;
             }
-            fence_proxy_async_smem();
+            tc_fence_after();
+            if (leader) issue_pv(t, sv, first, 0, end);
+            __syncwarp();
+            if (!(t == 0 && stiles > 0 ? wait_all2(bar_pfull(0), pp[0], bar_kfull(sk), pk)
+                                       : wait_all(bar_pfull(t), pp[t])))
+              return false;
+            pp[t] ^= 1;
+            tc_fence_after();
+            if (leader) {
+              issue_pv(t, sv, false, 1, end);
+              if (last) mma_commit(bar_ofinal(t));
+              if (t == cur.ntiles - 1) mma_commit(bar_vempty(sv));
+            }
             __syncwarp();
           }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t < cur.ntiles) {  // PV_t in two halves: P of the first 64 keys comes earlier
-              if (t > 0) ok = wait_all(bar_phalf(t), pn[t] & 1);
-              if (ok && j == 0) ok = wait_all(bar_oempty(t), (un[t] & 1) ^ 1);
-              if (!ok) break;
+          if (t < stiles) {
+            if (last) {
+              if (!wait_all(bar_qfull(t), qp[t])) return false;
+              qp[t] ^= 1;
               tc_fence_after();
-              if (leader) issue_pv(t, sv, j == 0, 0, end);
-              __syncwarp();
-              ok = t == 0 && stiles > 0 ? wait_all2(bar_pfull(0), pn[0] & 1, bar_kfull(sk), (kc / SK) & 1)
-                                        : wait_all(bar_pfull(t), pn[t] & 1);
-              ++pn[t];
-              if (!ok) break;
-              tc_fence_after();
-              if (leader) {
-                issue_pv(t, sv, false, 1, end);
-                if (last) mma_commit(bar_ofinal(t));
-                if (t == cur.ntiles - 1) mma_commit(bar_vempty(sv));
-              }
-              __syncwarp();
             }
-            if (t < stiles) {
-              if (last) {
-                ok = wait_all(bar_qfull(t), qn[t]++ & 1);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              if (leader) {
-                issue_qk(t, sk, idesc);
-                if (q_done) mma_commit(bar_qempty(t));
-                if (t == stiles - 1) mma_commit(bar_kempty(sk));
-              }
-              __syncwarp();
+            if (leader) {
+              issue_qk(t, sk, idesc);
+              if (q_done) mma_commit(bar_qempty(t));
+              if (t == stiles - 1) mma_commit(bar_kempty(sk));
             }
+            __syncwarp();
           }
-          ++vc;
-          if (stiles > 0) ++kc;
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (t < cur.ntiles) ++un[t];
+        if (++sv == SV) {
+          sv = 0;
+          pv ^= 1;
+        }
+        if (stiles > 0) next_k();
+        return true;
+      };
+      for (int k = 0; ok && cur.ntiles > 0; ++k) {
+        const uint32_t idesc_end = idesc_last(cur);
+        for (int j = 0; j + 1 < cur.nkv && ok; ++j) {
+          ok = wait_all2(bar_vfull(sv), pv, bar_phalf(0), pp[0]);
+          if (!ok) break;
+          const bool q_done = j + 2 == cur.nkv;
+          ok = step(j == 0, false, cur.ntiles, q_done ? idesc_end : C::kIdescQK, q_done, kBlockN / 16);
+        }
+        if (ok) ok = take_item(k + 1, nxt);
+        if (ok) ok = wait_all2(bar_vfull(sv), pv, bar_phalf(0), pp[0]);
+        if (!ok) break;
+        const int end = steps16(cur.last_keys);
+        if (cur.last_keys < 16 * end) {
+          // zero the value rows past the keys as far as PV reads (whole 128-byte rows: the swizzle
+          // permutes 16-byte pieces within a row)
+          uint8_t* vb = sV + sv * C::kTileBytes;
+          const int nrows = 16 * end - cur.last_keys;
+          for (int i = lane; i < nrows * C::kBoxes * 8; i += 32) {
+            const int r = cur.last_keys + i / (C::kBoxes * 8), rem = i % (C::kBoxes * 8);
+            *reinterpret_cast<uint4*>(vb + (rem >> 3) * C::kBoxBytes + r * 128 + (rem & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ok = step(cur.nkv == 1, true, nxt.ntiles, nxt.nkv == 1 ? idesc_last(nxt) : C::kIdescQK, nxt.nkv == 1, end);
         cur = nxt;
       }
       if (!ok && leader) record_error(err, kErrTimeout);
