@@ -297,7 +297,7 @@ H3_API h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* desc, const 
                                           size_t workspace_bytes, h3_stream_t stream);
 
 /* Workspace bytes of h3_varlen_cross_attn_bwd (the work plan, rowsum(do * o), and the partial sums of
- * key tiles whose query range is cut: at most about 160 MB at head_dim 128); 0 for invalid sizes. */
+ * tiles whose range is cut: at most about 120 MB at head_dim 128); 0 for invalid sizes. */
 H3_API size_t h3_varlen_cross_attn_bwd_workspace_size(const h3_cross_attn_desc* desc);
 
 /* Gradient of h3_varlen_cross_attn_fwd (with equal offsets, also of h3_varlen_attn_fwd), with

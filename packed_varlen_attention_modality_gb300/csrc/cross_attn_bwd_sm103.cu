@@ -8,8 +8,9 @@
 // CTA's accumulators: the dK/dV kernel keeps a 128-key tile and runs over the queries, the dQ kernel
 // keeps a 128-row query tile and runs over the keys.  Each recomputes S and dP (7 products in all
 // instead of 5); in exchange nothing is summed through memory in an order that depends on timing
-// (no atomics), and no fp32 gradient goes through memory.  When there are too few key tiles to fill
-// the GPU, their query range is cut into chunks whose fp32 partial sums a last kernel adds in order.
+// (no atomics), and no fp32 gradient goes through memory, but for the tiles of a last, partly filled
+// wave of CTAs: their range is cut into chunks so that they fill it too (4,096 x 4,096 x 24 heads is
+// 5.05 waves of tiles in each kernel), and a last kernel adds the chunks' fp32 sums in order.
 //
 // dK/dV works on transposed scores: S^T = K Q^T and dP^T = V dO^T have keys as TMEM lanes, so P^T and
 // dS^T are written back to TMEM as the A operands of dV += P^T dO and dK += dS^T Q, and one copy of Q
@@ -29,6 +30,8 @@
 // in shared memory as far as a product reads them, and masked by select where they would meet an
 // exponential.  Every wait is bounded; a wait that runs out records a timeout and unwinds the CTA.
 #include <cuda_bf16.h>
+
+#include <cstddef>
 
 #include "h3_internal.h"
 #include "launch.h"
@@ -67,18 +70,32 @@ __device__ __forceinline__ bool valid_segment(const CrossSegments& s, int g, con
 }
 
 // ---- plan ------------------------------------------------------------------------------------------
-// Words: [0] dQ items, [1] dK/dV items, [2] chunks of the query range per key tile (at most), [3] key
-// tiles, then the exclusive prefixes of dQ items, dK/dV items and key tiles, [S + 1] each.
+// Tiles of each kernel are numbered over the segments (head-major within one).  Whole waves of tiles are
+// an item each; the tiles behind them are cut into `chunks` items each.
+struct Plan {
+  uint32_t items_q, items_k;  // of dQ and of dK/dV
+  uint32_t whole_q, whole_k;  // tiles that are an item
+  uint32_t chunks_q, chunks_k;
+  uint32_t tiles_q, tiles_k;
+  uint32_t prefix[1];  // exclusive prefix of query tiles x heads [S + 1], then of key tiles x key heads
+};
+static_assert(offsetof(Plan, prefix) == kCrossBwdHeader * sizeof(uint32_t), "the header's words");
+__device__ __forceinline__ const Plan& plan_of(const uint32_t* ws) { return *reinterpret_cast<const Plan*>(ws); }
 __device__ __forceinline__ int kv_steps(const Segment& r, int group) {  // (head, query tile) pairs
   return r.used > 0 ? group * tiles_of(r.rows) : 0;
 }
-__device__ __forceinline__ int chunks_of(int steps, int most) { return max(1, min(steps, most)); }
-__device__ __forceinline__ const uint32_t* prefix_q(const uint32_t* plan) { return plan + kCrossBwdHeader; }
-__device__ __forceinline__ const uint32_t* prefix_kv(const uint32_t* plan, int S) {
-  return plan + kCrossBwdHeader + S + 1;
+// Item of a kernel -> tile and chunk.
+struct Cut {
+  uint32_t tile;
+  int chunk, chunks;
+};
+__device__ __forceinline__ Cut cut_of(uint32_t item, uint32_t whole, uint32_t chunks) {
+  if (item < whole) return Cut{item, 0, 1};
+  return Cut{whole + (item - whole) / chunks, static_cast<int>((item - whole) % chunks), static_cast<int>(chunks)};
 }
-__device__ __forceinline__ const uint32_t* prefix_tiles(const uint32_t* plan, int S) {
-  return plan + kCrossBwdHeader + 2 * (S + 1);
+// A tile of n steps is cut into at most n chunks; chunk c's steps begin at n c / chunks.
+__device__ __forceinline__ int step_at(int n, int c, int chunks) {
+  return static_cast<int>(static_cast<int64_t>(n) * c / chunks);
 }
 
 // Exclusive sum over the block (whole warps) and the total.
@@ -110,7 +127,7 @@ __device__ __forceinline__ uint32_t exclusive_scan(uint32_t v, uint32_t* s_warp,
 // One block: a warp when the segments fit its lanes (three short scans, no block barrier), else 1,024
 // threads with several segments each.
 __global__ void __launch_bounds__(kPlanThreads)
-cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws, int slots, int sms,
+cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws, int slots, uint32_t sms,
                       unsigned int* err) {
   __shared__ uint32_t s_warp[kPlanThreads / 32];
   grid_dependency_wait();
@@ -128,56 +145,64 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
     }
     return r;
   };
-  auto q_items = [&](const Segment& r) { return static_cast<uint32_t>(tiles_of(r.rows)) * seg.num_q_heads; };
+  auto q_tiles = [&](const Segment& r) { return static_cast<uint32_t>(tiles_of(r.rows)) * seg.num_q_heads; };
   auto k_tiles = [&](const Segment& r) { return static_cast<uint32_t>(tiles_of(r.keys)) * seg.num_kv_heads; };
   Segment mine{};  // this thread's only segment, when it has one
   if (chunk == 1 && lo < hi) mine = checked(lo);
   auto segment = [&](int g) { return chunk == 1 ? mine : checked(g); };
-  uint32_t nq = 0, nt = 0, work = 0, nk = 0, total_q, tiles, total_work, total_k;
+  uint32_t nq = 0, nk = 0, wq = 0, wk = 0, tiles_q, tiles_k, work_q, work_k;  // work: steps of all tiles
   for (int g = lo; g < hi; ++g) {
     const Segment r = segment(g);
-    nq += q_items(r);
-    nt += k_tiles(r);
-    work += static_cast<uint32_t>((static_cast<uint64_t>(k_tiles(r)) * kv_steps(r, group) + 3) / 4);  // in fours
+    nq += q_tiles(r);
+    nk += k_tiles(r);
+    wq += q_tiles(r) * static_cast<uint32_t>(tiles_of(r.used));
+    wk += k_tiles(r) * static_cast<uint32_t>(kv_steps(r, group));
   }
-  uint32_t at_q = exclusive_scan(nq, s_warp, total_q), at_t = exclusive_scan(nt, s_warp, tiles);
-  exclusive_scan(work, s_warp, total_work);
-  // Chunks per key tile: what makes the waves of items (of steps / c steps, and about 3 steps' time
-  // of start and end each) shortest, as far as the slots reach.
-  int most = 1;
-  if (tiles > 0) {
-    const float steps = 4.f * static_cast<float>(total_work) / static_cast<float>(tiles);
-    float best = INFINITY;
-    for (int c = 1; c <= kCrossBwdMaxChunks && (c == 1 || static_cast<int64_t>(tiles) * c <= slots); ++c) {
-      const float waves = static_cast<float>((static_cast<int64_t>(tiles) * c + sms - 1) / sms);
-      const float cost = waves * (steps / static_cast<float>(c) + 3.f);
-      if (cost < best) {
-        best = cost;
-        most = c;
-      }
-    }
-  }
-  auto kv_items = [&](const Segment& r) { return k_tiles(r) * chunks_of(kv_steps(r, group), most); };
-  for (int g = lo; g < hi; ++g) nk += kv_items(segment(g));
-  uint32_t at_k = exclusive_scan(nk, s_warp, total_k);
-  uint32_t *pq = ws + kCrossBwdHeader, *pk = pq + S + 1, *pt = pk + S + 1;
+  uint32_t at_q = exclusive_scan(nq, s_warp, tiles_q), at_k = exclusive_scan(nk, s_warp, tiles_k);
+  exclusive_scan(wq, s_warp, work_q);
+  exclusive_scan(wk, s_warp, work_k);
+  uint32_t *pq = ws + kCrossBwdHeader, *pk = pq + S + 1;
   for (int g = lo; g < hi; ++g) {
     const Segment r = segment(g);
     pq[g] = at_q;
     pk[g] = at_k;
-    pt[g] = at_t;
-    at_q += q_items(r);
-    at_k += kv_items(r);
-    at_t += k_tiles(r);
+    at_q += q_tiles(r);
+    at_k += k_tiles(r);
   }
-  if (tid == 0) {
-    pq[S] = total_q;
-    pk[S] = total_k;
-    pt[S] = tiles;
-    ws[0] = total_q;
-    ws[1] = total_k;
-    ws[2] = static_cast<uint32_t>(most);
-    ws[3] = tiles;
+  // Chunks of the tiles behind the whole waves: what makes their waves of items (of steps / c steps,
+  // and about 3 steps' time of start and end each; 2 more for the sum of several chunks) shortest, as
+  // far as the slots reach.  Lanes 0-15 weigh 1 to 16 chunks for the query tiles, 16-31 for the key
+  // tiles.
+  if (tid < 32) {
+    const bool keys = tid >= 16;
+    const uint32_t c = (tid & 15) + 1, tiles = keys ? tiles_k : tiles_q, rest = tiles % sms;
+    const float steps = tiles > 0 ? static_cast<float>(keys ? work_k : work_q) / static_cast<float>(tiles) : 0.f;
+    float cost = static_cast<float>((rest * c + sms - 1) / sms) * (steps / static_cast<float>(c) + 3.f) + (c > 1 ? 2.f : 0.f);
+    if (c > kCrossBwdMaxChunks || (c > 1 && rest * c > static_cast<uint32_t>(slots))) cost = INFINITY;
+    uint32_t best = c;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, cost, o);
+      const uint32_t other_c = __shfl_xor_sync(0xffffffffu, best, o);
+      if (other < cost || (other == cost && other_c < best)) {
+        cost = other;
+        best = other_c;
+      }
+    }
+    const uint32_t best_q = __shfl_sync(0xffffffffu, best, 0), best_k = __shfl_sync(0xffffffffu, best, 16);
+    if (tid == 0) {
+      pq[S] = tiles_q;
+      pk[S] = tiles_k;
+      Plan& p = *reinterpret_cast<Plan*>(ws);
+      p.tiles_q = tiles_q;
+      p.tiles_k = tiles_k;
+      p.whole_q = tiles_q - tiles_q % sms;
+      p.whole_k = tiles_k - tiles_k % sms;
+      p.chunks_q = best_q;
+      p.chunks_k = best_k;
+      p.items_q = p.whole_q + (tiles_q - p.whole_q) * best_q;
+      p.items_k = p.whole_k + (tiles_k - p.whole_k) * best_k;
+    }
   }
 }
 
@@ -284,13 +309,12 @@ struct KvWork {
 
 __device__ __forceinline__ KvWork decode_kv(uint32_t item, const uint32_t* __restrict__ ws, const CrossSegments& seg) {
   const int S = seg.num_segments, group = seg.num_q_heads / seg.num_kv_heads;
-  const uint32_t* prefix = prefix_kv(ws, S);
-  const int g = find_segment(prefix, S, item);
+  const Plan& plan = plan_of(ws);
+  const uint32_t* prefix = plan.prefix + S + 1;
+  const Cut cut = cut_of(item, plan.whole_k, plan.chunks_k);
+  const int g = find_segment(prefix, S, cut.tile);
   const Segment r = segment_of(seg, g);
-  const int steps = kv_steps(r, group), chunks = chunks_of(steps, static_cast<int>(ws[2])), tiles = tiles_of(r.keys);
-  int local = static_cast<int>(item - prefix[g]);
-  const int chunk = local % chunks;
-  local /= chunks;
+  const int tiles = tiles_of(r.keys), local = static_cast<int>(cut.tile - prefix[g]);
   KvWork d;
   d.more = 1;
   d.kv_head = local / tiles;
@@ -298,18 +322,19 @@ __device__ __forceinline__ KvWork decode_kv(uint32_t item, const uint32_t* __res
   d.k_row = r.k0 + kt * kTile;
   d.rows = min(kTile, r.keys - kt * kTile);
   d.used = max(0, min(kTile, r.used - kt * kTile));
-  d.first = static_cast<int>(static_cast<int64_t>(steps) * chunk / chunks);
-  d.steps = static_cast<int>(static_cast<int64_t>(steps) * (chunk + 1) / chunks) - d.first;
-  d.slot = chunks > 1 ? static_cast<int>(item) : -1;
+  const int steps = d.used > 0 ? kv_steps(r, group) : 0;  // none: zeros, from the first chunk
+  const int chunks = max(1, min(cut.chunks, steps));
+  if (cut.chunk >= chunks) {
+    d.steps = d.first = d.rows = 0;
+  } else {
+    d.first = step_at(steps, cut.chunk, chunks);
+    d.steps = step_at(steps, cut.chunk + 1, chunks) - d.first;
+  }
+  d.slot = chunks > 1 && cut.chunk < chunks ? static_cast<int>(item - plan.whole_k) : -1;
   d.head0 = d.kv_head * group;
   d.qtiles = max(1, tiles_of(r.rows));
   d.q0 = r.q0;
   d.q_end = r.q0 + r.rows;
-  if (d.used == 0) {  // no key of the tile is used: zeros, written once
-    d.steps = 0;
-    d.slot = -1;
-    if (chunk > 0) d.rows = 0;
-  }
   return d;
 }
 
@@ -383,7 +408,7 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
   grid_dependency_wait();
   launch_dependents();
   if (__syncthreads_or(a.err != nullptr && *reinterpret_cast<volatile unsigned int*>(a.err) == kErrTimeout)) return;
-  const uint32_t total = a.plan[1];
+  const uint32_t total = plan_of(a.plan).items_k;
   if (blockIdx.x >= total) return;
   if ((smem_u32(smem) & 1023u) != 0) {  // the tiles' swizzle needs it; not met on any known driver
     if (threadIdx.x == 0) record_error(a.err, kErrTimeout);
@@ -734,45 +759,55 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
   }
 }
 
-// Sums the chunks of every cut key tile, in chunk order: 16 rows of one tile's dV or dK to a unit.
+// Sums the chunks of every cut tile, in chunk order: 16 rows of one tile's dV, dK or dQ to a unit.
 template <int D>
 __global__ void __launch_bounds__(256)
-cross_dkv_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
+cross_bwd_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
   grid_dependency_wait();
   launch_dependents();
   if (a.err != nullptr && *reinterpret_cast<const volatile unsigned int*>(a.err) == kErrTimeout) return;
-  const int most = static_cast<int>(a.plan[2]);
-  if (most <= 1) return;  // nothing was cut
+  const Plan& plan = plan_of(a.plan);
   const int S = a.seg.num_segments, group = a.seg.num_q_heads / a.seg.num_kv_heads;
-  constexpr int kParts = 8, kRows = kTile / kParts;
-  const uint32_t units = a.plan[3] * 2 * kParts;
-  for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const uint32_t tile = u / (2 * kParts);
-    const int which = u / kParts % 2, r0 = u % kParts * kRows;
-    const int g = find_segment(prefix_tiles(a.plan, S), S, tile);
+  constexpr uint32_t kParts = 8;
+  constexpr int kRows = kTile / kParts;
+  const uint32_t units_k = plan.chunks_k > 1 ? (plan.tiles_k - plan.whole_k) * 2 * kParts : 0;
+  const uint32_t units_q = plan.chunks_q > 1 ? (plan.tiles_q - plan.whole_q) * kParts : 0;
+  for (uint32_t u = blockIdx.x; u < units_k + units_q; u += gridDim.x) {
+    const bool keys = u < units_k;
+    const uint32_t v = keys ? u : u - units_k, per_tile = keys ? 2 * kParts : kParts;
+    const uint32_t index = v / per_tile;  // of the tile behind the whole waves
+    const int which = keys ? static_cast<int>(v / kParts % 2) : 0, r0 = static_cast<int>(v % kParts) * kRows;
+    const uint32_t* prefix = keys ? plan.prefix + S + 1 : plan.prefix;
+    const uint32_t tile = (keys ? plan.whole_k : plan.whole_q) + index;
+    const int most = static_cast<int>(keys ? plan.chunks_k : plan.chunks_q);
+    const int g = find_segment(prefix, S, tile);
     const Segment r = segment_of(a.seg, g);
-    const int chunks = chunks_of(kv_steps(r, group), most), tiles = tiles_of(r.keys);
-    const uint32_t local = tile - prefix_tiles(a.plan, S)[g];
-    const int kt = static_cast<int>(local) % tiles, kv_head = static_cast<int>(local) / tiles;
-    if (chunks == 1 || kt * kTile >= r.used) continue;  // written already
-    const size_t slot = prefix_kv(a.plan, S)[g] + static_cast<size_t>(local) * chunks;
-    const float* part = a.partials + (slot * 2 + which) * kTile * D;
-    const int64_t stride = which == 0 ? a.dv_stride : a.dk_stride;
-    __nv_bfloat16* out = (which == 0 ? a.dv : a.dk) + (static_cast<int64_t>(r.k0) + kt * kTile) * stride + kv_head * D;
-    const int rows = min(kTile, r.keys - kt * kTile);
+    const int tiles = tiles_of(keys ? r.keys : r.rows), local = static_cast<int>(tile - prefix[g]);
+    const int head = local / tiles, row_tile = local % tiles * kTile;
+    const int steps = keys ? (row_tile < r.used ? kv_steps(r, group) : 0) : tiles_of(r.used);
+    const int chunks = max(1, min(most, steps));
+    if (chunks == 1) continue;  // written already
+    const size_t slot = static_cast<size_t>(index) * most;
+    const size_t step = keys ? 2 * kTile * D : kTile * D;
+    const float* part = keys ? a.partials + slot * step + static_cast<size_t>(which) * kTile * D
+                             : a.partials_q + slot * step;
+    const int64_t stride = keys ? (which == 0 ? a.dv_stride : a.dk_stride) : a.dq_stride;
+    __nv_bfloat16* out = (keys ? (which == 0 ? a.dv : a.dk) : a.dq) +
+                         (static_cast<int64_t>(keys ? r.k0 : r.q0) + row_tile) * stride + head * D;
+    const int rows = min(kTile, (keys ? r.keys : r.rows) - row_tile);
     for (int i = threadIdx.x; i < kRows * (D / 8); i += 256) {
       const int row = r0 + i / (D / 8), col = i % (D / 8) * 8;
       if (row >= rows) continue;
-      float s[8] = {};
-#pragma unroll 4
+      float f[8] = {};
+#pragma unroll 8
       for (int c = 0; c < chunks; ++c) {
-        const float4* src = reinterpret_cast<const float4*>(part + static_cast<size_t>(c) * 2 * kTile * D + row * D + col);
+        const float4* src = reinterpret_cast<const float4*>(part + c * step + row * D + col);
         const float4 x = src[0], y = src[1];
-        s[0] += x.x; s[1] += x.y; s[2] += x.z; s[3] += x.w;
-        s[4] += y.x; s[5] += y.y; s[6] += y.z; s[7] += y.w;
+        f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+        f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
       }
       *reinterpret_cast<uint4*>(out + row * stride + col) =
-          make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]), pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+          make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
     }
   }
 }
@@ -782,24 +817,30 @@ struct QWork {
   int more;
   int head, kv_head;
   int q_row, q_end;
-  int k_row, nkv, last_keys;  // nkv 0: no keys, dq = 0 (such items are not handed on)
+  int k_row, nkv, last_keys;  // nkv 0: no keys (such items are not handed on)
+  int slot;                   // the chunk's sum goes to this slot; -1: straight to dq
 };
 
 __device__ __forceinline__ QWork decode_q(uint32_t item, const uint32_t* __restrict__ ws, const CrossSegments& seg) {
   const int S = seg.num_segments, group = seg.num_q_heads / seg.num_kv_heads;
-  const uint32_t* prefix = prefix_q(ws);
-  const int g = find_segment(prefix, S, item);
+  const Plan& plan = plan_of(ws);
+  const Cut cut = cut_of(item, plan.whole_q, plan.chunks_q);
+  const int g = find_segment(plan.prefix, S, cut.tile);
   const Segment r = segment_of(seg, g);
-  const int tiles = tiles_of(r.rows), local = static_cast<int>(item - prefix[g]);
+  const int tiles = tiles_of(r.rows), local = static_cast<int>(cut.tile - plan.prefix[g]);
+  const int steps = tiles_of(r.used), chunks = max(1, min(cut.chunks, steps));
   QWork d;
   d.more = 1;
   d.head = local / tiles;
   d.kv_head = d.head / group;
   d.q_row = r.q0 + local % tiles * kTile;
-  d.q_end = r.q0 + r.rows;
-  d.k_row = r.k0;
-  d.nkv = tiles_of(r.used);
-  d.last_keys = r.used - (d.nkv - 1) * kTile;
+  d.q_end = cut.chunk < chunks ? r.q0 + r.rows : d.q_row;  // a chunk past the last has no rows
+  const int first = step_at(steps, min(cut.chunk, chunks), chunks);
+  const int end = step_at(steps, min(cut.chunk + 1, chunks), chunks);
+  d.k_row = r.k0 + first * kTile;
+  d.nkv = end - first;
+  d.last_keys = min(kTile, r.used - (end - 1) * kTile);
+  d.slot = chunks > 1 ? static_cast<int>(item - plan.whole_q) : -1;
   return d;
 }
 
@@ -878,7 +919,7 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
   grid_dependency_wait();
   launch_dependents();
   if (__syncthreads_or(a.err != nullptr && *reinterpret_cast<volatile unsigned int*>(a.err) == kErrTimeout)) return;
-  const uint32_t total = a.plan[0];
+  const uint32_t total = plan_of(a.plan).items_q;
   if (blockIdx.x >= total) return;
   if ((smem_u32(smem) & 1023u) != 0) {  // the tiles' swizzle needs it; not met on any known driver
     if (threadIdx.x == 0) record_error(a.err, kErrTimeout);
@@ -1223,6 +1264,7 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
       if (!ok) break;
       tc_fence_after();
       // epilogue: each warpgroup stores half the columns
+      float* part = a.partials_q + (static_cast<size_t>(max(d.slot, 0)) * kTile + row) * D;
       const int odd = lane & 1, r0 = d.q_row + row - odd;
       __nv_bfloat16* p0 = a.dq + static_cast<int64_t>(r0) * a.dq_stride + d.head * D + 16 * odd;
 #pragma unroll 1
@@ -1235,7 +1277,15 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
           tc_fence_before();
           arrive_warp(acc_empty);
         }
-        store_columns(x, a.scale, p0 + c0, p0 + a.dq_stride + c0, r0 < d.q_end, r0 + 1 < d.q_end, a.wide);
+        if (d.slot >= 0) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4*>(part + c0 + 4 * c) =
+                make_float4(__uint_as_float(x[4 * c]) * a.scale, __uint_as_float(x[4 * c + 1]) * a.scale,
+                            __uint_as_float(x[4 * c + 2]) * a.scale, __uint_as_float(x[4 * c + 3]) * a.scale);
+        } else {
+          store_columns(x, a.scale, p0 + c0, p0 + a.dq_stride + c0, r0 < d.q_end, r0 + 1 < d.q_end, a.wide);
+        }
       }
       d = nxt;
     }
@@ -1259,7 +1309,7 @@ cudaError_t launch(const CrossBwdArgs& a, cudaStream_t stream) {
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return cudaErrorInvalidDevice;
   e = launch_programmatic(cross_bwd_plan_kernel, dim3(1), dim3(a.seg.num_segments <= 32 ? 32 : kPlanThreads), 0, stream,
-                          a.seg, a.plan, a.slots, sms, a.err);
+                          a.seg, a.plan, a.slots, static_cast<uint32_t>(sms), a.err);
   if (e != cudaSuccess) return e;
   if (a.seg.capacity_q > 0) {
     e = launch_programmatic(cross_dq_kernel<D>, dim3(sms), dim3(kDqThreads), QCfg<D>::kSmemBytes, stream, a);
@@ -1268,8 +1318,9 @@ cudaError_t launch(const CrossBwdArgs& a, cudaStream_t stream) {
   if (a.seg.capacity_k > 0) {
     e = launch_programmatic(cross_dkv_kernel<D>, dim3(sms), dim3(kThreads), KvCfg<D>::kSmemBytes, stream, a);
     if (e != cudaSuccess) return e;
-    e = launch_programmatic(cross_dkv_sum_kernel<D>, dim3(4 * sms), dim3(256), 0, stream, a);
   }
+  if (a.slots > 0)
+    e = launch_programmatic(cross_bwd_sum_kernel<D>, dim3(2 * sms), dim3(256), 0, stream, a);
   return e;
 }
 

@@ -191,12 +191,11 @@ struct CrossArgs {
 };
 cudaError_t launch_cross_attn(const CrossArgs& a, int head_dim, cudaStream_t stream);
 
-// Gradient.  Work plan: header words, then the prefixes of the two product kernels' items and of key
-// tiles.  A key tile's
-// query range may be cut into up to kCrossBwdMaxChunks chunks, whose partial sums take a slot each
-// (two tiles of 128 x head_dim fp32).
-constexpr int kCrossBwdHeader = 4;
-constexpr int kCrossBwdMaxSlots = 1216;  // 8 x 152
+// Gradient.  Work plan: header words, then the prefixes of query and key tiles.  A tile of the last,
+// partly filled wave may be cut into up to kCrossBwdMaxChunks chunks, whose partial sums take a slot
+// each: two tiles of 128 x head_dim fp32 for a key tile, one for a query tile.
+constexpr int kCrossBwdHeader = 8;
+constexpr int kCrossBwdMaxSlots = 608;  // 4 x 152
 constexpr int kCrossBwdMaxChunks = 16;
 struct CrossBwdArgs {
   CUtensorMap tmap_q, tmap_k, tmap_v, tmap_do;
@@ -209,28 +208,36 @@ struct CrossBwdArgs {
   float scale;
   uint32_t* plan;
   float* delta;     // [num_q_heads, capacity_q]
-  float* partials;  // slots x 2 x 128 x head_dim
+  float* partials;    // slots x 2 x 128 x head_dim: dV, dK
+  float* partials_q;  // slots x 128 x head_dim: dQ
   int slots;
   unsigned int* err;
   uint64_t wait_limit_ns;
   uint32_t stall_after_tiles;
 };
 struct CrossBwdWorkspace {
-  size_t delta, partials, bytes;  // offsets (the plan is at 0) and the whole
+  size_t delta, partials, partials_q, bytes;  // offsets (the plan is at 0) and the whole
   int slots;
 };
 inline CrossBwdWorkspace cross_bwd_workspace(const CrossSegments& s, int head_dim) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   CrossBwdWorkspace w;
-  w.delta = up((kCrossBwdHeader + 3 * (static_cast<size_t>(s.num_segments) + 1)) * sizeof(uint32_t));
+  w.delta = up((kCrossBwdHeader + 2 * (static_cast<size_t>(s.num_segments) + 1)) * sizeof(uint32_t));
   w.partials = w.delta + up(static_cast<size_t>(s.num_q_heads) * s.capacity_q * sizeof(float));
-  // no more slots than chunks of all key tiles the capacity allows
-  const int64_t tiles = (static_cast<int64_t>(s.capacity_k) / 128 + s.num_segments) * s.num_kv_heads;
-  const int64_t steps = static_cast<int64_t>(s.num_q_heads / s.num_kv_heads) * ((s.max_seqlen_q + 127) / 128);
-  const int64_t chunks = steps < kCrossBwdMaxChunks ? steps : kCrossBwdMaxChunks;
-  const int64_t all = chunks > 1 ? tiles * chunks : 0;  // one chunk goes straight to the gradients
+  // no more slots than chunks of all tiles that the capacities allow
+  const int64_t k_tiles = (static_cast<int64_t>(s.capacity_k) / 128 + s.num_segments) * s.num_kv_heads;
+  const int64_t q_tiles = (static_cast<int64_t>(s.capacity_q) / 128 + s.num_segments) * s.num_q_heads;
+  const int64_t k_steps = static_cast<int64_t>(s.num_q_heads / s.num_kv_heads) * ((s.max_seqlen_q + 127) / 128);
+  const int64_t q_steps = (s.capacity_k + 127) / 128;
+  auto slots = [](int64_t tiles, int64_t steps) {
+    const int64_t chunks = steps < kCrossBwdMaxChunks ? steps : kCrossBwdMaxChunks;
+    return chunks > 1 ? tiles * chunks : 0;  // one chunk goes straight to the gradients
+  };
+  const int64_t a = slots(k_tiles, k_steps), b = slots(q_tiles, q_steps), all = a > b ? a : b;
   w.slots = static_cast<int>(all < kCrossBwdMaxSlots ? all : kCrossBwdMaxSlots);
-  w.bytes = w.partials + static_cast<size_t>(w.slots) * 2 * 128 * head_dim * sizeof(float);
+  const size_t slot = static_cast<size_t>(w.slots) * 128 * head_dim * sizeof(float);
+  w.partials_q = w.partials + 2 * slot;
+  w.bytes = w.partials_q + slot;
   return w;
 }
 cudaError_t launch_cross_bwd(const CrossBwdArgs& a, int head_dim, cudaStream_t stream);

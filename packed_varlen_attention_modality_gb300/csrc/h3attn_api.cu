@@ -701,6 +701,7 @@ h3_status h3_varlen_cross_attn_bwd(const h3_cross_attn_desc* d, const void* dout
   a.plan = reinterpret_cast<uint32_t*>(base);
   a.delta = reinterpret_cast<float*>(base + w.delta);
   a.partials = reinterpret_cast<float*>(base + w.partials);
+  a.partials_q = reinterpret_cast<float*>(base + w.partials_q);
   a.slots = w.slots;
   a.err = device_error_ptr();
   a.wait_limit_ns = h3::wait_limit_ns();
