@@ -586,7 +586,8 @@ H3_API h3_status h3_sp_exchange_plan(const int32_t grid[3], const int32_t win[3]
  * in force before the call. */
 H3_API uint64_t h3_set_wait_limit_ns(uint64_t nanoseconds);
 
-/* The key/value loader of each attention CTA issues at most `tiles` tiles and then stops, as if
+/* The key/value loader of each attention CTA (packed, window, VSA and cross attention, and the loaders
+ * of the cross attention gradient) issues at most `tiles` tiles and then stops, as if
  * it had stalled, so the waits of the warps that consume them run out; negative (the default)
  * restores normal operation.  Nothing is read or written out of bounds and every wait still ends
  * by its limit.  Returns the previous setting. */

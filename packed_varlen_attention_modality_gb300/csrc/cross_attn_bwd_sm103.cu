@@ -22,8 +22,11 @@
 // kernel of its own for it reads do once more: 59 us of a text case's 589).
 // In dQ the products come from two warps (S and dP from one, dQ from the other): a warp's polls queue
 // behind its own products, so one warp alone leaves the tensor core idle at each wait (4,096 x 4,096 x
-// 24 x 128: 236 us, 290 with one).  In dK/dV the four products of a step alternate between two chains
-// and one warp keeps them in that order; two warps measured slower there (350 us against 295).
+// 24 x 128: 290 us with one, 236 with two, 207 now).  In dK/dV the four products of a step alternate between two chains
+// and one warp keeps them in that order; two warps measured slower there (350 us against 295, now 262).
+// What bounds both: the chain scores -> exponential -> dS -> product of one tile, which keeps the tensor
+// core 66 % busy in dK/dV, 63 % in dQ, and 47 % in dQ when key lists are five tiles, where reading dQ out
+// of TMEM between two items is not hidden (the fourth warpgroup cannot do it: it has delta to compute).
 //
 // P and dS are rounded to bf16 for the tensor core (half a step, 2^-8 relative at most); everything
 // else is fp32 until the gradients are rounded once.  Rows and keys past a segment's end are zeroed

@@ -18,8 +18,14 @@
 //   - items are decoded one ahead, and queries and keys have a producer each, so neither waits on
 //     the other's ring;
 //   - a last key tile is multiplied only as far as it holds keys (in steps of 16).
-// With all of it in the softmax warpgroups and one producer (the packed self-attention kernel's
-// structure), 58,758 rows x 558 keys x 40 heads x 128 took 787 us.
+// 58,758 rows x 558 keys x 40 heads x 128 take 545 us so (1,235 TFLOP/s); with all of it in the softmax
+// warpgroups and one producer (the packed self-attention kernel's structure) they took 787 us.  A step
+// takes some 2,900 cycles (2,048 of tensor work: the chain scores -> softmax -> product of each tile sets
+// the pace), the step between two items 5,000: that is the first softmax of an item waiting for the last
+// product of the one before, and bounds short key lists.  Tried and slower: both tiles' softmax by all
+// eight warps, half a row each (581 us); one copy of the step's code for both kinds (615 us); the value
+// rows past the keys zeroed by a warp of their own (563 us); two warps issuing products (tiles fall in
+// phase).
 //
 // Warp roles (512 threads; registers moved with setmaxnreg):
 //   warps 0-3 / 4-7   softmax of query tile 0 / 1: thread r owns row r = TMEM lane r
@@ -31,7 +37,7 @@
 // Keys past the segment's end are masked to -inf by select and the value rows PV reads past it are
 // zeroed in shared memory, so NaN/Inf there cannot leak.  A segment without keys takes one tile
 // whose keys are all masked: its rows come out as 0 with an LSE of -inf.
-// P is rounded to bf16 for the tensor core (half a step, 2^-9 of each weight on average); scores,
+// P is rounded to bf16 for the tensor core (half a step, 2^-8 relative at most); scores,
 // running max and sum, and O stay fp32, and the result is rounded to bf16 once.
 // Every wait is bounded; a wait that runs out records a timeout and unwinds the CTA.
 #include <cuda_bf16.h>
