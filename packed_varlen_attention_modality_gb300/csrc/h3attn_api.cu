@@ -67,6 +67,24 @@ EncodeTiledFn encode_tiled_fn() {
   return fn;
 }
 
+// A bf16 map of `rank` dimensions with 128-byte swizzle; elements outside read as zero.  The driver wants a
+// context that is current in the calling thread, and a thread that has made no such runtime call yet (a
+// worker, an engine's backward thread) has none: it then gets its device's and the map is made again.
+bool encode_bf16_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  auto encode = [&] {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
+}
+
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -74,19 +92,13 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // row_stride: elements between rows (0: heads * head_dim).
 bool make_qkv_map(CUtensorMap* m, const void* base, int rows, int heads, int head_dim,
                   int64_t row_stride = 0) {
-  EncodeTiledFn enc = encode_tiled_fn();
-  if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
                                  (row_stride > 0 ? static_cast<cuuint64_t>(row_stride)
                                                  : static_cast<cuuint64_t>(heads) * head_dim) * 2};
   const cuuint32_t box[3] = {64, 1, 128};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_bf16_map(m, base, 3, dims, strides, box);
 }
 
 // 5-D view {D, heads, W, H, T} of a bf16 [T*H*W, heads, D] tensor in row-major token order; box
@@ -94,8 +106,6 @@ bool make_qkv_map(CUtensorMap* m, const void* base, int rows, int heads, int hea
 // outside the grid (edge windows) read as zero.
 bool make_window_map(CUtensorMap* m, const void* base, const int32_t grid[3], const int32_t win[3],
                      int frames, int heads, int head_dim) {
-  EncodeTiledFn enc = encode_tiled_fn();
-  if (enc == nullptr) return false;
   const cuuint64_t row = static_cast<cuuint64_t>(heads) * head_dim * 2;
   const cuuint64_t dims[5] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(grid[2]), static_cast<cuuint64_t>(grid[1]),
@@ -104,11 +114,7 @@ bool make_window_map(CUtensorMap* m, const void* base, const int32_t grid[3], co
                                  row * grid[2] * grid[1]};
   const cuuint32_t box[5] = {64, 1, static_cast<cuuint32_t>(win[2]), static_cast<cuuint32_t>(win[1]),
                              static_cast<cuuint32_t>(frames)};
-  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_bf16_map(m, base, 5, dims, strides, box);
 }
 
 bool device_is_sm103() {
