@@ -55,10 +55,17 @@ constexpr int kRegsSoftmax = 176, kRegsEpilogue = 80, kRegsOther = 80;
 static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOther == 65536 / 128, "the split of the registers at launch");
 constexpr int kTmemCols = 512, kColO = 0, kColS = 256;
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the running max grows by > 2^8
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;   // at most: kSortMax when the segments are that few
 constexpr int kSortMax = 256;         // segments ordered by keys up to this count
 constexpr int kHeader = kAttnWsHeaderWords;
+// The last, partly filled wave, in steps of a key tile (one query tile alone takes nearly as long as two:
+// the chain of each sets the pace).  An item's start and end take about two, joining chunks (partial
+// results through memory, a kernel with something to do) about eight: 2,048 x 2,048 x 24 heads, 16 steps
+// whole or 11 in shares, take 64 us whole, 55 us cut; 3 x 300 x 2,500 x 40 heads, 20 or 16 with the items of
+// the last wave short, 81 us either way.
+constexpr uint32_t kCostItem = 2, kCostJoin = 8;
 constexpr int kSplitMinTiles = 8;     // cut only items of at least 8 key tiles
+constexpr int kSplitMinChunk = 3;     // into chunks of at least 3
 constexpr int kSplitMaxChunks = 64;
 
 __host__ __device__ constexpr int key_tiles(int keys) {
@@ -72,7 +79,8 @@ struct CrossEntry {
   int chunk, chunks;  // chunks == 1: whole
 };
 static_assert(sizeof(CrossEntry) == 8 * sizeof(int32_t), "entries are 8 words");
-__host__ __device__ constexpr size_t split_items_offset() {  // first entries of the cut items
+// first entries of the cut items (fewer than a wave), then the first entry of each CTA and their number
+__host__ __device__ constexpr size_t split_items_offset() {
   return static_cast<size_t>(kSplitMaxEntries) * sizeof(CrossEntry);
 }
 __host__ __device__ constexpr size_t split_partials_offset() {
@@ -112,7 +120,7 @@ __device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s
   __syncthreads();
   uint32_t before = 0, all = 0;
 #pragma unroll 1
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
     if (w < warp) before += s_warp[w];
     all += s_warp[w];
   }
@@ -121,15 +129,21 @@ __device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s
 }
 
 // Plan: segment order and item prefix, and the entries of the last wave.  Words of ws: [0] cut
-// items, [1] work items, [2] whole items before the last wave, [3] its entries, then the order
-// [S] and the exclusive prefix [S + 1].
+// items, [1] unused, [2] whole items before the last wave, [3] its entries, then the order [S] and the
+// exclusive prefix [S + 1].
+// The last wave's work is laid end to end and dealt to the CTAs in equal shares, so an item is cut where
+// a share ends (four requests of 213 to 292 rows x 12,369 to 13,961 keys x 24 heads, 120 items of about 100
+// key tiles on 152 CTAs: 163 us; an item per CTA 183 us; the same without the heads apart 188 us, as each
+// row of K and V then comes from memory in pieces at different times).
 __global__ void __launch_bounds__(kPlanThreads)
 cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws,
                   uint8_t* __restrict__ split_area, int wave, unsigned int* err) {
   __shared__ int s_rows[kSortMax], s_keys[kSortMax], s_order[kSortMax];
   __shared__ uint32_t s_prefix[kSortMax + 1];
   __shared__ uint32_t s_warp[kPlanThreads / 32];
-  __shared__ uint32_t s_cut;
+  __shared__ uint32_t s_cut, s_most;
+  __shared__ uint2 s_item[kSplitMaxEntries / 2];  // of the last wave: where it starts, its key tiles
+  __shared__ uint4 s_at[kSplitMaxEntries / 2];    // of each CTA: where its share starts, cuts before it
   grid_dependency_wait();
   launch_dependents();
   const int S = seg.num_segments, tid = threadIdx.x;
@@ -156,7 +170,7 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
     const int rows = sorted ? s_rows[s_order[i]] : checked_segment(seg, i, err).x;
     return static_cast<uint32_t>(pairs_of(rows, group)) * seg.num_kv_heads;
   };
-  const int chunk = (S + kPlanThreads - 1) / kPlanThreads;
+  const int chunk = (S + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
   const int lo = min(S, tid * chunk), hi = min(S, lo + chunk);
   uint32_t local = 0, total;
   for (int i = lo; i < hi; ++i) local += items_at(i);
@@ -172,61 +186,103 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
     if (sorted) s_prefix[S] = total;
   }
   const uint32_t tail = total / wave * wave, R = total - tail;
-  if (split_area == nullptr || !sorted || R == 0 || R > static_cast<uint32_t>(kSplitMaxEntries)) {
+  if (split_area == nullptr || !sorted || R == 0 || 2 * wave + 1 > kSplitMaxEntries) {
     if (tid == 0) {
       ws[0] = 0;
-      ws[1] = ws[2] = total;
+      ws[2] = total;
       ws[3] = 0;
     }
     return;
   }
-  __syncthreads();  // the prefix is complete
+  const bool mine = tid < static_cast<int>(R);  // fewer than a wave
+  if (tid == 0) s_cut = s_most = 0u;
+  __syncthreads();  // also: the prefix is complete
   CrossEntry e{};
   int nkv = 0;
-  if (tid < static_cast<int>(R)) {
-    const uint32_t item = tail + tid;
+  uint32_t cost = 0;
+  // Key heads apart, a group of CTAs each, where no whole wave comes before: then the heads of a segment
+  // are cut alike and read the same key rows at the same time.
+  const int heads = seg.num_kv_heads;
+  const bool apart = tail == 0 && heads <= wave;
+  const int groups = apart ? heads : 1, members = wave / groups;  // of CTAs; CTAs in a group
+  const uint32_t per = R / groups;                                // items of a group
+  if (mine) {
+    const uint32_t item = apart ? tid % per * heads : tail + tid;  // (prefixes count all heads)
     int l = 0, h = S - 1;
     while (l < h) {
       const int mid = (l + h + 1) >> 1;
       if (s_prefix[mid] <= item) l = mid; else h = mid - 1;
     }
     e.segment = s_order[l];
-    const int pairs = pairs_of(s_rows[e.segment], group);
+    const int rows = s_rows[e.segment], pairs = pairs_of(rows, group);
     const int loc = static_cast<int>(item - s_prefix[l]);
-    e.kv_head = loc / pairs;
-    e.pair = loc % pairs;
+    e.kv_head = apart ? tid / static_cast<int>(per) : loc / pairs;
+    e.pair = apart ? loc / heads : loc % pairs;
     nkv = key_tiles(s_keys[e.segment]);
+    cost = static_cast<uint32_t>(nkv) + kCostItem;  // a wave's sum fits 32 bits
+    atomicMax(&s_most, cost);
   }
-  // The wave's long items are cut so that their chunks about fill one round of its CTAs, each of
-  // at least 4 key tiles.
-  const bool longish = nkv >= kSplitMinTiles;
-  uint32_t n_long, entries;
-  block_exclusive_scan(longish ? 1u : 0u, s_warp, n_long);
-  const int want = n_long > 0 ? min(kSplitMaxChunks, wave / static_cast<int>(n_long)) : 1;
-  int c = tid < static_cast<int>(R) ? (longish ? max(1, min(want, nkv / 4)) : 1) : 0;
-  uint32_t first = block_exclusive_scan(static_cast<uint32_t>(c), s_warp, entries);
-  if (entries > static_cast<uint32_t>(kSplitMaxEntries)) {  // more than the area holds: stay whole
-    c = tid < static_cast<int>(R) ? 1 : 0;
-    first = static_cast<uint32_t>(tid);
-    entries = R;
-  }
-  if (tid == 0) s_cut = 0u;
+  uint32_t all;
+  const uint32_t start = block_exclusive_scan(cost, s_warp, all);  // (its barriers also order s_most)
+  if (mine) s_item[tid] = make_uint2(start, static_cast<uint32_t>(nkv));
   __syncthreads();
-  if (c > 1)  // listed for the merge; the list's order is immaterial
-    reinterpret_cast<uint32_t*>(split_area + split_items_offset())[atomicAdd(&s_cut, 1u)] = first;
-  __syncthreads();
-  e.first = static_cast<int>(first);
-  e.chunks = c;
-  for (e.chunk = 0; e.chunk < c; ++e.chunk) {
-    e.kv0 = static_cast<int>(static_cast<int64_t>(nkv) * e.chunk / c);
-    e.kv1 = static_cast<int>(static_cast<int64_t>(nkv) * (e.chunk + 1) / c);
-    reinterpret_cast<CrossEntry*>(split_area)[first + e.chunk] = e;
+  // a CTA's share; no cut where whole items end as soon as the shares and their joining would
+  const uint32_t whole = all / groups;  // a group's
+  uint32_t share = max((whole + members - 1) / members, s_most / (kSplitMaxChunks - 4) + 1);
+  share = max(share, 2u * kSplitMinChunk);
+  const bool cut = s_most > share + kCostJoin;
+  // CTA k starts in item at.x, at its key tile at.y (0: at its start)
+  uint2 at = make_uint2(R, 0u);
+  const uint32_t from = tid / members * whole, into = share * (tid % members);
+  if (tid < groups * members && cut) {
+    const uint32_t x = from + min(into, whole);
+    int l = 0, h = static_cast<int>(R) - 1;
+    while (l < h) {
+      const int mid = (l + h + 1) >> 1;
+      if (s_item[mid].x <= x) l = mid; else h = mid - 1;
+    }
+    const uint32_t n = s_item[l].y, j = min(n, x - s_item[l].x);
+    const bool inside = n >= static_cast<uint32_t>(kSplitMinTiles) && j >= static_cast<uint32_t>(kSplitMinChunk) &&
+                        j + kSplitMinChunk <= n;
+    at = inside ? make_uint2(l, j) : make_uint2(2 * j < n ? l : l + 1, 0u);
+  } else if (!cut) {
+    at.x = min(static_cast<uint32_t>(tid), R);
   }
+  uint32_t cuts;
+  const uint32_t before = block_exclusive_scan(tid < wave && at.y > 0 ? 1u : 0u, s_warp, cuts);
+  uint32_t* items = reinterpret_cast<uint32_t*>(split_area + split_items_offset());
+  if (tid < wave) {
+    s_at[tid] = make_uint4(at.x, at.y, before, 0u);
+    items[wave + tid] = at.x + before + (at.y > 0 ? 1u : 0u);
+  }
+  if (tid == 0) items[2 * wave] = R + cuts;
+  __syncthreads();
+  if (mine) {
+    // the cuts inside this item, in order: CTAs whose share starts inside it
+    uint32_t k = cut ? start / whole * members + start % whole / share : static_cast<uint32_t>(wave);
+    while (k < static_cast<uint32_t>(wave) && s_at[k].x < static_cast<uint32_t>(tid)) ++k;
+    const uint32_t earlier = k < static_cast<uint32_t>(wave) ? s_at[k].z : (cut ? cuts : 0u);
+    uint32_t last = k;
+    int c = 1;
+    for (; last < static_cast<uint32_t>(wave) && s_at[last].x == static_cast<uint32_t>(tid); ++last)
+      c += s_at[last].y > 0;
+    const uint32_t first = tid + earlier;
+    if (c > 1) items[atomicAdd(&s_cut, 1u)] = first;  // listed for the merge; the list's order is immaterial
+    e.first = static_cast<int>(first);
+    e.chunks = c;
+    e.kv0 = 0;
+    for (e.chunk = 0; e.chunk < c; ++e.chunk, ++k) {
+      while (k < last && s_at[k].y == 0) ++k;
+      e.kv1 = k < last ? static_cast<int>(s_at[k].y) : nkv;
+      reinterpret_cast<CrossEntry*>(split_area)[first + e.chunk] = e;
+      e.kv0 = e.kv1;
+    }
+  }
+  __syncthreads();
   if (tid == 0) {
     ws[0] = s_cut;
-    ws[1] = tail + entries;
     ws[2] = tail;
-    ws[3] = entries;
+    ws[3] = R + cuts;
   }
 }
 
@@ -359,7 +415,15 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
   // a timeout recorded earlier and not read yet: leave at once, all threads together
   if (__syncthreads_or(err != nullptr && *reinterpret_cast<volatile unsigned int*>(err) == kErrTimeout))
     return;
-  if (blockIdx.x >= ws[1]) return;
+  // this CTA's items: every gridDim.x-th of the whole ones, then its entries of the last wave
+  const uint32_t whole = ws[2];
+  uint32_t entry = 0, entry_end = 0;
+  if (ws[3] > 0) {
+    const uint32_t* firsts = reinterpret_cast<const uint32_t*>(split_area + split_items_offset()) + gridDim.x;
+    entry = firsts[blockIdx.x];
+    entry_end = firsts[blockIdx.x + 1];
+  }
+  if (blockIdx.x >= whole && entry == entry_end) return;
 
   if (warp == 12 && lane == 0) {
     tma_prefetch_desc(&tmap_q);
@@ -445,14 +509,14 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
       for (uint32_t i = 0; i < SV && i < vt; ++i) mbar_wait(bar_vfull((vt - 1 - i) % SV), ((vt - 1 - i) / SV) & 1);
     } else if (warp == 15) {
       // ================= scheduler and query producer =================
-      const uint32_t total = ws[1];
       const uint64_t pol_stream = l2_policy_evict_first();
       uint32_t qn[2] = {0u, 0u};
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const uint32_t item = blockIdx.x + static_cast<uint32_t>(k) * gridDim.x;
         CrossWork d{};
-        if (item < total) d = decode(item, ws, seg, split_area);
+        if (item < whole) d = decode(item, ws, seg, split_area);
+        else if (entry < entry_end) d = decode(whole + entry++, ws, seg, split_area);
         ok = wait_long(bar_wempty(k & 1), ((k >> 1) & 1) ^ 1);
         if (!ok) break;
         if (lane == 0) {
@@ -669,18 +733,18 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         const uint32_t o_addr = tmem + lane_base + kColO + 128 * t;
         if (d.partial >= 0) {
           float* mine = reinterpret_cast<float*>(split_area + split_partials_offset()) +
-                        (static_cast<size_t>(d.partial) * 2 + t) * kPartial<D>;
+                        (static_cast<size_t>(d.partial) * 2 + t) * kPartial<D> + static_cast<size_t>(row) * D;
+          const bool sectors = (reinterpret_cast<uintptr_t>(mine) & 31u) == 0;
 #pragma unroll 1
           for (int c0 = 0; c0 < D; c0 += 32) {
             uint32_t r[32];
             tmem_ld32(o_addr + c0, r);
             tmem_ld_wait();
             tmem_reg_fence<32>(r);
-            float4* dst = reinterpret_cast<float4*>(mine + static_cast<size_t>(row) * D + c0);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              dst[c] = make_float4(__uint_as_float(r[4 * c]) * inv_l, __uint_as_float(r[4 * c + 1]) * inv_l,
-                                   __uint_as_float(r[4 * c + 2]) * inv_l, __uint_as_float(r[4 * c + 3]) * inv_l);
+            for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * inv_l);
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) st_global_32(mine + c0 + c, r + c, sectors);
           }
           tc_fence_before();
           arrive_warp(bar_oempty(t));
@@ -855,6 +919,7 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
 // A unit is 16 rows of one tile; memory-bound and short (the partials are in L2).
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 16;
+static_assert(kMergeThreads == 16 * kMergeRows, "16 lanes to a row");
 constexpr int kMergeUnits = 2 * (kBlockM / kMergeRows);
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
@@ -882,18 +947,23 @@ cross_merge_kernel(const uint32_t* __restrict__ ws, const uint8_t* __restrict__ 
     if (tile >= per_head * group || row0 >= seg_end) continue;  // the whole CTA
     auto part = [&](int ch) { return parts + (static_cast<size_t>(e + ch) * 2 + t) * kPartial<D>; };
     __syncthreads();  // the previous unit's weights have been used
-    if (threadIdx.x < kMergeRows) {
-      const int r = threadIdx.x;
+    {  // 16 lanes to a row
+      const int r = threadIdx.x / 16, lane16 = threadIdx.x % 16;
       float mx = -INFINITY, den = 0.f;
-      for (int ch = 0; ch < en.chunks; ++ch) {
+      for (int ch = lane16; ch < en.chunks; ch += 16) {
         const float v = part(ch)[static_cast<size_t>(kBlockM) * D + r0 + r];
         s_w[r][ch] = v;
         mx = fmaxf(mx, v);
       }
-      for (int ch = 0; ch < en.chunks; ++ch) den += __expf(s_w[r][ch] - mx);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      for (int ch = lane16; ch < en.chunks; ch += 16) den += __expf(s_w[r][ch] - mx);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
       const float all = mx + logf(den);
-      for (int ch = 0; ch < en.chunks; ++ch) s_w[r][ch] = __expf(s_w[r][ch] - all);
-      if (lse != nullptr && row0 + r < seg_end) lse[static_cast<size_t>(head) * seg.capacity_q + row0 + r] = all;
+      for (int ch = lane16; ch < en.chunks; ch += 16) s_w[r][ch] = __expf(s_w[r][ch] - all);
+      if (lane16 == 0 && lse != nullptr && row0 + r < seg_end)
+        lse[static_cast<size_t>(head) * seg.capacity_q + row0 + r] = all;
     }
     __syncthreads();
     for (int u = threadIdx.x; u < kMergeRows * (D / 8); u += kMergeThreads) {
@@ -930,7 +1000,8 @@ cudaError_t launch(const CrossArgs& a, cudaStream_t stream) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   uint32_t* ws = static_cast<uint32_t*>(a.workspace);
   uint8_t* split = static_cast<uint8_t*>(a.split_area);
-  e = launch_programmatic(cross_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, a.seg, ws, split, sms, a.err);
+  e = launch_programmatic(cross_plan_kernel, dim3(1), dim3(a.seg.num_segments <= kSortMax ? kSortMax : kPlanThreads), 0,
+                          stream, a.seg, ws, split, sms, a.err);
   if (e != cudaSuccess) return e;
   e = launch_programmatic(cross_attn_kernel<D>, dim3(sms), dim3(kThreads), C::kSmemBytes, stream, a.tmap_q,
                           a.tmap_k, a.tmap_v, static_cast<__nv_bfloat16*>(a.o), a.wide, a.lse, a.seg, a.scale,
@@ -938,7 +1009,7 @@ cudaError_t launch(const CrossArgs& a, cudaStream_t stream) {
                           static_cast<unsigned long long>(a.wait_limit_ns), a.stall_after_tiles);
   if (e != cudaSuccess) return e;
   if (split != nullptr)
-    e = launch_programmatic(cross_merge_kernel<D>, dim3(4 * sms), dim3(kMergeThreads), 0, stream,
+    e = launch_programmatic(cross_merge_kernel<D>, dim3(8 * sms), dim3(kMergeThreads), 0, stream,
                             static_cast<const uint32_t*>(ws), static_cast<const uint8_t*>(split),
                             static_cast<__nv_bfloat16*>(a.o), a.lse, a.seg,
                             static_cast<const unsigned int*>(a.err));

@@ -289,3 +289,35 @@ def test_binding_refuses(h3):
                 dict(lse=torch.zeros(4, 5)), dict(out=q.transpose(0, 1))):
         with pytest.raises(ValueError):
             call(**bad)
+
+
+# Work dealt in shares (a last wave of items is cut where a CTA's share ends): rows, keys, heads.
+SHARES = {
+    "heads_apart": ([200, 300], [3000, 2500], 5, 5, 64, None),
+    "shared_heads_apart": ([100, 40], [2500, 5000], 12, 3, 64, None),
+    "one_item": ([30], [20000], 1, 1, 64, None),
+    "long_and_short_keys": ([30, 270, 20, 5, 140], [9000, 200, 1100, 1, 3001], 4, 4, 64, [8990, 150, 1024, 1, 3001]),
+    "behind_a_whole_wave": ([20, 30, 17, 140, 40, 21, 33], [1100, 2300, 1500, 1300, 3000, 1025, 0], 24, 24, 64, None),
+    "more_heads_than_ctas": ([20], [1300], 160, 160, 64, None),
+    "two_items_a_cta_or_none": ([257] * 3, [1600] * 3, 20, 10, 128, None),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", SHARES)
+def test_shares(h3, dev, name):
+    c = Case(*SHARES[name], seed=6)
+    args, where = c.on(dev)
+    where["max_seqlen_k"] = max(where["max_seqlen_k"], 1024)
+    out = torch.full(c.q.shape, 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((c.q.shape[1], c.cq), 7.0, device=dev)
+    n = h3.varlen_cross_attn_workspace_size(len(c.lq), c.max_q, where["max_seqlen_k"], c.cq, c.ck, c.q.shape[1],
+                                            c.k.shape[1], c.q.shape[2])
+    ws = torch.full((n + 16,), 255, dtype=torch.uint8, device=dev)  # 16 bytes past a 32-byte boundary
+    h3.varlen_cross_attn_fwd(**args, **where, out=out, lse=lse, workspace=ws[16:])
+    torch.cuda.synchronize()
+    assert h3.get_device_error(dev) == 0
+    _check(c, out, lse)
+    assert (out[c.nq:] == 7.0).all() and (lse[:, c.nq:] == 7.0).all()
+    again, lse2 = h3.varlen_cross_attn_fwd(**args, **where, return_lse=True)
+    assert torch.equal(again[:c.nq], out[:c.nq]) and torch.equal(lse2[:, :c.nq], lse[:, :c.nq])
