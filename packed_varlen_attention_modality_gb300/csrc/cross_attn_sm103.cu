@@ -11,31 +11,34 @@
 //
 // An encoder's key lists are short (a few 128-key tiles), so an item is over after a few thousand
 // cycles and what happens between items costs as much as the items do.  Hence:
-//   - the MMA warp runs straight on from one item into the next (order PV0_last, S0_first of the
+//   - the MMA warps run straight on from one item into the next (order PV0_last, S0_first of the
 //     next item, PV1_last, S1_first: the boundary looks like any other step);
+//   - they are two, one for each query tile, and take turns: a warp's polls wait behind the products that
+//     it has issued, so with one warp the tensor core runs dry at each poll (4,096 x 4,096 x 24 x 128:
+//     148 us, 162 with one);
 //   - O is read out, normalised and stored by a warpgroup of its own, which hands the accumulator
 //     back before it stores, while the softmax warpgroups are in the next item;
 //   - items are decoded one ahead, and queries and keys have a producer each, so neither waits on
 //     the other's ring;
 //   - a last key tile is multiplied only as far as it holds keys (in steps of 16).
-// 58,758 rows x 558 keys x 40 heads x 128 take 545 us so (1,235 TFLOP/s); with all of it in the softmax
+// 58,758 rows x 558 keys x 40 heads x 128 take 530 us so (1,267 TFLOP/s); with all of it in the softmax
 // warpgroups and one producer (the packed self-attention kernel's structure) they took 787 us.  A step
-// takes some 2,900 cycles (2,048 of tensor work: the chain scores -> softmax -> product of each tile sets
-// the pace), the step between two items 5,000: that is the first softmax of an item waiting for the last
-// product of the one before, and bounds short key lists.  Tried and slower: both tiles' softmax by all
-// eight warps, half a row each (581 us); one copy of the step's code for both kinds (615 us); the value
-// rows past the keys zeroed by a warp of their own (563 us); two warps issuing products (tiles fall in
-// phase).
+// takes some 2,700 cycles (2,048 of tensor work: the chain scores -> softmax -> product of each tile sets
+// the pace), the step between two items 3,700.  The kernel draws the GPU's 1.37 kW at that, at 1.91 to
+// 1.95 GHz, so cycles saved come back as a lower clock in part.  Tried and slower: both tiles' softmax by
+// all eight warps, half a row each (581 us); a third query tile's buffer for a key/value tile's (556 us); one
+// copy of the issuing code for both kinds of step (615 us); two issuing warps without turns (the tiles fall
+// in phase).
 //
 // Warp roles (512 threads; registers moved with setmaxnreg):
 //   warps 0-3 / 4-7   softmax of query tile 0 / 1: thread r owns row r = TMEM lane r
 //   warps 8-11        epilogue of both tiles
-//   warps 12, 13, 15  key/value producer, MMA issuer, scheduler + query producer
+//   warps 12-15       key/value producer, MMA issuers of tile 0 and 1, scheduler + query producer
 // TMEM (512 columns): O0 [0,128), O1 [128,256), S0/P0 [256,384), S1/P1 [384,512).
-// Shared memory at D = 128: 2 Q + 3 K + 2 V tiles of 32 KB.
+// Shared memory at D = 128: 2 Q tiles and a ring of 5 K and V tiles in turn, 32 KB each.
 //
 // Keys past the segment's end are masked to -inf by select and the value rows PV reads past it are
-// zeroed in shared memory, so NaN/Inf there cannot leak.  A segment without keys takes one tile
+// zeroed in shared memory (by the producer), so NaN/Inf there cannot leak.  A segment without keys takes one tile
 // whose keys are all masked: its rows come out as 0 with an LSE of -inf.
 // P is rounded to bf16 for the tensor core (half a step, 2^-8 relative at most); scores,
 // running max and sum, and O stay fp32, and the result is rounded to bf16 once.
@@ -133,8 +136,8 @@ __device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s
 // exclusive prefix [S + 1].
 // The last wave's work is laid end to end and dealt to the CTAs in equal shares, so an item is cut where
 // a share ends (four requests of 213 to 292 rows x 12,369 to 13,961 keys x 24 heads, 120 items of about 100
-// key tiles on 152 CTAs: 163 us; an item per CTA 183 us; the same without the heads apart 188 us, as each
-// row of K and V then comes from memory in pieces at different times).
+// key tiles on 152 CTAs: 163 us when an item per CTA took 183 us; the same without the heads apart 188 us,
+// as each row of K and V then comes from memory in pieces at different times).
 __global__ void __launch_bounds__(kPlanThreads)
 cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws,
                   uint8_t* __restrict__ split_area, int wave, unsigned int* err) {
@@ -349,11 +352,11 @@ struct Cfg {
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kBlockM * D * 2;
   static constexpr int kBoxBytes = kBlockM * 128;
-  static constexpr int kStagesK = D == 128 ? 3 : 4, kStagesV = D == 128 ? 2 : 4;
+  static constexpr int kStages = D == 128 ? 5 : 8;  // key and value tiles in turn
   // q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_final[2], o_empty[2], l_full[2],
-  // w_full[2], w_empty[2], drain, then k_full, k_empty, v_full, v_empty
-  static constexpr int kNumBars = 21 + 2 * kStagesK + 2 * kStagesV;
-  static constexpr int kSmemBytes = 1024 + kTileBytes * (2 + kStagesK + kStagesV) + kNumBars * 8 + 24 +
+  // w_full[2], w_empty[2], drain[2], turn[2], then kv_full, kv_empty, v_tail
+  static constexpr int kNumBars = 24 + 3 * kStages;
+  static constexpr int kSmemBytes = 1024 + kTileBytes * (2 + kStages) + kNumBars * 8 + 24 +
                                     2 * sizeof(CrossWork) + 2 * kBlockM * sizeof(float);
   static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(kBlockM, kBlockN, false);
@@ -368,14 +371,13 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
                   float scale_log2, const uint32_t* __restrict__ ws, uint8_t* __restrict__ split_area,
                   unsigned int* err, unsigned long long wait_ns, unsigned int stall_after) {
   using C = Cfg<D>;
-  constexpr int SK = C::kStagesK, SV = C::kStagesV;
+  constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = smem;
-  uint8_t* sK = sQ + 2 * C::kTileBytes;
-  uint8_t* sV = sK + SK * C::kTileBytes;
-  float* s_norm = reinterpret_cast<float*>(sV + SV * C::kTileBytes);  // [2][128]: 1 / row sum
+  uint8_t* sKV = sQ + 2 * C::kTileBytes;
+  float* s_norm = reinterpret_cast<float*>(sKV + kStages * C::kTileBytes);  // [2][128]: 1 / row sum
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_norm + 2 * kBlockM);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   CrossWork* work = reinterpret_cast<CrossWork*>(tmem_slot + 2);  // 2-slot ring
@@ -391,11 +393,11 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
   auto bar_lfull = [&](int t) { return bar(14 + t); };
   auto bar_wfull = [&](int i) { return bar(16 + i); };
   auto bar_wempty = [&](int i) { return bar(18 + i); };
-  const uint32_t bar_drain = bar(20);
-  auto bar_kfull = [&](int s) { return bar(21 + s); };
-  auto bar_kempty = [&](int s) { return bar(21 + SK + s); };
-  auto bar_vfull = [&](int s) { return bar(21 + 2 * SK + s); };
-  auto bar_vempty = [&](int s) { return bar(21 + 2 * SK + SV + s); };
+  auto bar_drain = [&](int t) { return bar(20 + t); };
+  auto bar_turn = [&](int t) { return bar(22 + t); };
+  auto bar_full = [&](int s) { return bar(24 + s); };
+  auto bar_empty = [&](int s) { return bar(24 + kStages + s); };
+  auto bar_vtail = [&](int s) { return bar(24 + 2 * kStages + s); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto pwait = [&](uint32_t b, uint32_t parity) { return mbar_wait(b, parity, wait_ns); };
@@ -439,17 +441,15 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
       mbar_init(bar_oempty(t), 4);  // warps
       mbar_init(bar_lfull(t), 4);  // warps
       mbar_init(bar_wfull(t), 1);
-      mbar_init(bar_wempty(t), 14);  // 12 softmax and epilogue warps, key/value producer, MMA warp
+      mbar_init(bar_drain(t), 1);
+      mbar_init(bar_turn(t), 1);
+      mbar_init(bar_wempty(t), 15);  // softmax and epilogue warps, key/value producer, MMA warps
     }
-    for (int s = 0; s < SK; ++s) {
-      mbar_init(bar_kfull(s), 1);
-      mbar_init(bar_kempty(s), 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 2);  // MMA warps
+      mbar_init(bar_vtail(s), 1);
     }
-    for (int s = 0; s < SV; ++s) {
-      mbar_init(bar_vfull(s), 1);
-      mbar_init(bar_vempty(s), 1);
-    }
-    mbar_init(bar_drain, 1);
     fence_mbarrier_init();
   }
   if (warp == 13) {
@@ -470,14 +470,37 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
     return true;
   };
 
+  // An item's last key tile is multiplied as far as it holds keys, in steps of 16 and at least one; value
+  // rows past the keys that PV reads all the same are zeroed.
+  auto steps16 = [](int keys) { return max(1, (keys + 15) / 16); };
+  auto has_tail = [&](int keys) { return keys < 16 * steps16(keys); };
+
   if (warp >= 12) {
     setmaxnreg_dec<kRegsOther>();
     if (warp == 12) {
       // ================= key/value producer =================
       const uint64_t pol_keep = l2_policy_evict_last();  // shared by the CTAs of a key head
-      uint32_t kt = 0, vt = 0;
-      bool ok = true, stalled = false;
+      uint32_t loaded = 0, v_last = 0;  // tiles; the last value tile of an item
+      int tail_keys = 0;
+      bool ok = true, stalled = false, tail = false;
       CrossWork d;
+      // The tail of an item's last value tile, once it has landed: while the next key tile is on its way,
+      // before the next value tile.  (Whole 128-byte rows: the swizzle permutes 16-byte pieces within a row.)
+      auto zero_tail = [&] {
+        if (!tail) return true;
+        tail = false;
+        const uint32_t s = v_last % kStages;
+        if (!wait_long(bar_full(s), (v_last / kStages) & 1)) return false;
+        uint8_t* vb = sKV + s * C::kTileBytes;
+        for (int i = lane; i < (16 * steps16(tail_keys) - tail_keys) * C::kBoxes * 8; i += 32) {
+          const int r = tail_keys + i / (C::kBoxes * 8), rem = i % (C::kBoxes * 8);
+          *reinterpret_cast<uint4*>(vb + (rem >> 3) * C::kBoxBytes + r * 128 + (rem & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        arrive_warp(bar_vtail(s));
+        return true;
+      };
       for (int k = 0; ok && !stalled; ++k) {
         ok = take(k, d);
         if (!ok || d.ntiles == 0) break;
@@ -488,25 +511,29 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
             tma_load_3d_hint(smem_u32(dst + x * C::kBoxBytes), map, x * 64, d.kv_head, row, b, pol_keep);
         };
         for (int j = 0; j < d.nkv; ++j) {
-          if (kt >= stall_after) {  // testing hook: as if the loads had stalled
+          if (loaded / 2 >= stall_after) {  // testing hook: as if the loads had stalled
             stalled = true;
             break;
           }
-          const int s = static_cast<int>(kt % SK), v = static_cast<int>(vt % SV);
-          ok = wait_long(bar_kempty(s), ((kt / SK) & 1) ^ 1);
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const int s = static_cast<int>(loaded % kStages);
+            ok = (v == 0 || zero_tail()) && wait_long(bar_empty(s), ((loaded / kStages) & 1) ^ 1);
+            if (!ok) break;
+            load(sKV + s * C::kTileBytes, v == 0 ? &tmap_k : &tmap_v, d.kv_row + j * kBlockN, bar_full(s));
+            ++loaded;
+          }
           if (!ok) break;
-          load(sK + s * C::kTileBytes, &tmap_k, d.kv_row + j * kBlockN, bar_kfull(s));
-          ++kt;
-          ok = wait_long(bar_vempty(v), ((vt / SV) & 1) ^ 1);
-          if (!ok) break;
-          load(sV + v * C::kTileBytes, &tmap_v, d.kv_row + j * kBlockN, bar_vfull(v));
-          ++vt;
         }
+        tail = ok && !stalled && has_tail(d.last_keys);
+        tail_keys = d.last_keys;
+        v_last = loaded - 1;
       }
+      if (ok && !stalled) ok = zero_tail();
       if (!ok && lane == 0) record_error(err, kErrTimeout);
       // never leave while a copy may still land: the last loads sit on distinct stages
-      for (uint32_t i = 0; i < SK && i < kt; ++i) mbar_wait(bar_kfull((kt - 1 - i) % SK), ((kt - 1 - i) / SK) & 1);
-      for (uint32_t i = 0; i < SV && i < vt; ++i) mbar_wait(bar_vfull((vt - 1 - i) % SV), ((vt - 1 - i) / SV) & 1);
+      for (uint32_t i = 0; i < kStages && i < loaded; ++i)
+        mbar_wait(bar_full((loaded - 1 - i) % kStages), ((loaded - 1 - i) / kStages) & 1);
     } else if (warp == 15) {
       // ================= scheduler and query producer =================
       const uint64_t pol_stream = l2_policy_evict_first();
@@ -542,43 +569,32 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
       if (!ok && lane == 0) record_error(err, kErrTimeout);
       for (int t = 0; t < 2; ++t)
         if (qn[t] > 0) mbar_wait(bar_qfull(t), (qn[t] - 1) & 1);
-    } else if (warp == 13) {
-      // ================= MMA issuer =================
-      auto wait_all2 = [&](uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) {  // polls overlap
-        bool r0 = mbar_try_wait(b0, p0), r1 = mbar_try_wait(b1, p1);
-        if (!r0) r0 = pwait(b0, p0);
-        if (!r1) r1 = pwait(b1, p1);
-        return __all_sync(0xffffffffu, r0 && r1);
-      };
+    } else {
+      // ================= MMA issuers: warp 13 for tile 0, 14 for tile 1 =================
+      // A warp's polls wait for the products that it has issued before, so the tensor core would run dry at
+      // each poll of a single issuer.  Two take turns: what one polls for, it does while the other's products
+      // run.  Their order is kept (a turn barrier each), or the tiles would fall in phase.
+      const int t = warp - 13;
       constexpr uint32_t kTile16 = C::kTileBytes >> 4;
-      const SmemDesc dq = sw128_desc_split(smem_u32(sQ), 16, 1024);
-      const SmemDesc dk = sw128_desc_split(smem_u32(sK), 16, 1024);
-      const SmemDesc dv = sw128_desc_split(smem_u32(sV), C::kBoxBytes, 1024);
-      auto issue_qk = [&](int t, int s, uint32_t idesc) {  // S_t = Q_t K_s^T
-        const uint32_t qlo = dq.lo + t * kTile16, klo = dk.lo + s * kTile16;
+      const SmemDesc dq = sw128_desc_split(smem_u32(sQ) + t * C::kTileBytes, 16, 1024);
+      const SmemDesc dk = sw128_desc_split(smem_u32(sKV), 16, 1024);
+      const SmemDesc dv = sw128_desc_split(smem_u32(sKV), C::kBoxBytes, 1024);
+      const uint32_t s_tmem = tmem + kColS + 128 * t, o_tmem = tmem + kColO + 128 * t;
+      auto issue_qk = [&](int s, uint32_t idesc) {  // S_t = Q_t K_s^T
+        const uint32_t klo = dk.lo + s * kTile16;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
-          mma_ss_split(tmem + kColS + 128 * t, qlo + off, dq.hi, klo + off, dk.hi, idesc, kk > 0 ? 1u : 0u);
+          mma_ss_split(s_tmem, dq.lo + off, dq.hi, klo + off, dk.hi, idesc, kk > 0 ? 1u : 0u);
         }
         mma_commit(bar_sfull(t));
       };
-      // O_t += P_t V_s over one half of the tile's 16-key steps, as far as `end`
-      auto issue_pv = [&](int t, int s, bool first, int half, int end) {
-        const uint32_t p = tmem + kColS + 128 * t + half * (kBlockN / 32) * 8;
-        const uint32_t vlo = dv.lo + s * kTile16 + half * (kBlockN / 32) * (2048 >> 4);
-        const int n = end - half * (kBlockN / 32);
-        if (n >= kBlockN / 32) {
+      auto issue_pv = [&](int s, bool first, int from) {  // O_t += P_t V_s over four steps of 16 keys
+        const uint32_t vlo = dv.lo + s * kTile16;
 #pragma unroll
-          for (int kk = 0; kk < kBlockN / 32; ++kk)
-            mma_ts_split(tmem + kColO + 128 * t, p + kk * 8, vlo + kk * (2048 >> 4), dv.hi, C::kIdescPV,
-                         (!first || kk > 0) ? 1u : 0u);
-        } else {
-#pragma unroll 1
-          for (int kk = 0; kk < n; ++kk)
-            mma_ts_split(tmem + kColO + 128 * t, p + kk * 8, vlo + kk * (2048 >> 4), dv.hi, C::kIdescPV,
-                         (!first || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = from; kk < from + 4; ++kk)
+          mma_ts_split(o_tmem, s_tmem + kk * 8, vlo + kk * (2048 >> 4), dv.hi, C::kIdescPV,
+                       (!first || kk > 0) ? 1u : 0u);
       };
       const bool leader = elect_one();
       struct Item {  // what is needed of an item here
@@ -591,122 +607,161 @@ cross_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_const
         if (leader) mbar_arrive(bar_wempty(k & 1));
         return true;
       };
-      // an item's last key tile is multiplied as far as it holds keys, but at least one step
-      auto steps16 = [](int keys) { return max(1, (keys + 15) / 16); };
       auto idesc_last = [&](const Item& i) {
         return i.last_keys < kBlockN ? idesc_bf16_f32(kBlockM, 16 * steps16(i.last_keys), false) : C::kIdescQK;
       };
-      // Ring positions as stage and phase: what the one issuing thread computes between two products
-      // delays them.
-      int sk = 0, sv = 0;
-      uint32_t pk = 0, pv = 0;                                 // phases of the K and V rings
-      uint32_t qp[2] = {0u, 0u}, pp[2] = {0u, 0u}, op[2] = {1u, 1u};  // phases of Q, P and O per tile
+      int sk = 0, sv = 1;
+      uint32_t pk = 0, pv = 0;  // phases of the stages of the next key and value tile
+      uint32_t qp = 0u, pp = 0u, op = 1u, turn = t == 0 ? 1u : 0u;  // phases of Q, P, O and the turns
+      uint32_t tails = 0;  // phases of the value tails, a bit per stage
       auto next_k = [&] {
-        if (++sk == SK) {
-          sk = 0;
+        if ((sk += 2) >= kStages) {
+          sk -= kStages;
           pk ^= 1;
         }
       };
+      auto next_v = [&] {
+        if ((sv += 2) >= kStages) {
+          sv -= kStages;
+          pv ^= 1;
+        }
+      };
+      // Waits for this warp's turn and whatever else is asked for; the polls overlap.
+      auto wait_turn = [&](bool v, bool k, bool q, bool p, uint32_t p_bar, bool o, bool z) {
+        bool r[7];
+        r[0] = !p || mbar_try_wait(p_bar, pp);
+        r[1] = mbar_try_wait(bar_turn(t), turn);
+        r[2] = !v || mbar_try_wait(bar_full(sv), pv);
+        r[3] = !k || mbar_try_wait(bar_full(sk), pk);
+        r[4] = !q || mbar_try_wait(bar_qfull(t), qp);
+        r[5] = !o || mbar_try_wait(bar_oempty(t), op);
+        r[6] = !z || mbar_try_wait(bar_vtail(sv), tails >> sv & 1u);
+        bool all = true;
+        if (!r[0]) all = pwait(p_bar, pp);
+        if (!r[1]) all = pwait(bar_turn(t), turn) && all;
+        if (!r[2]) all = pwait(bar_full(sv), pv) && all;
+        if (!r[3]) all = pwait(bar_full(sk), pk) && all;
+        if (!r[4]) all = pwait(bar_qfull(t), qp) && all;
+        if (!r[5]) all = pwait(bar_oempty(t), op) && all;
+        if (!r[6]) all = pwait(bar_vtail(sv), tails >> sv & 1u) && all;
+        turn ^= 1;
+        if (z) tails ^= 1u << sv;
+        if (q) qp ^= 1;
+        if (o) op ^= 1;
+        return __all_sync(0xffffffffu, all) != 0;
+      };
       bool ok = take_item(0, cur), issued = false;
       if (ok && cur.ntiles > 0) {  // the first item's first scores
-        ok = wait_all(bar_kfull(0), 0);
-        const uint32_t idesc = cur.nkv == 1 ? idesc_last(cur) : C::kIdescQK;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || t >= cur.ntiles) break;
-          ok = wait_all(bar_qfull(t), qp[t]);
-          qp[t] ^= 1;
-          if (!ok) break;
+        ok = wait_all(bar_full(0), 0);
+        if (ok && t < cur.ntiles) {
+          ok = wait_all(bar_qfull(t), 0);
+          qp = 1;
           tc_fence_after();
-          if (leader) {
-            issue_qk(t, 0, idesc);
+          if (ok && leader) {
+            issue_qk(0, cur.nkv == 1 ? idesc_last(cur) : C::kIdescQK);
             if (cur.nkv == 1) mma_commit(bar_qempty(t));
-            if (t == cur.ntiles - 1) mma_commit(bar_kempty(0));
+            mma_commit(bar_empty(0));
           }
-          issued = true;
+          issued = ok;
           __syncwarp();
+        } else if (ok && leader) {
+          mbar_arrive(bar_empty(0));
         }
         next_k();
       }
-      // One step: PV of the item's key tile, and the scores of the next one (its own, or the next item's
-      // first: last).  PV_t runs in two halves, as P of the first 64 keys comes earlier.
-      auto step = [&](bool first, bool last, int stiles, uint32_t idesc, bool q_done, int end) {
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t < cur.ntiles) {
-            if (t > 0 && !wait_all(bar_phalf(t), pp[t])) return false;
-            if (first) {
-              if (!wait_all(bar_oempty(t), op[t])) return false;
-              op[t] ^= 1;
-            }
-            tc_fence_after();
-            if (leader) issue_pv(t, sv, first, 0, end);
-            __syncwarp();
-            if (!(t == 0 && stiles > 0 ? wait_all2(bar_pfull(0), pp[0], bar_kfull(sk), pk)
-                                       : wait_all(bar_pfull(t), pp[t])))
-              return false;
-            pp[t] ^= 1;
-            tc_fence_after();
-            if (leader) {
-              issue_pv(t, sv, false, 1, end);
-              if (last) mma_commit(bar_ofinal(t));
-              if (t == cur.ntiles - 1) mma_commit(bar_vempty(sv));
-            }
-            __syncwarp();
+      // One step within an item: PV of its key tile, and the scores of the next one.
+      auto step = [&](bool first, uint32_t idesc, bool q_done) {
+        if (t < cur.ntiles) {
+          if (!wait_turn(true, true, false, true, bar_phalf(t), first, false)) return false;
+          tc_fence_after();
+          if (leader) issue_pv(sv, first, 0);
+          __syncwarp();
+          if (!wait_all(bar_pfull(t), pp)) return false;
+          pp ^= 1;
+          tc_fence_after();
+          if (leader) issue_pv(sv, false, 4);
+          if (leader) {
+            mma_commit(bar_empty(sv));
+            issue_qk(sk, idesc);
+            if (q_done) mma_commit(bar_qempty(t));
+            mma_commit(bar_empty(sk));
+            mbar_arrive(bar_turn(t ^ 1));
           }
-          if (t < stiles) {
-            if (last) {
-              if (!wait_all(bar_qfull(t), qp[t])) return false;
-              qp[t] ^= 1;
-              tc_fence_after();
-            }
-            if (leader) {
-              issue_qk(t, sk, idesc);
-              if (q_done) mma_commit(bar_qempty(t));
-              if (t == stiles - 1) mma_commit(bar_kempty(sk));
-            }
-            __syncwarp();
+          __syncwarp();
+        } else {
+          if (!wait_turn(true, true, false, false, 0, false, false)) return false;
+          if (leader) {
+            mbar_arrive(bar_empty(sv));
+            mbar_arrive(bar_empty(sk));
+            mbar_arrive(bar_turn(t ^ 1));
           }
+          __syncwarp();
         }
-        if (++sv == SV) {
-          sv = 0;
-          pv ^= 1;
+        next_v();
+        next_k();
+        return true;
+      };
+      // The step between two items: PV of the last key tile, as far as it holds keys, and the next item's
+      // first scores.
+      auto boundary = [&](bool first) {
+        const bool has_pv = t < cur.ntiles, has_qk = t < nxt.ntiles, more = nxt.ntiles > 0;
+        const int end = steps16(cur.last_keys);
+        const uint32_t idesc = nxt.nkv == 1 ? idesc_last(nxt) : C::kIdescQK;
+        if (!wait_turn(true, more, has_qk, has_pv, bar_pfull(t), has_pv && first,
+                       has_tail(cur.last_keys))) return false;
+        if (has_pv) pp ^= 1;
+        tc_fence_after();
+        if (has_pv) {
+          if (end == kBlockN / 16) {
+            if (leader) {
+              issue_pv(sv, first, 0);
+              issue_pv(sv, false, 4);
+            }
+          } else if (leader) {
+#pragma unroll 1
+            for (int kk = 0; kk < end; ++kk)
+              mma_ts_split(o_tmem, s_tmem + kk * 8, dv.lo + sv * kTile16 + kk * (2048 >> 4), dv.hi, C::kIdescPV,
+                           (!first || kk > 0) ? 1u : 0u);
+          }
+          if (leader) {
+            mma_commit(bar_ofinal(t));
+            mma_commit(bar_empty(sv));
+          }
+        } else if (leader) {
+          mbar_arrive(bar_empty(sv));
         }
-        if (stiles > 0) next_k();
+        __syncwarp();
+        if (has_qk) {
+          if (leader) {
+            issue_qk(sk, idesc);
+            if (nxt.nkv == 1) mma_commit(bar_qempty(t));
+            mma_commit(bar_empty(sk));
+          }
+          issued = true;
+        } else if (more && leader) {
+          mbar_arrive(bar_empty(sk));
+        }
+        __syncwarp();
+        if (leader) mbar_arrive(bar_turn(t ^ 1));
+        __syncwarp();
+        next_v();
+        if (more) next_k();
         return true;
       };
       for (int k = 0; ok && cur.ntiles > 0; ++k) {
         const uint32_t idesc_end = idesc_last(cur);
         for (int j = 0; j + 1 < cur.nkv && ok; ++j) {
-          ok = wait_all2(bar_vfull(sv), pv, bar_phalf(0), pp[0]);
-          if (!ok) break;
           const bool q_done = j + 2 == cur.nkv;
-          ok = step(j == 0, false, cur.ntiles, q_done ? idesc_end : C::kIdescQK, q_done, kBlockN / 16);
+          ok = step(j == 0, q_done ? idesc_end : C::kIdescQK, q_done);
         }
         if (ok) ok = take_item(k + 1, nxt);
-        if (ok) ok = wait_all2(bar_vfull(sv), pv, bar_phalf(0), pp[0]);
-        if (!ok) break;
-        const int end = steps16(cur.last_keys);
-        if (cur.last_keys < 16 * end) {
-          // zero the value rows past the keys as far as PV reads (whole 128-byte rows: the swizzle
-          // permutes 16-byte pieces within a row)
-          uint8_t* vb = sV + sv * C::kTileBytes;
-          const int nrows = 16 * end - cur.last_keys;
-          for (int i = lane; i < nrows * C::kBoxes * 8; i += 32) {
-            const int r = cur.last_keys + i / (C::kBoxes * 8), rem = i % (C::kBoxes * 8);
-            *reinterpret_cast<uint4*>(vb + (rem >> 3) * C::kBoxBytes + r * 128 + (rem & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        ok = step(cur.nkv == 1, true, nxt.ntiles, nxt.nkv == 1 ? idesc_last(nxt) : C::kIdescQK, nxt.nkv == 1, end);
+        if (ok) ok = boundary(cur.nkv == 1);
         cur = nxt;
       }
       if (!ok && leader) record_error(err, kErrTimeout);
       if (issued && leader) {  // every MMA issued has completed before TMEM is released
-        mma_commit(bar_drain);
-        mbar_wait(bar_drain, 0);
+        mma_commit(bar_drain(t));
+        mbar_wait(bar_drain(t), 0);
       }
       __syncwarp();
     }
