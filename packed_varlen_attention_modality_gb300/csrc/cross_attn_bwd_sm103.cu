@@ -766,20 +766,26 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
 template <int D>
 __global__ void __launch_bounds__(256)
 cross_bwd_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
-  grid_dependency_wait();
-  launch_dependents();
-  if (a.err != nullptr && *reinterpret_cast<const volatile unsigned int*>(a.err) == kErrTimeout) return;
+  // The plan and the first unit's place are read before the wait: this kernel starts once all CTAs of the
+  // one before it run, so the plan kernel is over (33.7 us for the short case below, 35.1 after the wait).
   const Plan& plan = plan_of(a.plan);
   const int S = a.seg.num_segments, group = a.seg.num_q_heads / a.seg.num_kv_heads;
   constexpr uint32_t kParts = 8;
   constexpr int kRows = kTile / kParts;
   const uint32_t units_k = plan.chunks_k > 1 ? (plan.tiles_k - plan.whole_k) * 2 * kParts : 0;
   const uint32_t units_q = plan.chunks_q > 1 ? (plan.tiles_q - plan.whole_q) * kParts : 0;
-  for (uint32_t u = blockIdx.x; u < units_k + units_q; u += gridDim.x) {
+  struct Unit {
+    int chunks, r0, rows;
+    size_t step;  // floats between chunks
+    const float* part;
+    int64_t stride;
+    __nv_bfloat16* out;
+  };
+  auto locate = [&](uint32_t u) {
     const bool keys = u < units_k;
     const uint32_t v = keys ? u : u - units_k, per_tile = keys ? 2 * kParts : kParts;
     const uint32_t index = v / per_tile;  // of the tile behind the whole waves
-    const int which = keys ? static_cast<int>(v / kParts % 2) : 0, r0 = static_cast<int>(v % kParts) * kRows;
+    const int which = keys ? static_cast<int>(v / kParts % 2) : 0;
     const uint32_t* prefix = keys ? plan.prefix + S + 1 : plan.prefix;
     const uint32_t tile = (keys ? plan.whole_k : plan.whole_q) + index;
     const int most = static_cast<int>(keys ? plan.chunks_k : plan.chunks_q);
@@ -788,28 +794,38 @@ cross_bwd_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
     const int tiles = tiles_of(keys ? r.keys : r.rows), local = static_cast<int>(tile - prefix[g]);
     const int head = local / tiles, row_tile = local % tiles * kTile;
     const int steps = keys ? (row_tile < r.used ? kv_steps(r, group) : 0) : tiles_of(r.used);
-    const int chunks = max(1, min(most, steps));
-    if (chunks == 1) continue;  // written already
     const size_t slot = static_cast<size_t>(index) * most;
-    const size_t step = keys ? 2 * kTile * D : kTile * D;
-    const float* part = keys ? a.partials + slot * step + static_cast<size_t>(which) * kTile * D
-                             : a.partials_q + slot * step;
-    const int64_t stride = keys ? (which == 0 ? a.dv_stride : a.dk_stride) : a.dq_stride;
-    __nv_bfloat16* out = (keys ? (which == 0 ? a.dv : a.dk) : a.dq) +
-                         (static_cast<int64_t>(keys ? r.k0 : r.q0) + row_tile) * stride + head * D;
-    const int rows = min(kTile, (keys ? r.keys : r.rows) - row_tile);
+    Unit x;
+    x.chunks = max(1, min(most, steps));
+    x.r0 = static_cast<int>(v % kParts) * kRows;
+    x.rows = min(kTile, (keys ? r.keys : r.rows) - row_tile);
+    x.step = keys ? 2 * kTile * D : kTile * D;
+    x.part = keys ? a.partials + slot * x.step + static_cast<size_t>(which) * kTile * D : a.partials_q + slot * x.step;
+    x.stride = keys ? (which == 0 ? a.dv_stride : a.dk_stride) : a.dq_stride;
+    x.out = (keys ? (which == 0 ? a.dv : a.dk) : a.dq) +
+            (static_cast<int64_t>(keys ? r.k0 : r.q0) + row_tile) * x.stride + head * D;
+    return x;
+  };
+  Unit x{};
+  if (blockIdx.x < units_k + units_q) x = locate(blockIdx.x);
+  grid_dependency_wait();
+  launch_dependents();
+  if (a.err != nullptr && *reinterpret_cast<const volatile unsigned int*>(a.err) == kErrTimeout) return;
+  for (uint32_t u = blockIdx.x; u < units_k + units_q; u += gridDim.x) {
+    if (u != blockIdx.x) x = locate(u);
+    if (x.chunks == 1) continue;  // written already
     for (int i = threadIdx.x; i < kRows * (D / 8); i += 256) {
-      const int row = r0 + i / (D / 8), col = i % (D / 8) * 8;
-      if (row >= rows) continue;
+      const int row = x.r0 + i / (D / 8), col = i % (D / 8) * 8;
+      if (row >= x.rows) continue;
       float f[8] = {};
 #pragma unroll 8
-      for (int c = 0; c < chunks; ++c) {
-        const float4* src = reinterpret_cast<const float4*>(part + c * step + row * D + col);
-        const float4 x = src[0], y = src[1];
-        f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-        f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+      for (int c = 0; c < x.chunks; ++c) {
+        const float4* src = reinterpret_cast<const float4*>(x.part + c * x.step + row * D + col);
+        const float4 y = src[0], z = src[1];
+        f[0] += y.x; f[1] += y.y; f[2] += y.z; f[3] += y.w;
+        f[4] += z.x; f[5] += z.y; f[6] += z.z; f[7] += z.w;
       }
-      *reinterpret_cast<uint4*>(out + row * stride + col) =
+      *reinterpret_cast<uint4*>(x.out + row * x.stride + col) =
           make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
     }
   }

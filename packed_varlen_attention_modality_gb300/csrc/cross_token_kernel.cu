@@ -7,8 +7,8 @@
 // memory (16-byte asynchronous copies, no barrier between warps), computes S = Q K^T and O += P V
 // with 16 x 8 x 16 matrix instructions, and keeps a running max and sum; the warps are merged in
 // order at the end.  Rows this few leave tcgen05's 128-row tiles all but empty: 32 segments of one
-// row x 8 key heads x 64 query heads with 512 to 4,096 keys take 242 us there, 58 us here (323 MB read:
-// 5.5 TB/s, 81 % of a plain copy's rate; the merge's launch is 5 us of it).
+// row x 8 key heads x 64 query heads with 512 to 4,096 keys take 242 us there, 57 us here (323 MB read:
+// 5.7 TB/s, 84 % of a plain copy's rate; the merge's launch is 4 us of it).
 // Chunks write partial results (O normalised by its own sum, fp32, and the LSE), which a merge
 // kernel joins in chunk order; with one chunk the CTA writes o itself.
 // Scores, max, sum and O are fp32; P is rounded to bf16 for the product with V, o once at the end.
@@ -268,33 +268,51 @@ cross_token_kernel(const __grid_constant__ CrossTokenArgs a) {
   }
 }
 
-// Joins the chunks of each (segment, key head), in chunk order.
+// Joins the chunks of each (segment, key head), in chunk order.  The segment's place is read before the
+// wait: this kernel starts once all CTAs of the one before it run, so the offsets are there (56.8 us for
+// the case above, 58.4 read after the wait and one chunk at a time).
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 cross_token_merge_kernel(const __grid_constant__ CrossTokenArgs a) {
-  grid_dependency_wait();
-  launch_dependents();
   const int kv_head = blockIdx.x, g = blockIdx.y;
   const TokenSegment s = token_segment(a.seg, g, nullptr);
   const int group = a.seg.num_q_heads / a.seg.num_kv_heads;
   const int n = min(a.chunks, (s.keys + a.chunk_keys - 1) / a.chunk_keys);
   const float* part = partial_of<D>(a.partials, a, static_cast<size_t>(g) * a.seg.num_kv_heads + kv_head, 0);
   const size_t step = cross_token_partial(a.max_rows, D);
+  grid_dependency_wait();
+  launch_dependents();
   for (int i = threadIdx.x; i < s.rows * (D / 8); i += kThreads) {
     const int r = i / (D / 8), col = i % (D / 8) * 8;
-    float top = -INFINITY;
-    for (int c = 0; c < n; ++c) top = fmaxf(top, part[c * step + a.max_rows * D + r]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, x[8] = {};
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
-      const float f = __expf(part[c * step + a.max_rows * D + r] - base);
-      const float4* src = reinterpret_cast<const float4*>(part + c * step + r * D + col);
-      const float4 u = src[0], v = src[1];
-      const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-      sum += f;
+    float top = -INFINITY, sum = 0.f, x[8] = {};
+    constexpr int kBatch = 4;  // chunks loaded at once
+    for (int c0 = 0; c0 < n; c0 += kBatch) {
+      float w[kBatch];
+      float4 u[kBatch], v[kBatch];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(f, y[e], x[e]);
+      for (int c = 0; c < kBatch; ++c) {
+        const float* p = part + min(c0 + c, n - 1) * step;
+        w[c] = c0 + c < n ? p[a.max_rows * D + r] : -INFINITY;
+        u[c] = reinterpret_cast<const float4*>(p + r * D + col)[0];
+        v[c] = reinterpret_cast<const float4*>(p + r * D + col)[1];
+      }
+      float mx = top;
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) mx = fmaxf(mx, w[c]);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      const float old = __expf(top - base);
+      top = mx;
+      sum *= old;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= old;
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        const float f = __expf(w[c] - base);
+        const float y[8] = {u[c].x, u[c].y, u[c].z, u[c].w, v[c].x, v[c].y, v[c].z, v[c].w};
+        sum += f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = c0 + c < n ? fmaf(f, y[e], x[e]) : x[e];
+      }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int row = s.row0 + r / group, head = kv_head * group + r % group;
