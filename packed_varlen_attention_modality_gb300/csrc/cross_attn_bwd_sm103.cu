@@ -766,8 +766,10 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
 template <int D>
 __global__ void __launch_bounds__(256)
 cross_bwd_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
-  // The plan and the first unit's place are read before the wait: this kernel starts once all CTAs of the
-  // one before it run, so the plan kernel is over (33.7 us for the short case below, 35.1 after the wait).
+  // Nothing is read before the wait, the plan and the offsets included (they say where this kernel writes):
+  // only the wait makes another kernel's writes visible here.
+  grid_dependency_wait();
+  launch_dependents();
   const Plan& plan = plan_of(a.plan);
   const int S = a.seg.num_segments, group = a.seg.num_q_heads / a.seg.num_kv_heads;
   constexpr uint32_t kParts = 8;
@@ -806,13 +808,9 @@ cross_bwd_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
             (static_cast<int64_t>(keys ? r.k0 : r.q0) + row_tile) * x.stride + head * D;
     return x;
   };
-  Unit x{};
-  if (blockIdx.x < units_k + units_q) x = locate(blockIdx.x);
-  grid_dependency_wait();
-  launch_dependents();
   if (a.err != nullptr && *reinterpret_cast<const volatile unsigned int*>(a.err) == kErrTimeout) return;
   for (uint32_t u = blockIdx.x; u < units_k + units_q; u += gridDim.x) {
-    if (u != blockIdx.x) x = locate(u);
+    const Unit x = locate(u);
     if (x.chunks == 1) continue;  // written already
     for (int i = threadIdx.x; i < kRows * (D / 8); i += 256) {
       const int row = x.r0 + i / (D / 8), col = i % (D / 8) * 8;

@@ -268,20 +268,19 @@ cross_token_kernel(const __grid_constant__ CrossTokenArgs a) {
   }
 }
 
-// Joins the chunks of each (segment, key head), in chunk order.  The segment's place is read before the
-// wait: this kernel starts once all CTAs of the one before it run, so the offsets are there (56.8 us for
-// the case above, 58.4 read after the wait and one chunk at a time).
+// Joins the chunks of each (segment, key head), in chunk order, four chunks loaded at once.  Nothing is read
+// before the wait, the offsets included: only the wait makes another kernel's writes visible here.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
 cross_token_merge_kernel(const __grid_constant__ CrossTokenArgs a) {
+  grid_dependency_wait();
+  launch_dependents();
   const int kv_head = blockIdx.x, g = blockIdx.y;
   const TokenSegment s = token_segment(a.seg, g, nullptr);
   const int group = a.seg.num_q_heads / a.seg.num_kv_heads;
   const int n = min(a.chunks, (s.keys + a.chunk_keys - 1) / a.chunk_keys);
   const float* part = partial_of<D>(a.partials, a, static_cast<size_t>(g) * a.seg.num_kv_heads + kv_head, 0);
   const size_t step = cross_token_partial(a.max_rows, D);
-  grid_dependency_wait();
-  launch_dependents();
   for (int i = threadIdx.x; i < s.rows * (D / 8); i += kThreads) {
     const int r = i / (D / 8), col = i % (D / 8) * 8;
     float top = -INFINITY, sum = 0.f, x[8] = {};

@@ -1,0 +1,86 @@
+"""Offsets that the cross attention calls meet on the device: changed between calls by the kernel before."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def h3():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import packed_varlen_attention_modality_gb300 as h3
+
+    h3.load_library()
+    return h3
+
+
+@pytest.fixture(scope="module")
+def dev():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    torch.cuda.set_device(0)
+    return torch.device("cuda", 0)
+
+
+def _i32(dev, *v):
+    return torch.tensor(v, dtype=torch.int32, device=dev)
+
+
+def _random(dev, *shape, seed=0):
+    return torch.randn(*shape, device=dev, generator=torch.Generator(device=dev).manual_seed(seed)).to(torch.bfloat16)
+
+
+# Two layouts of the same tensors: rows and key rows of each segment.
+LAYOUTS = {
+    "tokens": ([[1, 2, 1], [2, 1, 1]], [[3000, 700, 900], [40, 2560, 2000]], 8, 2, 64),
+    "cut_keys": ([[30, 60, 100], [90, 20, 80]], [[3000, 700, 900], [1400, 2560, 640]], 4, 4, 128),
+    "cut_rows": ([[2300, 60, 100], [90, 20, 2350]], [[130, 70, 60], [60, 40, 160]], 4, 2, 64),
+}
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("name", LAYOUTS)
+def test_offsets_written_by_the_kernel_before(h3, dev, name, captured):
+    rows, keys, hq, hk, d = LAYOUTS[name]
+    nq, nk = sum(rows[0]), sum(keys[0])
+    q, do = _random(dev, nq, hq, d), _random(dev, nq, hq, d, seed=1)
+    k, v = _random(dev, nk, hk, d, seed=2), _random(dev, nk, hk, d, seed=3)
+    most = max(map(max, rows)), max(map(max, keys))
+    cus = [(_i32(dev, *np.cumsum([0, *r]).tolist()), _i32(dev, *np.cumsum([0, *x]).tolist()))
+           for r, x in zip(rows, keys)]
+
+    def run(cu_q, cu_k, ws, bws):
+        o, lse = h3.varlen_cross_attn_fwd(q, k, v, cu_q, cu_k, *most, return_lse=True, workspace=ws)
+        return (o, lse, *h3.varlen_cross_attn_bwd(do, q, k, v, o, lse, cu_q, cu_k, *most, workspace=bws))
+
+    want = [[t.clone() for t in run(*cu, None, None)] for cu in cus]
+    assert not torch.equal(want[0][0], want[1][0])
+    sizes = (3, *most, nq, nk, hq, hk, d)
+    ws, bws = (torch.zeros(f(*sizes), dtype=torch.uint8, device=dev)
+               for f in (h3.varlen_cross_attn_workspace_size, h3.varlen_cross_attn_bwd_workspace_size))
+    cu_q, cu_k = (t.clone() for t in cus[0])
+    results = []
+
+    def both():
+        for a, b in cus:
+            cu_q.copy_(a), cu_k.copy_(b)
+            results.append(run(cu_q, cu_k, ws, bws))
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            both()
+        for _ in range(5):
+            for r in results:
+                for t in r:
+                    t.fill_(7.0)
+            graph.replay()
+            assert all(torch.equal(a, b) for r, w in zip(results, want) for a, b in zip(r, w))
+    else:
+        for _ in range(20):
+            both()
+        for i, r in enumerate(results):
+            assert all(torch.equal(a, b) for a, b in zip(r, want[i % 2]))
+    assert h3.get_device_error(dev) == 0
