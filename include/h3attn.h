@@ -286,8 +286,9 @@ H3_API size_t h3_varlen_cross_attn_workspace_size(const h3_cross_attn_desc* desc
  * workspace  : device, h3_varlen_cross_attn_workspace_size() bytes, 16-byte aligned; need not be
  *              initialised.  Calls that may run at the same time need separate workspaces.
  * A segment whose offsets or n_g are out of range, or with more rows than max_seqlen_q, is skipped
- * (its rows are not written); one with more keys than max_seqlen_k is computed in full.  Both are
- * recorded as H3_ERR_BAD_CU_SEQLENS.
+ * (its rows are not written); one with more keys than max_seqlen_k is computed in full.  When offsets run
+ * backwards and segments overlap until they hold more 128-row tiles per head than capacity_q / 128 +
+ * num_segments, no row need be written.  All are recorded as H3_ERR_BAD_CU_SEQLENS.
  * Errors: H3_ERR_NULL, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED, H3_ERR_MISALIGNED,
  *         H3_ERR_WORKSPACE, H3_ERR_CUDA; device-side H3_ERR_BAD_CU_SEQLENS / H3_ERR_TIMEOUT. */
 H3_API h3_status h3_varlen_cross_attn_fwd(const h3_cross_attn_desc* desc, const void* q,
@@ -313,8 +314,8 @@ H3_API size_t h3_varlen_cross_attn_bwd_workspace_size(const h3_cross_attn_desc* 
  * workspace   : device, h3_varlen_cross_attn_bwd_workspace_size() bytes, 16-byte aligned; need not be
  *               initialised.  Calls that may run at the same time need separate workspaces.
  * Sums over queries and keys are taken in a fixed order: the result does not depend on timing.
- * A side with capacity 0 may be NULL.  Bad segments as for the forward; a skipped segment's rows are
- * not written on either side.
+ * A side with capacity 0 may be NULL.  Bad segments and overlapping ones (here on either side) as for the
+ * forward; a skipped segment's rows are not written on either side.
  * Errors: as h3_varlen_cross_attn_fwd. */
 H3_API h3_status h3_varlen_cross_attn_bwd(const h3_cross_attn_desc* desc, const void* dout,
                                           const void* q, const void* k, const void* v,

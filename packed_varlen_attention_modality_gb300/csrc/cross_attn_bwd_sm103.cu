@@ -102,12 +102,13 @@ __device__ __forceinline__ int step_at(int n, int c, int chunks) {
 }
 
 // Exclusive sum over the block (whole warps) and the total.
-__device__ __forceinline__ uint32_t exclusive_scan(uint32_t v, uint32_t* s_warp, uint32_t& total) {
+template <typename T>
+__device__ __forceinline__ T exclusive_scan(T v, T* s_warp, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  uint32_t x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (warps == 1) {
@@ -117,7 +118,7 @@ __device__ __forceinline__ uint32_t exclusive_scan(uint32_t v, uint32_t* s_warp,
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  uint32_t before = 0;
+  T before = 0;
   total = 0;
 #pragma unroll 1
   for (int w = 0; w < warps; ++w) {
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads)
 cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws, int slots, uint32_t sms,
                       unsigned int* err) {
   __shared__ uint32_t s_warp[kPlanThreads / 32];
+  __shared__ uint64_t s_warp64[kPlanThreads / 32];
   grid_dependency_wait();
   launch_dependents();
   const int S = seg.num_segments, tid = threadIdx.x, group = seg.num_q_heads / seg.num_kv_heads;
@@ -153,7 +155,8 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
   Segment mine{};  // this thread's only segment, when it has one
   if (chunk == 1 && lo < hi) mine = checked(lo);
   auto segment = [&](int g) { return chunk == 1 ? mine : checked(g); };
-  uint32_t nq = 0, nk = 0, wq = 0, wk = 0, tiles_q, tiles_k, work_q, work_k;  // work: steps of all tiles
+  uint64_t nq = 0, nk = 0, sum_q, sum_k;
+  uint32_t wq = 0, wk = 0, work_q, work_k;  // work: steps of all tiles
   for (int g = lo; g < hi; ++g) {
     const Segment r = segment(g);
     nq += q_tiles(r);
@@ -161,7 +164,13 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
     wq += q_tiles(r) * static_cast<uint32_t>(tiles_of(r.used));
     wk += k_tiles(r) * static_cast<uint32_t>(kv_steps(r, group));
   }
-  uint32_t at_q = exclusive_scan(nq, s_warp, tiles_q), at_k = exclusive_scan(nk, s_warp, tiles_k);
+  uint32_t at_q = static_cast<uint32_t>(exclusive_scan(nq, s_warp64, sum_q));
+  uint32_t at_k = static_cast<uint32_t>(exclusive_scan(nk, s_warp64, sum_k));
+  // Segments that overlap can hold more tiles than the capacities (and more than 32 bits count): then no item.
+  const bool over = sum_q > (static_cast<uint64_t>(seg.capacity_q) / kTile + S) * seg.num_q_heads ||
+                    sum_k > (static_cast<uint64_t>(seg.capacity_k) / kTile + S) * seg.num_kv_heads;
+  if (over && tid == 0) record_error(err, kErrBadCuSeqlens);
+  const uint32_t tiles_q = over ? 0u : static_cast<uint32_t>(sum_q), tiles_k = over ? 0u : static_cast<uint32_t>(sum_k);
   exclusive_scan(wq, s_warp, work_q);
   exclusive_scan(wk, s_warp, work_k);
   uint32_t *pq = ws + kCrossBwdHeader, *pk = pq + S + 1;

@@ -109,19 +109,19 @@ __device__ __forceinline__ int pairs_of(int rows, int group) {
   return ((rows + kBlockM - 1) / kBlockM * group + 1) / 2;
 }
 
-__device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s_warp,
-                                                         uint32_t& total) {
+template <typename T>
+__device__ __forceinline__ T block_exclusive_scan(T v, T* s_warp, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  uint32_t before = 0, all = 0;
+  T before = 0, all = 0;
 #pragma unroll 1
   for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
     if (w < warp) before += s_warp[w];
@@ -144,6 +144,7 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
   __shared__ int s_rows[kSortMax], s_keys[kSortMax], s_order[kSortMax];
   __shared__ uint32_t s_prefix[kSortMax + 1];
   __shared__ uint32_t s_warp[kPlanThreads / 32];
+  __shared__ uint64_t s_warp64[kPlanThreads / 32];
   __shared__ uint32_t s_cut, s_most;
   __shared__ uint2 s_item[kSplitMaxEntries / 2];  // of the last wave: where it starts, its key tiles
   __shared__ uint4 s_at[kSplitMaxEntries / 2];    // of each CTA: where its share starts, cuts before it
@@ -175,9 +176,18 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
   };
   const int chunk = (S + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
   const int lo = min(S, tid * chunk), hi = min(S, lo + chunk);
-  uint32_t local = 0, total;
+  uint64_t local = 0, items;
   for (int i = lo; i < hi; ++i) local += items_at(i);
-  uint32_t run = block_exclusive_scan(local, s_warp, total);
+  uint32_t run = static_cast<uint32_t>(block_exclusive_scan(local, s_warp64, items));
+  // Segments that overlap can hold more tiles than the capacity (and more than 32 bits count): then no item.
+  if (items > (static_cast<uint64_t>(seg.capacity_q) / kBlockM + S) * seg.num_q_heads) {
+    if (tid == 0) {
+      record_error(err, kErrBadCuSeqlens);
+      ws[0] = ws[2] = ws[3] = 0;
+    }
+    return;
+  }
+  const uint32_t total = static_cast<uint32_t>(items);
   for (int i = lo; i < hi; ++i) {
     order[i] = static_cast<uint32_t>(sorted ? s_order[i] : i);
     prefix[i] = run;
@@ -253,12 +263,12 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
   }
   uint32_t cuts;
   const uint32_t before = block_exclusive_scan(tid < wave && at.y > 0 ? 1u : 0u, s_warp, cuts);
-  uint32_t* items = reinterpret_cast<uint32_t*>(split_area + split_items_offset());
+  uint32_t* listed = reinterpret_cast<uint32_t*>(split_area + split_items_offset());
   if (tid < wave) {
     s_at[tid] = make_uint4(at.x, at.y, before, 0u);
-    items[wave + tid] = at.x + before + (at.y > 0 ? 1u : 0u);
+    listed[wave + tid] = at.x + before + (at.y > 0 ? 1u : 0u);
   }
-  if (tid == 0) items[2 * wave] = R + cuts;
+  if (tid == 0) listed[2 * wave] = R + cuts;
   __syncthreads();
   if (mine) {
     // the cuts inside this item, in order: CTAs whose share starts inside it
@@ -270,7 +280,7 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
     for (; last < static_cast<uint32_t>(wave) && s_at[last].x == static_cast<uint32_t>(tid); ++last)
       c += s_at[last].y > 0;
     const uint32_t first = tid + earlier;
-    if (c > 1) items[atomicAdd(&s_cut, 1u)] = first;  // listed for the merge; the list's order is immaterial
+    if (c > 1) listed[atomicAdd(&s_cut, 1u)] = first;  // listed for the merge; the list's order is immaterial
     e.first = static_cast<int>(first);
     e.chunks = c;
     e.kv0 = 0;

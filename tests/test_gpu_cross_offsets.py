@@ -1,9 +1,12 @@
-"""Offsets that the cross attention calls meet on the device: changed between calls by the kernel before."""
+"""Offsets that the cross attention calls meet on the device: changed between calls by the kernel before,
+and overlapping."""
 import numpy as np
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+
+BAD_OFFSETS = 3  # H3_ERR_BAD_CU_SEQLENS
 
 
 @pytest.fixture(scope="module")
@@ -84,3 +87,28 @@ def test_offsets_written_by_the_kernel_before(h3, dev, name, captured):
         for i, r in enumerate(results):
             assert all(torch.equal(a, b) for a, b in zip(r, want[i % 2]))
     assert h3.get_device_error(dev) == 0
+
+
+def _overlapping(dev, segments, rows):
+    """Every other segment is all rows, those between run backwards."""
+    return _i32(dev, *[(i % 2) * rows for i in range(segments + 1)])
+
+
+def test_overlapping_query_segments_are_refused(h3, dev):
+    # 32 segments of all 4,096 rows: more tiles than 4,096 rows and 64 segments can hold
+    n, s = 4096, 64
+    q, k, do = _random(dev, n, 2, 64), _random(dev, n, 2, 64, seed=1), _random(dev, n, 2, 64, seed=2)
+    even = _i32(dev, *range(0, n + 1, n // s))
+    want, lse = h3.varlen_cross_attn_fwd(q, k, k, even, even, n // s, n // s, return_lse=True)
+    out, l2 = torch.full_like(q, 7.0), torch.full_like(lse, 7.0)
+    assert h3.get_device_error(dev) == 0
+    h3.varlen_cross_attn_fwd(q, k, k, _overlapping(dev, s, n), even, n, n // s, out=out, lse=l2)
+    assert h3.get_device_error(dev) == BAD_OFFSETS
+    assert (out == 7.0).all() and (l2 == 7.0).all()
+    grads = [torch.full_like(q, 7.0) for _ in range(3)]
+    for cu_q, cu_k, most in ((_overlapping(dev, s, n), even, (n, n // s)), (even, _overlapping(dev, s, n), (n // s, n))):
+        h3.varlen_cross_attn_bwd(do, q, k, k, want, lse, cu_q, cu_k, *most, dq=grads[0], dk=grads[1], dv=grads[2])
+        assert h3.get_device_error(dev) == BAD_OFFSETS
+        assert all((g == 7.0).all() for g in grads)
+    again, l3 = h3.varlen_cross_attn_fwd(q, k, k, even, even, n // s, n // s, return_lse=True)
+    assert h3.get_device_error(dev) == 0 and torch.equal(again, want) and torch.equal(l3, lse)
