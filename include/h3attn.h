@@ -200,7 +200,9 @@ H3_API size_t h3_varlen_attn_workspace_size(int32_t num_segments, int32_t num_he
  * o           : device bf16 [capacity, H, D]; rows of every segment written, others untouched.
  * lse         : device fp32 [H, capacity] (natural log) or NULL.
  * cu_seqlens  : device int32 [num_segments + 1]; must start at 0, not decrease, end <= capacity.
- *               Empty segments are allowed.
+ *               Empty segments are allowed.  When offsets run backwards and segments overlap
+ *               until they hold more 256-row items per head than capacity / 256 + num_segments,
+ *               no row need be written.
  * max_seqlen  : host upper bound on the longest segment.  A longer segment is still computed in
  *               full but reported as H3_ERR_BAD_CU_SEQLENS.
  * softmax_scale: <= 0 selects 1/sqrt(head_dim).

@@ -394,24 +394,24 @@ attn_merge_kernel(const uint32_t* __restrict__ ws, const uint8_t* __restrict__ s
 
 // Exclusive prefix sum over the block (kPlanThreads threads) of one value per thread, and the
 // total: a shuffle scan inside each warp, then the warps' totals through shared memory.
-__device__ __forceinline__ uint32_t block_exclusive_scan(uint32_t v, uint32_t* s_warp,
-                                                         uint32_t& total) {
+template <typename T>
+__device__ __forceinline__ T block_exclusive_scan(T v, T* s_warp, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();  // s_warp may still be read from a previous call
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
   if (warp == 0) {  // exclusive scan of the warps' totals (32 warps), total in the last slot
-    const uint32_t t = s_warp[lane];
-    uint32_t y = t;
+    const T t = s_warp[lane];
+    T y = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
+      const T z = __shfl_up_sync(0xffffffffu, y, o);
       if (lane >= o) y += z;
     }
     s_warp[lane] = y - t;
@@ -429,6 +429,7 @@ attn_plan_kernel(const int32_t* __restrict__ cu, int num_segments, int capacity,
   __shared__ int s_len[kSortMax];
   __shared__ uint32_t s_prefix[kSortMax + 1];   // the item prefix again, for the split's lookups
   __shared__ uint32_t s_warp[kPlanThreads / 32 + 1];
+  __shared__ uint64_t s_warp64[kPlanThreads / 32 + 1];
   __shared__ uint32_t s_ngroups;
   grid_dependency_wait();  // cu_seqlens may come from the kernel before this one
   launch_dependents();     // the attention kernel may be scheduled now; it waits for this plan
@@ -459,10 +460,18 @@ attn_plan_kernel(const int32_t* __restrict__ cu, int num_segments, int capacity,
   // exclusive prefix of items over the ordered segments: per-thread chunks + block scan
   const int chunk = (S + kPlanThreads - 1) / kPlanThreads;
   const int lo = min(S, tid * chunk), hi = min(S, lo + chunk);
-  uint32_t local = 0;
+  uint64_t local = 0, items;
   for (int i = lo; i < hi; ++i) local += items_of(len_of(static_cast<int>(order[i])), num_heads);
-  uint32_t total;
-  uint32_t run = block_exclusive_scan(local, s_warp, total);
+  uint32_t run = static_cast<uint32_t>(block_exclusive_scan(local, s_warp64, items));
+  // Segments that overlap can hold more items than the capacity (and more than 32 bits count): then none.
+  if (items > (static_cast<uint64_t>(capacity) / kRowsPerItem + S) * num_heads) {
+    if (tid == 0) {
+      record_error(err, kErrBadCuSeqlens);
+      ws[0] = ws[1] = ws[2] = ws[3] = 0;
+    }
+    return;
+  }
+  const uint32_t total = static_cast<uint32_t>(items);
   for (int i = lo; i < hi; ++i) {
     prefix[i] = run;
     if (sorted) s_prefix[i] = run;

@@ -112,3 +112,15 @@ def test_overlapping_query_segments_are_refused(h3, dev):
         assert all((g == 7.0).all() for g in grads)
     again, l3 = h3.varlen_cross_attn_fwd(q, k, k, even, even, n // s, n // s, return_lse=True)
     assert h3.get_device_error(dev) == 0 and torch.equal(again, want) and torch.equal(l3, lse)
+
+
+def test_overlapping_packed_segments_are_refused(h3, dev):
+    n, s = 4096, 64
+    q = _random(dev, n, 2, 64)
+    out, lse = torch.full_like(q, 7.0), torch.full((2, n), 7.0, device=dev)
+    assert h3.get_device_error(dev) == 0
+    h3.varlen_attn_fwd(q, q, q, _overlapping(dev, s, n), n, out=out, lse=lse)
+    assert h3.get_device_error(dev) == BAD_OFFSETS
+    assert (out == 7.0).all() and (lse == 7.0).all()
+    h3.varlen_attn_fwd(q, q, q, _i32(dev, *range(0, n + 1, n // s)), n // s, out=out, lse=lse)
+    assert h3.get_device_error(dev) == 0 and not (out == 7.0).any() and not (lse == 7.0).any()
