@@ -254,8 +254,8 @@ H3_API h3_status h3_varlen_attn_fwd_noalloc(const void* q, const void* k, const 
  * Query head h reads key head h / (num_q_heads / num_kv_heads).  Per row, as h3_varlen_attn_fwd:
  *   S_ij = scale * <q_i, k_j>;  P = softmax_j(S);  o_i = sum_j P_ij v_j;  lse_i = log sum_j exp(S_ij)
  * Keys that a segment does not use get weight exactly zero (they are never multiplied in, so
- * NaN/Inf there cannot leak).  A segment without keys gives o = 0 and lse = -inf.  With equal
- * offsets and head counts this is h3_varlen_attn_fwd. */
+ * NaN/Inf there cannot leak).  A segment without keys gives o = 0 and lse = -inf, as does a row whose
+ * scores are all -inf.  With equal offsets and head counts this is otherwise h3_varlen_attn_fwd. */
 typedef struct {
   int32_t num_segments;
   int32_t max_seqlen_q; /* host upper bound on the query rows of a segment, <= capacity_q */

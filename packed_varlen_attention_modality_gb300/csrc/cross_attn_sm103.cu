@@ -1022,11 +1022,12 @@ cross_merge_kernel(const uint32_t* __restrict__ ws, const uint8_t* __restrict__ 
       }
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      for (int ch = lane16; ch < en.chunks; ch += 16) den += __expf(s_w[r][ch] - mx);
+      const float base = mx == -INFINITY ? 0.f : mx;  // no chunk has weights: o is 0, the LSE -inf
+      for (int ch = lane16; ch < en.chunks; ch += 16) den += __expf(s_w[r][ch] - base);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-      const float all = mx + logf(den);
-      for (int ch = lane16; ch < en.chunks; ch += 16) s_w[r][ch] = __expf(s_w[r][ch] - all);
+      const float all = base + logf(den);
+      for (int ch = lane16; ch < en.chunks; ch += 16) s_w[r][ch] = den == 0.f ? 0.f : __expf(s_w[r][ch] - all);
       if (lane16 == 0 && lse != nullptr && row0 + r < seg_end)
         lse[static_cast<size_t>(head) * seg.capacity_q + row0 + r] = all;
     }
