@@ -315,6 +315,7 @@ H3_API size_t h3_varlen_cross_attn_bwd_workspace_size(const h3_cross_attn_desc* 
  *               untouched.  Must not overlap an input.
  * workspace   : device, h3_varlen_cross_attn_bwd_workspace_size() bytes, 16-byte aligned; need not be
  *               initialised.  Calls that may run at the same time need separate workspaces.
+ * A row whose lse is -inf has no weights: its dq is 0 and it adds nothing to dk and dv.
  * Sums over queries and keys are taken in a fixed order: the result does not depend on timing.
  * A side with capacity 0 may be NULL.  Bad segments and overlapping ones (here on either side) as for the
  * forward; a skipped segment's rows are not written on either side.

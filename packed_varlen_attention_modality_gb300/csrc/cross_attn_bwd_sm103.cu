@@ -72,6 +72,12 @@ __device__ __forceinline__ bool valid_segment(const CrossSegments& s, int g, con
          (g > 0 || (r.q0 == 0 && r.k0 == 0));
 }
 
+// A row's LSE in units of log 2 as the exponent's offset.  A row without weights (LSE -inf: no keys, or
+// all scores -inf) gets +inf, so that its weights are exp2(S - inf) = 0 and it takes no part.
+__device__ __forceinline__ float lse_log2(float lse) {
+  return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+}
+
 // ---- plan ------------------------------------------------------------------------------------------
 // Tiles of each kernel are numbered over the segments (head-major within one).  Whole waves of tiles are
 // an item each; the tiles behind them are cut into `chunks` items each.
@@ -631,7 +637,7 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {  // rows past the end: weight exp2(0 - inf) = 0
           const int r = row + lane + 32 * x;
-          l[x] = r < d.q_end ? a.lse[at + r] * 1.4426950408889634f : INFINITY;
+          l[x] = r < d.q_end ? lse_log2(a.lse[at + r]) : INFINITY;
           e[x] = r < d.q_end ? a.delta[at + r] : 0.f;
         }
         ok = wait_long(st_empty(s), ((n / SO) & 1) ^ 1);
@@ -1010,7 +1016,7 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
       const int64_t at = d.q_row * step + d.head * kLanes + lane % kLanes;
       const int rows = min(kTile, d.q_end - d.q_row);
       const size_t stats = static_cast<size_t>(d.head) * a.seg.capacity_q + d.q_row;
-      s_rows[(k & 1) * kTile + row].x = row < rows ? a.lse[stats + row] * 1.4426950408889634f : 0.f;
+      s_rows[(k & 1) * kTile + row].x = row < rows ? lse_log2(a.lse[stats + row]) : 0.f;
 #pragma unroll 1
       for (int r0 = (warp & 3) * 32; r0 < (warp & 3) * 32 + 32; r0 += kRows * kUnroll) {
         uint4 x[kUnroll], y[kUnroll];

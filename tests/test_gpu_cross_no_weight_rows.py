@@ -1,7 +1,8 @@
 """Rows whose scores are all -inf: the query's products with every key of its segment overflow fp32.
-Such a row has no weights, as one of a segment without keys: o = 0 and lse = -inf, however the work is
-cut.  The rows next to it are checked against the fp64 oracle with the tolerances of
-test_gpu_cross_attn.py.
+Such a row has no weights, as one of a segment without keys: o = 0, lse = -inf, and a gradient of 0
+in which it takes no part -- however the work is cut.  The rows next to it are checked against the fp64
+oracle with the tolerances of test_gpu_cross_attn.py and test_gpu_cross_attn_bwd.py (the oracle is given a
+gradient of 0 for the rows without weights, so that they add nothing to its dk and dv).
 
 Queries of -3e38 and keys of at least 0.1: 64 products of -3e37 or less are beyond fp32's 3.4e38, and with
 one sign only no NaN can arise on the way.
@@ -10,7 +11,9 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 from tests.test_gpu_cross_attn import HALF, Case
+from tests.test_gpu_cross_attn_bwd import _check as check_gradient
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +70,18 @@ def test_forward(h3, dev, name):
     err = np.abs(got.numpy() - o)[ok]
     assert np.all(err <= ((HALF + 2e-4) * (1 + HALF) * size + HALF * np.abs(o))[ok])
     assert np.all(np.abs(gl.numpy() - l.T)[ok] <= 1e-4 * np.maximum(np.abs(l.T), 1.0)[ok])
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_gradient(h3, dev, name):
+    c, bad = _case(name)
+    args, where = c.on(dev)
+    o, l, _ = c.reference()
+    out, lse = torch.full(c.q.shape, float("nan")), torch.full((c.q.shape[1], c.cq), float("nan"))
+    out[:c.nq], lse[:, :c.nq] = torch.from_numpy(o).float(), torch.from_numpy(l).float()
+    out[bad], lse.T[bad] = 0.0, float("-inf")
+    got = h3.varlen_cross_attn_bwd(c.do.to(dev), **args, out=out.to(torch.bfloat16).to(dev), lse=lse.to(dev), **where)
+    assert h3.get_device_error(dev) == 0
+    assert (got[0].cpu()[bad] == 0).all()
+    c.do[bad] = 0.0
+    check_gradient(c, got)
