@@ -67,7 +67,9 @@ typedef enum {
   H3_ERR_TIMEOUT = 7,         /* (device) a bounded wait inside a kernel ran out */
   H3_ERR_MISALIGNED = 8,      /* a device pointer or row size is not 16-byte aligned */
   H3_ERR_BAD_PERM = 9,        /* (device) a permutation entry is out of range */
-  H3_ERR_BAD_BLOCK_INDEX = 10 /* (device) a selected VSA block index is out of range */
+  H3_ERR_BAD_BLOCK_INDEX = 10, /* (device) a selected VSA block index is out of range */
+  H3_ERR_SMEM_LAYOUT = 11     /* (device) a kernel's shared memory does not start on a 1024-byte boundary:
+                                 nothing was computed (not met on any known driver) */
 } h3_status;
 
 enum { H3_TAG_TEXT = 0, H3_TAG_VIDEO = 1, H3_TAG_AUDIO = 2 };
@@ -319,7 +321,7 @@ H3_API size_t h3_varlen_cross_attn_bwd_workspace_size(const h3_cross_attn_desc* 
  * Sums over queries and keys are taken in a fixed order: the result does not depend on timing.
  * A side with capacity 0 may be NULL.  Bad segments and overlapping ones (here on either side) as for the
  * forward; a skipped segment's rows are not written on either side.
- * Errors: as h3_varlen_cross_attn_fwd. */
+ * Errors: as h3_varlen_cross_attn_fwd; also device-side H3_ERR_SMEM_LAYOUT. */
 H3_API h3_status h3_varlen_cross_attn_bwd(const h3_cross_attn_desc* desc, const void* dout,
                                           const void* q, const void* k, const void* v,
                                           const void* o, const float* lse,

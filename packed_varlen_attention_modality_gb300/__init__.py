@@ -56,7 +56,8 @@ _lib = None
 
 _STATUS = {0: "H3_OK", 1: "H3_ERR_NULL", 2: "H3_ERR_INVALID_ARG", 3: "H3_ERR_BAD_CU_SEQLENS",
            4: "H3_ERR_UNSUPPORTED", 5: "H3_ERR_WORKSPACE", 6: "H3_ERR_CUDA", 7: "H3_ERR_TIMEOUT",
-           8: "H3_ERR_MISALIGNED", 9: "H3_ERR_BAD_PERM", 10: "H3_ERR_BAD_BLOCK_INDEX"}
+           8: "H3_ERR_MISALIGNED", 9: "H3_ERR_BAD_PERM", 10: "H3_ERR_BAD_BLOCK_INDEX",
+           11: "H3_ERR_SMEM_LAYOUT"}
 
 
 class H3Error(RuntimeError):

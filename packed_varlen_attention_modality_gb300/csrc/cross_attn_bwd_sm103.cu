@@ -429,7 +429,7 @@ cross_dkv_kernel(const __grid_constant__ CrossBwdArgs a) {
   const uint32_t total = plan_of(a.plan).items_k;
   if (blockIdx.x >= total) return;
   if ((smem_u32(smem) & 1023u) != 0) {  // the tiles' swizzle needs it; not met on any known driver
-    if (threadIdx.x == 0) record_error(a.err, kErrTimeout);
+    if (threadIdx.x == 0) record_error(a.err, kErrSmemLayout);
     return;
   }
   if (warp == 8 && lane == 0) {
@@ -823,7 +823,10 @@ cross_bwd_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
             (static_cast<int64_t>(keys ? r.k0 : r.q0) + row_tile) * x.stride + head * D;
     return x;
   };
-  if (a.err != nullptr && *reinterpret_cast<const volatile unsigned int*>(a.err) == kErrTimeout) return;
+  if (a.err != nullptr) {  // the sums are incomplete
+    const unsigned int code = *reinterpret_cast<const volatile unsigned int*>(a.err);
+    if (code == kErrTimeout || code == kErrSmemLayout) return;
+  }
   for (uint32_t u = blockIdx.x; u < units_k + units_q; u += gridDim.x) {
     const Unit x = locate(u);
     if (x.chunks == 1) continue;  // written already
@@ -954,7 +957,7 @@ cross_dq_kernel(const __grid_constant__ CrossBwdArgs a) {
   const uint32_t total = plan_of(a.plan).items_q;
   if (blockIdx.x >= total) return;
   if ((smem_u32(smem) & 1023u) != 0) {  // the tiles' swizzle needs it; not met on any known driver
-    if (threadIdx.x == 0) record_error(a.err, kErrTimeout);
+    if (threadIdx.x == 0) record_error(a.err, kErrSmemLayout);
     return;
   }
   if (warp == 8 && lane == 0) {

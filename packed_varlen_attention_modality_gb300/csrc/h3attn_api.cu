@@ -195,6 +195,7 @@ const char* h3_status_string(h3_status s) {
     case H3_ERR_MISALIGNED: return "a device pointer or row size is not 16-byte aligned";
     case H3_ERR_BAD_PERM: return "a permutation entry is out of range";
     case H3_ERR_BAD_BLOCK_INDEX: return "a selected block index is out of range";
+    case H3_ERR_SMEM_LAYOUT: return "a kernel's shared memory does not start on a 1024-byte boundary";
   }
   return "unknown status";
 }

@@ -16,6 +16,7 @@ enum : unsigned int {
   kErrTimeout = 7,
   kErrBadPerm = 9,
   kErrBadBlockIndex = 10,
+  kErrSmemLayout = 11,
 };
 
 // Longest legitimate wait inside one kernel is microseconds; give up after 2 s.
