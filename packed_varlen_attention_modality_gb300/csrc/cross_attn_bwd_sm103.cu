@@ -108,13 +108,12 @@ __device__ __forceinline__ int step_at(int n, int c, int chunks) {
 }
 
 // Exclusive sum over the block (whole warps) and the total.
-template <typename T>
-__device__ __forceinline__ T exclusive_scan(T v, T* s_warp, T& total) {
+__device__ __forceinline__ uint64_t exclusive_scan(uint64_t v, uint64_t* s_warp, uint64_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  T x = v;
+  uint64_t x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (warps == 1) {
@@ -124,7 +123,7 @@ __device__ __forceinline__ T exclusive_scan(T v, T* s_warp, T& total) {
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  T before = 0;
+  uint64_t before = 0;
   total = 0;
 #pragma unroll 1
   for (int w = 0; w < warps; ++w) {
@@ -139,8 +138,7 @@ __device__ __forceinline__ T exclusive_scan(T v, T* s_warp, T& total) {
 __global__ void __launch_bounds__(kPlanThreads)
 cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws, int slots, uint32_t sms,
                       unsigned int* err) {
-  __shared__ uint32_t s_warp[kPlanThreads / 32];
-  __shared__ uint64_t s_warp64[kPlanThreads / 32];
+  __shared__ uint64_t s_warp[kPlanThreads / 32];
   grid_dependency_wait();
   launch_dependents();
   const int S = seg.num_segments, tid = threadIdx.x, group = seg.num_q_heads / seg.num_kv_heads;
@@ -162,16 +160,16 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
   if (chunk == 1 && lo < hi) mine = checked(lo);
   auto segment = [&](int g) { return chunk == 1 ? mine : checked(g); };
   uint64_t nq = 0, nk = 0, sum_q, sum_k;
-  uint32_t wq = 0, wk = 0, work_q, work_k;  // work: steps of all tiles
+  uint64_t wq = 0, wk = 0, work_q, work_k;  // work: steps of all tiles (rows x keys x heads pass 32 bits first)
   for (int g = lo; g < hi; ++g) {
     const Segment r = segment(g);
     nq += q_tiles(r);
     nk += k_tiles(r);
-    wq += q_tiles(r) * static_cast<uint32_t>(tiles_of(r.used));
-    wk += k_tiles(r) * static_cast<uint32_t>(kv_steps(r, group));
+    wq += static_cast<uint64_t>(q_tiles(r)) * tiles_of(r.used);
+    wk += static_cast<uint64_t>(k_tiles(r)) * kv_steps(r, group);
   }
-  uint32_t at_q = static_cast<uint32_t>(exclusive_scan(nq, s_warp64, sum_q));
-  uint32_t at_k = static_cast<uint32_t>(exclusive_scan(nk, s_warp64, sum_k));
+  uint32_t at_q = static_cast<uint32_t>(exclusive_scan(nq, s_warp, sum_q));
+  uint32_t at_k = static_cast<uint32_t>(exclusive_scan(nk, s_warp, sum_k));
   // Segments that overlap can hold more tiles than the capacities (and more than 32 bits count): then no item.
   const bool over = sum_q > (static_cast<uint64_t>(seg.capacity_q) / kTile + S) * seg.num_q_heads ||
                     sum_k > (static_cast<uint64_t>(seg.capacity_k) / kTile + S) * seg.num_kv_heads;

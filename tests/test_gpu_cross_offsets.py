@@ -1,12 +1,12 @@
 """Offsets that the cross attention calls meet on the device: changed between calls by the kernel before,
-and overlapping."""
+overlapping, and with lengths whose products pass 32 bits."""
 import numpy as np
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
 
-BAD_OFFSETS = 3  # H3_ERR_BAD_CU_SEQLENS
+BAD_OFFSETS, TIMEOUT = 3, 7  # H3_ERR_BAD_CU_SEQLENS, H3_ERR_TIMEOUT
 
 
 @pytest.fixture(scope="module")
@@ -124,3 +124,43 @@ def test_overlapping_packed_segments_are_refused(h3, dev):
     assert (out == 7.0).all() and (lse == 7.0).all()
     h3.varlen_attn_fwd(q, q, q, _i32(dev, *range(0, n + 1, n // s)), n // s, out=out, lse=lse)
     assert h3.get_device_error(dev) == 0 and not (out == 7.0).any() and not (lse == 7.0).any()
+
+
+def _chunks(sms, slots, tiles, steps):
+    """The gradient plan's rule: chunks of the tiles behind the whole waves."""
+    rest, best = tiles % sms, (float("inf"), 0)
+    for c in range(1, 17):
+        cost = np.float32(-(-rest * c // sms)) * (np.float32(steps) / np.float32(c) + np.float32(3))
+        cost += np.float32(2 if c > 1 else 0)
+        if c > 1 and rest * c > slots:
+            continue
+        best = min(best, (float(cost), c))
+    return best[1]
+
+
+def test_work_of_the_plan_past_32_bits(h3, dev):
+    """2^32 steps in all.  The loaders stop after three tiles, as in test_gpu_cross_timeout.py, so the two
+    product kernels leave by their waits' limit; the plan before them is complete."""
+    nq, nk, heads = 1 << 20, 1 << 24, 4
+    q, k = (torch.zeros(n, h, 64, dtype=torch.bfloat16, device=dev) for n, h in ((nq, heads), (nk, 1)))
+    lse = torch.zeros(heads, nq, device=dev)
+    size = h3.varlen_cross_attn_bwd_workspace_size(1, nq, nk, nq, nk, heads, 1, 64)
+    ws = torch.zeros(size, dtype=torch.uint8, device=dev)
+    assert h3.get_device_error(dev) == 0
+    h3.set_wait_limit_ns(20_000_000)
+    h3.debug_stall_loads(3)
+    try:
+        h3.varlen_cross_attn_bwd(q, q, k, k, q, lse, _i32(dev, 0, nq), _i32(dev, 0, nk), nq, nk, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        h3.debug_stall_loads(-1)
+        h3.set_wait_limit_ns(0)
+    assert h3.get_device_error(dev) == TIMEOUT
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    q_tiles, k_tiles = nq // 128 * heads, nk // 128
+    slots = 4 * 152
+    items_q, items_k, whole_q, whole_k, chunks_q, chunks_k = ws[:24].view(torch.int32).tolist()
+    assert (whole_q, whole_k) == (q_tiles - q_tiles % sms, k_tiles - k_tiles % sms)
+    assert chunks_q == _chunks(sms, slots, q_tiles, nk // 128) > 1
+    assert chunks_k == _chunks(sms, slots, k_tiles, heads * nq // 128) > 1
+    assert items_q == whole_q + q_tiles % sms * chunks_q and items_k == whole_k + k_tiles % sms * chunks_k
