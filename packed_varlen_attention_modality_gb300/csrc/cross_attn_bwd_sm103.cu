@@ -107,38 +107,53 @@ __device__ __forceinline__ int step_at(int n, int c, int chunks) {
   return static_cast<int>(static_cast<int64_t>(n) * c / chunks);
 }
 
-// Exclusive sum over the block (whole warps) and the total.
-__device__ __forceinline__ uint64_t exclusive_scan(uint64_t v, uint64_t* s_warp, uint64_t& total) {
+// Tiles and steps of each kernel.  Tiles are counted in 64 bits: overlapping segments can hold more than 32
+// bits count.  Of the steps (rows x keys x heads pass 32 bits first) only the mean is wanted.
+struct PlanSums {
+  uint64_t tiles_q, tiles_k;
+  float steps_q, steps_k;
+  __device__ __forceinline__ void add(const PlanSums& o) {
+    tiles_q += o.tiles_q;
+    tiles_k += o.tiles_k;
+    steps_q += o.steps_q;
+    steps_k += o.steps_k;
+  }
+  __device__ __forceinline__ PlanSums shfl(int from) const {
+    return PlanSums{__shfl_sync(0xffffffffu, tiles_q, from), __shfl_sync(0xffffffffu, tiles_k, from),
+                    __shfl_sync(0xffffffffu, steps_q, from), __shfl_sync(0xffffffffu, steps_k, from)};
+  }
+};
+// Sum over the block's threads (whole warps) before this one (tiles only) and over all; the four sums' shuffles
+// overlap.
+__device__ __forceinline__ PlanSums exclusive_scan(const PlanSums& v, PlanSums* s_warp, PlanSums& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  uint64_t x = v;
+  PlanSums x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const PlanSums y = x.shfl((lane - o) & 31);
+    if (lane >= o) x.add(y);
   }
-  if (warps == 1) {
-    total = __shfl_sync(0xffffffffu, x, 31);
-    return x - v;
-  }
+  total = x.shfl(31);
+  x.tiles_q -= v.tiles_q;
+  x.tiles_k -= v.tiles_k;
+  if (warps == 1) return x;
+  if (lane == 31) s_warp[warp] = total;
   __syncthreads();
-  if (lane == 31) s_warp[warp] = x;
-  __syncthreads();
-  uint64_t before = 0;
-  total = 0;
+  total = PlanSums{};
 #pragma unroll 1
   for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
+    if (w == warp) x.add(total);
+    total.add(s_warp[w]);
   }
-  return before + x - v;
+  return x;
 }
 
-// One block: a warp when the segments fit its lanes (three short scans, no block barrier), else 1,024
+// One block: a warp when the segments fit its lanes (one scan, no block barrier), else 1,024
 // threads with several segments each.
 __global__ void __launch_bounds__(kPlanThreads)
 cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restrict__ ws, int slots, uint32_t sms,
                       unsigned int* err) {
-  __shared__ uint64_t s_warp[kPlanThreads / 32];
+  __shared__ PlanSums s_warp[kPlanThreads / 32];
   grid_dependency_wait();
   launch_dependents();
   const int S = seg.num_segments, tid = threadIdx.x, group = seg.num_q_heads / seg.num_kv_heads;
@@ -159,24 +174,21 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
   Segment mine{};  // this thread's only segment, when it has one
   if (chunk == 1 && lo < hi) mine = checked(lo);
   auto segment = [&](int g) { return chunk == 1 ? mine : checked(g); };
-  uint64_t nq = 0, nk = 0, sum_q, sum_k;
-  uint64_t wq = 0, wk = 0, work_q, work_k;  // work: steps of all tiles (rows x keys x heads pass 32 bits first)
+  PlanSums own{}, all;
   for (int g = lo; g < hi; ++g) {
     const Segment r = segment(g);
-    nq += q_tiles(r);
-    nk += k_tiles(r);
-    wq += static_cast<uint64_t>(q_tiles(r)) * tiles_of(r.used);
-    wk += static_cast<uint64_t>(k_tiles(r)) * kv_steps(r, group);
+    const uint32_t nq = q_tiles(r), nk = k_tiles(r);
+    own.add(PlanSums{nq, nk, static_cast<float>(nq) * static_cast<float>(tiles_of(r.used)),
+                     static_cast<float>(nk) * static_cast<float>(kv_steps(r, group))});
   }
-  uint32_t at_q = static_cast<uint32_t>(exclusive_scan(nq, s_warp, sum_q));
-  uint32_t at_k = static_cast<uint32_t>(exclusive_scan(nk, s_warp, sum_k));
-  // Segments that overlap can hold more tiles than the capacities (and more than 32 bits count): then no item.
-  const bool over = sum_q > (static_cast<uint64_t>(seg.capacity_q) / kTile + S) * seg.num_q_heads ||
-                    sum_k > (static_cast<uint64_t>(seg.capacity_k) / kTile + S) * seg.num_kv_heads;
+  const PlanSums before = exclusive_scan(own, s_warp, all);
+  uint32_t at_q = static_cast<uint32_t>(before.tiles_q), at_k = static_cast<uint32_t>(before.tiles_k);
+  // Segments that overlap can hold more tiles than the capacities: then no item.
+  const bool over = all.tiles_q > (static_cast<uint64_t>(seg.capacity_q) / kTile + S) * seg.num_q_heads ||
+                    all.tiles_k > (static_cast<uint64_t>(seg.capacity_k) / kTile + S) * seg.num_kv_heads;
   if (over && tid == 0) record_error(err, kErrBadCuSeqlens);
-  const uint32_t tiles_q = over ? 0u : static_cast<uint32_t>(sum_q), tiles_k = over ? 0u : static_cast<uint32_t>(sum_k);
-  exclusive_scan(wq, s_warp, work_q);
-  exclusive_scan(wk, s_warp, work_k);
+  const uint32_t tiles_q = over ? 0u : static_cast<uint32_t>(all.tiles_q);
+  const uint32_t tiles_k = over ? 0u : static_cast<uint32_t>(all.tiles_k);
   uint32_t *pq = ws + kCrossBwdHeader, *pk = pq + S + 1;
   for (int g = lo; g < hi; ++g) {
     const Segment r = segment(g);
@@ -192,7 +204,7 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
   if (tid < 32) {
     const bool keys = tid >= 16;
     const uint32_t c = (tid & 15) + 1, tiles = keys ? tiles_k : tiles_q, rest = tiles % sms;
-    const float steps = tiles > 0 ? static_cast<float>(keys ? work_k : work_q) / static_cast<float>(tiles) : 0.f;
+    const float steps = tiles > 0 ? (keys ? all.steps_k : all.steps_q) / static_cast<float>(tiles) : 0.f;
     float cost = static_cast<float>((rest * c + sms - 1) / sms) * (steps / static_cast<float>(c) + 3.f) + (c > 1 ? 2.f : 0.f);
     if (c > kCrossBwdMaxChunks || (c > 1 && rest * c > static_cast<uint32_t>(slots))) cost = INFINITY;
     uint32_t best = c;
