@@ -124,7 +124,7 @@ H3_API h3_status h3_rope_apply(const void* q_in, void* q_out, const void* k_in, 
  *   y = the rotation of h3_rope_apply applied to z (tags, bands, start frames as there), or z
  *       itself when pos and tag are NULL (queries and keys of cross attention)
  * in one pass.  Sums and rotation are fp32 and the result is rounded to bf16 once.  The angle is
- * good to about 1e-7 turns at any position (fp32 radians are not used). */
+ * good to about 1e-7 turns for positions (shift included) up to 1e7 (fp32 radians are not used). */
 enum { H3_WEIGHT_F32 = 0, H3_WEIGHT_BF16 = 1 };
 
 typedef struct {

@@ -16,8 +16,9 @@
 // All arithmetic is fp32; the results are rounded to bf16 once.
 //
 // Angles are kept in turns as a pair of floats (coordinate and frequency both hi + lo), so the
-// phase is good to about 1e-7 turns whatever the position; fp32 radians would lose 1e-3 already at
-// position 10^4.
+// phase is good to about 1e-7 turns for positions up to 1e7: the product's remainder, itself a float, stays
+// under a fifth of a turn there (its three roundings: 2^-25 of it each), and a frequency's pair is off by
+// 2^-49 of it, 3e-9 turns.  fp32 radians would lose 1e-3 already at position 10^4.
 #include <cuda_bf16.h>
 
 #include "h3_internal.h"
