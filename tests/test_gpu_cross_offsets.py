@@ -1,8 +1,13 @@
 """Offsets that the cross attention calls meet on the device: changed between calls by the kernel before,
-overlapping, and with lengths whose products pass 32 bits."""
+overlapping, of many segments, and with lengths whose products pass 32 bits."""
 import numpy as np
 import pytest
 import torch
+
+from tests.test_gpu_cross_attn import Case
+from tests.test_gpu_cross_attn import _check as check_forward
+from tests.test_gpu_cross_attn_bwd import _check as check_gradient
+from tests.test_gpu_cross_attn_bwd import _given
 
 pytestmark = pytest.mark.gpu
 
@@ -124,6 +129,34 @@ def test_overlapping_packed_segments_are_refused(h3, dev):
     assert (out == 7.0).all() and (lse == 7.0).all()
     h3.varlen_attn_fwd(q, q, q, _i32(dev, *range(0, n + 1, n // s)), n // s, out=out, lse=lse)
     assert h3.get_device_error(dev) == 0 and not (out == 7.0).any() and not (lse == 7.0).any()
+
+
+def test_more_segments_than_threads_of_the_plan(h3, dev):
+    n = 2500  # three to a thread
+    c = Case([(7 * i) % 23 for i in range(n)], [(5 * i) % 31 for i in range(n)], 2, 2, 64, seed=3)
+    args, where = c.on(dev)
+    out, lse = h3.varlen_cross_attn_fwd(**args, **where, return_lse=True)
+    check_forward(c, out, lse)
+    out, lse = _given(c, dev)
+    got = h3.varlen_cross_attn_bwd(c.do.to(dev), **args, out=out, lse=lse, **where)
+    assert h3.get_device_error(dev) == 0
+    check_gradient(c, got)
+
+
+def test_as_many_segments_as_are_allowed(h3, dev):
+    # one row and one key each: the weight is 1, so o = v and dv = do exactly, and dS = dP - rowsum(do * o) is
+    # the difference of two fp32 sums of the same 64 products
+    n = 65535
+    q, do, v = (_random(dev, n, 1, 64, seed=s) for s in range(3))
+    cu = torch.arange(n + 1, dtype=torch.int32, device=dev)
+    out, lse = h3.varlen_cross_attn_fwd(q, q, v, cu, cu, 17, 1, return_lse=True)  # 17: not the form for tokens
+    assert torch.equal(out, v)
+    dq, dk, dv = h3.varlen_cross_attn_bwd(do, q, q, v, out, lse, cu, cu, 17, 1)
+    assert h3.get_device_error(dev) == 0
+    assert torch.equal(dv, do)
+    # two sums of 64 terms, 2^-24 relative a step, of sum |do v| < 100 (5 standard deviations over all rows),
+    # times scale |q| <= 0.125 * 6: 2 * 64 * 6e-8 * 100 * 0.75 = 6e-4
+    assert dq.float().abs().max() < 1e-3 and dk.float().abs().max() < 1e-3
 
 
 def _chunks(sms, slots, tiles, steps):
