@@ -36,6 +36,7 @@
 
 #include <cstddef>
 
+#include "cross_segments.cuh"
 #include "h3_internal.h"
 #include "launch.h"
 #include "sm103_ptx.cuh"
@@ -53,24 +54,6 @@ constexpr int kPlanThreads = 1024;
 
 __host__ __device__ constexpr int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 __device__ __forceinline__ int steps16(int n) { return (n + 15) / 16; }
-
-struct Segment {
-  int q0, rows, k0, keys, used;  // key rows of the segment and how many of them it uses
-};
-__device__ __forceinline__ Segment segment_of(const CrossSegments& s, int g) {
-  Segment r;
-  r.q0 = s.cu_q[g];
-  r.rows = s.cu_q[g + 1] - r.q0;
-  r.k0 = s.cu_k[g];
-  r.keys = s.cu_k[g + 1] - r.k0;
-  r.used = s.seqused_k != nullptr ? s.seqused_k[g] : r.keys;
-  return r;
-}
-__device__ __forceinline__ bool valid_segment(const CrossSegments& s, int g, const Segment& r) {
-  return r.q0 >= 0 && r.rows >= 0 && r.q0 <= s.capacity_q - r.rows && r.rows <= s.max_seqlen_q && r.k0 >= 0 &&
-         r.keys >= 0 && r.k0 <= s.capacity_k - r.keys && r.used >= 0 && r.used <= r.keys &&
-         (g > 0 || (r.q0 == 0 && r.k0 == 0));
-}
 
 // A row's LSE in units of log 2 as the exponent's offset.  A row without weights (LSE -inf: no keys, or
 // all scores -inf) gets +inf, so that its weights are exp2(S - inf) = 0 and it takes no part.
@@ -90,7 +73,7 @@ struct Plan {
 };
 static_assert(offsetof(Plan, prefix) == kCrossBwdHeader * sizeof(uint32_t), "the header's words");
 __device__ __forceinline__ const Plan& plan_of(const uint32_t* ws) { return *reinterpret_cast<const Plan*>(ws); }
-__device__ __forceinline__ int kv_steps(const Segment& r, int group) {  // (head, query tile) pairs
+__device__ __forceinline__ int kv_steps(const CrossSegment& r, int group) {  // (head, query tile) pairs
   return r.used > 0 ? group * tiles_of(r.rows) : 0;
 }
 // Item of a kernel -> tile and chunk.
@@ -159,24 +142,14 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
   const int S = seg.num_segments, tid = threadIdx.x, group = seg.num_q_heads / seg.num_kv_heads;
   const int chunk = (S + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
   const int lo = min(S, tid * chunk), hi = min(S, lo + chunk);
-  auto checked = [&](int g) {
-    Segment r = segment_of(seg, g);
-    if (!valid_segment(seg, g, r)) {
-      record_error(err, kErrBadCuSeqlens);
-      r.rows = r.keys = r.used = 0;
-    } else if (r.used > seg.max_seqlen_k) {
-      record_error(err, kErrBadCuSeqlens);  // computed all the same
-    }
-    return r;
-  };
-  auto q_tiles = [&](const Segment& r) { return static_cast<uint32_t>(tiles_of(r.rows)) * seg.num_q_heads; };
-  auto k_tiles = [&](const Segment& r) { return static_cast<uint32_t>(tiles_of(r.keys)) * seg.num_kv_heads; };
-  Segment mine{};  // this thread's only segment, when it has one
-  if (chunk == 1 && lo < hi) mine = checked(lo);
-  auto segment = [&](int g) { return chunk == 1 ? mine : checked(g); };
+  auto q_tiles = [&](const CrossSegment& r) { return static_cast<uint32_t>(tiles_of(r.rows)) * seg.num_q_heads; };
+  auto k_tiles = [&](const CrossSegment& r) { return static_cast<uint32_t>(tiles_of(r.keys)) * seg.num_kv_heads; };
+  CrossSegment mine{};  // this thread's only segment, when it has one
+  if (chunk == 1 && lo < hi) mine = checked_cross_segment(seg, lo, err);
+  auto segment = [&](int g) { return chunk == 1 ? mine : checked_cross_segment(seg, g, err); };
   PlanSums own{}, all;
   for (int g = lo; g < hi; ++g) {
-    const Segment r = segment(g);
+    const CrossSegment r = segment(g);
     const uint32_t nq = q_tiles(r), nk = k_tiles(r);
     own.add(PlanSums{nq, nk, static_cast<float>(nq) * static_cast<float>(tiles_of(r.used)),
                      static_cast<float>(nk) * static_cast<float>(kv_steps(r, group))});
@@ -191,7 +164,7 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
   const uint32_t tiles_k = over ? 0u : static_cast<uint32_t>(all.tiles_k);
   uint32_t *pq = ws + kCrossBwdHeader, *pk = pq + S + 1;
   for (int g = lo; g < hi; ++g) {
-    const Segment r = segment(g);
+    const CrossSegment r = segment(g);
     pq[g] = at_q;
     pk[g] = at_k;
     at_q += q_tiles(r);
@@ -341,7 +314,7 @@ __device__ __forceinline__ KvWork decode_kv(uint32_t item, const uint32_t* __res
   const uint32_t* prefix = plan.prefix + S + 1;
   const Cut cut = cut_of(item, plan.whole_k, plan.chunks_k);
   const int g = find_segment(prefix, S, cut.tile);
-  const Segment r = segment_of(seg, g);
+  const CrossSegment r = cross_segment(seg, g);
   const int tiles = tiles_of(r.keys), local = static_cast<int>(cut.tile - prefix[g]);
   KvWork d;
   d.more = 1;
@@ -817,7 +790,7 @@ cross_bwd_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
     const uint32_t tile = (keys ? plan.whole_k : plan.whole_q) + index;
     const int most = static_cast<int>(keys ? plan.chunks_k : plan.chunks_q);
     const int g = find_segment(prefix, S, tile);
-    const Segment r = segment_of(a.seg, g);
+    const CrossSegment r = cross_segment(a.seg, g);
     const int tiles = tiles_of(keys ? r.keys : r.rows), local = static_cast<int>(tile - prefix[g]);
     const int head = local / tiles, row_tile = local % tiles * kTile;
     const int steps = keys ? (row_tile < r.used ? kv_steps(r, group) : 0) : tiles_of(r.used);
@@ -871,7 +844,7 @@ __device__ __forceinline__ QWork decode_q(uint32_t item, const uint32_t* __restr
   const Plan& plan = plan_of(ws);
   const Cut cut = cut_of(item, plan.whole_q, plan.chunks_q);
   const int g = find_segment(plan.prefix, S, cut.tile);
-  const Segment r = segment_of(seg, g);
+  const CrossSegment r = cross_segment(seg, g);
   const int tiles = tiles_of(r.rows), local = static_cast<int>(cut.tile - plan.prefix[g]);
   const int steps = tiles_of(r.used), chunks = max(1, min(cut.chunks, steps));
   QWork d;

@@ -45,6 +45,7 @@
 // Every wait is bounded; a wait that runs out records a timeout and unwinds the CTA.
 #include <cuda_bf16.h>
 
+#include "cross_segments.cuh"
 #include "h3_internal.h"
 #include "launch.h"
 #include "sm103_ptx.cuh"
@@ -92,18 +93,6 @@ __host__ __device__ constexpr size_t split_partials_offset() {
 template <int D>
 constexpr size_t kPartial = static_cast<size_t>(kBlockM) * (D + 1);  // floats of a tile's partial
 
-// Rows and keys of segment g; an invalid segment has neither.
-__device__ __forceinline__ int2 checked_segment(const CrossSegments& s, int g, unsigned int* err) {
-  const int a = s.cu_q[g], b = s.cu_q[g + 1], ka = s.cu_k[g], kb = s.cu_k[g + 1];
-  const int used = s.seqused_k != nullptr ? s.seqused_k[g] : kb - ka;
-  if (a < 0 || b < a || b > s.capacity_q || b - a > s.max_seqlen_q || ka < 0 || kb < ka || kb > s.capacity_k || used < 0 ||
-      used > kb - ka || (g == 0 && (a != 0 || ka != 0))) {
-    record_error(err, kErrBadCuSeqlens);
-    return make_int2(0, 0);
-  }
-  if (used > s.max_seqlen_k) record_error(err, kErrBadCuSeqlens);  // computed all the same
-  return make_int2(b - a, used);
-}
 // Items of a segment per key head: pairs of its group * ceil(rows / 128) tiles.
 __device__ __forceinline__ int pairs_of(int rows, int group) {
   return ((rows + kBlockM - 1) / kBlockM * group + 1) / 2;
@@ -157,9 +146,9 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
   const int group = seg.num_q_heads / seg.num_kv_heads;
   if (sorted) {
     if (tid < S) {
-      const int2 n = checked_segment(seg, tid, err);
-      s_rows[tid] = n.x;
-      s_keys[tid] = n.y;
+      const CrossSegment r = checked_cross_segment(seg, tid, err);
+      s_rows[tid] = r.rows;
+      s_keys[tid] = r.used;
     }
     __syncthreads();
     if (tid < S) {  // most keys first, ties by position
@@ -171,7 +160,7 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
     __syncthreads();
   }
   auto items_at = [&](int i) -> uint32_t {  // of the segment in place i
-    const int rows = sorted ? s_rows[s_order[i]] : checked_segment(seg, i, err).x;
+    const int rows = sorted ? s_rows[s_order[i]] : checked_cross_segment(seg, i, err).rows;
     return static_cast<uint32_t>(pairs_of(rows, group)) * seg.num_kv_heads;
   };
   const int chunk = (S + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);

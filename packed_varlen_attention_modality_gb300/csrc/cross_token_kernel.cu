@@ -14,6 +14,7 @@
 // Scores, max, sum and O are fp32; P is rounded to bf16 for the product with V, o once at the end.
 #include <cuda_bf16.h>
 
+#include "cross_segments.cuh"
 #include "h3_internal.h"
 #include "launch.h"
 #include "sm103_ptx.cuh"
@@ -65,15 +66,8 @@ struct TokenSegment {
   int key0, keys;
 };
 __device__ __forceinline__ TokenSegment token_segment(const CrossSegments& s, int g, unsigned int* err) {
-  const int a = s.cu_q[g], b = s.cu_q[g + 1], ka = s.cu_k[g], kb = s.cu_k[g + 1];
-  const int used = s.seqused_k != nullptr ? s.seqused_k[g] : kb - ka;
-  if (a < 0 || b < a || b > s.capacity_q || b - a > s.max_seqlen_q || ka < 0 || kb < ka ||
-      kb > s.capacity_k || used < 0 || used > kb - ka || (g == 0 && (a != 0 || ka != 0))) {
-    record_error(err, kErrBadCuSeqlens);
-    return TokenSegment{0, 0, 0, 0};
-  }
-  if (used > s.max_seqlen_k) record_error(err, kErrBadCuSeqlens);  // computed all the same
-  return TokenSegment{a, (b - a) * (s.num_q_heads / s.num_kv_heads), ka, used};
+  const CrossSegment r = checked_cross_segment(s, g, err);
+  return TokenSegment{r.q0, r.rows * (s.num_q_heads / s.num_kv_heads), r.k0, r.used};
 }
 
 // Partial results of chunk c of (segment, key head) pair p: max_rows rows of D values, their LSEs.
