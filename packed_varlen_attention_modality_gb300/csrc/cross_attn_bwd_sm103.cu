@@ -172,7 +172,9 @@ cross_bwd_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __res
   }
   // Chunks of the tiles behind the whole waves: what makes their waves of items (of steps / c steps,
   // and about 3 steps' time of start and end each; 2 more for the sum of several chunks) shortest, as
-  // far as the slots reach.  Lanes 0-15 weigh 1 to 16 chunks for the query tiles, 16-31 for the key
+  // far as the slots reach.  Measured with other terms: 0 for the 3: 2,048 x 2,048 x 24 207 us, not 171, four
+  // segments of 64 to 320 rows and 40 to 256 keys 57, not 42; 6: 157 and 42.  0 for the 2: 171 and 44; 8: 158 and
+  // 43.5.  Six other shapes are the same within 2 % but for 130 x 5,000 x 8 (50 us, not 48, at 0 for the 2).  Lanes 0-15 weigh 1 to 16 chunks for the query tiles, 16-31 for the key
   // tiles.
   if (tid < 32) {
     const bool keys = tid >= 16;
@@ -768,6 +770,7 @@ cross_bwd_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
   // only the wait makes another kernel's writes visible here.
   grid_dependency_wait();
   launch_dependents();
+  const unsigned int code = a.err != nullptr ? *reinterpret_cast<const volatile unsigned int*>(a.err) : 0u;
   const Plan& plan = plan_of(a.plan);
   const int S = a.seg.num_segments, group = a.seg.num_q_heads / a.seg.num_kv_heads;
   constexpr uint32_t kParts = 8;
@@ -806,12 +809,9 @@ cross_bwd_sum_kernel(const __grid_constant__ CrossBwdArgs a) {
             (static_cast<int64_t>(keys ? r.k0 : r.q0) + row_tile) * x.stride + head * D;
     return x;
   };
-  if (a.err != nullptr) {  // the sums are incomplete
-    const unsigned int code = *reinterpret_cast<const volatile unsigned int*>(a.err);
-    if (code == kErrTimeout || code == kErrSmemLayout) return;
-  }
   for (uint32_t u = blockIdx.x; u < units_k + units_q; u += gridDim.x) {
     const Unit x = locate(u);
+    if (code == kErrTimeout || code == kErrSmemLayout) return;  // the sums are incomplete
     if (x.chunks == 1) continue;  // written already
     for (int i = threadIdx.x; i < kRows * (D / 8); i += 256) {
       const int row = x.r0 + i / (D / 8), col = i % (D / 8) * 8;

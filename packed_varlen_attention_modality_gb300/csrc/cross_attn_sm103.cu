@@ -21,11 +21,12 @@
 //   - items are decoded one ahead, and queries and keys have a producer each, so neither waits on
 //     the other's ring;
 //   - a last key tile is multiplied only as far as it holds keys (in steps of 16).
-// 58,758 rows x 558 keys x 40 heads x 128 take 530 us so (1,267 TFLOP/s); with all of it in the softmax
-// warpgroups and one producer (the packed self-attention kernel's structure) they took 787 us.  A step
-// takes some 2,700 cycles (2,048 of tensor work: the chain scores -> softmax -> product of each tile sets
-// the pace), the step between two items 3,700.  The kernel draws the GPU's 1.37 kW at that, at 1.91 to
-// 1.95 GHz, so cycles saved come back as a lower clock in part.  Tried and slower: both tiles' softmax by
+// 58,758 rows x 558 keys x 40 heads x 128 take 558 to 565 us so (1,190 to 1,200 TFLOP/s; 530 on a cool GPU); with
+// all of it in the softmax warpgroups and one producer (the packed self-attention kernel's structure) they
+// took 787 us.  What bounds it: a step takes some 2,700 cycles (2,048 of tensor work: the chain scores ->
+// softmax -> product of each tile sets the pace), the step between two items, here every fifth, 3,700; the
+// tensor pipe is 51 % busy (62 % with 32 key tiles an item).  The GPU is at its power cap then, at 1.91 to
+// 1.95 GHz, as it is in the packed self-attention kernel at 1,640 TFLOP/s, so the cap is not the bound.  Tried and slower: both tiles' softmax by
 // all eight warps, half a row each (581 us); a third query tile's buffer for a key/value tile's (556 us); one
 // copy of the issuing code for both kinds of step (615 us); two issuing warps without turns (the tiles fall
 // in phase).
@@ -60,7 +61,9 @@ static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOther == 65536 / 128, "the
 constexpr int kTmemCols = 512, kColO = 0, kColS = 256;
 constexpr float kRescaleLog2 = 8.0f;  // rescale O only when the running max grows by > 2^8
 constexpr int kPlanThreads = 1024;   // at most: kSortMax when the segments are that few
-constexpr int kSortMax = 256;         // segments ordered by keys up to this count
+// Segments are ordered by keys, and the last wave cut, up to this count (the ordering compares all pairs).
+// Segments of 200 rows and 64, 200 or 4,000 keys x 8 heads: 256 of them 348 us (106 ns a key tile), 257 478 us (145).
+constexpr int kSortMax = 256;
 constexpr int kHeader = kAttnWsHeaderWords;
 // The last, partly filled wave, in steps of a key tile (one query tile alone takes nearly as long as two:
 // the chain of each sets the pace).  An item's start and end take about two, joining chunks (partial
@@ -68,8 +71,11 @@ constexpr int kHeader = kAttnWsHeaderWords;
 // whole or 11 in shares, take 64 us whole, 55 us cut; 3 x 300 x 2,500 x 40 heads, 20 or 16 with the items of
 // the last wave short, 81 us either way.
 constexpr uint32_t kCostItem = 2, kCostJoin = 8;
-constexpr int kSplitMinTiles = 8;     // cut only items of at least 8 key tiles
-constexpr int kSplitMinChunk = 3;     // into chunks of at least 3
+// Items of at least 8 key tiles are cut, into chunks of at least 3.  Items of 4 or of 16 at least: the same times
+// within 1 % at ten shapes of 1,000 to 30,000 keys.  Chunks of 6 at least: 2,048 x 2,048 x 24 61 us, not 53; of one
+// tile: 4,096 x 4,096 x 24 146 us, not 148, 8 x 128 x 1,500 x 24 50, not 53, 100 x 30,000 x 8 50.2, not 49.4.
+constexpr int kSplitMinTiles = 8;
+constexpr int kSplitMinChunk = 3;
 constexpr int kSplitMaxChunks = 64;
 
 __host__ __device__ constexpr int key_tiles(int keys) {
@@ -203,7 +209,8 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
   int nkv = 0;
   uint32_t cost = 0;
   // Key heads apart, a group of CTAs each, where no whole wave comes before: then the heads of a segment
-  // are cut alike and read the same key rows at the same time.
+  // are cut alike and read the same key rows at the same time (175 us where one space of all heads takes 181 for
+  // 213 to 292 rows x 12,369 to 13,961 keys x 24, 49.4 and 50.8 for 100 x 30,000 x 8; eight shorter shapes within 1 %).
   const int heads = seg.num_kv_heads;
   const bool apart = tail == 0 && heads <= wave;
   const int groups = apart ? heads : 1, members = wave / groups;  // of CTAs; CTAs in a group

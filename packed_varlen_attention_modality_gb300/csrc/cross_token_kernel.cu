@@ -7,8 +7,11 @@
 // memory (16-byte asynchronous copies, no barrier between warps), computes S = Q K^T and O += P V
 // with 16 x 8 x 16 matrix instructions, and keeps a running max and sum; the warps are merged in
 // order at the end.  Rows this few leave tcgen05's 128-row tiles all but empty: 32 segments of one
-// row x 8 key heads x 64 query heads with 512 to 4,096 keys take 242 us there, 57 us here (323 MB read:
-// 5.7 TB/s, 84 % of a plain copy's rate; the merge's launch is 4 us of it).
+// row x 8 key heads x 64 query heads with 512 to 4,096 keys take 242 us there, 58 us here (323 MB read:
+// 5.6 TB/s, 82 % of a plain copy's rate; the merge's launch is 4 us of it).
+// Behind the tile's 16 rows is a step: with one or two rows a segment these take 54 to 58 us, with three (24 rows
+// a key head) 224 us in the tile kernel, which gives each query head 128 rows of its own; 24 heads of their own keys
+// 144 us at 16 rows, 181 at 17.  The rule goes by max_seqlen_q, so a loose bound takes the slower kernel too.
 // Chunks write partial results (O normalised by its own sum, fp32, and the LSE), which a merge
 // kernel joins in chunk order; with one chunk the CTA writes o itself.
 // Scores, max, sum and O are fp32; P is rounded to bf16 for the product with V, o once at the end.

@@ -571,7 +571,8 @@ float cross_scale(const h3_cross_attn_desc* d) {
 namespace {
 
 // Few rows per segment take the key-streaming kernel: its 16-row tile holds all of a key head's
-// rows, so K and V are read once.
+// rows, so K and V are read once.  One row more and the tile kernel reads them once for each pair of query
+// heads (both sides measured in cross_token_kernel.cu).
 bool cross_few_rows(const h3_cross_attn_desc* d) {
   return static_cast<int64_t>(d->max_seqlen_q) * (d->num_q_heads / d->num_kv_heads) <= h3::kCrossTokenRows;
 }
