@@ -1337,7 +1337,7 @@ cudaError_t launch(const CrossBwdArgs& a, cudaStream_t stream) {
     e = launch_programmatic(cross_dkv_kernel<D>, dim3(sms), dim3(kThreads), KvCfg<D>::kSmemBytes, stream, a);
     if (e != cudaSuccess) return e;
   }
-  // as many CTAs as fit at once: a unit is a chain of dependent loads (2 CTAs an SM: 36.5 us, not 35.0,
+  // as many CTAs as fit at once: a unit is a chain of dependent loads (2 CTAs an SM: 39.5 us, not 36.2,
   // for four segments of 64 to 320 rows and 40 to 256 keys x 24 heads x 64)
   if (a.slots > 0)
     e = launch_programmatic(cross_bwd_sum_kernel<D>, dim3(8 * sms), dim3(256), 0, stream, a);
