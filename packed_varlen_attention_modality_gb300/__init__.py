@@ -557,8 +557,9 @@ def varlen_cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_
 
     q bf16 [Cq, Hq, D]; k, v bf16 [Ck, Hkv, D] with Hkv dividing Hq; each may be a part of a fused
     projection (heads and dims contiguous, any token stride that is a multiple of 8).  max_seqlen_q
-    and max_seqlen_k bound a segment's rows and used keys.  A segment without keys gives 0 and an LSE
-    of -inf; rows of `out` outside every segment are left untouched.  Returns out [Cq, Hq, D] (and lse
+    and max_seqlen_k bound a segment's rows and used keys; when max_seqlen_q * Hq / Hkv is at most 16 the keys
+    are read once for all of a key head's rows, so single tokens want a tight bound.  A segment without keys
+    gives 0 and an LSE of -inf; rows of `out` outside every segment are left untouched.  Returns out [Cq, Hq, D] (and lse
     fp32 [Hq, Cq] when requested).
     """
     sizes, offsets = _cross_inputs(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, seqused_k,

@@ -21,7 +21,7 @@
 //   - items are decoded one ahead, and queries and keys have a producer each, so neither waits on
 //     the other's ring;
 //   - a last key tile is multiplied only as far as it holds keys (in steps of 16).
-// 58,758 rows x 558 keys x 40 heads x 128 take 558 to 565 us so (1,190 to 1,200 TFLOP/s; 530 on a cool GPU); with
+// 58,758 rows x 558 keys x 40 heads x 128 take 558 to 565 us so (1,190 to 1,200 TFLOP/s; 530 at best); with
 // all of it in the softmax warpgroups and one producer (the packed self-attention kernel's structure) they
 // took 787 us.  What bounds it: a step takes some 2,700 cycles (2,048 of tensor work: the chain scores ->
 // softmax -> product of each tile sets the pace), the step between two items, here every fifth, 3,700; the
