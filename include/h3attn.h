@@ -68,11 +68,13 @@ typedef enum {
   H3_ERR_MISALIGNED = 8,      /* a device pointer or row size is not 16-byte aligned */
   H3_ERR_BAD_PERM = 9,        /* (device) a permutation entry is out of range */
   H3_ERR_BAD_BLOCK_INDEX = 10, /* (device) a selected VSA block index is out of range */
-  H3_ERR_SMEM_LAYOUT = 11     /* (device) a kernel's shared memory does not start on a 1024-byte boundary:
+  H3_ERR_SMEM_LAYOUT = 11,    /* (device) a kernel's shared memory does not start on a 1024-byte boundary:
                                  nothing was computed (not met on any known driver) */
+  H3_ERR_BAD_PAGE = 12         /* (device) a page id of a block table is out of range */
 } h3_status;
 
 enum { H3_TAG_TEXT = 0, H3_TAG_VIDEO = 1, H3_TAG_AUDIO = 2 };
+enum { H3_TYPE_F32 = 0, H3_TYPE_BF16 = 1, H3_TYPE_E4M3 = 2 };
 
 /* RoPE configuration ([H3-vLLM] sec. 3: the tag selects the frequencies).
  * Zero / negative fields select the defaults given in brackets. */
@@ -178,6 +180,82 @@ H3_API h3_status h3_qk_norm_rope_bwd(const h3_qk_norm_desc* desc, const void* dq
                                      const h3_rope_cfg* cfg, void* dq, void* dk, float* dq_weight,
                                      float* dk_weight, void* workspace, size_t workspace_bytes,
                                      h3_stream_t stream);
+
+/* ---- The step between two branches: gated residual and modulated norm -------------------------
+ * [H3-fast] AdaLN: six vectors per request (shift, scale and gate, twice) modulate a block.  The
+ * output y of a branch (attention, MLP) joins the stream x, which is then normed and modulated for
+ * the next branch.  With r the request of a token:
+ *   u = norm_b(y) w_b;   x' = alpha x + gate_r u;   h = norm(x') w (1 + scale_r) + shift_r
+ *   norm(x) = c / sqrt(mean(c^2) + eps), c = x (H3_NORM_RMS) or x - mean(x) (H3_NORM_LAYER)
+ * Absent vectors count as w = w_b = gate = 1, scale = shift = 0; H3_NORM_NONE as branch_norm takes
+ * y itself, as norm it leaves h out (the last residual step).  Without y, x' is x.  All arithmetic
+ * is fp32; x' and h are each rounded once, and h is taken from x' before that rounding. */
+enum { H3_NORM_NONE = 0, H3_NORM_RMS = 1, H3_NORM_LAYER = 2 };
+
+typedef struct {
+  int32_t num_tokens;
+  int32_t dim;          /* a multiple of 8, at most 8192 */
+  int32_t num_requests; /* requests of cu_requests; 1 when that is NULL */
+  int32_t norm;         /* H3_NORM_*: of the stream */
+  int32_t branch_norm;  /* H3_NORM_*: of y */
+  int32_t stream_type;  /* H3_TYPE_F32 or H3_TYPE_BF16: x, x_out, dx_out, dx.  y, h, dy, dh are bf16 */
+  int32_t weight_type;  /* H3_TYPE_F32 or H3_TYPE_BF16: weight, branch_weight */
+  int32_t mod_type;     /* H3_TYPE_F32 or H3_TYPE_BF16: scale, shift, gate */
+  float eps;            /* <= 0 selects 1e-6 */
+  float residual_scale; /* alpha */
+  /* Elements between the rows of a tensor (requests, for scale, shift and gate), so that rows may be
+   * parts of wider ones; a multiple of 16 bytes and at least dim; 0 = contiguous. */
+  int64_t x_stride, y_stride, x_out_stride, h_stride;
+  int64_t scale_stride, shift_stride, gate_stride;
+  int64_t dx_out_stride, dh_stride, dx_stride, dy_stride; /* backward */
+} h3_residual_norm_desc;
+
+/* x           : device [num_tokens, dim] of the stream's type.
+ * y           : device bf16 [num_tokens, dim] or NULL (then branch_norm is H3_NORM_NONE, branch_weight,
+ *               gate and x_out are NULL and residual_scale is 1).
+ * weight, branch_weight: device [dim] or NULL.  scale, shift, gate: device [num_requests, dim] or NULL.
+ *               weight, scale and shift are NULL when norm is H3_NORM_NONE.
+ * cu_requests : device int32 [num_requests + 1], request row offsets (0-based, non-decreasing, last =
+ *               num_tokens); NULL means one request covering every row.
+ * x_out       : device, x' in the stream's type; may be x itself with its stride.
+ * h           : device bf16; NULL when norm is H3_NORM_NONE; may be y itself with its stride.
+ * Outputs must not otherwise overlap an input or each other.  Pointers are 16-byte aligned.
+ * Errors: H3_ERR_NULL, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED (dim), H3_ERR_MISALIGNED, H3_ERR_CUDA;
+ * device-side H3_ERR_TIMEOUT. */
+H3_API h3_status h3_residual_norm(const h3_residual_norm_desc* desc, const void* x, const void* y,
+                                  const void* weight, const void* branch_weight, const void* scale,
+                                  const void* shift, const void* gate, const int32_t* cu_requests,
+                                  void* x_out, void* h, h3_stream_t stream);
+
+/* Workspace bytes of h3_residual_norm_bwd (column sums of each CTA's rows of each request); 0 for
+ * invalid sizes. */
+H3_API size_t h3_residual_norm_bwd_workspace_size(const h3_residual_norm_desc* desc);
+
+/* Gradient of h3_residual_norm.  With xh = norm(x'), yh = norm_b(y), rs and ry their factors:
+ *   g = dh w (1 + scale);   t = dx' + rs (g - [mean g] - xh mean(g xh));   dx = alpha t
+ *   gy = t gate w_b;   dy = ry (gy - [mean gy] - yh mean(gy yh))        ([..]: layer norm only)
+ *   dshift_r = sum dh;   dscale_r = w U_r;   dgate_r = w_b V_r;   U_r = sum dh xh, V_r = sum t yh,
+ *   dweight = sum_r (1 + scale_r) U_r;   dbranch_weight = sum_r gate_r V_r   (sums over r's tokens)
+ * dx_out      : device, the gradient of x' as the stream goes on, or NULL for none.
+ * dh          : device bf16, the gradient of h; NULL when norm is H3_NORM_NONE.
+ * x_out       : device, the forward's x' (x itself when y is NULL); not read when norm is H3_NORM_NONE.
+ * y, weight ... cu_requests: the forward's (gate matters for dy, shift not at all).
+ * dx          : device, stream's type; may be dx_out or x_out with their strides.
+ * dy          : device bf16; NULL without y; may be y or dh with their strides.
+ * dweight, dbranch_weight: device fp32 [dim], dscale, dshift, dgate: device fp32 [num_requests, dim],
+ *               contiguous; NULL where not wanted; 0 for a request without tokens.
+ * workspace   : device, h3_residual_norm_bwd_workspace_size() bytes, 16-byte aligned; need not be
+ *               initialised.  Calls that may run at the same time need separate workspaces.
+ * Sums are taken in a fixed order: the result does not depend on timing.
+ * Errors: as above, and H3_ERR_WORKSPACE. */
+H3_API h3_status h3_residual_norm_bwd(const h3_residual_norm_desc* desc, const void* dx_out,
+                                      const void* dh, const void* x_out, const void* y,
+                                      const void* weight, const void* branch_weight,
+                                      const void* scale, const void* gate,
+                                      const int32_t* cu_requests, void* dx, void* dy,
+                                      float* dweight, float* dbranch_weight, float* dscale,
+                                      float* dshift, float* dgate, void* workspace,
+                                      size_t workspace_bytes, h3_stream_t stream);
 
 /* Bytes of device workspace h3_varlen_attn_fwd wants for these sizes: the work plan written by
  * the call itself (segment order and item prefix, 8 bytes per segment, plus a 16-byte header,
@@ -329,6 +407,51 @@ H3_API h3_status h3_varlen_cross_attn_bwd(const h3_cross_attn_desc* desc, const 
                                           const int32_t* seqused_k, void* dq, void* dk, void* dv,
                                           void* workspace, size_t workspace_bytes,
                                           h3_stream_t stream);
+
+/* ---- Paged key/value cache ----------------------------------------------------------------------
+ * The keys and values of a running sequence (the windows of a continued video, the tokens of a stream)
+ * stay in pages of page_size tokens, shared by all sequences.  Position j of segment g stands in page
+ * block_table[g][j / page_size], row j % page_size.
+ * k_cache, v_cache: device [num_pages, num_heads, page_size, head_dim], bf16 or e4m3.  An e4m3 cache has
+ * one scale per row (a token of a head): k_scale, v_scale, device uint8 [num_pages, num_heads,
+ * page_size], hold e + 127 for the least integer e with max |x| <= 448 * 2^e (kept within [-110, 120]).
+ * The row stands for q * 2^e, q = x * 2^-e rounded to e4m3 (to nearest even, past 448 to 448; a NaN
+ * stays one), which bf16 holds exactly (but for what rounds to 2^128, which is Inf, as Inf itself is).
+ * Every call that reads the cache takes the row for that. */
+typedef struct {
+  int32_t num_segments;
+  int32_t capacity;           /* rows of k and v */
+  int32_t num_heads, head_dim; /* key heads; 64 or 128 */
+  int32_t cache_type;         /* H3_TYPE_BF16 or H3_TYPE_E4M3 */
+  int32_t page_size;          /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int32_t num_pages;          /* of the cache */
+  int32_t max_pages;          /* entries of a segment in block_table */
+  int64_t k_stride, v_stride; /* elements between the rows of k, v: as for h3_qk_norm_desc */
+} h3_kv_cache_desc;
+
+/* Row i of segment g, i.e. row cu_seqlens[g] + i of k and v, into the cache at position start[g] + i.
+ * k, v        : device bf16 [capacity, num_heads, head_dim].
+ * k_scale, v_scale: NULL for a bf16 cache.
+ * block_table : device int32 [num_segments, max_pages]; entries that no position needs are not read.
+ * cu_seqlens  : device int32 [num_segments + 1]; must start at 0, not decrease, end <= capacity.  Rows
+ *               past the last segment are not used.
+ * start       : device int32 [num_segments].
+ * A row whose position has no place in the table or whose page id is out of range is skipped and
+ * recorded (H3_ERR_BAD_CU_SEQLENS, H3_ERR_BAD_PAGE).  Two rows written to one place in one call (a page
+ * that two segments share) leave it undefined which is kept.
+ * Errors: H3_ERR_NULL, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED, H3_ERR_MISALIGNED, H3_ERR_CUDA. */
+H3_API h3_status h3_kv_cache_write(const h3_kv_cache_desc* desc, const void* k, const void* v,
+                                   void* k_cache, void* v_cache, uint8_t* k_scale, uint8_t* v_scale,
+                                   const int32_t* block_table, const int32_t* cu_seqlens,
+                                   const int32_t* start, h3_stream_t stream);
+
+/* The reverse: positions start[g] + i of the cache into row cu_seqlens[g] + i of k and v (bf16).  Rows
+ * of k and v past the last segment, and skipped ones, are left as they were. */
+H3_API h3_status h3_kv_cache_read(const h3_kv_cache_desc* desc, const void* k_cache,
+                                  const void* v_cache, const uint8_t* k_scale,
+                                  const uint8_t* v_scale, const int32_t* block_table,
+                                  const int32_t* cu_seqlens, const int32_t* start, void* k, void* v,
+                                  h3_stream_t stream);
 
 /* Number of windows of the partition (host only; no device work).
  * [H3-fast] "window attention across GPUs": along each axis of length L with window w and

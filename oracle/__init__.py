@@ -36,6 +36,8 @@ from .vsa import (vsa_block_counts, vsa_block_count, vsa_block_ids, vsa_block_me
                   vsa_block_scores, vsa_select, vsa_attention)
 from .norm import norm_rope, norm_rope_grad
 from .cross import cross_attention, cross_attention_grad
+from .residual import residual_norm, residual_norm_grad
+from .paged import e4m3_row_values, e4m3_round, e4m3_scale, paged_attention
 
 __all__ = [
     "varlen_attention", "attention_weights", "dense_masked_attention_bruteforce",
@@ -45,5 +47,6 @@ __all__ = [
     "window_unpack", "vsa_block_counts", "vsa_block_count", "vsa_block_ids", "vsa_block_means",
     "vsa_block_scores", "vsa_select", "vsa_attention", "ContinuationPlan", "continuation_plan",
     "continuation_pack", "continuation_append", "masked_update", "norm_rope", "norm_rope_grad", "cross_attention",
-    "cross_attention_grad",
+    "cross_attention_grad", "residual_norm", "residual_norm_grad", "e4m3_row_values", "e4m3_round",
+    "e4m3_scale", "paged_attention",
 ]

@@ -9,10 +9,14 @@ Calls:
   rope_apply        modality-tagged RoPE of Q and K with the continuation time shift
   qk_norm_rope / qk_norm_rope_bwd   RMS norm of Q and K per head with the rotation (or without)
                     in the same pass, and its gradient
+  residual_norm / residual_norm_bwd   the step between two branches of a block: gated residual with an
+                    optional norm of the branch, then the modulated norm of the stream; and its gradient
   varlen_attn_fwd   block-diagonal softmax attention over cu_seqlens segments
   varlen_cross_attn_fwd / varlen_cross_attn_bwd   packed cross attention: keys of another length per
                     segment, query heads sharing key heads, padded key batches; and its gradient
                     (with equal offsets, that of varlen_attn_fwd)
+  kv_cache_write / kv_cache_read   rows of keys and values into a paged cache (bf16, or e4m3 with a
+                    power-of-two scale per row), and back out of it
   window_count / window_pack / window_unpack   shifted 3D window partition and row gather/scatter
   window_attn_fwd   shifted 3D window attention read and written in place on the grid
   vsa_select / vsa_attn_fwd   block-sparse video attention: block gate scores + top-k
@@ -31,12 +35,14 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
 __all__ = ["H3Error", "RopeConfig", "lib_path", "load_library", "rope_apply", "qk_norm_rope",
-           "qk_norm_rope_bwd_workspace_size", "qk_norm_rope_bwd", "varlen_attn_fwd",
+           "qk_norm_rope_bwd_workspace_size", "qk_norm_rope_bwd", "residual_norm", "ResidualNormGrads",
+           "residual_norm_bwd_workspace_size", "residual_norm_bwd", "kv_cache_write", "kv_cache_read",
+           "varlen_attn_fwd",
            "varlen_attn_fwd_noalloc", "varlen_cross_attn_workspace_size", "varlen_cross_attn_fwd",
            "varlen_cross_attn_bwd_workspace_size", "varlen_cross_attn_bwd",
            "window_attn_fwd", "vsa_block_count",
@@ -57,7 +63,7 @@ _lib = None
 _STATUS = {0: "H3_OK", 1: "H3_ERR_NULL", 2: "H3_ERR_INVALID_ARG", 3: "H3_ERR_BAD_CU_SEQLENS",
            4: "H3_ERR_UNSUPPORTED", 5: "H3_ERR_WORKSPACE", 6: "H3_ERR_CUDA", 7: "H3_ERR_TIMEOUT",
            8: "H3_ERR_MISALIGNED", 9: "H3_ERR_BAD_PERM", 10: "H3_ERR_BAD_BLOCK_INDEX",
-           11: "H3_ERR_SMEM_LAYOUT"}
+           11: "H3_ERR_SMEM_LAYOUT", 12: "H3_ERR_BAD_PAGE"}
 
 
 class H3Error(RuntimeError):
@@ -88,6 +94,23 @@ class _QkNormDesc(ctypes.Structure):
                 ("weight_type", _I), ("eps", ctypes.c_float), ("q_stride", _L), ("k_stride", _L),
                 ("q_out_stride", _L), ("k_out_stride", _L), ("dq_stride", _L), ("dk_stride", _L)]
     pack = struct.Struct("@5if6q").pack  # the same bytes, several times faster than the class
+
+
+class _ResidualNormDesc(ctypes.Structure):
+    """Mirror of h3_residual_norm_desc."""
+    _fields_ = [("num_tokens", _I), ("dim", _I), ("num_requests", _I), ("norm", _I), ("branch_norm", _I),
+                ("stream_type", _I), ("weight_type", _I), ("mod_type", _I), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("x_stride", _L), ("y_stride", _L), ("x_out_stride", _L),
+                ("h_stride", _L), ("scale_stride", _L), ("shift_stride", _L), ("gate_stride", _L),
+                ("dx_out_stride", _L), ("dh_stride", _L), ("dx_stride", _L), ("dy_stride", _L)]
+    pack = struct.Struct("@8i2f11q").pack
+
+
+class _KvCacheDesc(ctypes.Structure):
+    """Mirror of h3_kv_cache_desc."""
+    _fields_ = [("num_segments", _I), ("capacity", _I), ("num_heads", _I), ("head_dim", _I), ("cache_type", _I),
+                ("page_size", _I), ("num_pages", _I), ("max_pages", _I), ("k_stride", _L), ("v_stride", _L)]
+    pack = struct.Struct("@8i2q").pack
 
 
 class _CrossAttnDesc(ctypes.Structure):
@@ -137,6 +160,11 @@ def load_library():
         "h3_qk_norm_rope_bwd_workspace_size": (U64, [I32]),
         "h3_qk_norm_rope_bwd": (I32, [P, P, P, P, P, P, P, P, P, P, I32, P,
                                       ctypes.POINTER(RopeConfig), P, P, P, P, P, U64, P]),
+        "h3_residual_norm": (I32, [P] * 12),
+        "h3_residual_norm_bwd_workspace_size": (U64, [P]),
+        "h3_residual_norm_bwd": (I32, [P] * 18 + [U64, P]),
+        "h3_kv_cache_write": (I32, [P] * 11),
+        "h3_kv_cache_read": (I32, [P] * 11),
         "h3_varlen_attn_workspace_size": (U64, [I32, I32, I32, I32]),
         "h3_varlen_attn_fwd": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P, U64, P]),
         "h3_varlen_attn_fwd_noalloc": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P]),
@@ -435,6 +463,306 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: Optional[torch.Tensor], q: to
             ctypes.byref(cfg) if cfg is not None else None, dq.data_ptr(), _ptr(dk), dqw.data_ptr(), _ptr(dkw),
             workspace.data_ptr(), workspace.numel())
     return dq, dk, dqw, dkw
+
+
+_NORMS = {None: 0, "none": 0, "rms": 1, "layer": 2}
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+class ResidualNormGrads(NamedTuple):
+    """Gradients of residual_norm's inputs; None where the input is absent."""
+    dx: torch.Tensor
+    dy: Optional[torch.Tensor]
+    weight: Optional[torch.Tensor]
+    branch_weight: Optional[torch.Tensor]
+    scale: Optional[torch.Tensor]
+    shift: Optional[torch.Tensor]
+    gate: Optional[torch.Tensor]
+
+
+def _matrix(t: torch.Tensor, name: str, dtype, device: torch.device, shape=None) -> int:
+    """Check [rows, dim] with contiguous rows; returns the row stride in elements, 0 when contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must be {'[rows, dim]' if shape is None else list(shape)}, got {list(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    sr, sc = t.stride()
+    if sc != 1 or (t.shape[0] > 1 and sr < t.shape[1]):
+        raise ValueError(f"{name} must have contiguous rows")
+    return sr if t.shape[0] > 1 else 0
+
+
+def _norm_kind(kind, name: str) -> int:
+    if kind not in _NORMS:
+        raise ValueError(f'{name} must be "rms", "layer" or "none"')
+    return _NORMS[kind]
+
+
+def _residual_norm_inputs(x, y, norm, weight, scale, shift, gate, branch_norm, branch_weight, residual_scale,
+                          cu_requests, eps, num_tokens):
+    """Checks shared by residual_norm and its backward; returns (sizes of the descriptor, row strides of
+    x and y, strides of scale, shift and gate, pointers of the vectors and cu_requests)."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _TYPES:
+        raise TypeError("the stream must be a float32 or bfloat16 tensor")
+    dev = x.device
+    x_stride, y_stride = _matrix(x, "x", x.dtype, dev), 0
+    C, dim = x.shape
+    n = C if num_tokens is None else int(num_tokens)
+    if not 0 <= n <= C:
+        raise ValueError("num_tokens must lie within the rows of x")
+    kind, branch_kind = _norm_kind(norm, "norm"), _norm_kind(branch_norm, "branch_norm")
+    if y is not None:
+        y_stride = _matrix(y, "y", _BF16, dev, x.shape)
+    elif branch_kind or gate is not None or branch_weight is not None or residual_scale != 1.0:
+        raise ValueError("branch_norm, branch_weight, gate and residual_scale need y")
+    if not kind and (y is None or weight is not None or scale is not None or shift is not None):
+        raise ValueError('norm "none" leaves h out: it needs y, and takes no weight, scale or shift')
+    requests, cu = 1, None
+    if cu_requests is not None:
+        _aux(cu_requests, "cu_requests", _I32, dev)
+        requests = cu_requests.numel() - 1
+        if requests < 1:
+            raise ValueError("cu_requests must have one entry per request and one more")
+        cu = cu_requests.data_ptr()
+    weight_type = mod_type = None
+    pointers, strides = [], []
+    for name, t in (("weight", weight), ("branch_weight", branch_weight)):
+        if t is None:
+            pointers.append(None)
+            continue
+        if weight_type is None:
+            weight_type = t.dtype if isinstance(t, torch.Tensor) else None
+            if weight_type not in _TYPES:
+                raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+        _aux(t, name, weight_type, dev)
+        if t.shape != (dim,):
+            raise ValueError(f"{name} must be [dim]")
+        pointers.append(t.data_ptr())
+    for name, t in (("scale", scale), ("shift", shift), ("gate", gate)):
+        if t is None:
+            pointers.append(None)
+            strides.append(0)
+            continue
+        if mod_type is None:
+            mod_type = t.dtype if isinstance(t, torch.Tensor) else None
+            if mod_type not in _TYPES:
+                raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+        strides.append(_matrix(t, name, mod_type, dev, (requests, dim)))
+        pointers.append(t.data_ptr())
+    pointers.append(cu)
+    sizes = (n, dim, requests, kind, branch_kind, _TYPES[x.dtype], _TYPES.get(weight_type, 0), _TYPES.get(mod_type, 0),
+             float(eps), float(residual_scale))
+    return sizes, x_stride, y_stride, strides, pointers
+
+
+def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, norm: Optional[str] = "rms",
+                  weight: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                  shift: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                  branch_norm: Optional[str] = None, branch_weight: Optional[torch.Tensor] = None,
+                  residual_scale: float = 1.0, cu_requests: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  num_tokens: Optional[int] = None, x_out: Optional[torch.Tensor] = None,
+                  h_out: Optional[torch.Tensor] = None):
+    """The step between two branches of a block: the branch's output y joins the stream x, which is
+    normed and modulated for the next branch.
+
+      x' = residual_scale * x + gate * branch_norm(y) * branch_weight
+      h  = norm(x') * weight * (1 + scale) + shift
+
+    x float32 or bfloat16 [C, dim] (dim a multiple of 8, at most 8192), y bfloat16 [C, dim] or None (then
+    x' is x); norm "rms", "layer" or "none" (no h), branch_norm the same ("none": y itself); weight,
+    branch_weight [dim]; scale, shift, gate [R, dim], of the request that cu_requests (int32 [R+1]; None: one
+    request) gives a token; each vector float32 or bfloat16, or None.  Rows may be parts of wider ones (a
+    fused projection's six vectors, say).  Writes new tensors unless x_out / h_out are given (x and y
+    themselves are allowed); rows past num_tokens are left as they were.  Returns (x', h), x' being x itself
+    without y and h None with norm "none".
+    """
+    sizes, x_stride, y_stride, mod, ptr = _residual_norm_inputs(x, y, norm, weight, scale, shift, gate, branch_norm,
+                                                                branch_weight, residual_scale, cu_requests, eps,
+                                                                num_tokens)
+    dev, x_out_stride, h_stride, h = x.device, 0, 0, None
+    if y is None:
+        if x_out is not None:
+            raise ValueError("x_out needs y: without it the stream stays x")
+        x_out = x
+    elif x_out is None:
+        x_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    else:
+        x_out_stride = _matrix(x_out, "x_out", x.dtype, dev, x.shape)
+    if sizes[3]:
+        if h_out is None:
+            h = torch.empty(x.shape, dtype=_BF16, device=dev)
+        else:
+            h, h_stride = h_out, _matrix(h_out, "h_out", _BF16, dev, x.shape)
+    elif h_out is not None:
+        raise ValueError('h_out needs a norm')
+    if sizes[0] == 0:
+        return x_out, h
+    desc = _ResidualNormDesc.pack(*sizes, x_stride, y_stride, x_out_stride, h_stride, *mod, 0, 0, 0, 0)
+    _launch(load_library().h3_residual_norm, "h3_residual_norm", dev, desc, x.data_ptr(), _ptr(y), *ptr,
+            None if y is None else x_out.data_ptr(), _ptr(h))
+    return x_out, h
+
+
+def residual_norm_bwd_workspace_size(num_tokens: int, dim: int, num_requests: int = 1) -> int:
+    desc = _ResidualNormDesc.pack(num_tokens, dim, num_requests, 0, 0, 0, 0, 0, 0.0, 1.0, *(0,) * 11)
+    return int(load_library().h3_residual_norm_bwd_workspace_size(desc))
+
+
+def residual_norm_bwd(dx_out: Optional[torch.Tensor], dh: Optional[torch.Tensor], x_out: torch.Tensor,
+                      y: Optional[torch.Tensor] = None, norm: Optional[str] = "rms",
+                      weight: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                      shift: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                      branch_norm: Optional[str] = None, branch_weight: Optional[torch.Tensor] = None,
+                      residual_scale: float = 1.0, cu_requests: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                      num_tokens: Optional[int] = None, dx: Optional[torch.Tensor] = None,
+                      dy: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradient of residual_norm: from dx_out and dh, the gradients of its outputs (dx_out None: the stream
+    is not used further), its output x_out (x itself without y) and its other inputs, to a
+    ResidualNormGrads: dx in the stream's type, dy bfloat16, the vectors' in float32 (shift's values are not
+    used: it says that its gradient is wanted).  dx may be dx_out or x_out, and dy y or dh; rows past
+    num_tokens are left as they were and count for nothing.  Sums over tokens are taken in a fixed order.
+    """
+    sizes, x_stride, y_stride, mod, ptr = _residual_norm_inputs(x_out, y, norm, weight, scale, shift, gate, branch_norm,
+                                                                branch_weight, residual_scale, cu_requests, eps,
+                                                                num_tokens)
+    dev, shape, has_y = x_out.device, x_out.shape, y is not None
+    dx_out_stride = dh_stride = dx_stride = dy_stride = 0
+    if dx_out is not None:
+        dx_out_stride = _matrix(dx_out, "dx_out", x_out.dtype, dev, shape)
+    elif not sizes[3]:
+        raise ValueError('with norm "none" dx_out is the only gradient')
+    if sizes[3]:
+        dh_stride = _matrix(dh, "dh", _BF16, dev, shape)
+    elif dh is not None:
+        raise ValueError('dh needs a norm')
+    if dx is None:
+        dx = torch.empty(shape, dtype=x_out.dtype, device=dev)
+    else:
+        dx_stride = _matrix(dx, "dx", x_out.dtype, dev, shape)
+    if not has_y:
+        if dy is not None:
+            raise ValueError("dy needs y")
+    elif dy is None:
+        dy = torch.empty(shape, dtype=_BF16, device=dev)
+    else:
+        dy_stride = _matrix(dy, "dy", _BF16, dev, shape)
+    requests, dim = sizes[2], sizes[1]
+    g = ResidualNormGrads(dx, dy, *(None if t is None else torch.empty(dim, dtype=_F32, device=dev)
+                                    for t in (weight, branch_weight)),
+                          *(None if t is None else torch.empty((requests, dim), dtype=_F32, device=dev)
+                            for t in (scale, shift, gate)))
+    if x_out.numel() == 0:  # no rows at all: no buffer to point at
+        for t in g[2:]:
+            if t is not None:
+                t.zero_()
+        return g
+    lib = load_library()
+    desc = _ResidualNormDesc.pack(*sizes, 0, y_stride, x_stride, 0, *mod, dx_out_stride, dh_stride, dx_stride, dy_stride)
+    if workspace is None:
+        workspace = torch.empty(lib.h3_residual_norm_bwd_workspace_size(desc) or 1, dtype=_U8, device=dev)
+    else:
+        _require(workspace, "workspace", _U8, dev)
+    _launch(lib.h3_residual_norm_bwd, "h3_residual_norm_bwd", dev, desc, _ptr(dx_out), _ptr(dh), x_out.data_ptr(),
+            _ptr(y), ptr[0], ptr[1], ptr[2], ptr[4], ptr[5], dx.data_ptr(), _ptr(dy), _ptr(g.weight),
+            _ptr(g.branch_weight), _ptr(g.scale), _ptr(g.shift), _ptr(g.gate), workspace.data_ptr(),
+            workspace.numel())
+    return g
+
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _cache_inputs(k_cache, v_cache, k_scale, v_scale, block_table, segments, dev):
+    """Checks of a paged cache; returns (heads, head_dim, type, page_size, num_pages, max_pages) and its pointers."""
+    kind = k_cache.dtype if isinstance(k_cache, torch.Tensor) else None
+    if kind is not _BF16 and kind is not _E4M3:
+        raise TypeError("k_cache must be a bfloat16 or float8_e4m3fn tensor")
+    _aux(k_cache, "k_cache", kind, dev)
+    _aux(v_cache, "v_cache", kind, dev)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be [num_pages, num_heads, page_size, head_dim]")
+    scales = None, None
+    if kind is _E4M3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        _aux(k_scale, "k_scale", _U8, dev)
+        _aux(v_scale, "v_scale", _U8, dev)
+        if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+            raise ValueError("k_scale and v_scale must be [num_pages, num_heads, page_size]")
+        scales = k_scale.data_ptr(), v_scale.data_ptr()
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("a bfloat16 cache takes no scales")
+    _aux(block_table, "block_table", _I32, dev)
+    if block_table.dim() != 2 or block_table.shape[0] != segments:
+        raise ValueError("block_table must be [num_segments, max_pages]")
+    return (shape[1], shape[3], 1 if kind is _BF16 else 2, shape[2], shape[0], block_table.shape[1]), \
+        (k_cache.data_ptr(), v_cache.data_ptr(), *scales, block_table.data_ptr())
+
+
+def _cache_call(name, rows, strides, k_cache, v_cache, block_table, cu_seqlens, start, k_scale, v_scale, write):
+    dev = k_cache.device
+    _aux(cu_seqlens, "cu_seqlens", _I32, dev)
+    _aux(start, "start", _I32, dev)
+    S = cu_seqlens.numel() - 1
+    if S < 0 or start.numel() != S:
+        raise ValueError("cu_seqlens must have one entry per segment and one more, start one per segment")
+    (heads, dim, *rest), pointers = _cache_inputs(k_cache, v_cache, k_scale, v_scale, block_table, S, dev)
+    C = rows[0].shape[0]
+    if rows[0].shape[1:] != (heads, dim):
+        raise ValueError("k and v must be [C, num_heads, head_dim] of the cache's heads")
+    if C == 0 or S == 0:
+        return
+    desc = _KvCacheDesc.pack(S, C, heads, dim, *rest, *strides)
+    kv, where = tuple(t.data_ptr() for t in rows), (*pointers, cu_seqlens.data_ptr(), start.data_ptr())
+    _launch(getattr(load_library(), name), name, dev, desc, *(kv + where if write else where + kv))
+
+
+def kv_cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_table: torch.Tensor, cu_seqlens: torch.Tensor, start: torch.Tensor,
+                   k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None) -> None:
+    """Row i of segment g (row cu_seqlens[g] + i of k and v, bf16 [C, H, D]) into a paged cache at position
+    start[g] + i of the segment: page block_table[g, position // page_size], row position % page_size.
+
+    k_cache, v_cache [num_pages, H, page_size, D], page_size 16, 32, 64, 128 or 256: bfloat16, or
+    float8_e4m3fn with k_scale, v_scale uint8 [num_pages, H, page_size], which hold e + 127 for the row's scale
+    2^e, the least with which its largest value fits e4m3.  block_table int32 [S, max_pages], cu_seqlens
+    int32 [S+1], start int32 [S].  k and v may be parts of a fused projection.
+    """
+    strides = _rows(k, "k", k_cache.device), _rows(v, "v", k_cache.device, k.shape)
+    _cache_call("h3_kv_cache_write", (k, v), strides, k_cache, v_cache, block_table, cu_seqlens, start, k_scale,
+                v_scale, True)
+
+
+def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                  cu_seqlens: torch.Tensor, start: torch.Tensor, num_rows: Optional[int] = None,
+                  k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                  k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None):
+    """The reverse of kv_cache_write: positions start[g] + i into row cu_seqlens[g] + i of k and v (bf16
+    [C, H, D]), the values that the cache holds.  New tensors of num_rows rows unless k_out and v_out are
+    given; rows past the last segment are left as they were.  Returns (k, v)."""
+    dev = k_cache.device
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, num_heads, page_size, head_dim]")
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out are given together")
+    if k_out is None:
+        if num_rows is None:
+            raise ValueError("num_rows or k_out and v_out are needed")
+        shape = (int(num_rows), k_cache.shape[1], k_cache.shape[3])
+        k_out, v_out = (torch.empty(shape, dtype=_BF16, device=dev) for _ in range(2))
+        strides = 0, 0
+    else:
+        strides = _rows(k_out, "k_out", dev), _rows(v_out, "v_out", dev, k_out.shape)
+    _cache_call("h3_kv_cache_read", (k_out, v_out), strides, k_cache, v_cache, block_table, cu_seqlens, start, k_scale,
+                v_scale, False)
+    return k_out, v_out
 
 
 def varlen_attn_workspace_size(num_segments: int, num_heads: int, max_seqlen: int, head_dim: int) -> int:

@@ -69,6 +69,64 @@ constexpr size_t norm_bwd_workspace_bytes(int head_dim) {
 }
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int head_dim, bool backward, cudaStream_t stream);
 
+// ---- gated residual and modulated norm of the stream ----------------------------------------
+constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;
+// Strides in elements between the rows of a tensor; vectors of a request `*_stride` elements apart.
+struct ResidualNormArgs {
+  int num_tokens, dim, num_requests, norm, branch_norm;
+  int x_fp32, weight_bf16, mod_bf16;
+  float eps, residual_scale;
+  const void* x;  // forward: the stream before the branch; backward: after it
+  const __nv_bfloat16* y;
+  const void *weight, *branch_weight, *scale, *shift, *gate;
+  int64_t x_stride, y_stride, scale_stride, shift_stride, gate_stride;
+  const int32_t* cu_requests;
+  // forward
+  void* x_out;
+  __nv_bfloat16* h;
+  int64_t x_out_stride, h_stride;
+  // backward
+  const void* dx_out;
+  const __nv_bfloat16* dh;
+  void* dx;
+  __nv_bfloat16* dy;
+  int64_t dx_out_stride, dh_stride, dx_stride, dy_stride;
+  float *dweight, *dbranch_weight, *dscale, *dshift, *dgate;  // null: not wanted
+  float* partials;  // residual_norm_bwd_bytes()
+  unsigned int* err;
+};
+constexpr int kResidualNormMaxDim = 8192;
+constexpr int kResidualNormMaxCtas = 304;  // 2 x 152 SMs
+inline int residual_norm_ctas(int num_tokens, int resident) {
+  const int most = resident < kResidualNormMaxCtas ? resident : kResidualNormMaxCtas;
+  return num_tokens < most ? num_tokens : most;
+}
+// three column sums for each pair of a CTA and a request with rows in it
+inline size_t residual_norm_bwd_bytes(int num_tokens, int num_requests, int dim) {
+  const size_t pairs = static_cast<size_t>(residual_norm_ctas(num_tokens, kResidualNormMaxCtas)) + num_requests;
+  return pairs * 3 * dim * sizeof(float);
+}
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool backward, cudaStream_t stream);
+
+// ---- paged key/value cache --------------------------------------------------------------------
+// Cache [pages, heads, page, D]; e4m3 with one biased exponent per row, [pages, heads, page].
+constexpr int kScaleMin = -110, kScaleMax = 120;
+struct PagedTable {
+  const int32_t* pages;  // [segments, per_segment]
+  int per_segment, num_pages, page_shift;
+};
+struct KvCacheArgs {
+  __nv_bfloat16 *k, *v;  // packed rows (only read when the cache is written)
+  int64_t k_stride, v_stride;
+  void *k_cache, *v_cache;
+  uint8_t *k_scale, *v_scale;  // null: a bf16 cache
+  PagedTable table;
+  const int32_t *cu, *start;
+  int num_segments, capacity, heads;
+  unsigned int* err;
+};
+cudaError_t launch_kv_cache(const KvCacheArgs& a, int head_dim, bool write, cudaStream_t stream);
+
 // ---- window partition ---------------------------------------------------------------------
 struct WindowGeom {
   int L[3];      // grid extent per axis (T, H, W)

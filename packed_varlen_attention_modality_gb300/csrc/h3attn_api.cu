@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include <cuda.h>
@@ -196,6 +197,7 @@ const char* h3_status_string(h3_status s) {
     case H3_ERR_BAD_PERM: return "a permutation entry is out of range";
     case H3_ERR_BAD_BLOCK_INDEX: return "a selected block index is out of range";
     case H3_ERR_SMEM_LAYOUT: return "a kernel's shared memory does not start on a 1024-byte boundary";
+    case H3_ERR_BAD_PAGE: return "a page id of a block table is out of range";
   }
   return "unknown status";
 }
@@ -419,6 +421,218 @@ h3_status h3_qk_norm_rope_bwd(const h3_qk_norm_desc* desc, const void* dq_out, c
   a.partials = static_cast<float*>(workspace);
   if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
   return from_cuda(h3::launch_norm_rope(a, D, true, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---- gated residual and modulated norm ------------------------------------------------------------
+
+namespace {
+
+bool residual_norm_sizes_ok(const h3_residual_norm_desc* d) {
+  return d->num_tokens >= 0 && d->dim > 0 && d->num_requests > 0;
+}
+
+// A row stride in elements of `bytes` each: 0 selects contiguous rows; else at least a row, whole 16-byte units.
+h3_status row_stride(int64_t stride, int dim, int bytes, int64_t* out) {
+  if (stride == 0) stride = dim;
+  if (stride < dim || stride > INT32_MAX) return H3_ERR_INVALID_ARG;
+  if (stride * bytes % 16 != 0) return H3_ERR_MISALIGNED;
+  *out = stride;
+  return H3_OK;
+}
+
+bool all_aligned16(std::initializer_list<const void*> pointers) {
+  return std::all_of(pointers.begin(), pointers.end(), aligned16);
+}
+
+// Checks shared by the forward and the backward, and the arguments common to both.
+h3_status residual_norm_args(const h3_residual_norm_desc* d, const void* y, const void* weight,
+                             const void* branch_weight, const void* scale, const void* shift, const void* gate,
+                             const int32_t* cu_requests, h3::ResidualNormArgs* a) {
+  if (d == nullptr) return H3_ERR_NULL;
+  if (!residual_norm_sizes_ok(d) || d->norm < H3_NORM_NONE || d->norm > H3_NORM_LAYER ||
+      d->branch_norm < H3_NORM_NONE || d->branch_norm > H3_NORM_LAYER)
+    return H3_ERR_INVALID_ARG;
+  for (int32_t t : {d->stream_type, d->weight_type, d->mod_type})
+    if (t != H3_TYPE_F32 && t != H3_TYPE_BF16) return H3_ERR_INVALID_ARG;
+  if (!(d->eps <= 0.f || std::isfinite(d->eps)) || !std::isfinite(d->residual_scale)) return H3_ERR_INVALID_ARG;
+  if (cu_requests == nullptr && d->num_requests != 1) return H3_ERR_INVALID_ARG;
+  if (d->dim % 8 != 0 || d->dim > h3::kResidualNormMaxDim) return H3_ERR_UNSUPPORTED;
+  // nothing to do, or something that would not be used
+  if (d->norm == H3_NORM_NONE && (y == nullptr || weight != nullptr || scale != nullptr || shift != nullptr))
+    return H3_ERR_INVALID_ARG;
+  if (y == nullptr && (d->branch_norm != H3_NORM_NONE || branch_weight != nullptr || gate != nullptr ||
+                       d->residual_scale != 1.f))
+    return H3_ERR_INVALID_ARG;
+  if (!all_aligned16({y, weight, branch_weight, scale, shift, gate}) || (reinterpret_cast<uintptr_t>(cu_requests) & 3u))
+    return H3_ERR_MISALIGNED;
+  const int mod = d->mod_type == H3_TYPE_F32 ? 4 : 2;
+  h3_status st;
+  if ((st = row_stride(d->y_stride, d->dim, 2, &a->y_stride)) != H3_OK ||
+      (st = row_stride(d->scale_stride, d->dim, mod, &a->scale_stride)) != H3_OK ||
+      (st = row_stride(d->shift_stride, d->dim, mod, &a->shift_stride)) != H3_OK ||
+      (st = row_stride(d->gate_stride, d->dim, mod, &a->gate_stride)) != H3_OK)
+    return st;
+  a->num_tokens = d->num_tokens;
+  a->dim = d->dim;
+  a->num_requests = d->num_requests;
+  a->norm = d->norm;
+  a->branch_norm = d->branch_norm;
+  a->x_fp32 = d->stream_type == H3_TYPE_F32;
+  a->weight_bf16 = d->weight_type == H3_TYPE_BF16;
+  a->mod_bf16 = d->mod_type == H3_TYPE_BF16;
+  a->eps = d->eps > 0.f ? d->eps : 1e-6f;
+  a->residual_scale = d->residual_scale;
+  a->y = static_cast<const __nv_bfloat16*>(y);
+  a->weight = weight;
+  a->branch_weight = branch_weight;
+  a->scale = scale;
+  a->shift = shift;
+  a->gate = gate;
+  a->cu_requests = cu_requests;
+  return H3_OK;
+}
+
+}  // namespace
+
+h3_status h3_residual_norm(const h3_residual_norm_desc* desc, const void* x, const void* y, const void* weight,
+                           const void* branch_weight, const void* scale, const void* shift, const void* gate,
+                           const int32_t* cu_requests, void* x_out, void* h, h3_stream_t stream) {
+  h3::ResidualNormArgs a{};
+  h3_status st = residual_norm_args(desc, y, weight, branch_weight, scale, shift, gate, cu_requests, &a);
+  if (st != H3_OK) return st;
+  if (x == nullptr || (y != nullptr) != (x_out != nullptr) || (a.norm != h3::kNormNone) != (h != nullptr))
+    return H3_ERR_NULL;
+  if (!all_aligned16({x, x_out, h})) return H3_ERR_MISALIGNED;
+  const int stream_bytes = a.x_fp32 ? 4 : 2;
+  if ((st = row_stride(desc->x_stride, a.dim, stream_bytes, &a.x_stride)) != H3_OK ||
+      (st = row_stride(desc->x_out_stride, a.dim, stream_bytes, &a.x_out_stride)) != H3_OK ||
+      (st = row_stride(desc->h_stride, a.dim, 2, &a.h_stride)) != H3_OK)
+    return st;
+  a.x = x;
+  a.x_out = x_out;
+  a.h = static_cast<__nv_bfloat16*>(h);
+  if (a.num_tokens == 0) return H3_OK;
+  if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
+  a.err = device_error_ptr();
+  if (a.err == nullptr) return H3_ERR_CUDA;
+  return from_cuda(h3::launch_residual_norm(a, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t h3_residual_norm_bwd_workspace_size(const h3_residual_norm_desc* d) {
+  if (d == nullptr || !residual_norm_sizes_ok(d)) return 0;
+  return h3::residual_norm_bwd_bytes(d->num_tokens, d->num_requests, d->dim);
+}
+
+h3_status h3_residual_norm_bwd(const h3_residual_norm_desc* desc, const void* dx_out, const void* dh,
+                               const void* x_out, const void* y, const void* weight, const void* branch_weight,
+                               const void* scale, const void* gate, const int32_t* cu_requests, void* dx, void* dy,
+                               float* dweight, float* dbranch_weight, float* dscale, float* dshift, float* dgate,
+                               void* workspace, size_t workspace_bytes, h3_stream_t stream) {
+  h3::ResidualNormArgs a{};
+  h3_status st = residual_norm_args(desc, y, weight, branch_weight, scale, nullptr, gate, cu_requests, &a);
+  if (st != H3_OK) return st;
+  const bool has_h = a.norm != h3::kNormNone, has_y = y != nullptr;
+  if (has_h != (dh != nullptr) || (has_h && x_out == nullptr) || dx == nullptr || has_y != (dy != nullptr))
+    return H3_ERR_NULL;
+  if (!has_h && dx_out == nullptr) return H3_ERR_NULL;
+  if ((!has_h && (dweight != nullptr || dscale != nullptr || dshift != nullptr)) ||
+      (!has_y && (dbranch_weight != nullptr || dgate != nullptr)))
+    return H3_ERR_INVALID_ARG;
+  if (!all_aligned16({dx_out, dh, x_out, dx, dy, workspace}) ||
+      ((reinterpret_cast<uintptr_t>(dweight) | reinterpret_cast<uintptr_t>(dbranch_weight) |
+        reinterpret_cast<uintptr_t>(dscale) | reinterpret_cast<uintptr_t>(dshift) |
+        reinterpret_cast<uintptr_t>(dgate)) & 3u))
+    return H3_ERR_MISALIGNED;
+  const int stream_bytes = a.x_fp32 ? 4 : 2;
+  if ((st = row_stride(desc->x_out_stride, a.dim, stream_bytes, &a.x_stride)) != H3_OK ||
+      (st = row_stride(desc->dx_out_stride, a.dim, stream_bytes, &a.dx_out_stride)) != H3_OK ||
+      (st = row_stride(desc->dx_stride, a.dim, stream_bytes, &a.dx_stride)) != H3_OK ||
+      (st = row_stride(desc->dh_stride, a.dim, 2, &a.dh_stride)) != H3_OK ||
+      (st = row_stride(desc->dy_stride, a.dim, 2, &a.dy_stride)) != H3_OK)
+    return st;
+  if (workspace == nullptr || workspace_bytes < h3_residual_norm_bwd_workspace_size(desc)) return H3_ERR_WORKSPACE;
+  a.x = x_out;
+  a.dx_out = dx_out;
+  a.dh = static_cast<const __nv_bfloat16*>(dh);
+  a.dx = dx;
+  a.dy = static_cast<__nv_bfloat16*>(dy);
+  a.dweight = dweight;
+  a.dbranch_weight = dbranch_weight;
+  a.dscale = dscale;
+  a.dshift = dshift;
+  a.dgate = dgate;
+  a.partials = static_cast<float*>(workspace);
+  if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
+  a.err = device_error_ptr();
+  if (a.err == nullptr) return H3_ERR_CUDA;
+  return from_cuda(h3::launch_residual_norm(a, true, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---- paged key/value cache --------------------------------------------------------------------------
+
+namespace {
+
+int page_shift_of(int32_t page_size) {  // -1: not a page size
+  for (int shift = 4; shift <= 8; ++shift)
+    if (page_size == 1 << shift) return shift;
+  return -1;
+}
+
+h3_status kv_cache_call(const h3_kv_cache_desc* d, const void* k, const void* v, const void* k_cache,
+                        const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                        const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* start, bool write,
+                        h3_stream_t stream) {
+  if (d == nullptr) return H3_ERR_NULL;
+  if (d->num_segments < 0 || d->num_segments > 65535 || d->capacity < 0 || d->num_heads <= 0 ||
+      d->num_heads > 65535 || d->num_pages < 0 || d->max_pages < 0 ||
+      (d->cache_type != H3_TYPE_BF16 && d->cache_type != H3_TYPE_E4M3) || page_shift_of(d->page_size) < 0)
+    return H3_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return H3_ERR_UNSUPPORTED;
+  const bool e4m3 = d->cache_type == H3_TYPE_E4M3;
+  h3::KvCacheArgs a{};
+  h3_status st;
+  if ((st = token_stride(d->k_stride, d->num_heads, d->head_dim, &a.k_stride)) != H3_OK ||
+      (st = token_stride(d->v_stride, d->num_heads, d->head_dim, &a.v_stride)) != H3_OK)
+    return st;
+  if (e4m3 != (k_scale != nullptr) || e4m3 != (v_scale != nullptr)) return H3_ERR_NULL;
+  if (!all_aligned16({k, v, k_cache, v_cache}) ||
+      ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(cu_seqlens) |
+        reinterpret_cast<uintptr_t>(start)) & 3u))
+    return H3_ERR_MISALIGNED;
+  if (d->num_segments == 0 || d->capacity == 0) return H3_OK;
+  if (k == nullptr || v == nullptr || cu_seqlens == nullptr || start == nullptr ||
+      (d->max_pages > 0 && block_table == nullptr) || (d->num_pages > 0 && (k_cache == nullptr || v_cache == nullptr)))
+    return H3_ERR_NULL;
+  if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
+  a.k = static_cast<__nv_bfloat16*>(const_cast<void*>(k));
+  a.v = static_cast<__nv_bfloat16*>(const_cast<void*>(v));
+  a.k_cache = const_cast<void*>(k_cache);
+  a.v_cache = const_cast<void*>(v_cache);
+  a.k_scale = const_cast<uint8_t*>(k_scale);
+  a.v_scale = const_cast<uint8_t*>(v_scale);
+  a.table = h3::PagedTable{block_table, d->max_pages, d->num_pages, page_shift_of(d->page_size)};
+  a.cu = cu_seqlens;
+  a.start = start;
+  a.num_segments = d->num_segments;
+  a.capacity = d->capacity;
+  a.heads = d->num_heads;
+  a.err = device_error_ptr();
+  if (a.err == nullptr) return H3_ERR_CUDA;
+  return from_cuda(h3::launch_kv_cache(a, d->head_dim, write, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+h3_status h3_kv_cache_write(const h3_kv_cache_desc* desc, const void* k, const void* v, void* k_cache, void* v_cache,
+                            uint8_t* k_scale, uint8_t* v_scale, const int32_t* block_table, const int32_t* cu_seqlens,
+                            const int32_t* start, h3_stream_t stream) {
+  return kv_cache_call(desc, k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, start, true, stream);
+}
+
+h3_status h3_kv_cache_read(const h3_kv_cache_desc* desc, const void* k_cache, const void* v_cache,
+                           const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                           const int32_t* cu_seqlens, const int32_t* start, void* k, void* v, h3_stream_t stream) {
+  return kv_cache_call(desc, k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, start, false, stream);
 }
 
 size_t h3_varlen_attn_workspace_size(int32_t num_segments, int32_t num_heads, int32_t max_seqlen,

@@ -43,7 +43,7 @@ inline int num_sms_of_current_device() {
 // harmless).
 template <int kBytes, typename K>
 inline cudaError_t allow_shared_memory(K* kernel) {
-  static std::atomic<K*> done[64][2];  // kernels of one type (one per head_dim) at most
+  static std::atomic<K*> done[64][8];  // kernels of one type at most; one more is set again at each call
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -17,6 +17,7 @@ enum : unsigned int {
   kErrBadPerm = 9,
   kErrBadBlockIndex = 10,
   kErrSmemLayout = 11,
+  kErrBadPage = 12,
 };
 
 // Longest legitimate wait inside one kernel is microseconds; give up after 2 s.
