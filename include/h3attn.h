@@ -415,9 +415,10 @@ H3_API h3_status h3_varlen_cross_attn_bwd(const h3_cross_attn_desc* desc, const 
  * k_cache, v_cache: device [num_pages, num_heads, page_size, head_dim], bf16 or e4m3.  An e4m3 cache has
  * one scale per row (a token of a head): k_scale, v_scale, device uint8 [num_pages, num_heads,
  * page_size], hold e + 127 for the least integer e with max |x| <= 448 * 2^e (kept within [-110, 120]).
- * The row stands for q * 2^e, q = x * 2^-e rounded to e4m3 (to nearest even, past 448 to 448; a NaN
- * stays one), which bf16 holds exactly (but for what rounds to 2^128, which is Inf, as Inf itself is).
- * Every call that reads the cache takes the row for that. */
+ * The row stands for q * 2^e, q = x * 2^-e rounded to e4m3 (to nearest even, past 448 to 448), which
+ * bf16 holds exactly (but for what rounds to 2^128, which is Inf, as Inf itself is).  A row with a
+ * NaN in it has the scale 255 and stands for NaN throughout; other NaN codes are not looked for.  Every
+ * call that reads the cache takes the row for that. */
 typedef struct {
   int32_t num_segments;
   int32_t capacity;           /* rows of k and v */
@@ -452,6 +453,65 @@ H3_API h3_status h3_kv_cache_read(const h3_kv_cache_desc* desc, const void* k_ca
                                   const uint8_t* v_scale, const int32_t* block_table,
                                   const int32_t* cu_seqlens, const int32_t* start, void* k, void* v,
                                   h3_stream_t stream);
+
+/* ---- Attention over a paged cache -----------------------------------------------------------------
+ * New tokens of running sequences (one each, or a chunk: a latent frame, a window) attend to the cached
+ * ones and to each other; their own keys and values are in the cache already (h3_kv_cache_write).
+ * Segment g has seqused_k[g] = n cached tokens, of which its query rows [cu_seqlens_q[g],
+ * cu_seqlens_q[g+1]) are the last.  The row at position p of the sequence sees the keys
+ *   j < n                                    with causal_block B = 0
+ *   j < min(n, (floor(p / B) + 1) * B)       otherwise: its own block of B tokens (1: causal by token;
+ *                                            the tokens of a latent frame: causal by frame) and all before
+ * and, with query head h reading key head h / (num_q_heads / num_kv_heads),
+ *   S_j = scale * <q, k_j>;  P = softmax(S);  o = sum_j P_j v_j;  lse = log sum_j exp(S_j)
+ * A row that sees no key (more rows than cached tokens; no cached token) gives o = 0 and lse = -inf.
+ * Cached tokens at n and past it are never multiplied in.  A token that a row must not see but another
+ * row of its segment sees has weight zero; it may be multiplied by that zero, so an Inf or NaN among its
+ * values in a bf16 cache can reach rows before it. */
+typedef struct {
+  int32_t num_segments;
+  int32_t max_seqlen_q; /* host upper bound on the query rows of a segment, <= capacity_q */
+  int32_t max_seqlen_k; /* host upper bound on the cached tokens of a segment */
+  int32_t capacity_q;   /* rows of q and o; row stride of lse */
+  int32_t num_q_heads;
+  int32_t num_kv_heads; /* divides num_q_heads, at most 128 query heads to a key head */
+  int32_t head_dim;     /* 64 or 128 */
+  int32_t cache_type;   /* as for h3_kv_cache_desc, and so are the next three */
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_pages;
+  int32_t causal_block; /* B >= 0 */
+  float softmax_scale;  /* <= 0 selects 1/sqrt(head_dim) */
+  int64_t q_stride;     /* elements between the rows of q: as for h3_cross_attn_desc */
+} h3_paged_attn_desc;
+
+/* Workspace bytes of h3_paged_attn_fwd for these sizes; 0 for invalid ones. */
+H3_API size_t h3_paged_attn_workspace_size(const h3_paged_attn_desc* desc);
+
+/* q           : device bf16 [capacity_q, num_q_heads, head_dim].
+ * k_cache, v_cache, k_scale, v_scale, block_table: as for h3_kv_cache_write (entries past a segment's
+ *               cached tokens are not read).
+ * cu_seqlens_q: device int32 [num_segments + 1]; must start at 0, not decrease, end <= capacity_q.
+ * seqused_k   : device int32 [num_segments]; at most max_pages * page_size each.
+ * o           : device bf16 [capacity_q, num_q_heads, head_dim], contiguous; rows of every segment
+ *               written, others untouched.  Must not overlap an input.
+ * lse         : device fp32 [num_q_heads, capacity_q] (natural log) or NULL.
+ * workspace   : device, h3_paged_attn_workspace_size() bytes, 16-byte aligned; need not be initialised.
+ *               Calls that may run at the same time need separate workspaces.
+ * A segment whose offsets or length are out of range, or with more rows than max_seqlen_q, is skipped
+ * (its rows are not written); one with more tokens than max_seqlen_k is computed in full; both are
+ * recorded as H3_ERR_BAD_CU_SEQLENS.  A page id out of range is read as page 0 and recorded as
+ * H3_ERR_BAD_PAGE.
+ * When max_seqlen_q * num_q_heads / num_kv_heads is at most 16 the cache is streamed once, split evenly
+ * over the GPU: single tokens want a tight bound.
+ * Errors: H3_ERR_NULL, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED, H3_ERR_MISALIGNED, H3_ERR_WORKSPACE,
+ *         H3_ERR_CUDA; device-side H3_ERR_BAD_CU_SEQLENS / H3_ERR_BAD_PAGE / H3_ERR_TIMEOUT. */
+H3_API h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* desc, const void* q, const void* k_cache,
+                                   const void* v_cache, const uint8_t* k_scale,
+                                   const uint8_t* v_scale, const int32_t* block_table,
+                                   const int32_t* cu_seqlens_q, const int32_t* seqused_k, void* o,
+                                   float* lse, void* workspace, size_t workspace_bytes,
+                                   h3_stream_t stream);
 
 /* Number of windows of the partition (host only; no device work).
  * [H3-fast] "window attention across GPUs": along each axis of length L with window w and

@@ -17,6 +17,8 @@ Calls:
                     (with equal offsets, that of varlen_attn_fwd)
   kv_cache_write / kv_cache_read   rows of keys and values into a paged cache (bf16, or e4m3 with a
                     power-of-two scale per row), and back out of it
+  paged_attn_fwd    attention of new tokens (single ones or chunks) over a paged cache, causal by token or
+                    by blocks of tokens
   window_count / window_pack / window_unpack   shifted 3D window partition and row gather/scatter
   window_attn_fwd   shifted 3D window attention read and written in place on the grid
   vsa_select / vsa_attn_fwd   block-sparse video attention: block gate scores + top-k
@@ -42,6 +44,7 @@ import torch
 __all__ = ["H3Error", "RopeConfig", "lib_path", "load_library", "rope_apply", "qk_norm_rope",
            "qk_norm_rope_bwd_workspace_size", "qk_norm_rope_bwd", "residual_norm", "ResidualNormGrads",
            "residual_norm_bwd_workspace_size", "residual_norm_bwd", "kv_cache_write", "kv_cache_read",
+           "paged_attn_workspace_size", "paged_attn_fwd",
            "varlen_attn_fwd",
            "varlen_attn_fwd_noalloc", "varlen_cross_attn_workspace_size", "varlen_cross_attn_fwd",
            "varlen_cross_attn_bwd_workspace_size", "varlen_cross_attn_bwd",
@@ -113,6 +116,15 @@ class _KvCacheDesc(ctypes.Structure):
     pack = struct.Struct("@8i2q").pack
 
 
+class _PagedAttnDesc(ctypes.Structure):
+    """Mirror of h3_paged_attn_desc."""
+    _fields_ = [("num_segments", _I), ("max_seqlen_q", _I), ("max_seqlen_k", _I), ("capacity_q", _I),
+                ("num_q_heads", _I), ("num_kv_heads", _I), ("head_dim", _I), ("cache_type", _I), ("page_size", _I),
+                ("num_pages", _I), ("max_pages", _I), ("causal_block", _I), ("softmax_scale", ctypes.c_float),
+                ("q_stride", _L)]
+    pack = struct.Struct("@12ifq").pack
+
+
 class _CrossAttnDesc(ctypes.Structure):
     """Mirror of h3_cross_attn_desc."""
     _fields_ = [("num_segments", _I), ("max_seqlen_q", _I), ("max_seqlen_k", _I), ("capacity_q", _I),
@@ -165,6 +177,8 @@ def load_library():
         "h3_residual_norm_bwd": (I32, [P] * 18 + [U64, P]),
         "h3_kv_cache_write": (I32, [P] * 11),
         "h3_kv_cache_read": (I32, [P] * 11),
+        "h3_paged_attn_workspace_size": (U64, [P]),
+        "h3_paged_attn_fwd": (I32, [P] * 12 + [U64, P]),
         "h3_varlen_attn_workspace_size": (U64, [I32, I32, I32, I32]),
         "h3_varlen_attn_fwd": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P, U64, P]),
         "h3_varlen_attn_fwd_noalloc": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P]),
@@ -763,6 +777,67 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: tor
     _cache_call("h3_kv_cache_read", (k_out, v_out), strides, k_cache, v_cache, block_table, cu_seqlens, start, k_scale,
                 v_scale, False)
     return k_out, v_out
+
+
+def paged_attn_workspace_size(num_segments: int, max_seqlen_q: int, max_seqlen_k: int, capacity_q: int,
+                              num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int = 16) -> int:
+    desc = _PagedAttnDesc.pack(num_segments, max_seqlen_q, max_seqlen_k, capacity_q, num_q_heads, num_kv_heads,
+                               head_dim, 1, page_size, 0, 0, 0, 0.0, 0)
+    return int(load_library().h3_paged_attn_workspace_size(desc))
+
+
+def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                   cu_seqlens_q: torch.Tensor, seqused_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                   k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                   causal_block: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False,
+                   lse: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """Attention of new tokens over a paged cache: the query rows of segment g (cu_seqlens_q, int32 [S+1]) are
+    the last of its seqused_k[g] cached tokens (int32 [S]), whose keys and values kv_cache_write has put
+    into k_cache, v_cache (and k_scale, v_scale) under block_table.
+
+    q bf16 [C, Hq, D], Hkv dividing Hq; may be a part of a fused projection.  causal_block 0: every row sees
+    every cached token; B > 0: the row at position p of its sequence sees those before (p // B + 1) * B, so
+    1 is causal by token and the tokens of a frame causal by frame.  max_seqlen_q and max_seqlen_k bound a
+    segment's rows and tokens; when max_seqlen_q * Hq / Hkv is at most 16 the cache is streamed once for all
+    of a key head's rows, so single tokens want a tight bound.  A row that sees nothing gives 0 and an
+    LSE of -inf; rows of `out` outside every segment are left untouched.  Returns out [C, Hq, D] (and lse
+    fp32 [Hq, C] when requested).
+    """
+    dev = q.device
+    q_stride = _rows(q, "q", dev)
+    C, H, D = q.shape
+    _aux(cu_seqlens_q, "cu_seqlens_q", _I32, dev)
+    _aux(seqused_k, "seqused_k", _I32, dev)
+    S = cu_seqlens_q.numel() - 1
+    if S < 0 or seqused_k.numel() != S:
+        raise ValueError("cu_seqlens_q must have one entry per segment and one more, seqused_k one per segment")
+    (heads, dim, *rest), cache = _cache_inputs(k_cache, v_cache, k_scale, v_scale, block_table, S, dev)
+    if dim != D:
+        raise ValueError("the cache must have q's head_dim")
+    if out is None:
+        out = torch.empty(q.shape, dtype=_BF16, device=dev)
+    else:
+        _require(out, "out", _BF16, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is not None:
+        _require(lse, "lse", _F32, dev)
+        if lse.shape != (H, C):
+            raise ValueError("lse must be [Hq, C]")
+    elif return_lse:
+        lse = torch.empty((H, C), dtype=_F32, device=dev)
+    if C > 0:
+        lib = load_library()
+        desc = _PagedAttnDesc.pack(S, int(max_seqlen_q), int(max_seqlen_k), C, H, heads, D, *rest, int(causal_block),
+                                   0.0 if softmax_scale is None else float(softmax_scale), q_stride)
+        if workspace is None:
+            workspace = torch.empty(lib.h3_paged_attn_workspace_size(desc) or 16, dtype=_U8, device=dev)
+        else:
+            _require(workspace, "workspace", _U8, dev)
+        _launch(lib.h3_paged_attn_fwd, "h3_paged_attn_fwd", dev, desc, q.data_ptr(), *cache, cu_seqlens_q.data_ptr(),
+                seqused_k.data_ptr(), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel())
+    return (out, lse) if lse is not None else out
 
 
 def varlen_attn_workspace_size(num_segments: int, num_heads: int, max_seqlen: int, head_dim: int) -> int:

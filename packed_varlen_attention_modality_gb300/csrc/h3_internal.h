@@ -111,6 +111,7 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool backward, cudaS
 // ---- paged key/value cache --------------------------------------------------------------------
 // Cache [pages, heads, page, D]; e4m3 with one biased exponent per row, [pages, heads, page].
 constexpr int kScaleMin = -110, kScaleMax = 120;
+constexpr uint32_t kScaleNan = 255;
 struct PagedTable {
   const int32_t* pages;  // [segments, per_segment]
   int per_segment, num_pages, page_shift;
@@ -329,6 +330,42 @@ inline size_t cross_token_bytes(const CrossSegments& s, int head_dim) {
   return chunks == 1 || all < 256 ? 256 : all;  // never none: the call always takes a workspace
 }
 cudaError_t launch_cross_token(const CrossTokenArgs& a, int head_dim, cudaStream_t stream);
+
+// ---- attention over a paged cache ---------------------------------------------------------------
+struct PagedSegments {
+  const int32_t* cu_q;
+  const int32_t* used;  // tokens of each segment, the new ones included
+  PagedTable table;
+  int num_segments, max_seqlen_q, max_seqlen_k, capacity_q, num_q_heads, num_kv_heads;
+  int causal_block;  // tokens of a causal block; 0: every row sees every key
+};
+
+// Few rows per segment: at most kPagedTokenRows of (rows x query heads per key head).
+constexpr int kPagedTokenRows = 16;
+constexpr int kPagedTokenCtas = 304;  // 2 x 152
+struct PagedTokenArgs {
+  PagedSegments seg;
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  const void *k, *v;  // [pages, heads, page, D]
+  const uint8_t *k_scale, *v_scale;
+  __nv_bfloat16* o;
+  float* lse;
+  float scale;
+  int max_rows;  // max_seqlen_q x query heads per key head
+  int4* joins;   // [kPagedTokenCtas]: segment, key head, slot of the first piece, pieces
+  float* partials;
+  unsigned int* err;
+};
+// floats of a piece's partial results: rows of head_dim values, then the rows' LSEs (16-byte units)
+constexpr size_t paged_token_partial(int rows, int head_dim) {
+  return static_cast<size_t>(rows) * head_dim + (rows + 3) / 4 * 4;
+}
+constexpr size_t paged_token_joins_bytes() { return kPagedTokenCtas * sizeof(int4); }
+constexpr size_t paged_token_bytes(int rows, int head_dim) {
+  return paged_token_joins_bytes() + 2 * kPagedTokenCtas * paged_token_partial(rows, head_dim) * sizeof(float);
+}
+cudaError_t launch_paged_token(const PagedTokenArgs& a, int head_dim, cudaStream_t stream);
 
 // ---- VSA block gate + top-k ----------------------------------------------------------------
 struct VsaGeom {

@@ -635,6 +635,87 @@ h3_status h3_kv_cache_read(const h3_kv_cache_desc* desc, const void* k_cache, co
   return kv_cache_call(desc, k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, start, false, stream);
 }
 
+// ---- attention over a paged cache -------------------------------------------------------------------
+
+namespace {
+
+bool paged_sizes_ok(const h3_paged_attn_desc* d) {
+  return d->num_segments >= 0 && d->num_segments <= 65535 && d->max_seqlen_q >= 0 && d->max_seqlen_k >= 0 &&
+         d->capacity_q >= 0 && d->max_seqlen_q <= d->capacity_q && d->num_q_heads > 0 && d->num_q_heads <= 65535 &&
+         d->num_kv_heads > 0 && d->num_q_heads % d->num_kv_heads == 0 && d->num_q_heads / d->num_kv_heads <= 128 &&
+         (d->cache_type == H3_TYPE_BF16 || d->cache_type == H3_TYPE_E4M3) && page_shift_of(d->page_size) >= 0 &&
+         d->num_pages >= 0 && d->max_pages >= 0 && d->causal_block >= 0;
+}
+
+// Few rows per segment take the key-streaming kernel: its 16-row tile holds all of a key head's rows.
+bool paged_few_rows(const h3_paged_attn_desc* d) {
+  return static_cast<int64_t>(d->max_seqlen_q) * (d->num_q_heads / d->num_kv_heads) <= h3::kPagedTokenRows;
+}
+
+}  // namespace
+
+size_t h3_paged_attn_workspace_size(const h3_paged_attn_desc* d) {
+  if (d == nullptr || !paged_sizes_ok(d) || d->num_segments == 0 || d->max_seqlen_q == 0) return 0;
+  if (d->head_dim != 64 && d->head_dim != 128) return 0;
+  if (paged_few_rows(d))
+    return h3::paged_token_bytes(d->max_seqlen_q * (d->num_q_heads / d->num_kv_heads), d->head_dim);
+  return 0;
+}
+
+h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* d, const void* q, const void* k_cache, const void* v_cache,
+                            const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                            const int32_t* cu_seqlens_q, const int32_t* seqused_k, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, h3_stream_t stream) {
+  if (d == nullptr) return H3_ERR_NULL;
+  if (!paged_sizes_ok(d) || !(d->softmax_scale <= 0.f || std::isfinite(d->softmax_scale))) return H3_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return H3_ERR_UNSUPPORTED;
+  const bool e4m3 = d->cache_type == H3_TYPE_E4M3;
+  if (e4m3 != (k_scale != nullptr) || e4m3 != (v_scale != nullptr)) return H3_ERR_NULL;
+  int64_t q_stride;
+  const h3_status st = token_stride(d->q_stride, d->num_q_heads, d->head_dim, &q_stride);
+  if (st != H3_OK) return st;
+  // a page's rows of a head are one coordinate of a tensor map
+  if (static_cast<int64_t>(d->num_pages) * d->num_kv_heads > INT32_MAX) return H3_ERR_INVALID_ARG;
+  if (!all_aligned16({q, k_cache, v_cache, k_scale, v_scale, o, workspace}) ||
+      ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(cu_seqlens_q) |
+        reinterpret_cast<uintptr_t>(seqused_k) | reinterpret_cast<uintptr_t>(lse)) & 3u))
+    return H3_ERR_MISALIGNED;
+  if (d->num_segments == 0 || d->max_seqlen_q == 0) return H3_OK;
+  if (q == nullptr || o == nullptr || cu_seqlens_q == nullptr || seqused_k == nullptr ||
+      (d->max_pages > 0 && block_table == nullptr) || (d->num_pages > 0 && (k_cache == nullptr || v_cache == nullptr)))
+    return H3_ERR_NULL;
+  const size_t need = h3_paged_attn_workspace_size(d);
+  if (workspace == nullptr || workspace_bytes < need) return H3_ERR_WORKSPACE;
+  if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
+  unsigned int* err = device_error_ptr();
+  if (err == nullptr) return H3_ERR_CUDA;
+  const int group = d->num_q_heads / d->num_kv_heads;
+  const float scale = d->softmax_scale > 0.f ? d->softmax_scale : static_cast<float>(1.0 / std::sqrt(d->head_dim));
+  const h3::PagedSegments seg{cu_seqlens_q, seqused_k,
+                              h3::PagedTable{block_table, d->max_pages, d->num_pages, page_shift_of(d->page_size)},
+                              d->num_segments, d->max_seqlen_q, d->max_seqlen_k, d->capacity_q, d->num_q_heads,
+                              d->num_kv_heads, d->causal_block};
+  if (paged_few_rows(d)) {
+    h3::PagedTokenArgs t{};
+    t.seg = seg;
+    t.q = static_cast<const __nv_bfloat16*>(q);
+    t.q_stride = q_stride;
+    t.k = k_cache;
+    t.v = v_cache;
+    t.k_scale = k_scale;
+    t.v_scale = v_scale;
+    t.o = static_cast<__nv_bfloat16*>(o);
+    t.lse = lse;
+    t.scale = scale;
+    t.max_rows = d->max_seqlen_q * group;
+    t.joins = static_cast<int4*>(workspace);
+    t.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + h3::paged_token_joins_bytes());
+    t.err = err;
+    return from_cuda(h3::launch_paged_token(t, d->head_dim, reinterpret_cast<cudaStream_t>(stream)));
+  }
+  return H3_ERR_UNSUPPORTED;
+}
+
 size_t h3_varlen_attn_workspace_size(int32_t num_segments, int32_t num_heads, int32_t max_seqlen,
                                      int32_t head_dim) {
   (void)num_heads;

@@ -6,7 +6,8 @@
 // magnitude is at most 448 * 2^e, so no value saturates and none but the smallest lose bits to e4m3's
 // subnormals; e4m3 is a floating type, so a finer scale would gain nothing.  A value is off by half an e4m3
 // step, 2^-4 of itself at most (or 2^-10 * 2^e below 2^-6 * 2^e), and q * 2^e is exact in bf16: what is
-// read back is what the cache holds.
+// read back is what the cache holds.  A row with a NaN in it is marked by its scale and reads back as NaN
+// throughout, so no reader has to look for NaN among the values.
 //
 // Memory-bound: each row is read once and written once.  A row is D / 8 lanes of eight values; a warp takes
 // a token, finds its page once and runs over the heads of K and V with kUnroll rows a lane in flight; when
@@ -120,19 +121,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_cache_kernel(const __grid_
         }
         const uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
         if (kWrite) {
-          float x[8], most = 0.f;
+          float x[8];
+          uint32_t most = 0u;  // the largest magnitude's bits: their order is the values', NaN above all
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             x[2 * i] = __uint_as_float(w[i] << 16);
             x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            most = fmaxf(most, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));  // a NaN is passed over
+            most = max(most, max(w[i] << 16 & 0x7fffffffu, w[i] & 0x7fff0000u));
           }
 #pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
           // most = 1.m * 2^(b - 127) <= 448 * 2^e = 1.75 * 2^(8 + e)
-          const int b = static_cast<int>(__float_as_uint(most) >> 23);
-          const int e = min(max(b - 127 - 8 + ((__float_as_uint(most) & 0x7fffffu) > 0x600000u ? 1 : 0), kScaleMin),
-                            kScaleMax);
+          const int b = static_cast<int>(most >> 23);
+          const int e = min(max(b - 127 - 8 + ((most & 0x7fffffu) > 0x600000u ? 1 : 0), kScaleMin), kScaleMax);
           const float inv = scale_of(127 - e);
           uint2 q;
           q.x = e4m3x2_pack(x[0] * inv, x[1] * inv) | e4m3x2_pack(x[2] * inv, x[3] * inv) << 16;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_cache_kernel(const __grid_
           if (j >= rows) continue;
           const size_t c = cached(j);
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(j >= a.heads ? a.v_cache : a.k_cache) + c * D + col) = q;
-          if (col == 0) (j >= a.heads ? a.v_scale : a.k_scale)[c] = static_cast<uint8_t>(e + 127);
+          if (col == 0) (j >= a.heads ? a.v_scale : a.k_scale)[c] = static_cast<uint8_t>(most > 0x7f800000u ? kScaleNan : e + 127);
         } else {
           if (j >= rows) continue;
           const float s = scale_of(byte[u]);

@@ -12,6 +12,34 @@ __device__ __forceinline__ int page_id(const PagedTable& t, int g, int p) {
 }
 __device__ __forceinline__ bool page_ok(const PagedTable& t, int id) { return id >= 0 && id < t.num_pages; }
 
+struct PagedSegment {
+  int q0, rows;  // query rows
+  int used;      // cached tokens, of which the rows are the last
+};
+
+// Segment g; one that is out of range has neither rows nor keys, and is recorded.
+__device__ __forceinline__ PagedSegment checked_paged_segment(const PagedSegments& s, int g, unsigned int* err) {
+  const int a = s.cu_q[g], b = s.cu_q[g + 1], used = s.used[g];
+  const bool ordered = a >= 0 && a <= b && b <= s.capacity_q && (g > 0 || a == 0);
+  const int64_t room = s.table.num_pages > 0 ? static_cast<int64_t>(s.table.per_segment) << s.table.page_shift : 0;
+  if (!ordered || b - a > s.max_seqlen_q || used < 0 || used > room) {
+    record_error(err, kErrBadCuSeqlens);
+    return PagedSegment{0, 0, 0};
+  }
+  if (used > s.max_seqlen_k) record_error(err, kErrBadCuSeqlens);  // computed all the same
+  return PagedSegment{a, b - a, used};
+}
+
+// Keys that row i of a segment sees.  Its position, used - rows + i, is negative when there are more rows than
+// tokens; such a row sees none.
+__device__ __forceinline__ int row_limit(const PagedSegment& s, int i, int block) {
+  if (block == 0) return s.used;
+  const int p = s.used - s.rows + i;
+  if (p < 0) return 0;
+  const int rest = block - p % block;  // to the end of the row's block
+  return s.used - p <= rest ? s.used : p + rest;
+}
+
 // Two e4m3 values (the low and the high byte) as floats.
 __device__ __forceinline__ float2 e4m3x2_floats(uint32_t pair) {
   uint32_t h;
@@ -28,7 +56,19 @@ __device__ __forceinline__ uint32_t e4m3x2_pack(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// 2^e of a row's biased exponent
-__device__ __forceinline__ float scale_of(uint32_t biased) { return __uint_as_float(biased << 23); }
+// Two e4m3 bytes, picked twice each out of x and y by `pick` (low byte's, low byte's, high byte's, high byte's), as
+// packed bf16, exactly: sign and the seven other bits go to their places in bf16, where they stand for the value
+// times 2^(7 - 127) (a subnormal e4m3 for a subnormal bf16), and a product takes that back.
+__device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t x, uint32_t y, uint32_t pick) {
+  const uint32_t b = __byte_perm(x, y, pick);
+  const uint32_t bits = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bits), "r"(0x7b807b80u));  // 2^120
+  return r;
+}
+// 2^e of a row's biased exponent; NaN for kScaleNan, which marks a row that held a NaN
+__device__ __forceinline__ float scale_of(uint32_t biased) {
+  return __uint_as_float(biased == kScaleNan ? 0x7fffffffu : biased << 23);
+}
 
 }  // namespace h3

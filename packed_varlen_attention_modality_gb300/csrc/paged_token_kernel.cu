@@ -1,0 +1,580 @@
+// Attention over a paged cache for a few rows per segment (the single tokens of running streams): every key
+// row is read once and meets at most 16 query rows, so the call is bound by reading K and V.
+//
+// Work is laid out in units of 64 keys of a (segment, key head) and dealt to two CTAs an SM in equal shares, so
+// streams of unlike lengths keep the GPU even; every CTA finds its share by a scan of the lengths.  A pair that a
+// share's end cuts leaves fp32 partial results (O normalised by its own sum, and the LSE), which a second kernel
+// joins in order.  The 16 rows of the tensor-core tile are the segment's rows times the query heads that share
+// the key head, so shared heads cost no second read.  Each of a CTA's four warps streams 16-key blocks of K and V
+// through its own ring in shared memory (16-byte asynchronous copies, the next piece's blocks included), computes
+// S = Q K^T and O += P V with 16 x 8 x 16 matrix instructions, and keeps a running max and sum; the warps are
+// added in order at the end of a piece.  A block lies in one page, whose id is looked up a block ahead.
+//
+// An e4m3 block becomes bf16 in registers: its bits, moved to bf16's places, are the value times 2^-120, which one
+// product mends exactly (subnormals too); the rows' scales go to the scores and to P, which are fp32.  The
+// order of the dims in S's product and in O's columns is chosen so that a lane's bytes lie together.
+// Scores, max, sum and O are fp32; P is rounded to bf16 for the product with V, o once at the end.
+#include <cuda_bf16.h>
+
+#include "h3_internal.h"
+#include "launch.h"
+#include "paged_segments.cuh"
+#include "sm103_ptx.cuh"
+
+namespace h3 {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kRows = 16;    // query rows of a CTA
+constexpr int kBlock = 16;   // keys of a block
+constexpr int kUnit = kBlock * kWarps;
+constexpr int kCtasPerSm = 2;
+constexpr int kMinShare = 2;   // units
+constexpr int kMaxPieces = 16;  // looked up at once
+static_assert(kRows == kPagedTokenRows, "host and device agree");
+
+template <int D, bool kE4m3>
+struct Cfg {
+  static constexpr int kRowBytes = kE4m3 ? D : 2 * D;
+  static constexpr int kHalf = kBlock * kRowBytes;                          // K's part of a stage
+  static constexpr int kStageBytes = 2 * kHalf + (kE4m3 ? 2 * kBlock : 0);  // K, V, their scales
+  static constexpr int kStages = kE4m3 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
+  static constexpr int kOut = D + 8;  // floats of a row while the warps are added (the pad keeps banks apart)
+  static constexpr int kSmemBytes = kWarps * kStages * kStageBytes + kRows * kOut * 4;
+  // where a 16-byte piece of a row lies: as the reads below meet no bank twice
+  __device__ static __forceinline__ int piece_at(int row, int piece) {
+    return row * kRowBytes + ((kRowBytes == 64 ? piece ^ ((row >> 1) & 3) : piece ^ (row & 7)) << 4);
+  }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The part of a (segment, key head) pair that a CTA takes: keys [first, end).
+struct Piece {
+  PagedSegment s;
+  int g, head, first, end;
+  int slot;  // -1: the whole pair
+};
+
+// Units of a pair.
+__device__ __forceinline__ int units_of(const PagedSegment& s, int block) {
+  const int keys = s.rows == 0 ? 0 : row_limit(s, s.rows - 1, block);
+  return s.rows == 0 ? 0 : keys <= kUnit ? 1 : (keys + kUnit - 1) / kUnit;
+}
+
+// What the scan of the segments leaves: those of a tile of kThreads, and the units before each.
+struct Scan {
+  PagedSegment seg[kThreads];
+  uint64_t before[kThreads + 1];  // units of all key heads
+  uint64_t warp[kWarps];
+};
+
+__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* s_warp, uint64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  uint64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_warp[w];
+    all += s_warp[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+template <int D>
+__device__ __forceinline__ float* partial_of(const PagedTokenArgs& a, int cta, int slot) {
+  return a.partials + (static_cast<size_t>(cta) * 2 + slot) * paged_token_partial(a.max_rows, D);
+}
+
+template <int D, bool kE4m3>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
+  using C = Cfg<D, kE4m3>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Scan scan;
+  __shared__ Piece pieces[kMaxPieces];
+  __shared__ int s_pieces, s_more;
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  grid_dependency_wait();
+  launch_dependents();
+  const int S = a.seg.num_segments, heads = a.seg.num_kv_heads, block = a.seg.causal_block;
+  const int group = a.seg.num_q_heads / heads;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gr = lane >> 2, quad = lane & 3, c2 = quad * 2;  // this lane's rows gr, gr + 8 and column pair
+  unsigned int* scan_err = blockIdx.x == 0 ? a.err : nullptr;  // one CTA records what is wrong with the offsets
+
+  // ---- this CTA's share of the units
+  auto scan_tile = [&](int g0, uint64_t base, unsigned int* err) {  // returns the units up to the tile's end
+    PagedSegment s{0, 0, 0};
+    if (g0 + tid < S) s = checked_paged_segment(a.seg, g0 + tid, err);
+    const uint64_t n = static_cast<uint64_t>(units_of(s, block)) * heads;
+    uint64_t total;
+    const uint64_t at = block_scan(n, scan.warp, &total);
+    scan.seg[tid] = s;
+    scan.before[tid] = base + at;
+    if (tid == 0) scan.before[kThreads] = base + total;
+    __syncthreads();
+    return base + total;
+  };
+  uint64_t all = 0;
+  for (int g0 = 0; g0 < S; g0 += kThreads) all = scan_tile(g0, all, scan_err);
+  uint64_t share = (all + gridDim.x - 1) / gridDim.x;
+  if (share < kMinShare) share = kMinShare;
+  const uint64_t begin = share * blockIdx.x;
+  const uint64_t stop = begin + share < all ? begin + share : all;
+  if (tid == 0) a.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (begin >= stop) return;
+
+  uint8_t* ring = smem + warp * kStages * C::kStageBytes;
+  const uint32_t ring32 = smem_u32(ring);
+  float* s_o = reinterpret_cast<float*>(smem + kWarps * kStages * C::kStageBytes);
+  const float scale_log2 = a.scale * 1.4426950408889634f;
+
+  int tile = 0;
+  uint64_t at = begin;
+  if (S > kThreads) {  // the tile with the first unit (with one tile it is there already)
+    for (uint64_t base = 0;; tile += kThreads) {
+      base = scan_tile(tile, base, nullptr);
+      if (at < base) break;
+      __syncthreads();
+    }
+  }
+  for (;;) {
+    // ---- the next pieces, by one thread
+    if (tid == 0) {
+      int n = 0;
+      while (n < kMaxPieces && at < stop && at < scan.before[kThreads]) {
+        int lo = 0, hi = kThreads - 1;  // the last segment with before <= at
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (scan.before[mid] <= at) lo = mid; else hi = mid - 1;
+        }
+        Piece p;
+        p.s = scan.seg[lo];
+        p.g = tile + lo;
+        const int units = units_of(p.s, block);
+        const uint64_t in = at - scan.before[lo];
+        p.head = static_cast<int>(in / units);
+        const int u0 = static_cast<int>(in % units);
+        const int u1 = static_cast<int>(u0 + (stop - at) < static_cast<uint64_t>(units) ? u0 + (stop - at) : units);
+        const int keys = row_limit(p.s, p.s.rows - 1, block);
+        p.first = u0 * kUnit;
+        p.end = u1 == units ? keys : u1 * kUnit;
+        // the piece at the start of the share has slot 0, one at its end slot 1
+        p.slot = u0 == 0 && u1 == units ? -1 : at == begin ? 0 : 1;
+        if (u0 == 0 && u1 < units) {  // the first of a cut pair: all but the first of the others are whole shares
+          const uint64_t rest = units - u1;
+          a.joins[blockIdx.x] = make_int4(p.g, p.head, p.slot, 1 + static_cast<int>((rest + share - 1) / share));
+        }
+        pieces[n++] = p;
+        at += u1 - u0;
+      }
+      s_pieces = n;
+      s_more = at < stop;
+    }
+    __syncthreads();
+    const int num_pieces = s_pieces;
+
+    // ---- loads: a cursor that runs ahead of the computation, over the pieces' blocks
+    struct Cursor {
+      int piece, b, blocks;  // this warp's block b of the piece's
+    };
+    auto blocks_of = [&](int p) { return (pieces[p].end - pieces[p].first + kBlock - 1) / kBlock; };
+    auto settle = [&](Cursor& c) {  // onto the next block there is
+      while (c.piece < num_pieces && c.b >= c.blocks) {
+        ++c.piece;
+        c.b = warp;
+        c.blocks = c.piece < num_pieces ? blocks_of(c.piece) : 0;
+      }
+    };
+    auto lookup = [&](const Cursor& c) {
+      if (c.piece >= num_pieces) return 0;
+      const Piece& p = pieces[c.piece];
+      return page_id(a.seg.table, p.g, (p.first + c.b * kBlock) >> a.seg.table.page_shift);
+    };
+    auto load = [&](const Cursor& c, int id, int stage) {
+      if (c.piece >= num_pieces) return;
+      const Piece& p = pieces[c.piece];
+      if (!page_ok(a.seg.table, id)) {
+        if (lane == 0) record_error(a.err, kErrBadPage);
+        id = 0;
+      }
+      const int key = p.first + c.b * kBlock, left = p.end - key;
+      const int shift = a.seg.table.page_shift;
+      const size_t row = ((static_cast<size_t>(id) * heads + p.head) << shift) + (key & ((1 << shift) - 1));
+      const uint32_t dst = ring32 + stage * C::kStageBytes;
+      constexpr int kPieces = C::kRowBytes / 16;
+      const uint8_t* kp = static_cast<const uint8_t*>(a.k) + row * C::kRowBytes;
+      const uint8_t* vp = static_cast<const uint8_t*>(a.v) + row * C::kRowBytes;
+#pragma unroll
+      for (int i = lane; i < kBlock * kPieces; i += 32) {  // a block's rows lie back to back; zeros past the end
+        const int r = i / kPieces;
+        const uint32_t bytes = r < left ? 16u : 0u, off = C::piece_at(r, i % kPieces);
+        cp_async16(dst + off, kp + i * 16, bytes);
+        cp_async16(dst + C::kHalf + off, vp + i * 16, bytes);
+      }
+      if (kE4m3 && lane < 2)
+        cp_async16(dst + 2 * C::kHalf + lane * kBlock, (lane == 0 ? a.k_scale : a.v_scale) + row, 16);
+    };
+    Cursor ahead{0, warp, blocks_of(0)};
+    settle(ahead);
+    int stage = 0, id = lookup(ahead);
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) {
+      load(ahead, id, i);
+      cp_async_commit();
+      ahead.b += kWarps;
+      settle(ahead);
+      id = lookup(ahead);
+    }
+
+#pragma unroll 1
+    for (int pi = 0; pi < num_pieces; ++pi) {
+      const Piece& p = pieces[pi];
+      const int rows = p.s.rows * group;
+      // Q fragments: row r = (segment row r / group, head r % group of the key head's)
+      uint32_t q[D / 16][4];
+      int limit[2], low = p.end;  // keys that this lane's rows see; the least of all rows
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = gr + 8 * h;
+        const __nv_bfloat16* row = a.q + static_cast<size_t>(p.s.q0 + r / group) * a.q_stride +
+                                   (p.head * group + r % group) * D;
+        if (kE4m3) {  // step kk: dims 4 kk + {0, 1} and {2, 3} of the lane's D / 4
+          const uint2* src = reinterpret_cast<const uint2*>(row + quad * (D / 4));
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint2 x = r < rows ? src[kk] : make_uint2(0u, 0u);
+            q[kk][h] = x.x;
+            q[kk][2 + h] = x.y;
+          }
+        } else {
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(row + c2);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            q[kk][h] = r < rows ? src[kk * 8] : 0u;
+            q[kk][2 + h] = r < rows ? src[kk * 8 + 4] : 0u;
+          }
+        }
+        limit[h] = r < rows ? row_limit(p.s, r / group, block) : p.end;
+      }
+      low = min(low, row_limit(p.s, 0, block));
+
+      float o[D / 8][4] = {};
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      const int nblocks = (p.end - p.first + kBlock - 1) / kBlock;
+#pragma unroll 1
+      for (int b = warp; b < nblocks; b += kWarps) {
+        load(ahead, id, stage == 0 ? kStages - 1 : stage - 1);
+        cp_async_commit();
+        ahead.b += kWarps;
+        settle(ahead);
+        id = lookup(ahead);
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        const uint32_t kb = ring32 + stage * C::kStageBytes, vb = kb + C::kHalf;
+        const uint8_t* base = ring + stage * C::kStageBytes;
+        const int key = p.first + b * kBlock;
+        const int mat = lane >> 3, mr = lane & 7;
+        float sc[2][4] = {};
+        if (!kE4m3) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t f[4];  // keys 0-7: dims 0-7, 8-15 of the step; keys 8-15 the same
+            ldmatrix4(f, kb + C::piece_at((mat >> 1) * 8 + mr, 2 * kk + (mat & 1)));
+            mma_16816(sc[0], q[kk], f[0], f[1]);
+            mma_16816(sc[1], q[kk], f[2], f[3]);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const int row = n * 8 + gr;
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+              const uint4 w4 = *reinterpret_cast<const uint4*>(base + C::piece_at(row, quad * (D / 64) + x));
+              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_16816(sc[n], q[4 * x + i], e4m3_pair_bf16(w[i], w[i], 0x1100), e4m3_pair_bf16(w[i], w[i], 0x3322));
+            }
+            const uint32_t ks = *reinterpret_cast<const uint16_t*>(base + 2 * C::kHalf + n * 8 + c2);
+            const float s0 = scale_of(ks & 0xffu), s1 = scale_of(ks >> 8);
+            sc[n][0] *= s0;
+            sc[n][1] *= s1;
+            sc[n][2] *= s0;
+            sc[n][3] *= s1;
+          }
+        }
+        if (key + kBlock > low) {  // by select, so NaN/Inf there is discarded
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key + n * 8 + c2 + (i & 1) >= min(limit[i >> 1], p.end)) sc[n][i] = -INFINITY;
+        }
+        // row maxima over the quad; the reference max moves only when it grows by more than 2^8
+        float alpha[2] = {1.f, 1.f};
+        bool moved = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          if (x > m[h] && (m[h] == -INFINITY || (x - m[h]) * scale_log2 > 8.f)) {
+            alpha[h] = ex2_approx((m[h] - x) * scale_log2);
+            m[h] = x;
+            l[h] *= alpha[h];
+            moved = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][i] *= alpha[i >> 1];
+        }
+        uint32_t pw[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float v0 = 1.f, v1 = 1.f;
+          if (kE4m3) {
+            const uint32_t vs = *reinterpret_cast<const uint16_t*>(base + 2 * C::kHalf + kBlock + n * 8 + c2);
+            v0 = scale_of(vs & 0xffu);
+            v1 = scale_of(vs >> 8);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float mb = m[h] == -INFINITY ? 0.f : m[h] * scale_log2;
+            const float e0 = ex2_approx(fmaf(sc[n][2 * h], scale_log2, -mb));
+            const float e1 = ex2_approx(fmaf(sc[n][2 * h + 1], scale_log2, -mb));
+            l[h] += e0 + e1;
+            // (a weight of zero stays one: past the end lie rows whose scale may be anything)
+            pw[2 * n + h] = kE4m3 ? pack_bf16x2(e0 == 0.f ? 0.f : e0 * v0, e1 == 0.f ? 0.f : e1 * v1) : pack_bf16x2(e0, e1);
+          }
+        }
+        if (!kE4m3) {
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            uint32_t f[4];  // dims 0-7 of the step: keys 0-7, 8-15; dims 8-15 the same
+            ldmatrix4_trans(f, vb + C::piece_at((mat & 1) * 8 + mr, 2 * n + (mat >> 1)));
+            mma_16816(o[2 * n], pw, f[0], f[1]);
+            mma_16816(o[2 * n + 1], pw, f[2], f[3]);
+          }
+        } else {
+          // column gr of tile j is dim gr * D / 8 + j: the lane's dims of a key are D / 8 bytes in a row
+          const uint8_t* vbase = base + C::kHalf;
+          uint32_t w[4][D / 32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = c2 + (k & 1) + 8 * (k >> 1);
+            if (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vbase + C::piece_at(row, gr));
+              w[k][0] = x.x;
+              w[k][1] = x.y;
+              w[k][D / 32 - 2] = x.z;
+              w[k][D / 32 - 1] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(vbase + C::piece_at(row, gr >> 1) + (gr & 1) * 8);
+              w[k][0] = x.x;
+              w[k][1] = x.y;
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            const uint32_t sel = (j & 3) * 0x11 + 0x4400 + (j & 3) * 0x1100;  // byte j of each, twice
+            mma_16816(o[j], pw, e4m3_pair_bf16(w[0][j / 4], w[1][j / 4], sel), e4m3_pair_bf16(w[2][j / 4], w[3][j / 4], sel));
+          }
+        }
+        __syncwarp();  // the stage is read: it may be loaded again
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+      }
+
+      // ---- the warps, added in order
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        if (quad == 0) {
+          s_m[warp][gr + 8 * h] = m[h];
+          s_l[warp][gr + 8 * h] = l[h];
+        }
+      }
+      __syncthreads();
+      float f[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][gr + 8 * h]);
+        f[h] = top == -INFINITY ? 0.f : ex2_approx((m[h] - top) * scale_log2);  // 0 for a warp without keys
+      }
+#pragma unroll 1
+      for (int w = 0; w < kWarps; ++w) {
+        if (warp == w) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int col = kE4m3 ? (c2 + e) * (D / 8) + n : n * 8 + c2 + e;
+                float* dst = s_o + (gr + 8 * h) * C::kOut + col;
+                const float x = f[h] * o[n][2 * h + e];
+                *dst = w == 0 ? x : *dst + x;
+              }
+        }
+        __syncthreads();
+      }
+      for (int i = tid; i < rows * (D / 8); i += kThreads) {
+        const int r = i / (D / 8), col = i % (D / 8) * 8;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+        const float mb = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum = fmaf(ex2_approx((s_m[w][r] - mb) * scale_log2), s_l[w][r], sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no keys: 0, and an LSE of -inf
+        const float lse = top * a.scale + logf(sum);
+        const float* x = s_o + r * C::kOut + col;
+        if (p.slot >= 0) {
+          float* part = partial_of<D>(a, blockIdx.x, p.slot);
+          float4* dst = reinterpret_cast<float4*>(part + r * D + col);
+          dst[0] = make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+          dst[1] = make_float4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+          if (col == 0) part[a.max_rows * D + r] = lse;
+        } else {
+          const int row = p.s.q0 + r / group, head = p.head * group + r % group;
+          *reinterpret_cast<uint4*>(a.o + (static_cast<size_t>(row) * a.seg.num_q_heads + head) * D + col) =
+              make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
+                         pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv));
+          if (col == 0 && a.lse != nullptr) a.lse[static_cast<size_t>(head) * a.seg.capacity_q + row] = lse;
+        }
+      }
+      __syncthreads();  // s_o, s_m and s_l are read
+    }
+    cp_async_wait<0>();
+    const bool more = s_more != 0;
+    __syncthreads();  // the pieces and s_more are read
+    if (!more) return;
+    // the tile's segments are used up, or the list of pieces was full
+    uint64_t next;
+    if (tid == 0) scan.warp[0] = at;
+    __syncthreads();
+    next = scan.warp[0];
+    const uint64_t tile_end = scan.before[kThreads];
+    __syncthreads();
+    if (next >= tile_end) {
+      tile += kThreads;
+      scan_tile(tile, tile_end, nullptr);
+    }
+  }
+}
+
+// Joins the pieces of a cut pair, in order, four loaded at once.  CTA c joins the pair whose first piece CTA c of
+// the kernel before took; nothing is read before the wait.
+template <int D>
+__global__ void __launch_bounds__(kThreads)
+paged_token_join_kernel(const __grid_constant__ PagedTokenArgs a) {
+  grid_dependency_wait();
+  launch_dependents();
+  const int4 join = a.joins[blockIdx.x];
+  const int n = join.w;
+  if (n <= 1) return;
+  const int g = join.x, kv_head = join.y;
+  const PagedSegment s = checked_paged_segment(a.seg, g, nullptr);
+  const int group = a.seg.num_q_heads / a.seg.num_kv_heads;
+  auto piece = [&](int c) { return partial_of<D>(a, blockIdx.x + c, c == 0 ? join.z : 0); };
+  for (int i = threadIdx.x; i < s.rows * group * (D / 8); i += kThreads) {
+    const int r = i / (D / 8), col = i % (D / 8) * 8;
+    float top = -INFINITY, sum = 0.f, x[8] = {};
+    constexpr int kBatch = 4;  // pieces loaded at once
+    for (int c0 = 0; c0 < n; c0 += kBatch) {
+      float w[kBatch];
+      float4 u[kBatch], v[kBatch];
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        const float* p = piece(min(c0 + c, n - 1));
+        w[c] = c0 + c < n ? p[a.max_rows * D + r] : -INFINITY;
+        u[c] = reinterpret_cast<const float4*>(p + r * D + col)[0];
+        v[c] = reinterpret_cast<const float4*>(p + r * D + col)[1];
+      }
+      float mx = top;
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) mx = fmaxf(mx, w[c]);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      const float old = __expf(top - base);
+      top = mx;
+      sum *= old;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= old;
+#pragma unroll
+      for (int c = 0; c < kBatch; ++c) {
+        const float f = __expf(w[c] - base);
+        const float y[8] = {u[c].x, u[c].y, u[c].z, u[c].w, v[c].x, v[c].y, v[c].z, v[c].w};
+        sum += f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = c0 + c < n ? fmaf(f, y[e], x[e]) : x[e];
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int row = s.q0 + r / group, head = kv_head * group + r % group;
+    *reinterpret_cast<uint4*>(a.o + (static_cast<size_t>(row) * a.seg.num_q_heads + head) * D + col) =
+        make_uint4(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv),
+                   pack_bf16x2(x[4] * inv, x[5] * inv), pack_bf16x2(x[6] * inv, x[7] * inv));
+    if (col == 0 && a.lse != nullptr) a.lse[static_cast<size_t>(head) * a.seg.capacity_q + row] = top + logf(sum);
+  }
+}
+
+template <int D, bool kE4m3>
+cudaError_t launch(const PagedTokenArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, kE4m3>;
+  cudaError_t e = allow_shared_memory<C::kSmemBytes>(paged_token_kernel<D, kE4m3>);
+  if (e != cudaSuccess) return e;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const int ctas = sms * kCtasPerSm < kPagedTokenCtas ? sms * kCtasPerSm : kPagedTokenCtas;
+  e = launch_programmatic(paged_token_kernel<D, kE4m3>, dim3(ctas), dim3(kThreads), C::kSmemBytes, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_programmatic(paged_token_join_kernel<D>, dim3(ctas), dim3(kThreads), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_token(const PagedTokenArgs& a, int head_dim, cudaStream_t stream) {
+  if (a.k_scale != nullptr) return head_dim == 128 ? launch<128, true>(a, stream) : launch<64, true>(a, stream);
+  return head_dim == 128 ? launch<128, false>(a, stream) : launch<64, false>(a, stream);
+}
+
+}  // namespace h3
