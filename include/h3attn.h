@@ -472,7 +472,7 @@ typedef struct {
   int32_t num_segments;
   int32_t max_seqlen_q; /* host upper bound on the query rows of a segment, <= capacity_q */
   int32_t max_seqlen_k; /* host upper bound on the cached tokens of a segment */
-  int32_t capacity_q;   /* rows of q and o; row stride of lse */
+  int32_t capacity_q;   /* rows of q and o, at most 2^29; row stride of lse */
   int32_t num_q_heads;
   int32_t num_kv_heads; /* divides num_q_heads, at most 128 query heads to a key head */
   int32_t head_dim;     /* 64 or 128 */
@@ -492,7 +492,7 @@ H3_API size_t h3_paged_attn_workspace_size(const h3_paged_attn_desc* desc);
  * k_cache, v_cache, k_scale, v_scale, block_table: as for h3_kv_cache_write (entries past a segment's
  *               cached tokens are not read).
  * cu_seqlens_q: device int32 [num_segments + 1]; must start at 0, not decrease, end <= capacity_q.
- * seqused_k   : device int32 [num_segments]; at most max_pages * page_size each.
+ * seqused_k   : device int32 [num_segments]; at most max_pages * page_size and 2^30 each.
  * o           : device bf16 [capacity_q, num_q_heads, head_dim], contiguous; rows of every segment
  *               written, others untouched.  Must not overlap an input.
  * lse         : device fp32 [num_q_heads, capacity_q] (natural log) or NULL.

@@ -332,6 +332,7 @@ inline size_t cross_token_bytes(const CrossSegments& s, int head_dim) {
 cudaError_t launch_cross_token(const CrossTokenArgs& a, int head_dim, cudaStream_t stream);
 
 // ---- attention over a paged cache ---------------------------------------------------------------
+constexpr int kPagedMaxTokens = 1 << 30;  // of a segment: key counts then fit 32 bits with room for a tile
 struct PagedSegments {
   const int32_t* cu_q;
   const int32_t* used;  // tokens of each segment, the new ones included
@@ -366,6 +367,23 @@ constexpr size_t paged_token_bytes(int rows, int head_dim) {
   return paged_token_joins_bytes() + 2 * kPagedTokenCtas * paged_token_partial(rows, head_dim) * sizeof(float);
 }
 cudaError_t launch_paged_token(const PagedTokenArgs& a, int head_dim, cudaStream_t stream);
+
+struct PagedTileArgs {
+  CUtensorMap tmap_q;          // {D, H, rows}, a box of a key head's query heads x 128 / their number
+  CUtensorMap tmap_k, tmap_v;  // {D, page, pages x heads}, a box of a page (128 rows of it at most)
+  PagedSegments seg;
+  const uint8_t *k_scale, *v_scale;
+  void* o;
+  int wide;  // o may be stored in 32-byte pieces
+  float* lse;
+  float scale;
+  void* workspace;   // attn_plan_bytes(num_segments): the work plan
+  void* split_area;  // attn_split_bytes(head_dim) after it, or null (no item is cut)
+  unsigned int* err;
+  uint64_t wait_limit_ns;
+  uint32_t stall_after_tiles;
+};
+cudaError_t launch_paged_attn(const PagedTileArgs& a, int head_dim, cudaStream_t stream);
 
 // ---- VSA block gate + top-k ----------------------------------------------------------------
 struct VsaGeom {

@@ -68,37 +68,42 @@ EncodeTiledFn encode_tiled_fn() {
   return fn;
 }
 
-// A bf16 map of `rank` dimensions with 128-byte swizzle; elements outside read as zero.  The driver wants a
-// context that is current in the calling thread, and a thread that has made no such runtime call yet (a
-// worker, an engine's backward thread) has none: it then gets its device's and the map is made again.
-bool encode_bf16_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                     const cuuint32_t* box) {
+// A map of `rank` dimensions; elements outside read as zero.  The driver wants a context that is current in the
+// calling thread, and a thread that has made no such runtime call yet (a worker, an engine's backward thread) has
+// none: it then gets its device's and the map is made again.
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int rank,
+                const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn enc = encode_tiled_fn();
   if (enc == nullptr) return false;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   auto encode = [&] {
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims,
-               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
   if (encode()) return true;
   int dev = 0;
   return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
+// bf16, 128-byte swizzle
+bool encode_bf16_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box) {
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, base, rank, dims, strides, box);
+}
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// 3-D view {D, H, rows} of a bf16 [rows, H, D] tensor; box {64, 1, 128}, 128-byte swizzle.
+// 3-D view {D, H, rows} of a bf16 [rows, H, D] tensor; box {64, box_heads, box_rows}, 128-byte swizzle.
 // row_stride: elements between rows (0: heads * head_dim).
 bool make_qkv_map(CUtensorMap* m, const void* base, int rows, int heads, int head_dim,
-                  int64_t row_stride = 0) {
+                  int64_t row_stride = 0, int box_heads = 1, int box_rows = 128) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
                                  (row_stride > 0 ? static_cast<cuuint64_t>(row_stride)
                                                  : static_cast<cuuint64_t>(heads) * head_dim) * 2};
-  const cuuint32_t box[3] = {64, 1, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
   return encode_bf16_map(m, base, 3, dims, strides, box);
 }
 
@@ -116,6 +121,20 @@ bool make_window_map(CUtensorMap* m, const void* base, const int32_t grid[3], co
   const cuuint32_t box[5] = {64, 1, static_cast<cuuint32_t>(win[2]), static_cast<cuuint32_t>(win[1]),
                              static_cast<cuuint32_t>(frames)};
   return encode_bf16_map(m, base, 5, dims, strides, box);
+}
+
+// 3-D view {D, page, pages * heads} of a paged cache; a box is a page's rows of a head, 128 at most: of 64 bf16 values
+// (128-byte swizzle), or of all D e4m3 values (a swizzle as wide as they are).
+bool make_cache_map(CUtensorMap* m, const void* base, bool e4m3, int64_t planes, int page_size, int head_dim) {
+  const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * (e4m3 ? 1 : 2);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(page_size),
+                              static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[2] = {row, row * page_size};
+  const cuuint32_t rows = static_cast<cuuint32_t>(page_size < 128 ? page_size : 128);
+  const cuuint32_t box[3] = {e4m3 ? static_cast<cuuint32_t>(head_dim) : 64u, rows, 1};
+  if (!e4m3) return encode_bf16_map(m, base, 3, dims, strides, box);
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    base, 3, dims, strides, box);
 }
 
 bool device_is_sm103() {
@@ -644,7 +663,11 @@ bool paged_sizes_ok(const h3_paged_attn_desc* d) {
          d->capacity_q >= 0 && d->max_seqlen_q <= d->capacity_q && d->num_q_heads > 0 && d->num_q_heads <= 65535 &&
          d->num_kv_heads > 0 && d->num_q_heads % d->num_kv_heads == 0 && d->num_q_heads / d->num_kv_heads <= 128 &&
          (d->cache_type == H3_TYPE_BF16 || d->cache_type == H3_TYPE_E4M3) && page_shift_of(d->page_size) >= 0 &&
-         d->num_pages >= 0 && d->max_pages >= 0 && d->causal_block >= 0;
+         d->num_pages >= 0 && d->max_pages >= 0 && d->causal_block >= 0 && d->capacity_q <= 1 << 29 &&
+         // work items are counted in 32 bits, and a page's rows of a head are one coordinate of a tensor map
+         (static_cast<int64_t>(d->capacity_q) / (128 / (d->num_q_heads / d->num_kv_heads)) + d->num_segments) *
+                 d->num_kv_heads <= INT32_MAX &&
+         static_cast<int64_t>(d->num_pages) * d->num_kv_heads <= INT32_MAX;
 }
 
 // Few rows per segment take the key-streaming kernel: its 16-row tile holds all of a key head's rows.
@@ -659,7 +682,7 @@ size_t h3_paged_attn_workspace_size(const h3_paged_attn_desc* d) {
   if (d->head_dim != 64 && d->head_dim != 128) return 0;
   if (paged_few_rows(d))
     return h3::paged_token_bytes(d->max_seqlen_q * (d->num_q_heads / d->num_kv_heads), d->head_dim);
-  return 0;
+  return h3::attn_workspace_bytes(d->num_segments, d->max_seqlen_k, d->head_dim);
 }
 
 h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* d, const void* q, const void* k_cache, const void* v_cache,
@@ -674,8 +697,6 @@ h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* d, const void* q, const vo
   int64_t q_stride;
   const h3_status st = token_stride(d->q_stride, d->num_q_heads, d->head_dim, &q_stride);
   if (st != H3_OK) return st;
-  // a page's rows of a head are one coordinate of a tensor map
-  if (static_cast<int64_t>(d->num_pages) * d->num_kv_heads > INT32_MAX) return H3_ERR_INVALID_ARG;
   if (!all_aligned16({q, k_cache, v_cache, k_scale, v_scale, o, workspace}) ||
       ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(cu_seqlens_q) |
         reinterpret_cast<uintptr_t>(seqused_k) | reinterpret_cast<uintptr_t>(lse)) & 3u))
@@ -713,7 +734,29 @@ h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* d, const void* q, const vo
     t.err = err;
     return from_cuda(h3::launch_paged_token(t, d->head_dim, reinterpret_cast<cudaStream_t>(stream)));
   }
-  return H3_ERR_UNSUPPORTED;
+
+  h3::PagedTileArgs a{};
+  // no page at all: any valid map will do, every row is masked
+  const bool none = d->num_pages == 0;
+  const int64_t planes = static_cast<int64_t>(d->num_pages) * d->num_kv_heads;
+  if (!make_qkv_map(&a.tmap_q, q, d->capacity_q, d->num_q_heads, d->head_dim, q_stride, group, 128 / group) ||
+      !make_cache_map(&a.tmap_k, none ? q : k_cache, e4m3, none ? 1 : planes, none ? 1 : d->page_size, d->head_dim) ||
+      !make_cache_map(&a.tmap_v, none ? q : v_cache, e4m3, none ? 1 : planes, none ? 1 : d->page_size, d->head_dim))
+    return H3_ERR_CUDA;
+  a.seg = seg;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.o = o;
+  a.wide = aligned32(o);
+  a.lse = lse;
+  a.scale = scale;
+  a.workspace = workspace;
+  if (d->max_seqlen_k >= h3::kSplitMinSeqlen)
+    a.split_area = static_cast<uint8_t*>(workspace) + h3::attn_plan_bytes(d->num_segments);
+  a.err = err;
+  a.wait_limit_ns = h3::wait_limit_ns();
+  a.stall_after_tiles = h3::stall_after_tiles();
+  return from_cuda(h3::launch_paged_attn(a, d->head_dim, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t h3_varlen_attn_workspace_size(int32_t num_segments, int32_t num_heads, int32_t max_seqlen,

@@ -1,0 +1,426 @@
+// Attention of chunks of new tokens over a paged cache, on the tile kernel of attn_tile.cuh (TMA + tcgen05 + TMEM).
+//
+//   S = scale q k^T over the keys that a row sees,  P = softmax(S),  o = P v,  lse = log sum exp(S)
+//
+// A 128-row query tile holds 128 / group tokens with all the query heads that share a key head, so a chunk of a few
+// tokens fills a tile and every key is read once for the whole group.  An item is two consecutive tiles of a
+// (segment, key head); both stream the same 128-key tiles, which a key/value producer gathers from pages: each of its
+// lanes looks up one page of the tile, a tile ahead, and issues that page's copy.  An e4m3 tile arrives as bytes
+// with its rows' scales, and the epilogue's warps, idle between items, turn it into bf16 in shared memory (exactly);
+// the products and the softmax then are those of a bf16 cache.
+//
+// Causal by blocks of tokens: an item's key tiles end at its last row's limit, a tile in which some row sees less is
+// masked row by row, others are not.  Items of a segment come with the longest first and waves alternate in
+// direction, so the CTAs' sums stay near one another; what a last, partly filled wave and unlike items leave idle
+// is evened out by cutting that wave's items where each CTA's share of the whole ends.
+#include <cuda_bf16.h>
+
+#include "attn_tile.cuh"
+#include "h3_internal.h"
+#include "launch.h"
+#include "paged_segments.cuh"
+#include "sm103_ptx.cuh"
+
+namespace h3 {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kSortMax = 256;  // segments that are ordered by keys, and whose last wave is cut
+// In steps of a key tile, as measured for cross attention: an item's start and end, joining chunks; items cut at
+// all, least chunk.
+constexpr uint32_t kCostItem = 2, kCostJoin = 8;
+constexpr int kSplitMinTiles = 8, kSplitMinChunk = 3;
+constexpr int kMaxChunks = 160;  // of an item: one for each CTA
+
+__device__ __forceinline__ int tiles_of(int rows, int tokens) { return (rows + tokens - 1) / tokens; }
+__device__ __forceinline__ int pairs_of(int rows, int tokens) { return (tiles_of(rows, tokens) + 1) / 2; }
+// Keys of a segment's pair of tiles: what its last row sees.
+__device__ __forceinline__ int pair_limit(const PagedSegment& s, int pair, int tokens, int block) {
+  const int64_t end = static_cast<int64_t>(2 * pair + 2) * tokens;
+  return row_limit(s, (end < s.rows ? static_cast<int>(end) : s.rows) - 1, block);
+}
+
+// Whole item k of CTA c of `ctas`: the waves alternate in direction.
+__device__ __forceinline__ uint32_t item_of(uint32_t k, uint32_t c, uint32_t ctas) {
+  return k * ctas + (k & 1 ? ctas - 1 - c : c);
+}
+
+// Plan: segment order and item prefix, and the entries of the last wave.  Words of ws: [0] cut items, [1] unused,
+// [2] whole items before the last wave, [3] its entries, then the order [S] and the exclusive prefix [S + 1].
+__global__ void __launch_bounds__(kPlanThreads)
+paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_t* __restrict__ ws,
+                  uint8_t* __restrict__ split_area, int wave, unsigned int* err) {
+  __shared__ PagedSegment s_seg[kSortMax];
+  __shared__ int s_order[kSortMax];
+  __shared__ uint32_t s_prefix[kSortMax + 1];
+  __shared__ uint32_t s_warp[kPlanThreads / 32];
+  __shared__ uint64_t s_warp64[kPlanThreads / 32];
+  __shared__ uint32_t s_cut, s_most, s_uncut, s_top;
+  __shared__ uint2 s_item[kSplitMaxEntries / 2];  // of the last wave: where it starts, its key tiles
+  __shared__ uint32_t s_load[kSplitMaxEntries / 2];  // of each CTA before the last wave
+  __shared__ uint4 s_at[kSplitMaxEntries / 2];    // of each CTA: where its share starts, cuts before it, a cut itself
+  grid_dependency_wait();
+  launch_dependents();
+  const int S = seg.num_segments, tid = threadIdx.x, heads = seg.num_kv_heads;
+  uint32_t* order = ws + kHeader;
+  uint32_t* prefix = ws + kHeader + S;
+  const bool sorted = S <= kSortMax;
+  if (sorted) {
+    if (tid < S) s_seg[tid] = checked_paged_segment(seg, tid, err);
+    __syncthreads();
+    if (tid < S) {  // most keys first, ties by position
+      int rank = 0;
+      for (int h = 0; h < S; ++h)
+        rank += s_seg[h].used > s_seg[tid].used || (s_seg[h].used == s_seg[tid].used && h < tid);
+      s_order[rank] = tid;
+    }
+    __syncthreads();
+  }
+  auto items_at = [&](int i) -> uint32_t {  // of the segment in place i
+    const int rows = sorted ? s_seg[s_order[i]].rows : checked_paged_segment(seg, i, err).rows;
+    return static_cast<uint32_t>(pairs_of(rows, tokens)) * heads;
+  };
+  const int chunk = (S + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
+  const int lo = min(S, tid * chunk), hi = min(S, lo + chunk);
+  uint64_t local = 0, items;
+  for (int i = lo; i < hi; ++i) local += items_at(i);
+  uint32_t run = static_cast<uint32_t>(block_exclusive_scan(local, s_warp64, items));
+  // Segments that overlap can hold more tiles than the capacity (and more than 32 bits count): then no item.
+  if (items > (static_cast<uint64_t>(seg.capacity_q) / tokens + S) * heads) {
+    if (tid == 0) {
+      record_error(err, kErrBadCuSeqlens);
+      ws[0] = ws[2] = ws[3] = 0;
+    }
+    return;
+  }
+  const uint32_t total = static_cast<uint32_t>(items);
+  for (int i = lo; i < hi; ++i) {
+    order[i] = static_cast<uint32_t>(sorted ? s_order[i] : i);
+    prefix[i] = run;
+    if (sorted) s_prefix[i] = run;
+    run += items_at(i);
+  }
+  if (tid == 0) {
+    prefix[S] = total;
+    if (sorted) s_prefix[S] = total;
+  }
+  const uint32_t waves = total / wave, tail = waves * wave, R = total - tail;
+  if (split_area == nullptr || !sorted || R == 0 || 2 * wave + 1 > kSplitMaxEntries) {
+    if (tid == 0) {
+      ws[0] = 0;
+      ws[2] = total;
+      ws[3] = 0;
+    }
+    return;
+  }
+  if (tid == 0) s_cut = s_most = s_uncut = s_top = 0u;
+  __syncthreads();  // also: the prefix is complete
+  auto entry_of = [&](uint32_t item) {
+    int l = 0, h = S - 1;
+    while (l < h) {
+      const int mid = (l + h + 1) >> 1;
+      if (s_prefix[mid] <= item) l = mid; else h = mid - 1;
+    }
+    TileEntry e{};
+    e.segment = s_order[l];
+    const PagedSegment s = s_seg[e.segment];
+    const int loc = static_cast<int>(item - s_prefix[l]);
+    e.kv_head = loc % heads;
+    e.pair = pairs_of(s.rows, tokens) - 1 - loc / heads;
+    e.kv1 = key_tiles(pair_limit(s, e.pair, tokens, seg.causal_block));
+    return e;
+  };
+  uint32_t load = 0;
+  if (tid < wave) {
+    for (uint32_t w = 0; w < waves; ++w) load += entry_of(item_of(w, tid, wave)).kv1 + kCostItem;
+    s_load[tid] = load;
+    atomicMax(&s_top, load);
+  }
+  // Behind an odd number of waves the CTAs' loads fall with their number reversed, so the items come reversed too.
+  const bool reversed = waves & 1;
+  const bool mine = tid < static_cast<int>(R);  // fewer than a wave
+  TileEntry e{};
+  int nkv = 0;
+  uint32_t cost = 0;
+  if (mine) {
+    e = entry_of(tail + (reversed ? R - 1 - tid : tid));
+    nkv = e.kv1;
+    cost = static_cast<uint32_t>(nkv) + kCostItem;  // a wave's sum fits 32 bits
+    atomicMax(&s_most, cost);
+  }
+  uint32_t rest, before_all;
+  const uint32_t start = block_exclusive_scan(cost, s_warp, rest);  // (its barriers also order s_most and s_load)
+  block_exclusive_scan(tid < wave ? load : 0u, s_warp, before_all);
+  if (mine) {
+    s_item[tid] = make_uint2(start, static_cast<uint32_t>(nkv));
+    atomicMax(&s_uncut, cost + s_load[reversed ? wave - static_cast<int>(R) + tid : tid]);
+  }
+  __syncthreads();
+  // a CTA's share fills it up to the mean; no cut where whole items end as soon as the shares and their joining would
+  const uint32_t target = (rest + before_all + wave - 1) / wave;
+  const bool cut = s_uncut > max(target, s_top) + kCostJoin;
+  uint32_t share = 0;
+  if (tid < wave && load < target)
+    share = max(max(target - load, 2u * kSplitMinChunk), s_most / (kMaxChunks - 4) + 1);
+  uint32_t shares;
+  const uint32_t from = block_exclusive_scan(share, s_warp, shares);
+  // CTA k starts in item at.x, at its key tile at.y (0: at its start)
+  uint2 at = make_uint2(R, 0u);
+  if (tid < wave && cut) {
+    if (from < rest) {
+      int l = 0, h = static_cast<int>(R) - 1;
+      while (l < h) {
+        const int mid = (l + h + 1) >> 1;
+        if (s_item[mid].x <= from) l = mid; else h = mid - 1;
+      }
+      const uint32_t n = s_item[l].y, j = min(n, from - s_item[l].x);
+      const bool inside = n >= static_cast<uint32_t>(kSplitMinTiles) && j >= static_cast<uint32_t>(kSplitMinChunk) &&
+                          j + kSplitMinChunk <= n;
+      at = inside ? make_uint2(l, j) : make_uint2(2 * j < n ? l : l + 1, 0u);
+    }
+    if (tid == 0) at = make_uint2(0u, 0u);
+  } else if (!cut) {
+    const int first = reversed ? max(0, tid - (wave - static_cast<int>(R))) : tid;
+    at.x = min(static_cast<uint32_t>(first), R);
+  }
+  // CTAs without a share start where the next one does: one of them stands for the cut there
+  const bool counts = tid < wave && at.y > 0 && share > 0;
+  uint32_t cuts;
+  const uint32_t before = block_exclusive_scan(counts ? 1u : 0u, s_warp, cuts);
+  uint32_t* listed = reinterpret_cast<uint32_t*>(split_area + split_items_offset());
+  if (tid < wave) {
+    s_at[tid] = make_uint4(at.x, at.y, before, counts ? 1u : 0u);
+    listed[wave + tid] = at.x + before + (at.y > 0 ? 1u : 0u);  // (the cut where it starts, whoever stands for it)
+  }
+  if (tid == 0) listed[2 * wave] = R + cuts;
+  __syncthreads();
+  if (mine) {
+    // the cuts inside this item, in order: CTAs whose share starts inside it
+    int k = 0, end = wave;  // the first CTA that starts in this item or behind
+    while (k < end) {
+      const int mid = (k + end) >> 1;
+      if (s_at[mid].x < static_cast<uint32_t>(tid)) k = mid + 1; else end = mid;
+    }
+    const uint32_t earlier = !cut ? 0u : k < wave ? s_at[k].z : cuts;
+    int last = cut ? k : wave;
+    int c = 1;
+    for (; last < wave && s_at[last].x == static_cast<uint32_t>(tid); ++last) c += s_at[last].w;
+    const uint32_t first = tid + earlier;
+    if (c > 1) listed[atomicAdd(&s_cut, 1u)] = first;  // listed for the merge; the list's order is immaterial
+    e.first = static_cast<int>(first);
+    e.chunks = c;
+    e.kv0 = 0;
+    for (e.chunk = 0; e.chunk < c; ++e.chunk, ++k) {
+      while (k < last && s_at[k].w == 0) ++k;
+      e.kv1 = c > 1 && k < last ? static_cast<int>(s_at[k].y) : nkv;
+      reinterpret_cast<TileEntry*>(split_area)[first + e.chunk] = e;
+      e.kv0 = e.kv1;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    ws[0] = s_cut;
+    ws[2] = tail;
+    ws[3] = R + cuts;
+  }
+}
+
+template <int kD, bool kE4m3>
+struct PagedSource {
+  static constexpr int kDim = kD, kChunks = kMaxChunks;
+  static constexpr bool kConvert = kE4m3, kRowLimits = true;
+  CUtensorMap tmap_q, tmap_k, tmap_v;
+  PagedSegments seg;
+  const uint8_t *k_scale, *v_scale;
+  int group, tokens;  // query heads of a key head, tokens of a tile
+
+  struct Work {
+    int ntiles;          // 0: no more work
+    int q0[2];           // first row of each tile
+    int seg_end, head;   // the segment's last row + 1, the key head's first query head
+    int segment, kv_head;
+    int kv0;             // the item's first key tile
+    int nkv, last_keys;  // key tiles, and keys in the last of them (0: rows that see no key)
+    int used;            // tokens of the segment
+    int partial;         // entry whose partial results the item writes, -1 for o itself
+    __device__ __forceinline__ int q_head(int) const { return head; }
+  };
+
+  __device__ __forceinline__ uint32_t q_bytes() const { return tokens * group * kD * 2; }
+  __device__ static __forceinline__ uint32_t whole_item(uint32_t k) { return item_of(k, blockIdx.x, gridDim.x); }
+  __device__ __forceinline__ TileRow row(int r) const {
+    return TileRow{r < tokens * group ? r / group : 1 << 29, r % group};
+  }
+  __device__ __forceinline__ int row_keys(const Work& d, int t, TileRow r) const {
+    const int rows = d.seg_end - (d.q0[t] + r.token);  // from this one to the segment's last
+    return row_limit(PagedSegment{0, rows, d.used}, 0, seg.causal_block) - d.kv0 * kBlockN;
+  }
+
+  __device__ __forceinline__ Work decode(uint32_t item, const uint32_t* __restrict__ ws,
+                                         const uint8_t* __restrict__ split_area) const {
+    const int S = seg.num_segments;
+    const uint32_t tail = ws[2];
+    Work d;
+    int pair, kv1 = -1;
+    d.kv0 = 0;
+    d.partial = -1;
+    if (ws[3] > 0 && item >= tail) {
+      const TileEntry e = reinterpret_cast<const TileEntry*>(split_area)[item - tail];
+      d.segment = e.segment;
+      pair = e.pair;
+      d.kv_head = e.kv_head;
+      d.kv0 = e.kv0;
+      kv1 = e.kv1;
+      if (e.chunks > 1) d.partial = e.first + e.chunk;
+    } else {
+      const uint32_t* prefix = ws + kHeader + S;
+      int lo = 0, hi = S - 1;  // last i with prefix[i] <= item
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= item) lo = mid; else hi = mid - 1;
+      }
+      d.segment = static_cast<int>((ws + kHeader)[lo]);
+      const int pairs = pairs_of(seg.cu_q[d.segment + 1] - seg.cu_q[d.segment], tokens);
+      const int loc = static_cast<int>(item - prefix[lo]);
+      d.kv_head = loc % seg.num_kv_heads;
+      pair = pairs - 1 - loc / seg.num_kv_heads;
+    }
+    const int a = seg.cu_q[d.segment];
+    d.seg_end = seg.cu_q[d.segment + 1];
+    d.used = seg.used[d.segment];
+    d.head = d.kv_head * group;
+    d.ntiles = min(2, tiles_of(d.seg_end - a, tokens) - 2 * pair);
+    d.q0[0] = a + 2 * pair * tokens;
+    d.q0[1] = d.q0[0] + tokens;
+    const int keys = pair_limit(PagedSegment{a, d.seg_end - a, d.used}, pair, tokens, seg.causal_block);
+    const int all = key_tiles(keys);
+    if (kv1 < 0) kv1 = all;
+    d.nkv = kv1 - d.kv0;
+    d.last_keys = kv1 == all ? keys - (all - 1) * kBlockN : kBlockN;
+    return d;
+  }
+
+  __device__ __forceinline__ TilePlace place(const TileEntry& en, int t) const {
+    const int a = seg.cu_q[en.segment], end = seg.cu_q[en.segment + 1], tile = 2 * en.pair + t;
+    return TilePlace{tile < tiles_of(end - a, tokens), a + tile * tokens, en.kv_head * group, end};
+  }
+
+  // The key/value producer: lane i has page i of a key tile, looked up a tile ahead.
+  struct Fetch {
+    int shift, rows;  // log2 of a page, its rows in a tile
+    int id, next;     // this lane's page of the current tile and the next one
+    __device__ __forceinline__ int pages(const Work& d, int j) const {
+      const int keys = j == d.nkv - 1 ? d.last_keys : kBlockN;
+      return (keys + rows - 1) / rows;
+    }
+    __device__ __forceinline__ int look(const PagedSource& s, const Work& d, int j) const {
+      const int lane = threadIdx.x & 31;
+      if (j >= d.nkv || lane >= pages(d, j)) return 0;
+      return page_id(s.seg.table, d.segment, ((d.kv0 + j) * kBlockN >> shift) + lane);
+    }
+    __device__ __forceinline__ Fetch(const PagedSource& s, const Work& d)
+        : shift(s.seg.table.page_shift), rows(min(1 << shift, kBlockN)), id(0), next(look(s, d, 0)) {}
+    // Key (value) tile j of an item into a stage: v = 0, then v = 1.
+    __device__ __forceinline__ void tile(const PagedSource& s, const Work& d, int j, int v, uint8_t* dst, uint8_t* scales,
+                                         uint32_t bar, uint64_t policy, unsigned int* err) {
+      const int lane = threadIdx.x & 31, n = pages(d, j);
+      if (v == 0) {
+        id = next;
+        next = look(s, d, j + 1);
+        if (lane < n && !page_ok(s.seg.table, id)) {
+          record_error(err, kErrBadPage);
+          id = 0;
+        }
+      }
+      const uint32_t row_bytes = kE4m3 ? kD + 1 : 2 * kD;
+      if (lane == 0) mbar_arrive_expect_tx(bar, n * rows * row_bytes);
+      __syncwarp();
+      if (lane < n) {
+        const CUtensorMap* map = v == 0 ? &s.tmap_k : &s.tmap_v;
+        const int first = (d.kv0 + j) * kBlockN & ((1 << shift) - 1);  // of the page's rows (pages over 128 tokens)
+        const int plane = id * s.seg.num_kv_heads + d.kv_head;
+        if constexpr (kE4m3) {
+          tma_load_3d_hint(smem_u32(dst + lane * rows * kD), map, 0, first, plane, bar, policy);
+          const uint8_t* scale = (v == 0 ? s.k_scale : s.v_scale) + (static_cast<size_t>(plane) << shift) + first;
+          bulk_load(smem_u32(scales + lane * rows), scale, rows, bar);
+        } else {
+          for (int x = 0; x < kD / 64; ++x)
+            tma_load_3d_hint(smem_u32(dst + x * kBlockN * 128 + lane * rows * 128), map, x * 64, first, plane, bar,
+                             policy);
+        }
+      }
+      __syncwarp();
+    }
+  };
+
+  // Row `row` of a tile of bytes (swizzled as it came) into a bf16 tile (128-byte swizzle, 64 columns apart).
+  __device__ static __forceinline__ void convert_row(const uint8_t* raw, uint32_t biased, uint8_t* tile, int row, bool key,
+                                                     bool zero) {
+    auto at = [&](int piece) {  // 16 bytes of the bf16 row
+      return reinterpret_cast<uint4*>(tile + (piece >> 3) * kBlockN * 128 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+    };
+    if (key) {
+      // value = bits * 2^120 * 2^e, in one product where 2^(120 + e) is a bf16
+      const bool two = biased > 127 + 7;
+      const uint32_t first = (two ? 247u : biased + 120u) << 7, second = biased == kScaleNan ? 0x7fffu : biased << 7;
+      const uint32_t f2 = first | first << 16, s2 = second | second << 16;
+#pragma unroll
+      for (int p = 0; p < kD / 16; ++p) {
+        const int swizzled = kD == 128 ? p ^ (row & 7) : p ^ ((row >> 1) & 3);
+        const uint4 w4 = *reinterpret_cast<const uint4*>(raw + row * kD + (swizzled << 4));
+        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+        uint32_t b[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          b[2 * i] = bf16x2_mul(e4m3_pair_bits(w[i], w[i], 0x1100), f2);
+          b[2 * i + 1] = bf16x2_mul(e4m3_pair_bits(w[i], w[i], 0x3322), f2);
+        }
+        if (two) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) b[i] = bf16x2_mul(b[i], s2);
+        }
+        *at(2 * p) = make_uint4(b[0], b[1], b[2], b[3]);
+        *at(2 * p + 1) = make_uint4(b[4], b[5], b[6], b[7]);
+      }
+    } else if (zero) {
+#pragma unroll
+      for (int p = 0; p < kD / 8; ++p) *at(p) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+};
+
+template <int D, bool kE4m3>
+cudaError_t launch(const PagedTileArgs& a, cudaStream_t stream) {
+  using Source = PagedSource<D, kE4m3>;
+  using C = TileCfg<Source>;
+  cudaError_t e = allow_shared_memory<C::kSmemBytes>(attn_tile_kernel<Source>);
+  if (e != cudaSuccess) return e;
+  const int sms = num_sms_of_current_device();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  uint32_t* ws = static_cast<uint32_t*>(a.workspace);
+  uint8_t* split = static_cast<uint8_t*>(a.split_area);
+  const int group = a.seg.num_q_heads / a.seg.num_kv_heads, tokens = kBlockM / group;
+  e = launch_programmatic(paged_plan_kernel, dim3(1), dim3(a.seg.num_segments <= kSortMax ? kSortMax : kPlanThreads), 0,
+                          stream, a.seg, tokens, ws, split, sms, a.err);
+  if (e != cudaSuccess) return e;
+  const Source src{a.tmap_q, a.tmap_k, a.tmap_v, a.seg, a.k_scale, a.v_scale, group, tokens};
+  e = launch_programmatic(attn_tile_kernel<Source>, dim3(sms), dim3(kTileThreads), C::kSmemBytes, stream, src,
+                          static_cast<__nv_bfloat16*>(a.o), a.wide, a.lse, a.scale, a.scale * 1.4426950408889634f,
+                          static_cast<const uint32_t*>(ws), split, a.err,
+                          static_cast<unsigned long long>(a.wait_limit_ns), a.stall_after_tiles);
+  if (e != cudaSuccess) return e;
+  if (split != nullptr)
+    e = launch_programmatic(attn_tile_merge_kernel<Source>, dim3(8 * sms), dim3(kMergeThreads), 0, stream,
+                            static_cast<const uint32_t*>(ws), static_cast<const uint8_t*>(split),
+                            static_cast<__nv_bfloat16*>(a.o), a.lse, src, static_cast<const unsigned int*>(a.err));
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attn(const PagedTileArgs& a, int head_dim, cudaStream_t stream) {
+  if (a.k_scale != nullptr) return head_dim == 128 ? launch<128, true>(a, stream) : launch<64, true>(a, stream);
+  return head_dim == 128 ? launch<128, false>(a, stream) : launch<64, false>(a, stream);
+}
+
+}  // namespace h3

@@ -22,7 +22,7 @@ __device__ __forceinline__ PagedSegment checked_paged_segment(const PagedSegment
   const int a = s.cu_q[g], b = s.cu_q[g + 1], used = s.used[g];
   const bool ordered = a >= 0 && a <= b && b <= s.capacity_q && (g > 0 || a == 0);
   const int64_t room = s.table.num_pages > 0 ? static_cast<int64_t>(s.table.per_segment) << s.table.page_shift : 0;
-  if (!ordered || b - a > s.max_seqlen_q || used < 0 || used > room) {
+  if (!ordered || b - a > s.max_seqlen_q || used < 0 || used > room || used > kPagedMaxTokens) {
     record_error(err, kErrBadCuSeqlens);
     return PagedSegment{0, 0, 0};
   }
@@ -56,15 +56,21 @@ __device__ __forceinline__ uint32_t e4m3x2_pack(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two e4m3 bytes, picked twice each out of x and y by `pick` (low byte's, low byte's, high byte's, high byte's), as
-// packed bf16, exactly: sign and the seven other bits go to their places in bf16, where they stand for the value
-// times 2^(7 - 127) (a subnormal e4m3 for a subnormal bf16), and a product takes that back.
-__device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t x, uint32_t y, uint32_t pick) {
+// Two e4m3 bytes, picked twice each out of x and y by `pick` (low half's, low half's, high half's, high half's), with
+// sign and the seven other bits moved to their places in a pair of bf16: the values times 2^(7 - 127), a subnormal
+// e4m3 being a subnormal bf16.
+__device__ __forceinline__ uint32_t e4m3_pair_bits(uint32_t x, uint32_t y, uint32_t pick) {
   const uint32_t b = __byte_perm(x, y, pick);
-  const uint32_t bits = ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+  return ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t x, uint32_t y) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bits), "r"(0x7b807b80u));  // 2^120
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
+}
+// The same as values, exactly.
+__device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t x, uint32_t y, uint32_t pick) {
+  return bf16x2_mul(e4m3_pair_bits(x, y, pick), 0x7b807b80u);  // 2^120
 }
 // 2^e of a row's biased exponent; NaN for kScaleNan, which marks a row that held a NaN
 __device__ __forceinline__ float scale_of(uint32_t biased) {

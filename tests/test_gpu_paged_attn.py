@@ -6,6 +6,8 @@ both sides start from the same keys and values.  S and the sums are fp32; the we
     |o - o*| <= 2^-8 sum_j P_j |v_j| + 2^-8 |o| + fp32 terms,
 fp32 terms: the score's error (D products, 2^-24 each of |q||k|, and the exponential's 2^-22) moves each weight
 by under 1e-4 of itself at the scores used here: 2e-4 sum_j P_j |v_j|.
+A weight under 2^-126 of its row's largest is 0 (the exponential flushes it), which is an absolute error of
+2^-126 |v_j| for each key: it shows where every larger weight meets a value of exactly 0, as in e4m3.
 lse: the same error of the scores, absolute: 1e-4 * max(|lse|, 1) as elsewhere in this suite.
 """
 import numpy as np
@@ -79,7 +81,7 @@ def test_c_abi_refuses_pointers(h3):
             assert fwd(a) == (5 if i == 10 else 1), i
         a[i] = C.c_void_p(p.value + (2 if i in (5, 6, 7, 9) else 8))
         assert fwd(a) == 8, i
-    for rows in (2,):
+    for rows in (2, 9):
         d = _desc(h3, max_seqlen_q=rows, capacity_q=rows)
         need = lib.h3_paged_attn_workspace_size(C.byref(d))
         assert need > 0 and fwd([p] * 11, d, need - 1) == 5
@@ -174,7 +176,8 @@ class Case:
         got = _f64(o[:n])
         assert np.all(np.isfinite(got))
         off = np.abs(got - ref)
-        tol = (HALF + 2e-4) * size + HALF * np.abs(ref)
+        most = max([np.abs(v).sum(0).max() for v in self.rows["v"] if len(v)], default=0.0)
+        tol = (HALF + 2e-4) * size + HALF * np.abs(ref) + 2.0 ** -126 * most
         assert np.all(off <= tol), (off - tol).max()
         if lse is not None:
             gl = _f64(lse[:, :n])
@@ -229,3 +232,239 @@ def test_few_rows_large_scores_and_scale(h3, dev, e4m3):
     """Scores of some hundreds: the running maximum moves often."""
     case = Case([2, 1], [3000, 500], 8, 2, 128, 32, e4m3, 1, scale=2.0)
     case.check(*_run(h3, dev, case, softmax_scale=0.2), scale=0.2)
+
+
+# more rows than the token form takes: the tile form
+CHUNKS = [
+    ([17], [17], 1, 1, 16, 1),
+    ([20], [0], 2, 1, 16, 1),                        # no cached token at all
+    ([40, 3], [25, 130], 2, 2, 16, 1),               # more rows than tokens
+    ([9, 0, 33], [700, 40, 129], 8, 2, 32, 0),
+    ([7, 26, 1], [640, 26, 127], 40, 8, 64, 1),      # five heads share: 25 tokens a tile
+    ([130, 257], [131, 1000], 3, 3, 128, 5),
+    ([300], [555], 6, 2, 256, 100),
+    ([64, 65, 128, 129], [64, 193, 128, 257], 4, 1, 16, 1),
+    ([3, 2], [4000, 5], 128, 1, 64, 1),              # a tile per token
+    ([2, 1], [900, 40], 100, 1, 32, 1),              # 100 heads share: 28 rows of the tile stay empty
+    ([1000], [1000], 2, 1, 64, 1),                   # a first chunk, causal by token
+    ([600, 600], [2600, 1800], 4, 4, 64, 50),        # the last wave is cut
+    ([30, 500], [20000, 700], 2, 2, 128, 1),         # one item over many CTAs
+    ([20] * 300, [int(x) for x in _RNG.integers(0, 90, 300)], 2, 2, 16, 3),  # more segments than are ordered
+    ([700] * 3, [700, 1400, 2100], 24, 8, 64, 1),    # several waves of items of unlike length
+]
+
+
+@pytest_gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("shape", CHUNKS)
+def test_chunks(h3, dev, shape, e4m3, d):
+    lq, lk, hq, hk, page, block = shape
+    case = Case(lq, lk, hq, hk, d, page, e4m3, block)
+    case.check(*_run(h3, dev, case))
+
+
+@pytest_gpu
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunk_large_scores_and_scale(h3, dev, e4m3):
+    case = Case([150, 40], [1800, 300], 4, 2, 128, 32, e4m3, 7, scale=2.0)
+    case.check(*_run(h3, dev, case, softmax_scale=0.2), scale=0.2)
+
+
+@pytest_gpu
+@pytest.mark.parametrize("seed", range(8))
+def test_random_layouts(h3, dev, seed):
+    rng = np.random.default_rng(100 + seed)
+    for _ in range(6):
+        hk = int(rng.choice([1, 2, 3, 8]))
+        hq = hk * int(rng.choice([1, 2, 3, 5, 8]))
+        s = int(rng.integers(1, 7))
+        few = rng.random() < 0.4
+        lq = [int(x) for x in rng.integers(0, (16 * hk // hq) + 1 if few else 200, s)]
+        lk = [max(0, q + int(rng.integers(-5, 700))) for q in lq]
+        if max(lq) == 0:
+            continue
+        case = Case(lq, lk, hq, hk, int(rng.choice([64, 128])), int(rng.choice([16, 32, 64, 128, 256])),
+                    bool(rng.random() < 0.5), int(rng.choice([0, 1, 2, 17, 64, 1000, 2 ** 31 - 1])), seed=seed)
+        case.check(*_run(h3, dev, case))
+
+
+@pytest_gpu
+def test_loose_bounds_and_no_lse(h3, dev):
+    """max_seqlen bounds above the lengths take another form and give the same within its tolerances."""
+    case = Case([2, 1], [300, 77], 8, 2, 128, 16, True, 1)
+    a = case.on(dev)
+    for mq, mk in ((2, 300), (3, 5000), (1000, 100000)):
+        a["q"] = torch.cat([case.q, torch.zeros(1000, 8, 128, dtype=torch.bfloat16)]).to(dev)
+        out = h3.paged_attn_fwd(**{**a, "max_seqlen_q": mq, "max_seqlen_k": mk})
+        torch.cuda.synchronize()
+        assert h3.get_device_error(dev) == 0
+        case.check(out, None)
+
+
+@pytest_gpu
+@pytest.mark.parametrize("rows", [2, 40])
+def test_bad_lengths_and_pages(h3, dev, rows):
+    """A bad segment is skipped and recorded, the others are computed; a bad page id is recorded."""
+    case = Case([rows, rows, rows], [200, 150, 90], 4, 2, 64, 16, False, 1)
+    good = case.on(dev)
+    want = h3.paged_attn_fwd(**good)
+    for what, status in (("used", 3), ("negative", 3), ("rows", 3), ("many", 3), ("long", 3), ("page", 12), ("below", 12)):
+        a = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in good.items()}
+        skipped = None
+        if what == "used":
+            a["seqused_k"][1], skipped = 16 * a["block_table"].shape[1] + 1, 1
+        elif what == "negative":
+            a["seqused_k"][1], skipped = -1, 1
+        elif what == "rows":
+            a["cu_seqlens_q"][1] = 4 * rows  # falls at the second segment, and too many rows in the first
+        elif what == "many":
+            a["max_seqlen_q"] = rows - 1
+        elif what == "long":
+            a["max_seqlen_k"] = 149  # computed all the same
+        elif what == "page":
+            a["block_table"][2, 1] = a["k_cache"].shape[0]
+        else:
+            a["block_table"][2, 1] = -3
+        out = torch.full_like(a["q"], 5.0)
+        h3.paged_attn_fwd(**a, out=out)
+        torch.cuda.synchronize()
+        assert h3.get_device_error(dev) == status, what
+        if skipped is not None:
+            at = [0, rows, 2 * rows, 3 * rows]
+            for g in range(3):
+                part = slice(at[g], at[g + 1])
+                assert torch.all(out[part] == 5.0) if g == skipped else torch.equal(out[part], want[part]), (what, g)
+        if what == "long":
+            assert torch.equal(out[:case.n], want[:case.n])
+        if what in ("page", "below"):
+            assert torch.equal(out[:2 * rows], want[:2 * rows])
+        if what == "many":
+            assert torch.all(out == 5.0)
+    out = h3.paged_attn_fwd(**good)
+    torch.cuda.synchronize()
+    assert h3.get_device_error(dev) == 0 and torch.equal(out[:case.n], want[:case.n])
+
+
+@pytest_gpu
+@pytest.mark.parametrize("rows", [2, 40])
+def test_empty_calls_and_no_pages(h3, dev, rows):
+    i32 = dict(dtype=torch.int32, device=dev)
+    q = torch.ones(rows, 4, 64, dtype=torch.bfloat16, device=dev)
+    none = torch.zeros(0, 2, 16, 64, dtype=torch.bfloat16, device=dev)
+    out, lse = h3.paged_attn_fwd(q, none, none, torch.zeros(1, 0, **i32), torch.tensor([0, rows], **i32),
+                                 torch.zeros(1, **i32), rows, 0, return_lse=True)
+    torch.cuda.synchronize()
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse)) and h3.get_device_error(dev) == 0
+    out = torch.full_like(q, 5.0)
+    h3.paged_attn_fwd(q, none, none, torch.zeros(1, 0, **i32), torch.tensor([0, rows], **i32), torch.ones(1, **i32), rows,
+                      1, out=out)  # a token that no page can hold
+    torch.cuda.synchronize()
+    assert torch.all(out == 5.0) and h3.get_device_error(dev) == 3
+    h3.paged_attn_fwd(q, none, none, torch.zeros(0, 0, **i32), torch.zeros(1, **i32), torch.zeros(0, **i32), 0, 0, out=out)
+    torch.cuda.synchronize()
+    assert torch.all(out == 5.0) and h3.get_device_error(dev) == 0
+
+
+@pytest_gpu
+@pytest.mark.parametrize("lq", [[2, 1], [40, 129]])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_nan_key_reaches_the_rows_that_see_it_alone(h3, dev, lq, e4m3):
+    case = Case(lq, [300, 280], 4, 2, 64, 32, e4m3, 1)
+    a = case.on(dev)
+    clean = h3.paged_attn_fwd(**a)
+    p = lq[0] - 1  # the first segment's last token alone, at position 299 of its key head 1
+    page = int(a["block_table"][0, 299 // 32])
+    if e4m3:
+        a["k_scale"][page, 1, 299 % 32] = 255
+    else:
+        a["k_cache"][page, 1, 299 % 32] = float("nan")
+    out = h3.paged_attn_fwd(**a)
+    torch.cuda.synchronize()
+    assert torch.isnan(out[p, 2:]).all()
+    keep = torch.ones(sum(lq), 4, dtype=torch.bool)
+    keep[p, 2:] = False
+    assert torch.equal(out[:case.n][keep], clean[:case.n][keep])
+
+
+@pytest_gpu
+@pytest.mark.parametrize("lq, lk", [([1, 2], [5000, 40]), ([200, 90], [1500, 2000])])
+def test_strides_streams_graphs_and_two_calls_at_once(h3, dev, lq, lk):
+    case = Case(lq, lk, 8, 2, 128, 32, True, 1)
+    a = case.on(dev)
+    out, lse = h3.paged_attn_fwd(**a, return_lse=True)
+    wide = torch.full((a["q"].shape[0], 12, 128), 3.0, dtype=torch.bfloat16, device=dev)
+    wide[:, 2:10] = a["q"]
+    assert torch.equal(h3.paged_attn_fwd(**{**a, "q": wide[:, 2:10]})[:case.n], out[:case.n])
+    torch.cuda.synchronize()
+    streams, results = [torch.cuda.Stream() for _ in range(2)], []
+    for st in streams:
+        with torch.cuda.stream(st):
+            for _ in range(4):
+                results.append(h3.paged_attn_fwd(**a, return_lse=True))
+    torch.cuda.synchronize()
+    for o, l in results:
+        assert torch.equal(o[:case.n], out[:case.n]) and torch.equal(l[:, :case.n], lse[:, :case.n])
+    # captured, then replayed on new contents: other lengths, other pages
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        o, l = h3.paged_attn_fwd(**a, return_lse=True)
+    for step in (0, 1):
+        a["seqused_k"].sub_(13 * step)
+        a["q"][:case.n].mul_(1 - 0.5 * step)
+        graph.replay()
+        want, wl = h3.paged_attn_fwd(**a, return_lse=True)
+        torch.cuda.synchronize()
+        assert torch.equal(o[:case.n], want[:case.n]) and torch.equal(l[:, :case.n], wl[:, :case.n])
+    assert h3.get_device_error(dev) == 0
+
+
+@pytest_gpu
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", [1, 30])
+def test_cache_past_2_31_elements(h3, dev, e4m3, rows):
+    """Pages whose first element lies past 2^31 and 2^32 elements."""
+    h, d, page, pages = 8, 128, 256, 17000  # 4.46e9 elements
+    case = Case([rows], [700], 16, h, d, page, e4m3, 1)
+    a = case.on(dev)
+    ids = [pages - 1, 8200, 16385]
+    for name in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        if name not in a:
+            continue
+        kind = torch.uint8 if a[name].dtype is torch.float8_e4m3fn else a[name].dtype
+        big = torch.empty((pages, *a[name].shape[1:]), dtype=kind, device=dev)
+        for i, p in enumerate(ids):
+            big[p] = a[name].view(kind)[int(case.table[0, i])]
+        a[name] = big.view(a[name].dtype)
+    a["block_table"] = torch.tensor([ids], dtype=torch.int32, device=dev)
+    out, lse = h3.paged_attn_fwd(**a, return_lse=True)
+    torch.cuda.synchronize()
+    assert h3.get_device_error(dev) == 0
+    case.check(out, lse)
+
+
+@pytest_gpu
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_wait_that_runs_out_ends_the_call(h3, dev, e4m3):
+    """As in test_gpu_cross_timeout.py: the loader stops after three tiles, the waits end by their limit."""
+    case = Case([200], [1500], 4, 2, 128, 64, e4m3, 1)
+    a = case.on(dev)
+    want = h3.paged_attn_fwd(**a)
+    torch.cuda.synchronize()
+    assert h3.get_device_error(dev) == 0
+    h3.set_wait_limit_ns(20_000_000)
+    h3.debug_stall_loads(3)
+    try:
+        h3.paged_attn_fwd(**a)
+        torch.cuda.synchronize()
+        later = torch.full_like(a["q"], 7.0)
+        h3.paged_attn_fwd(**a, out=later)  # leaves at once while the timeout is recorded
+        torch.cuda.synchronize()
+    finally:
+        h3.debug_stall_loads(-1)
+        h3.set_wait_limit_ns(0)
+    assert torch.all(later == 7.0)
+    assert h3.get_device_error(dev) == 7 and h3.get_device_error(dev) == 0
+    assert torch.equal(h3.paged_attn_fwd(**a)[:case.n], want[:case.n])
+    torch.cuda.synchronize()
+    assert h3.get_device_error(dev) == 0
