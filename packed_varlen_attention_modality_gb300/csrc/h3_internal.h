@@ -96,14 +96,13 @@ struct ResidualNormArgs {
   unsigned int* err;
 };
 constexpr int kResidualNormMaxDim = 8192;
-constexpr int kResidualNormMaxCtas = 304;  // 2 x 152 SMs
+constexpr int kResidualNormMaxBwdCtas = 8 * 152;
 inline int residual_norm_ctas(int num_tokens, int resident) {
-  const int most = resident < kResidualNormMaxCtas ? resident : kResidualNormMaxCtas;
-  return num_tokens < most ? num_tokens : most;
+  return num_tokens < resident ? num_tokens : resident;
 }
 // three column sums for each pair of a CTA and a request with rows in it
 inline size_t residual_norm_bwd_bytes(int num_tokens, int num_requests, int dim) {
-  const size_t pairs = static_cast<size_t>(residual_norm_ctas(num_tokens, kResidualNormMaxCtas)) + num_requests;
+  const size_t pairs = static_cast<size_t>(residual_norm_ctas(num_tokens, kResidualNormMaxBwdCtas)) + num_requests;
   return pairs * 3 * dim * sizeof(float);
 }
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool backward, cudaStream_t stream);

@@ -14,9 +14,9 @@
 // Memory-bound: the forward reads x, y and writes x', h once; the backward reads dx', dh, x', y and writes
 // dx, dy once.  A CTA takes a contiguous range of rows, so the request's vectors (w (1 + scale), shift,
 // w_b gate) stay in registers from row to row, eight columns a thread, and so do the backward's column
-// sums.  Rows come through a ring in shared memory by bulk copies that run several rows ahead: the row sums
-// of a row (a shuffle tree and one barrier each) wait on no load.  All arithmetic is fp32; the mean of a layer
-// norm is subtracted before the squares are summed, so a large mean costs no digits.
+// sums.  Rows come through a ring in shared memory by bulk copies that run several rows ahead, so a row waits on no
+// load but on its sums alone: the warps exchange them once for each norm (the backward: once for all that the
+// inputs give, once for the branch's dot product).  All arithmetic is fp32.
 #include <cuda_bf16.h>
 
 #include "h3_internal.h"
@@ -27,36 +27,37 @@ namespace h3 {
 namespace {
 
 constexpr int kMaxStages = 8;
+constexpr int kVecs = 2;  // groups of eight columns a thread
 
+// Eight values as packed pairs: an instruction takes two of them.
 struct Vec8 {
-  float v[8];
+  float2 p[4];
 };
-__device__ __forceinline__ Vec8 unpack(const uint4& p) {
-  const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ Vec8 all8(float v) { return Vec8{{both(v), both(v), both(v), both(v)}}; }
+__device__ __forceinline__ Vec8 load8(const __nv_bfloat16* p) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   Vec8 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = __uint_as_float(w[i] << 16);
-    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) r.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   return r;
 }
-__device__ __forceinline__ Vec8 load8(const __nv_bfloat16* p) { return unpack(*reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ Vec8 load8(const float* p) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  return Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+  return Vec8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const Vec8& r) {
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(r.v[0], r.v[1]), pack_bf16x2(r.v[2], r.v[3]),
-                                                 pack_bf16x2(r.v[4], r.v[5]), pack_bf16x2(r.v[6], r.v[7])));
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(r.p[0].x, r.p[0].y), pack_bf16x2(r.p[1].x, r.p[1].y),
+                                                 pack_bf16x2(r.p[2].x, r.p[2].y), pack_bf16x2(r.p[3].x, r.p[3].y)));
 }
 __device__ __forceinline__ void store8(float* p, const Vec8& r) {
-  __stcs(reinterpret_cast<float4*>(p), make_float4(r.v[0], r.v[1], r.v[2], r.v[3]));
-  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(r.v[4], r.v[5], r.v[6], r.v[7]));
+  __stcs(reinterpret_cast<float4*>(p), make_float4(r.p[0].x, r.p[0].y, r.p[1].x, r.p[1].y));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(r.p[2].x, r.p[2].y, r.p[3].x, r.p[3].y));
 }
 // Eight values of a weight or modulation vector; `none` where there is no vector.
 __device__ __forceinline__ Vec8 load_vector(const void* base, int64_t at, int bf16, float none) {
-  if (base == nullptr) return Vec8{{none, none, none, none, none, none, none, none}};
+  if (base == nullptr) return all8(none);
   return bf16 ? load8(static_cast<const __nv_bfloat16*>(base) + at) : load8(static_cast<const float*>(base) + at);
 }
 
@@ -80,30 +81,119 @@ __device__ __forceinline__ int request_of(const ResidualNormArgs& a, int n, int*
   return lo;
 }
 
-// Sums of two values over the CTA, in a fixed order.  One barrier: the slots alternate, and a slot is
-// written again only behind the next sum's barrier, which all threads reach after reading this one's.
-struct BlockSum {
-  float2 (*slots)[32];
+// The sums of N values over the lanes, on every lane.  Of three values and more a lane gives half to a partner and
+// takes the partner's share of the others while more than one is left, so they cost little more than one: lane l ends
+// with the value whose number its first bits spell, and hands it round.
+template <int N>
+__device__ __forceinline__ void lane_sums(float (&v)[N]) {
+  if constexpr (N <= 2) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  } else {
+    constexpr int P = N <= 4 ? 4 : 8;  // values, filled up to a power of two
+    const int lane = threadIdx.x & 31;
+    float w[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) w[i] = i < N ? v[i] : 0.f;
+    int o = 16;
+#pragma unroll
+    for (int n = P / 2; n > 0; n /= 2, o /= 2) {
+      const bool upper = lane & o;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float give = upper ? w[i] : w[n + i], keep = upper ? w[n + i] : w[i];
+        w[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+#pragma unroll
+    for (; o > 0; o /= 2) w[0] += __shfl_xor_sync(0xffffffffu, w[0], o);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, w[0], i * (32 / P));
+  }
+}
+
+// What the warps tell one another about a row, one barrier each time: the slots alternate, and one is written again
+// only behind the next exchange's barrier, which all threads reach after reading this one's.
+constexpr int kMaxTold = 6;
+template <int kWarps>
+struct Told {
+  float v[2][kWarps][kMaxTold];
+};
+template <int kWarps>
+struct Exchange {
+  Told<kWarps>& told;
   int turn = 0;
-  __device__ __forceinline__ float2 operator()(float a, float b) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  // Publishes the warp's v; then each lane holds the values of warp `lane` (0 past the last), `first` those of warp
+  // 0.  False if any thread says so.
+  template <int N>
+  __device__ __forceinline__ bool operator()(float (&v)[N], float (&first)[N], bool ok) {
+    static_assert(N <= kMaxTold);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
+      for (int i = 0; i < N; ++i) told.v[turn][warp][i] = v[i];
     }
-    if (lane == 0) slots[turn][warp] = make_float2(a, b);
-    __syncthreads();
-    float2 t = lane < warps ? slots[turn][lane] : make_float2(0.f, 0.f);
+    const bool failed = __syncthreads_or(!ok);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = lane < static_cast<int>(blockDim.x >> 5) ? told.v[turn][lane][i] : 0.f;
+      first[i] = told.v[turn][0][i];
+    }
     turn ^= 1;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
-      t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
-    }
-    return t;
+    return !failed;
   }
 };
+
+// The same in two halves, so that a warp can do something else while it waits for the others: say() publishes,
+// hear() waits.  Calls alternate; slots are written again two calls later, behind a hear() for which every warp has
+// left its own call before.
+template <int kWarps>
+struct Parley {
+  float v[2][kWarps][kMaxTold];
+  uint64_t bar;
+  int failed[2];
+};
+template <int kWarps, int N>
+struct Talk {
+  Parley<kWarps>& p;
+  int turn = 0, heard = 0;
+  __device__ __forceinline__ void say(const float (&v)[N], bool ok) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (!ok) p.failed[turn & 1] = 1;
+    __syncwarp();
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) p.v[turn & 1][warp][i] = v[i];
+      mbar_arrive(smem_u32(&p.bar));
+    }
+    ++turn;
+  }
+  // Each lane's v: the values of warp `lane` (0 past the last); `first`: those of warp 0.  False if any thread said
+  // so, or a wait runs out.
+  __device__ __forceinline__ bool hear(float (&v)[N], float (&first)[N]) {
+    const int lane = threadIdx.x & 31;
+    const bool there = mbar_wait(smem_u32(&p.bar), heard & 1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      v[i] = lane < static_cast<int>(blockDim.x >> 5) ? p.v[heard & 1][lane][i] : 0.f;
+      first[i] = p.v[heard & 1][0][i];
+    }
+    const bool fine = *const_cast<volatile int*>(&p.failed[heard & 1]) == 0;
+    ++heard;
+    return __all_sync(0xffffffffu, there && fine);
+  }
+};
+
+// Columns of warp w's.
+template <int kVecs>
+__device__ __forceinline__ float columns_of(int w, int dim) {
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) n += min(max(dim - (k * static_cast<int>(blockDim.x) + w * 32) * 8, 0), 256);
+  return static_cast<float>(w < static_cast<int>(blockDim.x >> 5) ? n : 0);
+}
 
 // A CTA's rows through a ring of stages in shared memory.  kTensors rows a stage, those of the stream's type
 // first; an absent tensor's place is not loaded.
@@ -120,72 +210,121 @@ struct RowRing {
   uint32_t at[kTensors], stage_bytes, load_bytes;
   int stages, first, rows;
 
-  __device__ __forceinline__ void issue(int i) {  // one thread; row first + i
-    const int s = i % stages;
+  int stage, parity;   // of the row that is read
+  int freed, freed_at;  // rows whose stages have been given back, the stage of the next one
+
+  __device__ __forceinline__ void issue(int i, int s) {  // one thread; the CTA's row i into stage s
+    const uint64_t policy = l2_policy_evict_first();  // every row is read once
     const uint32_t bar = smem_u32(bars + s);
     mbar_arrive_expect_tx(bar, load_bytes);
 #pragma unroll
     for (int t = 0; t < kTensors; ++t)
       if (src[t].base != nullptr)
-        bulk_load(smem_u32(smem + s * stage_bytes + at[t]), src[t].base + (first + i) * src[t].stride, src[t].bytes, bar);
+        bulk_load_hint(smem_u32(smem + s * stage_bytes + at[t]), src[t].base + (first + i) * src[t].stride,
+                       src[t].bytes, bar, policy);
   }
   __device__ __forceinline__ void start() {
+    stage = parity = freed = freed_at = 0;
     if (threadIdx.x == 0) {
       for (int s = 0; s < stages; ++s) mbar_init(smem_u32(bars + s), 1);
       fence_mbarrier_init();
-      for (int i = 0; i < min(stages, rows); ++i) issue(i);
+      for (int i = 0; i < min(stages, rows); ++i) issue(i, i);
     }
     __syncthreads();
   }
-  __device__ __forceinline__ bool wait(int i) const {
-    return mbar_wait(smem_u32(bars + i % stages), (i / stages) & 1);
+  __device__ __forceinline__ bool wait() const { return mbar_wait(smem_u32(bars + stage), parity); }
+  __device__ __forceinline__ const uint8_t* row(int t) const { return smem + stage * stage_bytes + at[t]; }
+  __device__ __forceinline__ void advance() {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1;
+    }
   }
-  __device__ __forceinline__ const uint8_t* row(int i, int t) const { return smem + i % stages * stage_bytes + at[t]; }
-  // behind a barrier that follows the last read of row i
-  __device__ __forceinline__ void refill(int i) {
-    if (threadIdx.x == 0 && i + stages < rows) issue(i + stages);
+  // Gives the stages of all rows before row i back, behind a barrier that follows their last read.
+  __device__ __forceinline__ void release(int i) {
+    for (; freed < i; ++freed) {
+      if (threadIdx.x == 0 && freed + stages < rows) issue(freed + stages, freed_at);
+      if (++freed_at == stages) freed_at = 0;
+    }
   }
-  // a wait ran out: nothing is left in flight
-  __device__ __forceinline__ void drain(int i, unsigned int* err) {
+  // A wait ran out (the current row's, or another warp's): nothing is left in flight.
+  __device__ __forceinline__ void drain(unsigned int* err) {
     if (threadIdx.x != 0) return;
     record_error(err, kErrTimeout);
-    for (int j = i; j < min(i + stages, rows); ++j) wait(j);
+    for (int j = freed; j < min(freed + stages, rows); ++j)
+      mbar_wait(smem_u32(bars + j % stages), (j / stages) & 1);
   }
 };
 
-__host__ __device__ constexpr uint32_t row_place(uint32_t bytes) { return (bytes + 127) / 128 * 128; }
+__host__ __device__ constexpr uint32_t row_place(size_t bytes) { return static_cast<uint32_t>((bytes + 127) / 128 * 128); }
 
-// 1 / sqrt(mean(c^2) + eps) of the row, which is centred in place for a layer norm; 1 without a norm.
+// The sums of a row that a norm needs, in two steps around an exchange.  A layer norm's squares are summed about the
+// warp's own mean, and the warps' sums are joined about the mean of all (from the first warp's, exactly in the
+// sense that no large numbers cancel), so a large mean costs no digits and one exchange does.
 template <int kVecs>
-__device__ __forceinline__ float row_factor(Vec8 (&x)[kVecs], const bool (&own)[kVecs], int kind, float inv_dim, float eps,
-                                            BlockSum& sum) {
-  if (kind == kNormNone) return 1.f;
-  if (kind == kNormLayer) {
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += x[k].v[e];
-    const float mean = sum(s, 0.f).x * inv_dim;
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[k].v[e] = own[k] ? x[k].v[e] - mean : 0.f;
-  }
-  float s = 0.f;
+__device__ __forceinline__ float warp_mean(const Vec8 (&x)[kVecs], float inv_columns) {
+  float2 s = make_float2(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < kVecs; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(x[k].v[e], x[k].v[e], s);
-  return rsqrtf(sum(s, 0.f).x * inv_dim + eps);
+    for (int e = 0; e < 4; ++e) s = fadd2(s, x[k].p[e]);
+  float t[1] = {s.x + s.y};
+  lane_sums(t);
+  return t[0] * inv_columns;
+}
+template <bool kLayer, int kVecs>
+__device__ __forceinline__ float lane_squares(const Vec8 (&x)[kVecs], const bool (&own)[kVecs], float mean) {
+  float2 s = make_float2(0.f, 0.f);
+  const float2 m = both(-mean);
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    if (!own[k]) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 c = kLayer ? fadd2(x[k].p[e], m) : x[k].p[e];
+      s = ffma2(c, c, s);
+    }
+  }
+  return s.x + s.y;
+}
+struct Stats {
+  float mean, factor;  // 0 and 1 / sqrt(mean(x^2) + eps) for an RMS norm
+};
+// One norm's statistics, by an exchange of their own.  (kLayer: a norm of the call is a layer norm.)
+template <int kVecs, bool kLayer, typename Tell>
+__device__ __forceinline__ bool row_stats(const Vec8 (&x)[kVecs], const bool (&own)[kVecs], int kind, float inv_mine,
+                                          float theirs, float inv_dim, float eps, Tell& tell, bool ok, Stats* r) {
+  if constexpr (kLayer) {
+    const bool layer = kind == kNormLayer;
+    float first[2], v[2];
+    v[0] = layer ? warp_mean(x, inv_mine) : 0.f;
+    float q[1] = {lane_squares<true>(x, own, v[0])};
+    lane_sums(q);
+    v[1] = q[0];
+    ok = tell(v, first, ok);
+    const float d = v[0] - first[0];  // of this lane's warp's mean from the first's
+    float t[2] = {theirs * d, fmaf(theirs * d, d, v[1])};
+    lane_sums(t);
+    const float shift = t[0] * inv_dim;
+    r->mean = first[0] + shift;
+    r->factor = rsqrtf((t[1] - t[0] * shift) * inv_dim + eps);
+  } else {
+    float q[1] = {lane_squares<false>(x, own, 0.f)}, first[1];
+    lane_sums(q);
+    ok = tell(q, first, ok);
+    lane_sums(q);
+    r->mean = 0.f;
+    r->factor = rsqrtf(q[0] * inv_dim + eps);
+  }
+  return ok;
 }
 
-template <typename X, int kVecs, int kThreads, int kCtas>
+template <typename X, int kVecs, int kThreads, int kCtas, bool kLayer>
 __global__ void __launch_bounds__(kThreads, kCtas)
 residual_norm_kernel(const __grid_constant__ ResidualNormArgs a, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[kMaxStages];
-  __shared__ float2 slots[2][32];
+  __shared__ Told<kThreads / 32> told;
   grid_dependency_wait();
   launch_dependents();
   const int dim = a.dim, ctas = static_cast<int>(gridDim.x);
@@ -204,8 +343,10 @@ residual_norm_kernel(const __grid_constant__ ResidualNormArgs a, int stages) {
   ring.load_bytes = xb + yb;
   ring.start();
 
-  BlockSum sum{slots};
+  Exchange<kThreads / 32> tell{told};
   const float inv_dim = 1.f / dim;
+  const float mine = columns_of<kVecs>(threadIdx.x >> 5, dim), theirs = columns_of<kVecs>(threadIdx.x & 31, dim);
+  const float inv_mine = mine > 0.f ? 1.f / mine : 0.f;
   int col[kVecs];
   bool own[kVecs];
 #pragma unroll
@@ -228,43 +369,58 @@ residual_norm_kernel(const __grid_constant__ ResidualNormArgs a, int stages) {
         const Vec8 g = load_vector(a.gate, r * a.gate_stride + col[k], a.mod_bf16, 1.f);
         shift[k] = load_vector(a.shift, r * a.shift_stride + col[k], a.mod_bf16, 0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          gain[k].v[e] = w.v[e] * (1.f + sc.v[e]);
-          gate[k].v[e] = wb.v[e] * g.v[e];
+        for (int e = 0; e < 4; ++e) {
+          gain[k].p[e] = fmul2(w.p[e], fadd2(both(1.f), sc.p[e]));
+          gate[k].p[e] = fmul2(wb.p[e], g.p[e]);
         }
       }
     }
-    const bool ok = ring.wait(i);
+    const bool ok = ring.wait();
     Vec8 x[kVecs], y[kVecs];
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       x[k] = y[k] = Vec8{};
       if (!own[k]) continue;
-      x[k] = load8(reinterpret_cast<const X*>(ring.row(i, 0)) + col[k]);
-      if (yb > 0) y[k] = load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(i, 1)) + col[k]);
+      x[k] = load8(reinterpret_cast<const X*>(ring.row(0)) + col[k]);
+      if (yb > 0) y[k] = load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(1)) + col[k]);
     }
-    if (__syncthreads_or(!ok)) {  // the whole CTA leaves together
-      ring.drain(i, a.err);
-      return;
+    // the first exchange of the row is also where a wait that ran out is heard of, and the last read of its stage
+    const bool branch = yb > 0 && a.branch_norm != kNormNone, norm = a.norm != kNormNone;
+    Stats st{0.f, 1.f};
+    bool fine = true;
+    if (branch) {
+      fine = row_stats<kVecs, kLayer>(y, own, a.branch_norm, inv_mine, theirs, inv_dim, a.eps, tell, ok, &st);
     }
-    ring.refill(i);
     if (yb > 0) {
-      const float ry = row_factor(y, own, a.branch_norm, inv_dim, a.eps, sum);
+      const float2 m = both(-st.mean), f = both(st.factor), alpha = both(a.residual_scale);
 #pragma unroll
       for (int k = 0; k < kVecs; ++k) {
         if (!own[k]) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[k].v[e] = fmaf(y[k].v[e] * ry, gate[k].v[e], a.residual_scale * x[k].v[e]);
-        store8(static_cast<X*>(a.x_out) + n * a.x_out_stride + col[k], x[k]);
+        for (int e = 0; e < 4; ++e) {
+          const float2 c = kLayer ? fadd2(y[k].p[e], m) : y[k].p[e];
+          x[k].p[e] = ffma2(fmul2(c, f), gate[k].p[e], fmul2(alpha, x[k].p[e]));
+        }
       }
     }
-    if (a.norm == kNormNone) continue;
-    const float rs = row_factor(x, own, a.norm, inv_dim, a.eps, sum);
+    if (norm) fine = row_stats<kVecs, kLayer>(x, own, a.norm, inv_mine, theirs, inv_dim, a.eps, tell, ok && fine, &st);
+    else if (!branch) fine = !__syncthreads_or(!ok);
+    if (!fine) {  // the whole CTA leaves together
+      ring.drain(a.err);
+      return;
+    }
+    ring.advance();
+    ring.release(i + 1);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       if (!own[k]) continue;
+      if (yb > 0) store8(static_cast<X*>(a.x_out) + n * a.x_out_stride + col[k], x[k]);
+      if (!norm) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[k].v[e] = fmaf(x[k].v[e] * rs, gain[k].v[e], shift[k].v[e]);
+      for (int e = 0; e < 4; ++e) {
+        const float2 c = kLayer ? fadd2(x[k].p[e], both(-st.mean)) : x[k].p[e];
+        x[k].p[e] = ffma2(fmul2(c, both(st.factor)), gain[k].p[e], shift[k].p[e]);
+      }
       store8(a.h + n * a.h_stride + col[k], x[k]);
     }
   }
@@ -274,12 +430,12 @@ residual_norm_kernel(const __grid_constant__ ResidualNormArgs a, int stages) {
 // r only grow, one at least at each new pair, so no two pairs share a slot.
 constexpr int kSums = 3;
 
-template <typename X, int kVecs, int kThreads, int kCtas>
+template <typename X, int kVecs, int kThreads, int kCtas, bool kLayer>
 __global__ void __launch_bounds__(kThreads, kCtas)
 residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[kMaxStages];
-  __shared__ float2 slots[2][32];
+  __shared__ Parley<kThreads / 32> inputs, dots;
   grid_dependency_wait();
   launch_dependents();
   const int dim = a.dim, ctas = static_cast<int>(gridDim.x);
@@ -306,10 +462,20 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
     ring.load_bytes += ring.src[t].bytes;
   }
   ring.stage_bytes = place;
+  if (threadIdx.x == 0) {
+    for (Parley<kThreads / 32>* p : {&inputs, &dots}) {
+      mbar_init(smem_u32(&p->bar), blockDim.x >> 5);
+      p->failed[0] = p->failed[1] = 0;
+    }
+  }
   ring.start();
 
-  BlockSum sum{slots};
+  constexpr int kTold = kLayer ? 6 : 3, kDots = kLayer ? 2 : 1;
+  Talk<kThreads / 32, kTold> row_talk{inputs};
+  Talk<kThreads / 32, kDots> dot_talk{dots};
   const float inv_dim = 1.f / dim;
+  const float mine = columns_of<kVecs>(threadIdx.x >> 5, dim), theirs = columns_of<kVecs>(threadIdx.x & 31, dim);
+  const float inv_mine = mine > 0.f ? 1.f / mine : 0.f;
   int col[kVecs];
   bool own[kVecs];
 #pragma unroll
@@ -319,6 +485,7 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
   }
   Vec8 gain[kVecs], gate[kVecs];
   Vec8 sums[kSums][kVecs] = {};
+  const bool want_shift = a.dshift != nullptr;
   int request = -1, request_end = ring.first;
   auto flush = [&] {
     if (request < 0) return;
@@ -330,12 +497,36 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
         if (own[k]) {
           float4* p = reinterpret_cast<float4*>(slot + static_cast<size_t>(j) * dim + col[k]);
           const Vec8& s = sums[j][k];
-          p[0] = make_float4(s.v[0], s.v[1], s.v[2], s.v[3]);
-          p[1] = make_float4(s.v[4], s.v[5], s.v[6], s.v[7]);
+          p[0] = make_float4(s.p[0].x, s.p[0].y, s.p[1].x, s.p[1].y);
+          p[1] = make_float4(s.p[2].x, s.p[2].y, s.p[3].x, s.p[3].y);
         }
         sums[j][k] = Vec8{};
       }
   };
+  const bool layer = kLayer && a.norm == kNormLayer, branch_layer = kLayer && a.branch_norm == kNormLayer;
+  const bool branch = has_y && a.branch_norm != kNormNone;
+  auto load_x = [&](int k) { return load8(reinterpret_cast<const X*>(ring.row(0)) + col[k]); };
+  auto load_g = [&](int k) { return load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(2)) + col[k]); };
+  auto load_y = [&](int k) { return load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(3)) + col[k]); };
+  Vec8 t[kVecs], y[kVecs];  // of the row whose dot product is on its way: t gate w_b and yh
+  float2 ry = both(1.f);
+  // The rest of row n once the dot products are there.
+  auto finish = [&](int n) {
+    float d[kDots], unused[kDots];
+    const bool fine = dot_talk.hear(d, unused);
+    lane_sums(d);
+    const float2 dot = both(-d[0] * inv_dim), mean = both(branch_layer ? -d[kDots - 1] * inv_dim : 0.f);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      if (!own[k]) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        t[k].p[e] = fmul2(ry, ffma2(y[k].p[e], dot, kLayer ? fadd2(t[k].p[e], mean) : t[k].p[e]));
+      store8(a.dy + n * a.dy_stride + col[k], t[k]);
+    }
+    return fine;
+  };
+  bool fine = true;
   for (int i = 0; i < ring.rows; ++i) {
     const int n = ring.first + i;
     if (n >= request_end) {
@@ -349,86 +540,130 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
         const Vec8 wb = load_vector(a.branch_weight, col[k], a.weight_bf16, 1.f);
         const Vec8 g = load_vector(a.gate, request * a.gate_stride + col[k], a.mod_bf16, 1.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          gain[k].v[e] = w.v[e] * (1.f + sc.v[e]);
-          gate[k].v[e] = wb.v[e] * g.v[e];
+        for (int e = 0; e < 4; ++e) {
+          gain[k].p[e] = fmul2(w.p[e], fadd2(both(1.f), sc.p[e]));
+          gate[k].p[e] = fmul2(wb.p[e], g.p[e]);
         }
       }
     }
-    const bool ok = ring.wait(i);
-    Vec8 x[kVecs], t[kVecs], g[kVecs], y[kVecs];
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      x[k] = t[k] = g[k] = y[k] = Vec8{};
-      if (!own[k]) continue;
+    // what the row's inputs give: the statistics of both norms and the sums of g and g xh
+    const bool ok = ring.wait();
+    {
+      float wx = 0.f, wy = 0.f, q[kLayer ? 4 : 3];
+      float2 xx = make_float2(0.f, 0.f), gs = xx, gx = xx;
+      q[2] = 0.f;
       if (has_h) {
-        x[k] = load8(reinterpret_cast<const X*>(ring.row(i, 0)) + col[k]);
-        g[k] = load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(i, 2)) + col[k]);
-      }
-      if (has_dx) t[k] = load8(reinterpret_cast<const X*>(ring.row(i, 1)) + col[k]);
-      if (has_y) y[k] = load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(i, 3)) + col[k]);
-    }
-    if (__syncthreads_or(!ok)) {
-      ring.drain(i, a.err);
-      return;
-    }
-    ring.refill(i);
-    if (has_h) {
-      const float rs = row_factor(x, own, a.norm, inv_dim, a.eps, sum);
-      float s0 = 0.f, s1 = 0.f;
+        Vec8 x[kVecs];
 #pragma unroll
-      for (int k = 0; k < kVecs; ++k)
+        for (int k = 0; k < kVecs; ++k) x[k] = own[k] ? load_x(k) : Vec8{};
+        if (layer) wx = warp_mean(x, inv_mine);
+        const float2 m = both(-wx);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[k].v[e] *= rs;
-          sums[0][k].v[e] += g[k].v[e];
-          sums[1][k].v[e] = fmaf(g[k].v[e], x[k].v[e], sums[1][k].v[e]);
-          g[k].v[e] = own[k] ? g[k].v[e] * gain[k].v[e] : 0.f;
-          s0 += g[k].v[e];
-          s1 = fmaf(g[k].v[e], x[k].v[e], s1);
+        for (int k = 0; k < kVecs; ++k) {
+          if (!own[k]) continue;
+          const Vec8 g = load_g(k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 c = kLayer ? fadd2(x[k].p[e], m) : x[k].p[e], weighted = fmul2(g.p[e], gain[k].p[e]);
+            if (want_shift) sums[0][k].p[e] = fadd2(sums[0][k].p[e], g.p[e]);
+            xx = ffma2(c, c, xx);
+            if (kLayer) gs = fadd2(gs, weighted);
+            gx = ffma2(weighted, c, gx);
+          }
         }
-      const float2 m = sum(s0, s1);
-      const float mean = a.norm == kNormLayer ? m.x * inv_dim : 0.f, dot = m.y * inv_dim;
-#pragma unroll
-      for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          t[k].v[e] = fmaf(rs, g[k].v[e] - mean - x[k].v[e] * dot, t[k].v[e]);
-    }
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      if (!own[k]) continue;
-      Vec8 d;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) d.v[e] = a.residual_scale * t[k].v[e];
-      store8(static_cast<X*>(a.dx) + n * a.dx_stride + col[k], d);
-    }
-    if (!has_y) continue;
-    const float ry = row_factor(y, own, a.branch_norm, inv_dim, a.eps, sum);
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int k = 0; k < kVecs; ++k)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[k].v[e] *= ry;
-        sums[2][k].v[e] = fmaf(t[k].v[e], y[k].v[e], sums[2][k].v[e]);
-        t[k].v[e] = own[k] ? t[k].v[e] * gate[k].v[e] : 0.f;
-        s0 += t[k].v[e];
-        s1 = fmaf(t[k].v[e], y[k].v[e], s1);
       }
-    float mean = 0.f, dot = 0.f;
-    if (a.branch_norm != kNormNone) {
-      const float2 m = sum(s0, s1);
-      mean = a.branch_norm == kNormLayer ? m.x * inv_dim : 0.f;
-      dot = m.y * inv_dim;
+      if (branch) {
+        Vec8 b[kVecs];
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) b[k] = own[k] ? load_y(k) : Vec8{};
+        if (branch_layer) wy = warp_mean(b, inv_mine);
+        q[2] = lane_squares<kLayer>(b, own, wy);
+      }
+      q[0] = xx.x + xx.y;
+      q[1] = gx.x + gx.y;
+      if constexpr (kLayer) {
+        q[3] = gs.x + gs.y;
+        lane_sums(q);
+        const float v[6] = {q[0], q[1], q[2], q[3], wx, wy};
+        row_talk.say(v, ok);
+      } else {
+        lane_sums(q);
+        row_talk.say(q, ok);
+      }
     }
+    if (branch && i > 0) fine = finish(n - 1);  // while the others' sums come in
+    float s[kTold], first[kTold];
+    fine = row_talk.hear(s, first) && fine;
+    if (!fine) break;
+    ring.release(i);  // every warp is behind its last read of the row before
+    float x_mean = 0.f, y_mean = 0.f, x_square, y_square, x_dot, g_sum = 0.f;  // of the centred rows
+    if constexpr (kLayer) {
+      const float dx = s[4] - first[4], dy = s[5] - first[5];  // of this lane's warp's means from the first's
+      float j[6] = {theirs * dx, fmaf(theirs * dx, dx, s[0]), fmaf(dx, s[3], s[1]), s[3], theirs * dy, fmaf(theirs * dy, dy, s[2])};
+      lane_sums(j);
+      const float sx = j[0] * inv_dim, sy = j[4] * inv_dim;
+      x_mean = first[4] + sx;
+      y_mean = first[5] + sy;
+      x_square = j[1] - j[0] * sx;
+      y_square = j[5] - j[4] * sy;
+      x_dot = j[2] - sx * j[3];
+      g_sum = j[3];
+    } else {
+      lane_sums(s);
+      x_square = s[0];
+      x_dot = s[1];
+      y_square = s[2];
+    }
+    const float factor = rsqrtf(x_square * inv_dim + a.eps);
+    const float2 rs = both(factor), mean = both(layer ? -g_sum * inv_dim : 0.f), dot = both(-factor * x_dot * inv_dim);
+    if (branch) ry = both(rsqrtf(y_square * inv_dim + a.eps));
+    float2 ts = make_float2(0.f, 0.f), ty = ts;
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       if (!own[k]) continue;
+      Vec8& u = t[k];
+      u = has_dx ? load8(reinterpret_cast<const X*>(ring.row(1)) + col[k]) : Vec8{};
+      if (has_h) {
+        const Vec8 x = load_x(k), g = load_g(k);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t[k].v[e] = ry * (t[k].v[e] - mean - y[k].v[e] * dot);
-      store8(a.dy + n * a.dy_stride + col[k], t[k]);
+        for (int e = 0; e < 4; ++e) {
+          const float2 xh = fmul2(kLayer ? fadd2(x.p[e], both(-x_mean)) : x.p[e], rs);
+          sums[1][k].p[e] = ffma2(g.p[e], xh, sums[1][k].p[e]);
+          const float2 weighted = kLayer ? ffma2(g.p[e], gain[k].p[e], mean) : fmul2(g.p[e], gain[k].p[e]);
+          u.p[e] = ffma2(rs, ffma2(xh, dot, weighted), u.p[e]);
+        }
+      }
+      Vec8 scaled = u;
+      if (a.residual_scale != 1.f) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) scaled.p[e] = fmul2(both(a.residual_scale), u.p[e]);
+      }
+      store8(static_cast<X*>(a.dx) + n * a.dx_stride + col[k], scaled);
+      if (!has_y) continue;
+      y[k] = load_y(k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[k].p[e] = fmul2(kLayer ? fadd2(y[k].p[e], both(-y_mean)) : y[k].p[e], ry);
+        sums[2][k].p[e] = ffma2(u.p[e], y[k].p[e], sums[2][k].p[e]);
+        u.p[e] = fmul2(u.p[e], gate[k].p[e]);
+        if (kLayer) ts = fadd2(ts, u.p[e]);
+        ty = ffma2(u.p[e], y[k].p[e], ty);
+      }
+      if (!branch) store8(a.dy + n * a.dy_stride + col[k], u);
     }
+    ring.advance();
+    if (branch) {
+      float d[kDots];
+      d[0] = ty.x + ty.y;
+      if (kLayer) d[kDots - 1] = ts.x + ts.y;
+      lane_sums(d);
+      dot_talk.say(d, true);
+    }
+  }
+  if (fine && branch && ring.rows > 0) fine = finish(ring.first + ring.rows - 1);
+  if (!fine) {  // a wait ran out
+    ring.drain(a.err);
+    return;
   }
   flush();
 }
@@ -436,7 +671,7 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
 // The requests' column sums: their CTAs' slots, in CTA order within each strand, then over the strands.
 // A request's terms of the weights' gradients replace its first slot (its own columns of this block alone),
 // where weight_sum_kernel adds them over the requests; a single request's are the gradients themselves.
-constexpr int kSumColumns = 32, kSumStrands = 8;
+constexpr int kSumColumns = 32, kSumStrands = 32;
 __global__ void __launch_bounds__(kSumColumns* kSumStrands)
 request_sum_kernel(const __grid_constant__ ResidualNormArgs a, int ctas) {
   __shared__ float part[kSums][kSumStrands][kSumColumns];
@@ -446,6 +681,8 @@ request_sum_kernel(const __grid_constant__ ResidualNormArgs a, int ctas) {
   const int c = blockIdx.x * kSumColumns + lane;
   const bool own = c < a.dim;
   const bool single = a.num_requests == 1;
+  const bool wanted[kSums] = {a.dshift != nullptr, a.dscale != nullptr || a.dweight != nullptr,
+                              a.dgate != nullptr || a.dbranch_weight != nullptr};
   for (int r = blockIdx.y; r < a.num_requests; r += gridDim.y) {
     const int n = a.num_tokens;
     const int first = r == 0 || a.cu_requests == nullptr ? 0 : min(max(a.cu_requests[r], 0), n);
@@ -457,12 +694,12 @@ request_sum_kernel(const __grid_constant__ ResidualNormArgs a, int ctas) {
       hi = static_cast<int>((static_cast<int64_t>(end) * ctas - 1) / n);
     }
     float s[kSums] = {};
-    if (own) {
-      for (int k = lo + strand; k <= hi; k += kSumStrands) {
-        const float* p = a.partials + static_cast<size_t>(k + r) * kSums * a.dim + c;
 #pragma unroll
-        for (int j = 0; j < kSums; ++j) s[j] += p[static_cast<size_t>(j) * a.dim];
-      }
+    for (int j = 0; j < kSums; ++j) {
+      if (!wanted[j] || !own) continue;
+#pragma unroll 4
+      for (int k = lo + strand; k <= hi; k += kSumStrands)
+        s[j] += a.partials[(static_cast<size_t>(k + r) * kSums + j) * a.dim + c];
     }
     __syncthreads();
 #pragma unroll
@@ -528,33 +765,50 @@ weight_sum_kernel(const __grid_constant__ ResidualNormArgs a, int ctas) {
   if (a.dbranch_weight != nullptr) a.dbranch_weight[c] = b;
 }
 
-// Threads of a row: eight columns each (sixteen above 5,120), whole warps.
-int row_threads(int dim, int vecs) { return (dim + 256 * vecs - 1) / (256 * vecs) * 32; }
+// Threads of a row: 8 * kVecs columns each, whole warps.
+int row_threads(int dim) { return (dim + 256 * kVecs - 1) / (256 * kVecs) * 32; }
 
-template <typename X, int kVecs, int kThreads, int kCtas>
-cudaError_t launch_rows(const ResidualNormArgs& a, bool backward, int sms, cudaStream_t stream) {
-  constexpr int kSmem = 224 * 1024 / kCtas - 2048;
-  auto fwd = residual_norm_kernel<X, kVecs, kThreads, kCtas>;
-  auto bwd = residual_norm_bwd_kernel<X, kVecs, kThreads, kCtas>;
-  const uint32_t xb = row_place(a.dim * sizeof(X)), yb = row_place(a.dim * 2);
+// CTAs of kThreads at most, kCtas of them an SM.
+template <typename X, int kThreads, int kCtas, bool kBackward>
+cudaError_t launch_rows(const ResidualNormArgs& a, int sms, int* ctas, cudaStream_t stream) {
+  constexpr int kSmem = 226 * 1024 / kCtas - 1024 - 128 - 2 * static_cast<int>(sizeof(Parley<kThreads / 32>));
+  const bool layer = a.norm == kNormLayer || a.branch_norm == kNormLayer;
   const bool has_h = a.norm != kNormNone, has_y = a.y != nullptr;
-  const uint32_t stage = backward ? (has_h ? xb + yb : 0) + (a.dx_out != nullptr ? xb : 0) + (has_y ? yb : 0)
-                                  : xb + (has_y ? yb : 0);
+  const uint32_t xb = row_place(a.dim * sizeof(X)), yb = row_place(a.dim * 2);
+  const uint32_t stage = kBackward ? (has_h ? xb + yb : 0) + (a.dx_out != nullptr ? xb : 0) + (has_y ? yb : 0)
+                                   : xb + (has_y ? yb : 0);
   int stages = static_cast<int>(kSmem / stage);
   stages = stages < 1 ? 1 : stages > kMaxStages ? kMaxStages : stages;
-  const cudaError_t e = allow_shared_memory<kSmem>(backward ? bwd : fwd);
+  void (*kernel)(const ResidualNormArgs, int);
+  if constexpr (kBackward) {
+    kernel = layer ? residual_norm_bwd_kernel<X, kVecs, kThreads, kCtas, true>
+                   : residual_norm_bwd_kernel<X, kVecs, kThreads, kCtas, false>;
+  } else {
+    kernel = layer ? residual_norm_kernel<X, kVecs, kThreads, kCtas, true>
+                   : residual_norm_kernel<X, kVecs, kThreads, kCtas, false>;
+  }
+  const cudaError_t e = allow_shared_memory<kSmem>(kernel);
   if (e != cudaSuccess) return e;
-  const int ctas = residual_norm_ctas(a.num_tokens, sms * kCtas);
-  return launch_programmatic(backward ? bwd : fwd, dim3(ctas), dim3(row_threads(a.dim, kVecs)), stages * stage, stream, a,
-                             stages);
+  *ctas = residual_norm_ctas(a.num_tokens, sms * kCtas);
+  return launch_programmatic(kernel, dim3(*ctas), dim3(row_threads(a.dim)), stages * stage, stream, a, stages);
 }
 
 template <typename X>
 cudaError_t launch_type(const ResidualNormArgs& a, bool backward, int sms, int* ctas, cudaStream_t stream) {
-  *ctas = residual_norm_ctas(a.num_tokens, sms * (a.dim <= 2560 ? 2 : 1));
-  if (a.dim <= 2560) return launch_rows<X, 1, 320, 2>(a, backward, sms, stream);
-  if (a.dim <= 5120) return launch_rows<X, 1, 640, 1>(a, backward, sms, stream);
-  return launch_rows<X, 2, 512, 1>(a, backward, sms, stream);
+  if (backward) {
+    if (a.dim <= 512) return launch_rows<X, 32, 8, true>(a, sms, ctas, stream);
+    if (a.dim <= 1024) return launch_rows<X, 64, 5, true>(a, sms, ctas, stream);
+    if (a.dim <= 1536) return launch_rows<X, 96, 4, true>(a, sms, ctas, stream);
+    if (a.dim <= 2560) return launch_rows<X, 160, 2, true>(a, sms, ctas, stream);
+    if (a.dim <= 5120) return launch_rows<X, 320, 1, true>(a, sms, ctas, stream);
+    return launch_rows<X, 512, 1, true>(a, sms, ctas, stream);
+  }
+  if (a.dim <= 512) return launch_rows<X, 32, 16, false>(a, sms, ctas, stream);
+  if (a.dim <= 1024) return launch_rows<X, 64, 8, false>(a, sms, ctas, stream);
+  if (a.dim <= 1536) return launch_rows<X, 96, 6, false>(a, sms, ctas, stream);
+  if (a.dim <= 2560) return launch_rows<X, 160, 4, false>(a, sms, ctas, stream);
+  if (a.dim <= 5120) return launch_rows<X, 320, 2, false>(a, sms, ctas, stream);
+  return launch_rows<X, 512, 1, false>(a, sms, ctas, stream);
 }
 
 }  // namespace
