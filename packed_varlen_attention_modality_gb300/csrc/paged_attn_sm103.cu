@@ -362,8 +362,7 @@ struct PagedSource {
     if (key) {
       // value = bits * 2^120 * 2^e, in one product where 2^(120 + e) is a bf16
       const bool two = biased > 127 + 7;
-      const uint32_t first = (two ? 247u : biased + 120u) << 7, second = biased == kScaleNan ? 0x7fffu : biased << 7;
-      const uint32_t f2 = first | first << 16, s2 = second | second << 16;
+      const uint32_t first = (two ? 247u : biased + 120u) << 7, f2 = first | first << 16;
 #pragma unroll
       for (int p = 0; p < kD / 16; ++p) {
         const int swizzled = kD == 128 ? p ^ (row & 7) : p ^ ((row >> 1) & 3);
@@ -372,15 +371,19 @@ struct PagedSource {
         uint32_t b[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          b[2 * i] = bf16x2_mul(e4m3_pair_bits(w[i], w[i], 0x1100), f2);
-          b[2 * i + 1] = bf16x2_mul(e4m3_pair_bits(w[i], w[i], 0x3322), f2);
-        }
-        if (two) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[i] = bf16x2_mul(b[i], s2);
+          b[2 * i] = bf16x2_mul(e4m3_pair_bits<0>(w[i]), f2);
+          b[2 * i + 1] = bf16x2_mul(e4m3_pair_bits<2>(w[i]), f2);
         }
         *at(2 * p) = make_uint4(b[0], b[1], b[2], b[3]);
         *at(2 * p + 1) = make_uint4(b[4], b[5], b[6], b[7]);
+      }
+      if (two) {  // rows of values past 57,344, or with a NaN: a second product (apart, to keep the loop above straight)
+        const uint32_t second = biased == kScaleNan ? 0x7fffu : biased << 7, s2 = second | second << 16;
+#pragma unroll 1
+        for (int p = 0; p < kD / 8; ++p) {
+          const uint4 v = *at(p);
+          *at(p) = make_uint4(bf16x2_mul(v.x, s2), bf16x2_mul(v.y, s2), bf16x2_mul(v.z, s2), bf16x2_mul(v.w, s2));
+        }
       }
     } else if (zero) {
 #pragma unroll
@@ -404,7 +407,7 @@ cudaError_t launch(const PagedTileArgs& a, cudaStream_t stream) {
                           stream, a.seg, tokens, ws, split, sms, a.err);
   if (e != cudaSuccess) return e;
   const Source src{a.tmap_q, a.tmap_k, a.tmap_v, a.seg, a.k_scale, a.v_scale, group, tokens};
-  e = launch_programmatic(attn_tile_kernel<Source>, dim3(sms), dim3(kTileThreads), C::kSmemBytes, stream, src,
+  e = launch_programmatic(attn_tile_kernel<Source>, dim3(sms), dim3(kTileThreads<Source>), C::kSmemBytes, stream, src,
                           static_cast<__nv_bfloat16*>(a.o), a.wide, a.lse, a.scale, a.scale * 1.4426950408889634f,
                           static_cast<const uint32_t*>(ws), split, a.err,
                           static_cast<unsigned long long>(a.wait_limit_ns), a.stall_after_tiles);

@@ -56,25 +56,40 @@ __device__ __forceinline__ uint32_t e4m3x2_pack(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two e4m3 bytes, picked twice each out of x and y by `pick` (low half's, low half's, high half's, high half's), with
-// sign and the seven other bits moved to their places in a pair of bf16: the values times 2^(7 - 127), a subnormal
-// e4m3 being a subnormal bf16.
-__device__ __forceinline__ uint32_t e4m3_pair_bits(uint32_t x, uint32_t y, uint32_t pick) {
-  const uint32_t b = __byte_perm(x, y, pick);
-  return ((b >> 4) & 0x07f007f0u) | (b & 0x80008000u);
+// Bytes `pick` and `pick` + 1 of a word of e4m3 as a pair of bf16 that stand for the values times 2^(7 - 127), a
+// subnormal e4m3 being a subnormal bf16: the seven low bits go to bits 4 to 10 and the sign from there to bit 15.  With
+// b = s 2^7 + r that is 16 b + 240 s 2^7, two multiply-adds that leave the ALU, which the softmax needs too, two
+// instructions of five (a shift and two masks by it took 4).
+template <int kPick>
+__device__ __forceinline__ uint32_t e4m3_pair_bits(uint32_t w) {
+  const uint32_t b = __byte_perm(w, 0u, kPick == 0 ? 0x4140 : 0x4342);  // a byte in each half
+  uint32_t wide, r;
+  asm("mul.lo.u32 %0, %1, 16;" : "=r"(wide) : "r"(b));
+  asm("mad.lo.u32 %0, %1, 240, %2;" : "=r"(r) : "r"(b & 0x00800080u), "r"(wide));
+  return r;
 }
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
-// The same as values, exactly.
-__device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t x, uint32_t y, uint32_t pick) {
-  return bf16x2_mul(e4m3_pair_bits(x, y, pick), 0x7b807b80u);  // 2^120
+// Two e4m3 bytes (the low or the high half of a word) as a pair of f16, which holds each exactly.
+template <int kHalf>
+__device__ __forceinline__ uint32_t e4m3_pair_f16(uint32_t w) {
+  uint32_t r;
+  if (kHalf == 0) asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+  else asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(w));
+  return r;
 }
 // 2^e of a row's biased exponent; NaN for kScaleNan, which marks a row that held a NaN
 __device__ __forceinline__ float scale_of(uint32_t biased) {
   return __uint_as_float(biased == kScaleNan ? 0x7fffffffu : biased << 23);
+}
+
+// e itself as a float, NaN likewise
+__device__ __forceinline__ float scale_log2_of(uint32_t biased) {
+  const float e = __uint_as_float(0x4b000000u | biased) - (8388608.f + 127.f);  // 2^23 + biased, exactly
+  return biased == kScaleNan ? __uint_as_float(0x7fffffffu) : e;
 }
 
 }  // namespace h3

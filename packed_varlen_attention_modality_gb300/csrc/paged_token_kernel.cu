@@ -10,10 +10,13 @@
 // S = Q K^T and O += P V with 16 x 8 x 16 matrix instructions, and keeps a running max and sum; the warps are
 // added in order at the end of a piece.  A block lies in one page, whose id is looked up a block ahead.
 //
-// An e4m3 block becomes bf16 in registers: its bits, moved to bf16's places, are the value times 2^-120, which one
-// product mends exactly (subnormals too); the rows' scales go to the scores and to P, which are fp32.  The
-// order of the dims in S's product and in O's columns is chosen so that a lane's bytes lie together.
-// Scores, max, sum and O are fp32; P is rounded to bf16 for the product with V, o once at the end.
+// An e4m3 block becomes f16 in registers, one instruction for two values, and exactly: the rows' scales go to the
+// scores and the weights, which are fp32.  Q's rows are brought to f16 by a power of two each (their largest value to
+// 2^14: what that rounds is 2^-39 of it at most).  The weights of V's rows are 2^(score + V's exponent), kept
+// under 2^8 by a reference of their own that follows their largest, so that f16 rounds each by 2^-11 and drops
+// what is under 2^-33 of the largest.  The order of the dims in S's product and in O's columns is chosen so that a
+// lane's bytes lie together.
+// Scores, max, sum and O are fp32; P is rounded to bf16 (f16) for the product with V, o once at the end.
 #include <cuda_bf16.h>
 
 #include "h3_internal.h"
@@ -72,6 +75,19 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 }
 
 // The part of a (segment, key head) pair that a CTA takes: keys [first, end).
+__device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 struct Piece {
   PagedSegment s;
   int g, head, first, end;
@@ -126,7 +142,7 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
   __shared__ Scan scan;
   __shared__ Piece pieces[kMaxPieces];
   __shared__ int s_pieces, s_more;
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_w[kWarps][kRows];
   grid_dependency_wait();
   launch_dependents();
   const int S = a.seg.num_segments, heads = a.seg.num_kv_heads, block = a.seg.causal_block;
@@ -290,10 +306,38 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         }
         limit[h] = r < rows ? row_limit(p.s, r / group, block) : p.end;
       }
+      float q_scale[2] = {1.f, 1.f};  // e4m3: what the f16 rows are to be multiplied with
+      if (kE4m3) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t most = 0u;  // the largest magnitude's bits (of both halves: the upper decides)
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t x = q[kk][h + 2 * i];
+              most = max(most, max(x << 16 & 0x7fffffffu, x & 0x7fff0000u));
+            }
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+          // 2^(e - 14) for the exponent e of the largest; both powers are fp32
+          const int e = min(max(static_cast<int>(most >> 23), 16), 254);
+          q_scale[h] = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+          const float inv = __uint_as_float(static_cast<uint32_t>(254 - (e - 14)) << 23);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t& x = q[kk][h + 2 * i];
+              x = pack_f16x2(__uint_as_float(x << 16) * inv, __uint_as_float(x & 0xffff0000u) * inv);
+            }
+        }
+      }
       low = min(low, row_limit(p.s, 0, block));
 
       float o[D / 8][4] = {};
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      float top_w[2] = {-INFINITY, -INFINITY};  // e4m3: log2 of the weights' reference
       const int nblocks = (p.end - p.first + kBlock - 1) / kBlock;
 #pragma unroll 1
       for (int b = warp; b < nblocks; b += kWarps) {
@@ -326,15 +370,14 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
               const uint4 w4 = *reinterpret_cast<const uint4*>(base + C::piece_at(row, quad * (D / 64) + x));
               const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_16816(sc[n], q[4 * x + i], e4m3_pair_bf16(w[i], w[i], 0x1100), e4m3_pair_bf16(w[i], w[i], 0x3322));
+              for (int i = 0; i < 4; ++i) mma_16816_f16(sc[n], q[4 * x + i], e4m3_pair_f16<0>(w[i]), e4m3_pair_f16<1>(w[i]));
             }
             const uint32_t ks = *reinterpret_cast<const uint16_t*>(base + 2 * C::kHalf + n * 8 + c2);
             const float s0 = scale_of(ks & 0xffu), s1 = scale_of(ks >> 8);
-            sc[n][0] *= s0;
-            sc[n][1] *= s1;
-            sc[n][2] *= s0;
-            sc[n][3] *= s1;
+            sc[n][0] *= s0 * q_scale[0];
+            sc[n][1] *= s1 * q_scale[0];
+            sc[n][2] *= s0 * q_scale[1];
+            sc[n][3] *= s1 * q_scale[1];
           }
         }
         if (key + kBlock > low) {  // by select, so NaN/Inf there is discarded
@@ -344,19 +387,46 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
             for (int i = 0; i < 4; ++i)
               if (key + n * 8 + c2 + (i & 1) >= min(limit[i >> 1], p.end)) sc[n][i] = -INFINITY;
         }
-        // row maxima over the quad; the reference max moves only when it grows by more than 2^8
-        float alpha[2] = {1.f, 1.f};
+        // e4m3: the log2 of V's rows' weights, score and V's exponent together (a masked key's stays -inf: past the end
+        // lie rows whose scale may be anything)
+        float u[2][4];
+        if (kE4m3) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t vs = *reinterpret_cast<const uint16_t*>(base + 2 * C::kHalf + kBlock + n * 8 + c2);
+            const float v0 = scale_log2_of(vs & 0xffu), v1 = scale_log2_of(vs >> 8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              u[n][i] = sc[n][i] == -INFINITY ? -INFINITY : fmaf(sc[n][i], scale_log2, i & 1 ? v1 : v0);
+          }
+        }
+        // row maxima over the quad; a reference moves only when it grows by more than 2^8
+        auto row_max = [&](const float (&x)[2][4], int h) {
+          float y = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
+          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+          return fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+        };
+        float alpha[2] = {1.f, 1.f};  // of O
         bool moved = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float x = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          const float x = row_max(sc, h);
           if (x > m[h] && (m[h] == -INFINITY || (x - m[h]) * scale_log2 > 8.f)) {
-            alpha[h] = ex2_approx((m[h] - x) * scale_log2);
+            const float f = ex2_approx((m[h] - x) * scale_log2);
             m[h] = x;
-            l[h] *= alpha[h];
-            moved = true;
+            l[h] *= f;
+            if (!kE4m3) {
+              alpha[h] = f;
+              moved = true;
+            }
+          }
+          if (kE4m3) {
+            const float w = row_max(u, h);
+            if (w > top_w[h] && (top_w[h] == -INFINITY || w - top_w[h] > 8.f)) {
+              alpha[h] = ex2_approx(top_w[h] - w);
+              top_w[h] = w;
+              moved = true;
+            }
           }
         }
         if (__any_sync(0xffffffffu, moved)) {
@@ -367,23 +437,20 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         }
         uint32_t pw[4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          float v0 = 1.f, v1 = 1.f;
-          if (kE4m3) {
-            const uint32_t vs = *reinterpret_cast<const uint16_t*>(base + 2 * C::kHalf + kBlock + n * 8 + c2);
-            v0 = scale_of(vs & 0xffu);
-            v1 = scale_of(vs >> 8);
-          }
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float mb = m[h] == -INFINITY ? 0.f : m[h] * scale_log2;
             const float e0 = ex2_approx(fmaf(sc[n][2 * h], scale_log2, -mb));
             const float e1 = ex2_approx(fmaf(sc[n][2 * h + 1], scale_log2, -mb));
             l[h] += e0 + e1;
-            // (a weight of zero stays one: past the end lie rows whose scale may be anything)
-            pw[2 * n + h] = kE4m3 ? pack_bf16x2(e0 == 0.f ? 0.f : e0 * v0, e1 == 0.f ? 0.f : e1 * v1) : pack_bf16x2(e0, e1);
+            if (kE4m3) {
+              const float wb = top_w[h] == -INFINITY ? 0.f : top_w[h];
+              pw[2 * n + h] = pack_f16x2(ex2_approx(u[n][2 * h] - wb), ex2_approx(u[n][2 * h + 1] - wb));
+            } else {
+              pw[2 * n + h] = pack_bf16x2(e0, e1);
+            }
           }
-        }
         if (!kE4m3) {
 #pragma unroll
           for (int n = 0; n < D / 16; ++n) {
@@ -412,9 +479,11 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
             }
           }
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            const uint32_t sel = (j & 3) * 0x11 + 0x4400 + (j & 3) * 0x1100;  // byte j of each, twice
-            mma_16816(o[j], pw, e4m3_pair_bf16(w[0][j / 4], w[1][j / 4], sel), e4m3_pair_bf16(w[2][j / 4], w[3][j / 4], sel));
+          for (int j = 0; j < D / 8; j += 2) {  // bytes j and j + 1 of two keys each, in one word
+            const uint32_t pick = j % 4 == 0 ? 0x5140 : 0x7362;
+            const uint32_t lo = __byte_perm(w[0][j / 4], w[1][j / 4], pick), hi = __byte_perm(w[2][j / 4], w[3][j / 4], pick);
+            mma_16816_f16(o[j], pw, e4m3_pair_f16<0>(lo), e4m3_pair_f16<0>(hi));
+            mma_16816_f16(o[j + 1], pw, e4m3_pair_f16<1>(lo), e4m3_pair_f16<1>(hi));
           }
         }
         __syncwarp();  // the stage is read: it may be loaded again
@@ -429,6 +498,7 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         if (quad == 0) {
           s_m[warp][gr + 8 * h] = m[h];
           s_l[warp][gr + 8 * h] = l[h];
+          s_w[warp][gr + 8 * h] = kE4m3 ? top_w[h] : m[h] * scale_log2;  // O's reference
         }
       }
       __syncthreads();
@@ -437,8 +507,8 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
       for (int h = 0; h < 2; ++h) {
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][gr + 8 * h]);
-        f[h] = top == -INFINITY ? 0.f : ex2_approx((m[h] - top) * scale_log2);  // 0 for a warp without keys
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_w[w][gr + 8 * h]);
+        f[h] = top == -INFINITY ? 0.f : ex2_approx(s_w[warp][gr + 8 * h] - top);  // 0 for a warp without keys
       }
 #pragma unroll 1
       for (int w = 0; w < kWarps; ++w) {
@@ -465,7 +535,14 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         const float mb = top == -INFINITY ? 0.f : top;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) sum = fmaf(ex2_approx((s_m[w][r] - mb) * scale_log2), s_l[w][r], sum);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no keys: 0, and an LSE of -inf
+        // no keys: 0, and an LSE of -inf.  O's reference is not the sum's for e4m3.
+        float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (kE4m3) {
+          float o_top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) o_top = fmaxf(o_top, s_w[w][r]);
+          inv = o_top == -INFINITY ? 0.f : inv * exp2f(o_top - mb * scale_log2);
+        }
         const float lse = top * a.scale + logf(sum);
         const float* x = s_o + r * C::kOut + col;
         if (p.slot >= 0) {
