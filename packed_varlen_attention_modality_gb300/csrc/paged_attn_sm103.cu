@@ -407,7 +407,7 @@ cudaError_t launch(const PagedTileArgs& a, cudaStream_t stream) {
                           stream, a.seg, tokens, ws, split, sms, a.err);
   if (e != cudaSuccess) return e;
   const Source src{a.tmap_q, a.tmap_k, a.tmap_v, a.seg, a.k_scale, a.v_scale, group, tokens};
-  e = launch_programmatic(attn_tile_kernel<Source>, dim3(sms), dim3(kTileThreads<Source>), C::kSmemBytes, stream, src,
+  e = launch_programmatic(attn_tile_kernel<Source>, dim3(sms), dim3(kTileThreads), C::kSmemBytes, stream, src,
                           static_cast<__nv_bfloat16*>(a.o), a.wide, a.lse, a.scale, a.scale * 1.4426950408889634f,
                           static_cast<const uint32_t*>(ws), split, a.err,
                           static_cast<unsigned long long>(a.wait_limit_ns), a.stall_after_tiles);
