@@ -9,8 +9,8 @@
 // read back is what the cache holds.  A row with a NaN in it is marked by its scale and reads back as NaN
 // throughout, so no reader has to look for NaN among the values.
 //
-// Memory-bound: each row is read once and written once.  A row is D / 8 lanes of eight values; a warp takes
-// a token, finds its page once and runs over the heads of K and V with kUnroll rows a lane in flight; when
+// Memory-bound: each row is read once and written once.  A row is D / 8 lanes of eight values; a warp
+// takes a token, finds its page once and runs over the heads of K and V with kRowsAhead rows a lane in flight; when
 // tokens are few, a token's heads are dealt to several warps.
 #include <cuda_bf16.h>
 
@@ -23,13 +23,18 @@ namespace h3 {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kUnroll = 4, kCtas = 6;
+constexpr int kRowsAhead = 4, kCtas = 4;
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 
 // Where a packed row stands in the cache.
 struct Place {
   bool ok;
-  size_t page;
-  int row;
+  size_t row;  // of the first head's, counting rows of D values
 };
 __device__ __forceinline__ Place place_of(const KvCacheArgs& a, int n) {
   int lo = 0, hi = a.num_segments - 1;  // largest g with cu[g] <= n
@@ -37,7 +42,7 @@ __device__ __forceinline__ Place place_of(const KvCacheArgs& a, int n) {
     const int mid = (lo + hi + 1) >> 1;
     if (a.cu[mid] <= n) lo = mid; else hi = mid - 1;
   }
-  Place p{false, 0, 0};
+  Place p{false, 0};
   const int begin = a.cu[lo];
   if (begin > n || n >= a.cu[lo + 1]) return p;  // behind the last segment (or offsets out of order)
   const int64_t at = static_cast<int64_t>(a.start[lo]) + (n - begin);
@@ -51,7 +56,8 @@ __device__ __forceinline__ Place place_of(const KvCacheArgs& a, int n) {
     record_error(a.err, kErrBadPage);
     return p;
   }
-  return Place{true, static_cast<size_t>(id), static_cast<int>(at & ((1 << a.table.page_shift) - 1))};
+  return Place{true, (static_cast<size_t>(id) * a.heads << a.table.page_shift) +
+                         static_cast<size_t>(at & ((1 << a.table.page_shift) - 1))};
 }
 
 // The first warp of the grid looks over the offsets: they start at 0, do not fall, end within the capacity.
@@ -64,86 +70,77 @@ __device__ __forceinline__ void check_offsets(const KvCacheArgs& a) {
 
 template <int D, bool kE4m3, bool kWrite>
 __global__ void __launch_bounds__(kThreads, kCtas) kv_cache_kernel(const __grid_constant__ KvCacheArgs a, int parts) {
-  constexpr int kLanes = D / 8, kGroups = 32 / kLanes, kBatch = kGroups * kUnroll;
+  constexpr int kLanes = D / 8, kGroups = 32 / kLanes, kBatch = kGroups * kRowsAhead;
   grid_dependency_wait();
   launch_dependents();
   check_offsets(a);
   const int lane = threadIdx.x & 31, group = lane / kLanes, col = lane % kLanes * 8;
-  const int rows = 2 * a.heads;  // K's, then V's
-  const int warps = gridDim.x * kWarps;
+  const int batches = (a.heads + kBatch - 1) / kBatch;  // of heads; K's, then V's
+  const int warps = gridDim.x * kWarps, shift = a.table.page_shift;
   for (int64_t unit = blockIdx.x * kWarps + threadIdx.x / 32; unit < static_cast<int64_t>(a.capacity) * parts;
        unit += warps) {
     const int n = static_cast<int>(unit / parts), part = static_cast<int>(unit % parts);
     const Place at = place_of(a, n);
     if (!at.ok) continue;
-    for (int j0 = part * kBatch; j0 < rows; j0 += parts * kBatch) {
-      uint4 in[kUnroll];
-      uint32_t byte[kUnroll];
-      auto packed = [&](int j) {  // row j of the token
-        const bool is_v = j >= a.heads;
-        return (is_v ? a.v + n * a.v_stride : a.k + n * a.k_stride) + (is_v ? j - a.heads : j) * D + col;
-      };
-      auto cached = [&](int j) {  // its row in the cache
-        return (at.page * a.heads + (j >= a.heads ? j - a.heads : j)) << a.table.page_shift | at.row;
-      };
+    for (int b = part; b < 2 * batches; b += parts) {
+      const bool is_v = b >= batches;
+      const int h0 = (is_v ? b - batches : b) * kBatch + group;  // this lane's first head
+      __nv_bfloat16* packed = (is_v ? a.v + n * a.v_stride : a.k + n * a.k_stride) + h0 * D + col;
+      const size_t first = at.row + (static_cast<size_t>(h0) << shift);  // its row in the cache
+      uint8_t* cache = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + (first * D + col) * (kE4m3 ? 1 : 2);
+      uint8_t* scale = kE4m3 ? (is_v ? a.v_scale : a.k_scale) + first : nullptr;
+      const size_t step = static_cast<size_t>(kGroups) << shift;  // rows to the lane's next head
+      uint4 in[kRowsAhead];
+      uint32_t byte[kRowsAhead];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int j = j0 + u * kGroups + group;
+      for (int u = 0; u < kRowsAhead; ++u) {
         in[u] = make_uint4(0u, 0u, 0u, 0u);
         byte[u] = 127u;
-        if (j >= rows) continue;
+        if (h0 + u * kGroups >= a.heads) continue;
         if (kWrite) {
-          in[u] = __ldcs(reinterpret_cast<const uint4*>(packed(j)));
+          in[u] = __ldcs(reinterpret_cast<const uint4*>(packed + u * kGroups * D));
         } else if (kE4m3) {
-          const size_t c = cached(j);
-          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(j >= a.heads ? a.v_cache : a.k_cache) +
-                                                          c * D + col);
+          const uint2 w = *reinterpret_cast<const uint2*>(cache + u * step * D);
           in[u].x = w.x;
           in[u].y = w.y;
-          byte[u] = (j >= a.heads ? a.v_scale : a.k_scale)[c];
+          byte[u] = scale[u * step];
         } else {
-          in[u] = *reinterpret_cast<const uint4*>(
-              static_cast<const __nv_bfloat16*>(j >= a.heads ? a.v_cache : a.k_cache) + cached(j) * D + col);
+          in[u] = *reinterpret_cast<const uint4*>(cache + u * step * D * 2);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int j = j0 + u * kGroups + group;
-        if (j0 + u * kGroups >= rows) break;  // the whole warp
-        if (!kE4m3) {
-          if (j >= rows) continue;
-          if (kWrite)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(j >= a.heads ? a.v_cache : a.k_cache) + cached(j) * D +
-                                      col) = in[u];
-          else
-            __stcs(reinterpret_cast<uint4*>(packed(j)), in[u]);
-          continue;
-        }
+      for (int u = 0; u < kRowsAhead; ++u) {
+        const bool here = h0 + u * kGroups < a.heads;
+        if (h0 - group + u * kGroups >= a.heads) break;  // the whole warp
         const uint32_t w[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
-        if (kWrite) {
-          float x[8];
-          uint32_t most = 0u;  // the largest magnitude's bits: their order is the values', NaN above all
+        if (!kE4m3) {
+          if (!here) continue;
+          if (kWrite)
+            *reinterpret_cast<uint4*>(cache + u * step * D * 2) = in[u];
+          else
+            __stcs(reinterpret_cast<uint4*>(packed + u * kGroups * D), in[u]);
+        } else if (kWrite) {
+          // the largest magnitude's bits, of evens and odds at once: their order is the values', NaN above all
+          uint32_t most = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                    max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) most = max_u16x2(most, __shfl_xor_sync(0xffffffffu, most, o));
+          most = max(most & 0xffffu, most >> 16);
+          // 1.m * 2^(b - 127) <= 448 * 2^e = 1.75 * 2^(8 + e)
+          const int e = min(max(static_cast<int>(most >> 7) - 127 - 8 + ((most & 0x7fu) > 0x60u ? 1 : 0), kScaleMin),
+                            kScaleMax);
+          const float2 inv = make_float2(scale_of(127 - e), scale_of(127 - e));
+          uint32_t q[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            most = max(most, max(w[i] << 16 & 0x7fffffffu, w[i] & 0x7fff0000u));
+            const float2 x = fmul2(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), inv);
+            q[i] = e4m3x2_pack(x.x, x.y);
           }
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-          // most = 1.m * 2^(b - 127) <= 448 * 2^e = 1.75 * 2^(8 + e)
-          const int b = static_cast<int>(most >> 23);
-          const int e = min(max(b - 127 - 8 + ((most & 0x7fffffu) > 0x600000u ? 1 : 0), kScaleMin), kScaleMax);
-          const float inv = scale_of(127 - e);
-          uint2 q;
-          q.x = e4m3x2_pack(x[0] * inv, x[1] * inv) | e4m3x2_pack(x[2] * inv, x[3] * inv) << 16;
-          q.y = e4m3x2_pack(x[4] * inv, x[5] * inv) | e4m3x2_pack(x[6] * inv, x[7] * inv) << 16;
-          if (j >= rows) continue;
-          const size_t c = cached(j);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(j >= a.heads ? a.v_cache : a.k_cache) + c * D + col) = q;
-          if (col == 0) (j >= a.heads ? a.v_scale : a.k_scale)[c] = static_cast<uint8_t>(most > 0x7f800000u ? kScaleNan : e + 127);
+          if (!here) continue;
+          *reinterpret_cast<uint2*>(cache + u * step * D) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+          if (col == 0) scale[u * step] = static_cast<uint8_t>(most > 0x7f80u ? kScaleNan : e + 127);
         } else {
-          if (j >= rows) continue;
+          if (!here) continue;
           const float s = scale_of(byte[u]);
           uint32_t r[4];
 #pragma unroll
@@ -151,23 +148,27 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv_cache_kernel(const __grid_
             const float2 f = e4m3x2_floats(w[i / 2] >> (16 * (i & 1)) & 0xffffu);
             r[i] = pack_bf16x2(f.x * s, f.y * s);
           }
-          __stcs(reinterpret_cast<uint4*>(packed(j)), make_uint4(r[0], r[1], r[2], r[3]));
+          __stcs(reinterpret_cast<uint4*>(packed + u * kGroups * D), make_uint4(r[0], r[1], r[2], r[3]));
         }
       }
     }
   }
 }
 
-template <int D, bool kE4m3>
-cudaError_t launch(const KvCacheArgs& a, bool write, int sms, cudaStream_t stream) {
-  constexpr int kBatch = 32 / (D / 8) * kUnroll;
+template <int D, bool kE4m3, bool kWrite>
+cudaError_t launch(const KvCacheArgs& a, int sms, cudaStream_t stream) {
+  constexpr int kBatch = 32 / (D / 8) * kRowsAhead;
   const int64_t n = a.capacity, warps = static_cast<int64_t>(sms) * kCtas * kWarps;
-  const int64_t most = (2 * a.heads + kBatch - 1) / kBatch, want = (warps + n - 1) / n;
+  const int64_t most = 2 * ((a.heads + kBatch - 1) / kBatch), want = (warps + n - 1) / n;
   const int parts = static_cast<int>(want < most ? want : most);
   const int64_t need = (n * parts + kWarps - 1) / kWarps;
   const int grid = static_cast<int>(need < sms * kCtas ? need : sms * kCtas);
-  return launch_programmatic(write ? kv_cache_kernel<D, kE4m3, true> : kv_cache_kernel<D, kE4m3, false>, dim3(grid),
-                             dim3(kThreads), 0, stream, a, parts);
+  return launch_programmatic(kv_cache_kernel<D, kE4m3, kWrite>, dim3(grid), dim3(kThreads), 0, stream, a, parts);
+}
+
+template <int D, bool kE4m3>
+cudaError_t launch(const KvCacheArgs& a, bool write, int sms, cudaStream_t stream) {
+  return write ? launch<D, kE4m3, true>(a, sms, stream) : launch<D, kE4m3, false>(a, sms, stream);
 }
 
 }  // namespace

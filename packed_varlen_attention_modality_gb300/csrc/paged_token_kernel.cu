@@ -1,20 +1,20 @@
 // Attention over a paged cache for a few rows per segment (the single tokens of running streams): every key
 // row is read once and meets at most 16 query rows, so the call is bound by reading K and V.
 //
-// Work is laid out in units of 64 keys of a (segment, key head) and dealt to two CTAs an SM in equal shares, so
+// Work is laid out in units of 64 keys (e4m3: 128, or 256 of 64 values) of a (segment, key head) and dealt to two CTAs an SM in equal shares, so
 // streams of unlike lengths keep the GPU even; every CTA finds its share by a scan of the lengths.  A pair that a
 // share's end cuts leaves fp32 partial results (O normalised by its own sum, and the LSE), which a second kernel
 // joins in order.  The 16 rows of the tensor-core tile are the segment's rows times the query heads that share
-// the key head, so shared heads cost no second read.  Each of a CTA's four warps streams 16-key blocks of K and V
-// through its own ring in shared memory (16-byte asynchronous copies, the next piece's blocks included), computes
+// the key head, so shared heads cost no second read.  Each of a CTA's four warps streams blocks of 16 (32, 64) keys of K
+// and V through its own ring in shared memory (16-byte asynchronous copies, the next piece's blocks included), computes
 // S = Q K^T and O += P V with 16 x 8 x 16 matrix instructions, and keeps a running max and sum; the warps are
-// added in order at the end of a piece.  A block lies in one page, whose id is looked up a block ahead.
+// added in order at the end of a piece.  16 keys lie in one page, whose id is looked up a block ahead.
 //
 // An e4m3 block becomes f16 in registers, one instruction for two values, and exactly: the rows' scales go to the
 // scores and the weights, which are fp32.  Q's rows are brought to f16 by a power of two each (their largest value to
 // 2^14: what that rounds is 2^-39 of it at most).  The weights of V's rows are 2^(score + V's exponent), kept
-// under 2^8 by a reference of their own that follows their largest, so that f16 rounds each by 2^-11 and drops
-// what is under 2^-33 of the largest.  The order of the dims in S's product and in O's columns is chosen so that a
+// under 2^8 by a reference of their own that follows their largest, so that f16 rounds each by 2^-11 of itself (2^-25
+// of the reference below 2^-14 of it; bf16 rounds by 2^-8).  The order of the dims in S's product and in O's columns is chosen so that a
 // lane's bytes lie together.
 // Scores, max, sum and O are fp32; P is rounded to bf16 (f16) for the product with V, o once at the end.
 #include <cuda_bf16.h>
@@ -29,8 +29,6 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRows = 16;    // query rows of a CTA
-constexpr int kBlock = 16;   // keys of a block
-constexpr int kUnit = kBlock * kWarps;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinShare = 2;   // units
 constexpr int kMaxPieces = 16;  // looked up at once
@@ -38,10 +36,15 @@ static_assert(kRows == kPagedTokenRows, "host and device agree");
 
 template <int D, bool kE4m3>
 struct Cfg {
+  // Keys of a block: steps of 16.  An e4m3 block is bound by its instructions, and look-ups, maxima and exchanges
+  // cost the same for each (64 streams of 20,000 tokens x 8 heads x 64: 280 us at 4 steps, 319 at 2; 2 streams of
+  // 95,000 x 8 x 128: 85 us at 2, 96 at 1).  Three stages do for all: bf16 reads at the rate of a plain copy.
+  static constexpr int kSteps = kE4m3 ? 256 / D : 1, kBlock = 16 * kSteps;
+  static constexpr int kUnit = kBlock * kWarps;
   static constexpr int kRowBytes = kE4m3 ? D : 2 * D;
   static constexpr int kHalf = kBlock * kRowBytes;                          // K's part of a stage
   static constexpr int kStageBytes = 2 * kHalf + (kE4m3 ? 2 * kBlock : 0);  // K, V, their scales
-  static constexpr int kStages = kE4m3 ? (D == 128 ? 6 : 8) : (D == 128 ? 3 : 6);
+  static constexpr int kStages = 3;
   static constexpr int kOut = D + 8;  // floats of a row while the warps are added (the pad keeps banks apart)
   static constexpr int kSmemBytes = kWarps * kStages * kStageBytes + kRows * kOut * 4;
   // where a 16-byte piece of a row lies: as the reads below meet no bank twice
@@ -95,6 +98,7 @@ struct Piece {
 };
 
 // Units of a pair.
+template <int kUnit>
 __device__ __forceinline__ int units_of(const PagedSegment& s, int block) {
   const int keys = s.rows == 0 ? 0 : row_limit(s, s.rows - 1, block);
   return s.rows == 0 ? 0 : keys <= kUnit ? 1 : (keys + kUnit - 1) / kUnit;
@@ -137,7 +141,7 @@ template <int D, bool kE4m3>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
   using C = Cfg<D, kE4m3>;
-  constexpr int kStages = C::kStages;
+  constexpr int kStages = C::kStages, kSteps = C::kSteps, kBlock = C::kBlock, kUnit = C::kUnit;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Scan scan;
   __shared__ Piece pieces[kMaxPieces];
@@ -155,7 +159,7 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
   auto scan_tile = [&](int g0, uint64_t base, unsigned int* err) {  // returns the units up to the tile's end
     PagedSegment s{0, 0, 0};
     if (g0 + tid < S) s = checked_paged_segment(a.seg, g0 + tid, err);
-    const uint64_t n = static_cast<uint64_t>(units_of(s, block)) * heads;
+    const uint64_t n = static_cast<uint64_t>(units_of<kUnit>(s, block)) * heads;
     uint64_t total;
     const uint64_t at = block_scan(n, scan.warp, &total);
     scan.seg[tid] = s;
@@ -200,7 +204,7 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         Piece p;
         p.s = scan.seg[lo];
         p.g = tile + lo;
-        const int units = units_of(p.s, block);
+        const int units = units_of<kUnit>(p.s, block);
         const uint64_t in = at - scan.before[lo];
         p.head = static_cast<int>(in / units);
         const int u0 = static_cast<int>(in % units);
@@ -235,38 +239,52 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         c.blocks = c.piece < num_pieces ? blocks_of(c.piece) : 0;
       }
     };
-    auto lookup = [&](const Cursor& c) {
-      if (c.piece >= num_pieces) return 0;
-      const Piece& p = pieces[c.piece];
-      return page_id(a.seg.table, p.g, (p.first + c.b * kBlock) >> a.seg.table.page_shift);
+    const int shift = a.seg.table.page_shift;
+    struct Ids {
+      int id[kSteps];  // pages of a block's steps
     };
-    auto load = [&](const Cursor& c, int id, int stage) {
+    auto lookup = [&](const Cursor& c) {
+      Ids r{};
+      if (c.piece >= num_pieces) return r;
+      const Piece& p = pieces[c.piece];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int key = p.first + c.b * kBlock + 16 * i;
+        if (key < p.end) r.id[i] = page_id(a.seg.table, p.g, key >> shift);
+      }
+      return r;
+    };
+    auto load = [&](const Cursor& c, const Ids& ids, int stage) {
       if (c.piece >= num_pieces) return;
       const Piece& p = pieces[c.piece];
-      if (!page_ok(a.seg.table, id)) {
-        if (lane == 0) record_error(a.err, kErrBadPage);
-        id = 0;
-      }
-      const int key = p.first + c.b * kBlock, left = p.end - key;
-      const int shift = a.seg.table.page_shift;
-      const size_t row = ((static_cast<size_t>(id) * heads + p.head) << shift) + (key & ((1 << shift) - 1));
       const uint32_t dst = ring32 + stage * C::kStageBytes;
-      constexpr int kPieces = C::kRowBytes / 16;
-      const uint8_t* kp = static_cast<const uint8_t*>(a.k) + row * C::kRowBytes;
-      const uint8_t* vp = static_cast<const uint8_t*>(a.v) + row * C::kRowBytes;
 #pragma unroll
-      for (int i = lane; i < kBlock * kPieces; i += 32) {  // a block's rows lie back to back; zeros past the end
-        const int r = i / kPieces;
-        const uint32_t bytes = r < left ? 16u : 0u, off = C::piece_at(r, i % kPieces);
-        cp_async16(dst + off, kp + i * 16, bytes);
-        cp_async16(dst + C::kHalf + off, vp + i * 16, bytes);
+      for (int step = 0; step < kSteps; ++step) {
+        int id = ids.id[step];
+        if (!page_ok(a.seg.table, id)) {
+          if (lane == 0) record_error(a.err, kErrBadPage);
+          id = 0;
+        }
+        const int key = p.first + c.b * kBlock + 16 * step, left = p.end - key;
+        const size_t row = ((static_cast<size_t>(id) * heads + p.head) << shift) + (key & ((1 << shift) - 1));
+        constexpr int kPieces = C::kRowBytes / 16;
+        const uint8_t* kp = static_cast<const uint8_t*>(a.k) + row * C::kRowBytes;
+        const uint8_t* vp = static_cast<const uint8_t*>(a.v) + row * C::kRowBytes;
+#pragma unroll
+        for (int i = lane; i < 16 * kPieces; i += 32) {  // a step's rows lie back to back; zeros past the end
+          const int r = i / kPieces;
+          const uint32_t bytes = r < left ? 16u : 0u, off = C::piece_at(16 * step + r, i % kPieces);
+          cp_async16(dst + off, kp + i * 16, bytes);
+          cp_async16(dst + C::kHalf + off, vp + i * 16, bytes);
+        }
+        if (kE4m3 && lane < 2 && left > 0)
+          cp_async16(dst + 2 * C::kHalf + lane * kBlock + 16 * step, (lane == 0 ? a.k_scale : a.v_scale) + row, 16);
       }
-      if (kE4m3 && lane < 2)
-        cp_async16(dst + 2 * C::kHalf + lane * kBlock, (lane == 0 ? a.k_scale : a.v_scale) + row, 16);
     };
     Cursor ahead{0, warp, blocks_of(0)};
     settle(ahead);
-    int stage = 0, id = lookup(ahead);
+    int stage = 0;
+    Ids id = lookup(ahead);
 #pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) {
       load(ahead, id, i);
@@ -352,18 +370,21 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         const uint8_t* base = ring + stage * C::kStageBytes;
         const int key = p.first + b * kBlock;
         const int mat = lane >> 3, mr = lane & 7;
-        float sc[2][4] = {};
-        if (!kE4m3) {
+        float sc[2 * kSteps][4] = {};
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t f[4];  // keys 0-7: dims 0-7, 8-15 of the step; keys 8-15 the same
-            ldmatrix4(f, kb + C::piece_at((mat >> 1) * 8 + mr, 2 * kk + (mat & 1)));
-            mma_16816(sc[0], q[kk], f[0], f[1]);
-            mma_16816(sc[1], q[kk], f[2], f[3]);
+        for (int step = 0; step < kSteps; ++step) {
+          if (!kE4m3) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              uint32_t f[4];  // keys 0-7: dims 0-7, 8-15 of the step; keys 8-15 the same
+              ldmatrix4(f, kb + C::piece_at(16 * step + (mat >> 1) * 8 + mr, 2 * kk + (mat & 1)));
+              mma_16816(sc[2 * step], q[kk], f[0], f[1]);
+              mma_16816(sc[2 * step + 1], q[kk], f[2], f[3]);
+            }
+            continue;
           }
-        } else {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 2 * step; n < 2 * step + 2; ++n) {
             const int row = n * 8 + gr;
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
@@ -382,17 +403,17 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         }
         if (key + kBlock > low) {  // by select, so NaN/Inf there is discarded
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2 * kSteps; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               if (key + n * 8 + c2 + (i & 1) >= min(limit[i >> 1], p.end)) sc[n][i] = -INFINITY;
         }
         // e4m3: the log2 of V's rows' weights, score and V's exponent together (a masked key's stays -inf: past the end
         // lie rows whose scale may be anything)
-        float u[2][4];
+        float u[2 * kSteps][4];
         if (kE4m3) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < 2 * kSteps; ++n) {
             const uint32_t vs = *reinterpret_cast<const uint16_t*>(base + 2 * C::kHalf + kBlock + n * 8 + c2);
             const float v0 = scale_log2_of(vs & 0xffu), v1 = scale_log2_of(vs >> 8);
 #pragma unroll
@@ -401,8 +422,10 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
           }
         }
         // row maxima over the quad; a reference moves only when it grows by more than 2^8
-        auto row_max = [&](const float (&x)[2][4], int h) {
-          float y = fmaxf(fmaxf(x[0][2 * h], x[0][2 * h + 1]), fmaxf(x[1][2 * h], x[1][2 * h + 1]));
+        auto row_max = [&](const float (&x)[2 * kSteps][4], int h) {
+          float y = fmaxf(x[0][2 * h], x[0][2 * h + 1]);
+#pragma unroll
+          for (int n = 1; n < 2 * kSteps; ++n) y = fmax3(y, x[n][2 * h], x[n][2 * h + 1]);
           y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
           return fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
         };
@@ -435,37 +458,41 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n][i] *= alpha[i >> 1];
         }
-        uint32_t pw[4];
+        uint32_t pw[kSteps][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2 * kSteps; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            uint32_t& w = pw[n / 2][2 * (n & 1) + h];
             const float mb = m[h] == -INFINITY ? 0.f : m[h] * scale_log2;
             const float e0 = ex2_approx(fmaf(sc[n][2 * h], scale_log2, -mb));
             const float e1 = ex2_approx(fmaf(sc[n][2 * h + 1], scale_log2, -mb));
             l[h] += e0 + e1;
             if (kE4m3) {
               const float wb = top_w[h] == -INFINITY ? 0.f : top_w[h];
-              pw[2 * n + h] = pack_f16x2(ex2_approx(u[n][2 * h] - wb), ex2_approx(u[n][2 * h + 1] - wb));
+              w = pack_f16x2(ex2_approx(u[n][2 * h] - wb), ex2_approx(u[n][2 * h + 1] - wb));
             } else {
-              pw[2 * n + h] = pack_bf16x2(e0, e1);
+              w = pack_bf16x2(e0, e1);
             }
           }
-        if (!kE4m3) {
 #pragma unroll
-          for (int n = 0; n < D / 16; ++n) {
-            uint32_t f[4];  // dims 0-7 of the step: keys 0-7, 8-15; dims 8-15 the same
-            ldmatrix4_trans(f, vb + C::piece_at((mat & 1) * 8 + mr, 2 * n + (mat >> 1)));
-            mma_16816(o[2 * n], pw, f[0], f[1]);
-            mma_16816(o[2 * n + 1], pw, f[2], f[3]);
+        for (int step = 0; step < kSteps; ++step) {
+          if (!kE4m3) {
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+              uint32_t f[4];  // dims 0-7 of the step: keys 0-7, 8-15; dims 8-15 the same
+              ldmatrix4_trans(f, vb + C::piece_at(16 * step + (mat & 1) * 8 + mr, 2 * n + (mat >> 1)));
+              mma_16816(o[2 * n], pw[step], f[0], f[1]);
+              mma_16816(o[2 * n + 1], pw[step], f[2], f[3]);
+            }
+            continue;
           }
-        } else {
           // column gr of tile j is dim gr * D / 8 + j: the lane's dims of a key are D / 8 bytes in a row
           const uint8_t* vbase = base + C::kHalf;
           uint32_t w[4][D / 32];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int row = c2 + (k & 1) + 8 * (k >> 1);
+            const int row = 16 * step + c2 + (k & 1) + 8 * (k >> 1);
             if (D == 128) {
               const uint4 x = *reinterpret_cast<const uint4*>(vbase + C::piece_at(row, gr));
               w[k][0] = x.x;
@@ -482,8 +509,8 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
           for (int j = 0; j < D / 8; j += 2) {  // bytes j and j + 1 of two keys each, in one word
             const uint32_t pick = j % 4 == 0 ? 0x5140 : 0x7362;
             const uint32_t lo = __byte_perm(w[0][j / 4], w[1][j / 4], pick), hi = __byte_perm(w[2][j / 4], w[3][j / 4], pick);
-            mma_16816_f16(o[j], pw, e4m3_pair_f16<0>(lo), e4m3_pair_f16<0>(hi));
-            mma_16816_f16(o[j + 1], pw, e4m3_pair_f16<1>(lo), e4m3_pair_f16<1>(hi));
+            mma_16816_f16(o[j], pw[step], e4m3_pair_f16<0>(lo), e4m3_pair_f16<0>(hi));
+            mma_16816_f16(o[j + 1], pw[step], e4m3_pair_f16<1>(lo), e4m3_pair_f16<1>(hi));
           }
         }
         __syncwarp();  // the stage is read: it may be loaded again

@@ -8,6 +8,9 @@ fp32 terms: the score's error (D products, 2^-24 each of |q||k|, and the exponen
 by under 1e-4 of itself at the scores used here: 2e-4 sum_j P_j |v_j|.
 A weight under 2^-126 of its row's largest is 0 (the exponential flushes it), which is an absolute error of
 2^-126 |v_j| for each key: it shows where every larger weight meets a value of exactly 0, as in e4m3.
+The token form of an e4m3 cache rounds the weights times V's scales, 2^(e_j) P_j, to f16 over a reference that is at
+most their largest: by 2^-11 of each or, below 2^-14 of the reference, by 2^-25 of the reference.  The first is inside
+2^-8 of each; the second adds 2^-25 max_j(2^(e_j)) sum_j |q_j|, with v_j = 2^(e_j) q_j and P_j <= 1.
 lse: the same error of the scores, absolute: 1e-4 * max(|lse|, 1) as elsewhere in this suite.
 """
 import numpy as np
@@ -131,6 +134,7 @@ class Case:
         ids = rng.permutation(pages)
         self.table = np.full((len(lk), max(counts) + 1), -5, dtype=np.int32)
         self.rows, self.cache = {"k": [], "v": []}, {}
+        self.scales = []  # of V, e4m3: exponents [n, hk] of each segment
         for name in "kv":
             kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
             store = torch.full((pages, hk, page, d), 448.0 if e4m3 else float("nan")).to(kind)
@@ -144,6 +148,8 @@ class Case:
                 if e4m3:
                     x = x.float() * torch.from_numpy(np.exp(rng.standard_normal((n, hk, 1)))).float()  # rows of unlike sizes
                     e = oracle.e4m3_scale(x) if n else np.zeros((0, hk), int)
+                    if name == "v":
+                        self.scales.append(e)
                     values = oracle.e4m3_round(_f64(x) / np.ldexp(1.0, e)[..., None])
                     self.rows[name].append(values * np.ldexp(1.0, e)[..., None])
                     put, es = torch.from_numpy(values).float().to(kind), torch.from_numpy(e + 127).to(torch.uint8)
@@ -178,6 +184,12 @@ class Case:
         off = np.abs(got - ref)
         most = max([np.abs(v).sum(0).max() for v in self.rows["v"] if len(v)], default=0.0)
         tol = (HALF + 2e-4) * size + HALF * np.abs(ref) + 2.0 ** -126 * most
+        if self.e4m3 and self.max_q * self.hq // self.rows["k"][0].shape[1] <= 16:
+            for g, e in enumerate(self.scales):
+                if e.size:
+                    q = np.abs(self.rows["v"][g]) / np.ldexp(1.0, e)[..., None]
+                    more = 2.0 ** -25 * np.ldexp(1.0, e.max(0))[:, None] * q.sum(0)  # [hk, d]
+                    tol[self.cu[g]:self.cu[g + 1]] += np.repeat(more, self.hq // e.shape[1], axis=0)
         assert np.all(off <= tol), (off - tol).max()
         if lse is not None:
             gl = _f64(lse[:, :n])
