@@ -494,8 +494,21 @@ class ResidualNormGrads(NamedTuple):
     gate: Optional[torch.Tensor]
 
 
+def _like(t: torch.Tensor, dtype) -> torch.Tensor:
+    """A new contiguous tensor of t's shape (empty_like is the cheaper call where it serves)."""
+    if t.dtype is dtype and t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty(t.shape, dtype=dtype, device=t.device)
+
+
 def _matrix(t: torch.Tensor, name: str, dtype, device: torch.device, shape=None) -> int:
     """Check [rows, dim] with contiguous rows; returns the row stride in elements, 0 when contiguous."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape:
+        if t.is_contiguous():  # the common cases first
+            return 0
+        sr, sc = t.stride()
+        if sc == 1 and sr >= shape[1] and shape[0] > 1:
+            return sr
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -605,12 +618,12 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, norm: Optio
             raise ValueError("x_out needs y: without it the stream stays x")
         x_out = x
     elif x_out is None:
-        x_out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        x_out = _like(x, x.dtype)
     else:
         x_out_stride = _matrix(x_out, "x_out", x.dtype, dev, x.shape)
     if sizes[3]:
         if h_out is None:
-            h = torch.empty(x.shape, dtype=_BF16, device=dev)
+            h = _like(x if y is None or x.dtype is _BF16 else y, _BF16)
         else:
             h, h_stride = h_out, _matrix(h_out, "h_out", _BF16, dev, x.shape)
     elif h_out is not None:
@@ -656,14 +669,14 @@ def residual_norm_bwd(dx_out: Optional[torch.Tensor], dh: Optional[torch.Tensor]
     elif dh is not None:
         raise ValueError('dh needs a norm')
     if dx is None:
-        dx = torch.empty(shape, dtype=x_out.dtype, device=dev)
+        dx = _like(x_out, x_out.dtype)
     else:
         dx_stride = _matrix(dx, "dx", x_out.dtype, dev, shape)
     if not has_y:
         if dy is not None:
             raise ValueError("dy needs y")
     elif dy is None:
-        dy = torch.empty(shape, dtype=_BF16, device=dev)
+        dy = _like(y, _BF16)
     else:
         dy_stride = _matrix(dy, "dy", _BF16, dev, shape)
     requests, dim = sizes[2], sizes[1]
@@ -816,7 +829,7 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     if dim != D:
         raise ValueError("the cache must have q's head_dim")
     if out is None:
-        out = torch.empty(q.shape, dtype=_BF16, device=dev)
+        out = _like(q, _BF16)
     else:
         _require(out, "out", _BF16, dev)
         if out.shape != q.shape:

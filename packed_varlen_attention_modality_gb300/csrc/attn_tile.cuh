@@ -8,6 +8,7 @@
 //   Work: an item -- ntiles (0: no more work), q0[2] (first row of each tile), seg_end, q_head(t), nkv and last_keys
 //     (key tiles, and keys in the last of them; 0 for none), partial (entry whose partial results the item
 //     writes, -1 for o itself)
+//   Entry: an entry of the last wave, with chunks (1: a whole item)
 //   whole_item(k): a CTA's k-th whole item;  decode(item, ws, split_area): its Work;  place(entry, t): a tile's place
 //   row(r): token and head of a tile's row r;  row_keys(work, t, row): keys it sees from the item's first one on
 //   Fetch: the key/value producer's state;  convert_row: a row of bytes into a bf16 tile
@@ -34,19 +35,15 @@ __host__ __device__ constexpr int key_tiles(int keys) {
   return keys > 0 ? (keys + kBlockN - 1) / kBlockN : 1;
 }
 
-// A chunk of the last wave (or a whole item of it): key tiles [kv0, kv1) of a segment's item.
-struct TileEntry {
-  int segment, kv_head, pair, kv0, kv1;
-  int first;          // the item's first entry
-  int chunk, chunks;  // chunks == 1: whole
-};
-static_assert(sizeof(TileEntry) == 8 * sizeof(int32_t), "entries are 8 words");
-// first entries of the cut items (fewer than a wave), then the first entry of each CTA and their number
+// The split area: entries (a chunk of the last wave, or a whole item of it), then the first entries of the cut items
+// (fewer than a wave), the first entry of each CTA and their number, then the partial results.
+template <typename Entry>
 __host__ __device__ constexpr size_t split_items_offset() {
-  return static_cast<size_t>(kSplitMaxEntries) * sizeof(TileEntry);
+  return static_cast<size_t>(kSplitMaxEntries) * sizeof(Entry);
 }
+template <typename Entry>
 __host__ __device__ constexpr size_t split_partials_offset() {
-  return split_items_offset() + static_cast<size_t>(kSplitMaxEntries) * sizeof(uint32_t);
+  return split_items_offset<Entry>() + static_cast<size_t>(kSplitMaxEntries) * sizeof(uint32_t);
 }
 template <int D>
 constexpr size_t kPartial = static_cast<size_t>(kBlockM) * (D + 1);  // floats of a tile's partial
@@ -108,6 +105,7 @@ attn_tile_kernel(const __grid_constant__ Source src, __nv_bfloat16* __restrict__
                  unsigned int* err, unsigned long long wait_ns, unsigned int stall_after) {
   using C = TileCfg<Source>;
   using Work = typename Source::Work;
+  using Entry = typename Source::Entry;
   constexpr int D = Source::kDim;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -154,21 +152,7 @@ attn_tile_kernel(const __grid_constant__ Source src, __nv_bfloat16* __restrict__
     if (lane == 0) mbar_arrive(b);
   };
 
-  grid_dependency_wait();
-  launch_dependents();
-  // a timeout recorded earlier and not read yet: leave at once, all threads together
-  if (__syncthreads_or(err != nullptr && *reinterpret_cast<volatile unsigned int*>(err) == kErrTimeout))
-    return;
-  // this CTA's items: every gridDim.x-th of the whole ones, then its entries of the last wave
-  const uint32_t whole = ws[2];  // of all CTAs
-  uint32_t entry = 0, entry_end = 0;
-  if (ws[3] > 0) {
-    const uint32_t* firsts = reinterpret_cast<const uint32_t*>(split_area + split_items_offset()) + gridDim.x;
-    entry = firsts[blockIdx.x];
-    entry_end = firsts[blockIdx.x + 1];
-  }
-  if (blockIdx.x >= whole && entry == entry_end) return;
-
+  // set up while the plan is made: nothing of it is read before the wait
   if (warp == 12 && lane == 0) {
     tma_prefetch_desc(&src.tmap_q);
     tma_prefetch_desc(&src.tmap_k);
@@ -206,6 +190,22 @@ attn_tile_kernel(const __grid_constant__ Source src, __nv_bfloat16* __restrict__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  launch_dependents();
+  // this CTA's items: every gridDim.x-th of the whole ones, then its entries of the last wave
+  const uint32_t whole = ws[2];  // of all CTAs
+  uint32_t entry = 0, entry_end = 0;
+  if (ws[3] > 0) {
+    const uint32_t* firsts = reinterpret_cast<const uint32_t*>(split_area + split_items_offset<Entry>()) + gridDim.x;
+    entry = firsts[blockIdx.x];
+    entry_end = firsts[blockIdx.x + 1];
+  }
+  // nothing to do, or a timeout recorded earlier and not read yet: leave at once, all threads together
+  const bool late = err != nullptr && *reinterpret_cast<volatile unsigned int*>(err) == kErrTimeout;
+  if (__syncthreads_or(late) || (blockIdx.x >= whole && entry == entry_end)) {
+    if (warp == 13) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
 
   // Item k from the ring, for one warp (every lane calls).  False when the wait ran out.
   auto take = [&](int k, Work& d) {
@@ -537,7 +537,7 @@ attn_tile_kernel(const __grid_constant__ Source src, __nv_bfloat16* __restrict__
       const float inv_l = s_norm[t * kBlockM + row];
       const uint32_t o_addr = tmem + lane_base + kColO + 128 * t;
       if (d.partial >= 0) {
-        float* mine = reinterpret_cast<float*>(split_area + split_partials_offset()) +
+        float* mine = reinterpret_cast<float*>(split_area + split_partials_offset<Entry>()) +
                       (static_cast<size_t>(d.partial) * 2 + t) * kPartial<D> + static_cast<size_t>(row) * D;
         const bool sectors = (reinterpret_cast<uintptr_t>(mine) & 31u) == 0;
 #pragma unroll 1
@@ -752,7 +752,7 @@ attn_tile_kernel(const __grid_constant__ Source src, __nv_bfloat16* __restrict__
       const float lse_row = m_used * scale + logf(l);  // -inf without keys
       const int q_row = d.q0[t] + mine.token;
       if (d.partial >= 0)
-        (reinterpret_cast<float*>(split_area + split_partials_offset()) +
+        (reinterpret_cast<float*>(split_area + split_partials_offset<Entry>()) +
          (static_cast<size_t>(d.partial) * 2 + t) * kPartial<D>)[static_cast<size_t>(kBlockM) * D + row] = lse_row;
       else if (lse != nullptr && q_row < d.seg_end)
         lse[static_cast<size_t>(d.q_head(t) + mine.head) * src.seg.capacity_q + q_row] = lse_row;
@@ -780,19 +780,20 @@ attn_tile_merge_kernel(const uint32_t* __restrict__ ws, const uint8_t* __restric
                        __nv_bfloat16* __restrict__ out, float* __restrict__ lse, const __grid_constant__ Source src,
                        const unsigned int* err) {
   constexpr int D = Source::kDim;
+  using Entry = typename Source::Entry;
   __shared__ float s_w[kMergeRows][Source::kChunks];
   grid_dependency_wait();
   launch_dependents();
   // after a timeout the partials are incomplete: leave the output as it is
   if (err != nullptr && *reinterpret_cast<const volatile unsigned int*>(err) == kErrTimeout) return;
   const int n_units = static_cast<int>(ws[0]) * kMergeUnits;
-  const uint32_t* items = reinterpret_cast<const uint32_t*>(split_area + split_items_offset());
-  const float* parts = reinterpret_cast<const float*>(split_area + split_partials_offset());
+  const uint32_t* items = reinterpret_cast<const uint32_t*>(split_area + split_items_offset<Entry>());
+  const float* parts = reinterpret_cast<const float*>(split_area + split_partials_offset<Entry>());
   for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
     const int e = static_cast<int>(items[unit / kMergeUnits]);
     const int t = unit % kMergeUnits / (kBlockM / kMergeRows);
     const int r0 = unit % (kBlockM / kMergeRows) * kMergeRows;
-    const TileEntry en = reinterpret_cast<const TileEntry*>(split_area)[e];
+    const Entry en = reinterpret_cast<const Entry*>(split_area)[e];
     const TilePlace at = src.place(en, t);
     if (!at.exists || at.q0 + src.row(r0).token >= at.seg_end) continue;  // the whole CTA
     auto inside = [&](int r) { return at.q0 + src.row(r0 + r).token < at.seg_end; };

@@ -72,6 +72,14 @@ constexpr int kSplitMinTiles = 8;
 constexpr int kSplitMinChunk = 3;
 constexpr int kSplitMaxChunks = 64;
 
+// A chunk of the last wave (or a whole item of it): key tiles [kv0, kv1) of a segment's item.
+struct TileEntry {
+  int segment, kv_head, pair, kv0, kv1;
+  int first;          // the item's first entry
+  int chunk, chunks;  // chunks == 1: whole
+};
+static_assert(sizeof(TileEntry) == 8 * sizeof(int32_t), "entries are 8 words");
+
 // Items of a segment per key head: pairs of its group * ceil(rows / 128) tiles.
 __device__ __forceinline__ int pairs_of(int rows, int group) {
   return ((rows + kBlockM - 1) / kBlockM * group + 1) / 2;
@@ -210,7 +218,7 @@ cross_plan_kernel(const __grid_constant__ CrossSegments seg, uint32_t* __restric
   }
   uint32_t cuts;
   const uint32_t before = block_exclusive_scan(tid < wave && at.y > 0 ? 1u : 0u, s_warp, cuts);
-  uint32_t* listed = reinterpret_cast<uint32_t*>(split_area + split_items_offset());
+  uint32_t* listed = reinterpret_cast<uint32_t*>(split_area + split_items_offset<TileEntry>());
   if (tid < wave) {
     s_at[tid] = make_uint4(at.x, at.y, before, 0u);
     listed[wave + tid] = at.x + before + (at.y > 0 ? 1u : 0u);
@@ -250,6 +258,7 @@ template <int kD>
 struct CrossSource {
   static constexpr int kDim = kD, kChunks = kSplitMaxChunks;
   static constexpr bool kConvert = false, kRowLimits = false;
+  using Entry = TileEntry;
   CUtensorMap tmap_q, tmap_k, tmap_v;
   CrossSegments seg;
 

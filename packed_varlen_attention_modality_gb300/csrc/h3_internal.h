@@ -367,6 +367,28 @@ constexpr size_t paged_token_bytes(int rows, int head_dim) {
 }
 cudaError_t launch_paged_token(const PagedTokenArgs& a, int head_dim, cudaStream_t stream);
 
+// A pair of 128-row query tiles of a segment (an item is a key head of one).
+struct alignas(16) PagedPair {
+  int segment;
+  int q0, seg_end;  // its first row, the segment's last + 1
+  int used, keys;   // tokens of the segment, and those that the pair's last row sees
+  int ntiles;
+  int unused[2];
+};
+__host__ __device__ constexpr int64_t paged_max_pairs(int capacity_q, int num_segments, int tokens) {
+  return static_cast<int64_t>(capacity_q) / (2 * tokens) + num_segments;
+}
+// Workspace: 8 header words, the list of pairs; then, where a segment can be kSplitMinSeqlen tokens, the split area
+// (entries, their lists, partial results as in attn_split_bytes).
+constexpr size_t kPagedEntryBytes = 64;
+constexpr size_t paged_plan_bytes(int capacity_q, int num_segments, int tokens) {
+  return (8 * sizeof(uint32_t) + static_cast<size_t>(paged_max_pairs(capacity_q, num_segments, tokens)) * sizeof(PagedPair) +
+          255) / 256 * 256;
+}
+constexpr size_t paged_split_bytes(int head_dim) {
+  return static_cast<size_t>(kSplitMaxEntries) * (kPagedEntryBytes + sizeof(uint32_t)) +
+         static_cast<size_t>(kSplitMaxEntries) * 2 * 128 * (head_dim + 1) * sizeof(float);
+}
 struct PagedTileArgs {
   CUtensorMap tmap_q;          // {D, H, rows}, a box of a key head's query heads x 128 / their number
   CUtensorMap tmap_k, tmap_v;  // {D, page, pages x heads}, a box of a page (128 rows of it at most)
@@ -376,8 +398,8 @@ struct PagedTileArgs {
   int wide;  // o may be stored in 32-byte pieces
   float* lse;
   float scale;
-  void* workspace;   // attn_plan_bytes(num_segments): the work plan
-  void* split_area;  // attn_split_bytes(head_dim) after it, or null (no item is cut)
+  void* workspace;   // paged_plan_bytes()
+  void* split_area;  // paged_split_bytes(head_dim) after it, or null (no item is cut)
   unsigned int* err;
   uint64_t wait_limit_ns;
   uint32_t stall_after_tiles;

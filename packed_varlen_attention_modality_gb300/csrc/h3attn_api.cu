@@ -682,7 +682,8 @@ size_t h3_paged_attn_workspace_size(const h3_paged_attn_desc* d) {
   if (d->head_dim != 64 && d->head_dim != 128) return 0;
   if (paged_few_rows(d))
     return h3::paged_token_bytes(d->max_seqlen_q * (d->num_q_heads / d->num_kv_heads), d->head_dim);
-  return h3::attn_workspace_bytes(d->num_segments, d->max_seqlen_k, d->head_dim);
+  return h3::paged_plan_bytes(d->capacity_q, d->num_segments, 128 / (d->num_q_heads / d->num_kv_heads)) +
+         (d->max_seqlen_k >= h3::kSplitMinSeqlen ? h3::paged_split_bytes(d->head_dim) : 0);
 }
 
 h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* d, const void* q, const void* k_cache, const void* v_cache,
@@ -752,7 +753,7 @@ h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* d, const void* q, const vo
   a.scale = scale;
   a.workspace = workspace;
   if (d->max_seqlen_k >= h3::kSplitMinSeqlen)
-    a.split_area = static_cast<uint8_t*>(workspace) + h3::attn_plan_bytes(d->num_segments);
+    a.split_area = static_cast<uint8_t*>(workspace) + h3::paged_plan_bytes(d->capacity_q, d->num_segments, 128 / group);
   a.err = err;
   a.wait_limit_ns = h3::wait_limit_ns();
   a.stall_after_tiles = h3::stall_after_tiles();

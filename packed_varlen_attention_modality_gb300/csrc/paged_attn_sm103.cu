@@ -10,9 +10,9 @@
 // the products and the softmax then are those of a bf16 cache.
 //
 // Causal by blocks of tokens: an item's key tiles end at its last row's limit, a tile in which some row sees less is
-// masked row by row, others are not.  Items of a segment come with the longest first and waves alternate in
-// direction, so the CTAs' sums stay near one another; what a last, partly filled wave and unlike items leave idle
-// is evened out by cutting that wave's items where each CTA's share of the whole ends.
+// masked row by row, others are not.  Items come with the longest first and waves alternate in direction, so the
+// CTAs' sums stay near one another; what a last, partly filled wave and unlike items leave idle is evened out by
+// cutting that wave's items where each CTA's share of the whole ends.
 #include <cuda_bf16.h>
 
 #include "attn_tile.cuh"
@@ -25,7 +25,9 @@ namespace h3 {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kSortMax = 256;  // segments that are ordered by keys, and whose last wave is cut
+constexpr int kSegments = 256;   // whose lengths the plan keeps in shared memory
+constexpr int kSorted = 1024;    // pairs of tiles that are ordered by length (the ordering compares all of them)
+constexpr int kWave = kSplitMaxEntries / 2;  // CTAs, at most
 // In steps of a key tile, as measured for cross attention: an item's start and end, joining chunks; items cut at
 // all, least chunk.
 constexpr uint32_t kCostItem = 2, kCostJoin = 8;
@@ -34,78 +36,140 @@ constexpr int kMaxChunks = 160;  // of an item: one for each CTA
 
 __device__ __forceinline__ int tiles_of(int rows, int tokens) { return (rows + tokens - 1) / tokens; }
 __device__ __forceinline__ int pairs_of(int rows, int tokens) { return (tiles_of(rows, tokens) + 1) / 2; }
-// Keys of a segment's pair of tiles: what its last row sees.
-__device__ __forceinline__ int pair_limit(const PagedSegment& s, int pair, int tokens, int block) {
-  const int64_t end = static_cast<int64_t>(2 * pair + 2) * tokens;
-  return row_limit(s, (end < s.rows ? static_cast<int>(end) : s.rows) - 1, block);
-}
 
 // Whole item k of CTA c of `ctas`: the waves alternate in direction.
 __device__ __forceinline__ uint32_t item_of(uint32_t k, uint32_t c, uint32_t ctas) {
   return k * ctas + (k & 1 ? ctas - 1 - c : c);
 }
 
-// Plan: segment order and item prefix, and the entries of the last wave.  Words of ws: [0] cut items, [1] unused,
-// [2] whole items before the last wave, [3] its entries, then the order [S] and the exclusive prefix [S + 1].
+// A pair of query tiles of a segment, and the keys that its last row sees.  Item i is head i % heads of pair
+// i / heads of the plan's list.
+static_assert(sizeof(PagedPair) == 8 * sizeof(int32_t), "whole vectors");
+__device__ __forceinline__ PagedPair pair_of(const PagedSegment& s, int segment, int pair, int tokens, int block) {
+  const int64_t end = static_cast<int64_t>(2 * pair + 2) * tokens;
+  const int keys = row_limit(s, (end < s.rows ? static_cast<int>(end) : s.rows) - 1, block);
+  return PagedPair{segment, s.q0 + 2 * pair * tokens, s.q0 + s.rows, s.used, keys,
+                   min(2, tiles_of(s.rows, tokens) - 2 * pair), 0, 0};
+}
+struct PagedEntry {
+  PagedPair pair;
+  int kv_head, kv0, kv1;
+  int first;          // the item's first entry
+  int chunk, chunks;  // chunks == 1: whole
+  int unused[2];
+};
+static_assert(sizeof(PagedEntry) <= kPagedEntryBytes, "the host makes room for them");
+
+// Exclusive prefix of v over the block's threads, and the sum.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  T x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  const T mine = lane < warps ? s_warp[lane] : 0;
+  T w = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  return __shfl_sync(0xffffffffu, w - mine, warp) + x - v;
+}
+
+// Plan: the list of pairs, the longest first (up to kSorted of them; else segment by segment), and the entries of the
+// last wave.  Words of ws: [0] cut items, [1] unused, [2] whole items before the last wave, [3] its entries; the list
+// lies behind them.
 __global__ void __launch_bounds__(kPlanThreads)
 paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_t* __restrict__ ws,
-                  uint8_t* __restrict__ split_area, int wave, unsigned int* err) {
-  __shared__ PagedSegment s_seg[kSortMax];
-  __shared__ int s_order[kSortMax];
-  __shared__ uint32_t s_prefix[kSortMax + 1];
-  __shared__ uint32_t s_warp[kPlanThreads / 32];
-  __shared__ uint64_t s_warp64[kPlanThreads / 32];
+                  PagedPair* __restrict__ list, uint8_t* __restrict__ split_area, int wave, unsigned int* err) {
+  __shared__ PagedSegment s_seg[kSegments];
+  __shared__ int s_first[kSegments];  // pairs before a segment's
+  __shared__ __align__(16) uint32_t s_tiles[kSorted];  // key tiles of a pair, by its place in the segments
+  __shared__ uint32_t s_sorted[kSorted];               // the same in the list's order
+  __shared__ uint64_t s_warp64[32];
+  __shared__ uint32_t s_warp[32];
   __shared__ uint32_t s_cut, s_most, s_uncut, s_top;
-  __shared__ uint2 s_item[kSplitMaxEntries / 2];  // of the last wave: where it starts, its key tiles
-  __shared__ uint32_t s_load[kSplitMaxEntries / 2];  // of each CTA before the last wave
-  __shared__ uint4 s_at[kSplitMaxEntries / 2];    // of each CTA: where its share starts, cuts before it, a cut itself
+  __shared__ uint2 s_item[kWave];     // of the last wave: where it starts, its key tiles
+  __shared__ uint32_t s_load[kWave];  // of each CTA before the last wave
+  __shared__ uint4 s_at[kWave];       // of each CTA: where its share starts, cuts before it, a cut itself
+  if (threadIdx.x == 0) s_cut = s_most = s_uncut = s_top = 0u;
   grid_dependency_wait();
   launch_dependents();
-  const int S = seg.num_segments, tid = threadIdx.x, heads = seg.num_kv_heads;
-  uint32_t* order = ws + kHeader;
-  uint32_t* prefix = ws + kHeader + S;
-  const bool sorted = S <= kSortMax;
-  if (sorted) {
-    if (tid < S) s_seg[tid] = checked_paged_segment(seg, tid, err);
-    __syncthreads();
-    if (tid < S) {  // most keys first, ties by position
-      int rank = 0;
-      for (int h = 0; h < S; ++h)
-        rank += s_seg[h].used > s_seg[tid].used || (s_seg[h].used == s_seg[tid].used && h < tid);
-      s_order[rank] = tid;
-    }
-    __syncthreads();
-  }
-  auto items_at = [&](int i) -> uint32_t {  // of the segment in place i
-    const int rows = sorted ? s_seg[s_order[i]].rows : checked_paged_segment(seg, i, err).rows;
-    return static_cast<uint32_t>(pairs_of(rows, tokens)) * heads;
-  };
-  const int chunk = (S + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
+  const int S = seg.num_segments, tid = threadIdx.x, threads = blockDim.x;
+  const uint32_t heads = seg.num_kv_heads;
+  // ---- the pairs of each segment
+  const int chunk = (S + threads - 1) / threads;  // segments of a thread: one each up to kSegments
   const int lo = min(S, tid * chunk), hi = min(S, lo + chunk);
-  uint64_t local = 0, items;
-  for (int i = lo; i < hi; ++i) local += items_at(i);
-  uint32_t run = static_cast<uint32_t>(block_exclusive_scan(local, s_warp64, items));
+  uint64_t local = 0, all;
+  for (int g = lo; g < hi; ++g) {
+    const PagedSegment s = checked_paged_segment(seg, g, err);
+    local += pairs_of(s.rows, tokens);
+    if (S <= kSegments) s_seg[g] = s;
+  }
+  const uint64_t before = block_scan(local, s_warp64, &all);
   // Segments that overlap can hold more tiles than the capacity (and more than 32 bits count): then no item.
-  if (items > (static_cast<uint64_t>(seg.capacity_q) / tokens + S) * heads) {
+  if (all > static_cast<uint64_t>(paged_max_pairs(seg.capacity_q, S, tokens))) {
     if (tid == 0) {
       record_error(err, kErrBadCuSeqlens);
       ws[0] = ws[2] = ws[3] = 0;
     }
     return;
   }
-  const uint32_t total = static_cast<uint32_t>(items);
-  for (int i = lo; i < hi; ++i) {
-    order[i] = static_cast<uint32_t>(sorted ? s_order[i] : i);
-    prefix[i] = run;
-    if (sorted) s_prefix[i] = run;
-    run += items_at(i);
+  const uint32_t n = static_cast<uint32_t>(all), total = n * heads;
+  const bool sorted = n <= kSorted && S <= kSegments;
+  if (S <= kSegments) {
+    if (tid < S) s_first[tid] = static_cast<int>(before);
+    __syncthreads();
+    for (uint32_t i = tid; i < n; i += threads) {
+      int l = 0, h = S - 1;  // the last segment that starts at i or before
+      while (l < h) {
+        const int mid = (l + h + 1) >> 1;
+        if (static_cast<uint32_t>(s_first[mid]) <= i) l = mid; else h = mid - 1;
+      }
+      const int pair = pairs_of(s_seg[l].rows, tokens) - 1 - static_cast<int>(i - s_first[l]);  // the last one first
+      const PagedPair p = pair_of(s_seg[l], l, pair, tokens, seg.causal_block);
+      if (sorted) s_tiles[i] = key_tiles(p.keys);
+      else list[i] = p;
+    }
+  } else {
+    uint32_t i = static_cast<uint32_t>(before);
+    for (int g = lo; g < hi; ++g) {
+      const PagedSegment s = checked_paged_segment(seg, g, nullptr);
+      for (int pair = pairs_of(s.rows, tokens) - 1; pair >= 0; --pair)
+        list[i++] = pair_of(s, g, pair, tokens, seg.causal_block);
+    }
   }
-  if (tid == 0) {
-    prefix[S] = total;
-    if (sorted) s_prefix[S] = total;
+  if (sorted) {  // a pair's place: those that are longer, and those as long that come before
+    for (uint32_t i = n + tid; i < (n + 3) / 4 * 4; i += threads) s_tiles[i] = 0u;
+    __syncthreads();
+    for (uint32_t i = tid; i < n; i += threads) {
+      const uint32_t mine = s_tiles[i];
+      uint32_t rank = 0;
+      for (uint32_t j = 0; j < n; j += 4) {
+        const uint4 t = *reinterpret_cast<const uint4*>(s_tiles + j);
+        rank += (t.x > mine || (t.x == mine && j < i)) + (t.y > mine || (t.y == mine && j + 1 < i)) +
+                (t.z > mine || (t.z == mine && j + 2 < i)) + (t.w > mine || (t.w == mine && j + 3 < i));
+      }
+      int l = 0, h = S - 1;
+      while (l < h) {
+        const int mid = (l + h + 1) >> 1;
+        if (static_cast<uint32_t>(s_first[mid]) <= i) l = mid; else h = mid - 1;
+      }
+      const int pair = pairs_of(s_seg[l].rows, tokens) - 1 - static_cast<int>(i - s_first[l]);
+      list[rank] = pair_of(s_seg[l], l, pair, tokens, seg.causal_block);
+      s_sorted[rank] = mine;
+    }
   }
   const uint32_t waves = total / wave, tail = waves * wave, R = total - tail;
-  if (split_area == nullptr || !sorted || R == 0 || 2 * wave + 1 > kSplitMaxEntries) {
+  if (split_area == nullptr || R == 0 || 2 * wave + 1 > kSplitMaxEntries) {
     if (tid == 0) {
       ws[0] = 0;
       ws[2] = total;
@@ -113,46 +177,29 @@ paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_
     }
     return;
   }
-  if (tid == 0) s_cut = s_most = s_uncut = s_top = 0u;
-  __syncthreads();  // also: the prefix is complete
-  auto entry_of = [&](uint32_t item) {
-    int l = 0, h = S - 1;
-    while (l < h) {
-      const int mid = (l + h + 1) >> 1;
-      if (s_prefix[mid] <= item) l = mid; else h = mid - 1;
-    }
-    TileEntry e{};
-    e.segment = s_order[l];
-    const PagedSegment s = s_seg[e.segment];
-    const int loc = static_cast<int>(item - s_prefix[l]);
-    e.kv_head = loc % heads;
-    e.pair = pairs_of(s.rows, tokens) - 1 - loc / heads;
-    e.kv1 = key_tiles(pair_limit(s, e.pair, tokens, seg.causal_block));
-    return e;
-  };
+  __syncthreads();  // the list is complete (written by this CTA: the barrier makes it visible here)
+  auto tiles_at = [&](uint32_t item) -> uint32_t { return sorted ? s_sorted[item / heads] : key_tiles(list[item / heads].keys); };
   uint32_t load = 0;
   if (tid < wave) {
-    for (uint32_t w = 0; w < waves; ++w) load += entry_of(item_of(w, tid, wave)).kv1 + kCostItem;
+    for (uint32_t w = 0; w < waves; ++w) load += tiles_at(item_of(w, tid, wave)) + kCostItem;
     s_load[tid] = load;
     atomicMax(&s_top, load);
   }
   // Behind an odd number of waves the CTAs' loads fall with their number reversed, so the items come reversed too.
   const bool reversed = waves & 1;
   const bool mine = tid < static_cast<int>(R);  // fewer than a wave
-  TileEntry e{};
-  int nkv = 0;
-  uint32_t cost = 0;
+  const uint32_t item = tail + (reversed ? R - 1 - tid : tid);
+  uint32_t nkv = 0, cost = 0;
   if (mine) {
-    e = entry_of(tail + (reversed ? R - 1 - tid : tid));
-    nkv = e.kv1;
-    cost = static_cast<uint32_t>(nkv) + kCostItem;  // a wave's sum fits 32 bits
+    nkv = tiles_at(item);
+    cost = nkv + kCostItem;  // a wave's sum fits 32 bits
     atomicMax(&s_most, cost);
   }
   uint32_t rest, before_all;
-  const uint32_t start = block_exclusive_scan(cost, s_warp, rest);  // (its barriers also order s_most and s_load)
-  block_exclusive_scan(tid < wave ? load : 0u, s_warp, before_all);
+  const uint32_t start = block_scan(cost, s_warp, &rest);  // (its barriers also order s_most, s_top and s_load)
+  block_scan(tid < wave ? load : 0u, s_warp, &before_all);
   if (mine) {
-    s_item[tid] = make_uint2(start, static_cast<uint32_t>(nkv));
+    s_item[tid] = make_uint2(start, nkv);
     atomicMax(&s_uncut, cost + s_load[reversed ? wave - static_cast<int>(R) + tid : tid]);
   }
   __syncthreads();
@@ -163,7 +210,7 @@ paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_
   if (tid < wave && load < target)
     share = max(max(target - load, 2u * kSplitMinChunk), s_most / (kMaxChunks - 4) + 1);
   uint32_t shares;
-  const uint32_t from = block_exclusive_scan(share, s_warp, shares);
+  const uint32_t from = block_scan(share, s_warp, &shares);
   // CTA k starts in item at.x, at its key tile at.y (0: at its start)
   uint2 at = make_uint2(R, 0u);
   if (tid < wave && cut) {
@@ -173,10 +220,10 @@ paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_
         const int mid = (l + h + 1) >> 1;
         if (s_item[mid].x <= from) l = mid; else h = mid - 1;
       }
-      const uint32_t n = s_item[l].y, j = min(n, from - s_item[l].x);
-      const bool inside = n >= static_cast<uint32_t>(kSplitMinTiles) && j >= static_cast<uint32_t>(kSplitMinChunk) &&
-                          j + kSplitMinChunk <= n;
-      at = inside ? make_uint2(l, j) : make_uint2(2 * j < n ? l : l + 1, 0u);
+      const uint32_t m = s_item[l].y, j = min(m, from - s_item[l].x);
+      const bool inside = m >= static_cast<uint32_t>(kSplitMinTiles) && j >= static_cast<uint32_t>(kSplitMinChunk) &&
+                          j + kSplitMinChunk <= m;
+      at = inside ? make_uint2(l, j) : make_uint2(2 * j < m ? l : l + 1, 0u);
     }
     if (tid == 0) at = make_uint2(0u, 0u);
   } else if (!cut) {
@@ -186,11 +233,11 @@ paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_
   // CTAs without a share start where the next one does: one of them stands for the cut there
   const bool counts = tid < wave && at.y > 0 && share > 0;
   uint32_t cuts;
-  const uint32_t before = block_exclusive_scan(counts ? 1u : 0u, s_warp, cuts);
-  uint32_t* listed = reinterpret_cast<uint32_t*>(split_area + split_items_offset());
+  const uint32_t earlier_cuts = block_scan(counts ? 1u : 0u, s_warp, &cuts);
+  uint32_t* listed = reinterpret_cast<uint32_t*>(split_area + split_items_offset<PagedEntry>());
   if (tid < wave) {
-    s_at[tid] = make_uint4(at.x, at.y, before, counts ? 1u : 0u);
-    listed[wave + tid] = at.x + before + (at.y > 0 ? 1u : 0u);  // (the cut where it starts, whoever stands for it)
+    s_at[tid] = make_uint4(at.x, at.y, earlier_cuts, counts ? 1u : 0u);
+    listed[wave + tid] = at.x + earlier_cuts + (at.y > 0 ? 1u : 0u);  // (the cut where it starts, whoever stands for it)
   }
   if (tid == 0) listed[2 * wave] = R + cuts;
   __syncthreads();
@@ -207,13 +254,16 @@ paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_
     for (; last < wave && s_at[last].x == static_cast<uint32_t>(tid); ++last) c += s_at[last].w;
     const uint32_t first = tid + earlier;
     if (c > 1) listed[atomicAdd(&s_cut, 1u)] = first;  // listed for the merge; the list's order is immaterial
+    PagedEntry e{};
+    e.pair = list[item / heads];
+    e.kv_head = static_cast<int>(item % heads);
     e.first = static_cast<int>(first);
     e.chunks = c;
     e.kv0 = 0;
     for (e.chunk = 0; e.chunk < c; ++e.chunk, ++k) {
       while (k < last && s_at[k].w == 0) ++k;
-      e.kv1 = c > 1 && k < last ? static_cast<int>(s_at[k].y) : nkv;
-      reinterpret_cast<TileEntry*>(split_area)[first + e.chunk] = e;
+      e.kv1 = c > 1 && k < last ? static_cast<int>(s_at[k].y) : static_cast<int>(nkv);
+      reinterpret_cast<PagedEntry*>(split_area)[first + e.chunk] = e;
       e.kv0 = e.kv1;
     }
   }
@@ -229,8 +279,10 @@ template <int kD, bool kE4m3>
 struct PagedSource {
   static constexpr int kDim = kD, kChunks = kMaxChunks;
   static constexpr bool kConvert = kE4m3, kRowLimits = true;
+  using Entry = PagedEntry;
   CUtensorMap tmap_q, tmap_k, tmap_v;
   PagedSegments seg;
+  const PagedPair* list;
   const uint8_t *k_scale, *v_scale;
   int group, tokens;  // query heads of a key head, tokens of a tile
 
@@ -258,51 +310,39 @@ struct PagedSource {
 
   __device__ __forceinline__ Work decode(uint32_t item, const uint32_t* __restrict__ ws,
                                          const uint8_t* __restrict__ split_area) const {
-    const int S = seg.num_segments;
-    const uint32_t tail = ws[2];
+    const uint32_t tail = ws[2], heads = seg.num_kv_heads;
     Work d;
-    int pair, kv1 = -1;
+    PagedPair p;
+    int kv1 = -1;
     d.kv0 = 0;
     d.partial = -1;
-    if (ws[3] > 0 && item >= tail) {
-      const TileEntry e = reinterpret_cast<const TileEntry*>(split_area)[item - tail];
-      d.segment = e.segment;
-      pair = e.pair;
+    if (item >= tail) {
+      const PagedEntry e = reinterpret_cast<const PagedEntry*>(split_area)[item - tail];
+      p = e.pair;
       d.kv_head = e.kv_head;
       d.kv0 = e.kv0;
       kv1 = e.kv1;
       if (e.chunks > 1) d.partial = e.first + e.chunk;
     } else {
-      const uint32_t* prefix = ws + kHeader + S;
-      int lo = 0, hi = S - 1;  // last i with prefix[i] <= item
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= item) lo = mid; else hi = mid - 1;
-      }
-      d.segment = static_cast<int>((ws + kHeader)[lo]);
-      const int pairs = pairs_of(seg.cu_q[d.segment + 1] - seg.cu_q[d.segment], tokens);
-      const int loc = static_cast<int>(item - prefix[lo]);
-      d.kv_head = loc % seg.num_kv_heads;
-      pair = pairs - 1 - loc / seg.num_kv_heads;
+      p = list[item / heads];
+      d.kv_head = static_cast<int>(item % heads);
     }
-    const int a = seg.cu_q[d.segment];
-    d.seg_end = seg.cu_q[d.segment + 1];
-    d.used = seg.used[d.segment];
+    d.segment = p.segment;
+    d.seg_end = p.seg_end;
+    d.used = p.used;
     d.head = d.kv_head * group;
-    d.ntiles = min(2, tiles_of(d.seg_end - a, tokens) - 2 * pair);
-    d.q0[0] = a + 2 * pair * tokens;
-    d.q0[1] = d.q0[0] + tokens;
-    const int keys = pair_limit(PagedSegment{a, d.seg_end - a, d.used}, pair, tokens, seg.causal_block);
-    const int all = key_tiles(keys);
+    d.ntiles = p.ntiles;
+    d.q0[0] = p.q0;
+    d.q0[1] = p.q0 + tokens;
+    const int all = key_tiles(p.keys);
     if (kv1 < 0) kv1 = all;
     d.nkv = kv1 - d.kv0;
-    d.last_keys = kv1 == all ? keys - (all - 1) * kBlockN : kBlockN;
+    d.last_keys = kv1 == all ? p.keys - (all - 1) * kBlockN : kBlockN;
     return d;
   }
 
-  __device__ __forceinline__ TilePlace place(const TileEntry& en, int t) const {
-    const int a = seg.cu_q[en.segment], end = seg.cu_q[en.segment + 1], tile = 2 * en.pair + t;
-    return TilePlace{tile < tiles_of(end - a, tokens), a + tile * tokens, en.kv_head * group, end};
+  __device__ __forceinline__ TilePlace place(const PagedEntry& e, int t) const {
+    return TilePlace{t < e.pair.ntiles, e.pair.q0 + t * tokens, e.kv_head * group, e.pair.seg_end};
   }
 
   // The key/value producer: lane i has page i of a key tile, looked up a tile ahead.
@@ -401,12 +441,13 @@ cudaError_t launch(const PagedTileArgs& a, cudaStream_t stream) {
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return cudaErrorInvalidDevice;
   uint32_t* ws = static_cast<uint32_t*>(a.workspace);
+  PagedPair* list = reinterpret_cast<PagedPair*>(ws + 2 * kHeader);
   uint8_t* split = static_cast<uint8_t*>(a.split_area);
   const int group = a.seg.num_q_heads / a.seg.num_kv_heads, tokens = kBlockM / group;
-  e = launch_programmatic(paged_plan_kernel, dim3(1), dim3(a.seg.num_segments <= kSortMax ? kSortMax : kPlanThreads), 0,
-                          stream, a.seg, tokens, ws, split, sms, a.err);
+  e = launch_programmatic(paged_plan_kernel, dim3(1), dim3(a.seg.num_segments <= kSegments ? 512 : kPlanThreads), 0,
+                          stream, a.seg, tokens, ws, list, split, sms, a.err);
   if (e != cudaSuccess) return e;
-  const Source src{a.tmap_q, a.tmap_k, a.tmap_v, a.seg, a.k_scale, a.v_scale, group, tokens};
+  const Source src{a.tmap_q, a.tmap_k, a.tmap_v, a.seg, list, a.k_scale, a.v_scale, group, tokens};
   e = launch_programmatic(attn_tile_kernel<Source>, dim3(sms), dim3(kTileThreads), C::kSmemBytes, stream, src,
                           static_cast<__nv_bfloat16*>(a.o), a.wide, a.lse, a.scale, a.scale * 1.4426950408889634f,
                           static_cast<const uint32_t*>(ws), split, a.err,
