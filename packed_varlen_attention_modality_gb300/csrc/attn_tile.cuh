@@ -195,11 +195,12 @@ attn_tile_kernel(const __grid_constant__ Source src, __nv_bfloat16* __restrict__
   // this CTA's items: every gridDim.x-th of the whole ones, then its entries of the last wave
   const uint32_t whole = ws[2];  // of all CTAs
   uint32_t entry = 0, entry_end = 0;
-  if (ws[3] > 0) {
+  if (split_area != nullptr) {  // (read before it is known whether there are any)
     const uint32_t* firsts = reinterpret_cast<const uint32_t*>(split_area + split_items_offset<Entry>()) + gridDim.x;
     entry = firsts[blockIdx.x];
     entry_end = firsts[blockIdx.x + 1];
   }
+  if (ws[3] == 0) entry = entry_end = 0;
   // nothing to do, or a timeout recorded earlier and not read yet: leave at once, all threads together
   const bool late = err != nullptr && *reinterpret_cast<volatile unsigned int*>(err) == kErrTimeout;
   if (__syncthreads_or(late) || (blockIdx.x >= whole && entry == entry_end)) {
@@ -540,6 +541,7 @@ attn_tile_kernel(const __grid_constant__ Source src, __nv_bfloat16* __restrict__
         float* mine = reinterpret_cast<float*>(split_area + split_partials_offset<Entry>()) +
                       (static_cast<size_t>(d.partial) * 2 + t) * kPartial<D> + static_cast<size_t>(row) * D;
         const bool sectors = (reinterpret_cast<uintptr_t>(mine) & 31u) == 0;
+        const bool real = d.q0[t] + (odd ? next : even).token < d.seg_end;  // this thread's row is one
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t r[32];
@@ -549,7 +551,8 @@ attn_tile_kernel(const __grid_constant__ Source src, __nv_bfloat16* __restrict__
 #pragma unroll
           for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * inv_l);
 #pragma unroll
-          for (int c = 0; c < 32; c += 8) st_global_32(mine + c0 + c, r + c, sectors);
+          for (int c = 0; c < 32; c += 8)
+            if (real) st_global_32(mine + c0 + c, r + c, sectors);
         }
         tc_fence_before();
         arrive_warp(bar_oempty(t));
@@ -770,6 +773,9 @@ attn_tile_kernel(const __grid_constant__ Source src, __nv_bfloat16* __restrict__
 
 // Merge of cut items, in chunk order: lse = log sum_c exp(lse_c), o = sum_c exp(lse_c - lse) o_c.
 // A unit is 16 rows of one tile; memory-bound and short (the partials are in L2).
+struct Float8 {
+  float4 x, y;
+};
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = 16;
 static_assert(kMergeThreads == 16 * kMergeRows, "16 lanes to a row");
@@ -784,13 +790,16 @@ attn_tile_merge_kernel(const uint32_t* __restrict__ ws, const uint8_t* __restric
   __shared__ float s_w[kMergeRows][Source::kChunks];
   grid_dependency_wait();
   launch_dependents();
+  // What is read here comes one read after another, each some 0.7 us: so the first item is read before it is known to
+  // be one, and a thread's values of the first chunks with the chunks' LSEs.
+  const uint32_t* items = reinterpret_cast<const uint32_t*>(split_area + split_items_offset<Entry>());
+  const uint32_t first = items[min(static_cast<int>(blockIdx.x) / kMergeUnits, kSplitMaxEntries - 1)];
+  const int n_units = static_cast<int>(ws[0]) * kMergeUnits;
   // after a timeout the partials are incomplete: leave the output as it is
   if (err != nullptr && *reinterpret_cast<const volatile unsigned int*>(err) == kErrTimeout) return;
-  const int n_units = static_cast<int>(ws[0]) * kMergeUnits;
-  const uint32_t* items = reinterpret_cast<const uint32_t*>(split_area + split_items_offset<Entry>());
   const float* parts = reinterpret_cast<const float*>(split_area + split_partials_offset<Entry>());
   for (int unit = blockIdx.x; unit < n_units; unit += gridDim.x) {
-    const int e = static_cast<int>(items[unit / kMergeUnits]);
+    const int e = static_cast<int>(unit == static_cast<int>(blockIdx.x) ? first : items[unit / kMergeUnits]);
     const int t = unit % kMergeUnits / (kBlockM / kMergeRows);
     const int r0 = unit % (kBlockM / kMergeRows) * kMergeRows;
     const Entry en = reinterpret_cast<const Entry*>(split_area)[e];
@@ -798,6 +807,19 @@ attn_tile_merge_kernel(const uint32_t* __restrict__ ws, const uint8_t* __restric
     if (!at.exists || at.q0 + src.row(r0).token >= at.seg_end) continue;  // the whole CTA
     auto inside = [&](int r) { return at.q0 + src.row(r0 + r).token < at.seg_end; };
     auto part = [&](int ch) { return parts + (static_cast<size_t>(e + ch) * 2 + t) * kPartial<D>; };
+    const int my_row = threadIdx.x / (D / 8), col = threadIdx.x % (D / 8) * 8;  // eight values of a row to a thread
+    const bool mine = my_row < kMergeRows && inside(my_row);
+    auto load = [&](int ch) {
+      const float4* p = reinterpret_cast<const float4*>(part(ch) + static_cast<size_t>(r0 + my_row) * D + col);
+      return Float8{p[0], p[1]};
+    };
+    constexpr int kAhead = 4;
+    Float8 ahead[kAhead] = {};
+    if (mine) {
+#pragma unroll
+      for (int ch = 0; ch < kAhead; ++ch)
+        if (ch < en.chunks) ahead[ch] = load(ch);
+    }
     __syncthreads();  // the previous unit's weights have been used
     {  // 16 lanes to a row
       const int r = threadIdx.x / 16, lane16 = threadIdx.x % 16;
@@ -821,27 +843,26 @@ attn_tile_merge_kernel(const uint32_t* __restrict__ ws, const uint8_t* __restric
       }
     }
     __syncthreads();
-    for (int u = threadIdx.x; u < kMergeRows * (D / 8); u += kMergeThreads) {
-      const int r = u / (D / 8), c = u % (D / 8) * 8;
-      if (!inside(r)) continue;
-      const TileRow to = src.row(r0 + r);
+    if (mine) {
+      const TileRow to = src.row(r0 + my_row);
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      auto add = [&](const Float8& v, float w) {
+        acc[0] = fmaf(w, v.x.x, acc[0]);
+        acc[1] = fmaf(w, v.x.y, acc[1]);
+        acc[2] = fmaf(w, v.x.z, acc[2]);
+        acc[3] = fmaf(w, v.x.w, acc[3]);
+        acc[4] = fmaf(w, v.y.x, acc[4]);
+        acc[5] = fmaf(w, v.y.y, acc[5]);
+        acc[6] = fmaf(w, v.y.z, acc[6]);
+        acc[7] = fmaf(w, v.y.w, acc[7]);
+      };
+#pragma unroll
+      for (int ch = 0; ch < kAhead; ++ch)
+        if (ch < en.chunks) add(ahead[ch], s_w[my_row][ch]);
 #pragma unroll 4
-      for (int ch = 0; ch < en.chunks; ++ch) {
-        const float4* src = reinterpret_cast<const float4*>(part(ch) + static_cast<size_t>(r0 + r) * D + c);
-        const float4 x = src[0], y = src[1];
-        const float w = s_w[r][ch];
-        acc[0] = fmaf(w, x.x, acc[0]);
-        acc[1] = fmaf(w, x.y, acc[1]);
-        acc[2] = fmaf(w, x.z, acc[2]);
-        acc[3] = fmaf(w, x.w, acc[3]);
-        acc[4] = fmaf(w, y.x, acc[4]);
-        acc[5] = fmaf(w, y.y, acc[5]);
-        acc[6] = fmaf(w, y.z, acc[6]);
-        acc[7] = fmaf(w, y.w, acc[7]);
-      }
+      for (int ch = kAhead; ch < en.chunks; ++ch) add(load(ch), s_w[my_row][ch]);
       *reinterpret_cast<uint4*>(out + (static_cast<size_t>(at.q0 + to.token) * src.seg.num_q_heads + at.head + to.head) * D +
-                                c) =
+                                col) =
           make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
                      pack_bf16x2(acc[6], acc[7]));
     }

@@ -99,7 +99,8 @@ paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_
   __shared__ uint32_t s_cut, s_most, s_uncut, s_top;
   __shared__ uint2 s_item[kWave];     // of the last wave: where it starts, its key tiles
   __shared__ uint32_t s_load[kWave];  // of each CTA before the last wave
-  __shared__ uint4 s_at[kWave];       // of each CTA: where its share starts, cuts before it, a cut itself
+  __shared__ uint2 s_at[kWave];       // of each CTA: the item in which its share starts, cuts before it
+  __shared__ uint32_t s_tile[kWave];  // the cuts: key tile
   if (threadIdx.x == 0) s_cut = s_most = s_uncut = s_top = 0u;
   grid_dependency_wait();
   launch_dependents();
@@ -195,9 +196,11 @@ paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_
     cost = nkv + kCostItem;  // a wave's sum fits 32 bits
     atomicMax(&s_most, cost);
   }
-  uint32_t rest, before_all;
-  const uint32_t start = block_scan(cost, s_warp, &rest);  // (its barriers also order s_most, s_top and s_load)
-  block_scan(tid < wave ? load : 0u, s_warp, &before_all);
+  // (two sums in one: the costs, and above them the loads; its barriers also order s_most, s_top and s_load)
+  uint64_t sums;
+  const uint32_t start =
+      static_cast<uint32_t>(block_scan(static_cast<uint64_t>(tid < wave ? load : 0u) << 32 | cost, s_warp64, &sums));
+  const uint32_t rest = static_cast<uint32_t>(sums), before_all = static_cast<uint32_t>(sums >> 32);
   if (mine) {
     s_item[tid] = make_uint2(start, nkv);
     atomicMax(&s_uncut, cost + s_load[reversed ? wave - static_cast<int>(R) + tid : tid]);
@@ -236,36 +239,42 @@ paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_
   const uint32_t earlier_cuts = block_scan(counts ? 1u : 0u, s_warp, &cuts);
   uint32_t* listed = reinterpret_cast<uint32_t*>(split_area + split_items_offset<PagedEntry>());
   if (tid < wave) {
-    s_at[tid] = make_uint4(at.x, at.y, earlier_cuts, counts ? 1u : 0u);
+    s_at[tid] = make_uint2(at.x, earlier_cuts);
+    if (counts) s_tile[earlier_cuts] = at.y;
     listed[wave + tid] = at.x + earlier_cuts + (at.y > 0 ? 1u : 0u);  // (the cut where it starts, whoever stands for it)
   }
   if (tid == 0) listed[2 * wave] = R + cuts;
   __syncthreads();
-  if (mine) {
-    // the cuts inside this item, in order: CTAs whose share starts inside it
-    int k = 0, end = wave;  // the first CTA that starts in this item or behind
-    while (k < end) {
-      const int mid = (k + end) >> 1;
-      if (s_at[mid].x < static_cast<uint32_t>(tid)) k = mid + 1; else end = mid;
+  // Cuts in the items before item i: those before the first CTA that starts in it or behind.
+  auto cuts_before = [&](uint32_t i) {
+    int l = 0, h = wave;
+    while (l < h) {
+      const int mid = (l + h) >> 1;
+      if (s_at[mid].x < i) l = mid + 1; else h = mid;
     }
-    const uint32_t earlier = !cut ? 0u : k < wave ? s_at[k].z : cuts;
-    int last = cut ? k : wave;
-    int c = 1;
-    for (; last < wave && s_at[last].x == static_cast<uint32_t>(tid); ++last) c += s_at[last].w;
-    const uint32_t first = tid + earlier;
-    if (c > 1) listed[atomicAdd(&s_cut, 1u)] = first;  // listed for the merge; the list's order is immaterial
+    return l < wave ? s_at[l].y : cuts;
+  };
+  // An entry: chunk `chunk` of item i of the last wave, whose cuts are [c0, c1).
+  auto write_entry = [&](uint32_t i, uint32_t c0, uint32_t c1, uint32_t chunk, uint32_t tiles) {
+    const uint32_t of = tail + (reversed ? R - 1 - i : i);
     PagedEntry e{};
-    e.pair = list[item / heads];
-    e.kv_head = static_cast<int>(item % heads);
-    e.first = static_cast<int>(first);
-    e.chunks = c;
-    e.kv0 = 0;
-    for (e.chunk = 0; e.chunk < c; ++e.chunk, ++k) {
-      while (k < last && s_at[k].w == 0) ++k;
-      e.kv1 = c > 1 && k < last ? static_cast<int>(s_at[k].y) : static_cast<int>(nkv);
-      reinterpret_cast<PagedEntry*>(split_area)[first + e.chunk] = e;
-      e.kv0 = e.kv1;
-    }
+    e.pair = list[of / heads];
+    e.kv_head = static_cast<int>(of % heads);
+    e.first = static_cast<int>(i + c0);
+    e.chunk = static_cast<int>(chunk);
+    e.chunks = static_cast<int>(1 + c1 - c0);
+    e.kv0 = chunk == 0 ? 0 : static_cast<int>(s_tile[c0 + chunk - 1]);
+    e.kv1 = c0 + chunk < c1 ? static_cast<int>(s_tile[c0 + chunk]) : static_cast<int>(tiles);
+    reinterpret_cast<PagedEntry*>(split_area)[i + c0 + chunk] = e;
+  };
+  if (mine) {
+    const uint32_t c0 = cuts_before(tid), c1 = cuts_before(tid + 1);
+    if (c1 > c0) listed[atomicAdd(&s_cut, 1u)] = tid + c0;  // for the merge; the list's order is immaterial
+    write_entry(tid, c0, c1, 0, nkv);
+  }
+  if (counts) {
+    const uint32_t c0 = cuts_before(at.x);
+    write_entry(at.x, c0, cuts_before(at.x + 1), earlier_cuts - c0 + 1, s_item[at.x].y);
   }
   __syncthreads();
   if (tid == 0) {
@@ -444,7 +453,7 @@ cudaError_t launch(const PagedTileArgs& a, cudaStream_t stream) {
   PagedPair* list = reinterpret_cast<PagedPair*>(ws + 2 * kHeader);
   uint8_t* split = static_cast<uint8_t*>(a.split_area);
   const int group = a.seg.num_q_heads / a.seg.num_kv_heads, tokens = kBlockM / group;
-  e = launch_programmatic(paged_plan_kernel, dim3(1), dim3(a.seg.num_segments <= kSegments ? 512 : kPlanThreads), 0,
+  e = launch_programmatic(paged_plan_kernel, dim3(1), dim3(a.seg.num_segments <= kSegments ? kSegments : kPlanThreads), 0,
                           stream, a.seg, tokens, ws, list, split, sms, a.err);
   if (e != cudaSuccess) return e;
   const Source src{a.tmap_q, a.tmap_k, a.tmap_v, a.seg, list, a.k_scale, a.v_scale, group, tokens};
