@@ -11,12 +11,18 @@
 //   U_r = sum of dh xh, V_r = sum of t yh over the request's rows:  dshift = sum of dh,
 //   dscale = w U, dgate = w_b V,  dw = sum_r (1 + scale_r) U_r,  dw_b = sum_r gate_r V_r
 //
-// Memory-bound: the forward reads x, y and writes x', h once; the backward reads dx', dh, x', y and writes
-// dx, dy once.  A CTA takes a contiguous range of rows, so the request's vectors (w (1 + scale), shift,
-// w_b gate) stay in registers from row to row, eight columns a thread, and so do the backward's column
-// sums.  Rows come through a ring in shared memory by bulk copies that run several rows ahead, so a row waits on no
-// load but on its sums alone: the warps exchange them once for each norm (the backward: once for all that the
-// inputs give, once for the branch's dot product).  All arithmetic is fp32.
+// Memory-bound: the forward reads x, y and writes x', h once; the backward reads dx', dh, x', y and writes dx, dy
+// once.  Measured at 47,000 rows of 5,120 values in 32 bits, eight requests: forward 378 us (floor 355 at the rate of
+// a copy, 94 %), backward 375 us (floor 263, 70 %; 298 without a branch norm, where a row needs fewer sums).
+//
+// A CTA takes a contiguous range of rows, so the request's vectors (w (1 + scale), shift, w_b gate) stay in registers
+// from row to row, 16 columns a thread, and so do the backward's column sums.  (8 columns, with the registers of twice
+// the threads: backward 436 us against 390.)  Rows come through a ring in shared memory by bulk copies that run
+// several rows ahead, so a row waits on no load but on its sums alone.  The copies name their lines as the first to
+// leave L2, since nothing reads them again: forward 386 us against 411 at that step.  The warps exchange a row's sums
+// once for each norm forward.  Backward all that the inputs give goes round once, the branch's dot product among it;
+// only with a layer norm a second exchange follows (for all norms: 390 us against 375).  All arithmetic is fp32, two
+// values an instruction (one at a time: forward 395 us, backward 441).
 #include <cuda_bf16.h>
 
 #include "h3_internal.h"
@@ -470,7 +476,7 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
   }
   ring.start();
 
-  constexpr int kTold = kLayer ? 6 : 3, kDots = kLayer ? 2 : 1;
+  constexpr int kTold = 6, kDots = 2;
   Talk<kThreads / 32, kTold> row_talk{inputs};
   Talk<kThreads / 32, kDots> dot_talk{dots};
   const float inv_dim = 1.f / dim;
@@ -508,20 +514,22 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
   auto load_x = [&](int k) { return load8(reinterpret_cast<const X*>(ring.row(0)) + col[k]); };
   auto load_g = [&](int k) { return load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(2)) + col[k]); };
   auto load_y = [&](int k) { return load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(3)) + col[k]); };
-  Vec8 t[kVecs], y[kVecs];  // of the row whose dot product is on its way: t gate w_b and yh
+  auto load_d = [&](int k) {
+    return has_dx ? load8(reinterpret_cast<const X*>(ring.row(1)) + col[k]) : Vec8{};
+  };
+  Vec8 t[kVecs], y[kVecs];  // (a layer norm) of the row whose dot product is on its way: t gate w_b and yh
   float2 ry = both(1.f);
   // The rest of row n once the dot products are there.
   auto finish = [&](int n) {
     float d[kDots], unused[kDots];
     const bool fine = dot_talk.hear(d, unused);
     lane_sums(d);
-    const float2 dot = both(-d[0] * inv_dim), mean = both(branch_layer ? -d[kDots - 1] * inv_dim : 0.f);
+    const float2 dot = both(-d[0] * inv_dim), mean = both(branch_layer ? -d[1] * inv_dim : 0.f);
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       if (!own[k]) continue;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        t[k].p[e] = fmul2(ry, ffma2(y[k].p[e], dot, kLayer ? fadd2(t[k].p[e], mean) : t[k].p[e]));
+      for (int e = 0; e < 4; ++e) t[k].p[e] = fmul2(ry, ffma2(y[k].p[e], dot, fadd2(t[k].p[e], mean)));
       store8(a.dy + n * a.dy_stride + col[k], t[k]);
     }
     return fine;
@@ -546,14 +554,17 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
         }
       }
     }
-    // what the row's inputs give: the statistics of both norms and the sums of g and g xh
+    // What the row's inputs give: the statistics of both norms and the sums of g and g xh.  Without a layer norm also
+    // the branch's dot product, from three sums that need no statistic:
+    //   sum t gate w_b y = sum dx' u + rs sum g u + rs dot sum xh u,  u = gate w_b y
+    // With one, centring would double them: t is then summed when it is known, in an exchange of its own.
     const bool ok = ring.wait();
-    {
-      float wx = 0.f, wy = 0.f, q[kLayer ? 4 : 3];
-      float2 xx = make_float2(0.f, 0.f), gs = xx, gx = xx;
-      q[2] = 0.f;
+    float v[kTold];
+    if constexpr (kLayer) {
+      float wx = 0.f, wy = 0.f, q[4] = {0.f, 0.f, 0.f, 0.f};
       if (has_h) {
         Vec8 x[kVecs];
+        float2 xx = make_float2(0.f, 0.f), gs = xx, gx = xx;
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) x[k] = own[k] ? load_x(k) : Vec8{};
         if (layer) wx = warp_mean(x, inv_mine);
@@ -564,34 +575,64 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
           const Vec8 g = load_g(k);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 c = kLayer ? fadd2(x[k].p[e], m) : x[k].p[e], weighted = fmul2(g.p[e], gain[k].p[e]);
+            const float2 c = fadd2(x[k].p[e], m), weighted = fmul2(g.p[e], gain[k].p[e]);
             if (want_shift) sums[0][k].p[e] = fadd2(sums[0][k].p[e], g.p[e]);
             xx = ffma2(c, c, xx);
-            if (kLayer) gs = fadd2(gs, weighted);
+            gs = fadd2(gs, weighted);
             gx = ffma2(weighted, c, gx);
           }
         }
+        q[0] = xx.x + xx.y;
+        q[1] = gx.x + gx.y;
+        q[3] = gs.x + gs.y;
       }
       if (branch) {
         Vec8 b[kVecs];
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) b[k] = own[k] ? load_y(k) : Vec8{};
         if (branch_layer) wy = warp_mean(b, inv_mine);
-        q[2] = lane_squares<kLayer>(b, own, wy);
+        q[2] = lane_squares<true>(b, own, wy);
       }
-      q[0] = xx.x + xx.y;
-      q[1] = gx.x + gx.y;
-      if constexpr (kLayer) {
-        q[3] = gs.x + gs.y;
-        lane_sums(q);
-        const float v[6] = {q[0], q[1], q[2], q[3], wx, wy};
-        row_talk.say(v, ok);
-      } else {
-        lane_sums(q);
-        row_talk.say(q, ok);
+      lane_sums(q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = q[e];
+      v[4] = wx;
+      v[5] = wy;
+    } else {
+      float2 q[kTold] = {};
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k) {
+        if (!own[k]) continue;
+        Vec8 x{}, weighted{};
+        if (has_h) {
+          x = load_x(k);
+          const Vec8 g = load_g(k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            weighted.p[e] = fmul2(g.p[e], gain[k].p[e]);
+            if (want_shift) sums[0][k].p[e] = fadd2(sums[0][k].p[e], g.p[e]);
+            q[0] = ffma2(x.p[e], x.p[e], q[0]);
+            q[1] = ffma2(weighted.p[e], x.p[e], q[1]);
+          }
+        }
+        if (branch) {
+          const Vec8 b = load_y(k), d = load_d(k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 u = fmul2(b.p[e], gate[k].p[e]);
+            q[2] = ffma2(b.p[e], b.p[e], q[2]);
+            q[3] = ffma2(d.p[e], u, q[3]);
+            q[4] = ffma2(weighted.p[e], u, q[4]);
+            q[5] = ffma2(x.p[e], u, q[5]);
+          }
+        }
       }
+#pragma unroll
+      for (int e = 0; e < kTold; ++e) v[e] = q[e].x + q[e].y;
+      lane_sums(v);
     }
-    if (branch && i > 0) fine = finish(n - 1);  // while the others' sums come in
+    row_talk.say(v, ok);
+    if (kLayer && branch && i > 0) fine = finish(n - 1);  // while the others' sums come in
     float s[kTold], first[kTold];
     fine = row_talk.hear(s, first) && fine;
     if (!fine) break;
@@ -614,15 +655,16 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
       x_dot = s[1];
       y_square = s[2];
     }
-    const float factor = rsqrtf(x_square * inv_dim + a.eps);
-    const float2 rs = both(factor), mean = both(layer ? -g_sum * inv_dim : 0.f), dot = both(-factor * x_dot * inv_dim);
-    if (branch) ry = both(rsqrtf(y_square * inv_dim + a.eps));
-    float2 ts = make_float2(0.f, 0.f), ty = ts;
+    const float factor = rsqrtf(x_square * inv_dim + a.eps), x_mean_dot = factor * x_dot * inv_dim;
+    const float2 rs = both(factor), mean = both(layer ? -g_sum * inv_dim : 0.f), dot = both(-x_mean_dot);
+    const float y_factor = branch ? rsqrtf(y_square * inv_dim + a.eps) : 1.f;
+    ry = both(y_factor);
+    float2 ts = make_float2(0.f, 0.f), ty = ts, y_dot = ts;
+    if (!kLayer && branch) y_dot = both(-y_factor * inv_dim * (s[3] + factor * (s[4] - x_mean_dot * factor * s[5])));
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
       if (!own[k]) continue;
-      Vec8& u = t[k];
-      u = has_dx ? load8(reinterpret_cast<const X*>(ring.row(1)) + col[k]) : Vec8{};
+      Vec8 u = load_d(k);
       if (has_h) {
         const Vec8 x = load_x(k), g = load_g(k);
 #pragma unroll
@@ -640,27 +682,33 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
       }
       store8(static_cast<X*>(a.dx) + n * a.dx_stride + col[k], scaled);
       if (!has_y) continue;
-      y[k] = load_y(k);
+      Vec8 z = load_y(k);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        y[k].p[e] = fmul2(kLayer ? fadd2(y[k].p[e], both(-y_mean)) : y[k].p[e], ry);
-        sums[2][k].p[e] = ffma2(u.p[e], y[k].p[e], sums[2][k].p[e]);
+        z.p[e] = fmul2(kLayer ? fadd2(z.p[e], both(-y_mean)) : z.p[e], ry);
+        sums[2][k].p[e] = ffma2(u.p[e], z.p[e], sums[2][k].p[e]);
         u.p[e] = fmul2(u.p[e], gate[k].p[e]);
-        if (kLayer) ts = fadd2(ts, u.p[e]);
-        ty = ffma2(u.p[e], y[k].p[e], ty);
+        if (kLayer) {
+          ts = fadd2(ts, u.p[e]);
+          ty = ffma2(u.p[e], z.p[e], ty);
+        } else if (branch) {
+          u.p[e] = fmul2(ry, ffma2(z.p[e], y_dot, u.p[e]));
+        }
       }
-      if (!branch) store8(a.dy + n * a.dy_stride + col[k], u);
+      if (!kLayer || !branch) store8(a.dy + n * a.dy_stride + col[k], u);
+      if (kLayer) {
+        t[k] = u;
+        y[k] = z;
+      }
     }
     ring.advance();
-    if (branch) {
-      float d[kDots];
-      d[0] = ty.x + ty.y;
-      if (kLayer) d[kDots - 1] = ts.x + ts.y;
+    if (kLayer && branch) {
+      float d[kDots] = {ty.x + ty.y, ts.x + ts.y};
       lane_sums(d);
       dot_talk.say(d, true);
     }
   }
-  if (fine && branch && ring.rows > 0) fine = finish(ring.first + ring.rows - 1);
+  if (kLayer && fine && branch && ring.rows > 0) fine = finish(ring.first + ring.rows - 1);
   if (!fine) {  // a wait ran out
     ring.drain(a.err);
     return;
@@ -793,6 +841,10 @@ cudaError_t launch_rows(const ResidualNormArgs& a, int sms, int* ctas, cudaStrea
   return launch_programmatic(kernel, dim3(*ctas), dim3(row_threads(a.dim)), stages * stage, stream, a, stages);
 }
 
+// A row's threads follow from dim, 16 columns each; so does how many CTAs' registers and rings an SM holds (threads *
+// CTAs * registers within 65,536).  The backward keeps three sums and two vectors a column: 320 threads fit once,
+// and held to half the registers twice, which spills (600 us and more against 390 at dim 5,120).  The forward keeps
+// three vectors and fits twice.
 template <typename X>
 cudaError_t launch_type(const ResidualNormArgs& a, bool backward, int sms, int* ctas, cudaStream_t stream) {
   if (backward) {
