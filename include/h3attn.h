@@ -497,10 +497,12 @@ H3_API size_t h3_paged_attn_workspace_size(const h3_paged_attn_desc* desc);
  *               written, others untouched.  Must not overlap an input.
  * lse         : device fp32 [num_q_heads, capacity_q] (natural log) or NULL.
  * workspace   : device, h3_paged_attn_workspace_size() bytes, 16-byte aligned; need not be initialised.
- *               Calls that may run at the same time need separate workspaces.
+ *               Calls that may run at the same time need separate workspaces.  For long chunks over an
+ *               e4m3 cache the size includes room for its tokens in bf16, up to 4 GiB; a workspace of
+ *               the size that a bf16 cache wants does too, gives the same results and takes longer.
  * A segment whose offsets or length are out of range, or with more rows than max_seqlen_q, is skipped
- * (its rows are not written); one with more tokens than max_seqlen_k is computed in full; both are
- * recorded as H3_ERR_BAD_CU_SEQLENS.  A page id out of range is read as page 0 and recorded as
+ * (its rows are not written); one with more tokens than max_seqlen_k is computed in full, or skipped
+ * where the cache is unpacked; both are recorded as H3_ERR_BAD_CU_SEQLENS.  A page id out of range is read as page 0 and recorded as
  * H3_ERR_BAD_PAGE.
  * When max_seqlen_q * num_q_heads / num_kv_heads is at most 16 the cache is streamed once, split evenly
  * over the GPU: single tokens want a tight bound.

@@ -793,9 +793,14 @@ def kv_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: tor
 
 
 def paged_attn_workspace_size(num_segments: int, max_seqlen_q: int, max_seqlen_k: int, capacity_q: int,
-                              num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int = 16) -> int:
+                              num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int = 16,
+                              e4m3: bool = False, max_pages: Optional[int] = None) -> int:
+    """Bytes for paged_attn_fwd's workspace; max_pages: the block table's width (None: what max_seqlen_k needs).
+    For long chunks over an e4m3 cache they include room for its tokens in bf16; without it (the size with
+    e4m3=False) the call gives the same and takes longer."""
+    pages = -(-max_seqlen_k // page_size) if max_pages is None else max_pages
     desc = _PagedAttnDesc.pack(num_segments, max_seqlen_q, max_seqlen_k, capacity_q, num_q_heads, num_kv_heads,
-                               head_dim, 1, page_size, 0, 0, 0, 0.0, 0)
+                               head_dim, 2 if e4m3 else 1, page_size, 1, pages, 0, 0.0, 0)
     return int(load_library().h3_paged_attn_workspace_size(desc))
 
 

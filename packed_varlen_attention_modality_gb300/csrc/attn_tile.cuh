@@ -3,8 +3,8 @@
 // chunks of cut items.  Its structure and what it measured stand in cross_attn_sm103.cu.
 //
 // A Source is a kernel parameter with
-//   kDim, kChunks (of an item, at most), kConvert (tiles arrive as bytes and are converted by the epilogue's warps), kRowLimits (rows of a tile
-//   see unlike numbers of keys); tmap_q, tmap_k, tmap_v; seg; q_bytes() of a query tile
+//   kDim, kChunks (of an item, at most), kConvert (tiles arrive as bytes and are converted by the epilogue's warps),
+//     kRowLimits (rows of a tile see unlike numbers of keys);  tmap_q, tmap_k, tmap_v;  seg;  q_bytes() of a query tile
 //   Work: an item -- ntiles (0: no more work), q0[2] (first row of each tile), seg_end, q_head(t), nkv and last_keys
 //     (key tiles, and keys in the last of them; 0 for none), partial (entry whose partial results the item
 //     writes, -1 for o itself)

@@ -389,6 +389,22 @@ constexpr size_t paged_split_bytes(int head_dim) {
   return static_cast<size_t>(kSplitMaxEntries) * (kPagedEntryBytes + sizeof(uint32_t)) +
          static_cast<size_t>(kSplitMaxEntries) * 2 * 128 * (head_dim + 1) * sizeof(float);
 }
+// An e4m3 cache's pages as bf16 (a page a slot, [slots, heads, page, D] of K, then of V) behind a table of the slots:
+// segment g's page p is slot g * per_segment + p.
+struct PagedUnpackArgs {
+  PagedSegments seg;  // of the cache
+  const uint8_t *k, *v, *k_scale, *v_scale;
+  int per_segment;
+  int32_t* table;
+  __nv_bfloat16 *k_out, *v_out;
+  unsigned int* err;
+};
+constexpr size_t paged_unpack_table_bytes(int64_t slots) { return (static_cast<size_t>(slots) * 4 + 255) / 256 * 256; }
+constexpr size_t paged_unpack_cache_elements(int64_t slots, int heads, int page_size, int head_dim) {
+  return static_cast<size_t>(slots) * heads * page_size * head_dim;
+}
+cudaError_t launch_paged_unpack(const PagedUnpackArgs& a, int head_dim, cudaStream_t stream);
+
 struct PagedTileArgs {
   CUtensorMap tmap_q;          // {D, H, rows}, a box of a key head's query heads x 128 / their number
   CUtensorMap tmap_k, tmap_v;  // {D, page, pages x heads}, a box of a page (128 rows of it at most)

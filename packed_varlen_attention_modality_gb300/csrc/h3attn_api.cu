@@ -675,15 +675,41 @@ bool paged_few_rows(const h3_paged_attn_desc* d) {
   return static_cast<int64_t>(d->max_seqlen_q) * (d->num_q_heads / d->num_kv_heads) <= h3::kPagedTokenRows;
 }
 
+// Bytes for the least workspace: a plan and, of long segments, the chunks' partial results.
+size_t paged_least_bytes(const h3_paged_attn_desc* d) {
+  const int group = d->num_q_heads / d->num_kv_heads;
+  if (paged_few_rows(d)) return h3::paged_token_bytes(d->max_seqlen_q * group, d->head_dim);
+  return h3::paged_plan_bytes(d->capacity_q, d->num_segments, 128 / group) +
+         (d->max_seqlen_k >= h3::kSplitMinSeqlen ? h3::paged_split_bytes(d->head_dim) : 0);
+}
+
+// An e4m3 cache is unpacked to bf16 first when more than kUnpackRows rows of a key head read each key (a third pair of
+// query tiles would convert it again) and the bf16 pages fit kUnpackMost bytes.  Converted as read against unpacked
+// first, 8 key heads x 128: 2 x 512 rows over 20,000 tokens 118 / 130 us, 600 rows 161 / 151, 2,048 rows 358 / 321;
+// with 40 query heads 4 x 512 rows over 12,000 tokens 561 / 397; x 64: 16 x 512 rows over 4,000 tokens 132 / 138, 800
+// rows 210 / 198.
+constexpr int kUnpackRows = 512;
+constexpr size_t kUnpackMost = size_t{4} << 30;
+int paged_unpack_pages(const h3_paged_attn_desc* d) {  // slots of a segment
+  const int64_t pages = (static_cast<int64_t>(d->max_seqlen_k) + d->page_size - 1) / d->page_size;
+  return static_cast<int>(pages < d->max_pages ? pages : d->max_pages);
+}
+size_t paged_unpack_bytes(const h3_paged_attn_desc* d) {  // 0: tiles are converted as they are read
+  const int64_t slots = static_cast<int64_t>(paged_unpack_pages(d)) * d->num_segments;
+  if (d->cache_type != H3_TYPE_E4M3 || d->num_pages == 0 || slots == 0 || slots > INT32_MAX / d->num_kv_heads ||
+      static_cast<int64_t>(d->max_seqlen_q) * (d->num_q_heads / d->num_kv_heads) <= kUnpackRows)
+    return 0;
+  const size_t bytes = 4 * h3::paged_unpack_cache_elements(slots, d->num_kv_heads, d->page_size, d->head_dim);
+  return bytes <= kUnpackMost ? h3::paged_unpack_table_bytes(slots) + bytes : 0;
+}
+
 }  // namespace
 
 size_t h3_paged_attn_workspace_size(const h3_paged_attn_desc* d) {
   if (d == nullptr || !paged_sizes_ok(d) || d->num_segments == 0 || d->max_seqlen_q == 0) return 0;
   if (d->head_dim != 64 && d->head_dim != 128) return 0;
-  if (paged_few_rows(d))
-    return h3::paged_token_bytes(d->max_seqlen_q * (d->num_q_heads / d->num_kv_heads), d->head_dim);
-  return h3::paged_plan_bytes(d->capacity_q, d->num_segments, 128 / (d->num_q_heads / d->num_kv_heads)) +
-         (d->max_seqlen_k >= h3::kSplitMinSeqlen ? h3::paged_split_bytes(d->head_dim) : 0);
+  const size_t least = paged_least_bytes(d), unpack = paged_unpack_bytes(d);
+  return unpack == 0 ? least : (least + 255) / 256 * 256 + unpack;
 }
 
 h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* d, const void* q, const void* k_cache, const void* v_cache,
@@ -706,7 +732,7 @@ h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* d, const void* q, const vo
   if (q == nullptr || o == nullptr || cu_seqlens_q == nullptr || seqused_k == nullptr ||
       (d->max_pages > 0 && block_table == nullptr) || (d->num_pages > 0 && (k_cache == nullptr || v_cache == nullptr)))
     return H3_ERR_NULL;
-  const size_t need = h3_paged_attn_workspace_size(d);
+  const size_t need = paged_least_bytes(d), unpack = paged_unpack_bytes(d), unpack_at = (need + 255) / 256 * 256;
   if (workspace == nullptr || workspace_bytes < need) return H3_ERR_WORKSPACE;
   if (!device_is_sm103()) return H3_ERR_UNSUPPORTED;
   unsigned int* err = device_error_ptr();
@@ -739,14 +765,40 @@ h3_status h3_paged_attn_fwd(const h3_paged_attn_desc* d, const void* q, const vo
   h3::PagedTileArgs a{};
   // no page at all: any valid map will do, every row is masked
   const bool none = d->num_pages == 0;
-  const int64_t planes = static_cast<int64_t>(d->num_pages) * d->num_kv_heads;
-  if (!make_qkv_map(&a.tmap_q, q, d->capacity_q, d->num_q_heads, d->head_dim, q_stride, group, 128 / group) ||
-      !make_cache_map(&a.tmap_k, none ? q : k_cache, e4m3, none ? 1 : planes, none ? 1 : d->page_size, d->head_dim) ||
-      !make_cache_map(&a.tmap_v, none ? q : v_cache, e4m3, none ? 1 : planes, none ? 1 : d->page_size, d->head_dim))
-    return H3_ERR_CUDA;
   a.seg = seg;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
+  const void *keys = none ? q : k_cache, *values = none ? q : v_cache;
+  if (unpack > 0 && workspace_bytes >= unpack_at + unpack) {
+    h3::PagedUnpackArgs u{};
+    u.seg = seg;
+    u.k = static_cast<const uint8_t*>(k_cache);
+    u.v = static_cast<const uint8_t*>(v_cache);
+    u.k_scale = k_scale;
+    u.v_scale = v_scale;
+    u.per_segment = paged_unpack_pages(d);
+    const int slots = u.per_segment * d->num_segments;
+    uint8_t* at = static_cast<uint8_t*>(workspace) + unpack_at;
+    u.table = reinterpret_cast<int32_t*>(at);
+    u.k_out = reinterpret_cast<__nv_bfloat16*>(at + h3::paged_unpack_table_bytes(slots));
+    u.v_out = u.k_out + h3::paged_unpack_cache_elements(slots, d->num_kv_heads, d->page_size, d->head_dim);
+    u.err = err;
+    const cudaError_t e = h3::launch_paged_unpack(u, d->head_dim, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return H3_ERR_CUDA;
+    // from here on a bf16 cache of the slots
+    keys = u.k_out;
+    values = u.v_out;
+    a.k_scale = a.v_scale = nullptr;
+    a.seg.table.pages = u.table;
+    a.seg.table.per_segment = u.per_segment;
+    a.seg.table.num_pages = slots;
+  }
+  const bool bytes = a.k_scale != nullptr;
+  const int64_t planes = none ? 1 : static_cast<int64_t>(a.seg.table.num_pages) * d->num_kv_heads;
+  if (!make_qkv_map(&a.tmap_q, q, d->capacity_q, d->num_q_heads, d->head_dim, q_stride, group, 128 / group) ||
+      !make_cache_map(&a.tmap_k, keys, bytes, planes, none ? 1 : d->page_size, d->head_dim) ||
+      !make_cache_map(&a.tmap_v, values, bytes, planes, none ? 1 : d->page_size, d->head_dim))
+    return H3_ERR_CUDA;
   a.o = o;
   a.wide = aligned32(o);
   a.lse = lse;

@@ -9,6 +9,15 @@
 // with its rows' scales, and the epilogue's warps, idle between items, turn it into bf16 in shared memory (exactly);
 // the products and the softmax then are those of a bf16 cache.
 //
+// What it measured: 2,000 rows over 58,758 bf16 tokens, causal by frame, 24 heads x 128, 873 to 915 us (1,650 TFLOP/s,
+// at the power cap as the packed kernel is); first chunks of 900 to 4,096 tokens, 24 heads on 8 x 64, 78 us, of which
+// the plan is 6 and the join 8.  Two chunks of 1,000 to 1,500 rows over 14,000 to 24,000 e4m3 tokens, 40 heads x 128,
+// took 1,025 us converted as they are read: shared memory's bandwidth bounds that, for a step of 2,700 cycles moves the
+// operands of the products (1,536 cycles of 128 bytes), the arriving bytes (256) and the conversion's reads and writes
+// (768); without the conversion it took 667 us, without its arithmetic 828, with a second converting warpgroup 1,338.
+// Where an item's keys are converted more than twice the host has them unpacked first (842 us; some 200 are the
+// unpacking, at the rate of a plain copy), and this file sees a bf16 cache.
+//
 // Causal by blocks of tokens: an item's key tiles end at its last row's limit, a tile in which some row sees less is
 // masked row by row, others are not.  Items come with the longest first and waves alternate in direction, so the
 // CTAs' sums stay near one another; what a last, partly filled wave and unlike items leave idle is evened out by
@@ -179,7 +188,9 @@ paged_plan_kernel(const __grid_constant__ PagedSegments seg, int tokens, uint32_
     return;
   }
   __syncthreads();  // the list is complete (written by this CTA: the barrier makes it visible here)
-  auto tiles_at = [&](uint32_t item) -> uint32_t { return sorted ? s_sorted[item / heads] : key_tiles(list[item / heads].keys); };
+  auto tiles_at = [&](uint32_t item) -> uint32_t {
+    return sorted ? s_sorted[item / heads] : key_tiles(list[item / heads].keys);
+  };
   uint32_t load = 0;
   if (tid < wave) {
     for (uint32_t w = 0; w < waves; ++w) load += tiles_at(item_of(w, tid, wave)) + kCostItem;

@@ -1,8 +1,9 @@
 // Attention over a paged cache for a few rows per segment (the single tokens of running streams): every key
 // row is read once and meets at most 16 query rows, so the call is bound by reading K and V.
 //
-// Work is laid out in units of 64 keys (e4m3: 128, or 256 of 64 values) of a (segment, key head) and dealt to two CTAs an SM in equal shares, so
-// streams of unlike lengths keep the GPU even; every CTA finds its share by a scan of the lengths.  A pair that a
+// Work is laid out in units of 64 keys (e4m3: 128, or 256 of 64 values) of a (segment, key head) and dealt to two
+// CTAs an SM in equal shares, so streams of unlike lengths keep the GPU even; every CTA finds its share by a scan of
+// the lengths.  A pair that a
 // share's end cuts leaves fp32 partial results (O normalised by its own sum, and the LSE), which a second kernel
 // joins in order.  The 16 rows of the tensor-core tile are the segment's rows times the query heads that share
 // the key head, so shared heads cost no second read.  Each of a CTA's four warps streams blocks of 16 (32, 64) keys of K
@@ -14,9 +15,14 @@
 // scores and the weights, which are fp32.  Q's rows are brought to f16 by a power of two each (their largest value to
 // 2^14: what that rounds is 2^-39 of it at most).  The weights of V's rows are 2^(score + V's exponent), kept
 // under 2^8 by a reference of their own that follows their largest, so that f16 rounds each by 2^-11 of itself (2^-25
-// of the reference below 2^-14 of it; bf16 rounds by 2^-8).  The order of the dims in S's product and in O's columns is chosen so that a
-// lane's bytes lie together.
+// of the reference below 2^-14 of it; bf16 rounds by 2^-8).  The order of the dims in S's product and in O's columns
+// is chosen so that a lane's bytes lie together.
 // Scores, max, sum and O are fp32; P is rounded to bf16 (f16) for the product with V, o once at the end.
+//
+// 32 streams of 512 to 4,096 tokens, 64 heads on 8 x 128, bf16: 62 us (floor 48; some 9 us are the launch, the scan
+// and the join; 128 streams of 4,096 tokens read at the rate of a plain copy).  Two streams of 90,000 to 100,000
+// tokens, 40 heads on 8 x 128, e4m3: 84 us (floor 57): there the instructions that turn bytes into f16 and take the
+// softmax bound it, 124 us with a conversion to bf16.  Eight warps in one CTA an SM: 93 us.
 #include <cuda_bf16.h>
 
 #include "h3_internal.h"

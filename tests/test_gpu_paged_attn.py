@@ -276,6 +276,74 @@ def test_chunks(h3, dev, shape, e4m3, d):
     case.check(*_run(h3, dev, case))
 
 
+# more than 512 rows of a key head over an e4m3 cache: it is unpacked first, where the workspace has room
+UNPACKED = [
+    ([513], [513], 1, 1, 16, 1),
+    ([600, 0, 3], [1400, 900, 77], 2, 2, 32, 0),       # a segment without new rows is not unpacked
+    ([300, 700], [20, 1300], 4, 2, 64, 50),            # more rows than tokens
+    ([140, 5], [1000, 0], 24, 3, 128, 7),
+    ([1030], [2100], 1, 1, 256, 1),
+]
+
+
+@pytest_gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", UNPACKED)
+def test_unpacked_chunks(h3, dev, shape, d):
+    lq, lk, hq, hk, page, block = shape
+    case = Case(lq, lk, hq, hk, d, page, True, block, seed=d)
+    a = case.on(dev)
+    sizes = [h3.paged_attn_workspace_size(len(lq), case.max_q, case.max_k, a["q"].shape[0], hq, hk, d, page, e4m3=e,
+                                          max_pages=a["block_table"].shape[1]) for e in (False, True)]
+    pages = len(lq) * -(-case.max_k // page)
+    assert sizes[1] - sizes[0] >= 4 * pages * page * hk * d
+    space = torch.full((sizes[1],), 255, dtype=torch.uint8, device=dev)  # NaN wherever the call does not write
+    out, lse = _run(h3, dev, case, workspace=space)
+    case.check(out, lse)
+    again, lse2 = _run(h3, dev, case, workspace=space[:sizes[0]].fill_(255))
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    # captured, then replayed with fewer tokens of each sequence, while another call runs beside it
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        got = h3.paged_attn_fwd(**a)
+    a["seqused_k"].sub_(3).clamp_(min=0)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    graph.replay()
+    with torch.cuda.stream(other):
+        want = h3.paged_attn_fwd(**a)
+    torch.cuda.synchronize()
+    assert torch.equal(got[:case.n], want[:case.n]) and h3.get_device_error(dev) == 0
+
+
+@pytest_gpu
+def test_unpacked_bad_lengths_and_pages(h3, dev):
+    case = Case([520, 520, 520], [700, 650, 90], 2, 2, 64, 16, True, 1)
+    good = case.on(dev)
+    want = h3.paged_attn_fwd(**good)
+    for what, status in (("used", 3), ("negative", 3), ("long", 3), ("page", 12), ("below", 12)):
+        a = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in good.items()}
+        same = [0, 1, 2]
+        if what == "used":
+            a["seqused_k"][1], same = 16 * a["block_table"].shape[1] + 1, [0, 2]
+        elif what == "negative":
+            a["seqused_k"][1], same = -1, [0, 2]
+        elif what == "long":  # the first is past what the bound makes room for
+            a["max_seqlen_k"], same = 660, [1, 2]
+        else:
+            a["block_table"][2, 1], same = (a["k_cache"].shape[0] if what == "page" else -3), [0, 1]
+        out = torch.full_like(a["q"], 5.0)
+        h3.paged_attn_fwd(**a, out=out)
+        torch.cuda.synchronize()
+        assert h3.get_device_error(dev) == status, what
+        for g in range(3):
+            part = slice(520 * g, 520 * (g + 1))
+            if g in same:
+                assert torch.equal(out[part], want[part]), (what, g)
+            elif status == 3:
+                assert torch.all(out[part] == 5.0), (what, g)
+
+
 @pytest_gpu
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_chunk_large_scores_and_scale(h3, dev, e4m3):
