@@ -179,7 +179,8 @@ cudaError_t launch(const KvCacheArgs& a, bool write, int sms, cudaStream_t strea
 }
 
 // An e4m3 cache's pages as bf16, for a call that reads each of them many times.  A warp takes 16 rows of a (slot, key
-// head) of K or V: eight bytes a lane and load, all of them under way before the first is used.
+// head) of K or V: eight bytes a lane and load, all of them under way before the first is used.  The warps count the
+// pages in use alone, 32 segments at once, so loose bounds cost nothing.
 template <int D>
 __global__ void __launch_bounds__(kThreads) paged_unpack_kernel(const __grid_constant__ PagedUnpackArgs a) {
   constexpr int kRows = 16, kLoads = kRows * D / (32 * 8), kLanes = D / 8;
@@ -187,38 +188,54 @@ __global__ void __launch_bounds__(kThreads) paged_unpack_kernel(const __grid_con
   launch_dependents();
   const int lane = threadIdx.x & 31, shift = a.seg.table.page_shift, heads = a.seg.num_kv_heads;
   const uint32_t parts = 2u << (shift - 4), units = heads * parts;  // of a slot
-  const uint32_t slots = static_cast<uint32_t>(a.seg.num_segments) * a.per_segment;
-  const uint64_t all = static_cast<uint64_t>(slots) * units, warps = static_cast<uint64_t>(gridDim.x) * kWarps;
-  for (uint64_t u = static_cast<uint64_t>(blockIdx.x) * kWarps + threadIdx.x / 32; u < all; u += warps) {
-    const uint32_t slot = static_cast<uint32_t>(u / units);
-    const uint32_t unit = static_cast<uint32_t>(u - static_cast<uint64_t>(slot) * units);
-    const int g = slot / a.per_segment, p = slot - g * a.per_segment;
-    if (unit == 0 && lane == 0) a.table[slot] = static_cast<int>(slot);
-    const uint32_t head = unit / parts, part = unit % parts;
-    const int row = static_cast<int>(part / 2) * kRows;
-    const int64_t at = (static_cast<int64_t>(p) << shift) + row;
-    const PagedSegment s = checked_paged_segment(a.seg, g, nullptr);  // (the plan records what is wrong with it)
-    if (s.rows == 0 || at >= s.used) continue;
-    int id = page_id(a.seg.table, g, p);
-    if (!page_ok(a.seg.table, id)) {
-      record_error(a.err, kErrBadPage);
-      id = 0;
+  const uint32_t warps = gridDim.x * kWarps;
+  uint32_t at = blockIdx.x * kWarps + threadIdx.x / 32, before = 0;  // this warp's unit, those of earlier segments
+  for (int g0 = 0; g0 < a.seg.num_segments; g0 += 32) {
+    int used = 0;  // (the plan records what is wrong with a segment, and skips one past the slots)
+    if (g0 + lane < a.seg.num_segments) {
+      const PagedSegment s = checked_paged_segment(a.seg, g0 + lane, nullptr);
+      if (s.rows > 0 && s.used <= static_cast<int64_t>(a.per_segment) << shift) used = s.used;
     }
-    const size_t from = (static_cast<size_t>(id) * heads + head << shift) + row;
-    const size_t to = (static_cast<size_t>(slot) * heads + head << shift) + row;
-    const uint8_t* in = (part & 1 ? a.v : a.k) + from * D + lane * 8;
-    const uint8_t* scale = (part & 1 ? a.v_scale : a.k_scale) + from + lane / kLanes;
-    __nv_bfloat16* out = (part & 1 ? a.v_out : a.k_out) + to * D + lane * 8;
-    uint2 w[kLoads];
-    uint32_t byte[kLoads];
+    const uint32_t mine = ((used + (1 << shift) - 1) >> shift) * units;
+    uint32_t end = mine;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      w[i] = __ldcs(reinterpret_cast<const uint2*>(in + i * 256));
-      byte[i] = scale[i * (32 / kLanes)];
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
     }
+    const uint32_t all = __shfl_sync(0xffffffffu, end, 31);
+    for (; at - before < all; at += warps) {
+      const uint32_t in = at - before;
+      const int l = __popc(__ballot_sync(0xffffffffu, end <= in));  // the lane whose segment it is
+      const int g = g0 + l, tokens = __shfl_sync(0xffffffffu, used, l);
+      const uint32_t rest = in - __shfl_sync(0xffffffffu, end - mine, l);
+      const uint32_t p = rest / units, unit = rest - p * units, head = unit / parts, part = unit - head * parts;
+      const size_t slot = static_cast<size_t>(g) * a.per_segment + p;
+      if (unit == 0 && lane == 0) a.table[slot] = static_cast<int>(slot);
+      const int row = static_cast<int>(part / 2) * kRows;
+      if (static_cast<int64_t>(p << shift) + row >= tokens) continue;
+      int id = page_id(a.seg.table, g, p);
+      if (!page_ok(a.seg.table, id)) {
+        record_error(a.err, kErrBadPage);
+        id = 0;
+      }
+      const size_t from = (static_cast<size_t>(id) * heads + head << shift) + row;
+      const size_t to = (slot * heads + head << shift) + row;
+      const uint8_t* in8 = (part & 1 ? a.v : a.k) + from * D + lane * 8;
+      const uint8_t* scale = (part & 1 ? a.v_scale : a.k_scale) + from + lane / kLanes;
+      __nv_bfloat16* out = (part & 1 ? a.v_out : a.k_out) + to * D + lane * 8;
+      uint2 w[kLoads];
+      uint32_t byte[kLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      *reinterpret_cast<uint4*>(out + i * 256) = e4m3x8_bf16(w[i], scale_of(byte[i]));
+      for (int i = 0; i < kLoads; ++i) {
+        w[i] = __ldcs(reinterpret_cast<const uint2*>(in8 + i * 256));
+        byte[i] = scale[i * (32 / kLanes)];
+      }
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        *reinterpret_cast<uint4*>(out + i * 256) = e4m3x8_bf16(w[i], scale_of(byte[i]));
+    }
+    before += all;
   }
 }
 
