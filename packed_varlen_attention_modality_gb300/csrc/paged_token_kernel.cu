@@ -96,6 +96,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// An 8 x 8 tile of 16-bit values with rows and columns exchanged: lane l's pair of row l / 4 becomes that of column l / 4.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 // The part of a (segment, key head) pair that a CTA takes: keys [first, end).
 struct Piece {
   PagedSegment s;
@@ -143,9 +150,11 @@ __device__ __forceinline__ float* partial_of(const PagedTokenArgs& a, int cta, i
   return a.partials + (static_cast<size_t>(cta) * 2 + slot) * paged_token_partial(a.max_rows, D);
 }
 
-template <int D, bool kE4m3>
+// kNarrow (e4m3, at most eight rows): keys are the products' rows and query rows their columns.
+template <int D, bool kE4m3, bool kNarrow>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
+  static_assert(kE4m3 || !kNarrow);
   using C = Cfg<D, kE4m3>;
   constexpr int kStages = C::kStages, kSteps = C::kSteps, kBlock = C::kBlock, kUnit = C::kUnit;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -158,7 +167,19 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
   const int S = a.seg.num_segments, heads = a.seg.num_kv_heads, block = a.seg.causal_block;
   const int group = a.seg.num_q_heads / heads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int gr = lane >> 2, quad = lane & 3, c2 = quad * 2;  // this lane's rows gr, gr + 8 and column pair
+  const int gr = lane >> 2, quad = lane & 3, c2 = quad * 2;  // this lane's rows gr, gr + 8 and columns c2, c2 + 1
+  // of a tile of scores, of which it has kValues of each of two query rows
+  constexpr int kScores = kNarrow ? kSteps : 2 * kSteps, kValues = 2 * kScores;
+  auto row_of = [&](int h) { return kNarrow ? c2 + h : gr + 8 * h; };
+  auto key_of = [&](int v) { return kNarrow ? (v >> 1) * 16 + gr + 8 * (v & 1) : (v >> 1) * 8 + c2 + (v & 1); };
+  auto value = [](float (&x)[kScores][4], int h, int v) -> float& {
+    return kNarrow ? x[v >> 1][2 * (v & 1) + h] : x[v >> 1][2 * h + (v & 1)];
+  };
+  auto over_row = [](float x, auto op) {  // over the lanes that share a query row
+#pragma unroll
+    for (int o = kNarrow ? 4 : 1; o < (kNarrow ? 32 : 4); o *= 2) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  };
   unsigned int* scan_err = blockIdx.x == 0 ? a.err : nullptr;  // one CTA records what is wrong with the offsets
 
   // ---- this CTA's share of the units
@@ -312,7 +333,9 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         const int r = gr + 8 * h;
         const __nv_bfloat16* row = a.q + static_cast<size_t>(p.s.q0 + r / group) * a.q_stride +
                                    (p.head * group + r % group) * D;
-        if (kE4m3) {  // step kk: dims 4 kk + {0, 1} and {2, 3} of the lane's D / 4
+        if (kNarrow && h == 1) {
+          // (its only row is gr)
+        } else if (kE4m3) {  // step kk: dims 4 kk + {0, 1} and {2, 3} of the lane's D / 4
           const uint2* src = reinterpret_cast<const uint2*>(row + quad * (D / 4));
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -328,12 +351,13 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
             q[kk][2 + h] = r < rows ? src[kk * 8 + 4] : 0u;
           }
         }
-        limit[h] = r < rows ? row_limit(p.s, r / group, block) : p.end;
+        const int scored = row_of(h);
+        limit[h] = scored < rows ? row_limit(p.s, scored / group, block) : p.end;
       }
       float q_scale[2] = {1.f, 1.f};  // e4m3: what the f16 rows are to be multiplied with
       if (kE4m3) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < (kNarrow ? 1 : 2); ++h) {
           uint32_t most = 0u;  // the largest magnitude's bits (of both halves: the upper decides)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
@@ -356,10 +380,17 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
               x = pack_f16x2(__uint_as_float(x << 16) * inv, __uint_as_float(x & 0xffff0000u) * inv);
             }
         }
+        if (kNarrow) {  // of the rows whose scores the lane has
+          const float own = q_scale[0];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) q_scale[h] = __shfl_sync(0xffffffffu, own, 4 * (c2 + h));
+        }
       }
       low = min(low, row_limit(p.s, 0, block));
 
-      float o[D / 8][4] = {};
+      // wide: column tile n of the rows; narrow: dims gr * D / 8 + 2 n and the next, of rows c2 and c2 + 1
+      constexpr int kTiles = kNarrow ? D / 16 : D / 8;
+      float o[kTiles][4] = {};
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
       float top_w[2] = {-INFINITY, -INFINITY};  // e4m3: log2 of the weights' reference
       const int nblocks = (p.end - p.first + kBlock - 1) / kBlock;
@@ -376,7 +407,7 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         const uint8_t* base = ring + stage * C::kStageBytes;
         const int key = p.first + b * kBlock;
         const int mat = lane >> 3, mr = lane & 7;
-        float sc[2 * kSteps][4] = {};
+        float sc[kScores][4] = {};
 #pragma unroll
         for (int step = 0; step < kSteps; ++step) {
           if (!kE4m3) {
@@ -389,15 +420,38 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
             }
             continue;
           }
+          if constexpr (kNarrow) {
+            const int row = 16 * step + gr;
 #pragma unroll
-          for (int n = 2 * step; n < 2 * step + 2; ++n) {
+            for (int x = 0; x < D / 64; ++x) {
+              const uint4 k0 = *reinterpret_cast<const uint4*>(base + C::piece_at(row, quad * (D / 64) + x));
+              const uint4 k1 = *reinterpret_cast<const uint4*>(base + C::piece_at(row + 8, quad * (D / 64) + x));
+              const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t f[4] = {e4m3_pair_f16<0>(w0[i]), e4m3_pair_f16<0>(w1[i]), e4m3_pair_f16<1>(w0[i]),
+                                       e4m3_pair_f16<1>(w1[i])};
+                mma_16816_f16(sc[step], f, q[4 * x + i][0], q[4 * x + i][2]);
+              }
+            }
+#pragma unroll
+            for (int v = 2 * step; v < 2 * step + 2; ++v) {
+              const float scale = scale_of(base[2 * C::kHalf + key_of(v)]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) value(sc, h, v) *= scale * q_scale[h];
+            }
+            continue;
+          }
+#pragma unroll
+          for (int n = 2 * step; n < (kNarrow ? 0 : 2 * step + 2); ++n) {
             const int row = n * 8 + gr;
 #pragma unroll
             for (int x = 0; x < D / 64; ++x) {
               const uint4 w4 = *reinterpret_cast<const uint4*>(base + C::piece_at(row, quad * (D / 64) + x));
               const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma_16816_f16(sc[n], q[4 * x + i], e4m3_pair_f16<0>(w[i]), e4m3_pair_f16<1>(w[i]));
+              for (int i = 0; i < 4; ++i)
+                mma_16816_f16(sc[n], q[4 * x + i], e4m3_pair_f16<0>(w[i]), e4m3_pair_f16<1>(w[i]));
             }
             const uint32_t ks = *reinterpret_cast<const uint16_t*>(base + 2 * C::kHalf + n * 8 + c2);
             const float s0 = scale_of(ks & 0xffu), s1 = scale_of(ks >> 8);
@@ -409,31 +463,36 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         }
         if (key + kBlock > low) {  // by select, so NaN/Inf there is discarded
 #pragma unroll
-          for (int n = 0; n < 2 * kSteps; ++n)
+          for (int v = 0; v < kValues; ++v)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (key + n * 8 + c2 + (i & 1) >= min(limit[i >> 1], p.end)) sc[n][i] = -INFINITY;
+            for (int h = 0; h < 2; ++h)
+              if (key + key_of(v) >= min(limit[h], p.end)) value(sc, h, v) = -INFINITY;
         }
         // e4m3: the log2 of V's rows' weights, score and V's exponent together (a masked key's stays -inf: past the end
         // lie rows whose scale may be anything)
-        float u[2 * kSteps][4];
+        float u[kScores][4];
         if (kE4m3) {
 #pragma unroll
-          for (int n = 0; n < 2 * kSteps; ++n) {
-            const uint32_t vs = *reinterpret_cast<const uint16_t*>(base + 2 * C::kHalf + kBlock + n * 8 + c2);
-            const float v0 = scale_log2_of(vs & 0xffu), v1 = scale_log2_of(vs >> 8);
+          for (int v = 0; v < kValues; v += 2) {
+            const uint8_t* vs = base + 2 * C::kHalf + kBlock;
+            uint32_t pair;
+            if (kNarrow) pair = vs[key_of(v)] | vs[key_of(v + 1)] << 8;
+            else pair = *reinterpret_cast<const uint16_t*>(vs + key_of(v));
+            const float v0 = scale_log2_of(pair & 0xffu), v1 = scale_log2_of(pair >> 8);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              u[n][i] = sc[n][i] == -INFINITY ? -INFINITY : fmaf(sc[n][i], scale_log2, i & 1 ? v1 : v0);
+            for (int h = 0; h < 2; ++h) {
+              const float s0 = value(sc, h, v), s1 = value(sc, h, v + 1);
+              value(u, h, v) = s0 == -INFINITY ? -INFINITY : fmaf(s0, scale_log2, v0);
+              value(u, h, v + 1) = s1 == -INFINITY ? -INFINITY : fmaf(s1, scale_log2, v1);
+            }
           }
         }
-        // row maxima over the quad; a reference moves only when it grows by more than 2^8
-        auto row_max = [&](const float (&x)[2 * kSteps][4], int h) {
-          float y = fmaxf(x[0][2 * h], x[0][2 * h + 1]);
+        // row maxima; a reference moves only when it grows by more than 2^8
+        auto row_max = [&](float (&x)[kScores][4], int h) {
+          float y = fmaxf(value(x, h, 0), value(x, h, 1));
 #pragma unroll
-          for (int n = 1; n < 2 * kSteps; ++n) y = fmax3(y, x[n][2 * h], x[n][2 * h + 1]);
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
-          return fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+          for (int v = 2; v < kValues; v += 2) y = fmax3(y, value(x, h, v), value(x, h, v + 1));
+          return over_row(y, [](float p, float q) { return fmaxf(p, q); });
         };
         float alpha[2] = {1.f, 1.f};  // of O
         bool moved = false;
@@ -460,25 +519,36 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n)
+          for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][i] *= alpha[i >> 1];
+            for (int i = 0; i < 4; ++i) o[n][i] *= alpha[kNarrow ? i & 1 : i >> 1];
         }
         uint32_t pw[kSteps][4];
+        float weight[2][kNarrow ? 2 : 1];  // of two keys, of both rows
 #pragma unroll
-        for (int n = 0; n < 2 * kSteps; ++n)
+        for (int v = 0; v < kValues; v += 2)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint32_t& w = pw[n / 2][2 * (n & 1) + h];
             const float mb = m[h] == -INFINITY ? 0.f : m[h] * scale_log2;
-            const float e0 = ex2_approx(fmaf(sc[n][2 * h], scale_log2, -mb));
-            const float e1 = ex2_approx(fmaf(sc[n][2 * h + 1], scale_log2, -mb));
+            const float e0 = ex2_approx(fmaf(value(sc, h, v), scale_log2, -mb));
+            const float e1 = ex2_approx(fmaf(value(sc, h, v + 1), scale_log2, -mb));
             l[h] += e0 + e1;
+            const int n = v / 2;
             if (kE4m3) {
               const float wb = top_w[h] == -INFINITY ? 0.f : top_w[h];
-              w = pack_f16x2(ex2_approx(u[n][2 * h] - wb), ex2_approx(u[n][2 * h + 1] - wb));
+              const float w0 = ex2_approx(value(u, h, v) - wb), w1 = ex2_approx(value(u, h, v + 1) - wb);
+              if constexpr (kNarrow) {
+                weight[0][h] = w0;
+                weight[1][h] = w1;
+                if (h == 1) {
+#pragma unroll
+                  for (int k = 0; k < 2; ++k) pw[n][k] = transpose8x8(pack_f16x2(weight[k][0], weight[k][1]));
+                }
+              } else {
+                pw[n / 2][2 * (n & 1) + h] = pack_f16x2(w0, w1);
+              }
             } else {
-              w = pack_bf16x2(e0, e1);
+              pw[n / 2][2 * (n & 1) + h] = pack_bf16x2(e0, e1);
             }
           }
 #pragma unroll
@@ -515,8 +585,13 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
           for (int j = 0; j < D / 8; j += 2) {  // bytes j and j + 1 of two keys each, in one word
             const uint32_t pick = j % 4 == 0 ? 0x5140 : 0x7362;
             const uint32_t lo = __byte_perm(w[0][j / 4], w[1][j / 4], pick), hi = __byte_perm(w[2][j / 4], w[3][j / 4], pick);
-            mma_16816_f16(o[j], pw[step], e4m3_pair_f16<0>(lo), e4m3_pair_f16<0>(hi));
-            mma_16816_f16(o[j + 1], pw[step], e4m3_pair_f16<1>(lo), e4m3_pair_f16<1>(hi));
+            const uint32_t f[4] = {e4m3_pair_f16<0>(lo), e4m3_pair_f16<1>(lo), e4m3_pair_f16<0>(hi), e4m3_pair_f16<1>(hi)};
+            if constexpr (kNarrow) {
+              mma_16816_f16(o[j / 2], f, pw[step][0], pw[step][1]);
+            } else {
+              mma_16816_f16(o[j], pw[step], f[0], f[2]);
+              mma_16816_f16(o[j + 1], pw[step], f[1], f[3]);
+            }
           }
         }
         __syncwarp();  // the stage is read: it may be loaded again
@@ -526,12 +601,11 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
       // ---- the warps, added in order
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-        l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        if (quad == 0) {
-          s_m[warp][gr + 8 * h] = m[h];
-          s_l[warp][gr + 8 * h] = l[h];
-          s_w[warp][gr + 8 * h] = kE4m3 ? top_w[h] : m[h] * scale_log2;  // O's reference
+        l[h] = over_row(l[h], [](float p, float q) { return p + q; });
+        if (kNarrow ? gr == 0 : quad == 0) {
+          s_m[warp][row_of(h)] = m[h];
+          s_l[warp][row_of(h)] = l[h];
+          s_w[warp][row_of(h)] = kE4m3 ? top_w[h] : m[h] * scale_log2;  // O's reference
         }
       }
       __syncthreads();
@@ -540,8 +614,8 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
       for (int h = 0; h < 2; ++h) {
         float top = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_w[w][gr + 8 * h]);
-        f[h] = top == -INFINITY ? 0.f : ex2_approx(s_w[warp][gr + 8 * h] - top);  // 0 for a warp without keys
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_w[w][row_of(h)]);
+        f[h] = top == -INFINITY ? 0.f : ex2_approx(s_w[warp][row_of(h)] - top);  // 0 for a warp without keys
       }
 #pragma unroll 1
       for (int w = 0; w < kWarps; ++w) {
@@ -549,12 +623,12 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
+            for (int n = 0; n < kTiles; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const int col = kE4m3 ? (c2 + e) * (D / 8) + n : n * 8 + c2 + e;
-                float* dst = s_o + (gr + 8 * h) * C::kOut + col;
-                const float x = f[h] * o[n][2 * h + e];
+                const int col = kNarrow ? gr * (D / 8) + 2 * n + e : kE4m3 ? (c2 + e) * (D / 8) + n : n * 8 + c2 + e;
+                float* dst = s_o + row_of(h) * C::kOut + col;
+                const float x = f[h] * o[n][kNarrow ? 2 * e + h : 2 * h + e];
                 *dst = w == 0 ? x : *dst + x;
               }
         }
@@ -667,15 +741,15 @@ paged_token_join_kernel(const __grid_constant__ PagedTokenArgs a) {
   }
 }
 
-template <int D, bool kE4m3>
+template <int D, bool kE4m3, bool kNarrow>
 cudaError_t launch(const PagedTokenArgs& a, cudaStream_t stream) {
   using C = Cfg<D, kE4m3>;
-  cudaError_t e = allow_shared_memory<C::kSmemBytes>(paged_token_kernel<D, kE4m3>);
+  cudaError_t e = allow_shared_memory<C::kSmemBytes>(paged_token_kernel<D, kE4m3, kNarrow>);
   if (e != cudaSuccess) return e;
   const int sms = num_sms_of_current_device();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const int ctas = sms * kCtasPerSm < kPagedTokenCtas ? sms * kCtasPerSm : kPagedTokenCtas;
-  e = launch_programmatic(paged_token_kernel<D, kE4m3>, dim3(ctas), dim3(kThreads), C::kSmemBytes, stream, a);
+  e = launch_programmatic(paged_token_kernel<D, kE4m3, kNarrow>, dim3(ctas), dim3(kThreads), C::kSmemBytes, stream, a);
   if (e != cudaSuccess) return e;
   return launch_programmatic(paged_token_join_kernel<D>, dim3(ctas), dim3(kThreads), 0, stream, a);
 }
@@ -683,8 +757,9 @@ cudaError_t launch(const PagedTokenArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_paged_token(const PagedTokenArgs& a, int head_dim, cudaStream_t stream) {
-  if (a.k_scale != nullptr) return head_dim == 128 ? launch<128, true>(a, stream) : launch<64, true>(a, stream);
-  return head_dim == 128 ? launch<128, false>(a, stream) : launch<64, false>(a, stream);
+  if (a.k_scale == nullptr) return head_dim == 128 ? launch<128, false, false>(a, stream) : launch<64, false, false>(a, stream);
+  if (a.max_rows <= 8) return head_dim == 128 ? launch<128, true, true>(a, stream) : launch<64, true, true>(a, stream);
+  return head_dim == 128 ? launch<128, true, false>(a, stream) : launch<64, true, false>(a, stream);
 }
 
 }  // namespace h3
