@@ -13,8 +13,8 @@
 //
 // Memory-bound: the forward reads x, y and writes x', h once; the backward reads dx', dh, x', y and writes dx, dy
 // once.  Measured with a bf16 stream of 5,120 values a row: forward, 58,758 rows of four requests, a layer norm and a
-// gate, 378 us (floor 355 at the rate of a copy, 94 %); backward, 29,001 rows of three requests, both norms RMS, 375 us
-// (floor 263, 70 %; 298 without a branch norm, where a row needs fewer sums).
+// gate, 378 us (floor 355 at the rate of a copy, 94 %); backward, 29,001 rows of three requests, both norms RMS, 357 us
+// (floor 263, 74 %).
 //
 // A CTA takes a contiguous range of rows, so the request's vectors (w (1 + scale), shift, w_b gate) stay in registers
 // from row to row, 16 columns a thread, and so do the backward's column sums.  (8 columns, with the registers of twice
@@ -42,17 +42,37 @@ struct Vec8 {
 };
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ Vec8 all8(float v) { return Vec8{{both(v), both(v), both(v), both(v)}}; }
-__device__ __forceinline__ Vec8 load8(const __nv_bfloat16* p) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  Vec8 r;
+// Eight values as they lie in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ Vec8 values() const {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    Vec8 r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-  return r;
-}
-__device__ __forceinline__ Vec8 load8(const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  return Vec8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+    for (int i = 0; i < 4; ++i) r.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    return r;
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ Vec8 values() const {
+    return Vec8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+  }
+};
+template <typename T>
+__device__ __forceinline__ Vec8 load8(const T* p) {
+  Raw8<T> r;
+  r.load(p);
+  return r.values();
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const Vec8& r) {
   __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(r.p[0].x, r.p[0].y), pack_bf16x2(r.p[1].x, r.p[1].y),
@@ -512,11 +532,27 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
   };
   const bool layer = kLayer && a.norm == kNormLayer, branch_layer = kLayer && a.branch_norm == kNormLayer;
   const bool branch = has_y && a.branch_norm != kNormNone;
-  auto load_x = [&](int k) { return load8(reinterpret_cast<const X*>(ring.row(0)) + col[k]); };
-  auto load_g = [&](int k) { return load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(2)) + col[k]); };
-  auto load_y = [&](int k) { return load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(3)) + col[k]); };
+  // A row is read once and kept as it lies in memory for the second look, where the registers are there for it (29,001
+  // rows of 5,120: 357 us against 375; with a layer norm it spills: 20,000 rows 425 against 334).
+  constexpr bool kKeep = !kLayer && 65536 / (kThreads * kCtas) > 128;
+  Raw8<X> raw_x[kVecs], raw_d[kVecs];
+  Raw8<__nv_bfloat16> raw_g[kVecs], raw_y[kVecs];
+  auto fetch = [&](int k) {
+    if (has_h) raw_x[k].load(reinterpret_cast<const X*>(ring.row(0)) + col[k]);
+    if (has_dx) raw_d[k].load(reinterpret_cast<const X*>(ring.row(1)) + col[k]);
+    if (has_h) raw_g[k].load(reinterpret_cast<const __nv_bfloat16*>(ring.row(2)) + col[k]);
+    if (has_y) raw_y[k].load(reinterpret_cast<const __nv_bfloat16*>(ring.row(3)) + col[k]);
+  };
+  auto load_x = [&](int k) { return kKeep ? raw_x[k].values() : load8(reinterpret_cast<const X*>(ring.row(0)) + col[k]); };
+  auto load_g = [&](int k) {
+    return kKeep ? raw_g[k].values() : load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(2)) + col[k]);
+  };
+  auto load_y = [&](int k) {
+    return kKeep ? raw_y[k].values() : load8(reinterpret_cast<const __nv_bfloat16*>(ring.row(3)) + col[k]);
+  };
   auto load_d = [&](int k) {
-    return has_dx ? load8(reinterpret_cast<const X*>(ring.row(1)) + col[k]) : Vec8{};
+    if (!has_dx) return Vec8{};
+    return kKeep ? raw_d[k].values() : load8(reinterpret_cast<const X*>(ring.row(1)) + col[k]);
   };
   Vec8 t[kVecs], y[kVecs];  // (a layer norm) of the row whose dot product is on its way: t gate w_b and yh
   float2 ry = both(1.f);
@@ -560,6 +596,11 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
     //   sum t gate w_b y = sum dx' u + rs sum g u + rs dot sum xh u,  u = gate w_b y
     // With one, centring would double them: t is then summed when it is known, in an exchange of its own.
     const bool ok = ring.wait();
+    if (kKeep) {
+#pragma unroll
+      for (int k = 0; k < kVecs; ++k)
+        if (own[k]) fetch(k);
+    }
     float v[kTold];
     if constexpr (kLayer) {
       float wx = 0.f, wy = 0.f, q[4] = {0.f, 0.f, 0.f, 0.f};
