@@ -24,6 +24,8 @@
 // once for each norm forward.  Backward all that the inputs give goes round once, the branch's dot product among it;
 // only with a layer norm a second exchange follows (for all norms: 390 us against 375).  All arithmetic is fp32, two
 // values an instruction (one at a time: forward 395 us, backward 441).
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "h3_internal.h"
@@ -881,6 +883,13 @@ cudaError_t launch_rows(const ResidualNormArgs& a, int sms, int* ctas, cudaStrea
   const cudaError_t e = allow_shared_memory<kSmem>(kernel);
   if (e != cudaSuccess) return e;
   *ctas = residual_norm_ctas(a.num_tokens, sms * kCtas);
+  if (kBackward) {
+    // A CTA's column sums are written and read again, so no more CTAs than the rows of the fullest need, and past one
+    // an SM three rows each (2,000 rows of 512: 15 us, 19 with one or two each; 317 of 2,560: 13, 14.4).
+    const int full = (a.num_tokens + *ctas - 1) / *ctas;
+    const int rows = std::max(full, std::min(3, (a.num_tokens + sms - 1) / sms));
+    *ctas = (a.num_tokens + rows - 1) / rows;
+  }
   return launch_programmatic(kernel, dim3(*ctas), dim3(row_threads(a.dim)), stages * stage, stream, a, stages);
 }
 
