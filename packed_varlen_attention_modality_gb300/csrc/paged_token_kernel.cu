@@ -19,10 +19,13 @@
 // is chosen so that a lane's bytes lie together.
 // Scores, max, sum and O are fp32; P is rounded to bf16 (f16) for the product with V, o once at the end.
 //
+// With at most eight rows (a head group's single token) the products take keys as rows and query rows as columns:
+// half the matrix instructions, exponentials and registers, for a transposition of the weights (64 streams of 20,000
+// tokens x 8 heads x 64: 215 us, 280 the other way).  A bf16 cache is bound by HBM either way.
+//
 // 32 streams of 512 to 4,096 tokens, 64 heads on 8 x 128, bf16: 62 us (floor 48; some 9 us are the launch, the scan
 // and the join; 128 streams of 4,096 tokens read at the rate of a plain copy).  Two streams of 90,000 to 100,000
-// tokens, 40 heads on 8 x 128, e4m3: 84 us (floor 57): there the instructions that turn bytes into f16 and take the
-// softmax bound it, 124 us with a conversion to bf16.  Eight warps in one CTA an SM: 93 us.
+// tokens, 40 heads on 8 x 128, e4m3: 79 us (floor 57; 124 with a conversion to bf16).  Eight warps in one CTA an SM: 93.
 #include <cuda_bf16.h>
 
 #include "h3_internal.h"
@@ -43,8 +46,8 @@ static_assert(kRows == kPagedTokenRows, "host and device agree");
 template <int D, bool kE4m3>
 struct Cfg {
   // Keys of a block: steps of 16.  An e4m3 block is bound by its instructions, and look-ups, maxima and exchanges
-  // cost the same for each (64 streams of 20,000 tokens x 8 heads x 64: 280 us at 4 steps, 319 at 2; 2 streams of
-  // 95,000 x 8 x 128: 85 us at 2, 96 at 1).  Three stages do for all: bf16 reads at the rate of a plain copy.
+  // cost the same for each (64 streams of 20,000 tokens x 8 heads x 64: 280 us at 4 steps, 319 at 2, with 16 rows; 2
+  // streams of 95,000 x 8 x 128: 85 us at 2, 96 at 1; with eight rows 82 at 2, 90 at 4).  Three stages do for all: bf16 reads at the rate of a plain copy.
   static constexpr int kSteps = kE4m3 ? 256 / D : 1, kBlock = 16 * kSteps;
   static constexpr int kUnit = kBlock * kWarps;
   static constexpr int kRowBytes = kE4m3 ? D : 2 * D;
