@@ -467,7 +467,7 @@ H3_API h3_status h3_kv_cache_read(const h3_kv_cache_desc* desc, const void* k_ca
  * A row that sees no key (more rows than cached tokens; no cached token) gives o = 0 and lse = -inf.
  * Cached tokens at n and past it are never multiplied in.  A token that a row must not see but another
  * row of its segment sees has weight zero; it may be multiplied by that zero, so an Inf or NaN among its
- * values in a bf16 cache can reach rows before it. */
+ * values (or, in an e4m3 cache, a row that stands for them) can reach rows before it. */
 typedef struct {
   int32_t num_segments;
   int32_t max_seqlen_q; /* host upper bound on the query rows of a segment, <= capacity_q */

@@ -882,7 +882,8 @@ cudaError_t launch_rows(const ResidualNormArgs& a, int sms, int* ctas, cudaStrea
   }
   const cudaError_t e = allow_shared_memory<kSmem>(kernel);
   if (e != cudaSuccess) return e;
-  *ctas = residual_norm_ctas(a.num_tokens, sms * kCtas);
+  const int resident = sms * kCtas;  // (the backward's workspace has slots for so many)
+  *ctas = residual_norm_ctas(a.num_tokens, kBackward ? std::min(resident, kResidualNormMaxBwdCtas) : resident);
   if (kBackward) {
     // A CTA's column sums are written and read again, so no more CTAs than the rows of the fullest need, and past one
     // an SM three rows each (2,000 rows of 512: 15 us, 19 with one or two each; 317 of 2,560: 13, 14.4).
