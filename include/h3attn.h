@@ -467,7 +467,10 @@ H3_API h3_status h3_kv_cache_read(const h3_kv_cache_desc* desc, const void* k_ca
  * A row that sees no key (more rows than cached tokens; no cached token) gives o = 0 and lse = -inf.
  * Cached tokens at n and past it are never multiplied in.  A token that a row must not see but another
  * row of its segment sees has weight zero; it may be multiplied by that zero, so an Inf or NaN among its
- * values (or, in an e4m3 cache, a row that stands for them) can reach rows before it. */
+ * values (or, in an e4m3 cache, a row that stands for them) can reach rows before it.
+ * Scores and sums are fp32.  P is rounded to bf16 before its product with v, by 2^-8 of itself.  In the form for few
+ * rows (below) over an e4m3 cache, 2^e P, with 2^e the scale of v's row, is rounded to f16 instead: by 2^-11 of itself
+ * or, below 2^-21 of the row's largest, by 2^-32 of that. */
 typedef struct {
   int32_t num_segments;
   int32_t max_seqlen_q; /* host upper bound on the query rows of a segment, <= capacity_q */

@@ -13,10 +13,11 @@
 //
 // An e4m3 block becomes f16 in registers, one instruction for two values, and exactly: the rows' scales go to the
 // scores and the weights, which are fp32.  Q's rows are brought to f16 by a power of two each (their largest value to
-// 2^14: what that rounds is 2^-39 of it at most).  The weights of V's rows are 2^(score + V's exponent), kept
-// under 2^8 by a reference of their own that follows their largest, so that f16 rounds each by 2^-11 of itself (2^-25
-// of the reference below 2^-14 of it; bf16 rounds by 2^-8).  The order of the dims in S's product and in O's columns
-// is chosen so that a lane's bytes lie together.
+// 2^14: what that rounds is 2^-39 of it at most).  The weights of V's rows are 2^(score + V's exponent) over a
+// reference of their own, which puts their largest between 2^7 and 2^15: f16 rounds each by 2^-11 of itself (bf16 by
+// 2^-8) or, below 2^-21 of the largest, by 2^-32 of the largest.  So a row that outweighs the others by its score or its
+// scale leaves them their digits up to a ratio of 2^21.  The order of the dims in S's product and in O's columns is
+// chosen so that a lane's bytes lie together.
 // Scores, max, sum and O are fp32; P is rounded to bf16 (f16) for the product with V, o once at the end.
 //
 // With at most eight rows (a head group's single token) the products take keys as rows and query rows as columns:
@@ -41,6 +42,7 @@ constexpr int kRows = 16;    // query rows of a CTA
 constexpr int kCtasPerSm = 2;
 constexpr int kMinShare = 2;   // units
 constexpr int kMaxPieces = 16;  // looked up at once
+constexpr float kTopWeight = 7.f;  // e4m3: log2 of the largest weight when the reference is set (f16 ends at 2^16)
 static_assert(kRows == kPagedTokenRows, "host and device agree");
 
 template <int D, bool kE4m3>
@@ -512,7 +514,7 @@ paged_token_kernel(const __grid_constant__ PagedTokenArgs a) {
             }
           }
           if (kE4m3) {
-            const float w = row_max(u, h);
+            const float w = row_max(u, h) - kTopWeight;
             if (w > top_w[h] && (top_w[h] == -INFINITY || w - top_w[h] > 8.f)) {
               alpha[h] = ex2_approx(top_w[h] - w);
               top_w[h] = w;
