@@ -216,12 +216,14 @@ typedef struct {
  * weight, branch_weight: device [dim] or NULL.  scale, shift, gate: device [num_requests, dim] or NULL.
  *               weight, scale and shift are NULL when norm is H3_NORM_NONE.
  * cu_requests : device int32 [num_requests + 1], request row offsets (0-based, non-decreasing, last =
- *               num_tokens); NULL means one request covering every row.
+ *               num_tokens); NULL means one request covering every row.  Offsets that are not so are
+ *               recorded as H3_ERR_BAD_CU_SEQLENS; each row then counts as some request's in range, and
+ *               the gradients of scale, shift, gate and the weights are not to be used.
  * x_out       : device, x' in the stream's type; may be x itself with its stride.
  * h           : device bf16; NULL when norm is H3_NORM_NONE; may be y itself with its stride.
  * Outputs must not otherwise overlap an input or each other.  Pointers are 16-byte aligned.
  * Errors: H3_ERR_NULL, H3_ERR_INVALID_ARG, H3_ERR_UNSUPPORTED (dim), H3_ERR_MISALIGNED, H3_ERR_CUDA;
- * device-side H3_ERR_TIMEOUT. */
+ * device-side H3_ERR_BAD_CU_SEQLENS / H3_ERR_TIMEOUT. */
 H3_API h3_status h3_residual_norm(const h3_residual_norm_desc* desc, const void* x, const void* y,
                                   const void* weight, const void* branch_weight, const void* scale,
                                   const void* shift, const void* gate, const int32_t* cu_requests,

@@ -603,11 +603,11 @@ def residual_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, norm: Optio
 
     x float32 or bfloat16 [C, dim] (dim a multiple of 8, at most 8192), y bfloat16 [C, dim] or None (then
     x' is x); norm "rms", "layer" or "none" (no h), branch_norm the same ("none": y itself); weight,
-    branch_weight [dim]; scale, shift, gate [R, dim], of the request that cu_requests (int32 [R+1]; None: one
-    request) gives a token; each vector float32 or bfloat16, or None.  Rows may be parts of wider ones (a
-    fused projection's six vectors, say).  Writes new tensors unless x_out / h_out are given (x and y
-    themselves are allowed); rows past num_tokens are left as they were.  Returns (x', h), x' being x itself
-    without y and h None with norm "none".
+    branch_weight [dim]; scale, shift, gate [R, dim], of the request that cu_requests (int32 [R+1], from 0 to
+    num_tokens; None: one request) gives a token; each vector float32 or bfloat16, or None.  Rows may be
+    parts of wider ones (a fused projection's six vectors, say).  Writes new tensors unless x_out / h_out are
+    given (x and y themselves are allowed); rows past num_tokens are left as they were.  Returns (x', h),
+    x' being x itself without y and h None with norm "none".
     """
     sizes, x_stride, y_stride, mod, ptr = _residual_norm_inputs(x, y, norm, weight, scale, shift, gate, branch_norm,
                                                                 branch_weight, residual_scale, cu_requests, eps,

@@ -96,7 +96,7 @@ __host__ __device__ __forceinline__ int range_start(int n, int ctas, int c) {
 }
 
 // The request of row n and the row at which the next one begins.  Offsets that are not what they should be
-// give some request in range.
+// (check_offsets records them) give some request in range.
 __device__ __forceinline__ int request_of(const ResidualNormArgs& a, int n, int* end) {
   int lo = 0;
   if (a.cu_requests != nullptr) {
@@ -108,6 +108,15 @@ __device__ __forceinline__ int request_of(const ResidualNormArgs& a, int n, int*
   }
   *end = a.cu_requests == nullptr || lo == a.num_requests - 1 ? a.num_tokens : a.cu_requests[lo + 1];
   return lo;
+}
+
+// The grid looks over the offsets: they start at 0, do not fall, end at num_tokens.
+__device__ __forceinline__ void check_offsets(const ResidualNormArgs& a) {
+  if (a.cu_requests == nullptr) return;
+  const int first = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x);
+  bool bad = first == 0 && (a.cu_requests[0] != 0 || a.cu_requests[a.num_requests] != a.num_tokens);
+  for (int64_t r = first; r < a.num_requests; r += gridDim.x * blockDim.x) bad |= a.cu_requests[r + 1] < a.cu_requests[r];
+  if (bad) record_error(a.err, kErrBadCuSeqlens);
 }
 
 // The sums of N values over the lanes, on every lane.  Of three values and more a lane gives half to a partner and
@@ -371,6 +380,7 @@ residual_norm_kernel(const __grid_constant__ ResidualNormArgs a, int stages) {
   ring.stage_bytes = row_place(xb) + row_place(yb);
   ring.load_bytes = xb + yb;
   ring.start();
+  check_offsets(a);
 
   Exchange<kThreads / 32> tell{told};
   const float inv_dim = 1.f / dim;
@@ -498,6 +508,7 @@ residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a, int stages)
     }
   }
   ring.start();
+  check_offsets(a);
 
   constexpr int kTold = 6, kDots = 2;
   Talk<kThreads / 32, kTold> row_talk{inputs};
