@@ -804,12 +804,27 @@ def paged_attn_workspace_size(num_segments: int, max_seqlen_q: int, max_seqlen_k
     return int(load_library().h3_paged_attn_workspace_size(desc))
 
 
+def _paged_workspace(lib, desc: bytes, e4m3: bool, limit: Optional[int], dev: torch.device) -> torch.Tensor:
+    """A workspace for the call: with room for unpacking where the limit and the device's memory allow it."""
+    size = lib.h3_paged_attn_workspace_size(desc) or 16
+    if not e4m3:
+        return torch.empty(size, dtype=_U8, device=dev)
+    if limit is None or size <= limit:
+        try:
+            return torch.empty(size, dtype=_U8, device=dev)
+        except torch.OutOfMemoryError:
+            pass
+    plain = _PagedAttnDesc.from_buffer_copy(desc)
+    plain.cache_type = 1  # what a bf16 cache wants is the least
+    return torch.empty(lib.h3_paged_attn_workspace_size(bytes(plain)) or 16, dtype=_U8, device=dev)
+
+
 def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                    cu_seqlens_q: torch.Tensor, seqused_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
                    k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
                    causal_block: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False,
                    lse: Optional[torch.Tensor] = None, softmax_scale: Optional[float] = None,
-                   workspace: Optional[torch.Tensor] = None):
+                   workspace: Optional[torch.Tensor] = None, workspace_limit: Optional[int] = None):
     """Attention of new tokens over a paged cache: the query rows of segment g (cu_seqlens_q, int32 [S+1]) are
     the last of its seqused_k[g] cached tokens (int32 [S]), whose keys and values kv_cache_write has put
     into k_cache, v_cache (and k_scale, v_scale) under block_table.
@@ -821,6 +836,11 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     of a key head's rows, so single tokens want a tight bound.  A row that sees nothing gives 0 and an
     LSE of -inf; rows of `out` outside every segment are left untouched.  Returns out [C, Hq, D] (and lse
     fp32 [Hq, C] when requested).
+
+    Long chunks (max_seqlen_q * Hq / Hkv above 512) over an e4m3 cache are fastest with its tokens unpacked to
+    bf16 in the workspace: twice the e4m3 bytes of S * max_seqlen_k tokens, so tight bounds save memory.  Where
+    that is more than 4 GiB, or workspace_limit bytes (None: no limit) or the device's free memory do not hold it, the
+    call allocates the least workspace instead, gives the same results and takes longer.
     """
     dev = q.device
     q_stride = _rows(q, "q", dev)
@@ -850,7 +870,7 @@ def paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
         desc = _PagedAttnDesc.pack(S, int(max_seqlen_q), int(max_seqlen_k), C, H, heads, D, *rest, int(causal_block),
                                    0.0 if softmax_scale is None else float(softmax_scale), q_stride)
         if workspace is None:
-            workspace = torch.empty(lib.h3_paged_attn_workspace_size(desc) or 16, dtype=_U8, device=dev)
+            workspace = _paged_workspace(lib, desc, e4m3=rest[0] == 2, limit=workspace_limit, dev=dev)
         else:
             _require(workspace, "workspace", _U8, dev)
         _launch(lib.h3_paged_attn_fwd, "h3_paged_attn_fwd", dev, desc, q.data_ptr(), *cache, cu_seqlens_q.data_ptr(),
