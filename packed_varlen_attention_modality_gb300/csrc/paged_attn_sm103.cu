@@ -9,8 +9,11 @@
 // with its rows' scales, and the epilogue's warps, idle between items, turn it into bf16 in shared memory (exactly);
 // the products and the softmax then are those of a bf16 cache.
 //
-// What it measured: 2,000 rows over 58,758 bf16 tokens, causal by frame, 24 heads x 128, 873 to 915 us (1,650 TFLOP/s,
-// at the power cap as the packed kernel is); first chunks of 900 to 4,096 tokens, 24 heads on 8 x 64, 78 us, of which
+// P is rounded to bf16 for the tensor core (half a step, 2^-8 of itself at most); scores, running max and sum, and O
+// stay fp32, and the result is rounded to bf16 once.
+//
+// What it measured: 2,000 rows over 58,758 bf16 tokens, causal by frame, 24 heads x 128, 873 us on a cool GPU (1,650
+// TFLOP/s) and up to 1,020 at the power cap on a warm one, as the packed kernel; first chunks of 900 to 4,096 tokens, 24 heads on 8 x 64, 78 us, of which
 // the plan is 6 and the join 8.  Two chunks of 1,000 to 1,500 rows over 14,000 to 24,000 e4m3 tokens, 40 heads x 128,
 // took 1,025 us converted as they are read: shared memory's bandwidth bounds that, for a step of 2,700 cycles moves the
 // operands of the products (1,536 cycles of 128 bytes), the arriving bytes (256) and the conversion's reads and writes

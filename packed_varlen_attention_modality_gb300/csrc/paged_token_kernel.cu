@@ -18,7 +18,8 @@
 // 2^-8) or, below 2^-21 of the largest, by 2^-32 of the largest.  So a row that outweighs the others by its score or its
 // scale leaves them their digits up to a ratio of 2^21.  The order of the dims in S's product and in O's columns is
 // chosen so that a lane's bytes lie together.
-// Scores, max, sum and O are fp32; P is rounded to bf16 (f16) for the product with V, o once at the end.
+// Scores, max, sum and O are fp32; P is rounded to bf16 (2^-8 of itself at most; e4m3: f16, as above) for the product
+// with V, o once at the end.
 //
 // With at most eight rows (a head group's single token) the products take keys as rows and query rows as columns:
 // half the matrix instructions, exponentials and registers, for a transposition of the weights (64 streams of 20,000

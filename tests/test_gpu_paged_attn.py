@@ -1,6 +1,7 @@
 """Attention over a paged cache on the GPU against the fp64 oracle.
 
-Tolerances, from the arithmetic (derived before the first run).  The cache's values are exact in bf16, so
+Tolerances, from the arithmetic (the terms of 2^-126 and 2^-25 were added, with theirs, after runs that met
+them).  The cache's values are exact in bf16, so
 both sides start from the same keys and values.  S and the sums are fp32; the weights are rounded to bf16
 (half a step, 2^-8 of each) before the product with V, and o is rounded to bf16 once more:
     |o - o*| <= 2^-8 sum_j P_j |v_j| + 2^-8 |o| + fp32 terms,
